@@ -8,6 +8,8 @@ or fails to load, importing the binding's entry points raises.
 Entry points keep the C names: bpt_layer_fwd, bpt_layer_bwd,
 bpt_attn_headchunk, bpt_attention_fwd, bpt_attention_bwd, bpt_attention_bwd_noalloc,
 bpt_lm_loss_fwd, bpt_lm_loss_bwd, bpt_lm_workspace_bytes,
+bpt_qk_norm_rope_fwd, bpt_qk_norm_rope_bwd, bpt_qk_norm_rope_workspace_bytes,
+bpt_clip_grads, bpt_clip_workspace_bytes,
 bpt_workspace_bytes, bpt_saved_bytes, bpt_attention_bwd_workspace_bytes,
 bpt_status_string, bpt_last_device_error, bpt_check_device_range, bpt_watchdog_selftest,
 bpt_profile_enable, bpt_profile_collect, bpt_profile_list.  The layer stack
@@ -32,6 +34,7 @@ BPT_FLAG_ACCUM_GRADS = 1
 BPT_FLAG_ONE_STREAM = 2
 BPT_FLAG_DETERMINISTIC = 4
 BPT_FLAG_DEBUG_CHECKS = 8
+BPT_DTYPE_F32, BPT_DTYPE_BF16 = 0, 1
 
 WEIGHT_FIELDS = ("ln1_w", "ln1_b", "wq", "bq", "wk", "bk", "wv", "bv", "wo", "bo",
                  "ln2_w", "ln2_b", "w1", "b1", "w2", "b2", "w3")
@@ -55,6 +58,10 @@ class BptGrads(ctypes.Structure):
 
 class BptLmConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n", "h", "vocab", "vocab_block", "flags")]
+
+
+class BptClipTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 class BptError(RuntimeError):
@@ -106,6 +113,16 @@ def lib() -> ctypes.CDLL:
         L.bpt_lm_loss_fwd.restype = i32
         L.bpt_lm_loss_bwd.argtypes = [lmp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, sz, vp]
         L.bpt_lm_loss_bwd.restype = i32
+        L.bpt_qk_norm_rope_workspace_bytes.argtypes = [cfgp]
+        L.bpt_qk_norm_rope_workspace_bytes.restype = sz
+        L.bpt_qk_norm_rope_fwd.argtypes = [cfgp, vp, vp, vp, vp, vp, vp]
+        L.bpt_qk_norm_rope_fwd.restype = i32
+        L.bpt_qk_norm_rope_bwd.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.bpt_qk_norm_rope_bwd.restype = i32
+        L.bpt_clip_workspace_bytes.argtypes = []
+        L.bpt_clip_workspace_bytes.restype = sz
+        L.bpt_clip_grads.argtypes = [i32, ctypes.POINTER(BptClipTensor), ctypes.c_float, i32, vp, vp, sz, vp]
+        L.bpt_clip_grads.restype = i32
         L.bpt_check_device_range.argtypes = [vp, sz]
         L.bpt_check_device_range.restype = i32
         L.bpt_watchdog_selftest.argtypes = [vp]
@@ -238,6 +255,98 @@ def bpt_lm_loss_bwd(cfg, x, w, targets, lse, dloss, dx, dw, ws, stream=None) -> 
     rc = lib().bpt_lm_loss_bwd(ctypes.byref(c), _ptr(x), _ptr(w), _ptr(targets), _ptr(lse), float(dloss),
                                _ptr(dx), _ptr(dw), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
     _check(rc, "bpt_lm_loss_bwd")
+
+
+def _want(where, t, dtype, numel, what, optional=False):
+    """Refuses (BPT_EINVAL) a tensor the library would read past or misread:
+    not on the current CUDA device, not contiguous, of another type or with
+    fewer elements than the call touches."""
+    import torch
+    if t is None:
+        if optional:
+            return
+        raise BptError(BPT_EINVAL, f"{where}: {what} is missing")
+    if not (t.is_cuda and t.device.index == torch.cuda.current_device() and t.is_contiguous() and t.dtype == dtype
+            and t.numel() >= numel):
+        raise BptError(BPT_EINVAL, f"{where}: {what} must be a contiguous {dtype} tensor of at least {numel} "
+                                   f"elements on the current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _packed_numel(c):
+    return c.b * c.s * (c.n_heads + 2 * c.n_kv_heads) * c.head_dim
+
+
+def bpt_qk_norm_rope_workspace_bytes(cfg) -> int:
+    return int(lib().bpt_qk_norm_rope_workspace_bytes(ctypes.byref(make_config(cfg))))
+
+
+def bpt_qk_norm_rope_fwd(cfg, qkv, wq, wk, positions, out, stream=None) -> None:
+    """Head norm (weights wq, wk [d]; both None: none) and rotation (base
+    cfg.rope_base; 0: none) of the query and key heads of qkv [b*s, (H +
+    2 H_kv) d] at `positions` [b*s] int32 (None: the row's index in its
+    sequence), into out (qkv itself: in place)."""
+    import torch
+    n, where = _packed_numel(cfg), "bpt_qk_norm_rope_fwd"
+    _want(where, qkv, torch.bfloat16, n, "qkv")
+    _want(where, out, torch.bfloat16, n, "out")
+    _want(where, wq, torch.bfloat16, cfg.head_dim, "wq", True)
+    _want(where, wk, torch.bfloat16, cfg.head_dim, "wk", True)
+    _want(where, positions, torch.int32, cfg.b * cfg.s, "positions", True)
+    c = make_config(cfg)
+    _check(lib().bpt_qk_norm_rope_fwd(ctypes.byref(c), _ptr(qkv), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(out),
+                                      _stream(stream)), where)
+
+
+def bpt_qk_norm_rope_bwd(cfg, qkv, wq, wk, positions, dout, dqkv, dwq, dwk, ws, stream=None) -> None:
+    """Gradients of bpt_qk_norm_rope_fwd: dqkv (dout itself: in place) and
+    the weights' dwq, dwk [d] fp32.  qkv is the forward's input, before the
+    norm.  Without weights qkv, dwq, dwk and ws may be None."""
+    import torch
+    n, where = _packed_numel(cfg), "bpt_qk_norm_rope_bwd"
+    none = wq is None and wk is None
+    _want(where, qkv, torch.bfloat16, n, "qkv", none)
+    _want(where, dout, torch.bfloat16, n, "dout")
+    _want(where, dqkv, torch.bfloat16, n, "dqkv")
+    _want(where, wq, torch.bfloat16, cfg.head_dim, "wq", True)
+    _want(where, wk, torch.bfloat16, cfg.head_dim, "wk", True)
+    _want(where, positions, torch.int32, cfg.b * cfg.s, "positions", True)
+    _want(where, dwq, torch.float32, cfg.head_dim, "dwq", none)
+    _want(where, dwk, torch.float32, cfg.head_dim, "dwk", none)
+    _want(where, ws, torch.uint8, 0, "ws", none)
+    c = make_config(cfg)
+    _check(lib().bpt_qk_norm_rope_bwd(ctypes.byref(c), _ptr(qkv), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(dout),
+                                      _ptr(dqkv), _ptr(dwq), _ptr(dwk), _ptr(ws), 0 if ws is None else ws.numel(),
+                                      _stream(stream)), where)
+
+
+def bpt_clip_workspace_bytes() -> int:
+    return int(lib().bpt_clip_workspace_bytes())
+
+
+def bpt_clip_grads(grads, max_norm, norm, ws, out=None, flags=0, stream=None) -> None:
+    """Global norm of the tensors `grads` (fp32 or bf16, contiguous) into
+    norm (one fp32 element), and grads * min(1, max_norm / (norm + 1e-6)) into
+    the tensors `out` (None: in place)."""
+    import torch
+    where = "bpt_clip_grads"
+    out = grads if out is None else out
+    if len(out) != len(grads):
+        raise BptError(BPT_EINVAL, f"{where}: {len(grads)} gradients, {len(out)} outputs")
+    _want(where, norm, torch.float32, 1, "norm")
+    _want(where, ws, torch.uint8, 0, "ws")
+    kinds = {torch.float32: BPT_DTYPE_F32, torch.bfloat16: BPT_DTYPE_BF16}
+    table = (BptClipTensor * max(1, len(grads)))()
+    dev = torch.cuda.current_device()
+    for e, g, o in zip(table, grads, out):
+        n = g.numel()
+        if g.dtype not in kinds or o.dtype != g.dtype or o.numel() != n or not (
+                g.is_cuda and o.is_cuda and g.device.index == dev and o.device.index == dev and g.is_contiguous()
+                and o.is_contiguous()):
+            raise BptError(BPT_EINVAL, f"{where}: gradients and outputs must be contiguous fp32 or bf16 tensors of "
+                                       f"equal type and size on the current device")
+        e.grad, e.out, e.numel, e.dtype = g.data_ptr(), o.data_ptr(), n, kinds[g.dtype]
+    _check(lib().bpt_clip_grads(len(grads), table, float(max_norm), int(flags), _ptr(norm), _ptr(ws), ws.numel(),
+                                _stream(stream)), where)
 
 
 BPT_LM_BAD_TARGET_SITE = 950

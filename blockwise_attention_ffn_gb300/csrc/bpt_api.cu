@@ -126,11 +126,6 @@ int check_weights(const bpt_config* c, const bpt_weights* w) {
 // touches through it, must lie inside one device allocation of the current
 // device; after the launches the call synchronises and reports the device
 // error word itself.
-struct Span {
-  const void* p;
-  int64_t bytes;
-};
-
 int check_spans(const Span* sp, int n) {
   for (int i = 0; i < n; ++i)
     if (sp[i].bytes > 0 && check_device_range(sp[i].p, (size_t)sp[i].bytes)) return BPT_EINVAL;
@@ -163,14 +158,29 @@ int check_grads_range(const bpt_config* c, const Dims& D, const bpt_grads* g) {
   return check_spans(sp, param_spans(c, D, f, 4, sp));
 }
 
+}  // namespace
+
+int bpt::debug_spans(const Span* sp, int n) { return check_spans(sp, n); }
+
 // After the launches: wait for them and report the error word (which the
 // read clears) or the failure of the synchronisation itself.
-int debug_finish(cudaStream_t st) {
+int bpt::debug_finish(cudaStream_t st) {
   unsigned int e[4] = {0, 0, 0, 0};
   if (read_device_error(st, e)) return BPT_ECUDA;
   if (!e[0]) return BPT_OK;
   return e[0] == BPT_EINVAL ? BPT_EINVAL : BPT_ETIMEOUT;
 }
+
+int bpt::packed_dims(const bpt_config* cfg, PackedDims* out) {
+  Dims D;
+  const int rc = validate(cfg, &D);
+  if (rc) return rc;
+  *out = PackedDims{D.b, D.s, D.H, D.Hkv, D.G, D.d, D.s_pad, D.rows, (D.H + 2 * D.Hkv) * D.d,
+                    D.det, D.debug, (cfg->flags & BPT_FLAG_ACCUM_GRADS) != 0};
+  return BPT_OK;
+}
+
+namespace {
 
 // ---------------------------------------------------------------- workspace
 struct Carve {

@@ -31,6 +31,23 @@ int sm_count();
 // 0 if [p, p + bytes) lies inside one device allocation of the current
 // device, else 1 (the debug checks of BPT_FLAG_DEBUG_CHECKS)
 int check_device_range(const void* p, size_t bytes);
+// The debug checks of the entry points: every span inside one device
+// allocation (0, else BPT_EINVAL); after the launches, the stream's and the
+// device error word's status.
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+int debug_spans(const Span* sp, int n);
+int debug_finish(cudaStream_t st);
+
+// A config's shape for the calls on the packed Q/K/V buffer alone, checked
+// like every layer call's (0 or a BPT_* status).
+struct PackedDims {
+  int64_t b, s, H, Hkv, G, d, s_pad, rows, width;  // width = (H + 2 Hkv) d
+  bool det, debug, accum;
+};
+int packed_dims(const bpt_config* cfg, PackedDims* out);
 
 // Raises a kernel's dynamic shared-memory limit to `bytes` on the current
 // device, once per device (the attribute belongs to the kernel's instance in

@@ -148,22 +148,6 @@ __global__ void __launch_bounds__(1024) lm_mean_kernel(int64_t n, const float* r
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-struct Span {
-  const void* p;
-  int64_t bytes;
-};
-int check_spans(const Span* sp, int k) {
-  for (int i = 0; i < k; ++i)
-    if (sp[i].bytes > 0 && check_device_range(sp[i].p, (size_t)sp[i].bytes)) return BPT_EINVAL;
-  return BPT_OK;
-}
-int debug_finish(cudaStream_t st) {
-  unsigned int e[4] = {0, 0, 0, 0};
-  if (read_device_error(st, e)) return BPT_ECUDA;
-  if (!e[0]) return BPT_OK;
-  return e[0] == BPT_EINVAL ? BPT_EINVAL : BPT_ETIMEOUT;
-}
-
 }  // namespace
 }  // namespace bpt
 
@@ -194,7 +178,7 @@ int bpt_lm_loss_fwd(const bpt_lm_config* cfg, const void* x, const void* w, cons
   if (D.debug) {
     const Span sp[] = {{x, D.n * D.h * 2}, {w, D.V * D.h * 2}, {targets, D.n * 4}, {loss, 4},
                        {lse, lse ? D.n * 4 : 0}, {ws, (int64_t)need}};
-    if (check_spans(sp, 6)) return BPT_EINVAL;
+    if (debug_spans(sp, 6)) return BPT_EINVAL;
   }
   plan_lm_fwd(D, ws, &W, lse == nullptr);
   float* lse_out = lse ? lse : W.lse;
@@ -243,7 +227,7 @@ int bpt_lm_loss_bwd(const bpt_lm_config* cfg, const void* x, const void* w, cons
   if (D.debug) {
     const Span sp[] = {{x, D.n * D.h * 2},  {w, D.V * D.h * 2}, {targets, D.n * 4}, {lse, D.n * 4},
                        {dx, D.n * D.h * 2}, {dw, D.V * D.h * 4}, {ws, (int64_t)need}};
-    if (check_spans(sp, 7)) return BPT_EINVAL;
+    if (debug_spans(sp, 7)) return BPT_EINVAL;
   }
   plan_lm_bwd(D, ws, &W);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -362,6 +362,74 @@ int bpt_lm_loss_bwd(const bpt_lm_config* cfg, const void* x, const void* w, cons
                     const float* lse, float dloss, void* dx, float* dw, void* ws, size_t ws_bytes,
                     void* stream);
 
+/* ------------------------------------------------------------------------
+ * Norm of every query and key head with the rotary position embedding, in
+ * one pass over the packed projection buffer (the step between a projection
+ * and the attention calls above, for models that normalise queries and keys).
+ *
+ * With x one head's d values of a row, w its weight vector (wq for the query
+ * heads, wk for the key heads) and R(p) the rotation of the layer's rotary
+ * embedding (pair (i, i + d/2) turned by p * rope_base^(-2i/d)):
+ *   forward   r = (mean x^2 + norm_eps)^(-1/2),  y = R(p) (x r * w)
+ *   backward  dn = R(p)^T dy,  dw = sum over rows and heads of dn * x r,
+ *             g = dn * w,  dx = r (g - x r mean(g * x r))
+ * One rounding to bf16 per output, everything between in fp32; angles are
+ * reduced exactly at every position.
+ *
+ *   cfg        b, s, heads, head_dim, norm_eps, rope_base (0: no rotation) and
+ *              flags are used; the rest must be a valid layer's
+ *   qkv        [b*s, (H + 2 H_kv) d] bf16: the projection, before the norm
+ *   wq, wk     [d] bf16, or both NULL: no norm, the rotation alone
+ *   positions  [b*s] int32 position of each row (any value), or NULL: the
+ *              row's index in its sequence
+ *   out        [b*s, (H + 2 H_kv) d] bf16: may be qkv itself (V is then left
+ *              as it is), else V's columns are copied
+ *   dout       gradient with respect to out, same layout; dqkv: gradient with
+ *              respect to qkv, may be dout itself, not qkv
+ *   dwq, dwk   [d] fp32 out (+= with BPT_FLAG_ACCUM_GRADS)
+ *   ws         backward with weights only: bpt_qk_norm_rope_workspace_bytes
+ * Without weights the backward reads neither qkv nor ws and writes no dw: all
+ * four may be NULL.  Buffers that overlap in part are refused.  Every sum is
+ * taken in a fixed order.  The weights need not be the layer's: the layer
+ * calls have no head norm. */
+size_t bpt_qk_norm_rope_workspace_bytes(const bpt_config* cfg);
+int bpt_qk_norm_rope_fwd(const bpt_config* cfg, const void* qkv, const void* wq, const void* wk,
+                         const int32_t* positions, void* out, void* stream);
+int bpt_qk_norm_rope_bwd(const bpt_config* cfg, const void* qkv, const void* wq, const void* wk,
+                         const int32_t* positions, const void* dout, void* dqkv, float* dwq, float* dwk, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Clipping by the global norm: the step between the backward pass of a stack
+ * and its optimizer.
+ *   norm = sqrt(sum over all tensors and elements of g^2)
+ *   out  = g * min(1, max_norm / (norm + 1e-6))
+ * The tensors of one call may mix fp32 and bf16.
+ *
+ *   t        n tensors (host array, read during the call): grad and out are
+ *            device pointers aligned to their element; out == grad clips in
+ *            place (nothing is written where the norm is within max_norm).
+ *            An output may not share memory with any other tensor of the call
+ *            (BPT_EINVAL): each is scaled once.
+ *   max_norm > 0; +inf computes the norm and copies
+ *   flags    0 or BPT_FLAG_DEBUG_CHECKS
+ *   norm     one fp32 (device), the norm before clipping; not part of a tensor
+ *   ws       bpt_clip_workspace_bytes() bytes, one per call in flight
+ * A norm that is inf gives a factor of 0, a NaN norm a NaN factor, as the
+ * formula says.  Squares are summed in fp32 by 32 (rescaled where they leave
+ * its range) and then in fp64, in an order fixed by the tensors' sizes,
+ * addresses modulo 16 and the device's SM count. */
+enum { BPT_DTYPE_F32 = 0, BPT_DTYPE_BF16 = 1 };
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel;
+  int32_t dtype; /* BPT_DTYPE_* */
+} bpt_clip_tensor;
+size_t bpt_clip_workspace_bytes(void);
+int bpt_clip_grads(int32_t n, const bpt_clip_tensor* t, float max_norm, int32_t flags, float* norm, void* ws,
+                   size_t ws_bytes, void* stream);
+
 /* Opt-in launch profiler.  bpt_profile_enable(1) makes every later launch
  * of this process record a pair of CUDA events on its stream, tagged with
  * the launch's kind and its algorithmic work (FLOPs for tensor-core kernels,
