@@ -8,6 +8,7 @@ or fails to load, importing the binding's entry points raises.
 Entry points keep the C names: bpt_layer_fwd, bpt_layer_bwd,
 bpt_attn_headchunk, bpt_attention_fwd, bpt_attention_bwd, bpt_attention_bwd_noalloc,
 bpt_lm_loss_fwd, bpt_lm_loss_bwd, bpt_lm_workspace_bytes,
+bpt_attention_mod_fwd, bpt_attention_mod_bwd, bpt_attention_mod_bwd_workspace_bytes,
 bpt_qk_norm_rope_fwd, bpt_qk_norm_rope_bwd, bpt_qk_norm_rope_workspace_bytes,
 bpt_clip_grads, bpt_clip_workspace_bytes,
 bpt_workspace_bytes, bpt_saved_bytes, bpt_attention_bwd_workspace_bytes,
@@ -20,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from dataclasses import dataclass
 
 from .presets import PRESETS, LayerConfig  # noqa: F401
 
@@ -58,6 +60,11 @@ class BptGrads(ctypes.Structure):
 
 class BptLmConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n", "h", "vocab", "vocab_block", "flags")]
+
+
+class BptScoreMod(ctypes.Structure):
+    _fields_ = [("row_begin", ctypes.c_void_p), ("row_end", ctypes.c_void_p), ("slopes", ctypes.c_void_p),
+                ("softcap", ctypes.c_float)]
 
 
 class BptClipTensor(ctypes.Structure):
@@ -113,6 +120,13 @@ def lib() -> ctypes.CDLL:
         L.bpt_lm_loss_fwd.restype = i32
         L.bpt_lm_loss_bwd.argtypes = [lmp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, sz, vp]
         L.bpt_lm_loss_bwd.restype = i32
+        modp = ctypes.POINTER(BptScoreMod)
+        L.bpt_attention_mod_fwd.argtypes = [cfgp, modp, vp, vp, vp, vp]
+        L.bpt_attention_mod_fwd.restype = i32
+        L.bpt_attention_mod_bwd_workspace_bytes.argtypes = [cfgp]
+        L.bpt_attention_mod_bwd_workspace_bytes.restype = sz
+        L.bpt_attention_mod_bwd.argtypes = [cfgp, modp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.bpt_attention_mod_bwd.restype = i32
         L.bpt_qk_norm_rope_workspace_bytes.argtypes = [cfgp]
         L.bpt_qk_norm_rope_workspace_bytes.restype = sz
         L.bpt_qk_norm_rope_fwd.argtypes = [cfgp, vp, vp, vp, vp, vp, vp]
@@ -274,6 +288,60 @@ def _want(where, t, dtype, numel, what, optional=False):
 
 def _packed_numel(c):
     return c.b * c.s * (c.n_heads + 2 * c.n_kv_heads) * c.head_dim
+
+
+@dataclass(frozen=True)
+class ScoreMod:
+    """What bpt_attention_mod_fwd/bwd change about the attention: the keys
+    [row_begin, row_end) that each query row sees ([b*s] int32 tensors, None:
+    from 0, to s), the per-head slopes of a bias -slope * |i - j| ([H] fp32),
+    and the cap of softcap * tanh(score / softcap) (0: none)."""
+    row_begin: object = None
+    row_end: object = None
+    slopes: object = None
+    softcap: float = 0.0
+
+
+def _score_mod(where, cfg, mod):
+    import torch
+    _want(where, mod.row_begin, torch.int32, cfg.b * cfg.s, "row_begin", True)
+    _want(where, mod.row_end, torch.int32, cfg.b * cfg.s, "row_end", True)
+    _want(where, mod.slopes, torch.float32, cfg.n_heads, "slopes", True)
+    return BptScoreMod(*(None if t is None else t.data_ptr() for t in (mod.row_begin, mod.row_end, mod.slopes)),
+                       float(mod.softcap))
+
+
+def bpt_attention_mod_fwd(cfg, mod, qkv, o, lse, stream=None) -> None:
+    """Attention of the packed qkv [b*s, (H + 2 H_kv) d] with the scores
+    modified by mod (a ScoreMod): o [b*s, H d] bf16 and lse [b, H, s_pad] fp32
+    (None: not wanted)."""
+    import torch
+    where = "bpt_attention_mod_fwd"
+    _want(where, qkv, torch.bfloat16, _packed_numel(cfg), "qkv")
+    _want(where, o, torch.bfloat16, cfg.b * cfg.s * cfg.n_heads * cfg.head_dim, "o")
+    _want(where, lse, torch.float32, cfg.b * cfg.n_heads * s_pad(cfg), "lse", True)
+    c, m = make_config(cfg), _score_mod(where, cfg, mod)
+    _check(lib().bpt_attention_mod_fwd(ctypes.byref(c), ctypes.byref(m), _ptr(qkv), _ptr(o), _ptr(lse),
+                                       _stream(stream)), where)
+
+
+def bpt_attention_mod_bwd_workspace_bytes(cfg) -> int:
+    return int(lib().bpt_attention_mod_bwd_workspace_bytes(ctypes.byref(make_config(cfg))))
+
+
+def bpt_attention_mod_bwd(cfg, mod, qkv, o, lse, dout, dqkv, ws, stream=None) -> None:
+    """Gradients of bpt_attention_mod_fwd with respect to qkv, given dout
+    [b*s, H d] and what the forward wrote; dqkv like qkv, a buffer of its own."""
+    import torch
+    where = "bpt_attention_mod_bwd"
+    n, hd = _packed_numel(cfg), cfg.b * cfg.s * cfg.n_heads * cfg.head_dim
+    for t, numel, what in ((qkv, n, "qkv"), (o, hd, "o"), (dout, hd, "dout"), (dqkv, n, "dqkv")):
+        _want(where, t, torch.bfloat16, numel, what)
+    _want(where, lse, torch.float32, cfg.b * cfg.n_heads * s_pad(cfg), "lse")
+    _want(where, ws, torch.uint8, 0, "ws")
+    c, m = make_config(cfg), _score_mod(where, cfg, mod)
+    _check(lib().bpt_attention_mod_bwd(ctypes.byref(c), ctypes.byref(m), _ptr(qkv), _ptr(o), _ptr(lse), _ptr(dout),
+                                       _ptr(dqkv), _ptr(ws), ws.numel(), _stream(stream)), where)
 
 
 def bpt_qk_norm_rope_workspace_bytes(cfg) -> int:

@@ -16,7 +16,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbpt.so")
 SOURCES = ["bpt_api.cu", "gemm_tc.cu", "gemm_pair.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_noalloc.cu", "norm_misc.cu",
-           "host_util.cu", "lm_loss.cu", "norm_rope.cu", "grad_clip.cu"]
+           "host_util.cu", "lm_loss.cu", "norm_rope.cu", "grad_clip.cu", "attn_mod.cu", "attn_mod_fwd.cu", "attn_mod_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 

@@ -63,15 +63,6 @@ __device__ __forceinline__ int out_head(const AttnFwdParams& p, int n) {
   return (n / p.o_seg) * p.o_seg_stride + n % p.o_seg;
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
-                                            int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
 // TMEM: two 128-column S buffers [0,256), O [256, 256+D+EXT), Q after it
 // (D/2 columns).  Q is copied into TMEM once per CTA (the A operand of
 // S = Q K_j^T) and each P is written over its own S buffer as bf16 pairs (the

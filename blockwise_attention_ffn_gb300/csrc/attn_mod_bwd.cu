@@ -1,0 +1,1124 @@
+// attn_mod_bwd.cu -- attention backward with a key window per query row, capped
+// scores and a distance bias (bpt_attention_mod_bwd).
+//
+// With x = q.k / sqrt(d), u = tanh(x / C), y = C u - a |i - j| (or y = x - ...
+// without a cap), P = exp(y - LSE) on the visible pairs and 0 elsewhere,
+//   dV = P^T dO,  dP = dO V^T,  D = rowsum(dO * O),
+//   dx = P * (dP - D) * (1 - u^2),  dQ = dx K / sqrt(d),  dK = dx^T Q / sqrt(d).
+// The bias has no gradient here (the slopes are constants).
+//
+// Two kernels after one that prepares the rows, in the form of the plain
+// backward: dK/dV with the key tile outermost, dQ with the query tile
+// outermost, both rebuilding their scores in 64-wide sub-tiles that two groups
+// of compute warps take in turn; no atomics.  What differs:
+//  * The query tiles that see a key tile, and the key tiles that a query tile
+//    sees, come from the windows; tiles outside are never loaded.
+//  * Without a cap, -LSE enters dK/dV's scores through the product, as before,
+//    but in three bf16 terms (24 bits: a biased LSE can be large); with one it
+//    has to be added after the tanh, and travels with the query stage as 128
+//    floats.  D's three terms enter through the product in both.
+//  * dK/dV's masks are per column: a stage carries its queries' windows, read
+//    only in sub-tiles that some window cuts.
+//  * P stays fp32 for dx; P (1 - u^2) replaces it in place, so the cap costs
+//    no registers.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "../../include/bpt.h"
+#include "attn_mod.cuh"
+#include "internal.h"
+
+namespace bpt {
+int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d);
+
+namespace {
+
+// The windows of one 128-query tile as the dK/dV kernel's stage takes them:
+// per row (lo, hi - lo), then per 64-row half the bounds that tell a sub-tile
+// that no window cuts.
+struct __align__(16) WinRecord {
+  int2 row[128];
+  int2 cut[2];  // (largest lo, least hi)
+  int4 unused;
+};
+static_assert(sizeof(WinRecord) % 16 == 0, "bulk copies move 16-byte units");
+
+struct ModBwdParams {
+  CUtensorMap map_qkv;  // 3-D {width, s, b}, box {CW, 128, 1}
+  CUtensorMap map_do;   // 3-D {H d, s, b}, box {CW, 128, 1}
+  CUtensorMap map_aux;  // 2-D {8, b*H*s_pad} bf16, box {8, 128}, no swizzle
+  int s, s_pad, H, Hkv, G, causal, n_t;
+  int k_col, v_col;
+  const float *dsum, *nl2;  // [b, H, s_pad]: dO . O and -LSE log2(e) (0 for a row that sees nothing)
+  const WinRecord* rec;     // [b, n_t]
+  const int2* span;         // [b, n_t]: least lo and largest hi of a query tile's rows
+  const __nv_bfloat16 *qkv, *dout;
+  __nv_bfloat16* dqkv;
+  long long width;
+  const int32_t *row_begin, *row_end;
+  const float* slopes;
+  float scale, scale_log2, inv_cap, cap_log2;
+  int one_issuer;  // fixed-order mode: warp 1 issues both groups' products
+  unsigned int* err;
+};
+
+// exp2 of 64 modified scores in log2 units and what dx multiplies (dP - D)
+// with: sv in, pe = P (1 - u^2) out, pk = P as bf16 pairs (WANT_P).
+// add(k): what is added to the (capped, scaled) score of element k, the bias
+// and -LSE; on(k): visible.  all: every element is visible.
+template <bool CAP, bool WANT_P, class Add, class On>
+__device__ __forceinline__ void probabilities(uint32_t (&sv)[64], float (&pe)[64], uint32_t (&pk)[32], float scale_log2,
+                                              float inv_cap, float cap_log2, bool all, Add add, On on) {
+  if constexpr (CAP) {
+    // u over sv
+    if (__all_sync(0xffffffffu, amax_of(sv) * inv_cap <= TANH_SMALL)) {
+      const uint64_t ic2 = f2(inv_cap, inv_cap);
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        const float2 t = f2split(tanh2_small(mul2(f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), ic2)));
+        sv[k] = __float_as_uint(t.x);
+        sv[k + 1] = __float_as_uint(t.y);
+      }
+    } else {
+      const float y2 = inv_cap * 2.8853900817779268f;
+#pragma unroll
+      for (int k = 0; k < 64; ++k) sv[k] = __float_as_uint(tanh_any(__uint_as_float(sv[k]) * y2));
+    }
+  }
+  const float cs = CAP ? cap_log2 : scale_log2;
+  const uint64_t cs2 = f2(cs, cs), one2 = f2(1.f, 1.f);
+#pragma unroll
+  for (int k = 0; k < 64; k += 2) {
+    const uint64_t u2 = f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]));
+    const float2 e = f2split(fma2(u2, cs2, add(k)));
+    float p0 = ex2(e.x), p1 = ex2(e.y);
+    if (!all) {
+      p0 = on(k) ? p0 : 0.f;
+      p1 = on(k + 1) ? p1 : 0.f;
+    }
+    if constexpr (WANT_P) pk[k / 2] = pack_bf16(p0, p1);
+    if constexpr (CAP) {
+      // 1 - u^2, then times P; a masked u may be NaN
+      const float2 f = f2split(fma2(u2 ^ 0x8000000080000000ull, u2, one2));
+      pe[k] = all || p0 != 0.f ? p0 * f.x : 0.f;
+      pe[k + 1] = all || p1 != 0.f ? p1 * f.y : 0.f;
+    } else {
+      pe[k] = p0;
+      pe[k + 1] = p1;
+    }
+  }
+}
+
+// ===========================================================================
+// dK / dV
+// ===========================================================================
+// Shared memory of dK/dV: (d > 80) K, V and their extra chunks; the stages of
+// Q, dO, the 128 queries' 16-byte extra rows, their windows and (with a cap)
+// -LSE log2(e); then zeros, the upper half of the extra contraction step.
+// TMEM: S^T [0, 128) and dP^T [128, 256) as two 64-column buffers each, dV at
+// 256, dK at 256 + D, and for d <= 80 K and V with their extra chunks.
+template <int D>
+struct ModDkdvCfg {
+  using T = TileGeom<D>;
+  static constexpr bool KV_TMEM = D <= 80;
+  static constexpr int AUX = 128 * 16;                 // 128 rows x 8 bf16
+  static constexpr int KV = KV_TMEM ? 0 : 2 * T::TILE + 2 * AUX;  // K, V, K extra, V extra
+  static constexpr int REC = 2 * T::TILE + AUX;        // offset of the windows
+  static constexpr int NL2 = REC + (int)sizeof(WinRecord);
+  static constexpr int STAGE = REC + 2048;             // 1024-byte aligned tiles
+  static_assert(sizeof(WinRecord) + 128 * 4 <= 2048, "the stage's tail");
+  static constexpr int ZERO = 2048;                    // the upper 8 columns
+  static constexpr int QS_FIT = (232448 - KV - ZERO - 1024 - 256) / STAGE;
+  static constexpr int QS = QS_FIT > 4 ? 4 : QS_FIT;
+  static constexpr int SMEM = KV + QS * STAGE + ZERO + 1024 + 256;
+  static constexpr uint32_t COL_DV = 256, COL_DK = 256 + D, COL_K = 256 + 2 * D, COL_V = 256 + 2 * D + D / 2 + 8;
+};
+
+// One CTA per 128-row key tile of one key/value head, over the G query heads of
+// its group and the query tiles that see it.  A step covers 64 queries:
+// sub-tile u is the half u % 2 of stage u / 2 and uses buffer u % 2; compute
+// warps 2..5 take the even sub-tiles, 6..9 the odd ones, with issuing warps 1
+// and 10, in the order S(u), dP(u), dV(u) (after P^T(u)), S(u+2), dK(u) (after
+// dS^T(u)), dP(u+2): what overwrites a buffer comes after its reader from the
+// same thread.  P^T is written over S^T and dS^T over dP^T as bf16 pairs, the
+// A operands of dV = P^T dO and dK = dS^T Q.  Both issuers add into dV and dK,
+// which the compute warps zero first.
+template <int D, bool CAP>
+__global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_constant__ ModBwdParams p) {
+  using T = TileGeom<D>;
+  using C = ModDkdvCfg<D>;
+  constexpr int QS = C::QS;
+  constexpr int STAGE = C::STAGE;
+  static_assert(C::COL_DK + D <= 512, "TMEM columns");
+  static_assert(!C::KV_TMEM || C::COL_V + D / 2 + 8 <= 512, "TMEM columns");
+  static_assert(QS >= 2, "Q/dO ring");
+  constexpr uint32_t ID_S = idesc_bf16(128, 64, false, false);
+  constexpr uint32_t ID_KV = idesc_bf16(128, D, false, true);
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKV = smem;                  // K, V, their extra chunks (head dims above 80)
+  uint8_t* sStage = smem + C::KV;
+  uint8_t* sZero = sStage + QS * STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sZero + C::ZERO);
+  uint64_t* kv_ready = bars;            // K', V' in place, dV, dK zeroed (8 compute warps)
+  uint64_t* qdo_full = bars + 1;        // [QS]
+  uint64_t* qdo_empty = qdo_full + QS;  // [QS], both issuers
+  uint64_t* s_full = qdo_empty + QS;    // [2] S^T(u) in buffer u % 2
+  uint64_t* dp_full = s_full + 2;       // [2]
+  uint64_t* p_full = dp_full + 2;       // [2] P^T(u) written (4 warps of the group)
+  uint64_t* ds_full = p_full + 2;       // [2] dS^T(u) written (4 warps)
+  uint64_t* all_done = ds_full + 2;     // both issuers' last products done
+  uint64_t* drain = all_done + 1;       // [2], one per issuer
+  uint64_t* kv_full = drain + 2;        // K, V tiles landed (shared-memory variant)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(kv_full + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* range = reinterpret_cast<int*>(tmem_holder + 2);  // first and last query tile that sees the key tile
+
+  const int warp = warp_id();
+  const int lane = lane_id();
+  // head-major, heaviest key tiles (smallest j) of a KV head first, so the
+  // CTAs in flight share that head's Q/dO stream in L2
+  const int nq_total = (p.s + 127) / 128;
+  const int pair = blockIdx.x / nq_total;
+  const int j = blockIdx.x % nq_total;
+  const int g = pair % p.Hkv;
+  const int bi = pair / p.Hkv;
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_ready, 8);
+    for (int i = 0; i < QS; ++i) {
+      mbar_init(&qdo_full[i], 1);
+      mbar_init(&qdo_empty[i], 2);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&dp_full[b], 1);
+      mbar_init(&p_full[b], 4);
+      mbar_init(&ds_full[b], 4);
+      mbar_init(&drain[b], 1);
+    }
+    mbar_init(all_done, 2);
+    mbar_init(kv_full, 1);
+    *abort_flag = 0;
+    range[0] = INT32_MAX;
+    range[1] = -1;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch(&p.map_qkv);
+    tma_prefetch(&p.map_do);
+    tma_prefetch(&p.map_aux);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x < C::ZERO / 16) {
+    reinterpret_cast<uint4*>(sZero)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  {
+    // query tiles with a row that may see this key tile; tiles between the
+    // first and the last that see nothing of it are masked like any other
+    int first = INT32_MAX, last = -1;
+    for (int i = threadIdx.x; i < nq_total; i += blockDim.x) {
+      const int2 w = p.span[(long long)bi * nq_total + i];
+      if (w.x < (j + 1) * 128 && w.y > j * 128) {
+        first = min(first, i);
+        last = max(last, i);
+      }
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0 && last >= 0) {
+      atomicMin(&range[0], first);
+      atomicMax(&range[1], last);
+    }
+    __syncthreads();
+  }
+  const int i0 = range[0];
+  const int n_i = range[1] < 0 ? 0 : range[1] - i0 + 1;
+  const int T_iter = p.G * n_i;  // stages
+  const int U = 2 * T_iter;      // sub-tiles
+  const uint32_t tS = tmem;          // + 64 b
+  const uint32_t tdP = tmem + 128;   // + 64 b
+  const uint32_t tdV = tmem + C::COL_DV;
+  const uint32_t tdK = tmem + C::COL_DK;
+  const uint32_t tKA = tmem + C::COL_K;
+  const uint32_t tVA = tmem + C::COL_V;
+
+  if (warp == 0) {
+    if (lane == 0 && U > 0) {
+      // ------------------------------------------------ TMA producer
+      if constexpr (!C::KV_TMEM) {
+        mbar_expect_tx(kv_full, 2 * T::TILE);
+#pragma unroll
+        for (int c = 0; c < T::NCH; ++c) {
+          tma_load_3d(sKV + c * T::CHUNK, &p.map_qkv, kv_full, p.k_col + g * D + c * T::CW, j * 128, bi);
+          tma_load_3d(sKV + T::TILE + c * T::CHUNK, &p.map_qkv, kv_full, p.v_col + g * D + c * T::CW, j * 128,
+                      bi);
+        }
+      }
+      int issued = 0;
+      for (int t = 0; t < T_iter; ++t) {
+        const int st = t % QS;
+        if (t >= QS && !bounded_wait(&qdo_empty[st], ((t / QS) & 1) ^ 1, abort_flag, 701, p.err)) break;
+        const int hn = g * p.G + t / n_i;
+        const int i = i0 + t % n_i;
+        uint8_t* sQ = sStage + st * STAGE;
+        uint8_t* sdO = sQ + T::TILE;
+        mbar_expect_tx(&qdo_full[st], C::REC + (int)sizeof(WinRecord) + (CAP ? 512 : 0));
+#pragma unroll
+        for (int c = 0; c < T::NCH; ++c) {
+          tma_load_3d(sQ + c * T::CHUNK, &p.map_qkv, &qdo_full[st], hn * D + c * T::CW, i * 128, bi);
+          tma_load_3d(sdO + c * T::CHUNK, &p.map_do, &qdo_full[st], hn * D + c * T::CW, i * 128, bi);
+        }
+        const int row = (bi * p.H + hn) * p.s_pad + i * 128;
+        tma_load_2d(sQ + 2 * T::TILE, &p.map_aux, &qdo_full[st], 0, row);
+        bulk_load(sQ + C::REC, p.rec + (long long)bi * nq_total + i, sizeof(WinRecord), &qdo_full[st]);
+        if constexpr (CAP) bulk_load(sQ + C::NL2, p.nl2 + row, 512, &qdo_full[st]);
+        issued = t + 1;
+      }
+      if (*abort_flag) {
+        if constexpr (!C::KV_TMEM) drain_wait(kv_full, 0);
+        for (int t = (issued > QS ? issued - QS : 0); t < issued; ++t)
+          drain_wait(&qdo_full[t % QS], (t / QS) & 1);
+      }
+    }
+  } else if (warp == 1 || warp == 10) {
+    // the whole warp runs the issue loop, one elected lane issues.  One
+    // issuer (fixed-order mode): warp 1 issues every sub-tile's products
+    // in sub-tile order, so dV and dK take their products in a fixed order
+    if (U > 0 && !(p.one_issuer && warp == 10)) {
+      // ------------------------------------------------ MMA issuers
+      const int b0 = warp == 1 ? 0 : 1;  // this issuer's first sub-tile
+      const int ustep = p.one_issuer ? 1 : 2;
+      const uint32_t uZero = smem_u32(sZero);
+      // the 64 query rows of sub-tile half b start 64 b rows into every
+      // chunk of the stage's tiles (whole swizzle atoms), and 64 b rows into
+      // its extra rows; sub-tile u uses buffer b = u % 2
+      auto stage_u = [&](int u) { return smem_u32(sStage + ((u >> 1) % QS) * STAGE); };
+      // K, V and their extra chunks in shared memory (head dims above 80):
+      // the extra chunk is 128 rows of 16 bytes, K-major core matrices
+      // without swizzle, its upper 8 columns the zeros
+      const uint32_t uK = smem_u32(sKV), uV = uK + T::TILE;
+      const uint32_t uKx = uK + 2 * T::TILE, uVx = uKx + C::AUX;
+      auto issue_s = [&](int u) {
+        const int b = u & 1;
+        const uint32_t tSb = tS + 64 * b;
+        const uint32_t uQ = stage_u(u) + 64 * T::SWB * b;
+        const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
+        if constexpr (C::KV_TMEM) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tKA + kk * 8, T::kmajor(uQ, kk), ID_S, kk > 0);
+          umma_bf16_tmem_a_w(tSb, tKA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) umma_bf16_w(tSb, T::kmajor(uK, kk), T::kmajor(uQ, kk), ID_S, kk > 0);
+          umma_bf16_w(tSb, sdesc(uKx, uZero - uKx, 128, 0u), sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+        }
+        umma_commit_w(&s_full[b]);
+      };
+      auto issue_dp = [&](int u) {
+        const int b = u & 1;
+        const uint32_t tdPb = tdP + 64 * b;
+        const uint32_t udO = stage_u(u) + T::TILE + 64 * T::SWB * b;
+        const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
+        if constexpr (C::KV_TMEM) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_tmem_a_w(tdPb, tVA + kk * 8, T::kmajor(udO, kk), ID_S, kk > 0);
+          umma_bf16_tmem_a_w(tdPb, tVA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) umma_bf16_w(tdPb, T::kmajor(uV, kk), T::kmajor(udO, kk), ID_S, kk > 0);
+          umma_bf16_w(tdPb, sdesc(uVx, uZero - uVx, 128, 0u), sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+        }
+        umma_commit_w(&dp_full[b]);
+      };
+      auto wait_stage = [&](int u) {
+        const int t = u >> 1;
+        return bounded_wait_w(&qdo_full[t % QS], (t / QS) & 1, abort_flag, 711, p.err);
+      };
+      bool ok = bounded_wait_w(kv_ready, 0, abort_flag, 712, p.err) &&
+                (C::KV_TMEM || bounded_wait_w(kv_full, 0, abort_flag, 716, p.err)) && wait_stage(b0);
+      if (ok) {
+        tc_fence_after();
+        // sub-tiles 0 and 1 share stage 0 (U is even)
+        for (int u = b0; u < 2; u += ustep) {
+          issue_s(u);
+          issue_dp(u);
+        }
+      }
+      for (int u = b0; ok && u < U; u += ustep) {
+        const int b = u & 1;
+        const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
+        const int st = (u >> 1) % QS;
+        const uint32_t uQ = stage_u(u);
+        const uint32_t udO = uQ + T::TILE;
+        const bool more = u + 2 < U;
+        // dV += P^T(u) dO(u): the P^T pairs sit over the first 32 columns of
+        // buffer b; dO rows 64b.. are K blocks 4b..4b+3 of the stage's tile
+        if (!bounded_wait_w(&p_full[b], (u >> 1) & 1, abort_flag, 713, p.err)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16_tmem_a_w(tdV, tSb + kk * 8, T::mnmajor(udO, 4 * b + kk), ID_KV, 1);
+        if (more) {
+          // S(u+2) overwrites P^T(u), after dV(u) in issue order
+          if (!wait_stage(u + 2)) { ok = false; break; }
+          tc_fence_after();
+          issue_s(u + 2);
+        }
+        // dK += dS^T(u) Q(u)
+        if (!bounded_wait_w(&ds_full[b], (u >> 1) & 1, abort_flag, 714, p.err)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16_tmem_a_w(tdK, tdPb + kk * 8, T::mnmajor(uQ, 4 * b + kk), ID_KV, 1);
+        umma_commit_w(&qdo_empty[st]);
+        // dP(u+2) overwrites dS^T(u), after dK(u) in issue order
+        if (more) issue_dp(u + 2);
+      }
+      if (ok) {
+        // all_done counts two commits: one per issuer, or both from one
+        umma_commit_w(all_done);
+        if (p.one_issuer) umma_commit_w(all_done);
+      }
+      if (!ok) {
+        umma_commit_w(&drain[b0]);
+        drain_wait(&drain[b0], 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------ compute (warps 2..9;
+    // warp 10 in the one-issuer mode falls through to the final barrier)
+    const int quarter = warp & 3;
+    const int b = (warp - 2) >> 2;  // group = buffer = sub-tile parity
+    const int r = quarter * 32 + lane;
+    const int kvp = j * 128 + r;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    if constexpr (!C::KV_TMEM) {
+      // the extra chunk of this thread's K row (group 0: 1 in columns 0..2)
+      // or V row (group 1: in columns 3..5), which pick the three terms of
+      // -LSE sqrt(d) and of -D from the query's extra row; and the group's
+      // accumulator (dV, dK) zeroed: both issuers add into it
+      reinterpret_cast<uint4*>(sKV + 2 * T::TILE + b * C::AUX)[r] =
+          b ? make_uint4(0u, 0x3F800000u, 0x3F803F80u, 0u) : make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u);
+      fence_proxy_async_smem();
+      uint32_t z[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) z[c] = 0u;
+#pragma unroll
+      for (int cc = 0; cc < D / 16; ++cc) tmem_st16_nw((b ? tdK : tdV) + lane_off + cc * 16, z);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kv_ready);
+    } else {
+      // K (group 0) or V (group 1) row of this thread into TMEM as bf16
+      // pairs with the extra chunk (rows past the sequence are zero), and
+      // the group's accumulator (dV, dK) zeroed: both issuers add into it
+      uint32_t w[D / 2 + 8];
+      const __nv_bfloat16* src = p.qkv + ((long long)bi * p.s + kvp) * p.width + (b ? p.v_col : p.k_col) +
+                                 (long long)g * D;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (kvp < p.s) v = *reinterpret_cast<const uint4*>(src + c * 8);
+        w[4 * c] = v.x;
+        w[4 * c + 1] = v.y;
+        w[4 * c + 2] = v.z;
+        w[4 * c + 3] = v.w;
+      }
+      // the extra chunk: K picks the three terms of -LSE sqrt(d) (columns
+      // 0..2 of the query's extra row), V those of -D (columns 3..5)
+      w[D / 2] = b ? 0u : 0x3F803F80u;
+      w[D / 2 + 1] = b ? 0x3F800000u : 0x00003F80u;
+      w[D / 2 + 2] = b ? 0x3F803F80u : 0u;
+#pragma unroll
+      for (int c = 3; c < 8; ++c) w[D / 2 + c] = 0u;
+      tmem_store_row<D / 2 + 8>((b ? tVA : tKA) + lane_off, w);
+      uint32_t z[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) z[c] = 0u;
+#pragma unroll
+      for (int cc = 0; cc < D / 16; ++cc) tmem_st16_nw((b ? tdK : tdV) + lane_off + cc * 16, z);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kv_ready);
+    }
+    const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
+    const bool bias = p.slopes != nullptr;
+    bool ok = true;
+    for (int u = b; u < U; u += 2) {
+      const int t = u >> 1;
+      const int q0 = (i0 + t % n_i) * 128 + 64 * b;
+      const uint8_t* stage = sStage + (t % QS) * STAGE;
+      // the stage's windows and -LSE's are read below: its copies have landed
+      // (the scores' products waited for them), seen here by this thread too
+      ok = bounded_wait(&qdo_full[t % QS], (t / QS) & 1, abort_flag, 724, p.err) &&
+           bounded_wait(&s_full[b], (u >> 1) & 1, abort_flag, 721, p.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc_fence_after();
+      // ---- phase 1: P^T = exp2 of the modified scores - LSE log2(e)
+      const WinRecord* rec = reinterpret_cast<const WinRecord*>(stage + C::REC);
+      const float* nl2 = reinterpret_cast<const float*>(stage + C::NL2) + 64 * b;
+      const int2 cut = rec->cut[b];
+      const bool all = cut.x <= j * 128 && cut.y >= j * 128 + 128;
+      const int2* win = rec->row + 64 * b;
+      float pe[64];
+      uint32_t pk[32];
+      {
+        uint32_t sv[64];
+        tmem_ld32_nw(tSb + lane_off, sv);
+        tmem_ld32_nw(tSb + lane_off + 32, sv + 32);
+        tmem_wait_ld(sv);
+        auto on = [&](int x) {
+          const int2 w = win[x];
+          return (unsigned)(kvp - w.x) < (unsigned)w.y;
+        };
+        auto lse2 = [&](int x) -> uint64_t {
+          if constexpr (CAP) return *reinterpret_cast<const uint64_t*>(nl2 + x);
+          else return 0ull;
+        };
+        if (!bias) {
+          probabilities<CAP, true>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, lse2, on);
+        } else {
+          const float slope2 = p.slopes[g * p.G + t / n_i] * 1.4426950408889634f;
+          // along the queries; with a causal mask those before the key are masked
+          const BiasLine bl = bias_line(slope2, kvp, q0, false, p.causal != 0);
+          if (!__any_sync(0xffffffffu, bl.mixed)) {
+            auto add = [&](int x) {
+              return add2(lse2(x), f2(fmaf(bl.step, (float)x, bl.base), fmaf(bl.step, (float)(x + 1), bl.base)));
+            };
+            probabilities<CAP, true>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+          } else {
+            const float dist = (float)(kvp - q0);
+            auto add = [&](int x) {
+              return add2(lse2(x), f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
+            };
+            probabilities<CAP, true>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+          }
+        }
+      }
+      tmem_st32(tSb + lane_off, pk);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[b]);
+      // ---- phase 2: dx^T = P^T (1 - u^2) dP'^T (dP' offset by -D)
+      ok = bounded_wait(&dp_full[b], (u >> 1) & 1, abort_flag, 722, p.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t dr[64];
+      tmem_ld32_nw(tdPb + lane_off, dr);
+      tmem_ld32_nw(tdPb + lane_off + 32, dr + 32);
+      tmem_wait_ld(dr);
+      uint32_t o[32];
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        const float2 v = f2split(mul2(f2(pe[k], pe[k + 1]), f2(__uint_as_float(dr[k]), __uint_as_float(dr[k + 1]))));
+        o[k / 2] = pack_bf16(v.x, v.y);
+      }
+      tmem_st32(tdPb + lane_off, o);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[b]);
+    }
+    // epilogue: group 0 writes dV, group 1 dK, once both issuers' products
+    // are done (TMEM loads by every lane, stores only for rows inside the
+    // sequence)
+    if (U == 0) {
+      // nothing sees this key tile
+      if (kvp < p.s) {
+        uint4* row = reinterpret_cast<uint4*>(p.dqkv + ((long long)bi * p.s + kvp) * p.width +
+                                              (b == 0 ? p.v_col : p.k_col) + (long long)g * D);
+#pragma unroll
+        for (int cc = 0; cc < D / 8; ++cc) row[cc] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      ok = false;
+    }
+    if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, 0, abort_flag, 723, p.err));
+    if (ok) {
+      tc_fence_after();
+      const bool valid = kvp < p.s;
+      const uint32_t tsrc = (b == 0 ? tdV : tdK) + lane_off;
+      __nv_bfloat16* row = p.dqkv + ((long long)bi * p.s + kvp) * p.width +
+                           (b == 0 ? p.v_col : p.k_col) + (long long)g * D;
+      const float sc = b == 0 ? 1.f : p.scale;
+      if constexpr (D <= 80) {
+        uint32_t acc[D];
+#pragma unroll
+        for (int cc = 0; cc < D / 16; ++cc) tmem_ld16_nw(tsrc + cc * 16, acc + cc * 16);
+        tmem_wait_ld(acc);
+        if (valid) {
+#pragma unroll
+          for (int cc = 0; cc < D / 16; ++cc) store_row16(row + cc * 16, acc + cc * 16, sc);
+        }
+      } else {
+        for (int cc = 0; cc < D / 16; ++cc) {
+          uint32_t v[16];
+          tmem_ld16_nw(tsrc + cc * 16, v);
+          tmem_wait_ld(v);
+          if (valid) store_row16(row + cc * 16, v, sc);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ===========================================================================
+// dQ
+// ===========================================================================
+// Shared memory of the dQ kernel: the K/V ring.
+template <int D>
+struct ModDqCfg {
+  using T = TileGeom<D>;
+  static constexpr int KVS_FIT = (232448 - 1280) / (2 * T::TILE);
+  static constexpr int KVS = KVS_FIT > 5 ? 5 : KVS_FIT;
+  static constexpr int SMEM = KVS * 2 * T::TILE + 1024 + 256;
+};
+
+// One CTA per 128-row query tile of one head, over the key tiles that some row
+// of it sees, in 64-key sub-tiles: sub-tile u is the half u % 2 of tile u / 2.
+// Q and dO sit in TMEM as the A operands of S = Q K^T and dP = dO V^T; dS goes
+// over the first 32 columns of its dP buffer as the A operand of dQ += dS K.
+// Compute warps 2..5 take the even sub-tiles, 6..9 the odd ones, with issuing
+// warps 1 and 10: S(u), dP(u), S(u+2) (once S(u) is read), dQ(u) (after
+// dS(u)), dP(u+2).  A row's window, LSE and D are scalars of its thread.
+// TMEM: S [0, 128), dP [128, 256) as two 64-column buffers each, dQ at 256,
+// Q at 256 + D, dO at 256 + 1.5 D.
+template <int D, bool CAP>
+__global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_constant__ ModBwdParams p) {
+  using T = TileGeom<D>;
+  using C = ModDqCfg<D>;
+  constexpr int KVS = C::KVS;
+  static_assert(256 + 2 * D <= 512, "TMEM columns");
+  constexpr uint32_t ID_S = idesc_bf16(128, 64, false, false);
+  constexpr uint32_t ID_DQ = idesc_bf16(128, D, false, true);
+  constexpr uint32_t COL_DQ = 256, COL_Q = 256 + D, COL_DO = 256 + D + D / 2;
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKV = smem;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + KVS * 2 * T::TILE);
+  uint64_t* qo_ready = bars;           // Q, dO in TMEM and dQ zeroed (8 compute warps)
+  uint64_t* kv_full = bars + 1;        // [KVS]
+  uint64_t* kv_empty = kv_full + KVS;  // [KVS], both issuers
+  uint64_t* s_full = kv_empty + KVS;   // [2] S(u) in buffer u % 2
+  uint64_t* s_free = s_full + 2;       // [2] S(u) read (4 warps of the group)
+  uint64_t* dp_full = s_free + 2;      // [2]
+  uint64_t* ds_full = dp_full + 2;     // [2] dS(u) written (4 warps)
+  uint64_t* all_done = ds_full + 2;    // both issuers' last products done
+  uint64_t* drain = all_done + 1;      // [2], one per issuer
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = warp_id();
+  const int lane = lane_id();
+  // head-major, heaviest query tiles of a head first; the query heads of one
+  // KV group are adjacent, so the CTAs in flight share K/V in L2
+  const int n_qt = (p.s + 127) / 128;
+  const int pair = blockIdx.x / n_qt;
+  const int i = n_qt - 1 - (int)(blockIdx.x % n_qt);
+  const int n = pair % p.H;
+  const int bi = pair / p.H;
+  const int g = n / p.G;
+  const int q0 = i * 128;
+  // key tiles [j0, j0 + nkv) hold every key that some row sees
+  const int2 span = p.span[(long long)bi * n_qt + i];
+  const int j0 = span.x < span.y ? span.x / 128 : 0;
+  const int nkv = span.x < span.y ? (span.y + 127) / 128 - j0 : 0;
+  const int U = 2 * nkv;
+
+  if (threadIdx.x == 0) {
+    mbar_init(qo_ready, 8);
+    for (int k = 0; k < KVS; ++k) {
+      mbar_init(&kv_full[k], 1);
+      mbar_init(&kv_empty[k], 2);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], 4);
+      mbar_init(&dp_full[b], 1);
+      mbar_init(&ds_full[b], 4);
+      mbar_init(&drain[b], 1);
+    }
+    mbar_init(all_done, 2);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) tma_prefetch(&p.map_qkv);
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t tS = tmem;         // + 64 b
+  const uint32_t tdP = tmem + 128;  // + 64 b
+  const uint32_t tdQ = tmem + COL_DQ;
+  const uint32_t tQA = tmem + COL_Q;
+  const uint32_t tOA = tmem + COL_DO;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------ TMA producer
+      int issued = 0;
+      for (int jt = 0; jt < nkv; ++jt) {
+        const int st = jt % KVS;
+        if (jt >= KVS && !bounded_wait(&kv_empty[st], ((jt / KVS) & 1) ^ 1, abort_flag, 731, p.err)) break;
+        uint8_t* sK = sKV + st * 2 * T::TILE;
+        uint8_t* sV = sK + T::TILE;
+        mbar_expect_tx(&kv_full[st], 2 * T::TILE);
+#pragma unroll
+        for (int c = 0; c < T::NCH; ++c) {
+          tma_load_3d(sK + c * T::CHUNK, &p.map_qkv, &kv_full[st], p.k_col + g * D + c * T::CW, (j0 + jt) * 128, bi);
+          tma_load_3d(sV + c * T::CHUNK, &p.map_qkv, &kv_full[st], p.v_col + g * D + c * T::CW, (j0 + jt) * 128, bi);
+        }
+        issued = jt + 1;
+      }
+      if (*abort_flag) {
+        for (int jt = (issued > KVS ? issued - KVS : 0); jt < issued; ++jt)
+          drain_wait(&kv_full[jt % KVS], (jt / KVS) & 1);
+      }
+    }
+  } else if (warp == 1 || warp == 10) {
+    // the whole warp runs the issue loop, one elected lane issues.  One
+    // issuer (fixed-order mode): warp 1 issues every sub-tile's products
+    // in sub-tile order, so dQ takes its products in a fixed order
+    if (U > 0 && !(p.one_issuer && warp == 10)) {
+      // ------------------------------------------------ MMA issuers
+      const int b0 = warp == 1 ? 0 : 1;  // this issuer's first sub-tile
+      const int ustep = p.one_issuer ? 1 : 2;
+      const uint32_t uKV = smem_u32(sKV);
+      // the 64 key rows of half b start 64 b rows into every chunk of the
+      // stage's K and V tiles (whole swizzle atoms); sub-tile u uses buffer
+      // b = u % 2
+      auto uK = [&](int u) { return uKV + ((u >> 1) % KVS) * 2 * T::TILE; };
+      auto issue_s = [&](int u) {
+        const int b = u & 1;
+        const uint32_t tSb = tS + 64 * b;
+        const uint32_t k = uK(u) + 64 * T::SWB * b;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tQA + kk * 8, T::kmajor(k, kk), ID_S, kk > 0);
+        umma_commit_w(&s_full[b]);
+      };
+      auto issue_dp = [&](int u) {
+        const int b = u & 1;
+        const uint32_t tdPb = tdP + 64 * b;
+        const uint32_t v = uK(u) + T::TILE + 64 * T::SWB * b;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tdPb, tOA + kk * 8, T::kmajor(v, kk), ID_S, kk > 0);
+        umma_commit_w(&dp_full[b]);
+      };
+      auto wait_stage = [&](int u) {
+        const int jt = u >> 1;
+        return bounded_wait_w(&kv_full[jt % KVS], (jt / KVS) & 1, abort_flag, 741, p.err);
+      };
+      bool ok = bounded_wait_w(qo_ready, 0, abort_flag, 742, p.err) && wait_stage(b0);
+      if (ok) {
+        tc_fence_after();
+        // sub-tiles 0 and 1 share stage 0 (U is even)
+        for (int u = b0; u < 2; u += ustep) {
+          issue_s(u);
+          issue_dp(u);
+        }
+      }
+      for (int u = b0; ok && u < U; u += ustep) {
+        const int b = u & 1;
+        const uint32_t tdPb = tdP + 64 * b;
+        const int st = (u >> 1) % KVS;
+        const bool more = u + 2 < U;
+        if (more) {
+          // S(u+2) once the group has read S(u)
+          if (!bounded_wait_w(&s_free[b], (u >> 1) & 1, abort_flag, 743, p.err) || !wait_stage(u + 2)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          issue_s(u + 2);
+        }
+        // dQ += dS(u) K_u: key rows 64b.. are K blocks 4b..4b+3 of the tile
+        if (!bounded_wait_w(&ds_full[b], (u >> 1) & 1, abort_flag, 744, p.err)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16_tmem_a_w(tdQ, tdPb + kk * 8, T::mnmajor(uK(u), 4 * b + kk), ID_DQ, 1);
+        umma_commit_w(&kv_empty[st]);
+        // dP(u+2) overwrites dS(u), after dQ(u) in issue order
+        if (more) issue_dp(u + 2);
+      }
+      if (ok) {
+        // all_done counts two commits: one per issuer, or both from one
+        umma_commit_w(all_done);
+        if (p.one_issuer) umma_commit_w(all_done);
+      }
+      if (!ok) {
+        umma_commit_w(&drain[b0]);
+        drain_wait(&drain[b0], 0);
+      }
+    }
+  } else {
+    // ------------------------------------------------ compute (warps 2..9;
+    // warp 10 in the one-issuer mode falls through to the final barrier)
+    const int quarter = warp & 3;
+    const int b = (warp - 2) >> 2;  // group = buffer = sub-tile parity
+    const int r = quarter * 32 + lane;
+    const int qpos = q0 + r;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    {
+      // Q (group 0) or dO (group 1) row of this thread into TMEM as bf16
+      // pairs (rows past the sequence are zero); group 0 also zeroes dQ
+      uint32_t w[D / 2];
+      const __nv_bfloat16* src = b == 0
+          ? p.qkv + ((long long)bi * p.s + qpos) * p.width + (long long)n * D
+          : p.dout + ((long long)bi * p.s + qpos) * p.H * D + (long long)n * D;
+#pragma unroll
+      for (int cc = 0; cc < D / 8; ++cc) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (qpos < p.s) v = *reinterpret_cast<const uint4*>(src + cc * 8);
+        w[4 * cc] = v.x;
+        w[4 * cc + 1] = v.y;
+        w[4 * cc + 2] = v.z;
+        w[4 * cc + 3] = v.w;
+      }
+      tmem_store_row<D / 2>((b == 0 ? tQA : tOA) + lane_off, w);
+      if (b == 0) {
+        uint32_t z[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) z[k] = 0u;
+#pragma unroll
+        for (int cc = 0; cc < D / 16; ++cc) tmem_st16_nw(tdQ + lane_off + cc * 16, z);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qo_ready);
+    }
+    const int2 win = key_window(p.row_begin, p.row_end, p.causal, p.s, bi, qpos);
+    const bool bias = p.slopes != nullptr;
+    const float slope2 = bias ? p.slopes[n] * 1.4426950408889634f : 0.f;
+    // this row's -LSE*log2(e) and dO.O sum (finite filler past the sequence)
+    const float nl = p.nl2[((long long)bi * p.H + n) * p.s_pad + qpos];
+    const float dsum = p.dsum[((long long)bi * p.H + n) * p.s_pad + qpos];
+    const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
+    bool ok = true;
+    for (int u = b; u < U; u += 2) {
+      ok = bounded_wait(&s_full[b], (u >> 1) & 1, abort_flag, 751, p.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc_fence_after();
+      // ---- phase 1: P (1 - u^2) of the 64 keys; [klo, khi) are visible
+      const int kv0 = (j0 + (u >> 1)) * 128 + 64 * b;
+      const int klo = max(win.x - kv0, 0), khi = min(win.y - kv0, 64);
+      uint32_t sv[64];
+      tmem_ld32_nw(tSb + lane_off, sv);
+      tmem_ld32_nw(tSb + lane_off + 32, sv + 32);
+      tmem_wait_ld(sv);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[b]);
+      float pe[64];
+      {
+        uint32_t pk[32];
+        const bool all = klo == 0 && khi == 64;
+        auto on = [&](int x) { return x >= klo && x < khi; };
+        const uint64_t nl2 = f2(nl, nl);
+        if (!bias) {
+          auto add = [&](int) { return nl2; };
+          probabilities<CAP, false>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+        } else {
+          const BiasLine bl = bias_line(slope2, qpos, kv0, p.causal != 0, false);
+          if (!__any_sync(0xffffffffu, bl.mixed)) {
+            auto add = [&](int x) {
+              return add2(nl2, f2(fmaf(bl.step, (float)x, bl.base), fmaf(bl.step, (float)(x + 1), bl.base)));
+            };
+            probabilities<CAP, false>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+          } else {
+            const float dist = (float)(qpos - kv0);
+            auto add = [&](int x) {
+              return add2(nl2, f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
+            };
+            probabilities<CAP, false>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+          }
+        }
+      }
+      // ---- phase 2: dS = P (dP - D), over the first 32 columns of buffer b
+      ok = bounded_wait(&dp_full[b], (u >> 1) & 1, abort_flag, 752, p.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t dr[64];
+      tmem_ld32_nw(tdPb + lane_off, dr);
+      tmem_ld32_nw(tdPb + lane_off + 32, dr + 32);
+      tmem_wait_ld(dr);
+      uint32_t o[32];
+      const uint64_t ds2 = f2(dsum, dsum);
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) {
+        const float2 v = f2split(
+            mul2(f2(pe[k], pe[k + 1]), sub2(f2(__uint_as_float(dr[k]), __uint_as_float(dr[k + 1])), ds2)));
+        o[k / 2] = pack_bf16(v.x, v.y);
+      }
+      tmem_st32(tdPb + lane_off, o);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[b]);
+    }
+    // epilogue: the two groups split dQ's 16-column chunks once both
+    // issuers' products are done
+    if (U == 0) {
+      // no row of the tile sees a key
+      if (b == 0 && qpos < p.s) {
+        uint4* row = reinterpret_cast<uint4*>(p.dqkv + ((long long)bi * p.s + qpos) * p.width + (long long)n * D);
+#pragma unroll
+        for (int cc = 0; cc < D / 8; ++cc) row[cc] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      ok = false;
+    }
+    if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, 0, abort_flag, 753, p.err));
+    if (ok) {
+      tc_fence_after();
+      constexpr int NC = D / 16;
+      constexpr int NC0 = (NC + 1) / 2;
+      const int cbeg = b == 0 ? 0 : NC0, cend = b == 0 ? NC0 : NC;
+      const bool valid = qpos < p.s;
+      __nv_bfloat16* qrow = p.dqkv + ((long long)bi * p.s + qpos) * p.width + (long long)n * D;
+      const uint32_t tq = tdQ + lane_off;
+      for (int cc = cbeg; cc < cend; ++cc) {
+        uint32_t v[16];
+        tmem_ld16_nw(tq + cc * 16, v);
+        tmem_wait_ld(v);
+        if (valid) store_row16(qrow + cc * 16, v, p.scale);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ===========================================================================
+// What both need of the rows
+// ===========================================================================
+// The first b * n_t blocks write the windows of one query tile each; the
+// others take (row, head) pairs, 16 lanes each: D = dO . O in fp32, and from
+// it and the log-sum-exp the per-row inputs of the two kernels.  A value as
+// three bf16 terms keeps 24 bits of it.
+__device__ __forceinline__ void three_terms(float v, uint32_t (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat16 h = __float2bfloat16(v);
+    t[i] = (uint32_t)__bfloat16_as_ushort(h);
+    v -= __bfloat162float(h);
+  }
+}
+
+__global__ void __launch_bounds__(256) attn_mod_prep_kernel(int b, int s, int n_t, int H, int d, int causal, int cap,
+                                                            float inv_scale, const int32_t* row_begin,
+                                                            const int32_t* row_end, const __nv_bfloat16* o,
+                                                            const __nv_bfloat16* dout, const float* lse,
+                                                            WinRecord* rec, int2* span, float* dsum, float* nl2,
+                                                            uint4* aux) {
+  const int s_pad = n_t * 128;
+  if ((int)blockIdx.x < b * n_t) {
+    __shared__ int part[4][4];
+    const int bi = blockIdx.x / n_t, t = blockIdx.x % n_t;
+    const int r = threadIdx.x;
+    WinRecord* out = rec + blockIdx.x;
+    if (r < 128) {
+      const int2 w = key_window(row_begin, row_end, causal, s, bi, t * 128 + r);
+      out->row[r] = make_int2(w.x, w.y - w.x);
+      const int lo = __reduce_min_sync(0xffffffffu, w.x < w.y ? w.x : INT32_MAX);
+      const int hi = __reduce_max_sync(0xffffffffu, w.y);
+      const int lo_cut = __reduce_max_sync(0xffffffffu, w.x), hi_cut = __reduce_min_sync(0xffffffffu, w.y);
+      if ((r & 31) == 0) {
+        part[r >> 5][0] = lo;
+        part[r >> 5][1] = hi;
+        part[r >> 5][2] = lo_cut;
+        part[r >> 5][3] = hi_cut;
+      }
+    }
+    __syncthreads();
+    if (r == 0) {
+      span[blockIdx.x] = make_int2(min(min(part[0][0], part[1][0]), min(part[2][0], part[3][0])),
+                                   max(max(part[0][1], part[1][1]), max(part[2][1], part[3][1])));
+      for (int h = 0; h < 2; ++h)
+        out->cut[h] = make_int2(max(part[2 * h][2], part[2 * h + 1][2]), min(part[2 * h][3], part[2 * h + 1][3]));
+      out->unused = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int64_t total = (int64_t)b * s_pad * H;
+  const int sub = threadIdx.x & 15;
+  const int64_t stride = (int64_t)(gridDim.x - b * n_t) * 16;
+  // whole half-warps step together: the shuffles below stay within one
+  for (int64_t it = (int64_t)(blockIdx.x - b * n_t) * 16 + (threadIdx.x >> 4); it < total; it += stride) {
+    const int hn = (int)(it % H);
+    const int64_t t = it / H;
+    const int q = (int)(t % s_pad);
+    const int bi = (int)(t / s_pad);
+    float acc = 0.f;
+    if (q < s && sub * 8 < d) {
+      const int64_t at = (((int64_t)bi * s + q) * H + hn) * d + sub * 8;
+      const uint4 x = *reinterpret_cast<const uint4*>(o + at), y = *reinterpret_cast<const uint4*>(dout + at);
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc = fmaf(bf16_lo(xw[k]), bf16_lo(yw[k]), fmaf(bf16_hi(xw[k]), bf16_hi(yw[k]), acc));
+    }
+    const unsigned mask = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+    for (int k = 8; k > 0; k >>= 1) acc += __shfl_xor_sync(mask, acc, k);
+    if (sub == 0) {
+      const int64_t row = ((int64_t)bi * H + hn) * s_pad + q;
+      float l = q < s ? lse[row] : 0.f;
+      if (l == -INFINITY) l = 0.f;  // a row that sees nothing: every P is masked
+      uint32_t a[3] = {0u, 0u, 0u}, c[3];
+      if (!cap) three_terms(-l * inv_scale, a);
+      three_terms(-acc, c);
+      dsum[row] = acc;
+      nl2[row] = -1.4426950408889634f * l;
+      aux[row] = make_uint4(a[0] | (a[1] << 16), a[2] | (c[0] << 16), c[1] | (c[2] << 16), 0u);
+    }
+  }
+}
+
+template <int D, bool CAP>
+int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
+  constexpr int SMEM_KV = ModDkdvCfg<D>::SMEM, SMEM_Q = ModDqCfg<D>::SMEM;
+  static_assert(SMEM_KV <= 232448 && SMEM_Q <= 232448, "tile sets exceed shared memory");
+  static std::atomic<uint64_t> attr_kv{0}, attr_q{0};  // devices whose limit is set
+  if (smem_limit_once(reinterpret_cast<const void*>(attn_mod_dkdv_kernel<D, CAP>), SMEM_KV, &attr_kv) ||
+      smem_limit_once(reinterpret_cast<const void*>(attn_mod_dq_kernel<D, CAP>), SMEM_Q, &attr_q))
+    return BPT_ECUDA;
+  {
+    ProfScope prof(PROF_ATTN_BWD, 8.0 * D * pairs * p.H * b, 0.0, st);
+    attn_mod_dkdv_kernel<D, CAP><<<p.n_t * p.Hkv * b, 352, SMEM_KV, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return BPT_ECUDA;
+  }
+  ProfScope prof(PROF_ATTN_BWD, 2.0 * D * pairs * p.H * b, 0.0, st);
+  attn_mod_dq_kernel<D, CAP><<<p.n_t * p.H * b, 352, SMEM_Q, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ECUDA;
+}
+
+struct ModBwdWs {
+  float *dsum, *nl2;
+  uint4* aux;
+  WinRecord* rec;
+  int2* span;
+};
+size_t plan(const PackedDims& D, void* base, ModBwdWs* w) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = base ? reinterpret_cast<uint8_t*>(base) + off : nullptr;
+    off += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  const size_t rows = (size_t)D.b * D.H * D.s_pad, tiles = (size_t)D.b * (D.s_pad / 128);
+  w->dsum = reinterpret_cast<float*>(take(rows * 4));
+  w->nl2 = reinterpret_cast<float*>(take(rows * 4));
+  w->aux = reinterpret_cast<uint4*>(take(rows * 16));
+  w->rec = reinterpret_cast<WinRecord*>(take(tiles * sizeof(WinRecord)));
+  w->span = reinterpret_cast<int2*>(take(tiles * sizeof(int2)));
+  return off;
+}
+
+}  // namespace
+
+size_t attention_mod_bwd_ws_bytes(const PackedDims& D) {
+  ModBwdWs w;
+  return plan(D, nullptr, &w);
+}
+
+int attention_mod_bwd(const PackedDims& D, int causal, const bpt_score_mod& mod, const void* qkv, const void* o,
+                      const float* lse, const void* dout, void* dqkv, void* ws, cudaStream_t st) {
+  ModBwdWs w;
+  plan(D, ws, &w);
+  const bool cap = mod.softcap > 0.f;
+  ModBwdParams p;
+  memset(&p, 0, sizeof(p));
+  const uint64_t rows = (uint64_t)D.b * D.H * D.s_pad;
+  if (make_attn_map(&p.map_qkv, qkv, (int)D.b, (int)D.s, D.width, (int)D.d) ||
+      make_attn_map(&p.map_do, dout, (int)D.b, (int)D.s, D.H * D.d, (int)D.d) ||
+      make_map_2d(&p.map_aux, w.aux, rows, 8, 8, 8, 128, 0))
+    return BPT_EINVAL;
+  p.s = (int)D.s;
+  p.s_pad = (int)D.s_pad;
+  p.H = (int)D.H;
+  p.Hkv = (int)D.Hkv;
+  p.G = (int)D.G;
+  p.causal = causal;
+  p.n_t = (int)(D.s_pad / 128);
+  p.k_col = (int)(D.H * D.d);
+  p.v_col = (int)((D.H + D.Hkv) * D.d);
+  p.dsum = w.dsum;
+  p.nl2 = w.nl2;
+  p.rec = w.rec;
+  p.span = w.span;
+  p.qkv = reinterpret_cast<const __nv_bfloat16*>(qkv);
+  p.dout = reinterpret_cast<const __nv_bfloat16*>(dout);
+  p.dqkv = reinterpret_cast<__nv_bfloat16*>(dqkv);
+  p.width = D.width;
+  p.row_begin = mod.row_begin;
+  p.row_end = mod.row_end;
+  p.slopes = mod.slopes;
+  p.scale = 1.f / sqrtf((float)D.d);
+  p.scale_log2 = p.scale * 1.4426950408889634f;
+  if (cap) {
+    p.inv_cap = p.scale / mod.softcap;
+    p.cap_log2 = mod.softcap * 1.4426950408889634f;
+  }
+  p.one_issuer = D.det ? 1 : 0;
+  p.err = device_error_word();
+  if (!p.err) return BPT_ECUDA;
+  const int nsm = sm_count();
+  if (nsm <= 0) return BPT_ECUDA;
+  const int tiles = (int)(D.b * p.n_t);
+  {
+    ProfScope prof(PROF_MISC, 0.0, 4.0 * D.rows * D.H * D.d + 28.0 * rows, st);
+    const int64_t pairs = (int64_t)rows;
+    const int blocks = (int)std::min<int64_t>((pairs + 15) / 16, (int64_t)nsm * 16);
+    attn_mod_prep_kernel<<<tiles + blocks, 256, 0, st>>>(
+        (int)D.b, p.s, p.n_t, p.H, (int)D.d, causal, cap, sqrtf((float)D.d), p.row_begin, p.row_end,
+        reinterpret_cast<const __nv_bfloat16*>(o), p.dout, lse, w.rec, w.span, w.dsum, w.nl2, w.aux);
+    if (cudaGetLastError() != cudaSuccess) return BPT_ECUDA;
+  }
+  // credited as without windows, which live on the device
+  const double pairs = causal ? (double)D.s * (D.s + 1) / 2 : (double)D.s * D.s;
+  const int b = (int)D.b;
+  switch (D.d) {
+    case 64: return cap ? launch_both<64, true>(p, b, pairs, st) : launch_both<64, false>(p, b, pairs, st);
+    case 80: return cap ? launch_both<80, true>(p, b, pairs, st) : launch_both<80, false>(p, b, pairs, st);
+    case 96: return cap ? launch_both<96, true>(p, b, pairs, st) : launch_both<96, false>(p, b, pairs, st);
+    case 112: return cap ? launch_both<112, true>(p, b, pairs, st) : launch_both<112, false>(p, b, pairs, st);
+    case 128: return cap ? launch_both<128, true>(p, b, pairs, st) : launch_both<128, false>(p, b, pairs, st);
+    default: return BPT_EUNSUPPORTED;
+  }
+}
+
+}  // namespace bpt

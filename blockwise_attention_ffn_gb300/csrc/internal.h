@@ -178,6 +178,14 @@ int attention_bwd(const AttnBwdShape& sh, const void* qkv, const void* o, const 
 int attention_bwd_call(const bpt_config* cfg, const void* qkv, const void* o, const void* lse, const void* dout,
                        void* dqkv, void* ws, size_t ws_bytes, void* stream, int ws_is_library);
 
+// Attention with key windows, capped scores and a distance bias, on the whole
+// packed buffer; lse [b, H, s_pad] fp32 (nullable in the forward).
+int attention_mod_fwd(const PackedDims& D, int causal, const bpt_score_mod& mod, const void* qkv, void* o, float* lse,
+                      cudaStream_t st);
+size_t attention_mod_bwd_ws_bytes(const PackedDims& D);
+int attention_mod_bwd(const PackedDims& D, int causal, const bpt_score_mod& mod, const void* qkv, const void* o,
+                      const float* lse, const void* dout, void* dqkv, void* ws, cudaStream_t st);
+
 // ---------------------------------------------------------------- norms & misc
 // y = norm(x) * w (+ b), rows of width h; x is bf16 or (x_f32) fp32; y bf16.
 int norm_fwd(int64_t rows, int h, int kind, float eps, const void* x, int x_f32, int64_t ldx,

@@ -311,6 +311,46 @@ int bpt_attention_bwd_noalloc(const bpt_config* cfg, const void* qkv, const void
                               const void* dout, void* dqkv, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Attention with modified scores, on the packed layout of bpt_attention_fwd.
+ * With x = q.k / sqrt(d) for query i and key j of one sequence and head h:
+ *   y = softcap * tanh(x / softcap)   (softcap > 0; else y = x)
+ *       - slopes[h] * |i - j|         (slopes != NULL)
+ *   visible iff row_begin[i] <= j < row_end[i], and j <= i with cfg->causal
+ *   P = softmax over the visible keys of y,  o = P V,  lse = log sum exp y
+ * The windows say in one form: documents packed into a sequence (begin = the
+ * document's first row, causal or with end = its last row + 1), a prefix seen
+ * both ways (end = max(i + 1, prefix)), sliding windows (begin = i - w + 1),
+ * padding (end = the length; 0 for the padded rows themselves).  Positions in
+ * row_begin, row_end and |i - j| count from the sequence's first row.  Key
+ * tiles that no row of a query tile sees cost nothing.
+ *
+ *   row_begin, row_end  [b*s] int32 (device), or NULL: 0, and s.  Any value:
+ *                       clamped to [0, s].  A row whose window is empty has
+ *                       o = 0, lse = -inf and gives no gradient.
+ *   slopes              [H] fp32 (device), or NULL; constants: no gradient
+ *   softcap             0: none; else in [2^-40, 2^40]
+ * lse [b, H, s_pad] is an fp32-accurate sum (0 in the rows past s); the
+ * backward takes it back with o.  Biases far beyond the scores' size cost the
+ * rebuilt probabilities what lse's fp32 cannot hold (2^-24 of its size); the
+ * windows above keep near keys in view, where lse is small.  A key's K and V
+ * must be finite if any row of its 128-key tile's queries is computed, as in
+ * bpt_attention_fwd: a masked pair adds 0 * V.
+ * dqkv as for bpt_attention_bwd, whose notes on the order of sums and on
+ * BPT_FLAG_DETERMINISTIC hold here too; b*H*s_pad above 2^31 - 1 returns
+ * BPT_EUNSUPPORTED from both calls.  dqkv must not overlap qkv or dout.
+ * ws: bpt_attention_mod_bwd_workspace_bytes(cfg), one per call in flight. */
+typedef struct {
+  const int32_t *row_begin, *row_end;
+  const float* slopes;
+  float softcap;
+} bpt_score_mod;
+int bpt_attention_mod_fwd(const bpt_config* cfg, const bpt_score_mod* mod, const void* qkv, void* o, void* lse,
+                          void* stream);
+size_t bpt_attention_mod_bwd_workspace_bytes(const bpt_config* cfg);
+int bpt_attention_mod_bwd(const bpt_config* cfg, const bpt_score_mod* mod, const void* qkv, const void* o,
+                          const void* lse, const void* dout, void* dqkv, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Language-model loss after the last layer, blockwise.
  *
  * "Blockwise Parallel Transformer for Long Context Large Models", section 3

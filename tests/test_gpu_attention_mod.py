@@ -1,0 +1,177 @@
+"""Attention with key windows, capped scores and a distance bias, forward and
+backward, on the GPU against the fp64 definition.
+
+Tolerances, entry by entry, from the roundings the method makes (h = 2^-8, half
+a bf16 step relative to the value):
+  score   fp32 sums of d exact products: at most d 2^-23 |q|.|k| / sqrt(d), then
+          fp32 steps of the modified score's and the log-sum-exp's size; a
+          probability moves by e = that, relative (worst case, so small against h)
+  O       bf16 P against an fp32 row sum: (h + e) P|V|, and its own rounding h |O|
+  LSE     e and fp32 steps of its size
+  dV      (h + e) P^T|dO| + h |dV|
+  D       |dO| . (error of O), as O is stored in bf16
+  dx      = P (dP - D)(1 - u^2): (h + e) |dx| + P (1 - u^2) err(D) + fp32 steps of
+          |dO|.|V|
+  dQ, dK  err(dx) times |K|, |Q| / sqrt(d), and their own rounding
+fp32 sums over the keys or queries add under s 2^-24 of the terms' sizes, inside
+the margin h leaves (s 2^-24 < h / 100 here)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import blockwise_attention_ffn_gb300 as bpt
+from blockwise_attention_ffn_gb300.presets import LayerConfig
+from oracle import train_ops as T
+from tests.gpu_helpers import to64
+
+pytestmark = pytest.mark.gpu
+
+H8 = 2.0 ** -8 * 1.02  # and the fp32 sums
+
+
+def windows(kind, b, s, seed=0):
+    """(causal, row_begin, row_end) as int lists of b*s, or None."""
+    rng = np.random.default_rng(seed)
+    begin, end = [], []
+    for i in range(b):
+        cuts = sorted({0, s, *rng.integers(0, s + 1, 1 + s // 90).tolist()})
+        doc = [(a, e) for a, e in zip(cuts, cuts[1:]) for _ in range(a, e)]
+        n = max(0, s - i * (s // 3 + 1))
+        if kind == "docs":
+            begin += [a for a, _ in doc]
+        elif kind == "docs_both":
+            begin += [a for a, _ in doc]
+            end += [e for _, e in doc]
+        elif kind == "prefix":
+            end += [max(q + 1, min(s // 3, n)) if q < n else 0 for q in range(s)]
+        elif kind == "window":
+            begin += [q - 20 for q in range(s)]
+        elif kind == "padded":
+            end += [n] * s
+        elif kind == "holes":  # rows of every kind: empty, reversed, far outside
+            lo, hi = rng.integers(-5, s + 5, (2, s))
+            lo[rng.random(s) < 0.1], hi[rng.random(s) < 0.1] = -2 ** 31, 2 ** 31 - 1
+            begin += lo.tolist()
+            end += hi.tolist()
+        elif kind == "none":
+            end += [0] * s
+    return int(kind in ("causal", "docs", "window")), begin or None, end or None
+
+
+def as_int32(v):
+    return None if v is None else torch.tensor(v, dtype=torch.int64).to(torch.int32).cuda()
+
+
+def make(b, s, H, K, d, seed, qscale=1.5):
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(b * s, (H + 2 * K) * d, generator=g)
+    qkv[:, :H * d] *= qscale
+    return qkv.to(torch.bfloat16), torch.randn(b * s, H * d, generator=g).to(torch.bfloat16)
+
+
+def run(cfg, mod, qkv, dout, flags=0):
+    cfg = cfg.with_(flags=flags)
+    rows = cfg.b * cfg.s
+    x = qkv.cuda()
+    o = torch.full((rows, cfg.n_heads * cfg.head_dim), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((cfg.b, cfg.n_heads, bpt.s_pad(cfg)), float("nan"), device="cuda")
+    bpt.bpt_attention_mod_fwd(cfg, mod, x, o, lse)
+    dqkv = torch.full_like(x, float("nan"))
+    ws = bpt.alloc_bytes(bpt.bpt_attention_mod_bwd_workspace_bytes(cfg))
+    ws.fill_(255)
+    bpt.bpt_attention_mod_bwd(cfg, mod, x, o, lse, dout.cuda(), dqkv, ws)
+    torch.cuda.synchronize()
+    assert bpt.bpt_last_device_error() == (bpt.BPT_OK, 0)
+    return o, lse, dqkv
+
+
+def check(what, got, want, bound):
+    assert np.array_equal(np.isfinite(got), np.isfinite(want)), f"{what}: finite entries differ"
+    ok = np.isfinite(want)
+    assert np.array_equal(got[~ok], want[~ok])
+    over = np.abs(got[ok] - want[ok]) - bound[ok]
+    assert not over.size or over.max() <= 0, f"{what}: {over.max():.3e} over its bound, {np.mean(over > 0):.2e} of the entries"
+
+
+def check_all(cfg, causal, begin, end, slopes, cap, qkv, dout, o, lse, dqkv):
+    b, s, H, K, d = cfg.b, cfg.s, cfg.n_heads, cfg.n_kv_heads, cfg.head_dim
+    G = H // K
+    x, do = to64(qkv).reshape(b, s, H + 2 * K, d), to64(dout).reshape(b, s, H, d)
+    o, lse, dx = to64(o).reshape(b, s, H, d), to64(lse), to64(dqkv).reshape(x.shape)
+    assert np.all(lse[:, :, s:] == 0)
+    for bi in range(b):
+        rows = slice(bi * s, (bi + 1) * s)
+        ok = T.allowed(s, causal, None if begin is None else begin[rows], None if end is None else end[rows])
+        for g in range(K):
+            k, v = x[bi, :, H + g], x[bi, :, H + K + g]
+            dk, dv, ek, ev = (np.zeros((s, d)) for _ in range(4))
+            for n in range(g * G, (g + 1) * G):
+                q, a = x[bi, :, n], 0.0 if slopes is None else float(slopes[n])
+                wo, wl, wq, wk, wv = T.attention_mod_head(q, k, v, ok, a, cap, do[bi, :, n])
+                raw = q @ k.T / math.sqrt(d)
+                u = np.tanh(raw / cap) if cap else np.zeros_like(raw)
+                far = a * np.abs(np.arange(s)[:, None] - np.arange(s)[None])
+                y = (cap * u if cap else raw) - far
+                fin = np.where(np.isfinite(wl), wl, 0.0)
+                p = np.where(ok, np.exp(np.minimum(y - fin[:, None], 0.0)), 0.0)
+                e = (d * 2.0 ** -23 * (np.abs(q) @ np.abs(k).T) / math.sqrt(d)
+                     + 2.0 ** -20 * (np.abs(raw if not cap else cap * u) + far + np.abs(fin)[:, None] + 8))
+                e = np.where(ok, e, 0.0)
+                bo = ((H8 + e) * p) @ np.abs(v) + H8 * np.abs(wo) + 1e-30
+                check(f"O[{bi}, {n}]", o[bi, :, n], wo, bo)
+                check(f"LSE[{bi}, {n}]", lse[bi, n, :s], wl, e.max(1) + 2.0 ** -21 * np.abs(fin) + 2.0 ** -21)
+                dk, dv = dk + wk, dv + wv
+                dO = np.abs(do[bi, :, n])
+                ev += ((H8 + e) * p).T @ dO
+                size = dO @ np.abs(v).T
+                dP = do[bi, :, n] @ v.T - (do[bi, :, n] * wo).sum(1, keepdims=True)
+                f = p * (1 - u * u)
+                edx = ((H8 + e) * f * np.abs(dP) + f * ((dO * bo).sum(1, keepdims=True) + d * 2.0 ** -22 * size)
+                       + 2.0 ** -21 * p * np.abs(dP)) / math.sqrt(d)
+                check(f"dQ[{bi}, {n}]", dx[bi, :, n], wq, edx @ np.abs(k) + H8 * np.abs(wq) + 1e-30)
+                ek += edx.T @ np.abs(q)
+            check(f"dK[{bi}, {g}]", dx[bi, :, H + g], dk, ek + H8 * np.abs(dk) + 1e-30)
+            check(f"dV[{bi}, {g}]", dx[bi, :, H + K + g], dv, ev + H8 * np.abs(dv) + 1e-30)
+
+
+CASES = [
+    # b, s, H, K, d, windows, cap, slopes
+    (1, 1, 1, 1, 64, "causal", 0.0, False),
+    (1, 2, 2, 1, 128, "docs", 30.0, True),
+    (1, 1, 1, 1, 80, "none", 30.0, True),
+    (2, 63, 2, 2, 80, "docs", 0.0, True),
+    (1, 64, 2, 1, 96, "docs_both", 20.0, False),
+    (3, 65, 2, 2, 112, "padded", 0.0, False),
+    (1, 127, 2, 2, 128, "window", 50.0, True),
+    (2, 128, 2, 1, 64, "prefix", 0.0, True),
+    (1, 129, 2, 2, 80, "holes", 10.0, True),
+    (2, 200, 4, 2, 112, "holes", 0.0, False),
+    (1, 300, 4, 1, 96, "docs", 5.0, False),
+    (2, 257, 3, 1, 128, "docs_both", 0.0, True),
+    (1, 513, 4, 2, 128, "docs", 30.0, False),
+    (1, 640, 2, 2, 64, "window", 0.0, False),
+    (2, 385, 2, 1, 80, "prefix", 20.0, True),
+    (1, 600, 2, 2, 96, "causal", 0.0, False),
+    (1, 600, 2, 2, 128, "all", 1.0, True),
+    (3, 390, 2, 2, 64, "padded", 60.0, False),
+    (1, 500, 2, 1, 112, "causal", 2.0, False),
+    (2, 300, 2, 2, 128, "none", 0.0, False),
+]
+
+
+@pytest.mark.parametrize("flags", [0, bpt.BPT_FLAG_DETERMINISTIC])
+@pytest.mark.parametrize("case", CASES, ids=str)
+def test_against_the_definition(case, flags):
+    b, s, H, K, d, kind, cap, biased = case
+    causal, begin, end = windows(kind, b, s, seed=s + d)
+    slopes = [2.0 ** -(1 + 3 * n) for n in range(H)] if biased else None
+    cfg = LayerConfig(b=b, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64, causal=causal)
+    mod = bpt.ScoreMod(as_int32(begin), as_int32(end), None if slopes is None else torch.tensor(slopes, device="cuda"), cap)
+    qkv, dout = make(b, s, H, K, d, seed=s)
+    got = run(cfg, mod, qkv, dout, flags)
+    check_all(cfg, causal, begin, end, slopes, cap, qkv, dout, *got)
+    if flags:
+        again = run(cfg, mod, qkv, dout, flags)
+        assert all(torch.equal(a, c) for a, c in zip(got, again))
