@@ -8,10 +8,10 @@
 // The cap's cost.  tanh through an exponential and a reciprocal takes two more
 // special-function operations per score beside the softmax's own, and those
 // units already bound the softmax.  Trained scores sit well inside the cap, so
-// wherever every score of a warp's tile has |x| <= 0.6 C an odd polynomial of
-// degree 9 in x / C is taken instead (error 2.8e-8, below fp32's own at the
-// scores' size), at half the arithmetic rate of fp32 pairs and no special
-// function; the exact form serves every other tile.
+// a warp whose 64 columns all have |x| <= C/4 takes an odd polynomial of
+// degree 5 in x (error 8e-8 C, below an fp32 step of the largest of them),
+// within 0.6 C one of degree 9 (3e-8 C), both in packed fp32 arithmetic, and
+// only beyond that the exact form.
 #pragma once
 
 #include "attn_common.cuh"
@@ -31,16 +31,42 @@ __device__ __forceinline__ int2 key_window(const int32_t* row_begin, const int32
   return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
 }
 
-// tanh for |y| <= 0.6, two at a time: y (1 + u (c1 + u (c2 + u (c3 + u c4)))),
-// u = y^2, a least-maximum fit of the odd polynomial of degree 9
-__device__ __forceinline__ uint64_t tanh2_small(uint64_t y) {
-  const uint64_t u = mul2(y, y);
-  uint64_t q = fma2(u, f2(0.01531921f, 0.01531921f), f2(-0.05199434f, -0.05199434f));
-  q = fma2(u, q, f2(0.13308098f, 0.13308098f));
-  q = fma2(u, q, f2(-0.33332248f, -0.33332248f));
-  return fma2(mul2(u, q), y, y);
+// The cap as the kernels take it: with z a raw score (q.k), x = z / sqrt(d)
+// and k = 1 / (C sqrt(d)), the polynomials of tanh(k z), least-maximum fits,
+// in powers of z: z (c[0] + w (c[1] + w c[2])) for |k z| <= 0.25 and
+// z (e[0] + w (e[1] + ... )) for |k z| <= 0.6, w = z^2, each times `out`.
+struct CapCoef {
+  float near1, near2;  // largest |z| of the two
+  float c[3], e[5];
+  float k2, out;  // 2 log2(e) k, and what tanh is multiplied with
+};
+inline CapCoef cap_coef(double k, double out) {
+  const double n5[3] = {1.0, -0.33322915, 0.128460431};
+  const double n9[5] = {1.0, -0.33332248, 0.133080983, -0.0519943379, 0.0153192074};
+  CapCoef f;
+  f.near1 = (float)(0.25 / k);
+  f.near2 = (float)(0.6 / k);
+  double kk = k * out;
+  for (int i = 0; i < 5; ++i, kk *= k * k) {
+    if (i < 3) f.c[i] = (float)(n5[i] * kk);
+    f.e[i] = (float)(n9[i] * kk);
+  }
+  f.k2 = (float)(2.8853900817779268 * k);
+  f.out = (float)out;
+  return f;
 }
-constexpr float TANH_SMALL = 0.6f;
+__device__ __forceinline__ uint64_t both(float v) { return f2(v, v); }
+__device__ __forceinline__ uint64_t cap_near1(const CapCoef& f, uint64_t z) {
+  const uint64_t w = mul2(z, z);
+  return mul2(z, fma2(w, fma2(w, both(f.c[2]), both(f.c[1])), both(f.c[0])));
+}
+__device__ __forceinline__ uint64_t cap_near2(const CapCoef& f, uint64_t z) {
+  const uint64_t w = mul2(z, z);
+  uint64_t q = fma2(w, both(f.e[4]), both(f.e[3]));
+  q = fma2(w, q, both(f.e[2]));
+  q = fma2(w, q, both(f.e[1]));
+  return mul2(z, fma2(w, q, both(f.e[0])));
+}
 
 // tanh(y) = 1 - 2 / (1 + e^(2y)): absolute error about 2^-23, saturating
 // exactly; y2 = 2 log2(e) y

@@ -59,35 +59,39 @@ struct ModBwdParams {
   long long width;
   const int32_t *row_begin, *row_end;
   const float* slopes;
-  float scale, scale_log2, inv_cap, cap_log2;
+  float scale, scale_log2, cap_log2;
+  CapCoef cap;  // tanh of the raw scores
   int one_issuer;  // fixed-order mode: warp 1 issues both groups' products
   unsigned int* err;
 };
 
 // exp2 of 64 modified scores in log2 units and what dx multiplies (dP - D)
 // with: sv in, pe = P (1 - u^2) out, pk = P as bf16 pairs (WANT_P).
-// add(k): what is added to the (capped, scaled) score of element k, the bias
+// add(k): what is added to the scaled scores of the pair (k, k + 1), the bias
 // and -LSE; on(k): visible.  all: every element is visible.
 template <bool CAP, bool WANT_P, class Add, class On>
-__device__ __forceinline__ void probabilities(uint32_t (&sv)[64], float (&pe)[64], uint32_t (&pk)[32], float scale_log2,
-                                              float inv_cap, float cap_log2, bool all, Add add, On on) {
+__device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&sv)[64], float (&pe)[64],
+                                              uint32_t (&pk)[32], bool all, Add add, On on) {
   if constexpr (CAP) {
     // u over sv
-    if (__all_sync(0xffffffffu, amax_of(sv) * inv_cap <= TANH_SMALL)) {
-      const uint64_t ic2 = f2(inv_cap, inv_cap);
+    auto put = [&](int k, uint64_t v) {
+      const float2 x = f2split(v);
+      sv[k] = __float_as_uint(x.x);
+      sv[k + 1] = __float_as_uint(x.y);
+    };
+    const float am = amax_of(sv);
+    if (__all_sync(0xffffffffu, am <= p.cap.near1)) {
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
-        const float2 t = f2split(tanh2_small(mul2(f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), ic2)));
-        sv[k] = __float_as_uint(t.x);
-        sv[k + 1] = __float_as_uint(t.y);
-      }
+      for (int k = 0; k < 64; k += 2) put(k, cap_near1(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
+    } else if (__all_sync(0xffffffffu, am <= p.cap.near2)) {
+#pragma unroll
+      for (int k = 0; k < 64; k += 2) put(k, cap_near2(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
     } else {
-      const float y2 = inv_cap * 2.8853900817779268f;
 #pragma unroll
-      for (int k = 0; k < 64; ++k) sv[k] = __float_as_uint(tanh_any(__uint_as_float(sv[k]) * y2));
+      for (int k = 0; k < 64; ++k) sv[k] = __float_as_uint(tanh_any(__uint_as_float(sv[k]) * p.cap.k2));
     }
   }
-  const float cs = CAP ? cap_log2 : scale_log2;
+  const float cs = CAP ? p.cap_log2 : p.scale_log2;
   const uint64_t cs2 = f2(cs, cs), one2 = f2(1.f, 1.f);
 #pragma unroll
   for (int k = 0; k < 64; k += 2) {
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
           else return 0ull;
         };
         if (!bias) {
-          probabilities<CAP, true>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, lse2, on);
+          probabilities<CAP, true>(p, sv, pe, pk, all, lse2, on);
         } else {
           const float slope2 = p.slopes[g * p.G + t / n_i] * 1.4426950408889634f;
           // along the queries; with a causal mask those before the key are masked
@@ -500,13 +504,13 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
             auto add = [&](int x) {
               return add2(lse2(x), f2(fmaf(bl.step, (float)x, bl.base), fmaf(bl.step, (float)(x + 1), bl.base)));
             };
-            probabilities<CAP, true>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+            probabilities<CAP, true>(p, sv, pe, pk, all, add, on);
           } else {
             const float dist = (float)(kvp - q0);
             auto add = [&](int x) {
               return add2(lse2(x), f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
             };
-            probabilities<CAP, true>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+            probabilities<CAP, true>(p, sv, pe, pk, all, add, on);
           }
         }
       }
@@ -846,20 +850,20 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
         const uint64_t nl2 = f2(nl, nl);
         if (!bias) {
           auto add = [&](int) { return nl2; };
-          probabilities<CAP, false>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+          probabilities<CAP, false>(p, sv, pe, pk, all, add, on);
         } else {
           const BiasLine bl = bias_line(slope2, qpos, kv0, p.causal != 0, false);
           if (!__any_sync(0xffffffffu, bl.mixed)) {
             auto add = [&](int x) {
               return add2(nl2, f2(fmaf(bl.step, (float)x, bl.base), fmaf(bl.step, (float)(x + 1), bl.base)));
             };
-            probabilities<CAP, false>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+            probabilities<CAP, false>(p, sv, pe, pk, all, add, on);
           } else {
             const float dist = (float)(qpos - kv0);
             auto add = [&](int x) {
               return add2(nl2, f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
             };
-            probabilities<CAP, false>(sv, pe, pk, p.scale_log2, p.inv_cap, p.cap_log2, all, add, on);
+            probabilities<CAP, false>(p, sv, pe, pk, all, add, on);
           }
         }
       }
@@ -1090,7 +1094,7 @@ int attention_mod_bwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   p.scale = 1.f / sqrtf((float)D.d);
   p.scale_log2 = p.scale * 1.4426950408889634f;
   if (cap) {
-    p.inv_cap = p.scale / mod.softcap;
+    p.cap = cap_coef(1.0 / (mod.softcap * sqrt((double)D.d)), 1.0);
     p.cap_log2 = mod.softcap * 1.4426950408889634f;
   }
   p.one_issuer = D.det ? 1 : 0;

@@ -380,6 +380,35 @@ __device__ __forceinline__ void named_bar(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// ---------------------------------------------------------------- work stealing
+// A running block takes over blocks of its grid that have not started
+// (cluster launch control): the request writes 16 bytes at `res` and
+// completes them on `bar`; the answer is the block's index, or -1 once every
+// block has started (then no further request may be made).
+__device__ __forceinline__ void request_block(void* res, uint64_t* bar) {
+  mbar_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(res)),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ int answered_block(const void* res) {
+  int x;
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+      : "=r"(x), "=r"(ok)
+      : "r"(smem_u32(res))
+      : "memory");
+  return ok ? x : -1;
+}
+
 // ---------------------------------------------------------------- CTA pairs
 // A cluster of two CTAs on two SMs that share one tensor-core product
 // (cta_group::2, M = 256): each CTA stages its 128 rows of A and half of B's

@@ -328,7 +328,7 @@ int bpt_attention_bwd_noalloc(const bpt_config* cfg, const void* qkv, const void
  *                       clamped to [0, s].  A row whose window is empty has
  *                       o = 0, lse = -inf and gives no gradient.
  *   slopes              [H] fp32 (device), or NULL; constants: no gradient
- *   softcap             0: none; else in [2^-40, 2^40]
+ *   softcap             0: none; else in [2^-10, 2^20]
  * lse [b, H, s_pad] is an fp32-accurate sum (0 in the rows past s); the
  * backward takes it back with o.  Biases far beyond the scores' size cost the
  * rebuilt probabilities what lse's fp32 cannot hold (2^-24 of its size); the
