@@ -28,6 +28,12 @@ struct TileGeom {
     const int off = ((kk * 16) % CW) * 2;
     return sdesc(tile + c * CHUNK + off, 16, 8 * SWB, LAYOUT);
   }
+  // what kk adds to kmajor(tile, 0) and mnmajor(tile, 0): the address field
+  // counts 16-byte units and never carries out of its 14 bits
+  static __device__ __forceinline__ constexpr uint64_t kmajor_step(int kk) {
+    return (uint64_t)(((kk * 16) / CW * CHUNK + ((kk * 16) % CW) * 2) >> 4);
+  }
+  static __device__ __forceinline__ constexpr uint64_t mnmajor_step(int kk) { return (uint64_t)((kk * 16 * SWB) >> 4); }
   // MN-major use (N = D): 16 rows (the contraction) starting at 16*kk
   static __device__ __forceinline__ uint64_t mnmajor(uint32_t tile, int kk) {
     return sdesc(tile + kk * 16 * SWB, CHUNK, 8 * SWB, LAYOUT);
@@ -41,6 +47,15 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
+}
+
+// box of the map's shape from shared memory to (x, y, z), counted in the
+// thread's bulk group; y and z start inside the tensor
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 
 // 16 TMEM fp32 columns of this thread's row -> 16 bf16 values (scaled)

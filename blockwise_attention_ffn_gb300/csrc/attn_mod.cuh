@@ -14,6 +14,8 @@
 // only beyond that the exact form.
 #pragma once
 
+#include <string.h>
+
 #include "attn_common.cuh"
 
 namespace bpt {
@@ -37,9 +39,14 @@ __device__ __forceinline__ int2 key_window(const int32_t* row_begin, const int32
 // z (e[0] + w (e[1] + ... )) for |k z| <= 0.6, w = z^2, each times `out`.
 struct CapCoef {
   float near1, near2;  // largest |z| of the two
-  float c[3], e[5];
-  float k2, out;  // 2 log2(e) k, and what tanh is multiplied with
+  uint64_t c[3], e[5];  // the coefficients, twice each: operands of packed arithmetic
+  float k2, out;        // 2 log2(e) k, and what tanh is multiplied with
 };
+inline uint64_t twice(float v) {
+  uint32_t u;
+  memcpy(&u, &v, 4);
+  return (uint64_t)u << 32 | u;
+}
 inline CapCoef cap_coef(double k, double out) {
   const double n5[3] = {1.0, -0.33322915, 0.128460431};
   const double n9[5] = {1.0, -0.33332248, 0.133080983, -0.0519943379, 0.0153192074};
@@ -48,8 +55,8 @@ inline CapCoef cap_coef(double k, double out) {
   f.near2 = (float)(0.6 / k);
   double kk = k * out;
   for (int i = 0; i < 5; ++i, kk *= k * k) {
-    if (i < 3) f.c[i] = (float)(n5[i] * kk);
-    f.e[i] = (float)(n9[i] * kk);
+    if (i < 3) f.c[i] = twice((float)(n5[i] * kk));
+    f.e[i] = twice((float)(n9[i] * kk));
   }
   f.k2 = (float)(2.8853900817779268 * k);
   f.out = (float)out;
@@ -58,14 +65,43 @@ inline CapCoef cap_coef(double k, double out) {
 __device__ __forceinline__ uint64_t both(float v) { return f2(v, v); }
 __device__ __forceinline__ uint64_t cap_near1(const CapCoef& f, uint64_t z) {
   const uint64_t w = mul2(z, z);
-  return mul2(z, fma2(w, fma2(w, both(f.c[2]), both(f.c[1])), both(f.c[0])));
+  return mul2(z, fma2(w, fma2(w, f.c[2], f.c[1]), f.c[0]));
 }
 __device__ __forceinline__ uint64_t cap_near2(const CapCoef& f, uint64_t z) {
   const uint64_t w = mul2(z, z);
-  uint64_t q = fma2(w, both(f.e[4]), both(f.e[3]));
-  q = fma2(w, q, both(f.e[2]));
-  q = fma2(w, q, both(f.e[1]));
-  return mul2(z, fma2(w, q, both(f.e[0])));
+  uint64_t q = fma2(w, f.e[4], f.e[3]);
+  q = fma2(w, q, f.e[2]);
+  q = fma2(w, q, f.e[1]);
+  return mul2(z, fma2(w, q, f.e[0]));
+}
+
+// The order of the grid: work items of tiles x heads, the tiles of all heads
+// of a group in turn, first tile index first, then the next group.  A group is
+// as many key/value heads (of any sequence) as L2 holds the streams of, so
+// that a group's last, small items balance its large first ones and every
+// stream is read from HBM once.
+struct ItemOrder {
+  int tiles, per_head, group, kv_heads;  // group: key/value heads in one; kv_heads: b * H_kv
+};
+struct Item {
+  int tile, kv, sub;  // kv: index of the key/value head over all sequences; sub < per_head
+};
+inline ItemOrder item_order(int64_t tiles, int64_t per_head, int64_t kv_heads, int64_t bytes_per_head) {
+  const int64_t fit = (int64_t)(48 << 20) / (bytes_per_head > 0 ? bytes_per_head : 1);
+  ItemOrder o;
+  o.tiles = (int)tiles;
+  o.per_head = (int)per_head;
+  o.kv_heads = (int)kv_heads;
+  o.group = (int)(fit < 1 ? 1 : fit > kv_heads ? kv_heads : fit);
+  return o;
+}
+__device__ __forceinline__ Item item_of(const ItemOrder& o, int block) {
+  const int full = o.group * o.per_head * o.tiles;
+  const int g = block / full;
+  const int rem = block - g * full;
+  const int heads = min(o.group, o.kv_heads - g * o.group) * o.per_head;
+  const int head = rem % heads;
+  return Item{rem / heads, g * o.group + head / o.per_head, head % o.per_head};
 }
 
 // tanh(y) = 1 - 2 / (1 + e^(2y)): absolute error about 2^-23, saturating
@@ -76,14 +112,22 @@ __device__ __forceinline__ float tanh_any(float y2) {
   return fmaf(-2.f, r, 1.f);
 }
 
-// largest |v| of N values (NaN ignored)
-template <int N>
-__device__ __forceinline__ float amax_of(const uint32_t (&v)[N]) {
-  float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < N; i += 2)
-    m[(i >> 1) & 3] = max3f(m[(i >> 1) & 3], fabsf(__uint_as_float(v[i])), fabsf(__uint_as_float(v[i + 1])));
-  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+// 64 score columns of this thread's row, and the largest of them (of their
+// magnitudes: ABS), which the load itself finds
+template <bool ABS>
+__device__ __forceinline__ float load_scores(uint32_t taddr, uint32_t (&sv)[64]) {
+  float a, b;
+  if constexpr (ABS) {
+    tmem_ld32_amax_nw(taddr, sv, a);
+    tmem_ld32_amax_nw(taddr + 32, sv + 32, b);
+  } else {
+    tmem_ld32_max_nw(taddr, sv, a);
+    tmem_ld32_max_nw(taddr + 32, sv + 32, b);
+  }
+  tmem_wait_ld(sv);
+  tmem_wait_max(a);
+  tmem_wait_max(b);
+  return fmaxf(a, b);
 }
 
 // The bias -a |i - j| along a run of 64 consecutive indices from `first`

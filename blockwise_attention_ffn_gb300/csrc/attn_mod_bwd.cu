@@ -66,11 +66,13 @@ struct ModBwdParams {
 };
 
 // exp2 of 64 modified scores in log2 units and what dx multiplies (dP - D)
-// with: sv in, pe = P (1 - u^2) out, pk = P as bf16 pairs (WANT_P).
-// add(k): what is added to the scaled scores of the pair (k, k + 1), the bias
-// and -LSE; on(k): visible.  all: every element is visible.
+// with: sv in, am their largest magnitude, pe = P (1 - u^2) out, pk = P as
+// bf16 pairs (WANT_P).  add(k): what is added to the scaled scores of the pair
+// (k, k + 1), the bias and -LSE; on(k): visible; all: every element is.
+// A masked u is replaced by one whose exponential is 0 and whose square is
+// finite, in a pass of its own, so that unmasked sub-tiles pay nothing for it.
 template <bool CAP, bool WANT_P, class Add, class On>
-__device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&sv)[64], float (&pe)[64],
+__device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&sv)[64], float am, float (&pe)[64],
                                               uint32_t (&pk)[32], bool all, Add add, On on) {
   if constexpr (CAP) {
     // u over sv
@@ -79,7 +81,6 @@ __device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&
       sv[k] = __float_as_uint(x.x);
       sv[k + 1] = __float_as_uint(x.y);
     };
-    const float am = amax_of(sv);
     if (__all_sync(0xffffffffu, am <= p.cap.near1)) {
 #pragma unroll
       for (int k = 0; k < 64; k += 2) put(k, cap_near1(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
@@ -91,23 +92,23 @@ __device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&
       for (int k = 0; k < 64; ++k) sv[k] = __float_as_uint(tanh_any(__uint_as_float(sv[k]) * p.cap.k2));
     }
   }
+  if (!all) {
+#pragma unroll
+    for (int k = 0; k < 64; ++k)
+      if (!on(k)) sv[k] = __float_as_uint(-1e18f);
+  }
   const float cs = CAP ? p.cap_log2 : p.scale_log2;
-  const uint64_t cs2 = f2(cs, cs), one2 = f2(1.f, 1.f);
+  const uint64_t cs2 = both(cs), one2 = both(1.f);
 #pragma unroll
   for (int k = 0; k < 64; k += 2) {
     const uint64_t u2 = f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]));
     const float2 e = f2split(fma2(u2, cs2, add(k)));
-    float p0 = ex2(e.x), p1 = ex2(e.y);
-    if (!all) {
-      p0 = on(k) ? p0 : 0.f;
-      p1 = on(k + 1) ? p1 : 0.f;
-    }
+    const float p0 = ex2(e.x), p1 = ex2(e.y);
     if constexpr (WANT_P) pk[k / 2] = pack_bf16(p0, p1);
     if constexpr (CAP) {
-      // 1 - u^2, then times P; a masked u may be NaN
-      const float2 f = f2split(fma2(u2 ^ 0x8000000080000000ull, u2, one2));
-      pe[k] = all || p0 != 0.f ? p0 * f.x : 0.f;
-      pe[k + 1] = all || p1 != 0.f ? p1 * f.y : 0.f;
+      const float2 f = f2split(mul2(f2(p0, p1), fma2(u2 ^ 0x8000000080000000ull, u2, one2)));
+      pe[k] = f.x;
+      pe[k + 1] = f.y;
     } else {
       pe[k] = p0;
       pe[k + 1] = p1;
@@ -483,9 +484,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
       uint32_t pk[32];
       {
         uint32_t sv[64];
-        tmem_ld32_nw(tSb + lane_off, sv);
-        tmem_ld32_nw(tSb + lane_off + 32, sv + 32);
-        tmem_wait_ld(sv);
+        const float am = load_scores<true>(tSb + lane_off, sv);
         auto on = [&](int x) {
           const int2 w = win[x];
           return (unsigned)(kvp - w.x) < (unsigned)w.y;
@@ -495,7 +494,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
           else return 0ull;
         };
         if (!bias) {
-          probabilities<CAP, true>(p, sv, pe, pk, all, lse2, on);
+          probabilities<CAP, true>(p, sv, am, pe, pk, all, lse2, on);
         } else {
           const float slope2 = p.slopes[g * p.G + t / n_i] * 1.4426950408889634f;
           // along the queries; with a causal mask those before the key are masked
@@ -504,13 +503,13 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
             auto add = [&](int x) {
               return add2(lse2(x), f2(fmaf(bl.step, (float)x, bl.base), fmaf(bl.step, (float)(x + 1), bl.base)));
             };
-            probabilities<CAP, true>(p, sv, pe, pk, all, add, on);
+            probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
           } else {
             const float dist = (float)(kvp - q0);
             auto add = [&](int x) {
               return add2(lse2(x), f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
             };
-            probabilities<CAP, true>(p, sv, pe, pk, all, add, on);
+            probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
           }
         }
       }
@@ -836,9 +835,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
       const int kv0 = (j0 + (u >> 1)) * 128 + 64 * b;
       const int klo = max(win.x - kv0, 0), khi = min(win.y - kv0, 64);
       uint32_t sv[64];
-      tmem_ld32_nw(tSb + lane_off, sv);
-      tmem_ld32_nw(tSb + lane_off + 32, sv + 32);
-      tmem_wait_ld(sv);
+      const float am = load_scores<true>(tSb + lane_off, sv);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[b]);
@@ -850,20 +847,20 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
         const uint64_t nl2 = f2(nl, nl);
         if (!bias) {
           auto add = [&](int) { return nl2; };
-          probabilities<CAP, false>(p, sv, pe, pk, all, add, on);
+          probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
         } else {
           const BiasLine bl = bias_line(slope2, qpos, kv0, p.causal != 0, false);
           if (!__any_sync(0xffffffffu, bl.mixed)) {
             auto add = [&](int x) {
               return add2(nl2, f2(fmaf(bl.step, (float)x, bl.base), fmaf(bl.step, (float)(x + 1), bl.base)));
             };
-            probabilities<CAP, false>(p, sv, pe, pk, all, add, on);
+            probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
           } else {
             const float dist = (float)(qpos - kv0);
             auto add = [&](int x) {
               return add2(nl2, f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
             };
-            probabilities<CAP, false>(p, sv, pe, pk, all, add, on);
+            probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
           }
         }
       }

@@ -8,14 +8,15 @@
 //  * A tile's first and last key tile come from its rows' windows, so packed
 //    documents, prefixes and padding cost only the tiles that some row sees.
 //  * Scores are modified between the tensor core and the softmax.  With a cap
-//    of at most 44 (2^64 in the exponent's units) and no bias the scores are
-//    bounded, so the running maximum is dropped: every row keeps m = 0.
+//    of at most 61 and no bias the exponentials stay within 2^-88 and 2^88,
+//    which leaves fp32 sums 2^39 for keys and values, so the running maximum is
+//    dropped: every row keeps m = 0.
 //  * Row sums are fp32 sums of the fp32 exponentials, so the log-sum-exp is an
 //    fp32-exact output; the tensor core's row sums of bf16 P would be off by
 //    up to 2^-9.
 //
-// Work item = one 128-row query tile of one head, heaviest tiles of a head
-// first.  The 128 keys of a tile are split in two halves, each with its own
+// Work item = one 128-row query tile of one head, the last (with a causal mask
+// heaviest) tiles first.  The 128 keys of a tile are split in two halves, each with its own
 // softmax warps (2..5, 6..9), MMA-issuing warp (1, 10), running maximum and O
 // accumulator, merged at the end by the log-sum-exp rule: the modified softmax
 // bounds the loop, and two warps per SM sub-partition hide each other's
@@ -25,10 +26,10 @@
 // hardware's own queue of unstarted blocks, so no counter in memory and the
 // order of the grid).  With windows an item is often a handful of key tiles,
 // and a CTA of its own spent about 12,000 cycles on starting, TMEM, barriers,
-// the first loads and its end, as much as ten key tiles.  Here warp 0 looks up
-// the next item's windows and loads its Q and K/V while the softmax is still
-// in the current one, and the issuers put the next item's first S before the
-// current item's last PV.
+// the first loads and its end, as much as ten key tiles.  Here warp 11 looks up
+// the next item's windows and warp 0 loads its Q and K/V while the softmax is
+// still in the current one, and its first S is made during the current item's
+// merge.
 #include <math.h>
 #include <string.h>
 
@@ -37,14 +38,16 @@
 #include "internal.h"
 
 namespace bpt {
-int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d);
+int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d, int box_rows);
 
 namespace {
 
 struct ModFwdParams {
   CUtensorMap map_qkv;  // 3-D {width, s, b}, box {CW, 128, 1}
+  CUtensorMap map_o;    // 3-D {H d, s, b}, box {CW, 32, 1}
   int s, s_pad, H, G, causal;
-  int k_col, v_col, n_qt;
+  int k_col, v_col;
+  ItemOrder order;
   __nv_bfloat16* o;
   float* lse;
   const int32_t *row_begin, *row_end;
@@ -55,14 +58,15 @@ struct ModFwdParams {
   unsigned int* err;
 };
 
-// One work item as warp 0 publishes it; n < 0: no more.
+// One work item as warp 11 publishes it; n < 0: no more.
 struct WorkItem {
   int n, bi, q0, j0, nkv;
 };
 
 // TMEM: S of half b as two 64-column buffers at 128 b, O_b at 256 + b D.
 // Shared memory: two Q tiles, a ring of K and V tiles in the order they are
-// used (K_0, K_1, V_0, K_2, V_1, ...), the merge's maxima and sums, barriers.
+// used (K_0, K_1, V_0, K_2, V_1, ..., V_last, then the next item's), the
+// merge's maxima and sums, barriers.
 template <int D>
 struct ModFwdCfg {
   using T = TileGeom<D>;
@@ -75,7 +79,7 @@ struct ModFwdCfg {
 };
 
 template <int D, bool CAP>
-__global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_constant__ ModFwdParams p) {
+__global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_constant__ ModFwdParams p) {
   using T = TileGeom<D>;
   using C = ModFwdCfg<D>;
   constexpr int NT = C::NT;
@@ -97,9 +101,9 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
   WorkItem* work = reinterpret_cast<WorkItem*>(answer + 32);  // [2], 32 bytes apart
   uint64_t* bars = reinterpret_cast<uint64_t*>(answer + 32 + 64);
   uint64_t* work_full = bars;           // [2]
-  uint64_t* work_empty = bars + 2;      // [2] 8 softmax warps, 2 issuers
+  uint64_t* work_empty = bars + 2;      // [2] 8 softmax warps, 2 issuers, the loads
   uint64_t* q_full = bars + 4;          // [2]
-  uint64_t* q_empty = bars + 6;         // [2] both issuers
+  uint64_t* q_empty = bars + 6;         // [2] both issuers' last S, 8 warps' O stored from it
   uint64_t* s_full = bars + 8;          // [half][buffer]
   uint64_t* p_full = bars + 12;         // [half][buffer] 4 warps
   uint64_t* pv_done = bars + 16;        // [half]
@@ -118,9 +122,9 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&work_full[i], 1);
-      mbar_init(&work_empty[i], 10);
+      mbar_init(&work_empty[i], 11);
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 2);
+      mbar_init(&q_empty[i], 2 + 8);
       mbar_init(&pv_done[i], 1);
       mbar_init(&drain[i], 1);
     }
@@ -138,7 +142,10 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) tma_prefetch(&p.map_qkv);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch(&p.map_qkv);
+    tma_prefetch(&p.map_o);
+  }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
@@ -148,13 +155,60 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == 0) {
-    // ------------------------------------------------ items and loads (the
-    // whole warp runs the loop, one lane issues)
-    int block = blockIdx.x;
-    int it = 0, qi = 0, c = 0;  // items, items with keys, tiles loaded
-    int v_row = -1, v_col = 0, v_bi = 0;  // V of the last step, loaded after the next K
-    bool ok = true, asked = false;
+  if (warp == 11) {
+    // ------------------------------------------------ items (the whole warp)
+    // The next item is asked for when every warp has begun the current one,
+    // so that a CTA holds one item back from the others at most.
+    int block = blockIdx.x, it = 0;
+    bool asked = false;
+    while (true) {
+      if (block < 0) {
+        if (lane == 0) {
+          item_at(it)->n = -1;
+          mbar_arrive(&work_full[it & 1]);
+        }
+        break;
+      }
+      const Item w = item_of(p.order, block);
+      const int bi = w.kv / (p.H / p.G), n = w.kv % (p.H / p.G) * p.G + w.sub;
+      const int q0 = (p.order.tiles - 1 - w.tile) * 128;
+      // key tiles [j0, j0 + nkv) hold every key that some row sees
+      int lo = INT32_MAX, hi = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int2 win = key_window(p.row_begin, p.row_end, p.causal, p.s, bi, q0 + 32 * k + lane);
+        if (win.x < win.y) lo = min(lo, win.x);
+        hi = max(hi, win.y);
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      const int j0 = lo < hi ? lo / 128 : 0;
+      if (lane == 0) {
+        volatile WorkItem* to = item_at(it);
+        to->n = n;
+        to->bi = bi;
+        to->q0 = q0;
+        to->j0 = j0;
+        to->nkv = lo < hi ? (hi + 127) / 128 - j0 : 0;
+        mbar_arrive(&work_full[it & 1]);
+      }
+      if (!bounded_wait_w(&work_empty[it & 1], (it >> 1) & 1, abort_flag, 252, p.err)) break;
+      if (lane == 0) request_block(answer + 16 * (it & 1), answered);
+      asked = true;
+      if (!bounded_wait_w(answered, it & 1, abort_flag, 257, p.err)) break;
+      asked = false;
+      block = answered_block(answer + 16 * (it & 1));
+      fence_proxy_async_smem();
+      __syncwarp();
+      ++it;
+    }
+    // a request in flight lands before the shared memory goes
+    if (asked) drain_wait(answered, it & 1);
+  } else if (warp == 0) {
+    // ------------------------------------------------ loads (the whole warp
+    // runs the loop, one lane issues)
+    int qi = 0, c = 0;  // items with keys, tiles loaded
+    bool ok = true;
     auto load_tile = [&](int col, int row, int bi) -> bool {
       const int st = c % NT;
       if (c >= NT && !bounded_wait_w(&t_empty[st], ((c / NT) & 1) ^ 1, abort_flag, 251, p.err)) return false;
@@ -167,104 +221,63 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
       ++c;
       return true;
     };
-    while (ok && block >= 0) {
-      if (lane == 0) request_block(answer + 16 * (it & 1), answered);
-      asked = true;
-      const int pair = block / p.n_qt;
-      const int n = pair % p.H, bi = pair / p.H;
-      const int q0 = (p.n_qt - 1 - block % p.n_qt) * 128;
-      const int g = n / p.G;
-      // key tiles [j0, j0 + nkv) hold every key that some row sees
-      int lo = INT32_MAX, hi = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int2 w = key_window(p.row_begin, p.row_end, p.causal, p.s, bi, q0 + 32 * k + lane);
-        if (w.x < w.y) lo = min(lo, w.x);
-        hi = max(hi, w.y);
-      }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      const int j0 = lo < hi ? lo / 128 : 0;
-      const int nkv = lo < hi ? (hi + 127) / 128 - j0 : 0;
-      if (it >= 2 && !bounded_wait_w(&work_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, 252, p.err)) { ok = false; break; }
-      if (lane == 0) {
-        volatile WorkItem* w = item_at(it);
-        w->n = n;
-        w->bi = bi;
-        w->q0 = q0;
-        w->j0 = j0;
-        w->nkv = nkv;
-        mbar_arrive(&work_full[it & 1]);
-      }
-      if (nkv > 0) {
-        const int sl = qi & 1;
-        if (qi >= 2 && !bounded_wait_w(&q_empty[sl], ((qi >> 1) & 1) ^ 1, abort_flag, 256, p.err)) { ok = false; break; }
-        if (lane == 0) {
-          mbar_expect_tx(&q_full[sl], T::TILE);
-#pragma unroll
-          for (int k = 0; k < T::NCH; ++k)
-            tma_load_3d(sQ + sl * T::TILE + k * T::CHUNK, &p.map_qkv, &q_full[sl], n * D + k * T::CW, q0, bi);
-        }
-        ++qi;
-        for (int j = j0; ok && j < j0 + nkv; ++j) {
-          ok = load_tile(p.k_col + g * D, j * 128, bi);
-          if (ok && v_row >= 0) ok = load_tile(v_col, v_row, v_bi);
-          v_row = j * 128;
-          v_col = p.v_col + g * D;
-          v_bi = bi;
-        }
-        if (!ok) break;
-      }
-      if (!bounded_wait_w(answered, it & 1, abort_flag, 257, p.err)) { ok = false; break; }
-      asked = false;
-      block = answered_block(answer + 16 * (it & 1));
-      fence_proxy_async_smem();
+    for (int it = 0; ok; ++it) {
+      if (!bounded_wait_w(&work_full[it & 1], (it >> 1) & 1, abort_flag, 250, p.err)) break;
+      volatile WorkItem* w = item_at(it);
+      const int n = w->n, bi = w->bi, q0 = w->q0, j0 = w->j0, nkv = w->nkv;
       __syncwarp();
-      ++it;
-    }
-    if (ok) {
-      if (it >= 2) ok = bounded_wait_w(&work_empty[it & 1], ((it >> 1) & 1) ^ 1, abort_flag, 252, p.err);
-      if (ok && lane == 0) {
-        item_at(it)->n = -1;
-        mbar_arrive(&work_full[it & 1]);
+      if (lane == 0) mbar_arrive(&work_empty[it & 1]);
+      if (n < 0) break;
+      if (nkv == 0) continue;
+      const int sl = qi & 1;
+      if (qi >= 2 && !bounded_wait_w(&q_empty[sl], ((qi >> 1) & 1) ^ 1, abort_flag, 256, p.err)) break;
+      if (lane == 0) {
+        mbar_expect_tx(&q_full[sl], T::TILE);
+#pragma unroll
+        for (int k = 0; k < T::NCH; ++k)
+          tma_load_3d(sQ + sl * T::TILE + k * T::CHUNK, &p.map_qkv, &q_full[sl], n * D + k * T::CW, q0, bi);
       }
-      if (ok && v_row >= 0) ok = load_tile(v_col, v_row, v_bi);
+      ++qi;
+      const int k_col = p.k_col + n / p.G * D, v_col = p.v_col + n / p.G * D;
+      for (int j = 0; ok && j <= nkv; ++j) {
+        if (j < nkv) ok = load_tile(k_col, (j0 + j) * 128, bi);
+        if (ok && j > 0) ok = load_tile(v_col, (j0 + j - 1) * 128, bi);
+      }
     }
     if (*abort_flag) {
-      // copies and the request in flight land before the shared memory goes
-      if (asked) drain_wait(answered, it & 1);
+      // copies in flight land before the shared memory goes
       for (int k = (qi > 2 ? qi - 2 : 0); k < qi; ++k) drain_wait(&q_full[k & 1], (k >> 1) & 1);
       for (int k = (c > NT ? c - NT : 0); k < c; ++k) drain_wait(&t_full[k % NT], (k / NT) & 1);
     }
   } else if (warp == 1 || warp == 10) {
     // ------------------------------------------------ MMA issuers (the
     // whole warp runs the loop, one elected lane issues).  Steps are counted
-    // through all items: S_b(t) into buffer t % 2, then PV_b(t-1); S_b(t)
-    // overwrites P_b(t-2) after PV_b(t-2) from the same thread.  The first PV
-    // of an item overwrites both O's once the item before has been read.
+    // through all items: S_b(t) into buffer t % 2, then PV_b(t-1) of the same
+    // item; an item's last PV comes before the next item's first S, which
+    // waits for loads that need not have come.  S_b(t) overwrites P_b(t-2)
+    // after PV_b(t-2) from the same thread.  The first PV of an item
+    // overwrites both O's once the item before has been read.
     const int b = warp == 1 ? 0 : 1;
     const uint32_t uKV = smem_u32(sKV), uQ = smem_u32(sQ);
     const uint32_t tSb = tmem + 128 * b;
     const uint32_t tOb = tmem + C::COL_O + b * D;
-    int t = 0, c = 0, qi = 0;
-    bool first_prev = false;  // the step before is its item's first
-    auto pv = [&](int tp, int items) -> bool {  // PV of step tp, of item number `items`
+    int t = 0, c = 0, qi = 0;  // steps and tiles through all items, items with keys
+    auto pv = [&](int tp, bool first) -> bool {  // PV of step tp, its item's first
       const int sb = tp & 1;
       if (!bounded_wait_w(&p_full[2 * b + sb], (tp >> 1) & 1, abort_flag, 255, p.err)) return false;
-      if (first_prev && items > 0 && !bounded_wait_w(o_free, (items - 1) & 1, abort_flag, 258, p.err)) return false;
+      if (first && qi > 0 && !bounded_wait_w(o_free, (qi - 1) & 1, abort_flag, 258, p.err)) return false;
       if (!bounded_wait_w(&t_full[c % NT], (c / NT) & 1, abort_flag, 253, p.err)) return false;
       tc_fence_after();
-      const uint32_t vt = uKV + (c % NT) * T::TILE;
+      const uint64_t v = T::mnmajor(uKV + (c % NT) * T::TILE, 4 * b);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        umma_bf16_tmem_a_w(tOb, tSb + sb * 64 + kk * 8, T::mnmajor(vt, 4 * b + kk), IDESC_PV, !first_prev || kk > 0);
+        umma_bf16_tmem_a_w(tOb, tSb + sb * 64 + kk * 8, v + T::mnmajor_step(kk), IDESC_PV, !first || kk > 0);
       umma_commit_w(&t_empty[c % NT]);
       umma_commit_w(&pv_done[b]);
       ++c;
       return true;
     };
     bool ok = true;
-    int prev_item = 0;
     for (int it = 0; ok; ++it) {
       if (!bounded_wait_w(&work_full[it & 1], (it >> 1) & 1, abort_flag, 254, p.err)) { ok = false; break; }
       const int n = item_at(it)->n, nkv = item_at(it)->nkv;
@@ -273,26 +286,23 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
       if (n < 0) break;
       if (nkv == 0) continue;
       if (!bounded_wait_w(&q_full[qi & 1], (qi >> 1) & 1, abort_flag, 259, p.err)) { ok = false; break; }
-      const uint32_t q = uQ + (qi & 1) * T::TILE;
-      for (int j = 0; j < nkv; ++j) {
+      const uint64_t q = T::kmajor(uQ + (qi & 1) * T::TILE, 0);
+      for (int j = 0; j < nkv; ++j, ++t) {
         if (!bounded_wait_w(&t_full[c % NT], (c / NT) & 1, abort_flag, 253, p.err)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t kt = uKV + (c % NT) * T::TILE + 64 * T::SWB * b;
+        const uint64_t k = T::kmajor(uKV + (c % NT) * T::TILE + 64 * T::SWB * b, 0);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_w(tSb + (t & 1) * 64, T::kmajor(q, kk), T::kmajor(kt, kk), IDESC_S, kk > 0);
+          umma_bf16_w(tSb + (t & 1) * 64, q + T::kmajor_step(kk), k + T::kmajor_step(kk), IDESC_S, kk > 0);
         umma_commit_w(&s_full[2 * b + (t & 1)]);
         umma_commit_w(&t_empty[c % NT]);
         if (j == nkv - 1) umma_commit_w(&q_empty[qi & 1]);
         ++c;
-        if (t > 0 && !pv(t - 1, prev_item)) { ok = false; break; }
-        first_prev = j == 0;
-        prev_item = qi;
-        ++t;
+        if (j > 0 && !pv(t - 1, j == 1)) { ok = false; break; }
       }
+      if (ok) ok = pv(t - 1, nkv == 1);
       ++qi;
     }
-    if (ok && t > 0) ok = pv(t - 1, prev_item);
     if (!ok) {
       umma_commit_w(&drain[b]);
       drain_wait(&drain[b], 0);
@@ -311,6 +321,12 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
     const float ce = (CAP || bias) ? 1.f : p.scale_log2;
     const bool fixed = CAP && p.fixed_max;
     int t = 0, items = 0;  // steps, through all items, and items with keys
+    auto stored = [&]() {  // the last item's O has left its Q buffer
+      if (lane == 0 && items > 0) {
+        bulk_wait_read0();
+        mbar_arrive(&q_empty[(items - 1) & 1]);
+      }
+    };
     bool ok = true;
     for (int it = 0; ok; ++it) {
       ok = __all_sync(0xffffffffu, bounded_wait(&work_full[it & 1], (it >> 1) & 1, abort_flag, 260, p.err));
@@ -320,6 +336,8 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) mbar_arrive(&work_empty[it & 1]);
       if (n < 0) break;
+      // (an item without keys leaves it to the next one with some)
+      if (nkv > 0) stored();
       const int2 win = key_window(p.row_begin, p.row_end, p.causal, p.s, bi, qpos);
       const bool valid = qpos < p.s;
       __nv_bfloat16* orow = p.o + (((long long)bi * p.s + qpos) * p.H + n) * D;
@@ -356,9 +374,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
           for (int i = 0; i < 32; ++i) pk[i] = 0u;
         } else {
           uint32_t sv[64];
-          tmem_ld32_nw(tb, sv);
-          tmem_ld32_nw(tb + 32, sv + 32);
-          tmem_wait_ld(sv);
+          const float largest = load_scores<CAP>(tb, sv);  // CAP: in magnitude
           auto z2 = [&](int i) { return f2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])); };
           uint64_t rs[2] = {0ull, 0ull};
           // the exponentials of e(i) = the pair (i, i+1) in log2 units
@@ -373,9 +389,8 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
           };
           bool near1 = false, near2 = false, done = false;
           if constexpr (CAP) {
-            const float am = amax_of(sv);
-            near1 = __all_sync(0xffffffffu, am <= p.cap.near1);
-            near2 = near1 || __all_sync(0xffffffffu, am <= p.cap.near2);
+            near1 = __all_sync(0xffffffffu, largest <= p.cap.near1);
+            near2 = near1 || __all_sync(0xffffffffu, largest <= p.cap.near2);
             if (fixed && near2 && __all_sync(0xffffffffu, full)) {
               // bounded scores, nothing masked: straight to the exponentials
               if (near1) exps([&](int i) { return cap_near1(p.cap, z2(i)); });
@@ -416,18 +431,27 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
                   sv[i] = __float_as_uint(fmaf(__uint_as_float(sv[i]), cs, -slope2 * fabsf(dist - (float)i)));
               }
             }
-            if (!full) {
-              // masked scores leave the maximum and the exponentials at 0
+            // masked scores to -inf; a window cuts a half on one side mostly
+            if (__any_sync(0xffffffffu, khi < 64)) {
 #pragma unroll
               for (int i = 0; i < 64; ++i)
-                if (i < klo || i >= khi) sv[i] = 0xFF800000u;
+                if (i >= khi) sv[i] = 0xFF800000u;
+            }
+            if (__any_sync(0xffffffffu, klo > 0)) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (i < klo) sv[i] = 0xFF800000u;
             }
             if (!fixed) {
-              float m4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+              float mx = largest;
+              if (CAP || bias || !full) {
+                float m4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-              for (int i = 0; i < 64; i += 2)
-                m4[(i >> 1) & 3] = max3f(m4[(i >> 1) & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-              const float m_new = fmaxf(m_run, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+                for (int i = 0; i < 64; i += 2)
+                  m4[(i >> 1) & 3] = max3f(m4[(i >> 1) & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+              }
+              const float m_new = fmaxf(m_run, mx);
               // the maximum is left stale while it moves by less than 2^8 (O
               // and l are scaled alike, so the result does not change)
               rescale = __any_sync(0xffffffffu, (m_new - m_run) * ce > 8.f);
@@ -439,7 +463,8 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
             // a row that has seen no key keeps m = -inf: offset 0, P = 2^-inf
             const float mc = (m_run == NEG_INF) ? 0.f : m_run * ce;
             const uint64_t c2 = both(ce), nmc2 = both(-mc);
-            exps([&](int i) { return fma2(z2(i), c2, nmc2); });
+            if (fixed) exps(z2);
+            else exps([&](int i) { return fma2(z2(i), c2, nmc2); });
           }
           const float2 rsum = f2split(add2(rs[0], rs[1]));
           l_run = fmaf(l_run, alpha, rsum.x + rsum.y);
@@ -481,7 +506,6 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
       ok = bounded_wait(&merged[4 * (b ^ 1) + quarter], items & 1, abort_flag, 265, p.err) &&
            bounded_wait(&pv_done[b ^ 1], (t - 1) & 1, abort_flag, 264, p.err);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      ++items;
       tc_fence_after();
       const float m_o = red_m[(b ^ 1) * 128 + r], l_o = red_l[(b ^ 1) * 128 + r];
       const float m = fmaxf(m_run, m_o);
@@ -491,35 +515,66 @@ __global__ void __launch_bounds__(352, 1) attn_mod_fwd_kernel(const __grid_const
       const float inv_l = l == 0.f ? 0.f : 1.f / l;  // nothing visible: O = 0
       const float w_self = a_self * inv_l, w_o = a_o * inv_l;
       const uint32_t tOo = tmem + C::COL_O + (b ^ 1) * D;
-      // each half writes half of the row's 16-column chunks
-      constexpr int NC = D / 16;
-      constexpr int NC0 = (NC + 1) / 2;
-      uint32_t vs[16 * NC0], vo[16 * NC0];
+      // Each half's warp merges its columns of its 32 rows and stores them by
+      // TMA (whole lines, and rows past the sequence are left out), staged in
+      // the item's Q tile, which every S product has read: O has Q's tile
+      // layout.  Direct stores of 32 bytes per row cost 3,000 cycles an item.
+      // Half a tile per half where it has an even number of chunks' columns,
+      // else the first half takes the odd one.
+      constexpr int NC = D / 16, CC = T::CW / 16;  // 16-column groups, per chunk
+      constexpr int NC0 = (T::NCH + 1) / 2 * CC;
       const int cbeg = b == 0 ? 0 : NC0, ncc = b == 0 ? NC0 : NC - NC0;
+      uint8_t* stage = sQ + (items & 1) * T::TILE;
 #pragma unroll
-      for (int cc = 0; cc < NC0; ++cc)
-        if (cc < ncc) {
-          tmem_ld16_nw(tOb + lane_off + (cbeg + cc) * 16, vs + cc * 16);
-          tmem_ld16_nw(tOo + lane_off + (cbeg + cc) * 16, vo + cc * 16);
+      for (int cc = 0; cc < NC0; cc += 2) {
+        uint32_t vs[32], vo[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (cc + h < ncc) {
+            tmem_ld16_nw(tOb + lane_off + (cbeg + cc + h) * 16, vs + 16 * h);
+            tmem_ld16_nw(tOo + lane_off + (cbeg + cc + h) * 16, vo + 16 * h);
+          }
+        tmem_wait_ld(vs);
+        tmem_wait_ld(vo);
+        if (cc + 2 >= NC0) {
+          // this warp's reads of both O's and of the other half's maxima are
+          // done: nothing overwrites either before all eight warps say so
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
         }
-      tmem_wait_ld(vs);
-      tmem_wait_ld(vo);
-      // this warp's reads of both O's and of the other half's maxima are done:
-      // nothing overwrites either before all eight warps say so
-      tc_fence_before();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (cc + h < ncc) {
+            const int col = cbeg + cc + h;  // group of 16 columns
+            uint8_t* chunk = stage + (col / CC) * T::CHUNK;
+            uint32_t pkd[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int e = 16 * h + 2 * k;
+              pkd[k] = pack_bf16(__uint_as_float(vs[e]) * w_self + __uint_as_float(vo[e]) * w_o,
+                                 __uint_as_float(vs[e + 1]) * w_self + __uint_as_float(vo[e + 1]) * w_o);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int unit = (col % CC) * 2 + k;  // 16-byte unit of the chunk's row, before the swizzle
+              const int at = T::SWB == 128 ? unit ^ (r & 7) : unit ^ ((r >> 2) & 1);
+              *reinterpret_cast<uint4*>(chunk + r * T::SWB + at * 16) =
+                  make_uint4(pkd[4 * k], pkd[4 * k + 1], pkd[4 * k + 2], pkd[4 * k + 3]);
+            }
+          }
+      }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
-#pragma unroll
-      for (int cc = 0; cc < NC0; ++cc)
-        if (cc < ncc) {
-          uint32_t vm[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            vm[k] = __float_as_uint(__uint_as_float(vs[16 * cc + k]) * w_self + __uint_as_float(vo[16 * cc + k]) * w_o);
-          if (valid) store_row16(orow + (cbeg + cc) * 16, vm, 1.f);
-        }
+      if (lane == 0) {
+        for (int ch = cbeg / CC; valid && ch < (cbeg + ncc) / CC; ++ch)  // not a box past the end
+          tma_store_3d(&p.map_o, stage + ch * T::CHUNK + quarter * 32 * T::SWB, n * D + ch * T::CW, qpos, bi);
+        bulk_commit();
+      }
+      ++items;
       if (b == 0 && lse) *lse = !valid ? 0.f : l == 0.f ? NEG_INF : fmaf(m * ce, LN2, logf(l));
     }
+    if (lane == 0) bulk_wait0();  // before the shared memory goes
   }
 
   tc_fence_before();
@@ -537,7 +592,7 @@ int launch_mod_fwd(const ModFwdParams& prm, int grid, cudaStream_t st) {
   static_assert(SMEM <= 232448, "attention forward tile set exceeds shared memory");
   static std::atomic<uint64_t> attr{0};  // devices whose limit is set
   if (smem_limit_once(reinterpret_cast<const void*>(attn_mod_fwd_kernel<D, CAP>), SMEM, &attr)) return BPT_ECUDA;
-  attn_mod_fwd_kernel<D, CAP><<<grid, 352, SMEM, st>>>(prm);
+  attn_mod_fwd_kernel<D, CAP><<<grid, 384, SMEM, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ECUDA;
 }
 
@@ -547,7 +602,9 @@ int attention_mod_fwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
                       cudaStream_t st) {
   ModFwdParams p;
   memset(&p, 0, sizeof(p));
-  if (make_attn_map(&p.map_qkv, qkv, (int)D.b, (int)D.s, D.width, (int)D.d)) return BPT_EINVAL;
+  if (make_attn_map(&p.map_qkv, qkv, (int)D.b, (int)D.s, D.width, (int)D.d, 128) ||
+      make_attn_map(&p.map_o, o, (int)D.b, (int)D.s, D.H * D.d, (int)D.d, 32))
+    return BPT_EINVAL;
   p.s = (int)D.s;
   p.s_pad = (int)D.s_pad;
   p.H = (int)D.H;
@@ -555,7 +612,7 @@ int attention_mod_fwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   p.causal = causal;
   p.k_col = (int)(D.H * D.d);
   p.v_col = (int)((D.H + D.Hkv) * D.d);
-  p.n_qt = (int)(D.s_pad / 128);
+  p.order = item_order(D.s_pad / 128, D.G, D.b * D.Hkv, 4 * D.s * D.d);
   p.o = reinterpret_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.row_begin = mod.row_begin;
@@ -566,11 +623,11 @@ int attention_mod_fwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   if (cap) {
     const double out = mod.softcap * 1.4426950408889634;
     p.cap = cap_coef(1.0 / (mod.softcap * sqrt((double)D.d)), out);
-    p.fixed_max = !mod.slopes && out <= 64.0;
+    p.fixed_max = !mod.slopes && out <= 88.0;
   }
   p.err = device_error_word();
   if (!p.err) return BPT_ECUDA;
-  const int grid = (int)(p.n_qt * D.H * D.b);
+  const int grid = (int)(D.s_pad / 128 * D.H * D.b);
   // credited as without windows, which live on the device
   const double pairs = causal ? (double)D.s * (D.s + 1) / 2 : (double)D.s * D.s;
   ProfScope prof(PROF_ATTN_FWD, 4.0 * D.d * pairs * D.H * D.b, 0.0, st);

@@ -128,21 +128,25 @@ int make_map_2d(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols,
 
 // 3-D map over a packed [b, s, ld] bf16 buffer: x = column, y = row in the
 // sequence, z = sequence.  Rows past s read as zeros within each sequence.
-// box = {chunk width, 128, 1}: 64 columns with 128-byte swizzle when d is a
+// box = {chunk width, box_rows, 1}: 64 columns with 128-byte swizzle when d is a
 // multiple of 64, else 16 columns with 32-byte swizzle.
-int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d) {
+int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d, int box_rows) {
   auto fn = encode_fn();
   if (!fn || !qkv) return 1;
   if ((reinterpret_cast<uintptr_t>(qkv) & 15) || ((ld * 2) & 15)) return 1;
   const int cw = (d % 64 == 0) ? 64 : 16;
   cuuint64_t dims[3] = {(cuuint64_t)ld, (cuuint64_t)s, (cuuint64_t)b};
   cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)s};
-  cuuint32_t box[3] = {(cuuint32_t)cw, 128, 1};
+  cuuint32_t box[3] = {(cuuint32_t)cw, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(qkv), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, cw == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : 1;
+}
+
+int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d) {
+  return make_attn_map(map, qkv, b, s, ld, d, 128);
 }
 
 // Watchdog self-test.  One thread waits, through the same bounded_wait every

@@ -293,6 +293,25 @@ __device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t* r) {
         "=r"(r[31])
       : "r"(taddr));
 }
+// The same with each thread's largest value (largest magnitude: _amax_) of
+// the 32, NaN left out; m too is valid after tmem_wait_ld, tied to it by
+// tmem_wait_max.
+#define BPT_TMEM_LD32_RED(name, op)                                                                            \
+  __device__ __forceinline__ void name(uint32_t taddr, uint32_t* r, float& m) {                                \
+    asm volatile("tcgen05.ld.red.sync.aligned.32x32b.x32." op ".f32 "                                          \
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"                                     \
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, %32, [%33];"               \
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),         \
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),     \
+                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),  \
+                   "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),  \
+                   "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=f"(m)                                 \
+                 : "r"(taddr));                                                                                \
+  }
+BPT_TMEM_LD32_RED(tmem_ld32_max_nw, "max")
+BPT_TMEM_LD32_RED(tmem_ld32_amax_nw, "max.abs")
+#undef BPT_TMEM_LD32_RED
+__device__ __forceinline__ void tmem_wait_max(float& m) { asm volatile("" : "+f"(m)); }
 // Waits for every outstanding TMEM load of this thread, then ties the N
 // registers of r to the wait so no use of them can be scheduled above it.
 template <int N>
