@@ -58,6 +58,25 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
                : "memory");
 }
 
+// Byte offset of 16-byte unit `unit` of row r in a tile's chunk, as TMA writes it
+template <int D>
+__device__ __forceinline__ int swizzled(int r, int unit) {
+  using T = TileGeom<D>;
+  return r * T::SWB + (T::SWB == 128 ? unit ^ (r & 7) : unit ^ ((r >> 2) & 1)) * 16;
+}
+// row r of a tile in shared memory as bf16 pairs
+template <int D>
+__device__ __forceinline__ void load_tile_row(const uint8_t* tile, int r, uint32_t* w) {
+  using T = TileGeom<D>;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + c * 8 / T::CW * T::CHUNK + swizzled<D>(r, c % (T::CW / 8)));
+    w[4 * c] = v.x;
+    w[4 * c + 1] = v.y;
+    w[4 * c + 2] = v.z;
+    w[4 * c + 3] = v.w;
+  }
+}
 // 16 TMEM fp32 columns of this thread's row -> 16 bf16 values (scaled)
 __device__ __forceinline__ void store_row16(__nv_bfloat16* dst, const uint32_t* v, float sc) {
   uint4 a, b;
@@ -71,6 +90,18 @@ __device__ __forceinline__ void store_row16(__nv_bfloat16* dst, const uint32_t* 
   b.w = pack_bf16(__uint_as_float(v[14]) * sc, __uint_as_float(v[15]) * sc);
   reinterpret_cast<uint4*>(dst)[0] = a;
   reinterpret_cast<uint4*>(dst)[1] = b;
+}
+
+// 16 columns (group col of the tile) of row r into a tile in shared memory
+template <int D>
+__device__ __forceinline__ void store_tile16(uint8_t* tile, int r, int col, const uint32_t* v, float sc) {
+  using T = TileGeom<D>;
+  constexpr int CC = T::CW / 16;
+  uint4 a[2];
+  store_row16(reinterpret_cast<__nv_bfloat16*>(a), v, sc);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    *reinterpret_cast<uint4*>(tile + col / CC * T::CHUNK + swizzled<D>(r, col % CC * 2 + k)) = a[k];
 }
 
 // N = D/2 consecutive 32-bit TMEM columns of this thread's lane from w

@@ -16,6 +16,8 @@
 
 #include <string.h>
 
+#include <algorithm>
+
 #include "attn_common.cuh"
 
 namespace bpt {
@@ -76,10 +78,10 @@ __device__ __forceinline__ uint64_t cap_near2(const CapCoef& f, uint64_t z) {
 }
 
 // The order of the grid: work items of tiles x heads, the tiles of all heads
-// of a group in turn, first tile index first, then the next group.  A group is
-// as many key/value heads (of any sequence) as L2 holds the streams of, so
-// that a group's last, small items balance its large first ones and every
-// stream is read from HBM once.
+// of a group in turn, first tile index first, then the next group, so that a
+// group's last, small items balance its large first ones.  A group is as many
+// key/value heads (of any sequence) as L2 holds the streams of, or 16: then
+// some ten CTAs still share a head's stream as they go.
 struct ItemOrder {
   int tiles, per_head, group, kv_heads;  // group: key/value heads in one; kv_heads: b * H_kv
 };
@@ -87,12 +89,12 @@ struct Item {
   int tile, kv, sub;  // kv: index of the key/value head over all sequences; sub < per_head
 };
 inline ItemOrder item_order(int64_t tiles, int64_t per_head, int64_t kv_heads, int64_t bytes_per_head) {
-  const int64_t fit = (int64_t)(48 << 20) / (bytes_per_head > 0 ? bytes_per_head : 1);
+  const int64_t fit = std::max<int64_t>(16, (48 << 20) / std::max<int64_t>(1, bytes_per_head));
   ItemOrder o;
   o.tiles = (int)tiles;
   o.per_head = (int)per_head;
   o.kv_heads = (int)kv_heads;
-  o.group = (int)(fit < 1 ? 1 : fit > kv_heads ? kv_heads : fit);
+  o.group = (int)std::min(fit, kv_heads);
   return o;
 }
 __device__ __forceinline__ Item item_of(const ItemOrder& o, int block) {

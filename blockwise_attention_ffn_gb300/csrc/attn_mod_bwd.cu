@@ -31,7 +31,7 @@
 #include "internal.h"
 
 namespace bpt {
-int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d);
+int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d, int box_rows);
 
 namespace {
 
@@ -48,8 +48,10 @@ static_assert(sizeof(WinRecord) % 16 == 0, "bulk copies move 16-byte units");
 struct ModBwdParams {
   CUtensorMap map_qkv;  // 3-D {width, s, b}, box {CW, 128, 1}
   CUtensorMap map_do;   // 3-D {H d, s, b}, box {CW, 128, 1}
+  CUtensorMap map_out;  // 3-D {width, s, b}, box {CW, 32, 1}: dqkv
   CUtensorMap map_aux;  // 2-D {8, b*H*s_pad} bf16, box {8, 128}, no swizzle
   int s, s_pad, H, Hkv, G, causal, n_t;
+  ItemOrder order_kv, order_q;
   int k_col, v_col;
   const float *dsum, *nl2;  // [b, H, s_pad]: dO . O and -LSE log2(e) (0 for a row that sees nothing)
   const WinRecord* rec;     // [b, n_t]
@@ -177,20 +179,19 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   uint64_t* ds_full = p_full + 2;       // [2] dS^T(u) written (4 warps)
   uint64_t* all_done = ds_full + 2;     // both issuers' last products done
   uint64_t* drain = all_done + 1;       // [2], one per issuer
-  uint64_t* kv_full = drain + 2;        // K, V tiles landed (shared-memory variant)
+  uint64_t* kv_full = drain + 2;        // K, V tiles landed
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(kv_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* range = reinterpret_cast<int*>(tmem_holder + 2);  // first and last query tile that sees the key tile
 
   const int warp = warp_id();
   const int lane = lane_id();
-  // head-major, heaviest key tiles (smallest j) of a KV head first, so the
-  // CTAs in flight share that head's Q/dO stream in L2
-  const int nq_total = (p.s + 127) / 128;
-  const int pair = blockIdx.x / nq_total;
-  const int j = blockIdx.x % nq_total;
-  const int g = pair % p.Hkv;
-  const int bi = pair / p.Hkv;
+  // the first (with a causal mask heaviest) key tiles first
+  const Item item = item_of(p.order_kv, blockIdx.x);
+  const int nq_total = p.n_t;
+  const int j = item.tile;
+  const int g = item.kv % p.Hkv;
+  const int bi = item.kv / p.Hkv;
 
   if (threadIdx.x == 0) {
     mbar_init(kv_ready, 8);
@@ -262,19 +263,20 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   if (warp == 0) {
     if (lane == 0 && U > 0) {
       // ------------------------------------------------ TMA producer
-      if constexpr (!C::KV_TMEM) {
-        mbar_expect_tx(kv_full, 2 * T::TILE);
+      // K and V: to stay (d > 80), or in the last stage until the compute
+      // warps have copied them to TMEM
+      uint8_t* kv = C::KV_TMEM ? sStage + (QS - 1) * STAGE : sKV;
+      mbar_expect_tx(kv_full, 2 * T::TILE);
 #pragma unroll
-        for (int c = 0; c < T::NCH; ++c) {
-          tma_load_3d(sKV + c * T::CHUNK, &p.map_qkv, kv_full, p.k_col + g * D + c * T::CW, j * 128, bi);
-          tma_load_3d(sKV + T::TILE + c * T::CHUNK, &p.map_qkv, kv_full, p.v_col + g * D + c * T::CW, j * 128,
-                      bi);
-        }
+      for (int c = 0; c < T::NCH; ++c) {
+        tma_load_3d(kv + c * T::CHUNK, &p.map_qkv, kv_full, p.k_col + g * D + c * T::CW, j * 128, bi);
+        tma_load_3d(kv + T::TILE + c * T::CHUNK, &p.map_qkv, kv_full, p.v_col + g * D + c * T::CW, j * 128, bi);
       }
       int issued = 0;
       for (int t = 0; t < T_iter; ++t) {
         const int st = t % QS;
         if (t >= QS && !bounded_wait(&qdo_empty[st], ((t / QS) & 1) ^ 1, abort_flag, 701, p.err)) break;
+        if (C::KV_TMEM && t == QS - 1 && !bounded_wait(kv_ready, 0, abort_flag, 702, p.err)) break;
         const int hn = g * p.G + t / n_i;
         const int i = i0 + t % n_i;
         uint8_t* sQ = sStage + st * STAGE;
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         issued = t + 1;
       }
       if (*abort_flag) {
-        if constexpr (!C::KV_TMEM) drain_wait(kv_full, 0);
+        drain_wait(kv_full, 0);
         for (int t = (issued > QS ? issued - QS : 0); t < issued; ++t)
           drain_wait(&qdo_full[t % QS], (t / QS) & 1);
       }
@@ -315,36 +317,41 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
       // without swizzle, its upper 8 columns the zeros
       const uint32_t uK = smem_u32(sKV), uV = uK + T::TILE;
       const uint32_t uKx = uK + 2 * T::TILE, uVx = uKx + C::AUX;
+      const uint64_t dK = T::kmajor(uK, 0), dV = T::kmajor(uV, 0);
+      const uint64_t dKx = sdesc(uKx, uZero - uKx, 128, 0u), dVx = sdesc(uVx, uZero - uVx, 128, 0u);
       auto issue_s = [&](int u) {
         const int b = u & 1;
         const uint32_t tSb = tS + 64 * b;
-        const uint32_t uQ = stage_u(u) + 64 * T::SWB * b;
+        const uint64_t q = T::kmajor(stage_u(u) + 64 * T::SWB * b, 0);
         const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
         if constexpr (C::KV_TMEM) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tKA + kk * 8, T::kmajor(uQ, kk), ID_S, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_tmem_a_w(tSb, tKA + kk * 8, q + T::kmajor_step(kk), ID_S, kk > 0);
           umma_bf16_tmem_a_w(tSb, tKA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
         } else {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) umma_bf16_w(tSb, T::kmajor(uK, kk), T::kmajor(uQ, kk), ID_S, kk > 0);
-          umma_bf16_w(tSb, sdesc(uKx, uZero - uKx, 128, 0u), sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_w(tSb, dK + T::kmajor_step(kk), q + T::kmajor_step(kk), ID_S, kk > 0);
+          umma_bf16_w(tSb, dKx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
         }
         umma_commit_w(&s_full[b]);
       };
       auto issue_dp = [&](int u) {
         const int b = u & 1;
         const uint32_t tdPb = tdP + 64 * b;
-        const uint32_t udO = stage_u(u) + T::TILE + 64 * T::SWB * b;
+        const uint64_t o = T::kmajor(stage_u(u) + T::TILE + 64 * T::SWB * b, 0);
         const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
         if constexpr (C::KV_TMEM) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_tmem_a_w(tdPb, tVA + kk * 8, T::kmajor(udO, kk), ID_S, kk > 0);
+            umma_bf16_tmem_a_w(tdPb, tVA + kk * 8, o + T::kmajor_step(kk), ID_S, kk > 0);
           umma_bf16_tmem_a_w(tdPb, tVA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
         } else {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) umma_bf16_w(tdPb, T::kmajor(uV, kk), T::kmajor(udO, kk), ID_S, kk > 0);
-          umma_bf16_w(tdPb, sdesc(uVx, uZero - uVx, 128, 0u), sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_w(tdPb, dV + T::kmajor_step(kk), o + T::kmajor_step(kk), ID_S, kk > 0);
+          umma_bf16_w(tdPb, dVx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
         }
         umma_commit_w(&dp_full[b]);
       };
@@ -366,8 +373,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         const int b = u & 1;
         const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
         const int st = (u >> 1) % QS;
-        const uint32_t uQ = stage_u(u);
-        const uint32_t udO = uQ + T::TILE;
+        const uint64_t dQm = T::mnmajor(stage_u(u), 4 * b), dOm = T::mnmajor(stage_u(u) + T::TILE, 4 * b);
         const bool more = u + 2 < U;
         // dV += P^T(u) dO(u): the P^T pairs sit over the first 32 columns of
         // buffer b; dO rows 64b.. are K blocks 4b..4b+3 of the stage's tile
@@ -375,7 +381,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_bf16_tmem_a_w(tdV, tSb + kk * 8, T::mnmajor(udO, 4 * b + kk), ID_KV, 1);
+          umma_bf16_tmem_a_w(tdV, tSb + kk * 8, dOm + T::mnmajor_step(kk), ID_KV, 1);
         if (more) {
           // S(u+2) overwrites P^T(u), after dV(u) in issue order
           if (!wait_stage(u + 2)) { ok = false; break; }
@@ -387,7 +393,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_bf16_tmem_a_w(tdK, tdPb + kk * 8, T::mnmajor(uQ, 4 * b + kk), ID_KV, 1);
+          umma_bf16_tmem_a_w(tdK, tdPb + kk * 8, dQm + T::mnmajor_step(kk), ID_KV, 1);
         umma_commit_w(&qdo_empty[st]);
         // dP(u+2) overwrites dS^T(u), after dK(u) in issue order
         if (more) issue_dp(u + 2);
@@ -428,21 +434,13 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive(kv_ready);
     } else {
-      // K (group 0) or V (group 1) row of this thread into TMEM as bf16
-      // pairs with the extra chunk (rows past the sequence are zero), and
-      // the group's accumulator (dV, dK) zeroed: both issuers add into it
+      // K (group 0) or V (group 1) row of this thread from the last stage,
+      // where TMA put them (zeros past the sequence), into TMEM with the
+      // extra chunk, and the group's accumulator (dV, dK) zeroed: both
+      // issuers add into it
       uint32_t w[D / 2 + 8];
-      const __nv_bfloat16* src = p.qkv + ((long long)bi * p.s + kvp) * p.width + (b ? p.v_col : p.k_col) +
-                                 (long long)g * D;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (kvp < p.s) v = *reinterpret_cast<const uint4*>(src + c * 8);
-        w[4 * c] = v.x;
-        w[4 * c + 1] = v.y;
-        w[4 * c + 2] = v.z;
-        w[4 * c + 3] = v.w;
-      }
+      const bool got = U == 0 || __all_sync(0xffffffffu, bounded_wait(kv_full, 0, abort_flag, 725, p.err));
+      if (got && U > 0) load_tile_row<D>(sStage + (QS - 1) * STAGE + b * T::TILE, r, w);
       // the extra chunk: K picks the three terms of -LSE sqrt(d) (columns
       // 0..2 of the query's extra row), V those of -D (columns 3..5)
       w[D / 2] = b ? 0u : 0x3F803F80u;
@@ -554,27 +552,27 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
     if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, 0, abort_flag, 723, p.err));
     if (ok) {
       tc_fence_after();
-      const bool valid = kvp < p.s;
+      // staged in the first stage's Q (dV) and dO (dK) tiles, which every
+      // product has read, and stored by TMA: whole lines, rows past the
+      // sequence left out
       const uint32_t tsrc = (b == 0 ? tdV : tdK) + lane_off;
-      __nv_bfloat16* row = p.dqkv + ((long long)bi * p.s + kvp) * p.width +
-                           (b == 0 ? p.v_col : p.k_col) + (long long)g * D;
+      uint8_t* tile = sStage + b * T::TILE;
       const float sc = b == 0 ? 1.f : p.scale;
-      if constexpr (D <= 80) {
-        uint32_t acc[D];
 #pragma unroll
-        for (int cc = 0; cc < D / 16; ++cc) tmem_ld16_nw(tsrc + cc * 16, acc + cc * 16);
-        tmem_wait_ld(acc);
-        if (valid) {
-#pragma unroll
-          for (int cc = 0; cc < D / 16; ++cc) store_row16(row + cc * 16, acc + cc * 16, sc);
-        }
-      } else {
-        for (int cc = 0; cc < D / 16; ++cc) {
-          uint32_t v[16];
-          tmem_ld16_nw(tsrc + cc * 16, v);
-          tmem_wait_ld(v);
-          if (valid) store_row16(row + cc * 16, v, sc);
-        }
+      for (int cc = 0; cc < D / 16; ++cc) {
+        uint32_t v[16];
+        tmem_ld16_nw(tsrc + cc * 16, v);
+        tmem_wait_ld(v);
+        store_tile16<D>(tile, r, cc, v, sc);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && kvp < p.s) {
+        for (int c = 0; c < T::NCH; ++c)
+          tma_store_3d(&p.map_out, tile + c * T::CHUNK + quarter * 32 * T::SWB,
+                       (b == 0 ? p.v_col : p.k_col) + g * D + c * T::CW, kvp, bi);
+        bulk_commit();
+        bulk_wait0();  // before the shared memory goes
       }
     }
   }
@@ -632,19 +630,20 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
   uint64_t* ds_full = dp_full + 2;     // [2] dS(u) written (4 warps)
   uint64_t* all_done = ds_full + 2;    // both issuers' last products done
   uint64_t* drain = all_done + 1;      // [2], one per issuer
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* qo_full = drain + 2;       // Q, dO landed in the last stage
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(qo_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = warp_id();
   const int lane = lane_id();
-  // head-major, heaviest query tiles of a head first; the query heads of one
-  // KV group are adjacent, so the CTAs in flight share K/V in L2
-  const int n_qt = (p.s + 127) / 128;
-  const int pair = blockIdx.x / n_qt;
-  const int i = n_qt - 1 - (int)(blockIdx.x % n_qt);
-  const int n = pair % p.H;
-  const int bi = pair / p.H;
-  const int g = n / p.G;
+  // the last (with a causal mask heaviest) query tiles first; the query heads
+  // of one key/value head are adjacent
+  const Item item = item_of(p.order_q, blockIdx.x);
+  const int n_qt = p.n_t;
+  const int i = n_qt - 1 - item.tile;
+  const int bi = item.kv / p.Hkv;
+  const int g = item.kv % p.Hkv;
+  const int n = g * p.G + item.sub;
   const int q0 = i * 128;
   // key tiles [j0, j0 + nkv) hold every key that some row sees
   const int2 span = p.span[(long long)bi * n_qt + i];
@@ -654,6 +653,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
 
   if (threadIdx.x == 0) {
     mbar_init(qo_ready, 8);
+    mbar_init(qo_full, 1);
     for (int k = 0; k < KVS; ++k) {
       mbar_init(&kv_full[k], 1);
       mbar_init(&kv_empty[k], 2);
@@ -687,10 +687,21 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------ TMA producer
+      // Q and dO, in the last stage until the compute warps have copied them
+      if (nkv > 0) {
+        uint8_t* q = sKV + (KVS - 1) * 2 * T::TILE;
+        mbar_expect_tx(qo_full, 2 * T::TILE);
+#pragma unroll
+        for (int c = 0; c < T::NCH; ++c) {
+          tma_load_3d(q + c * T::CHUNK, &p.map_qkv, qo_full, n * D + c * T::CW, q0, bi);
+          tma_load_3d(q + T::TILE + c * T::CHUNK, &p.map_do, qo_full, n * D + c * T::CW, q0, bi);
+        }
+      }
       int issued = 0;
       for (int jt = 0; jt < nkv; ++jt) {
         const int st = jt % KVS;
         if (jt >= KVS && !bounded_wait(&kv_empty[st], ((jt / KVS) & 1) ^ 1, abort_flag, 731, p.err)) break;
+        if (jt == KVS - 1 && !bounded_wait(qo_ready, 0, abort_flag, 732, p.err)) break;
         uint8_t* sK = sKV + st * 2 * T::TILE;
         uint8_t* sV = sK + T::TILE;
         mbar_expect_tx(&kv_full[st], 2 * T::TILE);
@@ -702,6 +713,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
         issued = jt + 1;
       }
       if (*abort_flag) {
+        if (nkv > 0) drain_wait(qo_full, 0);
         for (int jt = (issued > KVS ? issued - KVS : 0); jt < issued; ++jt)
           drain_wait(&kv_full[jt % KVS], (jt / KVS) & 1);
       }
@@ -722,17 +734,17 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
       auto issue_s = [&](int u) {
         const int b = u & 1;
         const uint32_t tSb = tS + 64 * b;
-        const uint32_t k = uK(u) + 64 * T::SWB * b;
+        const uint64_t k = T::kmajor(uK(u) + 64 * T::SWB * b, 0);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tQA + kk * 8, T::kmajor(k, kk), ID_S, kk > 0);
+        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tQA + kk * 8, k + T::kmajor_step(kk), ID_S, kk > 0);
         umma_commit_w(&s_full[b]);
       };
       auto issue_dp = [&](int u) {
         const int b = u & 1;
         const uint32_t tdPb = tdP + 64 * b;
-        const uint32_t v = uK(u) + T::TILE + 64 * T::SWB * b;
+        const uint64_t v = T::kmajor(uK(u) + T::TILE + 64 * T::SWB * b, 0);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tdPb, tOA + kk * 8, T::kmajor(v, kk), ID_S, kk > 0);
+        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tdPb, tOA + kk * 8, v + T::kmajor_step(kk), ID_S, kk > 0);
         umma_commit_w(&dp_full[b]);
       };
       auto wait_stage = [&](int u) {
@@ -765,9 +777,9 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
         // dQ += dS(u) K_u: key rows 64b.. are K blocks 4b..4b+3 of the tile
         if (!bounded_wait_w(&ds_full[b], (u >> 1) & 1, abort_flag, 744, p.err)) { ok = false; break; }
         tc_fence_after();
+        const uint64_t k = T::mnmajor(uK(u), 4 * b);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16_tmem_a_w(tdQ, tdPb + kk * 8, T::mnmajor(uK(u), 4 * b + kk), ID_DQ, 1);
+        for (int kk = 0; kk < 4; ++kk) umma_bf16_tmem_a_w(tdQ, tdPb + kk * 8, k + T::mnmajor_step(kk), ID_DQ, 1);
         umma_commit_w(&kv_empty[st]);
         // dP(u+2) overwrites dS(u), after dQ(u) in issue order
         if (more) issue_dp(u + 2);
@@ -791,21 +803,11 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
     const int qpos = q0 + r;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     {
-      // Q (group 0) or dO (group 1) row of this thread into TMEM as bf16
-      // pairs (rows past the sequence are zero); group 0 also zeroes dQ
+      // Q (group 0) or dO (group 1) row of this thread into TMEM (zeros past
+      // the sequence); group 0 also zeroes dQ
       uint32_t w[D / 2];
-      const __nv_bfloat16* src = b == 0
-          ? p.qkv + ((long long)bi * p.s + qpos) * p.width + (long long)n * D
-          : p.dout + ((long long)bi * p.s + qpos) * p.H * D + (long long)n * D;
-#pragma unroll
-      for (int cc = 0; cc < D / 8; ++cc) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (qpos < p.s) v = *reinterpret_cast<const uint4*>(src + cc * 8);
-        w[4 * cc] = v.x;
-        w[4 * cc + 1] = v.y;
-        w[4 * cc + 2] = v.z;
-        w[4 * cc + 3] = v.w;
-      }
+      const bool got = U == 0 || __all_sync(0xffffffffu, bounded_wait(qo_full, 0, abort_flag, 754, p.err));
+      if (got && U > 0) load_tile_row<D>(sKV + (KVS - 1) * 2 * T::TILE + b * T::TILE, r, w);
       tmem_store_row<D / 2>((b == 0 ? tQA : tOA) + lane_off, w);
       if (b == 0) {
         uint32_t z[16];
@@ -900,17 +902,24 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
     if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, 0, abort_flag, 753, p.err));
     if (ok) {
       tc_fence_after();
-      constexpr int NC = D / 16;
-      constexpr int NC0 = (NC + 1) / 2;
-      const int cbeg = b == 0 ? 0 : NC0, cend = b == 0 ? NC0 : NC;
-      const bool valid = qpos < p.s;
-      __nv_bfloat16* qrow = p.dqkv + ((long long)bi * p.s + qpos) * p.width + (long long)n * D;
+      // staged in the first stage, which every product has read, and stored
+      // by TMA
+      constexpr int CC = T::CW / 16, CH0 = (T::NCH + 1) / 2;
+      const int cbeg = b == 0 ? 0 : CH0, cend = b == 0 ? CH0 : T::NCH;  // chunks of this group
       const uint32_t tq = tdQ + lane_off;
-      for (int cc = cbeg; cc < cend; ++cc) {
+      for (int cc = cbeg * CC; cc < cend * CC; ++cc) {
         uint32_t v[16];
         tmem_ld16_nw(tq + cc * 16, v);
         tmem_wait_ld(v);
-        if (valid) store_row16(qrow + cc * 16, v, p.scale);
+        store_tile16<D>(sKV, r, cc, v, p.scale);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && qpos < p.s) {
+        for (int c = cbeg; c < cend; ++c)
+          tma_store_3d(&p.map_out, sKV + c * T::CHUNK + quarter * 32 * T::SWB, n * D + c * T::CW, qpos, bi);
+        bulk_commit();
+        bulk_wait0();  // before the shared memory goes
       }
     }
   }
@@ -1064,8 +1073,9 @@ int attention_mod_bwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   ModBwdParams p;
   memset(&p, 0, sizeof(p));
   const uint64_t rows = (uint64_t)D.b * D.H * D.s_pad;
-  if (make_attn_map(&p.map_qkv, qkv, (int)D.b, (int)D.s, D.width, (int)D.d) ||
-      make_attn_map(&p.map_do, dout, (int)D.b, (int)D.s, D.H * D.d, (int)D.d) ||
+  if (make_attn_map(&p.map_qkv, qkv, (int)D.b, (int)D.s, D.width, (int)D.d, 128) ||
+      make_attn_map(&p.map_do, dout, (int)D.b, (int)D.s, D.H * D.d, (int)D.d, 128) ||
+      make_attn_map(&p.map_out, dqkv, (int)D.b, (int)D.s, D.width, (int)D.d, 32) ||
       make_map_2d(&p.map_aux, w.aux, rows, 8, 8, 8, 128, 0))
     return BPT_EINVAL;
   p.s = (int)D.s;
@@ -1075,6 +1085,8 @@ int attention_mod_bwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   p.G = (int)D.G;
   p.causal = causal;
   p.n_t = (int)(D.s_pad / 128);
+  p.order_kv = item_order(p.n_t, 1, D.b * D.Hkv, 4 * D.G * D.s * D.d);
+  p.order_q = item_order(p.n_t, D.G, D.b * D.Hkv, 4 * D.s * D.d);
   p.k_col = (int)(D.H * D.d);
   p.v_col = (int)((D.H + D.Hkv) * D.d);
   p.dsum = w.dsum;

@@ -547,21 +547,10 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
         for (int h = 0; h < 2; ++h)
           if (cc + h < ncc) {
             const int col = cbeg + cc + h;  // group of 16 columns
-            uint8_t* chunk = stage + (col / CC) * T::CHUNK;
-            uint32_t pkd[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int e = 16 * h + 2 * k;
-              pkd[k] = pack_bf16(__uint_as_float(vs[e]) * w_self + __uint_as_float(vo[e]) * w_o,
-                                 __uint_as_float(vs[e + 1]) * w_self + __uint_as_float(vo[e + 1]) * w_o);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int unit = (col % CC) * 2 + k;  // 16-byte unit of the chunk's row, before the swizzle
-              const int at = T::SWB == 128 ? unit ^ (r & 7) : unit ^ ((r >> 2) & 1);
-              *reinterpret_cast<uint4*>(chunk + r * T::SWB + at * 16) =
-                  make_uint4(pkd[4 * k], pkd[4 * k + 1], pkd[4 * k + 2], pkd[4 * k + 3]);
-            }
+            for (int k = 16 * h; k < 16 * h + 16; ++k)
+              vs[k] = __float_as_uint(__uint_as_float(vs[k]) * w_self + __uint_as_float(vo[k]) * w_o);
+            store_tile16<D>(stage, r, col, vs + 16 * h, 1.f);
           }
       }
       fence_proxy_async_smem();
