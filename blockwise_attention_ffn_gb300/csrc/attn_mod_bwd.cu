@@ -152,6 +152,12 @@ struct ModDkdvCfg {
 // same thread.  P^T is written over S^T and dS^T over dP^T as bf16 pairs, the
 // A operands of dV = P^T dO and dK = dS^T Q.  Both issuers add into dV and dK,
 // which the compute warps zero first.
+//
+// Few key tiles (short sequences, few key/value heads) leave SMs idle, or the
+// last round of CTAs a poor fill.  Then a cluster of CTAs shares one item: each
+// takes an equal part of its (query head, query tile) stream, leaves its dV and
+// dK as fp32 in its own shared memory, and sums a share of the rows of all of
+// them in rank order through distributed shared memory.
 template <int D, bool CAP>
 __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_constant__ ModBwdParams p) {
   using T = TileGeom<D>;
@@ -187,7 +193,8 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   const int warp = warp_id();
   const int lane = lane_id();
   // the first (with a causal mask heaviest) key tiles first
-  const Item item = item_of(p.order_kv, blockIdx.x);
+  const int split = (int)cluster_size(), rank = (int)cluster_rank();
+  const Item item = item_of(p.order_kv, blockIdx.x / split);
   const int nq_total = p.n_t;
   const int j = item.tile;
   const int g = item.kv % p.Hkv;
@@ -251,8 +258,11 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   }
   const int i0 = range[0];
   const int n_i = range[1] < 0 ? 0 : range[1] - i0 + 1;
-  const int T_iter = p.G * n_i;  // stages
-  const int U = 2 * T_iter;      // sub-tiles
+  const int T_all = p.G * n_i;   // (query head, query tile) pairs of the item
+  auto part = [&](int r) { return (int)((long long)T_all * r / split); };
+  const int t0 = part(rank);
+  const int T_iter = part(rank + 1) - t0;  // stages: this CTA's pairs, from t0
+  const int U = 2 * T_iter;                // sub-tiles
   const uint32_t tS = tmem;          // + 64 b
   const uint32_t tdP = tmem + 128;   // + 64 b
   const uint32_t tdV = tmem + C::COL_DV;
@@ -277,8 +287,8 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         const int st = t % QS;
         if (t >= QS && !bounded_wait(&qdo_empty[st], ((t / QS) & 1) ^ 1, abort_flag, 701, p.err)) break;
         if (C::KV_TMEM && t == QS - 1 && !bounded_wait(kv_ready, 0, abort_flag, 702, p.err)) break;
-        const int hn = g * p.G + t / n_i;
-        const int i = i0 + t % n_i;
+        const int hn = g * p.G + (t0 + t) / n_i;
+        const int i = i0 + (t0 + t) % n_i;
         uint8_t* sQ = sStage + st * STAGE;
         uint8_t* sdO = sQ + T::TILE;
         mbar_expect_tx(&qdo_full[st], C::REC + (int)sizeof(WinRecord) + (CAP ? 512 : 0));
@@ -464,7 +474,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
     bool ok = true;
     for (int u = b; u < U; u += 2) {
       const int t = u >> 1;
-      const int q0 = (i0 + t % n_i) * 128 + 64 * b;
+      const int q0 = (i0 + (t0 + t) % n_i) * 128 + 64 * b;
       const uint8_t* stage = sStage + (t % QS) * STAGE;
       // the stage's windows and -LSE's are read below: its copies have landed
       // (the scores' products waited for them), seen here by this thread too
@@ -494,7 +504,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         if (!bias) {
           probabilities<CAP, true>(p, sv, am, pe, pk, all, lse2, on);
         } else {
-          const float slope2 = p.slopes[g * p.G + t / n_i] * 1.4426950408889634f;
+          const float slope2 = p.slopes[g * p.G + (t0 + t) / n_i] * 1.4426950408889634f;
           // along the queries; with a causal mask those before the key are masked
           const BiasLine bl = bias_line(slope2, kvp, q0, false, p.causal != 0);
           if (!__any_sync(0xffffffffu, bl.mixed)) {
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
     // epilogue: group 0 writes dV, group 1 dK, once both issuers' products
     // are done (TMEM loads by every lane, stores only for rows inside the
     // sequence)
-    if (U == 0) {
+    if (T_all == 0 && rank == 0) {
       // nothing sees this key tile
       if (kvp < p.s) {
         uint4* row = reinterpret_cast<uint4*>(p.dqkv + ((long long)bi * p.s + kvp) * p.width +
@@ -547,27 +557,35 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
 #pragma unroll
         for (int cc = 0; cc < D / 8; ++cc) row[cc] = make_uint4(0u, 0u, 0u, 0u);
       }
-      ok = false;
     }
+    ok = ok && U > 0;
     if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, 0, abort_flag, 723, p.err));
     if (ok) {
       tc_fence_after();
       // staged in the first stage's Q (dV) and dO (dK) tiles, which every
       // product has read, and stored by TMA: whole lines, rows past the
       // sequence left out
+      // (for the cluster's sum: units of four fp32 columns by 128 rows)
       const uint32_t tsrc = (b == 0 ? tdV : tdK) + lane_off;
       uint8_t* tile = sStage + b * T::TILE;
+      uint4* sums = reinterpret_cast<uint4*>(sStage) + b * (D / 4) * 128;
       const float sc = b == 0 ? 1.f : p.scale;
 #pragma unroll
       for (int cc = 0; cc < D / 16; ++cc) {
         uint32_t v[16];
         tmem_ld16_nw(tsrc + cc * 16, v);
         tmem_wait_ld(v);
-        store_tile16<D>(tile, r, cc, v, sc);
+        if (split == 1) {
+          store_tile16<D>(tile, r, cc, v, sc);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sums[(4 * cc + k) * 128 + r] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && kvp < p.s) {
+      if (split == 1 && lane == 0 && kvp < p.s) {
         for (int c = 0; c < T::NCH; ++c)
           tma_store_3d(&p.map_out, tile + c * T::CHUNK + quarter * 32 * T::SWB,
                        (b == 0 ? p.v_col : p.k_col) + g * D + c * T::CW, kvp, bi);
@@ -575,6 +593,46 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         bulk_wait0();  // before the shared memory goes
       }
     }
+  }
+
+  if (split > 1) {
+    // every CTA comes here, also after a timeout
+    static_assert(QS * STAGE >= 128 * 2 * D * 4, "the sums' columns");
+    __syncwarp();
+    cluster_sync_all();
+    if (warp >= 2 && warp < 10 && T_all > 0) {
+      const int rows = 128 / split, r0 = rank * rows;
+      const uint32_t mine = smem_u32(sStage);
+      for (int unit = threadIdx.x - 64; unit < rows * (2 * D / 16); unit += 256) {
+        const int row = r0 + unit % rows, cc = unit / rows;  // 16 columns of dV, then of dK
+        float acc[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[k] = 0.f;
+        for (int c = 0; c < split; ++c) {
+          if (part(c + 1) == part(c)) continue;  // it had no pairs
+          const uint32_t from = cluster_addr(mine, c) + (4 * cc * 128 + row) * 16;
+          float4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = ld_cluster_f32x4(from + k * 2048);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            acc[4 * k] += v[k].x;
+            acc[4 * k + 1] += v[k].y;
+            acc[4 * k + 2] += v[k].z;
+            acc[4 * k + 3] += v[k].w;
+          }
+        }
+        const int kv_row = j * 128 + row;
+        if (kv_row < p.s) {
+          const bool is_v = cc < D / 16;
+          __nv_bfloat16* dst = p.dqkv + ((long long)bi * p.s + kv_row) * p.width +
+                               (is_v ? p.v_col + 16 * cc : p.k_col + 16 * cc - D) + (long long)g * D;
+          store_row16(dst, reinterpret_cast<const uint32_t*>(acc), is_v ? 1.f : p.scale);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // the others have read this CTA's sums
   }
 
   tc_fence_before();
@@ -1018,6 +1076,19 @@ __global__ void __launch_bounds__(256) attn_mod_prep_kernel(int b, int s, int n_
   }
 }
 
+// CTAs that share one dK/dV item.  Sharing costs the sum over the cluster (some
+// 4,000 cycles a CTA), so only where items leave SMs idle, up to two CTAs per
+// SM, while a CTA's stream keeps a dozen query tiles.  Measured, dK/dV alone:
+// 108 items of up to 27 tiles (d = 96) 82 us unshared, 65 by 2, 85 by 4; 32
+// items of up to 256 tiles (d = 128) 417 us, 112 by 8; 1024 items of up to 16
+// tiles (d = 80) 121 us, 218 by 2.
+int split_for(int items, int stream) {
+  const int nsm = sm_count();
+  int s = 1;
+  while (s < 8 && items * 2 * s <= 2 * nsm && stream >= 2 * s * 12) s *= 2;
+  return s;
+}
+
 template <int D, bool CAP>
 int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
   constexpr int SMEM_KV = ModDkdvCfg<D>::SMEM, SMEM_Q = ModDqCfg<D>::SMEM;
@@ -1028,8 +1099,20 @@ int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
     return BPT_ECUDA;
   {
     ProfScope prof(PROF_ATTN_BWD, 8.0 * D * pairs * p.H * b, 0.0, st);
-    attn_mod_dkdv_kernel<D, CAP><<<p.n_t * p.Hkv * b, 352, SMEM_KV, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return BPT_ECUDA;
+    // CTAs per item: see split_for
+    const int items = p.n_t * p.Hkv * b, split = split_for(items, p.G * p.n_t);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items * split));
+    cfg.blockDim = dim3(352);
+    cfg.dynamicSmemBytes = SMEM_KV;
+    cfg.stream = st;
+    cudaLaunchAttribute a[1];
+    a[0].id = cudaLaunchAttributeClusterDimension;
+    a[0].val.clusterDim.x = (unsigned)split;
+    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+    cfg.attrs = a;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, attn_mod_dkdv_kernel<D, CAP>, p) != cudaSuccess) return BPT_ECUDA;
   }
   ProfScope prof(PROF_ATTN_BWD, 2.0 * D * pairs * p.H * b, 0.0, st);
   attn_mod_dq_kernel<D, CAP><<<p.n_t * p.H * b, 352, SMEM_Q, st>>>(p);

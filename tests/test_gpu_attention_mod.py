@@ -158,6 +158,11 @@ CASES = [
     (3, 390, 2, 2, 64, "padded", 60.0, False),
     (1, 500, 2, 1, 112, "causal", 2.0, False),
     (2, 300, 2, 2, 128, "none", 0.0, False),
+    # few key/value heads with many query heads: clusters share a key tile
+    (1, 513, 8, 1, 64, "docs", 0.0, False),
+    (1, 900, 8, 1, 128, "causal", 30.0, False),
+    (1, 1000, 16, 1, 96, "prefix", 20.0, True),
+    (1, 1030, 16, 1, 80, "none", 0.0, False),
 ]
 
 
