@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 
 from .presets import PRESETS, LayerConfig  # noqa: F401
@@ -135,7 +136,7 @@ def lib() -> ctypes.CDLL:
         L.bpt_qk_norm_rope_bwd.restype = i32
         L.bpt_clip_workspace_bytes.argtypes = []
         L.bpt_clip_workspace_bytes.restype = sz
-        L.bpt_clip_grads.argtypes = [i32, ctypes.POINTER(BptClipTensor), ctypes.c_float, i32, vp, vp, sz, vp]
+        L.bpt_clip_grads.argtypes = [i32, vp, ctypes.c_float, i32, vp, vp, sz, vp]
         L.bpt_clip_grads.restype = i32
         L.bpt_check_device_range.argtypes = [vp, sz]
         L.bpt_check_device_range.restype = i32
@@ -177,6 +178,8 @@ def make_grads(g: dict) -> BptGrads:
 def _stream(stream):
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():  # the current stream's handle, without building a Stream object
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
@@ -271,19 +274,20 @@ def bpt_lm_loss_bwd(cfg, x, w, targets, lse, dloss, dx, dw, ws, stream=None) -> 
     _check(rc, "bpt_lm_loss_bwd")
 
 
-def _want(where, t, dtype, numel, what, optional=False):
-    """Refuses (BPT_EINVAL) a tensor the library would read past or misread:
-    not on the current CUDA device, not contiguous, of another type or with
-    fewer elements than the call touches."""
-    import torch
+def _want(where, what, t, dtype, numel, dev):
+    """The address of t.  Refuses (BPT_EINVAL) a tensor the library would read
+    past or misread: not on the current CUDA device `dev`, not contiguous, of
+    another type or with fewer elements than the call touches."""
     if t is None:
-        if optional:
-            return
         raise BptError(BPT_EINVAL, f"{where}: {what} is missing")
-    if not (t.is_cuda and t.device.index == torch.cuda.current_device() and t.is_contiguous() and t.dtype == dtype
-            and t.numel() >= numel):
-        raise BptError(BPT_EINVAL, f"{where}: {what} must be a contiguous {dtype} tensor of at least {numel} "
-                                   f"elements on the current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
+    raise BptError(BPT_EINVAL, f"{where}: {what} must be a contiguous {dtype} tensor of at least {numel} elements on "
+                               f"the current device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _may(where, what, t, dtype, numel, dev):
+    return None if t is None else _want(where, what, t, dtype, numel, dev)
 
 
 def _packed_numel(c):
@@ -302,13 +306,12 @@ class ScoreMod:
     softcap: float = 0.0
 
 
-def _score_mod(where, cfg, mod):
+def _score_mod(where, cfg, mod, dev):
     import torch
-    _want(where, mod.row_begin, torch.int32, cfg.b * cfg.s, "row_begin", True)
-    _want(where, mod.row_end, torch.int32, cfg.b * cfg.s, "row_end", True)
-    _want(where, mod.slopes, torch.float32, cfg.n_heads, "slopes", True)
-    return BptScoreMod(*(None if t is None else t.data_ptr() for t in (mod.row_begin, mod.row_end, mod.slopes)),
-                       float(mod.softcap))
+    rows = cfg.b * cfg.s
+    return BptScoreMod(_may(where, "row_begin", mod.row_begin, torch.int32, rows, dev),
+                       _may(where, "row_end", mod.row_end, torch.int32, rows, dev),
+                       _may(where, "slopes", mod.slopes, torch.float32, cfg.n_heads, dev), mod.softcap)
 
 
 def bpt_attention_mod_fwd(cfg, mod, qkv, o, lse, stream=None) -> None:
@@ -316,13 +319,13 @@ def bpt_attention_mod_fwd(cfg, mod, qkv, o, lse, stream=None) -> None:
     modified by mod (a ScoreMod): o [b*s, H d] bf16 and lse [b, H, s_pad] fp32
     (None: not wanted)."""
     import torch
-    where = "bpt_attention_mod_fwd"
-    _want(where, qkv, torch.bfloat16, _packed_numel(cfg), "qkv")
-    _want(where, o, torch.bfloat16, cfg.b * cfg.s * cfg.n_heads * cfg.head_dim, "o")
-    _want(where, lse, torch.float32, cfg.b * cfg.n_heads * s_pad(cfg), "lse", True)
-    c, m = make_config(cfg), _score_mod(where, cfg, mod)
-    _check(lib().bpt_attention_mod_fwd(ctypes.byref(c), ctypes.byref(m), _ptr(qkv), _ptr(o), _ptr(lse),
-                                       _stream(stream)), where)
+    where, dev = "bpt_attention_mod_fwd", torch.cuda.current_device()
+    hd = cfg.b * cfg.s * cfg.n_heads * cfg.head_dim
+    c, m = make_config(cfg), _score_mod(where, cfg, mod, dev)
+    _check(lib().bpt_attention_mod_fwd(
+        c, m, _want(where, "qkv", qkv, torch.bfloat16, _packed_numel(cfg), dev),
+        _want(where, "o", o, torch.bfloat16, hd, dev),
+        _may(where, "lse", lse, torch.float32, cfg.b * cfg.n_heads * s_pad(cfg), dev), _stream(stream)), where)
 
 
 def bpt_attention_mod_bwd_workspace_bytes(cfg) -> int:
@@ -333,15 +336,14 @@ def bpt_attention_mod_bwd(cfg, mod, qkv, o, lse, dout, dqkv, ws, stream=None) ->
     """Gradients of bpt_attention_mod_fwd with respect to qkv, given dout
     [b*s, H d] and what the forward wrote; dqkv like qkv, a buffer of its own."""
     import torch
-    where = "bpt_attention_mod_bwd"
+    where, dev = "bpt_attention_mod_bwd", torch.cuda.current_device()
     n, hd = _packed_numel(cfg), cfg.b * cfg.s * cfg.n_heads * cfg.head_dim
-    for t, numel, what in ((qkv, n, "qkv"), (o, hd, "o"), (dout, hd, "dout"), (dqkv, n, "dqkv")):
-        _want(where, t, torch.bfloat16, numel, what)
-    _want(where, lse, torch.float32, cfg.b * cfg.n_heads * s_pad(cfg), "lse")
-    _want(where, ws, torch.uint8, 0, "ws")
-    c, m = make_config(cfg), _score_mod(where, cfg, mod)
-    _check(lib().bpt_attention_mod_bwd(ctypes.byref(c), ctypes.byref(m), _ptr(qkv), _ptr(o), _ptr(lse), _ptr(dout),
-                                       _ptr(dqkv), _ptr(ws), ws.numel(), _stream(stream)), where)
+    c, m = make_config(cfg), _score_mod(where, cfg, mod, dev)
+    _check(lib().bpt_attention_mod_bwd(
+        c, m, _want(where, "qkv", qkv, torch.bfloat16, n, dev), _want(where, "o", o, torch.bfloat16, hd, dev),
+        _want(where, "lse", lse, torch.float32, cfg.b * cfg.n_heads * s_pad(cfg), dev),
+        _want(where, "dout", dout, torch.bfloat16, hd, dev), _want(where, "dqkv", dqkv, torch.bfloat16, n, dev),
+        _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(), _stream(stream)), where)
 
 
 def bpt_qk_norm_rope_workspace_bytes(cfg) -> int:
@@ -354,15 +356,12 @@ def bpt_qk_norm_rope_fwd(cfg, qkv, wq, wk, positions, out, stream=None) -> None:
     2 H_kv) d] at `positions` [b*s] int32 (None: the row's index in its
     sequence), into out (qkv itself: in place)."""
     import torch
-    n, where = _packed_numel(cfg), "bpt_qk_norm_rope_fwd"
-    _want(where, qkv, torch.bfloat16, n, "qkv")
-    _want(where, out, torch.bfloat16, n, "out")
-    _want(where, wq, torch.bfloat16, cfg.head_dim, "wq", True)
-    _want(where, wk, torch.bfloat16, cfg.head_dim, "wk", True)
-    _want(where, positions, torch.int32, cfg.b * cfg.s, "positions", True)
-    c = make_config(cfg)
-    _check(lib().bpt_qk_norm_rope_fwd(ctypes.byref(c), _ptr(qkv), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(out),
-                                      _stream(stream)), where)
+    n, where, dev = _packed_numel(cfg), "bpt_qk_norm_rope_fwd", torch.cuda.current_device()
+    bf16, d = torch.bfloat16, cfg.head_dim
+    _check(lib().bpt_qk_norm_rope_fwd(
+        make_config(cfg), _want(where, "qkv", qkv, bf16, n, dev), _may(where, "wq", wq, bf16, d, dev),
+        _may(where, "wk", wk, bf16, d, dev), _may(where, "positions", positions, torch.int32, cfg.b * cfg.s, dev),
+        _want(where, "out", out, bf16, n, dev), _stream(stream)), where)
 
 
 def bpt_qk_norm_rope_bwd(cfg, qkv, wq, wk, positions, dout, dqkv, dwq, dwk, ws, stream=None) -> None:
@@ -370,21 +369,15 @@ def bpt_qk_norm_rope_bwd(cfg, qkv, wq, wk, positions, dout, dqkv, dwq, dwk, ws, 
     the weights' dwq, dwk [d] fp32.  qkv is the forward's input, before the
     norm.  Without weights qkv, dwq, dwk and ws may be None."""
     import torch
-    n, where = _packed_numel(cfg), "bpt_qk_norm_rope_bwd"
-    none = wq is None and wk is None
-    _want(where, qkv, torch.bfloat16, n, "qkv", none)
-    _want(where, dout, torch.bfloat16, n, "dout")
-    _want(where, dqkv, torch.bfloat16, n, "dqkv")
-    _want(where, wq, torch.bfloat16, cfg.head_dim, "wq", True)
-    _want(where, wk, torch.bfloat16, cfg.head_dim, "wk", True)
-    _want(where, positions, torch.int32, cfg.b * cfg.s, "positions", True)
-    _want(where, dwq, torch.float32, cfg.head_dim, "dwq", none)
-    _want(where, dwk, torch.float32, cfg.head_dim, "dwk", none)
-    _want(where, ws, torch.uint8, 0, "ws", none)
-    c = make_config(cfg)
-    _check(lib().bpt_qk_norm_rope_bwd(ctypes.byref(c), _ptr(qkv), _ptr(wq), _ptr(wk), _ptr(positions), _ptr(dout),
-                                      _ptr(dqkv), _ptr(dwq), _ptr(dwk), _ptr(ws), 0 if ws is None else ws.numel(),
-                                      _stream(stream)), where)
+    n, where, dev = _packed_numel(cfg), "bpt_qk_norm_rope_bwd", torch.cuda.current_device()
+    bf16, f32, d = torch.bfloat16, torch.float32, cfg.head_dim
+    need = _may if wq is None and wk is None else _want  # without weights these may be missing
+    _check(lib().bpt_qk_norm_rope_bwd(
+        make_config(cfg), need(where, "qkv", qkv, bf16, n, dev), _may(where, "wq", wq, bf16, d, dev),
+        _may(where, "wk", wk, bf16, d, dev), _may(where, "positions", positions, torch.int32, cfg.b * cfg.s, dev),
+        _want(where, "dout", dout, bf16, n, dev), _want(where, "dqkv", dqkv, bf16, n, dev),
+        need(where, "dwq", dwq, f32, d, dev), need(where, "dwk", dwk, f32, d, dev),
+        need(where, "ws", ws, torch.uint8, 0, dev), 0 if ws is None else ws.numel(), _stream(stream)), where)
 
 
 def bpt_clip_workspace_bytes() -> int:
@@ -396,25 +389,23 @@ def bpt_clip_grads(grads, max_norm, norm, ws, out=None, flags=0, stream=None) ->
     norm (one fp32 element), and grads * min(1, max_norm / (norm + 1e-6)) into
     the tensors `out` (None: in place)."""
     import torch
-    where = "bpt_clip_grads"
+    where, dev = "bpt_clip_grads", torch.cuda.current_device()
     out = grads if out is None else out
     if len(out) != len(grads):
         raise BptError(BPT_EINVAL, f"{where}: {len(grads)} gradients, {len(out)} outputs")
-    _want(where, norm, torch.float32, 1, "norm")
-    _want(where, ws, torch.uint8, 0, "ws")
-    kinds = {torch.float32: BPT_DTYPE_F32, torch.bfloat16: BPT_DTYPE_BF16}
-    table = (BptClipTensor * max(1, len(grads)))()
-    dev = torch.cuda.current_device()
-    for e, g, o in zip(table, grads, out):
-        n = g.numel()
-        if g.dtype not in kinds or o.dtype != g.dtype or o.numel() != n or not (
-                g.is_cuda and o.is_cuda and g.device.index == dev and o.device.index == dev and g.is_contiguous()
-                and o.is_contiguous()):
+    f32, bf16 = torch.float32, torch.bfloat16
+    rows = []  # BptClipTensor records as 64-bit words (the dtype in the low half of its last)
+    for g, o in zip(grads, out):
+        n, kind = g.numel(), g.dtype
+        if not ((kind is f32 or kind is bf16) and o.dtype is kind and o.numel() == n and g.get_device() == dev
+                and o.get_device() == dev and g.is_contiguous() and o.is_contiguous()):
             raise BptError(BPT_EINVAL, f"{where}: gradients and outputs must be contiguous fp32 or bf16 tensors of "
                                        f"equal type and size on the current device")
-        e.grad, e.out, e.numel, e.dtype = g.data_ptr(), o.data_ptr(), n, kinds[g.dtype]
-    _check(lib().bpt_clip_grads(len(grads), table, float(max_norm), int(flags), _ptr(norm), _ptr(ws), ws.numel(),
-                                _stream(stream)), where)
+        rows += (g.data_ptr(), o.data_ptr(), n, BPT_DTYPE_F32 if kind is f32 else BPT_DTYPE_BF16)
+    table = array("q", rows)
+    _check(lib().bpt_clip_grads(len(grads), table.buffer_info()[0], max_norm, flags,
+                                _want(where, "norm", norm, f32, 1, dev), _want(where, "ws", ws, torch.uint8, 0, dev),
+                                ws.numel(), _stream(stream)), where)
 
 
 BPT_LM_BAD_TARGET_SITE = 950

@@ -476,16 +476,31 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
       const int t = u >> 1;
       const int q0 = (i0 + (t0 + t) % n_i) * 128 + 64 * b;
       const uint8_t* stage = sStage + (t % QS) * STAGE;
-      // the stage's windows and -LSE's are read below: its copies have landed
-      // (the scores' products waited for them), seen here by this thread too
-      ok = bounded_wait(&qdo_full[t % QS], (t / QS) & 1, abort_flag, 724, p.err) &&
-           bounded_wait(&s_full[b], (u >> 1) & 1, abort_flag, 721, p.err);
+      // the stage's windows and (with a cap) -LSE's, read while the scores are
+      // still being made: the products take most of the shared memory's
+      // bandwidth, and loads among the exponentials waited for it (dK/dV of
+      // 8192 x (32 + 8 + 8) heads of 128, capped: 963 us, 930 so).  With K and V
+      // in TMEM there is room for them there and the registers are worth more
+      // (32 heads of 80: 768 us, 869 so).
+      constexpr bool EARLY = CAP && !C::KV_TMEM;
+      ok = bounded_wait(&qdo_full[t % QS], (t / QS) & 1, abort_flag, 724, p.err);
+      const WinRecord* rec = reinterpret_cast<const WinRecord*>(stage + C::REC);
+      const int2 cut = rec->cut[b];
+      const uint64_t* late = reinterpret_cast<const uint64_t*>(stage + C::NL2) + 32 * b;
+      uint64_t nl2[EARLY ? 32 : 1];
+      if constexpr (EARLY) {
+        const ulonglong2* from = reinterpret_cast<const ulonglong2*>(stage + C::NL2) + 16 * b;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const ulonglong2 v = from[k];
+          nl2[2 * k] = v.x;
+          nl2[2 * k + 1] = v.y;
+        }
+      }
+      ok = ok && bounded_wait(&s_full[b], (u >> 1) & 1, abort_flag, 721, p.err);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
       // ---- phase 1: P^T = exp2 of the modified scores - LSE log2(e)
-      const WinRecord* rec = reinterpret_cast<const WinRecord*>(stage + C::REC);
-      const float* nl2 = reinterpret_cast<const float*>(stage + C::NL2) + 64 * b;
-      const int2 cut = rec->cut[b];
       const bool all = cut.x <= j * 128 && cut.y >= j * 128 + 128;
       const int2* win = rec->row + 64 * b;
       float pe[64];
@@ -498,7 +513,8 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
           return (unsigned)(kvp - w.x) < (unsigned)w.y;
         };
         auto lse2 = [&](int x) -> uint64_t {
-          if constexpr (CAP) return *reinterpret_cast<const uint64_t*>(nl2 + x);
+          if constexpr (EARLY) return nl2[x / 2];
+          else if constexpr (CAP) return late[x / 2];
           else return 0ull;
         };
         if (!bias) {
@@ -995,9 +1011,10 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
 // What both need of the rows
 // ===========================================================================
 // The first b * n_t blocks write the windows of one query tile each; the
-// others take (row, head) pairs, 16 lanes each: D = dO . O in fp32, and from
-// it and the log-sum-exp the per-row inputs of the two kernels.  A value as
-// three bf16 terms keeps 24 bits of it.
+// others take 16 rows of one head per half-warp (whole lines in, and whole
+// lines of the [head][row] outputs): D = dO . O in fp32, and from it and the
+// log-sum-exp the per-row inputs of the two kernels.  A value as three bf16
+// terms keeps 24 bits of it.
 __device__ __forceinline__ void three_terms(float v, uint32_t (&t)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -1042,37 +1059,41 @@ __global__ void __launch_bounds__(256) attn_mod_prep_kernel(int b, int s, int n_
     }
     return;
   }
-  const int64_t total = (int64_t)b * s_pad * H;
   const int sub = threadIdx.x & 15;
-  const int64_t stride = (int64_t)(gridDim.x - b * n_t) * 16;
+  const int groups = s_pad / 16;
+  const int total = b * groups * H;
+  const int stride = (int)(gridDim.x - b * n_t) * 16;
+  const unsigned mask = 0xffffu << (threadIdx.x & 16);
   // whole half-warps step together: the shuffles below stay within one
-  for (int64_t it = (int64_t)(blockIdx.x - b * n_t) * 16 + (threadIdx.x >> 4); it < total; it += stride) {
-    const int hn = (int)(it % H);
-    const int64_t t = it / H;
-    const int q = (int)(t % s_pad);
-    const int bi = (int)(t / s_pad);
-    float acc = 0.f;
-    if (q < s && sub * 8 < d) {
-      const int64_t at = (((int64_t)bi * s + q) * H + hn) * d + sub * 8;
-      const uint4 x = *reinterpret_cast<const uint4*>(o + at), y = *reinterpret_cast<const uint4*>(dout + at);
-      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+  for (int it = (int)(blockIdx.x - b * n_t) * 16 + (threadIdx.x >> 4); it < total; it += stride) {
+    const int hn = it % H, rg = it / H;
+    const int bi = rg / groups, q0 = rg % groups * 16;
+    float mine = 0.f;  // row q0 + sub
+#pragma unroll 4
+    for (int k = 0; k < 16; ++k) {
+      float acc = 0.f;
+      if (q0 + k < s && sub * 8 < d) {
+        const int64_t at = (((int64_t)bi * s + q0 + k) * H + hn) * d + sub * 8;
+        const uint4 x = *reinterpret_cast<const uint4*>(o + at), y = *reinterpret_cast<const uint4*>(dout + at);
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc = fmaf(bf16_lo(xw[k]), bf16_lo(yw[k]), fmaf(bf16_hi(xw[k]), bf16_hi(yw[k]), acc));
-    }
-    const unsigned mask = 0xffffu << (threadIdx.x & 16);
+        for (int m = 0; m < 4; ++m)
+          acc = fmaf(bf16_lo(xw[m]), bf16_lo(yw[m]), fmaf(bf16_hi(xw[m]), bf16_hi(yw[m]), acc));
+      }
 #pragma unroll
-    for (int k = 8; k > 0; k >>= 1) acc += __shfl_xor_sync(mask, acc, k);
-    if (sub == 0) {
-      const int64_t row = ((int64_t)bi * H + hn) * s_pad + q;
-      float l = q < s ? lse[row] : 0.f;
-      if (l == -INFINITY) l = 0.f;  // a row that sees nothing: every P is masked
-      uint32_t a[3] = {0u, 0u, 0u}, c[3];
-      if (!cap) three_terms(-l * inv_scale, a);
-      three_terms(-acc, c);
-      dsum[row] = acc;
-      nl2[row] = -1.4426950408889634f * l;
-      aux[row] = make_uint4(a[0] | (a[1] << 16), a[2] | (c[0] << 16), c[1] | (c[2] << 16), 0u);
+      for (int m = 8; m > 0; m >>= 1) acc += __shfl_xor_sync(mask, acc, m);
+      if (sub == k) mine = acc;
     }
+    const int q = q0 + sub;
+    const int64_t row = ((int64_t)bi * H + hn) * s_pad + q;
+    float l = q < s ? lse[row] : 0.f;
+    if (l == -INFINITY) l = 0.f;  // a row that sees nothing: every P is masked
+    uint32_t a[3] = {0u, 0u, 0u}, c[3];
+    if (!cap) three_terms(-l * inv_scale, a);
+    three_terms(-mine, c);
+    dsum[row] = mine;
+    nl2[row] = -1.4426950408889634f * l;
+    aux[row] = make_uint4(a[0] | (a[1] << 16), a[2] | (c[0] << 16), c[1] | (c[2] << 16), 0u);
   }
 }
 
@@ -1197,8 +1218,8 @@ int attention_mod_bwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   const int tiles = (int)(D.b * p.n_t);
   {
     ProfScope prof(PROF_MISC, 0.0, 4.0 * D.rows * D.H * D.d + 28.0 * rows, st);
-    const int64_t pairs = (int64_t)rows;
-    const int blocks = (int)std::min<int64_t>((pairs + 15) / 16, (int64_t)nsm * 16);
+    const int64_t items = (int64_t)rows / 16;  // 16 per block and round
+    const int blocks = (int)std::min<int64_t>((items + 15) / 16, (int64_t)nsm * 16);
     attn_mod_prep_kernel<<<tiles + blocks, 256, 0, st>>>(
         (int)D.b, p.s, p.n_t, p.H, (int)D.d, causal, cap, sqrtf((float)D.d), p.row_begin, p.row_end,
         reinterpret_cast<const __nv_bfloat16*>(o), p.dout, lse, w.rec, w.span, w.dsum, w.nl2, w.aux);
