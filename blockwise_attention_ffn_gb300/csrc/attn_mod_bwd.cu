@@ -237,6 +237,10 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  // what the preparation wrote; the dQ kernel, which needs nothing of this
+  // one, fills the SMs that this one's last round leaves idle
+  wait_for_previous();
+  let_next_start();
   {
     // query tiles with a row that may see this key tile; tiles between the
     // first and the last that see nothing of it are masked like any other
@@ -1001,6 +1005,9 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // dK/dV started after the preparation had ended and let this kernel start,
+  // so nothing above waited for it; but the call ends when both have
+  if (blockIdx.x == gridDim.x - 1) wait_for_previous();
   if (warp == 1) {
     __syncwarp();
     tmem_dealloc(tmem, 512);
@@ -1122,22 +1129,13 @@ int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
     ProfScope prof(PROF_ATTN_BWD, 8.0 * D * pairs * p.H * b, 0.0, st);
     // CTAs per item: see split_for
     const int items = p.n_t * p.Hkv * b, split = split_for(items, p.G * p.n_t);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * split));
-    cfg.blockDim = dim3(352);
-    cfg.dynamicSmemBytes = SMEM_KV;
-    cfg.stream = st;
-    cudaLaunchAttribute a[1];
-    a[0].id = cudaLaunchAttributeClusterDimension;
-    a[0].val.clusterDim.x = (unsigned)split;
-    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
-    cfg.attrs = a;
-    cfg.numAttrs = split > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, attn_mod_dkdv_kernel<D, CAP>, p) != cudaSuccess) return BPT_ECUDA;
+    if (launch_dependent(attn_mod_dkdv_kernel<D, CAP>, items * split, split, dim3(352), SMEM_KV, st, p) != cudaSuccess)
+      return BPT_ECUDA;
   }
   ProfScope prof(PROF_ATTN_BWD, 2.0 * D * pairs * p.H * b, 0.0, st);
-  attn_mod_dq_kernel<D, CAP><<<p.n_t * p.H * b, 352, SMEM_Q, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ECUDA;
+  return launch_dependent(attn_mod_dq_kernel<D, CAP>, p.n_t * p.H * b, 1, dim3(352), SMEM_Q, st, p) == cudaSuccess
+             ? BPT_OK
+             : BPT_ECUDA;
 }
 
 struct ModBwdWs {

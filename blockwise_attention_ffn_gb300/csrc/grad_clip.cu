@@ -27,6 +27,7 @@
 
 #include "../../include/bpt.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace bpt {
 namespace {
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(CLIP_THREADS) clip_norm_kernel(const __grid_co
       acc += squares(w, k.bf16);
     }
   }
+  let_next_start();
   __shared__ double red[CLIP_THREADS / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
@@ -175,6 +177,7 @@ __global__ void __launch_bounds__(CLIP_THREADS) clip_scale_kernel(const __grid_c
                                                                   const double* part, int nparts, float max_norm,
                                                                   float* norm_out) {
   __shared__ double red[CLIP_THREADS / 32];
+  wait_for_previous();
   double acc = 0.0;
   for (int i = threadIdx.x; i < nparts; i += CLIP_THREADS) acc += part[i];
 #pragma unroll
@@ -277,8 +280,16 @@ int clip_launches(int n, const bpt_clip_tensor* t, float max_norm, float* norm, 
         nparts = grid;
         clip_norm_kernel<N><<<grid, CLIP_THREADS, 0, st>>>(tb, part, k);
       } else {
-        clip_scale_kernel<N><<<std::max(1, std::min(cap, chunks)), CLIP_THREADS, 0, st>>>(
-            tb, part, nparts, max_norm, k == 0 ? norm : nullptr);
+        // (of the last norm kernel; a later table's is an ordinary launch)
+        const int grid = std::max(1, std::min(cap, chunks));
+        float* out = k == 0 ? norm : nullptr;
+        if (k == 0) {
+          if (launch_dependent(clip_scale_kernel<N>, grid, 1, dim3(CLIP_THREADS), 0, st, tb, (const double*)part, nparts,
+                               max_norm, out) != cudaSuccess)
+            return BPT_ECUDA;
+        } else {
+          clip_scale_kernel<N><<<grid, CLIP_THREADS, 0, st>>>(tb, part, nparts, max_norm, out);
+        }
       }
       if (cudaGetLastError() != cudaSuccess) return BPT_ECUDA;
     }

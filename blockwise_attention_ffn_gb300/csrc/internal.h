@@ -63,6 +63,27 @@ inline int smem_limit_once(const void* kernel, int bytes, std::atomic<uint64_t>*
   return 0;
 }
 
+// Launches kernel(args...) as the dependent of the kernel before it in the
+// stream (ptx.cuh: wait_for_previous), in clusters of `cluster` blocks.
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), int grid, int cluster, dim3 block, size_t smem,
+                                    cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = (unsigned)cluster;
+  a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+}
+
 // ---------------------------------------------------------------- TMA maps
 // 2-D bf16 (or fp32) tensor map over a row-major matrix view [rows, cols]
 // with a leading dimension of `ld` elements.  box = {box_cols, box_rows};

@@ -255,6 +255,7 @@ __global__ void __launch_bounds__(NR_THREADS, BWD ? 2 : 3) norm_rope_kernel(cons
       }
     }
   }
+  if (BWD) let_next_start();
   if (p.copy_v) {
     const __nv_bfloat16* src = BWD ? p.dy : p.x;
     const int per = p.K * D / 8;  // 16-byte units of a row
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(NR_THREADS, BWD ? 2 : 3) norm_rope_kernel(cons
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int nparts, int d, float* dwq,
                                                             float* dwk, int accumulate) {
   __shared__ float red[32][33];
+  wait_for_previous();
   const int c = blockIdx.x * 32 + threadIdx.x;
   float s = 0.f;
   for (int i = threadIdx.y; i < nparts; i += 32) s += part[(int64_t)i * 2 * d + c];
@@ -429,9 +431,9 @@ int bpt_qk_norm_rope_bwd(const bpt_config* cfg, const void* qkv, const void* wq,
     ProfScope prof(PROF_NORM, 0.0, (wq ? 3.0 : 2.0) * (bytes - v) + (p.copy_v ? 2 * v : 0.0), st);
     rc = launch<true>(p, blocks, st);
     if (!rc && wq) {
-      norm_rope_dw_kernel<<<(unsigned)(2 * D.d / 32), dim3(32, 32), 0, st>>>(p.part, blocks, (int)D.d, dwq, dwk,
-                                                                             D.accum);
-      if (cudaGetLastError() != cudaSuccess) rc = BPT_ECUDA;
+      if (launch_dependent(norm_rope_dw_kernel, (int)(2 * D.d / 32), 1, dim3(32, 32), 0, st, (const float*)p.part,
+                           blocks, (int)D.d, dwq, dwk, (int)D.accum) != cudaSuccess)
+        rc = BPT_ECUDA;
     }
   }
   if (rc) return rc;

@@ -399,6 +399,13 @@ __device__ __forceinline__ void named_bar(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launch
+// A kernel launched as the dependent of the one before it in the stream may
+// start once every block of that one has let it (or ended); wait_for_previous
+// returns when that kernel has ended and its writes are visible.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- work stealing
 // A running block takes over blocks of its grid that have not started
 // (cluster launch control): the request writes 16 bytes at `res` and
