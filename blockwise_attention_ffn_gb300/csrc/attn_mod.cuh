@@ -65,17 +65,19 @@ inline CapCoef cap_coef(double k, double out) {
   return f;
 }
 __device__ __forceinline__ uint64_t both(float v) { return f2(v, v); }
-__device__ __forceinline__ uint64_t cap_near1(const CapCoef& f, uint64_t z) {
+__device__ __forceinline__ uint64_t near1_factor(const CapCoef& f, uint64_t z) {
   const uint64_t w = mul2(z, z);
-  return mul2(z, fma2(w, fma2(w, f.c[2], f.c[1]), f.c[0]));
+  return fma2(w, fma2(w, f.c[2], f.c[1]), f.c[0]);
 }
-__device__ __forceinline__ uint64_t cap_near2(const CapCoef& f, uint64_t z) {
+__device__ __forceinline__ uint64_t near2_factor(const CapCoef& f, uint64_t z) {
   const uint64_t w = mul2(z, z);
   uint64_t q = fma2(w, f.e[4], f.e[3]);
   q = fma2(w, q, f.e[2]);
   q = fma2(w, q, f.e[1]);
-  return mul2(z, fma2(w, q, f.e[0]));
+  return fma2(w, q, f.e[0]);
 }
+__device__ __forceinline__ uint64_t cap_near1(const CapCoef& f, uint64_t z) { return mul2(z, near1_factor(f, z)); }
+__device__ __forceinline__ uint64_t cap_near2(const CapCoef& f, uint64_t z) { return mul2(z, near2_factor(f, z)); }
 
 // The order of the grid: work items of tiles x heads, the tiles of all heads
 // of a group in turn, first tile index first, then the next group, so that a
@@ -132,18 +134,28 @@ __device__ __forceinline__ float load_scores(uint32_t taddr, uint32_t (&sv)[64])
   return fmaxf(a, b);
 }
 
-// The bias -a |i - j| along a run of 64 consecutive indices from `first`
-// against the fixed index `self`, as base + k * step for k = 0..63, unless
+// The bias -a |i - j| along a run of n consecutive indices from `first`
+// against the fixed index `self`, as base + k * step for k < n, unless
 // the run passes `self` strictly inside (mixed).  below_only: indices above
 // `self` are masked anyway; above_only: those below.
 struct BiasLine {
   float base, step;
   bool mixed;
 };
-__device__ __forceinline__ BiasLine bias_line(float slope2, int self, int first, bool below_only, bool above_only) {
+// (k, k + 1) as fp32 for even k < 64: operands of packed arithmetic
+#define BPT_PAIRS8(k) {k, k + 1}, {k + 2, k + 3}, {k + 4, k + 5}, {k + 6, k + 7}
+static __constant__ float2 index_pairs[32] = {BPT_PAIRS8(0.f),  BPT_PAIRS8(8.f),  BPT_PAIRS8(16.f), BPT_PAIRS8(24.f),
+                                              BPT_PAIRS8(32.f), BPT_PAIRS8(40.f), BPT_PAIRS8(48.f), BPT_PAIRS8(56.f)};
+#undef BPT_PAIRS8
+// base + k * step of the pair (k, k + 1)
+__device__ __forceinline__ uint64_t on_line(int k, uint64_t step2, uint64_t base2) {
+  const float2 i = index_pairs[k / 2];
+  return fma2(f2(i.x, i.y), step2, base2);
+}
+__device__ __forceinline__ BiasLine bias_line(float slope2, int self, int first, int n, bool below_only, bool above_only) {
   BiasLine b;
   const int dist = self - first;  // > 0: the run starts below self
-  const bool below = !above_only && dist >= (below_only ? 1 : 63);
+  const bool below = !above_only && dist >= (below_only ? 1 : n - 1);
   b.mixed = dist > 0 && !below && !above_only;
   b.base = below ? -slope2 * (float)dist : slope2 * (float)dist;
   b.step = below ? slope2 : -slope2;

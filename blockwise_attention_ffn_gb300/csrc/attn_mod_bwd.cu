@@ -526,10 +526,11 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         } else {
           const float slope2 = p.slopes[g * p.G + (t0 + t) / n_i] * 1.4426950408889634f;
           // along the queries; with a causal mask those before the key are masked
-          const BiasLine bl = bias_line(slope2, kvp, q0, false, p.causal != 0);
+          const BiasLine bl = bias_line(slope2, kvp, q0, 64, false, p.causal != 0);
           if (!__any_sync(0xffffffffu, bl.mixed)) {
+            const uint64_t step2 = both(bl.step), base2 = both(bl.base);
             auto add = [&](int x) {
-              return add2(lse2(x), f2(fmaf(bl.step, (float)x, bl.base), fmaf(bl.step, (float)(x + 1), bl.base)));
+              return CAP ? add2(lse2(x), on_line(x, step2, base2)) : on_line(x, step2, base2);
             };
             probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
           } else {
@@ -929,11 +930,10 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
           auto add = [&](int) { return nl2; };
           probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
         } else {
-          const BiasLine bl = bias_line(slope2, qpos, kv0, p.causal != 0, false);
+          const BiasLine bl = bias_line(slope2, qpos, kv0, 64, p.causal != 0, false);
           if (!__any_sync(0xffffffffu, bl.mixed)) {
-            auto add = [&](int x) {
-              return add2(nl2, f2(fmaf(bl.step, (float)x, bl.base), fmaf(bl.step, (float)(x + 1), bl.base)));
-            };
+            const uint64_t step2 = both(bl.step), base2 = both(bl.base + nl);
+            auto add = [&](int x) { return on_line(x, step2, base2); };
             probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
           } else {
             const float dist = (float)(qpos - kv0);

@@ -8,9 +8,10 @@
 //  * A tile's first and last key tile come from its rows' windows, so packed
 //    documents, prefixes and padding cost only the tiles that some row sees.
 //  * Scores are modified between the tensor core and the softmax.  With a cap
-//    of at most 61 and no bias the exponentials stay within 2^-88 and 2^88,
-//    which leaves fp32 sums 2^39 for keys and values, so the running maximum is
-//    dropped: every row keeps m = 0.
+//    of at most 61 the exponentials stay within 2^-88 and 2^88, which leaves
+//    fp32 sums 2^39 for keys and values: no maximum is looked for, m = 0 (or
+//    the largest bias seen).  Biased scores without a cap take the load's own
+//    maximum and the nearest key's bias for an upper bound of theirs.
 //  * Row sums are fp32 sums of the fp32 exponentials, so the log-sum-exp is an
 //    fp32-exact output; the tensor core's row sums of bf16 P would be off by
 //    up to 2^-9.
@@ -54,7 +55,7 @@ struct ModFwdParams {
   const float* slopes;
   float scale_log2;  // log2(e)/sqrt(d)
   CapCoef cap;       // capped scores in log2 units
-  int fixed_max;
+  int bounded;  // the capped scores' exponentials and their sums stay in fp32's range
   unsigned int* err;
 };
 
@@ -78,7 +79,7 @@ struct ModFwdCfg {
   static constexpr uint32_t COL_O = 256;
 };
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_constant__ ModFwdParams p) {
   using T = TileGeom<D>;
   using C = ModFwdCfg<D>;
@@ -115,6 +116,12 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
   uint64_t* t_empty = t_full + NT;      // [NT] both issuers
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(t_empty + NT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  // Step j's key tile.  With a bias the last comes first: the keys nearest to a
+  // row set its maximum, and the rest never move it (32 heads of 80, causal:
+  // 423 us, 475 in ascending order, where a steep head's O is rescaled at
+  // every step).  Else ascending: then the CTAs of a head begin with the same
+  // keys (32 + 8 + 8 heads of 128: 422 us, 436 descending).
+  auto key_tile = [](int j, int j0, int nkv) { return BIAS ? j0 + nkv - 1 - j : j0 + j; };
   auto item_at = [&](int it) { return reinterpret_cast<volatile WorkItem*>(reinterpret_cast<uint8_t*>(work) + 32 * (it & 1)); };
 
   const int warp = warp_id();
@@ -240,8 +247,8 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       ++qi;
       const int k_col = p.k_col + n / p.G * D, v_col = p.v_col + n / p.G * D;
       for (int j = 0; ok && j <= nkv; ++j) {
-        if (j < nkv) ok = load_tile(k_col, (j0 + j) * 128, bi);
-        if (ok && j > 0) ok = load_tile(v_col, (j0 + j - 1) * 128, bi);
+        if (j < nkv) ok = load_tile(k_col, key_tile(j, j0, nkv) * 128, bi);
+        if (ok && j > 0) ok = load_tile(v_col, key_tile(j - 1, j0, nkv) * 128, bi);
       }
     }
     if (*abort_flag) {
@@ -315,11 +322,11 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tSb = tmem + 128 * b;
     const uint32_t tOb = tmem + C::COL_O + b * D;
-    const bool bias = p.slopes != nullptr;
     // the units of m and of the scores when exponentiated: raw scores times
     // log2(e)/sqrt(d) without a modifier, else already log2
-    const float ce = (CAP || bias) ? 1.f : p.scale_log2;
-    const bool fixed = CAP && p.fixed_max;
+    const float ce = (CAP || BIAS) ? 1.f : p.scale_log2;
+    // bounded scores: the maximum is that of the bias alone (0 without one)
+    const bool bounded = CAP && p.bounded;
     int t = 0, items = 0;  // steps, through all items, and items with keys
     auto stored = [&]() {  // the last item's O has left its Q buffer
       if (lane == 0 && items > 0) {
@@ -353,8 +360,11 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
         }
         continue;
       }
-      const float slope2 = bias ? p.slopes[n] * 1.4426950408889634f : 0.f;
-      float m_run = fixed ? 0.f : NEG_INF, l_run = 0.f;
+      const float slope2 = BIAS ? p.slopes[n] * 1.4426950408889634f : 0.f;
+      float m_run = bounded && !BIAS ? 0.f : NEG_INF, l_run = 0.f;
+      // a maximum taken from the raw scores and the nearest key's bias is too
+      // large by what the bias falls within the 64 columns: 2^-40 at most of P
+      const bool gentle = fabsf(slope2) <= 0.6f;
       for (int j = 0; j < nkv; ++j, ++t) {
         const int sb = t & 1;
         const uint32_t tb = tSb + sb * 64 + lane_off;
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         // this half's key columns [klo, khi) of the 64 are visible
-        const int kv0 = (j0 + j) * 128 + 64 * b;
+        const int kv0 = key_tile(j, j0, nkv) * 128 + 64 * b;
         const int klo = max(win.x - kv0, 0), khi = min(win.y - kv0, 64);
         const bool full = klo == 0 && khi == 64;
         uint32_t pk[32];
@@ -387,15 +397,59 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
               pk[i / 2] = pack_bf16(e0, e1);
             }
           };
+          // m: the row's reference, in the units of the scores
+          auto refer = [&](float mx) {
+            const float m_new = fmaxf(m_run, mx);
+            // the maximum is left stale while it moves by less than 2^8 (O
+            // and l are scaled alike, so the result does not change)
+            rescale = __any_sync(0xffffffffu, (m_new - m_run) * ce > 8.f);
+            if (rescale) {
+              alpha = (m_run == NEG_INF) ? 0.f : ex2((m_run - m_new) * ce);
+              m_run = m_new;
+            }
+          };
+          const bool all = __all_sync(0xffffffffu, full);
           bool near1 = false, near2 = false, done = false;
           if constexpr (CAP) {
             near1 = __all_sync(0xffffffffu, largest <= p.cap.near1);
             near2 = near1 || __all_sync(0xffffffffu, largest <= p.cap.near2);
-            if (fixed && near2 && __all_sync(0xffffffffu, full)) {
-              // bounded scores, nothing masked: straight to the exponentials
-              if (near1) exps([&](int i) { return cap_near1(p.cap, z2(i)); });
-              else exps([&](int i) { return cap_near2(p.cap, z2(i)); });
+          }
+          BiasLine line{0.f, 0.f, false};
+          if (BIAS) line = bias_line(slope2, qpos, kv0, 64, p.causal != 0, false);
+          if (BIAS && (bounded || (!CAP && gentle && all))) {
+            // the nearest visible key's bias bounds the tile's (with a
+            // negative slope the farthest one's)
+            const int first = kv0 + klo, last = kv0 + khi - 1;
+            const int dist = slope2 >= 0.f ? abs(qpos - min(max(qpos, first), last))
+                                           : max(abs(qpos - first), abs(qpos - last));
+            const float top = klo < khi ? -slope2 * (float)dist : NEG_INF;
+            refer(bounded ? top : fmaf(largest, p.scale_log2, top));
+          }
+          // nothing masked and no maximum to look for: straight to the
+          // exponentials, of (score) + (bias - m) on the line
+          if (all && (!BIAS || !__any_sync(0xffffffffu, line.mixed))) {
+            const uint64_t step2 = both(line.step), base2 = both(line.base - m_run);
+            if constexpr (CAP) {
+              if (bounded && near2) {
+                done = true;
+                if (!BIAS) {
+                  if (near1) exps([&](int i) { return cap_near1(p.cap, z2(i)); });
+                  else exps([&](int i) { return cap_near2(p.cap, z2(i)); });
+                } else if (near1) {
+                  exps([&](int i) { return fma2(z2(i), near1_factor(p.cap, z2(i)), on_line(i, step2, base2)); });
+                } else {
+                  exps([&](int i) { return fma2(z2(i), near2_factor(p.cap, z2(i)), on_line(i, step2, base2)); });
+                }
+              }
+            } else if (!BIAS) {
               done = true;
+              refer(largest);
+              const uint64_t c2 = both(p.scale_log2), nmc2 = both(-m_run * p.scale_log2);
+              exps([&](int i) { return fma2(z2(i), c2, nmc2); });
+            } else if (gentle) {
+              done = true;
+              const uint64_t c2 = both(p.scale_log2);
+              exps([&](int i) { return fma2(z2(i), c2, on_line(i, step2, base2)); });
             }
           }
           if (!done) {
@@ -417,18 +471,18 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
                   sv[i] = __float_as_uint(tanh_any(__uint_as_float(sv[i]) * p.cap.k2) * p.cap.out);
               }
             }
-            if (bias) {
-              const float cs = CAP ? 1.f : p.scale_log2;
-              const BiasLine bl = bias_line(slope2, qpos, kv0, p.causal != 0, false);
-              if (!__any_sync(0xffffffffu, bl.mixed)) {
+            if (BIAS) {
+              const uint64_t cs2 = both(CAP ? 1.f : p.scale_log2);
+              if (!__any_sync(0xffffffffu, line.mixed)) {
+                const uint64_t step2 = both(line.step), base2 = both(line.base);
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  sv[i] = __float_as_uint(fmaf(__uint_as_float(sv[i]), cs, fmaf(bl.step, (float)i, bl.base)));
+                for (int i = 0; i < 64; i += 2) put(i, fma2(z2(i), cs2, on_line(i, step2, base2)));
               } else {
                 const float dist = (float)(qpos - kv0);
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  sv[i] = __float_as_uint(fmaf(__uint_as_float(sv[i]), cs, -slope2 * fabsf(dist - (float)i)));
+                for (int i = 0; i < 64; i += 2)
+                  put(i, fma2(z2(i), cs2,
+                              f2(-slope2 * fabsf(dist - (float)i), -slope2 * fabsf(dist - (float)(i + 1)))));
               }
             }
             // masked scores to -inf; a window cuts a half on one side mostly
@@ -442,28 +496,17 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
               for (int i = 0; i < 64; ++i)
                 if (i < klo) sv[i] = 0xFF800000u;
             }
-            if (!fixed) {
-              float mx = largest;
-              if (CAP || bias || !full) {
-                float m4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+            if (!bounded && !(BIAS && !CAP && gentle && all)) {
+              float m4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-                for (int i = 0; i < 64; i += 2)
-                  m4[(i >> 1) & 3] = max3f(m4[(i >> 1) & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-                mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-              }
-              const float m_new = fmaxf(m_run, mx);
-              // the maximum is left stale while it moves by less than 2^8 (O
-              // and l are scaled alike, so the result does not change)
-              rescale = __any_sync(0xffffffffu, (m_new - m_run) * ce > 8.f);
-              if (rescale) {
-                alpha = (m_run == NEG_INF) ? 0.f : ex2((m_run - m_new) * ce);
-                m_run = m_new;
-              }
+              for (int i = 0; i < 64; i += 2)
+                m4[(i >> 1) & 3] = max3f(m4[(i >> 1) & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+              refer(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
             }
             // a row that has seen no key keeps m = -inf: offset 0, P = 2^-inf
             const float mc = (m_run == NEG_INF) ? 0.f : m_run * ce;
             const uint64_t c2 = both(ce), nmc2 = both(-mc);
-            if (fixed) exps(z2);
+            if (bounded && !BIAS) exps(z2);
             else exps([&](int i) { return fma2(z2(i), c2, nmc2); });
           }
           const float2 rsum = f2split(add2(rs[0], rs[1]));
@@ -575,14 +618,20 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
   }
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool BIAS>
 int launch_mod_fwd(const ModFwdParams& prm, int grid, cudaStream_t st) {
   constexpr int SMEM = ModFwdCfg<D>::SMEM;
   static_assert(SMEM <= 232448, "attention forward tile set exceeds shared memory");
   static std::atomic<uint64_t> attr{0};  // devices whose limit is set
-  if (smem_limit_once(reinterpret_cast<const void*>(attn_mod_fwd_kernel<D, CAP>), SMEM, &attr)) return BPT_ECUDA;
-  attn_mod_fwd_kernel<D, CAP><<<grid, 384, SMEM, st>>>(prm);
+  if (smem_limit_once(reinterpret_cast<const void*>(attn_mod_fwd_kernel<D, CAP, BIAS>), SMEM, &attr)) return BPT_ECUDA;
+  attn_mod_fwd_kernel<D, CAP, BIAS><<<grid, 384, SMEM, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ECUDA;
+}
+
+template <int D>
+int launch_for(const ModFwdParams& p, bool cap, int grid, cudaStream_t st) {
+  if (p.slopes) return cap ? launch_mod_fwd<D, true, true>(p, grid, st) : launch_mod_fwd<D, false, true>(p, grid, st);
+  return cap ? launch_mod_fwd<D, true, false>(p, grid, st) : launch_mod_fwd<D, false, false>(p, grid, st);
 }
 
 }  // namespace
@@ -612,7 +661,7 @@ int attention_mod_fwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   if (cap) {
     const double out = mod.softcap * 1.4426950408889634;
     p.cap = cap_coef(1.0 / (mod.softcap * sqrt((double)D.d)), out);
-    p.fixed_max = !mod.slopes && out <= 88.0;
+    p.bounded = out <= 88.0;
   }
   p.err = device_error_word();
   if (!p.err) return BPT_ECUDA;
@@ -621,11 +670,11 @@ int attention_mod_fwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   const double pairs = causal ? (double)D.s * (D.s + 1) / 2 : (double)D.s * D.s;
   ProfScope prof(PROF_ATTN_FWD, 4.0 * D.d * pairs * D.H * D.b, 0.0, st);
   switch (D.d) {
-    case 64: return cap ? launch_mod_fwd<64, true>(p, grid, st) : launch_mod_fwd<64, false>(p, grid, st);
-    case 80: return cap ? launch_mod_fwd<80, true>(p, grid, st) : launch_mod_fwd<80, false>(p, grid, st);
-    case 96: return cap ? launch_mod_fwd<96, true>(p, grid, st) : launch_mod_fwd<96, false>(p, grid, st);
-    case 112: return cap ? launch_mod_fwd<112, true>(p, grid, st) : launch_mod_fwd<112, false>(p, grid, st);
-    case 128: return cap ? launch_mod_fwd<128, true>(p, grid, st) : launch_mod_fwd<128, false>(p, grid, st);
+    case 64: return launch_for<64>(p, cap, grid, st);
+    case 80: return launch_for<80>(p, cap, grid, st);
+    case 96: return launch_for<96>(p, cap, grid, st);
+    case 112: return launch_for<112>(p, cap, grid, st);
+    case 128: return launch_for<128>(p, cap, grid, st);
     default: return BPT_EUNSUPPORTED;
   }
 }

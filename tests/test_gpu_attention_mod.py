@@ -158,6 +158,10 @@ CASES = [
     (3, 390, 2, 2, 64, "padded", 60.0, False),
     (1, 500, 2, 1, 112, "causal", 2.0, False),
     (2, 300, 2, 2, 128, "none", 0.0, False),
+    (1, 300, 4, 2, 64, "causal", 0.0, "mixed"),
+    (1, 300, 4, 2, 80, "docs_both", 0.0, "mixed"),
+    (1, 200, 4, 2, 128, "window", 30.0, "mixed"),
+    (1, 260, 4, 2, 96, "all", 100.0, "mixed"),
     # few key/value heads with many query heads: clusters share a key tile
     (1, 513, 8, 1, 64, "docs", 0.0, False),
     (1, 900, 8, 1, 128, "causal", 30.0, False),
@@ -172,6 +176,8 @@ def test_against_the_definition(case, flags):
     b, s, H, K, d, kind, cap, biased = case
     causal, begin, end = windows(kind, b, s, seed=s + d)
     slopes = [2.0 ** -(1 + 3 * n) for n in range(H)] if biased else None
+    if biased == "mixed":  # steep, gentle and negative ones
+        slopes = [(3.0, -0.02, 0.3, -2.0)[n % 4] for n in range(H)]
     cfg = LayerConfig(b=b, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64, causal=causal)
     mod = bpt.ScoreMod(as_int32(begin), as_int32(end), None if slopes is None else torch.tensor(slopes, device="cuda"), cap)
     qkv, dout = make(b, s, H, K, d, seed=s)
