@@ -158,7 +158,7 @@ struct ModDkdvCfg {
 // takes an equal part of its (query head, query tile) stream, leaves its dV and
 // dK as fp32 in its own shared memory, and sums a share of the rows of all of
 // them in rank order through distributed shared memory.
-template <int D, bool CAP>
+template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_constant__ ModBwdParams p) {
   using T = TileGeom<D>;
   using C = ModDkdvCfg<D>;
@@ -474,7 +474,6 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(kv_ready);
     }
     const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
-    const bool bias = p.slopes != nullptr;
     bool ok = true;
     for (int u = b; u < U; u += 2) {
       const int t = u >> 1;
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
           else if constexpr (CAP) return late[x / 2];
           else return 0ull;
         };
-        if (!bias) {
+        if constexpr (!BIAS) {
           probabilities<CAP, true>(p, sv, am, pe, pk, all, lse2, on);
         } else {
           const float slope2 = p.slopes[g * p.G + (t0 + t) / n_i] * 1.4426950408889634f;
@@ -686,7 +685,7 @@ struct ModDqCfg {
 // dS(u)), dP(u+2).  A row's window, LSE and D are scalars of its thread.
 // TMEM: S [0, 128), dP [128, 256) as two 64-column buffers each, dQ at 256,
 // Q at 256 + D, dO at 256 + 1.5 D.
-template <int D, bool CAP>
+template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_constant__ ModBwdParams p) {
   using T = TileGeom<D>;
   using C = ModDqCfg<D>;
@@ -901,8 +900,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
       if (lane == 0) mbar_arrive(qo_ready);
     }
     const int2 win = key_window(p.row_begin, p.row_end, p.causal, p.s, bi, qpos);
-    const bool bias = p.slopes != nullptr;
-    const float slope2 = bias ? p.slopes[n] * 1.4426950408889634f : 0.f;
+    const float slope2 = BIAS ? p.slopes[n] * 1.4426950408889634f : 0.f;
     // this row's -LSE*log2(e) and dO.O sum (finite filler past the sequence)
     const float nl = p.nl2[((long long)bi * p.H + n) * p.s_pad + qpos];
     const float dsum = p.dsum[((long long)bi * p.H + n) * p.s_pad + qpos];
@@ -926,7 +924,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
         const bool all = klo == 0 && khi == 64;
         auto on = [&](int x) { return x >= klo && x < khi; };
         const uint64_t nl2 = f2(nl, nl);
-        if (!bias) {
+        if constexpr (!BIAS) {
           auto add = [&](int) { return nl2; };
           probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
         } else {
@@ -1117,25 +1115,32 @@ int split_for(int items, int stream) {
   return s;
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool BIAS>
 int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
   constexpr int SMEM_KV = ModDkdvCfg<D>::SMEM, SMEM_Q = ModDqCfg<D>::SMEM;
   static_assert(SMEM_KV <= 232448 && SMEM_Q <= 232448, "tile sets exceed shared memory");
   static std::atomic<uint64_t> attr_kv{0}, attr_q{0};  // devices whose limit is set
-  if (smem_limit_once(reinterpret_cast<const void*>(attn_mod_dkdv_kernel<D, CAP>), SMEM_KV, &attr_kv) ||
-      smem_limit_once(reinterpret_cast<const void*>(attn_mod_dq_kernel<D, CAP>), SMEM_Q, &attr_q))
+  if (smem_limit_once(reinterpret_cast<const void*>(attn_mod_dkdv_kernel<D, CAP, BIAS>), SMEM_KV, &attr_kv) ||
+      smem_limit_once(reinterpret_cast<const void*>(attn_mod_dq_kernel<D, CAP, BIAS>), SMEM_Q, &attr_q))
     return BPT_ECUDA;
   {
     ProfScope prof(PROF_ATTN_BWD, 8.0 * D * pairs * p.H * b, 0.0, st);
     // CTAs per item: see split_for
     const int items = p.n_t * p.Hkv * b, split = split_for(items, p.G * p.n_t);
-    if (launch_dependent(attn_mod_dkdv_kernel<D, CAP>, items * split, split, dim3(352), SMEM_KV, st, p) != cudaSuccess)
+    if (launch_dependent(attn_mod_dkdv_kernel<D, CAP, BIAS>, items * split, split, dim3(352), SMEM_KV, st, p) != cudaSuccess)
       return BPT_ECUDA;
   }
   ProfScope prof(PROF_ATTN_BWD, 2.0 * D * pairs * p.H * b, 0.0, st);
-  return launch_dependent(attn_mod_dq_kernel<D, CAP>, p.n_t * p.H * b, 1, dim3(352), SMEM_Q, st, p) == cudaSuccess
+  return launch_dependent(attn_mod_dq_kernel<D, CAP, BIAS>, p.n_t * p.H * b, 1, dim3(352), SMEM_Q, st, p) == cudaSuccess
              ? BPT_OK
              : BPT_ECUDA;
+}
+
+template <int D>
+int launch_for(const ModBwdParams& p, bool cap, int b, double pairs, cudaStream_t st) {
+  if (p.slopes)
+    return cap ? launch_both<D, true, true>(p, b, pairs, st) : launch_both<D, false, true>(p, b, pairs, st);
+  return cap ? launch_both<D, true, false>(p, b, pairs, st) : launch_both<D, false, false>(p, b, pairs, st);
 }
 
 struct ModBwdWs {
@@ -1227,11 +1232,11 @@ int attention_mod_bwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   const double pairs = causal ? (double)D.s * (D.s + 1) / 2 : (double)D.s * D.s;
   const int b = (int)D.b;
   switch (D.d) {
-    case 64: return cap ? launch_both<64, true>(p, b, pairs, st) : launch_both<64, false>(p, b, pairs, st);
-    case 80: return cap ? launch_both<80, true>(p, b, pairs, st) : launch_both<80, false>(p, b, pairs, st);
-    case 96: return cap ? launch_both<96, true>(p, b, pairs, st) : launch_both<96, false>(p, b, pairs, st);
-    case 112: return cap ? launch_both<112, true>(p, b, pairs, st) : launch_both<112, false>(p, b, pairs, st);
-    case 128: return cap ? launch_both<128, true>(p, b, pairs, st) : launch_both<128, false>(p, b, pairs, st);
+    case 64: return launch_for<64>(p, cap, b, pairs, st);
+    case 80: return launch_for<80>(p, cap, b, pairs, st);
+    case 96: return launch_for<96>(p, cap, b, pairs, st);
+    case 112: return launch_for<112>(p, cap, b, pairs, st);
+    case 128: return launch_for<128>(p, cap, b, pairs, st);
     default: return BPT_EUNSUPPORTED;
   }
 }
