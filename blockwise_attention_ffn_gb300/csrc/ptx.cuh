@@ -124,6 +124,18 @@ __device__ __forceinline__ void bulk_load(void* sdst, const void* gsrc, uint32_t
                "l"(reinterpret_cast<uint64_t>(gsrc)), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+// 1-D bulk copy of `bytes` from this CTA's shared memory to global memory in
+// the thread's bulk group; alignment as for bulk_load.
+__device__ __forceinline__ void bulk_store(void* gdst, const void* ssrc, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
+                   reinterpret_cast<uint64_t>(gdst)),
+               "r"(smem_u32(ssrc)), "r"(bytes)
+               : "memory");
+}
+// all but the thread's newest bulk group have been read from shared memory
+__device__ __forceinline__ void bulk_wait_read1() {
+  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
 // Makes this thread's generic-proxy shared-memory writes visible to the async
 // proxy (tensor core and TMA reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {

@@ -140,22 +140,50 @@ def test_norm_rope_backward(case, in_place):
             assert torch.equal(a, v + v)
 
 
-def test_norm_rope_many_rows():
-    """More items than the grid takes in one round: against the call on the
-    halves, row by row (bitwise: a row's result does not depend on the rest)."""
-    b, s, H, K, d = 1, 40001, 4, 2, 80
-    cfg = cfg_of(b, s, H, K, d, rope_base=10000.0)
+@pytest.mark.parametrize("H,K,d", [(4, 2, 80), (2, 1, 64), (32, 8, 128), (6, 6, 112), (3, 1, 96), (40, 40, 128)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_norm_rope_many_rows(H, K, d, in_place):
+    """More rows than the SMs take at once, against calls on a few rows each
+    (bitwise: a row's result does not depend on the rest), with a norm and
+    without."""
+    s = 20011
+    cfg = cfg_of(1, s, H, K, d, rope_base=10000.0)
     g = torch.Generator(device="cuda").manual_seed(3)
     x = torch.randn(s, (H + 2 * K) * d, generator=g, device="cuda").to(torch.bfloat16)
-    w = [(1 + 0.1 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16) for _ in range(2)]
-    out = torch.empty_like(x)
-    bpt.bpt_qk_norm_rope_fwd(cfg, x, *w, None, out)
+    dy = torch.randn(s, (H + 2 * K) * d, generator=g, device="cuda").to(torch.bfloat16)
+    norm = [(1 + 0.1 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16) for _ in range(2)]
     pos = torch.arange(s, dtype=torch.int32, device="cuda")
-    for a, e in ((0, 17), (17, 20001), (20001, s)):
-        part = torch.empty_like(x[a:e])
-        bpt.bpt_qk_norm_rope_fwd(cfg.with_(s=e - a), x[a:e], *w, pos[a:e].clone(), part)
+    ws = bpt.alloc_bytes(bpt.bpt_qk_norm_rope_workspace_bytes(cfg))
+    rng = np.random.default_rng(5)
+    for w in (norm, [None, None]):
+        out, dx = (x.clone(), dy.clone()) if in_place else (torch.empty_like(x), torch.empty_like(x))
+        bpt.bpt_qk_norm_rope_fwd(cfg, out if in_place else x, *w, None, out)
+        dw = [torch.zeros(d, device="cuda") for _ in range(2)]
+        bpt.bpt_qk_norm_rope_bwd(cfg, x, *w, None, dx if in_place else dy, dx, *dw, ws)
         sync()
-        assert torch.equal(part, out[a:e])
+        for a in (0, s - 9, *rng.integers(9, s - 18, 6).tolist()):
+            e = a + 9
+            part, dpart = torch.empty_like(x[a:e]), torch.empty_like(x[a:e])
+            small = cfg.with_(s=e - a)
+            bpt.bpt_qk_norm_rope_fwd(small, x[a:e], *w, pos[a:e].clone(), part)
+            bpt.bpt_qk_norm_rope_bwd(small, x[a:e], *w, pos[a:e].clone(), dy[a:e], dpart,
+                                     *[torch.zeros(d, device="cuda") for _ in range(2)], ws)
+            sync()
+            assert torch.equal(part, out[a:e]) and torch.equal(dpart, dx[a:e])
+        if w[0] is None:
+            continue
+        # the weights' gradients of all rows against fp64
+        u = x.double().view(s, H + 2 * K, d)[:, :H + K]
+        n = u * torch.rsqrt(u.square().mean(-1, keepdim=True) + cfg.norm_eps)
+        a = pos.double()[:, None] * 10000.0 ** (-2 * torch.arange(d // 2, device="cuda").double() / d)
+        z = dy.double().view(s, H + 2 * K, d)[:, :H + K]
+        z = torch.complex(z[..., :d // 2].contiguous(), z[..., d // 2:].contiguous()) * torch.polar(torch.ones_like(a), -a)[:, None]
+        terms = torch.cat((z.real, z.imag), -1) * n
+        for got, part in zip(dw, (terms[:, :H], terms[:, H:])):
+            # chains of at most rows * heads / lanes additions per lane, under
+            # 2^10, and angles' 2^-20: both of the terms' sum of sizes
+            bound = (2.0 ** -24 * 2 ** 10 + 2.0 ** -20) * part.abs().sum((0, 1))
+            assert bool(((got.double() - part.sum((0, 1))).abs() <= bound).all())
 
 
 def test_norm_rope_refusals():
