@@ -44,11 +44,10 @@ int bpt_attention_mod_fwd(const bpt_config* cfg, const bpt_score_mod* mod, const
   int rc = check(cfg, mod, &D);
   if (rc) return rc;
   if (!qkv || !o || !aligned16(qkv) || !aligned16(o) || !aligned16(lse)) return BPT_EINVAL;
-  if (D.debug) {
-    const Span sp[] = {{qkv, D.rows * D.width * 2}, {o, D.rows * D.H * D.d * 2},
-                       {lse, lse ? D.b * D.H * D.s_pad * 4 : 0}};
-    if (debug_spans(sp, 3) || mod_spans(D, mod)) return BPT_EINVAL;
-  }
+  const Span sp[] = {{qkv, D.rows * D.width * 2}, {o, D.rows * D.H * D.d * 2},
+                     {lse, lse ? D.b * D.H * D.s_pad * 4 : 0}};
+  if (overlaps(sp[1], sp, 1) || (lse && overlaps(sp[2], sp, 2))) return BPT_EINVAL;
+  if (D.debug && (debug_spans(sp, 3) || mod_spans(D, mod))) return BPT_EINVAL;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if ((rc = attention_mod_fwd(D, cfg->causal, *mod, qkv, o, reinterpret_cast<float*>(lse), st))) return rc;
   return D.debug ? debug_finish(st) : BPT_OK;
@@ -69,12 +68,11 @@ int bpt_attention_mod_bwd(const bpt_config* cfg, const bpt_score_mod* mod, const
     return BPT_EINVAL;
   const size_t need = attention_mod_bwd_ws_bytes(D);
   if (ws_bytes < need) return BPT_ENOSPC;
-  if (D.debug) {
-    const int64_t packed = D.rows * D.width * 2, hd = D.rows * D.H * D.d * 2;
-    const Span sp[] = {{qkv, packed}, {o, hd}, {lse, D.b * D.H * D.s_pad * 4}, {dout, hd}, {dqkv, packed},
-                       {ws, (int64_t)need}};
-    if (debug_spans(sp, 6) || mod_spans(D, mod)) return BPT_EINVAL;
-  }
+  const int64_t packed = D.rows * D.width * 2, hd = D.rows * D.H * D.d * 2;
+  const Span sp[] = {{qkv, packed}, {o, hd}, {lse, D.b * D.H * D.s_pad * 4}, {dout, hd}, {dqkv, packed},
+                     {ws, (int64_t)need}};
+  if (overlaps(sp[4], sp, 4) || overlaps(sp[5], sp, 5)) return BPT_EINVAL;
+  if (D.debug && (debug_spans(sp, 6) || mod_spans(D, mod))) return BPT_EINVAL;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if ((rc = attention_mod_bwd(D, cfg->causal, *mod, qkv, o, reinterpret_cast<const float*>(lse), dout, dqkv, ws, st)))
     return rc;

@@ -118,6 +118,14 @@ __device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&
   }
 }
 
+// A masked dP may be infinite (a value that no window reaches is anything
+// finite, and its product with dO is not); 0 times it would be NaN.
+__device__ __forceinline__ void mask_gradient(uint32_t (&dr)[64], const float (&pe)[64]) {
+#pragma unroll
+  for (int k = 0; k < 64; ++k)
+    if (pe[k] == 0.f) dr[k] = 0u;
+}
+
 // ===========================================================================
 // dK / dV
 // ===========================================================================
@@ -506,15 +514,15 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
       // ---- phase 1: P^T = exp2 of the modified scores - LSE log2(e)
       const bool all = cut.x <= j * 128 && cut.y >= j * 128 + 128;
       const int2* win = rec->row + 64 * b;
+      auto on = [&](int x) {
+        const int2 w = win[x];
+        return (unsigned)(kvp - w.x) < (unsigned)w.y;
+      };
       float pe[64];
       uint32_t pk[32];
       {
         uint32_t sv[64];
         const float am = load_scores<true>(tSb + lane_off, sv);
-        auto on = [&](int x) {
-          const int2 w = win[x];
-          return (unsigned)(kvp - w.x) < (unsigned)w.y;
-        };
         auto lse2 = [&](int x) -> uint64_t {
           if constexpr (EARLY) return nl2[x / 2];
           else if constexpr (CAP) return late[x / 2];
@@ -554,6 +562,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
       tmem_ld32_nw(tdPb + lane_off, dr);
       tmem_ld32_nw(tdPb + lane_off + 32, dr + 32);
       tmem_wait_ld(dr);
+      if (!all) mask_gradient(dr, pe);
       uint32_t o[32];
 #pragma unroll
       for (int k = 0; k < 64; k += 2) {
@@ -918,11 +927,11 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_free[b]);
+      const bool all = klo == 0 && khi == 64;
+      auto on = [&](int x) { return x >= klo && x < khi; };
       float pe[64];
       {
         uint32_t pk[32];
-        const bool all = klo == 0 && khi == 64;
-        auto on = [&](int x) { return x >= klo && x < khi; };
         const uint64_t nl2 = f2(nl, nl);
         if constexpr (!BIAS) {
           auto add = [&](int) { return nl2; };
@@ -950,6 +959,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
       tmem_ld32_nw(tdPb + lane_off, dr);
       tmem_ld32_nw(tdPb + lane_off + 32, dr + 32);
       tmem_wait_ld(dr);
+      if (!all) mask_gradient(dr, pe);
       uint32_t o[32];
       const uint64_t ds2 = f2(dsum, dsum);
 #pragma unroll

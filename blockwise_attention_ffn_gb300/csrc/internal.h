@@ -39,6 +39,15 @@ struct Span {
   int64_t bytes;
 };
 int debug_spans(const Span* sp, int n);
+// true if the output span shares bytes with one of the n others
+inline bool overlaps(const Span& out, const Span* others, int n) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(out.p), hi = lo + (uintptr_t)out.bytes;
+  for (int i = 0; i < n; ++i) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(others[i].p), e = a + (uintptr_t)others[i].bytes;
+    if (others[i].p && a < hi && lo < e) return true;
+  }
+  return false;
+}
 int debug_finish(cudaStream_t st);
 
 // A config's shape for the calls on the packed Q/K/V buffer alone, checked

@@ -73,6 +73,14 @@ class LibOps:
         from . import bpt_layer_bwd
         bpt_layer_bwd(cfg, W, x, saved, dy, dx, grads, ws, self.stream)
 
+    def clip(self, grads, max_norm, like):
+        import torch
+        from . import alloc_bytes, bpt_clip_grads, bpt_clip_workspace_bytes
+        norm = torch.empty(1, dtype=torch.float32, device=like.device)
+        ws = alloc_bytes(bpt_clip_workspace_bytes(), device=like.device)
+        bpt_clip_grads([g for d in grads for g in d.values() if g is not None], max_norm, norm, ws, stream=self.stream)
+        return norm
+
 
 @dataclass
 class StackState:
@@ -108,9 +116,12 @@ def stack_fwd(cfg, weights: list, x, k: int, ws=None, ops=None):
     return h, st
 
 
-def stack_bwd(cfg, weights: list, state: StackState, dy, ws=None, ops=None, grads=None):
+def stack_bwd(cfg, weights: list, state: StackState, dy, ws=None, ops=None, grads=None, max_norm=None):
     """Gradients of the stack given dy.  Returns (dx, grads) with one
-    gradient dict per layer (fp32, overwritten, or those passed in)."""
+    gradient dict per layer (fp32, overwritten, or those passed in).  With
+    max_norm the weight gradients of all layers are then clipped in place by
+    their global norm (bpt_clip_grads; inf: not clipped), and the norm, one
+    fp32 element on the device, is returned too: (dx, grads, norm)."""
     L = len(weights)
     if L != state.n_layers:
         raise ValueError("weights do not match the forward pass")
@@ -136,4 +147,6 @@ def stack_bwd(cfg, weights: list, state: StackState, dy, ws=None, ops=None, grad
             g = dx
         del seg_in
         del state.ckpt[s0]
-    return g, grads
+    if max_norm is None:
+        return g, grads
+    return g, grads, ops.clip(grads, max_norm, dy)

@@ -332,12 +332,14 @@ int bpt_attention_bwd_noalloc(const bpt_config* cfg, const void* qkv, const void
  * lse [b, H, s_pad] is an fp32-accurate sum (0 in the rows past s); the
  * backward takes it back with o.  Biases far beyond the scores' size cost the
  * rebuilt probabilities what lse's fp32 cannot hold (2^-24 of its size); the
- * windows above keep near keys in view, where lse is small.  A key's K and V
- * must be finite if any row of its 128-key tile's queries is computed, as in
- * bpt_attention_fwd: a masked pair adds 0 * V.
+ * windows above keep near keys in view, where lse is small.  Rows that no
+ * window reaches may hold any finite values: they leave no trace.  An infinity
+ * or a NaN in V does (0 * inf) wherever its 128-key tile is loaded, as in
+ * bpt_attention_fwd.
  * dqkv as for bpt_attention_bwd, whose notes on the order of sums and on
  * BPT_FLAG_DETERMINISTIC hold here too; b*H*s_pad above 2^31 - 1 returns
- * BPT_EUNSUPPORTED from both calls.  dqkv must not overlap qkv or dout.
+ * BPT_EUNSUPPORTED from both calls.  Outputs and ws that share bytes with an
+ * input or one another are refused (BPT_EINVAL).
  * ws: bpt_attention_mod_bwd_workspace_bytes(cfg), one per call in flight. */
 typedef struct {
   const int32_t *row_begin, *row_end;

@@ -186,3 +186,178 @@ def test_against_the_definition(case, flags):
     if flags:
         again = run(cfg, mod, qkv, dout, flags)
         assert all(torch.equal(a, c) for a, c in zip(got, again))
+
+
+def docs_mod(s, n, b=1):
+    i = torch.arange(s, dtype=torch.int32, device="cuda")
+    return bpt.ScoreMod(row_begin=(i // n * n).int().repeat(b), softcap=30.0)
+
+
+def test_equals_the_plain_attention_without_modifiers():
+    """No modifier: the plain calls' definition; O and the gradients agree to
+    their own roundings (each side within them), the log-sum-exp to the plain
+    one's bf16 row sums."""
+    b, s, H, K, d = 2, 333, 4, 2, 128
+    cfg = LayerConfig(b=b, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64)
+    qkv, dout = make(b, s, H, K, d, seed=1)
+    o, lse, dqkv = run(cfg, bpt.ScoreMod(), qkv, dout)
+    o2, lse2, dqkv2 = torch.empty_like(o), torch.empty_like(lse), torch.empty_like(dqkv)
+    bpt.bpt_attention_fwd(cfg, qkv.cuda(), o2, lse2)
+    ws = bpt.alloc_bytes(bpt.bpt_attention_bwd_workspace_bytes(cfg))
+    bpt.bpt_attention_bwd(cfg, qkv.cuda(), o2, lse2, dout.cuda(), dqkv2, ws)
+    torch.cuda.synchronize()
+    assert float((lse - lse2)[:, :, :s].abs().max()) <= 2.0 ** -8 * 1.02
+    for a, c in ((o, o2), (dqkv, dqkv2)):
+        assert float((a.float() - c.float()).norm() / c.float().norm()) < 5e-3
+
+
+def test_masked_rows_leave_no_trace():
+    """Whatever (finite) lies in rows that no window reaches changes nothing:
+    the largest bf16 values in the padding of each sequence."""
+    b, s, H, K, d = 3, 300, 4, 2, 64
+    cfg = LayerConfig(b=b, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64, causal=0)
+    n = [300, 131, 0]
+    end = as_int32([n[i] if q < n[i] else 0 for i in range(b) for q in range(s)])
+    qkv, dout = make(b, s, H, K, d, seed=2)
+    slopes = torch.tensor([0.5, 0.1, 0.01, 0.0], device="cuda")
+    for mod in (bpt.ScoreMod(None, end), bpt.ScoreMod(None, end, slopes, 20.0), bpt.ScoreMod(None, end, None, 100.0)):
+        clean = [t.clone() for t in run(cfg, mod, qkv, dout, bpt.BPT_FLAG_DETERMINISTIC)]
+        dirty, ddirty = qkv.clone().view(b, s, -1), dout.clone().view(b, s, -1)
+        for i in range(b):
+            dirty[i, n[i]:] = 3.3e38
+            dirty[i, n[i]:, ::2] = -3.3e38
+            ddirty[i, n[i]:] = 3.3e38
+        got = run(cfg, mod, dirty.view(b * s, -1), ddirty.view(b * s, -1), bpt.BPT_FLAG_DETERMINISTIC)
+        for a, c in zip(got, clean):
+            fin = c.isfinite()
+            assert torch.equal(fin, a.isfinite())
+            if mod.softcap == 0.0:
+                assert torch.equal(a, c)
+            else:
+                # a tile's scores, masked ones too, choose the form of tanh its
+                # warp takes: within 1e-6 of each other, so a rounding to bf16
+                # may fall to the other side, one step of 2^-7
+                a, c = a[fin].double(), c[fin].double()
+                assert float((a - c).norm()) <= 2.0 ** -7 * float(c.norm())
+        o, lse, dqkv = (t.view(b, s, -1) if t.dim() == 2 else t for t in got)
+        for i in range(b):
+            assert not o[i, n[i]:].any() and not dqkv[i, n[i]:].any()
+            assert bool((lse[i, :, n[i]:s] == -math.inf).all()) and not lse[i, :, s:].any()
+
+
+def test_streams_and_graphs():
+    """Two calls at once on two streams with workspaces of their own, and a
+    captured forward and backward replayed on new inputs, give bitwise what
+    the calls give alone (fixed-order mode)."""
+    s, H, K, d = 700, 8, 2, 128
+    cfg = LayerConfig(b=1, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64, flags=bpt.BPT_FLAG_DETERMINISTIC)
+    mod = docs_mod(s, 150)
+    ins = [make(1, s, H, K, d, seed=10 + i) for i in range(3)]
+    want = [[t.clone() for t in run(cfg, mod, *x, flags=cfg.flags)] for x in ins]
+
+    def buffers(x, do):
+        return dict(x=x.cuda(), do=do.cuda(), o=torch.empty(s, H * d, dtype=torch.bfloat16, device="cuda"),
+                    lse=torch.empty(1, H, bpt.s_pad(cfg), device="cuda"), dx=torch.empty(s, (H + 2 * K) * d, dtype=torch.bfloat16, device="cuda"),
+                    ws=bpt.alloc_bytes(bpt.bpt_attention_mod_bwd_workspace_bytes(cfg)))
+
+    def call(z, stream=None):
+        bpt.bpt_attention_mod_fwd(cfg, mod, z["x"], z["o"], z["lse"], stream)
+        bpt.bpt_attention_mod_bwd(cfg, mod, z["x"], z["o"], z["lse"], z["do"], z["dx"], z["ws"], stream)
+
+    zs = [buffers(*x) for x in ins]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for z, st in zip(zs, streams):
+            call(z, st)
+    torch.cuda.synchronize()
+    for z, w in zip(zs[:2], want):
+        assert torch.equal(z["o"], w[0]) and torch.equal(z["lse"], w[1]) and torch.equal(z["dx"], w[2])
+    graph = torch.cuda.CUDAGraph()
+    z = zs[2]
+    with torch.cuda.graph(graph):
+        call(z)
+    for x, w in zip(ins, want):
+        z["x"].copy_(x[0])
+        z["do"].copy_(x[1])
+        z["o"].zero_(), z["dx"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z["o"], w[0]) and torch.equal(z["lse"], w[1]) and torch.equal(z["dx"], w[2])
+    assert bpt.bpt_last_device_error() == (bpt.BPT_OK, 0)
+
+
+def test_far_offsets():
+    """A packed buffer of more than 2^31 elements: documents at its end equal
+    the same documents alone, within both sides' roundings (their tiles differ)."""
+    b, s, H, K, d, n = 3, 131072, 32, 8, 128, 128
+    cfg = LayerConfig(b=b, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64, flags=bpt.BPT_FLAG_DETERMINISTIC)
+    mod = docs_mod(s, n, b)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    qkv = torch.randn(b * s, (H + 2 * K) * d, generator=g, device="cuda", dtype=torch.bfloat16)
+    dout = torch.randn(b * s, H * d, generator=g, device="cuda", dtype=torch.bfloat16)
+    assert qkv.numel() > 2 ** 31
+    o, dqkv = torch.empty_like(dout), torch.empty_like(qkv)
+    lse = torch.empty(b, H, s, device="cuda")
+    ws = bpt.alloc_bytes(bpt.bpt_attention_mod_bwd_workspace_bytes(cfg))
+    bpt.bpt_attention_mod_fwd(cfg, mod, qkv, o, lse)
+    bpt.bpt_attention_mod_bwd(cfg, mod, qkv, o, lse, dout, dqkv, ws)
+    torch.cuda.synchronize()
+    assert bpt.bpt_last_device_error() == (bpt.BPT_OK, 0)
+    # documents of one tile: the call on four of them alone runs the same tiles
+    small = cfg.with_(b=1, s=4 * n)
+    for at in (0, s - 4 * n, 2 * s - 4 * n, 3 * s - 4 * n):
+        e = at + 4 * n
+        so, sx = torch.empty(4 * n, H * d, dtype=torch.bfloat16, device="cuda"), torch.empty_like(qkv[at:e])
+        sl = torch.empty(1, H, 4 * n, device="cuda")
+        sws = bpt.alloc_bytes(bpt.bpt_attention_mod_bwd_workspace_bytes(small))
+        part = bpt.ScoreMod(row_begin=(torch.arange(4 * n, device="cuda") // n * n).int(), softcap=30.0)
+        bpt.bpt_attention_mod_fwd(small, part, qkv[at:e], so, sl)
+        bpt.bpt_attention_mod_bwd(small, part, qkv[at:e], so, sl, dout[at:e].contiguous(), sx, sws)
+        torch.cuda.synchronize()
+        assert torch.equal(so, o[at:e]) and torch.equal(sl[0], lse[at // s, :, at % s:at % s + 4 * n])
+        assert float((sx.float() - dqkv[at:e].float()).norm() / sx.float().norm()) < 1e-3
+
+
+def test_lse_is_optional_and_debug_checks():
+    s, H, K, d = 200, 2, 2, 80
+    cfg = LayerConfig(b=1, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64)
+    qkv, dout = make(1, s, H, K, d, seed=5)
+    mod = docs_mod(s, 60)
+    want = run(cfg, mod, qkv, dout, bpt.BPT_FLAG_DETERMINISTIC)
+    o = torch.empty_like(want[0])
+    bpt.bpt_attention_mod_fwd(cfg, mod, qkv.cuda(), o, None)
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0])
+    got = run(cfg, mod, qkv, dout, bpt.BPT_FLAG_DETERMINISTIC | bpt.BPT_FLAG_DEBUG_CHECKS)
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+
+
+def test_refusals():
+    s, H, K, d = 200, 2, 2, 64
+    cfg = LayerConfig(b=1, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64)
+    qkv, dout = (t.cuda() for t in make(1, s, H, K, d, seed=6))
+    o, lse = torch.empty_like(dout), torch.empty(1, H, 256, device="cuda")
+    dx, ws = torch.empty_like(qkv), bpt.alloc_bytes(bpt.bpt_attention_mod_bwd_workspace_bytes(cfg))
+    plain = bpt.ScoreMod()
+    lo = torch.zeros(s, dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: bpt.bpt_attention_mod_fwd(cfg, bpt.ScoreMod(lo[:-1]), qkv, o, lse),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, bpt.ScoreMod(lo.long()), qkv, o, lse),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, bpt.ScoreMod(None, lo.cpu()), qkv, o, lse),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, bpt.ScoreMod(None, None, torch.zeros(1, device="cuda")), qkv, o, lse),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, bpt.ScoreMod(softcap=-3.0), qkv, o, lse),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, plain, qkv[:, ::2], o, lse),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, plain, qkv.half(), o, lse),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, plain, qkv, o[:-1], lse),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, plain, qkv, o, lse[:, :, :s].contiguous()),
+        lambda: bpt.bpt_attention_mod_fwd(cfg, plain, qkv, qkv.view(-1)[:o.numel()].view_as(o), lse),
+        lambda: bpt.bpt_attention_mod_bwd(cfg, plain, qkv, o, lse, dout, qkv, ws),
+        lambda: bpt.bpt_attention_mod_bwd(cfg, plain, qkv, o, None, dout, dx, ws),
+        lambda: bpt.bpt_attention_mod_bwd(cfg, plain, qkv, o, lse, dout, dx, ws[:1024]),
+    ]
+    for call in bad:
+        with pytest.raises(bpt.BptError):
+            call()
+    torch.cuda.synchronize()
+    assert bpt.bpt_last_device_error() == (bpt.BPT_OK, 0)

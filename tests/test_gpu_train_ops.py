@@ -345,6 +345,57 @@ def test_clip_is_repeatable_and_captures():
     assert {float(norm)} == norms and all(torch.equal(a, b) for a, b in zip(outs, want))
 
 
+def test_clip_far_offsets():
+    """A gradient of more than 2^31 elements: its squares and its last element."""
+    n = 2 ** 31 + 12345
+    t = torch.full((n,), 2.0 ** -10, dtype=torch.bfloat16, device="cuda")
+    t[-1] = 64.0
+    norm = clip_call([t], 1.0)
+    want = math.sqrt((n - 1) * 2.0 ** -20 + 64.0 ** 2)
+    assert abs(norm - want) <= 2.0 ** -20 * want
+    for i, v in ((0, 2.0 ** -10), (n // 2, 2.0 ** -10), (n - 2, 2.0 ** -10), (n - 1, 64.0)):
+        assert abs(float(t[i]) - v / want) <= 2.0 ** -8 * v / want + 2.0 ** -18 * v
+
+
+def test_norm_rope_streams_and_graphs():
+    """Two calls at once on two streams, and captured calls replayed on other
+    inputs, both forms (few rows and many)."""
+    H, K, d = 8, 4, 64
+    for s in (50, 12000):
+        cfg = cfg_of(1, s, H, K, d, rope_base=10000.0)
+        g = torch.Generator(device="cuda").manual_seed(s)
+        mk = lambda: torch.randn(s, (H + 2 * K) * d, generator=g, device="cuda").bfloat16()  # noqa: E731
+        w = torch.ones(d, device="cuda", dtype=torch.bfloat16)
+        zs = [dict(x=mk(), dy=mk(), out=mk(), dx=mk(), a=torch.zeros(d, device="cuda"), c=torch.zeros(d, device="cuda"),
+                   ws=bpt.alloc_bytes(bpt.bpt_qk_norm_rope_workspace_bytes(cfg))) for _ in range(3)]
+
+        def call(z, stream=None):
+            bpt.bpt_qk_norm_rope_fwd(cfg, z["x"], w, w, None, z["out"], stream)
+            bpt.bpt_qk_norm_rope_bwd(cfg, z["x"], w, w, None, z["dy"], z["dx"], z["a"], z["c"], z["ws"], stream)
+
+        want = []
+        for z in zs:
+            call(z)
+            sync()
+            want.append({k: v.clone() for k, v in z.items() if k != "ws"})
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        for _ in range(20):
+            for z, st in zip(zs, streams):
+                call(z, st)
+        sync()
+        for z, v in zip(zs, want):
+            assert all(torch.equal(z[k], v[k]) for k in v)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(zs[2])
+        for v in want:
+            zs[2]["x"].copy_(v["x"])
+            zs[2]["dy"].copy_(v["dy"])
+            graph.replay()
+            sync()
+            assert all(torch.equal(zs[2][k], v[k]) for k in v)
+
+
 def test_clip_refusals():
     a = torch.ones(64, device="cuda")
     norm = torch.full((1,), 7.0, device="cuda")
