@@ -108,6 +108,81 @@ __device__ __forceinline__ Item item_of(const ItemOrder& o, int block) {
   return Item{rem / heads, g * o.group + head / o.per_head, head % o.per_head};
 }
 
+// One work item as the scheduling warp of a persistent CTA publishes it; n < 0:
+// no more.
+struct WorkItem {
+  int n, bi, q0, j0, nkv;  // query head, sequence, first row, first key tile, key tiles
+};
+constexpr int WORK_BYTES = 2 * 16 + 2 * 32;  // two answers, two items
+struct WorkQueue {
+  uint8_t* mem;          // WORK_BYTES, 16-byte aligned
+  uint64_t* full;        // [2], count 1
+  uint64_t* empty;       // [2], one arrival per reading warp
+  uint64_t* answered;    // count 1
+  __device__ __forceinline__ volatile WorkItem* item(int it) const {
+    return reinterpret_cast<volatile WorkItem*>(mem + 32 + 32 * (it & 1));
+  }
+};
+// The scheduling warp: publishes describe(block) for this CTA's block and then
+// for the blocks it takes over, the next one asked for when every warp has
+// begun the current one and the loading warp is through with it: a CTA that
+// took an item earlier would hold it back from the others.  Returns whether `last` was among them.
+template <class Describe>
+__device__ __forceinline__ bool publish_items(const WorkQueue& q, int block, int last, volatile int* abort_flag,
+                                              unsigned int* err, Describe describe) {
+  const int lane = lane_id();
+  bool asked = false, took_last = false;
+  int it = 0;
+  while (true) {
+    if (block < 0) {
+      if (lane == 0) {
+        q.item(it)->n = -1;
+        mbar_arrive(&q.full[it & 1]);
+      }
+      break;
+    }
+    took_last |= block == last;
+    const WorkItem w = describe(block);
+    if (lane == 0) {
+      volatile WorkItem* to = q.item(it);
+      to->n = w.n;
+      to->bi = w.bi;
+      to->q0 = w.q0;
+      to->j0 = w.j0;
+      to->nkv = w.nkv;
+      mbar_arrive(&q.full[it & 1]);
+    }
+    if (!bounded_wait_w(&q.empty[it & 1], (it >> 1) & 1, abort_flag, 252, err)) break;
+    uint8_t* answer = q.mem + 16 * (it & 1);
+    if (lane == 0) request_block(answer, q.answered);
+    asked = true;
+    if (!bounded_wait_w(q.answered, it & 1, abort_flag, 257, err)) break;
+    asked = false;
+    block = answered_block(answer);
+    fence_proxy_async_smem();
+    __syncwarp();
+    ++it;
+  }
+  // a request in flight lands before the shared memory goes
+  if (asked) drain_wait(q.answered, it & 1);
+  return took_last;
+}
+__device__ __forceinline__ void release_item(const WorkQueue& q, int it) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(&q.empty[it & 1]);
+}
+// A reading warp's copy of item it; false after a timeout.  The loading warp
+// (keep) releases it itself.
+template <bool keep = false>
+__device__ __forceinline__ bool next_item(const WorkQueue& q, int it, WorkItem* w, volatile int* abort_flag,
+                                          unsigned int* err) {
+  if (!bounded_wait_w(&q.full[it & 1], (it >> 1) & 1, abort_flag, 250, err)) return false;
+  volatile WorkItem* from = q.item(it);
+  *w = WorkItem{from->n, from->bi, from->q0, from->j0, from->nkv};
+  if (!keep) release_item(q, it);
+  return true;
+}
+
 // tanh(y) = 1 - 2 / (1 + e^(2y)): absolute error about 2^-23, saturating
 // exactly; y2 = 2 log2(e) y
 __device__ __forceinline__ float tanh_any(float y2) {

@@ -315,11 +315,11 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
         if constexpr (CAP) bulk_load(sQ + C::NL2, p.nl2 + row, 512, &qdo_full[st]);
         issued = t + 1;
       }
-      if (*abort_flag) {
-        drain_wait(kv_full, 0);
-        for (int t = (issued > QS ? issued - QS : 0); t < issued; ++t)
-          drain_wait(&qdo_full[t % QS], (t / QS) & 1);
-      }
+      // every copy lands before the shared memory goes, also when a wait
+      // elsewhere in the block gives up later
+      drain_wait(kv_full, 0);
+      for (int t = (issued > QS ? issued - QS : 0); t < issued; ++t)
+        drain_wait(&qdo_full[t % QS], (t / QS) & 1);
     }
   } else if (warp == 1 || warp == 10) {
     // the whole warp runs the issue loop, one elected lane issues.  One
@@ -676,87 +676,90 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
 // ===========================================================================
 // dQ
 // ===========================================================================
-// Shared memory of the dQ kernel: the K/V ring.
+// Shared memory of the dQ kernel: dQ on its way out, a ring of tiles (Q, dO,
+// K_0, V_0, K_1, ... of one item after the other), barriers.
 template <int D>
 struct ModDqCfg {
   using T = TileGeom<D>;
-  static constexpr int KVS_FIT = (232448 - 1280) / (2 * T::TILE);
-  static constexpr int KVS = KVS_FIT > 5 ? 5 : KVS_FIT;
-  static constexpr int SMEM = KVS * 2 * T::TILE + 1024 + 256;
+  static constexpr int CTL = 640;
+  static constexpr int FIT = (232448 - T::TILE - CTL) / T::TILE;
+  static constexpr int NT = FIT > 10 ? 10 : FIT;
+  static constexpr int SMEM = (1 + NT) * T::TILE + CTL;
 };
 
-// One CTA per 128-row query tile of one head, over the key tiles that some row
-// of it sees, in 64-key sub-tiles: sub-tile u is the half u % 2 of tile u / 2.
-// Q and dO sit in TMEM as the A operands of S = Q K^T and dP = dO V^T; dS goes
-// over the first 32 columns of its dP buffer as the A operand of dQ += dS K.
-// Compute warps 2..5 take the even sub-tiles, 6..9 the odd ones, with issuing
-// warps 1 and 10: S(u), dP(u), S(u+2) (once S(u) is read), dQ(u) (after
-// dS(u)), dP(u+2).  A row's window, LSE and D are scalars of its thread.
+// One work item per 128-row query tile of one head, over the key tiles that
+// some row of it sees, in 64-key sub-tiles: sub-tile u is the half u % 2 of
+// tile u / 2.  Q and dO sit in TMEM as the A operands of S = Q K^T and dP = dO
+// V^T; dS goes over the first 32 columns of its dP buffer as the A operand of
+// dQ += dS K.  Compute warps 2..5 take the even sub-tiles, 6..9 the odd ones,
+// with issuing warps 1 and 10: S(u), dP(u), S(u+2) (once S(u) is read), dQ(u)
+// (after dS(u)), dP(u+2).  A row's window, LSE and D are scalars of its thread.
+// Persistent like the forward: warp 11 takes the items, warp 0 loads the next
+// one's Q and dO and its first keys during the current one.  (A CTA of its own
+// per item spent 11,000 cycles outside its loop, of 25,000 with documents of
+// 1500: start and TMEM 3,300, the first loads 2,500, the stores 900, the next
+// CTA's launch 1,400.)
 // TMEM: S [0, 128), dP [128, 256) as two 64-column buffers each, dQ at 256,
 // Q at 256 + D, dO at 256 + 1.5 D.
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_constant__ ModBwdParams p) {
+__global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_constant__ ModBwdParams p) {
   using T = TileGeom<D>;
   using C = ModDqCfg<D>;
-  constexpr int KVS = C::KVS;
+  constexpr int NT = C::NT;
+  static_assert(NT >= 6, "Q, dO, K and V of two tiles");
   static_assert(256 + 2 * D <= 512, "TMEM columns");
+  static_assert((2 * NT + 17) * 8 + WORK_BYTES + 8 <= C::CTL, "control block");
   constexpr uint32_t ID_S = idesc_bf16(128, 64, false, false);
   constexpr uint32_t ID_DQ = idesc_bf16(128, D, false, true);
   constexpr uint32_t COL_DQ = 256, COL_Q = 256 + D, COL_DO = 256 + D + D / 2;
 
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sKV = smem;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + KVS * 2 * T::TILE);
-  uint64_t* qo_ready = bars;           // Q, dO in TMEM and dQ zeroed (8 compute warps)
-  uint64_t* kv_full = bars + 1;        // [KVS]
-  uint64_t* kv_empty = kv_full + KVS;  // [KVS], both issuers
-  uint64_t* s_full = kv_empty + KVS;   // [2] S(u) in buffer u % 2
-  uint64_t* s_free = s_full + 2;       // [2] S(u) read (4 warps of the group)
-  uint64_t* dp_full = s_free + 2;      // [2]
-  uint64_t* ds_full = dp_full + 2;     // [2] dS(u) written (4 warps)
-  uint64_t* all_done = ds_full + 2;    // both issuers' last products done
-  uint64_t* drain = all_done + 1;      // [2], one per issuer
-  uint64_t* qo_full = drain + 2;       // Q, dO landed in the last stage
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(qo_full + 1);
+  // the tiles' swizzle needs 1024-byte alignment, which the declaration gives
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sOut = smem;                 // dQ
+  uint8_t* sRing = smem + T::TILE;
+  uint8_t* control = sRing + NT * T::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(control + WORK_BYTES);
+  // (read by 8 compute warps, 2 issuers, the loads)
+  const WorkQueue queue{control, bars, bars + 2, bars + 4};
+  uint64_t* qo_ready = bars + 5;   // Q, dO copied to TMEM, dQ zeroed (8 compute warps)
+  uint64_t* s_full = bars + 6;     // [2] S(u) in buffer u % 2
+  uint64_t* s_free = bars + 8;     // [2] S(u) read (4 warps of the group)
+  uint64_t* dp_full = bars + 10;   // [2]
+  uint64_t* ds_full = bars + 12;   // [2] dS(u) written (4 warps)
+  uint64_t* all_done = bars + 14;  // both issuers' last products of an item done
+  uint64_t* drain = bars + 15;     // [2], one per issuer
+  uint64_t* t_full = bars + 17;    // [NT]
+  uint64_t* t_empty = t_full + NT; // [NT], once per issuer (both sub-tiles' products of a K or V tile)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(t_empty + NT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = warp_id();
   const int lane = lane_id();
-  // the last (with a causal mask heaviest) query tiles first; the query heads
-  // of one key/value head are adjacent
-  const Item item = item_of(p.order_q, blockIdx.x);
-  const int n_qt = p.n_t;
-  const int i = n_qt - 1 - item.tile;
-  const int bi = item.kv / p.Hkv;
-  const int g = item.kv % p.Hkv;
-  const int n = g * p.G + item.sub;
-  const int q0 = i * 128;
-  // key tiles [j0, j0 + nkv) hold every key that some row sees
-  const int2 span = p.span[(long long)bi * n_qt + i];
-  const int j0 = span.x < span.y ? span.x / 128 : 0;
-  const int nkv = span.x < span.y ? (span.y + 127) / 128 - j0 : 0;
-  const int U = 2 * nkv;
-
   if (threadIdx.x == 0) {
-    mbar_init(qo_ready, 8);
-    mbar_init(qo_full, 1);
-    for (int k = 0; k < KVS; ++k) {
-      mbar_init(&kv_full[k], 1);
-      mbar_init(&kv_empty[k], 2);
-    }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&queue.full[b], 1);
+      mbar_init(&queue.empty[b], 11);
       mbar_init(&s_full[b], 1);
       mbar_init(&s_free[b], 4);
       mbar_init(&dp_full[b], 1);
       mbar_init(&ds_full[b], 4);
       mbar_init(&drain[b], 1);
     }
+    mbar_init(queue.answered, 1);
+    mbar_init(qo_ready, 8);
     mbar_init(all_done, 2);
+    for (int k = 0; k < NT; ++k) {
+      mbar_init(&t_full[k], 1);
+      mbar_init(&t_empty[k], 2);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0 && lane == 0) tma_prefetch(&p.map_qkv);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch(&p.map_qkv);
+    tma_prefetch(&p.map_do);
+    tma_prefetch(&p.map_out);
+  }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
@@ -770,244 +773,286 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
   const uint32_t tdQ = tmem + COL_DQ;
   const uint32_t tQA = tmem + COL_Q;
   const uint32_t tOA = tmem + COL_DO;
+  bool took_last = false;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------ TMA producer
-      // Q and dO, in the last stage until the compute warps have copied them
-      if (nkv > 0) {
-        uint8_t* q = sKV + (KVS - 1) * 2 * T::TILE;
-        mbar_expect_tx(qo_full, 2 * T::TILE);
+  if (warp == 11) {
+    // ------------------------------------------------ items (the whole warp)
+    took_last = publish_items(queue, blockIdx.x, gridDim.x - 1, abort_flag, p.err, [&](int block) {
+      // the last (with a causal mask heaviest) query tiles first; the query
+      // heads of one key/value head are adjacent
+      const Item w = item_of(p.order_q, block);
+      const int i = p.n_t - 1 - w.tile, bi = w.kv / p.Hkv;
+      // key tiles [j0, j0 + nkv) hold every key that some row sees
+      const int2 span = p.span[(long long)bi * p.n_t + i];
+      const int j0 = span.x < span.y ? span.x / 128 : 0;
+      return WorkItem{w.kv % p.Hkv * p.G + w.sub, bi, i * 128, j0, span.x < span.y ? (span.y + 127) / 128 - j0 : 0};
+    });
+  } else if (warp == 0) {
+    // ------------------------------------------------ loads (the whole warp
+    // runs the loop, one lane issues)
+    int c = 0;  // tiles loaded
+    auto load_tile = [&](const CUtensorMap* map, int col, int row, int bi) -> bool {
+      const int st = c % NT;
+      if (c >= NT && !bounded_wait_w(&t_empty[st], ((c / NT) & 1) ^ 1, abort_flag, 731, p.err)) return false;
+      if (lane == 0) {
+        mbar_expect_tx(&t_full[st], T::TILE);
 #pragma unroll
-        for (int c = 0; c < T::NCH; ++c) {
-          tma_load_3d(q + c * T::CHUNK, &p.map_qkv, qo_full, n * D + c * T::CW, q0, bi);
-          tma_load_3d(q + T::TILE + c * T::CHUNK, &p.map_do, qo_full, n * D + c * T::CW, q0, bi);
-        }
+        for (int k = 0; k < T::NCH; ++k)
+          tma_load_3d(sRing + st * T::TILE + k * T::CHUNK, map, &t_full[st], col + k * T::CW, row, bi);
       }
-      int issued = 0;
-      for (int jt = 0; jt < nkv; ++jt) {
-        const int st = jt % KVS;
-        if (jt >= KVS && !bounded_wait(&kv_empty[st], ((jt / KVS) & 1) ^ 1, abort_flag, 731, p.err)) break;
-        if (jt == KVS - 1 && !bounded_wait(qo_ready, 0, abort_flag, 732, p.err)) break;
-        uint8_t* sK = sKV + st * 2 * T::TILE;
-        uint8_t* sV = sK + T::TILE;
-        mbar_expect_tx(&kv_full[st], 2 * T::TILE);
-#pragma unroll
-        for (int c = 0; c < T::NCH; ++c) {
-          tma_load_3d(sK + c * T::CHUNK, &p.map_qkv, &kv_full[st], p.k_col + g * D + c * T::CW, (j0 + jt) * 128, bi);
-          tma_load_3d(sV + c * T::CHUNK, &p.map_qkv, &kv_full[st], p.v_col + g * D + c * T::CW, (j0 + jt) * 128, bi);
-        }
-        issued = jt + 1;
+      ++c;
+      return true;
+    };
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      WorkItem w;
+      if (!next_item<true>(queue, it, &w, abort_flag, p.err) || w.n < 0) break;
+      if (w.nkv == 0) {
+        release_item(queue, it);
+        continue;
       }
-      if (*abort_flag) {
-        if (nkv > 0) drain_wait(qo_full, 0);
-        for (int jt = (issued > KVS ? issued - KVS : 0); jt < issued; ++jt)
-          drain_wait(&kv_full[jt % KVS], (jt / KVS) & 1);
-      }
+      ok = load_tile(&p.map_qkv, w.n * D, w.q0, w.bi) && load_tile(&p.map_do, w.n * D, w.q0, w.bi);
+      const int k_col = p.k_col + w.n / p.G * D, v_col = p.v_col + w.n / p.G * D;
+      for (int j = w.j0; ok && j < w.j0 + w.nkv; ++j)
+        ok = load_tile(&p.map_qkv, k_col, j * 128, w.bi) && load_tile(&p.map_qkv, v_col, j * 128, w.bi);
+      release_item(queue, it);
     }
+    // every copy lands before the shared memory goes, also when a wait elsewhere
+    // in the block gives up later
+    for (int k = (c > NT ? c - NT : 0); k < c; ++k) drain_wait(&t_full[k % NT], (k / NT) & 1);
   } else if (warp == 1 || warp == 10) {
-    // the whole warp runs the issue loop, one elected lane issues.  One
-    // issuer (fixed-order mode): warp 1 issues every sub-tile's products
-    // in sub-tile order, so dQ takes its products in a fixed order
-    if (U > 0 && !(p.one_issuer && warp == 10)) {
-      // ------------------------------------------------ MMA issuers
-      const int b0 = warp == 1 ? 0 : 1;  // this issuer's first sub-tile
-      const int ustep = p.one_issuer ? 1 : 2;
-      const uint32_t uKV = smem_u32(sKV);
-      // the 64 key rows of half b start 64 b rows into every chunk of the
-      // stage's K and V tiles (whole swizzle atoms); sub-tile u uses buffer
-      // b = u % 2
-      auto uK = [&](int u) { return uKV + ((u >> 1) % KVS) * 2 * T::TILE; };
-      auto issue_s = [&](int u) {
-        const int b = u & 1;
-        const uint32_t tSb = tS + 64 * b;
-        const uint64_t k = T::kmajor(uK(u) + 64 * T::SWB * b, 0);
+    // ------------------------------------------------ MMA issuers (the whole
+    // warp runs the loop, one elected lane issues).  One issuer (fixed-order
+    // mode): warp 1 issues every sub-tile's products in sub-tile order, so dQ
+    // takes its products in a fixed order, and warp 10 only reads the items.
+    const bool issues = !(p.one_issuer && warp == 10);
+    const int b0 = warp == 1 ? 0 : 1;  // this issuer's first sub-tile
+    const int ustep = p.one_issuer ? 1 : 2;
+    const uint32_t ring = smem_u32(sRing);
+    // the 64 key rows of half b start 64 b rows into every chunk of K's and
+    // V's tiles (whole swizzle atoms); sub-tile u uses buffer b = u % 2.  tg,
+    // qi: key tiles, items with keys before this one
+    int tg = 0, qi = 0;
+    auto tile = [&](int u, int v) { return 2 * (tg + qi) + 2 + 2 * (u >> 1) + v; };
+    auto slot = [&](int u, int v) { return tile(u, v) % NT; };
+    auto landed = [&](int u, int v) {
+      return bounded_wait_w(&t_full[slot(u, v)], (tile(u, v) / NT) & 1, abort_flag, 741, p.err);
+    };
+    auto issue_s = [&](int u) {
+      const int b = u & 1;
+      const uint32_t tSb = tS + 64 * b;
+      const uint64_t k = T::kmajor(ring + slot(u, 0) * T::TILE + 64 * T::SWB * b, 0);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tQA + kk * 8, k + T::kmajor_step(kk), ID_S, kk > 0);
-        umma_commit_w(&s_full[b]);
-      };
-      auto issue_dp = [&](int u) {
-        const int b = u & 1;
-        const uint32_t tdPb = tdP + 64 * b;
-        const uint64_t v = T::kmajor(uK(u) + T::TILE + 64 * T::SWB * b, 0);
+      for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tQA + kk * 8, k + T::kmajor_step(kk), ID_S, kk > 0);
+      umma_commit_w(&s_full[b]);
+    };
+    auto issue_dp = [&](int u) {
+      const int b = u & 1;
+      const uint32_t tdPb = tdP + 64 * b;
+      const uint64_t v = T::kmajor(ring + slot(u, 1) * T::TILE + 64 * T::SWB * b, 0);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tdPb, tOA + kk * 8, v + T::kmajor_step(kk), ID_S, kk > 0);
-        umma_commit_w(&dp_full[b]);
-      };
-      auto wait_stage = [&](int u) {
-        const int jt = u >> 1;
-        return bounded_wait_w(&kv_full[jt % KVS], (jt / KVS) & 1, abort_flag, 741, p.err);
-      };
-      bool ok = bounded_wait_w(qo_ready, 0, abort_flag, 742, p.err) && wait_stage(b0);
-      if (ok) {
-        tc_fence_after();
-        // sub-tiles 0 and 1 share stage 0 (U is even)
-        for (int u = b0; u < 2; u += ustep) {
-          issue_s(u);
-          issue_dp(u);
+      for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tdPb, tOA + kk * 8, v + T::kmajor_step(kk), ID_S, kk > 0);
+      umma_commit_w(&dp_full[b]);
+      umma_commit_w(&t_empty[slot(u, 1)]);
+    };
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      WorkItem w;
+      if (!next_item(queue, it, &w, abort_flag, p.err)) { ok = false; break; }
+      if (w.n < 0) break;
+      if (w.nkv == 0 || !issues) continue;
+      const int U = 2 * w.nkv;
+      ok = bounded_wait_w(qo_ready, qi & 1, abort_flag, 742, p.err);
+      if (!ok) break;
+      if (lane == 0) {
+        // the tiles of Q and dO are free
+        for (int k = 0; k < 2; ++k) {
+          uint64_t* bar = &t_empty[(2 * (tg + qi) + k) % NT];
+          mbar_arrive(bar);
+          if (p.one_issuer) mbar_arrive(bar);
         }
       }
-      for (int u = b0; ok && u < U; u += ustep) {
+      ok = landed(b0, 0);
+      if (!ok) break;
+      tc_fence_after();
+      // sub-tiles 0 and 1 share the first tiles (U is even)
+      for (int u = b0; u < 2; u += ustep) issue_s(u);
+      ok = landed(b0, 1);
+      if (!ok) break;
+      tc_fence_after();
+      for (int u = b0; u < 2; u += ustep) issue_dp(u);
+      for (int u = b0; u < U; u += ustep) {
         const int b = u & 1;
-        const uint32_t tdPb = tdP + 64 * b;
-        const int st = (u >> 1) % KVS;
+        const uint32_t phase = (tg + (u >> 1)) & 1;
         const bool more = u + 2 < U;
         if (more) {
           // S(u+2) once the group has read S(u)
-          if (!bounded_wait_w(&s_free[b], (u >> 1) & 1, abort_flag, 743, p.err) || !wait_stage(u + 2)) {
-            ok = false;
-            break;
-          }
+          ok = bounded_wait_w(&s_free[b], phase, abort_flag, 743, p.err) && landed(u + 2, 0);
+          if (!ok) break;
           tc_fence_after();
           issue_s(u + 2);
         }
         // dQ += dS(u) K_u: key rows 64b.. are K blocks 4b..4b+3 of the tile
-        if (!bounded_wait_w(&ds_full[b], (u >> 1) & 1, abort_flag, 744, p.err)) { ok = false; break; }
+        ok = bounded_wait_w(&ds_full[b], phase, abort_flag, 744, p.err);
+        if (!ok) break;
         tc_fence_after();
-        const uint64_t k = T::mnmajor(uK(u), 4 * b);
+        const uint64_t k = T::mnmajor(ring + slot(u, 0) * T::TILE, 4 * b);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) umma_bf16_tmem_a_w(tdQ, tdPb + kk * 8, k + T::mnmajor_step(kk), ID_DQ, 1);
-        umma_commit_w(&kv_empty[st]);
-        // dP(u+2) overwrites dS(u), after dQ(u) in issue order
-        if (more) issue_dp(u + 2);
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16_tmem_a_w(tdQ, tdP + 64 * b + kk * 8, k + T::mnmajor_step(kk), ID_DQ, 1);
+        umma_commit_w(&t_empty[slot(u, 0)]);
+        if (more) {
+          // dP(u+2) overwrites dS(u), after dQ(u) in issue order
+          ok = landed(u + 2, 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_dp(u + 2);
+        }
       }
-      if (ok) {
-        // all_done counts two commits: one per issuer, or both from one
-        umma_commit_w(all_done);
-        if (p.one_issuer) umma_commit_w(all_done);
-      }
-      if (!ok) {
-        umma_commit_w(&drain[b0]);
-        drain_wait(&drain[b0], 0);
-      }
+      if (!ok) break;
+      // all_done counts two commits: one per issuer, or both from one
+      umma_commit_w(all_done);
+      if (p.one_issuer) umma_commit_w(all_done);
+      tg += w.nkv;
+      ++qi;
+    }
+    if (!ok) {
+      umma_commit_w(&drain[b0]);
+      drain_wait(&drain[b0], 0);
     }
   } else {
-    // ------------------------------------------------ compute (warps 2..9;
-    // warp 10 in the one-issuer mode falls through to the final barrier)
+    // ------------------------------------------------ compute (warps 2..9)
     const int quarter = warp & 3;
     const int b = (warp - 2) >> 2;  // group = buffer = sub-tile parity
     const int r = quarter * 32 + lane;
-    const int qpos = q0 + r;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    {
-      // Q (group 0) or dO (group 1) row of this thread into TMEM (zeros past
-      // the sequence); group 0 also zeroes dQ
-      uint32_t w[D / 2];
-      const bool got = U == 0 || __all_sync(0xffffffffu, bounded_wait(qo_full, 0, abort_flag, 754, p.err));
-      if (got && U > 0) load_tile_row<D>(sKV + (KVS - 1) * 2 * T::TILE + b * T::TILE, r, w);
-      tmem_store_row<D / 2>((b == 0 ? tQA : tOA) + lane_off, w);
-      if (b == 0) {
-        uint32_t z[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) z[k] = 0u;
-#pragma unroll
-        for (int cc = 0; cc < D / 16; ++cc) tmem_st16_nw(tdQ + lane_off + cc * 16, z);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qo_ready);
-    }
-    const int2 win = key_window(p.row_begin, p.row_end, p.causal, p.s, bi, qpos);
-    const float slope2 = BIAS ? p.slopes[n] * 1.4426950408889634f : 0.f;
-    // this row's -LSE*log2(e) and dO.O sum (finite filler past the sequence)
-    const float nl = p.nl2[((long long)bi * p.H + n) * p.s_pad + qpos];
-    const float dsum = p.dsum[((long long)bi * p.H + n) * p.s_pad + qpos];
     const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
+    constexpr int CC = T::CW / 16, CH0 = (T::NCH + 1) / 2;
+    const int cbeg = b == 0 ? 0 : CH0, cend = b == 0 ? CH0 : T::NCH;  // dQ's chunks of this group
+    uint32_t zero[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) zero[k] = 0u;
+    for (int cc = cbeg * CC; cc < cend * CC; ++cc) tmem_st16_nw(tdQ + lane_off + cc * 16, zero);
+    int tg = 0, qi = 0;  // key tiles of the items before, items with keys
     bool ok = true;
-    for (int u = b; u < U; u += 2) {
-      ok = bounded_wait(&s_full[b], (u >> 1) & 1, abort_flag, 751, p.err);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      tc_fence_after();
-      // ---- phase 1: P (1 - u^2) of the 64 keys; [klo, khi) are visible
-      const int kv0 = (j0 + (u >> 1)) * 128 + 64 * b;
-      const int klo = max(win.x - kv0, 0), khi = min(win.y - kv0, 64);
-      uint32_t sv[64];
-      const float am = load_scores<true>(tSb + lane_off, sv);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[b]);
-      const bool all = klo == 0 && khi == 64;
-      auto on = [&](int x) { return x >= klo && x < khi; };
-      float pe[64];
+    for (int it = 0; ok; ++it) {
+      WorkItem w;
+      if (!next_item(queue, it, &w, abort_flag, p.err) || w.n < 0) break;
+      const int qpos = w.q0 + r;
+      if (w.nkv == 0) {
+        // no row of the tile sees a key
+        if (b == 0 && qpos < p.s) {
+          uint4* row = reinterpret_cast<uint4*>(p.dqkv + ((long long)w.bi * p.s + qpos) * p.width + (long long)w.n * D);
+#pragma unroll
+          for (int cc = 0; cc < D / 8; ++cc) row[cc] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      const int2 win = key_window(p.row_begin, p.row_end, p.causal, p.s, w.bi, qpos);
+      const float slope2 = BIAS ? p.slopes[w.n] * 1.4426950408889634f : 0.f;
+      // this row's -LSE*log2(e) and dO.O sum (finite filler past the sequence)
+      const float nl = p.nl2[((long long)w.bi * p.H + w.n) * p.s_pad + qpos];
+      const float dsum = p.dsum[((long long)w.bi * p.H + w.n) * p.s_pad + qpos];
       {
-        uint32_t pk[32];
-        const uint64_t nl2 = f2(nl, nl);
-        if constexpr (!BIAS) {
-          auto add = [&](int) { return nl2; };
-          probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
-        } else {
-          const BiasLine bl = bias_line(slope2, qpos, kv0, 64, p.causal != 0, false);
-          if (!__any_sync(0xffffffffu, bl.mixed)) {
-            const uint64_t step2 = both(bl.step), base2 = both(bl.base + nl);
-            auto add = [&](int x) { return on_line(x, step2, base2); };
+        // Q (group 0) or dO (group 1) row of this thread into TMEM (zeros past
+        // the sequence)
+        uint32_t row[D / 2];
+        const int c = 2 * (tg + qi) + b;
+        ok = __all_sync(0xffffffffu, bounded_wait(&t_full[c % NT], (c / NT) & 1, abort_flag, 754, p.err));
+        if (!ok) break;
+        load_tile_row<D>(sRing + c % NT * T::TILE, r, row);
+        tmem_store_row<D / 2>((b == 0 ? tQA : tOA) + lane_off, row);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qo_ready);
+      }
+      const int U = 2 * w.nkv;
+      for (int u = b; u < U; u += 2) {
+        const uint32_t phase = (tg + (u >> 1)) & 1;
+        ok = bounded_wait(&s_full[b], phase, abort_flag, 751, p.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        // ---- phase 1: P (1 - u^2) of the 64 keys; [klo, khi) are visible
+        const int kv0 = (w.j0 + (u >> 1)) * 128 + 64 * b;
+        const int klo = max(win.x - kv0, 0), khi = min(win.y - kv0, 64);
+        uint32_t sv[64];
+        const float am = load_scores<true>(tSb + lane_off, sv);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[b]);
+        const bool all = klo == 0 && khi == 64;
+        auto on = [&](int x) { return x >= klo && x < khi; };
+        float pe[64];
+        {
+          uint32_t pk[32];
+          const uint64_t nl2 = f2(nl, nl);
+          if constexpr (!BIAS) {
+            auto add = [&](int) { return nl2; };
             probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
           } else {
-            const float dist = (float)(qpos - kv0);
-            auto add = [&](int x) {
-              return add2(nl2, f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
-            };
-            probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
+            const BiasLine bl = bias_line(slope2, qpos, kv0, 64, p.causal != 0, false);
+            if (!__any_sync(0xffffffffu, bl.mixed)) {
+              const uint64_t step2 = both(bl.step), base2 = both(bl.base + nl);
+              auto add = [&](int x) { return on_line(x, step2, base2); };
+              probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
+            } else {
+              const float dist = (float)(qpos - kv0);
+              auto add = [&](int x) {
+                return add2(nl2, f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
+              };
+              probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
+            }
           }
         }
-      }
-      // ---- phase 2: dS = P (dP - D), over the first 32 columns of buffer b
-      ok = bounded_wait(&dp_full[b], (u >> 1) & 1, abort_flag, 752, p.err);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t dr[64];
-      tmem_ld32_nw(tdPb + lane_off, dr);
-      tmem_ld32_nw(tdPb + lane_off + 32, dr + 32);
-      tmem_wait_ld(dr);
-      if (!all) mask_gradient(dr, pe);
-      uint32_t o[32];
-      const uint64_t ds2 = f2(dsum, dsum);
+        // ---- phase 2: dx = P (1 - u^2) (dP - D), over the first 32 columns of buffer b
+        ok = bounded_wait(&dp_full[b], phase, abort_flag, 752, p.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t dr[64];
+        tmem_ld32_nw(tdPb + lane_off, dr);
+        tmem_ld32_nw(tdPb + lane_off + 32, dr + 32);
+        tmem_wait_ld(dr);
+        if (!all) mask_gradient(dr, pe);
+        uint32_t o[32];
+        const uint64_t ds2 = f2(dsum, dsum);
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
-        const float2 v = f2split(
-            mul2(f2(pe[k], pe[k + 1]), sub2(f2(__uint_as_float(dr[k]), __uint_as_float(dr[k + 1])), ds2)));
-        o[k / 2] = pack_bf16(v.x, v.y);
+        for (int k = 0; k < 64; k += 2) {
+          const float2 v = f2split(
+              mul2(f2(pe[k], pe[k + 1]), sub2(f2(__uint_as_float(dr[k]), __uint_as_float(dr[k + 1])), ds2)));
+          o[k / 2] = pack_bf16(v.x, v.y);
+        }
+        tmem_st32(tdPb + lane_off, o);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ds_full[b]);
       }
-      tmem_st32(tdPb + lane_off, o);
-      tmem_st_wait();
-      tc_fence_before();
+      tg += w.nkv;
+      // both issuers' products of the item are done
+      if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, qi & 1, abort_flag, 753, p.err));
+      if (!ok) break;
+      ++qi;
+      tc_fence_after();
+      // each group's half of dQ out by TMA, and zeroed for the next item
+      if (lane == 0) bulk_wait_read0();  // this warp's part of the tile is free
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[b]);
-    }
-    // epilogue: the two groups split dQ's 16-column chunks once both
-    // issuers' products are done
-    if (U == 0) {
-      // no row of the tile sees a key
-      if (b == 0 && qpos < p.s) {
-        uint4* row = reinterpret_cast<uint4*>(p.dqkv + ((long long)bi * p.s + qpos) * p.width + (long long)n * D);
-#pragma unroll
-        for (int cc = 0; cc < D / 8; ++cc) row[cc] = make_uint4(0u, 0u, 0u, 0u);
-      }
-      ok = false;
-    }
-    if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, 0, abort_flag, 753, p.err));
-    if (ok) {
-      tc_fence_after();
-      // staged in the first stage, which every product has read, and stored
-      // by TMA
-      constexpr int CC = T::CW / 16, CH0 = (T::NCH + 1) / 2;
-      const int cbeg = b == 0 ? 0 : CH0, cend = b == 0 ? CH0 : T::NCH;  // chunks of this group
-      const uint32_t tq = tdQ + lane_off;
       for (int cc = cbeg * CC; cc < cend * CC; ++cc) {
         uint32_t v[16];
-        tmem_ld16_nw(tq + cc * 16, v);
+        tmem_ld16_nw(tdQ + lane_off + cc * 16, v);
         tmem_wait_ld(v);
-        store_tile16<D>(sKV, r, cc, v, p.scale);
+        tmem_st16_nw(tdQ + lane_off + cc * 16, zero);
+        store_tile16<D>(sOut, r, cc, v, p.scale);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && qpos < p.s) {
         for (int c = cbeg; c < cend; ++c)
-          tma_store_3d(&p.map_out, sKV + c * T::CHUNK + quarter * 32 * T::SWB, n * D + c * T::CW, qpos, bi);
+          tma_store_3d(&p.map_out, sOut + c * T::CHUNK + quarter * 32 * T::SWB, w.n * D + c * T::CW, qpos, w.bi);
         bulk_commit();
-        bulk_wait0();  // before the shared memory goes
       }
     }
+    if (lane == 0) bulk_wait0();  // before the shared memory goes
   }
 
   tc_fence_before();
@@ -1015,7 +1060,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dq_kernel(const __grid_consta
   tc_fence_after();
   // dK/dV started after the preparation had ended and let this kernel start,
   // so nothing above waited for it; but the call ends when both have
-  if (blockIdx.x == gridDim.x - 1) wait_for_previous();
+  if (took_last) wait_for_previous();
   if (warp == 1) {
     __syncwarp();
     tmem_dealloc(tmem, 512);
@@ -1141,7 +1186,7 @@ int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
       return BPT_ECUDA;
   }
   ProfScope prof(PROF_ATTN_BWD, 2.0 * D * pairs * p.H * b, 0.0, st);
-  return launch_dependent(attn_mod_dq_kernel<D, CAP, BIAS>, p.n_t * p.H * b, 1, dim3(352), SMEM_Q, st, p) == cudaSuccess
+  return launch_dependent(attn_mod_dq_kernel<D, CAP, BIAS>, p.n_t * p.H * b, 1, dim3(384), SMEM_Q, st, p) == cudaSuccess
              ? BPT_OK
              : BPT_ECUDA;
 }

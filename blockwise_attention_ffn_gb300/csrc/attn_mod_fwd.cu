@@ -59,11 +59,6 @@ struct ModFwdParams {
   unsigned int* err;
 };
 
-// One work item as warp 11 publishes it; n < 0: no more.
-struct WorkItem {
-  int n, bi, q0, j0, nkv;
-};
-
 // TMEM: S of half b as two 64-column buffers at 128 b, O_b at 256 + b D.
 // Shared memory: two Q tiles, a ring of K and V tiles in the order they are
 // used (K_0, K_1, V_0, K_2, V_1, ..., V_last, then the next item's), the
@@ -86,7 +81,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
   constexpr int NT = C::NT;
   static_assert(NT >= 4, "K and V of two steps");
   static_assert(C::COL_O + 2 * D <= 512, "TMEM columns");
-  static_assert((2 * NT + 30) * 8 + 2 * 32 + 2 * 16 + 8 <= C::CTL, "control block");
+  static_assert((2 * NT + 30) * 8 + WORK_BYTES + 8 <= C::CTL, "control block");
   constexpr uint32_t IDESC_S = idesc_bf16(128, 64, false, false);
   constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
   constexpr float NEG_INF = -INFINITY;
@@ -98,18 +93,16 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
   uint8_t* sKV = smem + 2 * T::TILE;
   float* red_m = reinterpret_cast<float*>(sKV + NT * T::TILE);  // [half][row]
   float* red_l = red_m + 256;
-  uint8_t* answer = reinterpret_cast<uint8_t*>(red_l + 256);  // [2] 16 bytes
-  WorkItem* work = reinterpret_cast<WorkItem*>(answer + 32);  // [2], 32 bytes apart
-  uint64_t* bars = reinterpret_cast<uint64_t*>(answer + 32 + 64);
-  uint64_t* work_full = bars;           // [2]
-  uint64_t* work_empty = bars + 2;      // [2] 8 softmax warps, 2 issuers, the loads
+  uint8_t* control = reinterpret_cast<uint8_t*>(red_l + 256);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(control + WORK_BYTES);
+  // (read by 8 softmax warps, 2 issuers, the loads)
+  const WorkQueue queue{control, bars, bars + 2, bars + 19};
   uint64_t* q_full = bars + 4;          // [2]
   uint64_t* q_empty = bars + 6;         // [2] both issuers' last S, 8 warps' O stored from it
   uint64_t* s_full = bars + 8;          // [half][buffer]
   uint64_t* p_full = bars + 12;         // [half][buffer] 4 warps
   uint64_t* pv_done = bars + 16;        // [half]
   uint64_t* o_free = bars + 18;         // both O's read (8 warps)
-  uint64_t* answered = bars + 19;       // the request for the next item
   uint64_t* drain = bars + 20;          // [half]
   uint64_t* merged = bars + 22;         // [half][quarter] its maxima and sums are written
   uint64_t* t_full = bars + 30;         // [NT]
@@ -122,14 +115,13 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
   // every step).  Else ascending: then the CTAs of a head begin with the same
   // keys (32 + 8 + 8 heads of 128: 422 us, 436 descending).
   auto key_tile = [](int j, int j0, int nkv) { return BIAS ? j0 + nkv - 1 - j : j0 + j; };
-  auto item_at = [&](int it) { return reinterpret_cast<volatile WorkItem*>(reinterpret_cast<uint8_t*>(work) + 32 * (it & 1)); };
 
   const int warp = warp_id();
   const int lane = lane_id();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&work_full[i], 1);
-      mbar_init(&work_empty[i], 11);
+      mbar_init(&queue.full[i], 1);
+      mbar_init(&queue.empty[i], 11);
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 2 + 8);
       mbar_init(&pv_done[i], 1);
@@ -141,7 +133,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     }
     for (int i = 0; i < 8; ++i) mbar_init(&merged[i], 1);
     mbar_init(o_free, 8);
-    mbar_init(answered, 1);
+    mbar_init(queue.answered, 1);
     for (int i = 0; i < NT; ++i) {
       mbar_init(&t_full[i], 1);
       mbar_init(&t_empty[i], 2);
@@ -164,18 +156,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
 
   if (warp == 11) {
     // ------------------------------------------------ items (the whole warp)
-    // The next item is asked for when every warp has begun the current one,
-    // so that a CTA holds one item back from the others at most.
-    int block = blockIdx.x, it = 0;
-    bool asked = false;
-    while (true) {
-      if (block < 0) {
-        if (lane == 0) {
-          item_at(it)->n = -1;
-          mbar_arrive(&work_full[it & 1]);
-        }
-        break;
-      }
+    publish_items(queue, blockIdx.x, -1, abort_flag, p.err, [&](int block) {
       const Item w = item_of(p.order, block);
       const int bi = w.kv / (p.H / p.G), n = w.kv % (p.H / p.G) * p.G + w.sub;
       const int q0 = (p.order.tiles - 1 - w.tile) * 128;
@@ -190,30 +171,16 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       lo = __reduce_min_sync(0xffffffffu, lo);
       hi = __reduce_max_sync(0xffffffffu, hi);
       const int j0 = lo < hi ? lo / 128 : 0;
-      if (lane == 0) {
-        volatile WorkItem* to = item_at(it);
-        to->n = n;
-        to->bi = bi;
-        to->q0 = q0;
-        to->j0 = j0;
-        to->nkv = lo < hi ? (hi + 127) / 128 - j0 : 0;
-        mbar_arrive(&work_full[it & 1]);
-      }
-      if (!bounded_wait_w(&work_empty[it & 1], (it >> 1) & 1, abort_flag, 252, p.err)) break;
-      if (lane == 0) request_block(answer + 16 * (it & 1), answered);
-      asked = true;
-      if (!bounded_wait_w(answered, it & 1, abort_flag, 257, p.err)) break;
-      asked = false;
-      block = answered_block(answer + 16 * (it & 1));
-      fence_proxy_async_smem();
-      __syncwarp();
-      ++it;
-    }
-    // a request in flight lands before the shared memory goes
-    if (asked) drain_wait(answered, it & 1);
+      return WorkItem{n, bi, q0, j0, lo < hi ? (hi + 127) / 128 - j0 : 0};
+    });
   } else if (warp == 0) {
     // ------------------------------------------------ loads (the whole warp
-    // runs the loop, one lane issues)
+    // runs the loop, one lane issues).  The next item is asked for three key
+    // tiles before the last load.  At the last load is too late for its tiles
+    // to be there (documents of 1500, 32 heads of 80: 132 us against 122), at
+    // the item's start too early to balance the CTAs (324 items of prefix rows,
+    // heads of 96: 38 us against 32)
+    constexpr int LEAD = 3;
     int qi = 0, c = 0;  // items with keys, tiles loaded
     bool ok = true;
     auto load_tile = [&](int col, int row, int bi) -> bool {
@@ -229,12 +196,11 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       return true;
     };
     for (int it = 0; ok; ++it) {
-      if (!bounded_wait_w(&work_full[it & 1], (it >> 1) & 1, abort_flag, 250, p.err)) break;
-      volatile WorkItem* w = item_at(it);
-      const int n = w->n, bi = w->bi, q0 = w->q0, j0 = w->j0, nkv = w->nkv;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&work_empty[it & 1]);
+      WorkItem w;
+      if (!next_item<true>(queue, it, &w, abort_flag, p.err)) break;
+      const int n = w.n, bi = w.bi, q0 = w.q0, j0 = w.j0, nkv = w.nkv;
       if (n < 0) break;
+      if (nkv < LEAD) release_item(queue, it);
       if (nkv == 0) continue;
       const int sl = qi & 1;
       if (qi >= 2 && !bounded_wait_w(&q_empty[sl], ((qi >> 1) & 1) ^ 1, abort_flag, 256, p.err)) break;
@@ -249,13 +215,13 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       for (int j = 0; ok && j <= nkv; ++j) {
         if (j < nkv) ok = load_tile(k_col, key_tile(j, j0, nkv) * 128, bi);
         if (ok && j > 0) ok = load_tile(v_col, key_tile(j - 1, j0, nkv) * 128, bi);
+        if (j == nkv - LEAD) release_item(queue, it);
       }
     }
-    if (*abort_flag) {
-      // copies in flight land before the shared memory goes
-      for (int k = (qi > 2 ? qi - 2 : 0); k < qi; ++k) drain_wait(&q_full[k & 1], (k >> 1) & 1);
-      for (int k = (c > NT ? c - NT : 0); k < c; ++k) drain_wait(&t_full[k % NT], (k / NT) & 1);
-    }
+    // every copy lands before the shared memory goes, also when a wait elsewhere
+    // in the block gives up later
+    for (int k = (qi > 2 ? qi - 2 : 0); k < qi; ++k) drain_wait(&q_full[k & 1], (k >> 1) & 1);
+    for (int k = (c > NT ? c - NT : 0); k < c; ++k) drain_wait(&t_full[k % NT], (k / NT) & 1);
   } else if (warp == 1 || warp == 10) {
     // ------------------------------------------------ MMA issuers (the
     // whole warp runs the loop, one elected lane issues).  Steps are counted
@@ -286,11 +252,10 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     };
     bool ok = true;
     for (int it = 0; ok; ++it) {
-      if (!bounded_wait_w(&work_full[it & 1], (it >> 1) & 1, abort_flag, 254, p.err)) { ok = false; break; }
-      const int n = item_at(it)->n, nkv = item_at(it)->nkv;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&work_empty[it & 1]);
-      if (n < 0) break;
+      WorkItem w;
+      if (!next_item(queue, it, &w, abort_flag, p.err)) { ok = false; break; }
+      const int nkv = w.nkv;
+      if (w.n < 0) break;
       if (nkv == 0) continue;
       if (!bounded_wait_w(&q_full[qi & 1], (qi >> 1) & 1, abort_flag, 259, p.err)) { ok = false; break; }
       const uint64_t q = T::kmajor(uQ + (qi & 1) * T::TILE, 0);
@@ -336,12 +301,9 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     };
     bool ok = true;
     for (int it = 0; ok; ++it) {
-      ok = __all_sync(0xffffffffu, bounded_wait(&work_full[it & 1], (it >> 1) & 1, abort_flag, 260, p.err));
-      if (!ok) break;
-      volatile WorkItem* w = item_at(it);
-      const int n = w->n, bi = w->bi, qpos = w->q0 + r, j0 = w->j0, nkv = w->nkv;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&work_empty[it & 1]);
+      WorkItem w;
+      if (!next_item(queue, it, &w, abort_flag, p.err)) break;
+      const int n = w.n, bi = w.bi, qpos = w.q0 + r, j0 = w.j0, nkv = w.nkv;
       if (n < 0) break;
       // (an item without keys leaves it to the next one with some)
       if (nkv > 0) stored();
