@@ -245,6 +245,17 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  if (warp == 0 && lane == 0) {
+    // K and V, of which the preparation writes nothing: to stay (d > 80), or in
+    // the last stage until the compute warps have copied them to TMEM
+    uint8_t* kv = C::KV_TMEM ? sStage + (QS - 1) * STAGE : sKV;
+    mbar_expect_tx(kv_full, 2 * T::TILE);
+#pragma unroll
+    for (int c = 0; c < T::NCH; ++c) {
+      tma_load_3d(kv + c * T::CHUNK, &p.map_qkv, kv_full, p.k_col + g * D + c * T::CW, j * 128, bi);
+      tma_load_3d(kv + T::TILE + c * T::CHUNK, &p.map_qkv, kv_full, p.v_col + g * D + c * T::CW, j * 128, bi);
+    }
+  }
   // what the preparation wrote; the dQ kernel, which needs nothing of this
   // one, fills the SMs that this one's last round leaves idle
   wait_for_previous();
@@ -283,17 +294,8 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   const uint32_t tVA = tmem + C::COL_V;
 
   if (warp == 0) {
-    if (lane == 0 && U > 0) {
+    if (lane == 0) {
       // ------------------------------------------------ TMA producer
-      // K and V: to stay (d > 80), or in the last stage until the compute
-      // warps have copied them to TMEM
-      uint8_t* kv = C::KV_TMEM ? sStage + (QS - 1) * STAGE : sKV;
-      mbar_expect_tx(kv_full, 2 * T::TILE);
-#pragma unroll
-      for (int c = 0; c < T::NCH; ++c) {
-        tma_load_3d(kv + c * T::CHUNK, &p.map_qkv, kv_full, p.k_col + g * D + c * T::CW, j * 128, bi);
-        tma_load_3d(kv + T::TILE + c * T::CHUNK, &p.map_qkv, kv_full, p.v_col + g * D + c * T::CW, j * 128, bi);
-      }
       int issued = 0;
       for (int t = 0; t < T_iter; ++t) {
         const int st = t % QS;
