@@ -31,6 +31,12 @@
 // the next item's windows and warp 0 loads its Q and K/V while the softmax is
 // still in the current one, and its first S is made during the current item's
 // merge.
+//
+// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: 433 us plain scores
+// (1,270 TFLOP/s of unmasked pairs), 480 capped (1,145), 469 biased; documents of
+// 1500: 126 us, 145 capped.  What bounds it is the chain S, modified softmax, P,
+// PV of each half (at 4096 rows, capped: tensor core 43% busy, issue slots 41%):
+// the two halves' warps overlap each other's waits but not all of them.
 #include <math.h>
 #include <string.h>
 
