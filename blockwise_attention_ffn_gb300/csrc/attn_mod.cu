@@ -27,12 +27,13 @@ int check(const bpt_config* cfg, const bpt_score_mod* mod, PackedDims* D) {
   return BPT_OK;
 }
 
-int mod_spans(const PackedDims& D, const bpt_score_mod* mod) {
-  const Span sp[] = {{mod->row_begin, mod->row_begin ? D.rows * 4 : 0},
-                     {mod->row_end, mod->row_end ? D.rows * 4 : 0},
-                     {mod->slopes, mod->slopes ? D.H * 4 : 0}};
-  return debug_spans(sp, 3);
-}
+struct ModSpans {
+  Span sp[3];
+  ModSpans(const PackedDims& D, const bpt_score_mod* mod)
+      : sp{{mod->row_begin, mod->row_begin ? D.rows * 4 : 0},
+           {mod->row_end, mod->row_end ? D.rows * 4 : 0},
+           {mod->slopes, mod->slopes ? D.H * 4 : 0}} {}
+};
 
 }  // namespace
 
@@ -46,8 +47,10 @@ int bpt_attention_mod_fwd(const bpt_config* cfg, const bpt_score_mod* mod, const
   if (!qkv || !o || !aligned16(qkv) || !aligned16(o) || !aligned16(lse)) return BPT_EINVAL;
   const Span sp[] = {{qkv, D.rows * D.width * 2}, {o, D.rows * D.H * D.d * 2},
                      {lse, lse ? D.b * D.H * D.s_pad * 4 : 0}};
+  const ModSpans ms(D, mod);
   if (overlaps(sp[1], sp, 1) || (lse && overlaps(sp[2], sp, 2))) return BPT_EINVAL;
-  if (D.debug && (debug_spans(sp, 3) || mod_spans(D, mod))) return BPT_EINVAL;
+  if (overlaps(sp[1], ms.sp, 3) || (lse && overlaps(sp[2], ms.sp, 3))) return BPT_EINVAL;
+  if (D.debug && (debug_spans(sp, 3) || debug_spans(ms.sp, 3))) return BPT_EINVAL;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if ((rc = attention_mod_fwd(D, cfg->causal, *mod, qkv, o, reinterpret_cast<float*>(lse), st))) return rc;
   return D.debug ? debug_finish(st) : BPT_OK;
@@ -71,8 +74,10 @@ int bpt_attention_mod_bwd(const bpt_config* cfg, const bpt_score_mod* mod, const
   const int64_t packed = D.rows * D.width * 2, hd = D.rows * D.H * D.d * 2;
   const Span sp[] = {{qkv, packed}, {o, hd}, {lse, D.b * D.H * D.s_pad * 4}, {dout, hd}, {dqkv, packed},
                      {ws, (int64_t)need}};
+  const ModSpans ms(D, mod);
   if (overlaps(sp[4], sp, 4) || overlaps(sp[5], sp, 5)) return BPT_EINVAL;
-  if (D.debug && (debug_spans(sp, 6) || mod_spans(D, mod))) return BPT_EINVAL;
+  if (overlaps(sp[4], ms.sp, 3) || overlaps(sp[5], ms.sp, 3)) return BPT_EINVAL;
+  if (D.debug && (debug_spans(sp, 6) || debug_spans(ms.sp, 3))) return BPT_EINVAL;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if ((rc = attention_mod_bwd(D, cfg->causal, *mod, qkv, o, reinterpret_cast<const float*>(lse), dout, dqkv, ws, st)))
     return rc;

@@ -301,15 +301,18 @@ int clip_launches(int n, const bpt_clip_tensor* t, float max_norm, float* norm, 
   return BPT_OK;
 }
 
-// true if some output's bytes are also another tensor's input or output (a
-// tensor's own input may be its output)
-bool overlapping(int n, const bpt_clip_tensor* t) {
+// true if some output's bytes (norm and ws among them) are also another
+// tensor's input or output (a tensor's own input may be its output)
+bool overlapping(int n, const bpt_clip_tensor* t, const void* norm, const void* ws) {
   struct Range {
     uintptr_t lo, hi;
     bool out;
   };
   std::vector<Range> r;
-  r.reserve(2 * (size_t)n);
+  r.reserve(2 * (size_t)n + 2);
+  const uintptr_t pn = reinterpret_cast<uintptr_t>(norm), pw = reinterpret_cast<uintptr_t>(ws);
+  r.push_back(Range{pn, pn + sizeof(float), true});
+  r.push_back(Range{pw, pw + bpt_clip_workspace_bytes(), true});
   for (int i = 0; i < n; ++i) {
     const uintptr_t bytes = (uintptr_t)t[i].numel * (t[i].dtype == BPT_DTYPE_BF16 ? 2 : 4);
     if (!bytes) continue;
@@ -353,7 +356,7 @@ int bpt_clip_grads(int32_t n, const bpt_clip_tensor* t, float max_norm, int32_t 
   }
   if (ws_bytes < bpt_clip_workspace_bytes()) return BPT_ENOSPC;
   try {
-    if (overlapping(n, t)) return BPT_EINVAL;
+    if (overlapping(n, t, norm, ws)) return BPT_EINVAL;
   } catch (...) {  // no host memory for the check
     return BPT_EUNSUPPORTED;
   }

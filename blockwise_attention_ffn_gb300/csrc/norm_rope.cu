@@ -625,11 +625,10 @@ int bpt_qk_norm_rope_fwd(const bpt_config* cfg, const void* qkv, const void* wq,
   if (!qkv || !out || !aligned16(qkv) || !aligned16(out)) return BPT_EINVAL;
   const int64_t bytes = D.rows * D.width * 2;
   if (part_overlap(qkv, out, bytes)) return BPT_EINVAL;
-  if (D.debug) {
-    const Span sp[] = {{qkv, bytes}, {out, bytes}, {wq, wq ? D.d * 2 : 0}, {wk, wk ? D.d * 2 : 0},
-                       {positions, positions ? D.rows * 4 : 0}};
-    if (debug_spans(sp, 5)) return BPT_EINVAL;
-  }
+  const Span sp[] = {{wq, wq ? D.d * 2 : 0}, {wk, wk ? D.d * 2 : 0}, {positions, positions ? D.rows * 4 : 0},
+                     {qkv, bytes}, {out, bytes}};
+  if (overlaps(sp[4], sp, 3)) return BPT_EINVAL;
+  if (D.debug && debug_spans(sp, 5)) return BPT_EINVAL;
   NormRopeParams p;
   fill(cfg, D, wq, wk, positions, &p);
   p.x = reinterpret_cast<const __nv_bfloat16*>(qkv);
@@ -660,12 +659,15 @@ int bpt_qk_norm_rope_bwd(const bpt_config* cfg, const void* qkv, const void* wq,
     if (qkv == dqkv || part_overlap(qkv, dqkv, bytes)) return BPT_EINVAL;
     if (ws_bytes < ws_need(D)) return BPT_ENOSPC;
   }
-  if (D.debug) {
-    const int64_t dw = wq ? D.d * 4 : 0;
-    const Span sp[] = {{qkv, wq ? bytes : 0}, {dout, bytes}, {dqkv, bytes}, {wq, dw / 2}, {wk, dw / 2}, {dwq, dw},
-                       {dwk, dw}, {ws, wq ? (int64_t)ws_need(D) : 0}, {positions, positions ? D.rows * 4 : 0}};
-    if (debug_spans(sp, 9)) return BPT_EINVAL;
-  }
+  const int64_t dw = wq ? D.d * 4 : 0;
+  const Span sp[] = {{wq, dw / 2}, {wk, dw / 2}, {positions, positions ? D.rows * 4 : 0}, {dqkv, bytes}, {dout, bytes},
+                     {wq ? qkv : nullptr, wq ? bytes : 0}, {wq ? dwq : nullptr, dw}, {wq ? dwk : nullptr, dw},
+                     {wq ? ws : nullptr, wq ? (int64_t)ws_need(D) : 0}};
+  // (dqkv may be dout)
+  if (overlaps(sp[3], sp, 3)) return BPT_EINVAL;
+  for (int i = 6; wq && i < 9; ++i)
+    if (overlaps(sp[i], sp, i)) return BPT_EINVAL;
+  if (D.debug && debug_spans(sp, 9)) return BPT_EINVAL;
   NormRopeParams p;
   fill(cfg, D, wq, wk, positions, &p);
   p.x = reinterpret_cast<const __nv_bfloat16*>(qkv);

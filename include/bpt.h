@@ -431,7 +431,8 @@ int bpt_lm_loss_bwd(const bpt_lm_config* cfg, const void* x, const void* w, cons
  *   dwq, dwk   [d] fp32 out (+= with BPT_FLAG_ACCUM_GRADS)
  *   ws         backward with weights only: bpt_qk_norm_rope_workspace_bytes
  * Without weights the backward reads neither qkv nor ws and writes no dw: all
- * four may be NULL.  Buffers that overlap in part are refused.  Every sum is
+ * four may be NULL.  Outputs and ws that share bytes with an input or one
+ * another otherwise than above are refused (BPT_EINVAL).  Every sum is
  * taken in a fixed order.  The weights need not be the layer's: the layer
  * calls have no head norm. */
 size_t bpt_qk_norm_rope_workspace_bytes(const bpt_config* cfg);
@@ -451,8 +452,8 @@ int bpt_qk_norm_rope_bwd(const bpt_config* cfg, const void* qkv, const void* wq,
  *   t        n tensors (host array, read during the call): grad and out are
  *            device pointers aligned to their element; out == grad clips in
  *            place (nothing is written where the norm is within max_norm).
- *            An output may not share memory with any other tensor of the call
- *            (BPT_EINVAL): each is scaled once.
+ *            An output may not share memory with any other tensor of the call,
+ *            with norm or with ws (BPT_EINVAL): each is scaled once.
  *   max_norm > 0; +inf computes the norm and copies
  *   flags    0 or BPT_FLAG_DEBUG_CHECKS
  *   norm     one fp32 (device), the norm before clipping; not part of a tensor

@@ -90,6 +90,16 @@ def test_attention_rejects_shapes_modifiers_and_workspace(lib):
     assert lib.bpt_attention_mod_bwd_workspace_bytes(cfg(head_dim=72)) == 0
 
 
+@pytest.mark.parametrize("i", range(3))
+def test_attention_rejects_outputs_over_the_modifiers(lib, i):
+    """o, lse, dqkv and ws may not share bytes with the windows or slopes."""
+    mod = bpt.BptScoreMod(*[far(7) if j == i else None for j in range(3)], 0.0)
+    for kw in (dict(o=far(7)), dict(lse=far(7)), dict(o=far(7) - 512)):
+        assert fwd(lib, mod=mod, **kw) == bpt.BPT_EINVAL, kw
+    for kw in (dict(dqkv=far(7)), dict(ws=far(7)), dict(ws=far(7) - 4096)):
+        assert bwd(lib, mod=mod, **kw) == bpt.BPT_EINVAL, kw
+
+
 def norm_fwd(lib, c=None, **kw):
     a = dict(qkv=far(1), wq=far(2), wk=far(3), pos=None, out=far(4)) | kw
     return lib.bpt_qk_norm_rope_fwd(cfg() if c is None else c, a["qkv"], a["wq"], a["wk"], a["pos"], a["out"], None)
@@ -113,6 +123,22 @@ def test_norm_rope_rejects(lib):
                dict(dqkv=far(1)), dict(dqkv=far(4) + 64), dict(dqkv=far(1) + 64), dict(wq=None), dict(dwq=far(6) + 2)):
         assert norm_bwd(lib, **kw) == bpt.BPT_EINVAL, kw
     assert norm_bwd(lib, n=16) == bpt.BPT_ENOSPC
+
+
+def test_norm_rope_rejects_outputs_over_other_buffers(lib):
+    for kw in (dict(out=far(2)), dict(out=far(3) - 4096), dict(out=far(9), pos=far(9)), dict(pos=far(4) + 4096)):
+        assert norm_fwd(lib, **kw) == bpt.BPT_EINVAL, kw
+    for kw in (dict(dqkv=far(2)), dict(dqkv=far(9), pos=far(9)), dict(dwq=far(7)), dict(dwk=far(6) + 128),
+               dict(dwq=far(5) + 64), dict(dwk=far(4)), dict(dwq=far(1)), dict(dwq=far(2)), dict(ws=far(5)),
+               dict(ws=far(6)), dict(ws=far(1) + 256), dict(ws=far(3) - 256), dict(dwk=far(9), pos=far(9))):
+        assert norm_bwd(lib, **kw) == bpt.BPT_EINVAL, kw
+
+
+def test_clip_rejects_tensors_over_norm_and_workspace(lib):
+    for bad in ([(far(20), far(2), 100, 0)], [(far(1), far(20) - 4, 2, 0)], [(far(21) + 64, far(2), 100, 0)],
+                [(far(1), far(21), 100, 1)]):
+        assert clip(lib, bad) == bpt.BPT_EINVAL, bad
+    assert clip(lib, [], norm=far(21)) == bpt.BPT_EINVAL
 
 
 def clip(lib, tensors, max_norm=1.0, flags=0, norm=far(20), ws=far(21), n=None, size=None):
