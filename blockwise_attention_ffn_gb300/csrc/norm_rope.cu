@@ -21,9 +21,9 @@
 //
 // Two forms.  With rows for every SM several times over, blocks stream tiles
 // of whole rows through shared memory by bulk copies (32768 rows of 32 + 32 + 32
-// heads of 64: 127 us, 95% of a copy's bandwidth; of 80: 192 us, backward 285 us;
-// 65536 rows of 32 + 8 + 8 heads of 128: 303 us, where the arithmetic of four heads
-// a warp holds it at 78%).  Fewer rows are read straight into registers, their
+// heads of 64: 130 us, 92% of a copy's bandwidth; of 80: 162 us, backward 249 us;
+// 65536 rows of 32 + 8 + 8 heads of 128: 290 us, where the arithmetic of four heads
+// a warp holds it at 82%).  Fewer rows are read straight into registers, their
 // heads spread over all warps (40 heads of 8 rows: one step of 80 warps).
 //
 // Angles: p * theta in turns, as a 64-bit fraction of a turn.  The product of
@@ -342,8 +342,9 @@ __global__ void __launch_bounds__(NR_THREADS, BWD ? 2 : 3) norm_rope_kernel(cons
 // of KB are in flight per SM whatever the warps do, and V's columns pass
 // through without a register.  Backward a stage holds the rows of dy, computed
 // in place, and the query and key columns of x.
+constexpr int NR_STAGES = 2;
 struct Stages {
-  int rows, count;           // rows of a stage; stages
+  int rows;                  // rows of a stage; 0: not even one fits
   int y_bytes, x_bytes;      // of a row: of dy (x forward), and backward of x
 };
 template <int L, bool BWD>
@@ -353,10 +354,10 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const _
   constexpr int HPW = 32 / L, D = 16 * L, HALF = 8 * L;
   extern __shared__ __align__(128) uint8_t smem[];
   const int stage_bytes = g.rows * (g.y_bytes + g.x_bytes);
-  float* cosines = reinterpret_cast<float*>(smem + g.count * stage_bytes);
+  float* cosines = reinterpret_cast<float*>(smem + NR_STAGES * stage_bytes);
   float* sines = cosines + g.rows * HALF;
   float* weights = sines + g.rows * HALF;  // wq, wk in fp32
-  __shared__ __align__(8) uint64_t full[4];
+  __shared__ __align__(8) uint64_t full[NR_STAGES];
   __shared__ int abort_flag;
   const int lane = lane_id(), slot = lane / L, idx = lane % L, base = slot * L;
   const bool lane_on = slot < HPW;
@@ -368,9 +369,9 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const _
     const int64_t row0 = tile_of(k) * g.rows;
     if (row0 >= p.rows) return;
     const int rows = (int)min((int64_t)g.rows, p.rows - row0);
-    uint8_t* y = smem + (k % g.count) * stage_bytes;
+    uint8_t* y = smem + (k % NR_STAGES) * stage_bytes;
     uint8_t* x = y + g.rows * g.y_bytes;
-    uint64_t* bar = &full[k % g.count];
+    uint64_t* bar = &full[k % NR_STAGES];
     mbar_expect_tx(bar, rows * (g.y_bytes + g.x_bytes));
     for (int r = 0; r < rows; ++r) {
       bulk_load(y + r * g.y_bytes, in + (row0 + r) * p.width, g.y_bytes, bar);
@@ -378,10 +379,10 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const _
     }
   };
   if (threadIdx.x == 0) {
-    for (int i = 0; i < g.count; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < NR_STAGES; ++i) mbar_init(&full[i], 1);
     abort_flag = 0;
     fence_mbar_init();
-    for (int k = 0; k < g.count; ++k) load(k);
+    for (int k = 0; k < NR_STAGES; ++k) load(k);
   }
   if (norm)
     for (int i = threadIdx.x; i < 2 * D; i += NR_THREADS)
@@ -400,16 +401,24 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const _
     const int64_t row0 = tile_of(k) * g.rows;
     const int rows = (int)min((int64_t)g.rows, p.rows - row0);
     if (p.rope) angle_table(p, row0, rows, HALF, cosines, sines);
-    ok = bounded_wait(&full[k % g.count], (k / g.count) & 1, &abort_flag, 960, err);
+    ok = bounded_wait(&full[k % NR_STAGES], (k / NR_STAGES) & 1, &abort_flag, 960, err);
     ok = __syncthreads_and(ok);
     if (!ok) break;
-    uint8_t* y = smem + (k % g.count) * stage_bytes;
+    uint8_t* y = smem + (k % NR_STAGES) * stage_bytes;
     const uint8_t* x = BWD ? y + g.rows * g.y_bytes : y;
     const int x_stride = BWD ? g.x_bytes : g.y_bytes;
 #pragma unroll 1
     for (int sec = 0; sec < 2; ++sec) {
       const int n = sec ? p.K : p.H, col0 = sec ? p.H * D : 0;
       const int pairs = rows * n;
+      // Between the sections the stage before this one has been stored, and
+      // its next tile still has half of this one's time to arrive (loaded at
+      // this tile's end: backward of 32 + 32 + 32 heads of 80 285 us, 249 so; a
+      // check inside the loop below costs more than a better moment gains).
+      if (sec == 1 && k > 0 && threadIdx.x == 0) {
+        bulk_wait_read0();
+        load(k - 1 + NR_STAGES);
+      }
       uint64_t wa[4], wb[4];
       if (norm && lane_on) {
         const float* w = weights + sec * D + 8 * idx;
@@ -451,16 +460,13 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const _
     if (threadIdx.x == 0) {
       for (int r = 0; r < rows; ++r) bulk_store(p.out + (row0 + r) * p.width, y + r * g.y_bytes, g.y_bytes);
       bulk_commit();
-      // the stage before this one has been stored: its next tile
-      bulk_wait_read1();
-      if (k > 0) load(k - 1 + g.count);
     }
   }
   if (threadIdx.x == 0) {
     bulk_wait0();
     if (!ok) {
       // loads in flight land before the shared memory goes
-      for (int i = 0; i < g.count; ++i) {
+      for (int i = 0; i < NR_STAGES; ++i) {
         drain_wait(&full[i], 0);
         drain_wait(&full[i], 1);
       }
@@ -512,24 +518,20 @@ int launch_staged(const NormRopeParams& p, const Stages& g, int blocks, int smem
   return cudaGetLastError() == cudaSuccess ? BPT_OK : BPT_ECUDA;
 }
 
-// The stages for rows of these sizes, two blocks per SM: forward three of up
-// to 36 KB, backward, whose rows are longer, two of up to 56 KB (smaller ones
-// leave warps without a head at every stage's end; 32768 rows of 32 + 32 heads
-// of 80: forward 192 us, 246 with two, 334 with three of 20 KB; backward 285 us,
-// 372 with two of 36 KB).  count 0: not even one row fits.
-Stages stages_for(const PackedDims& D, int want, int y_bytes, int x_bytes, int* smem) {
+// The stages for rows of these sizes, two blocks per SM: two of up to 56 KB.
+// Smaller ones leave warps without a head at every stage's end (forward, three
+// of 36 KB: 32768 rows of 32 + 32 + 32 heads of 80 189 us, 162 so; of 64 125 us,
+// 130 so); three blocks of two of 37 KB, 85 registers a thread, are no faster
+// where rows are long (heads of 128: 259 us, 244 so).
+Stages stages_for(const PackedDims& D, int y_bytes, int x_bytes, int* smem) {
   const int table = (int)(2 * D.d * 4);            // weights
   const int angles = (int)(D.d / 2 * 2 * 4);       // of one row
   const int row = y_bytes + x_bytes;
-  Stages g{0, 0, y_bytes, x_bytes};
-  const int rows = std::min((112 * 1024 - table) / (want * row + angles), std::max(1, (want == 3 ? 36 : 56) * 1024 / row));
-  if (rows >= 1) {
-    g.count = want;
-    g.rows = std::min(rows, NR_ROWS);
-  }
+  const int rows = std::min((112 * 1024 - table) / (NR_STAGES * row + angles), std::max(1, 56 * 1024 / row));
+  const Stages g{std::min(rows, NR_ROWS), y_bytes, x_bytes};
   // a block's weight gradient sums take the stages' place at the end
   const int sums = NR_WARPS * (32 / (int)(D.d / 16)) * (int)D.d * 4;
-  *smem = std::max(g.count * g.rows * row, sums) + g.rows * angles + table;
+  *smem = std::max(NR_STAGES * g.rows * row, sums) + g.rows * angles + table;
   return g;
 }
 
@@ -541,8 +543,8 @@ int launch(const NormRopeParams& p, const PackedDims& D, int* blocks, cudaStream
   const int heads = (int)((D.H + D.Hkv) * D.d * 2);
   const int y_bytes = p.copy_v ? (int)(D.width * 2) : heads, x_bytes = BWD && p.wq ? heads : 0;
   int smem = 0;
-  const Stages g = D.width * 2 <= 112 * 1024 ? stages_for(D, BWD ? 2 : 3, y_bytes, x_bytes, &smem) : Stages{0, 0, 0, 0};
-  const bool staged = g.count && D.rows >= (int64_t)nsm * 2 * g.rows * NR_STAGED_TILES;
+  const Stages g = D.width * 2 <= 112 * 1024 ? stages_for(D, y_bytes, x_bytes, &smem) : Stages{0, 0, 0};
+  const bool staged = g.rows && D.rows >= (int64_t)nsm * 2 * g.rows * NR_STAGED_TILES;
   const int hpw = 32 / (int)(D.d / 16);
   if (staged) {
     *blocks = nsm * 2;

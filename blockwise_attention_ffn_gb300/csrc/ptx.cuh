@@ -132,10 +132,6 @@ __device__ __forceinline__ void bulk_store(void* gdst, const void* ssrc, uint32_
                "r"(smem_u32(ssrc)), "r"(bytes)
                : "memory");
 }
-// all but the thread's newest bulk group have been read from shared memory
-__device__ __forceinline__ void bulk_wait_read1() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
 // Makes this thread's generic-proxy shared-memory writes visible to the async
 // proxy (tensor core and TMA reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {
