@@ -21,9 +21,8 @@
 //
 // Two forms.  With rows for every SM several times over, blocks stream tiles
 // of whole rows through shared memory by bulk copies (32768 rows of 32 + 32 + 32
-// heads of 64: 130 us, 92% of a copy's bandwidth; of 80: 162 us, backward 249 us;
-// 65536 rows of 32 + 8 + 8 heads of 128: 290 us, where the arithmetic of four heads
-// a warp holds it at 82%).  Fewer rows are read straight into registers, their
+// heads of 64: 135 us, 89% of a copy's bandwidth; of 80: 153 us, 96%, backward 233 us;
+// 65536 rows of 32 + 8 + 8 heads of 128: 258 us, 91%, backward 409 us).  Fewer rows are read straight into registers, their
 // heads spread over all warps (40 heads of 8 rows: one step of 80 warps).
 //
 // Angles: p * theta in turns, as a 64-bit fraction of a turn.  The product of
@@ -169,12 +168,14 @@ __device__ __forceinline__ void head_math(uint4 va, uint4 vb, uint4 ya, uint4 yb
     }
   }
 }
-// sines and cosines of `rows` rows from row0
-__device__ __forceinline__ void angle_table(const NormRopeParams& p, int64_t row0, int rows, int half, float* cosines,
-                                            float* sines) {
+// sines and cosines of `rows` rows from row0, the first one's index in its
+// sequence being index0
+__device__ __forceinline__ void angle_table(const NormRopeParams& p, int64_t row0, int index0, int rows, int half,
+                                            float* cosines, float* sines) {
   for (int u = threadIdx.x; u < rows * half; u += blockDim.x) {
-    const int64_t row = row0 + u / half;
-    const int64_t pos = p.pos ? (int64_t)p.pos[row] : row % p.s;
+    const int r = u / half;
+    const uint32_t index = (uint32_t)index0 + r;
+    const int64_t pos = p.pos ? (int64_t)p.pos[row0 + r] : index < (uint32_t)p.s ? index : index % (uint32_t)p.s;
     const uint64_t turn = (uint64_t)pos * p.turn[u % half];
     sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sines[u], &cosines[u]);
   }
@@ -263,7 +264,7 @@ __device__ __forceinline__ void section(const NormRopeParams& p, int n, int col0
     fetch();
     if (p.rope) {
       __syncthreads();  // the tile before has been read
-      angle_table(p, row0, rows, HALF, cosines, sines);
+      angle_table(p, row0, (int)(row0 % p.s), rows, HALF, cosines, sines);
       __syncthreads();
     }
     // a warp's slots step together: the shuffles take all its lanes
@@ -346,6 +347,7 @@ constexpr int NR_STAGES = 2;
 struct Stages {
   int rows;                  // rows of a stage; 0: not even one fits
   int y_bytes, x_bytes;      // of a row: of dy (x forward), and backward of x
+  uint32_t part_q, part_k;   // ceil(2^22 / heads): f * part >> 22 = f / heads, as f * heads < 2^22
 };
 template <int L, bool BWD>
 __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const __grid_constant__ NormRopeParams p,
@@ -397,10 +399,15 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const _
     sn[i] = 0ull;
   }
   bool ok = true;
+  // a tile's first row's index in its sequence
+  uint32_t index0 = (uint32_t)((int64_t)blockIdx.x * g.rows % p.s);
+  const uint32_t index_step = (uint32_t)((int64_t)gridDim.x * g.rows % p.s);
   for (int k = 0; tile_of(k) < tiles; ++k) {
     const int64_t row0 = tile_of(k) * g.rows;
     const int rows = (int)min((int64_t)g.rows, p.rows - row0);
-    if (p.rope) angle_table(p, row0, rows, HALF, cosines, sines);
+    if (p.rope) angle_table(p, row0, index0, rows, HALF, cosines, sines);
+    index0 += index_step;
+    if (index0 >= (uint32_t)p.s) index0 -= p.s;
     ok = bounded_wait(&full[k % NR_STAGES], (k / NR_STAGES) & 1, &abort_flag, 960, err);
     ok = __syncthreads_and(ok);
     if (!ok) break;
@@ -433,7 +440,7 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const _
       for (int f0 = first * HPW; f0 < pairs; f0 += NR_WARPS * HPW) {
         const int f = f0 + slot;
         const bool on = lane_on && f < pairs;
-        const int row = on ? f / n : 0, head = on ? f - row * n : 0;
+        const int row = on ? (int)((uint32_t)f * (sec ? g.part_k : g.part_q) >> 22) : 0, head = on ? f - row * n : 0;
         const int at = (col0 + head * D + 8 * idx) * 2;
         uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va, ya = va, yb = va;
         if (on && (!BWD || norm)) {
@@ -528,7 +535,9 @@ Stages stages_for(const PackedDims& D, int y_bytes, int x_bytes, int* smem) {
   const int angles = (int)(D.d / 2 * 2 * 4);       // of one row
   const int row = y_bytes + x_bytes;
   const int rows = std::min((112 * 1024 - table) / (NR_STAGES * row + angles), std::max(1, 56 * 1024 / row));
-  const Stages g{std::min(rows, NR_ROWS), y_bytes, x_bytes};
+  const auto part = [](int64_t n) { return (uint32_t)(((1 << 22) + n - 1) / n); };
+  // (a tile has fewer than 1024 heads of either kind, and f * part stays below 2^32)
+  const Stages g{std::min(rows, NR_ROWS), y_bytes, x_bytes, part(D.H), part(D.Hkv)};
   // a block's weight gradient sums take the stages' place at the end
   const int sums = NR_WARPS * (32 / (int)(D.d / 16)) * (int)D.d * 4;
   *smem = std::max(NR_STAGES * g.rows * row, sums) + g.rows * angles + table;
@@ -543,7 +552,7 @@ int launch(const NormRopeParams& p, const PackedDims& D, int* blocks, cudaStream
   const int heads = (int)((D.H + D.Hkv) * D.d * 2);
   const int y_bytes = p.copy_v ? (int)(D.width * 2) : heads, x_bytes = BWD && p.wq ? heads : 0;
   int smem = 0;
-  const Stages g = D.width * 2 <= 112 * 1024 ? stages_for(D, y_bytes, x_bytes, &smem) : Stages{0, 0, 0};
+  const Stages g = D.width * 2 <= 112 * 1024 ? stages_for(D, y_bytes, x_bytes, &smem) : Stages{0, 0, 0, 0, 0};
   const bool staged = g.rows && D.rows >= (int64_t)nsm * 2 * g.rows * NR_STAGED_TILES;
   const int hpw = 32 / (int)(D.d / 16);
   if (staged) {

@@ -186,6 +186,34 @@ def test_norm_rope_many_rows(H, K, d, in_place):
             assert bool(((got.double() - part.sum((0, 1))).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("b,s,H,K,d", [(23, 1291, 2, 1, 64), (5000, 7, 2, 1, 64), (30001, 1, 1, 1, 80), (9, 555, 32, 8, 128),
+                                       (7, 901, 12, 12, 96), (2, 30011, 1, 1, 112)])
+def test_norm_rope_rows_of_many_sequences(b, s, H, K, d):
+    """Without positions a row's is its index in its sequence, whatever part of
+    how many sequences a block takes at once (bitwise the call with them)."""
+    cfg = cfg_of(b, s, H, K, d, rope_base=10000.0)
+    g = torch.Generator(device="cuda").manual_seed(b)
+    x, dy = (torch.randn(b * s, (H + 2 * K) * d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    w = [(1 + 0.1 * torch.randn(d, generator=g, device="cuda")).to(torch.bfloat16) for _ in range(2)]
+    ws = bpt.alloc_bytes(bpt.bpt_qk_norm_rope_workspace_bytes(cfg))
+    got = []
+    for pos in (None, (torch.arange(b * s, device="cuda") % s).to(torch.int32)):
+        out, dx, dw = torch.empty_like(x), torch.empty_like(x), [torch.empty(d, device="cuda") for _ in range(2)]
+        bpt.bpt_qk_norm_rope_fwd(cfg, x, *w, pos, out)
+        bpt.bpt_qk_norm_rope_bwd(cfg, x, *w, pos, dy, dx, *dw, ws)
+        sync()
+        got.append([out, dx, *dw])
+    for a, c in zip(*got):
+        assert torch.equal(a, c)
+    # and the first row of the last sequences against a call on one row each
+    one = cfg.with_(b=3, s=1)
+    rows = torch.arange(b - min(b, 3), b, device="cuda") * s
+    part = torch.empty_like(x[:3])
+    bpt.bpt_qk_norm_rope_fwd(one.with_(b=len(rows)), x[rows], *w, None, part[:len(rows)])
+    sync()
+    assert torch.equal(part[:len(rows)], got[0][0][rows])
+
+
 def test_norm_rope_refusals():
     cfg = cfg_of(1, 8, 2, 1, 64, rope_base=10000.0)
     x = torch.zeros(8, 256, dtype=torch.bfloat16, device="cuda")
