@@ -126,10 +126,13 @@ struct WorkQueue {
 // The scheduling warp: publishes describe(block) for this CTA's block and then
 // for the blocks it takes over, the next one asked for when every warp has
 // begun the current one and the loading warp is through with it: a CTA that
-// took an item earlier would hold it back from the others.  Returns whether `last` was among them.
-template <class Describe>
-__device__ __forceinline__ bool publish_items(const WorkQueue& q, int block, int last, volatile int* abort_flag,
-                                              unsigned int* err, Describe describe) {
+// took an item earlier would hold it back from the others (more = false: no
+// further one is asked for).  published(it, item) follows each.  Returns whether
+// `last` was among them.
+template <class Describe, class Published>
+__device__ __forceinline__ bool publish_items(const WorkQueue& q, int block, int last, bool more,
+                                              volatile int* abort_flag, unsigned int* err, Describe describe,
+                                              Published published) {
   const int lane = lane_id();
   bool asked = false, took_last = false;
   int it = 0;
@@ -152,15 +155,19 @@ __device__ __forceinline__ bool publish_items(const WorkQueue& q, int block, int
       to->nkv = w.nkv;
       mbar_arrive(&q.full[it & 1]);
     }
+    if (!published(it, w)) break;
     if (!bounded_wait_w(&q.empty[it & 1], (it >> 1) & 1, abort_flag, 252, err)) break;
-    uint8_t* answer = q.mem + 16 * (it & 1);
-    if (lane == 0) request_block(answer, q.answered);
-    asked = true;
-    if (!bounded_wait_w(q.answered, it & 1, abort_flag, 257, err)) break;
-    asked = false;
-    block = answered_block(answer);
-    fence_proxy_async_smem();
-    __syncwarp();
+    block = -1;
+    if (more) {
+      uint8_t* answer = q.mem + 16 * (it & 1);
+      if (lane == 0) request_block(answer, q.answered);
+      asked = true;
+      if (!bounded_wait_w(q.answered, it & 1, abort_flag, 257, err)) break;
+      asked = false;
+      block = answered_block(answer);
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
     ++it;
   }
   // a request in flight lands before the shared memory goes

@@ -141,9 +141,10 @@ __device__ __forceinline__ void mask_gradient(uint32_t (&dr)[64], const float (&
 // ===========================================================================
 // dK / dV
 // ===========================================================================
-// Shared memory of dK/dV: (d > 80) K, V and their extra chunks; the stages of
-// Q, dO, the 128 queries' 16-byte extra rows, their windows and (with a cap)
-// -LSE log2(e); then zeros, the upper half of the extra contraction step.
+// Shared memory of dK/dV: K and V, (d > 80) their extra chunks; dK and dV on
+// their way out, for d > 80 in K's and V's place; the stages of Q, dO, the 128
+// queries' 16-byte extra rows, their windows and (with a cap) -LSE log2(e); then
+// zeros, the upper half of the extra contraction step.
 // TMEM: S^T [0, 128) and dP^T [128, 256) as two 64-column buffers each, dV at
 // 256, dK at 256 + D, and for d <= 80 K and V with their extra chunks.
 template <int D>
@@ -151,15 +152,17 @@ struct ModDkdvCfg {
   using T = TileGeom<D>;
   static constexpr bool KV_TMEM = D <= 80;
   static constexpr int AUX = 128 * 16;                 // 128 rows x 8 bf16
-  static constexpr int KV = KV_TMEM ? 0 : 2 * T::TILE + 2 * AUX;  // K, V, K extra, V extra
+  static constexpr int KV = 2 * T::TILE + (KV_TMEM ? 2 * T::TILE : 2 * AUX);  // K, V, then results or extra chunks
+  static constexpr int OUT = KV_TMEM ? 2 * T::TILE : 0;
+  static constexpr int CTL = 512;
   static constexpr int REC = 2 * T::TILE + AUX;        // offset of the windows
   static constexpr int NL2 = REC + (int)sizeof(WinRecord);
   static constexpr int STAGE = REC + 2048;             // 1024-byte aligned tiles
   static_assert(sizeof(WinRecord) + 128 * 4 <= 2048, "the stage's tail");
   static constexpr int ZERO = 2048;                    // the upper 8 columns
-  static constexpr int QS_FIT = (232448 - KV - ZERO - 1024 - 256) / STAGE;
+  static constexpr int QS_FIT = (232448 - KV - ZERO - CTL) / STAGE;
   static constexpr int QS = QS_FIT > 4 ? 4 : QS_FIT;
-  static constexpr int SMEM = KV + QS * STAGE + ZERO + 1024 + 256;
+  static constexpr int SMEM = KV + QS * STAGE + ZERO + CTL;
   static constexpr uint32_t COL_DV = 256, COL_DK = 256 + D, COL_K = 256 + 2 * D, COL_V = 256 + 2 * D + D / 2 + 8;
 };
 
@@ -172,6 +175,8 @@ struct ModDkdvCfg {
 // same thread.  P^T is written over S^T and dS^T over dP^T as bf16 pairs, the
 // A operands of dV = P^T dO and dK = dS^T Q.  Both issuers add into dV and dK,
 // which the compute warps zero first.
+// Persistent like the forward: warp 11 takes the items and loads their K and V,
+// warp 0 the stages.
 //
 // Few key tiles (short sequences, few key/value heads) leave SMs idle, or the
 // last round of CTAs a poor fill.  Then a cluster of CTAs shares one item: each
@@ -179,7 +184,7 @@ struct ModDkdvCfg {
 // dK as fp32 in its own shared memory, and sums a share of the rows of all of
 // them in rank order through distributed shared memory.
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_constant__ ModBwdParams p) {
+__global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_constant__ ModBwdParams p) {
   using T = TileGeom<D>;
   using C = ModDkdvCfg<D>;
   constexpr int QS = C::QS;
@@ -190,60 +195,66 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   constexpr uint32_t ID_S = idesc_bf16(128, 64, false, false);
   constexpr uint32_t ID_KV = idesc_bf16(128, D, false, true);
 
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  static_assert((2 * QS + 19) * 8 + WORK_BYTES + 8 <= C::CTL, "control block");
+  // the tiles' swizzle needs 1024-byte alignment, which the declaration gives
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sKV = smem;                  // K, V, their extra chunks (head dims above 80)
+  uint8_t* sOut = smem + C::OUT;        // dV, dK
   uint8_t* sStage = smem + C::KV;
   uint8_t* sZero = sStage + QS * STAGE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sZero + C::ZERO);
-  uint64_t* kv_ready = bars;            // K', V' in place, dV, dK zeroed (8 compute warps)
-  uint64_t* qdo_full = bars + 1;        // [QS]
+  uint8_t* control = sZero + C::ZERO;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(control + WORK_BYTES);
+  // (read by 8 compute warps, 2 issuers, the loads)
+  const WorkQueue queue{control, bars, bars + 2, bars + 4};
+  uint64_t* kv_full = bars + 5;         // K, V landed, of every item
+  uint64_t* kv_free = bars + 6;         // and their place free again (8 compute warps)
+  uint64_t* kv_ready = bars + 7;        // K', V' in place, dV, dK zeroed (8 compute warps), of items with pairs
+  uint64_t* all_done = bars + 8;        // both issuers' last products of an item with pairs done
+  uint64_t* s_full = bars + 9;          // [2] S^T(u) in buffer u % 2
+  uint64_t* dp_full = bars + 11;        // [2]
+  uint64_t* p_full = bars + 13;         // [2] P^T(u) written (4 warps of the group)
+  uint64_t* ds_full = bars + 15;        // [2] dS^T(u) written (4 warps)
+  uint64_t* drain = bars + 17;          // [2], one per issuer
+  uint64_t* qdo_full = bars + 19;       // [QS]
   uint64_t* qdo_empty = qdo_full + QS;  // [QS], both issuers
-  uint64_t* s_full = qdo_empty + QS;    // [2] S^T(u) in buffer u % 2
-  uint64_t* dp_full = s_full + 2;       // [2]
-  uint64_t* p_full = dp_full + 2;       // [2] P^T(u) written (4 warps of the group)
-  uint64_t* ds_full = p_full + 2;       // [2] dS^T(u) written (4 warps)
-  uint64_t* all_done = ds_full + 2;     // both issuers' last products done
-  uint64_t* drain = all_done + 1;       // [2], one per issuer
-  uint64_t* kv_full = drain + 2;        // K, V tiles landed
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(kv_full + 1);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(qdo_empty + QS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* range = reinterpret_cast<int*>(tmem_holder + 2);  // first and last query tile that sees the key tile
 
   const int warp = warp_id();
   const int lane = lane_id();
-  // the first (with a causal mask heaviest) key tiles first
+  // the first (with a causal mask heaviest) key tiles first; a cluster's item
+  // is its only one
   const int split = (int)cluster_size(), rank = (int)cluster_rank();
-  const Item item = item_of(p.order_kv, blockIdx.x / split);
   const int nq_total = p.n_t;
-  const int j = item.tile;
-  const int g = item.kv % p.Hkv;
-  const int bi = item.kv / p.Hkv;
+  auto part = [&](int pairs, int r) { return (int)((long long)pairs * r / split); };
 
   if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(kv_free, 8);
     mbar_init(kv_ready, 8);
+    mbar_init(all_done, 2);
+    mbar_init(queue.answered, 1);
     for (int i = 0; i < QS; ++i) {
       mbar_init(&qdo_full[i], 1);
       mbar_init(&qdo_empty[i], 2);
     }
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&queue.full[b], 1);
+      mbar_init(&queue.empty[b], 11);
       mbar_init(&s_full[b], 1);
       mbar_init(&dp_full[b], 1);
       mbar_init(&p_full[b], 4);
       mbar_init(&ds_full[b], 4);
       mbar_init(&drain[b], 1);
     }
-    mbar_init(all_done, 2);
-    mbar_init(kv_full, 1);
     *abort_flag = 0;
-    range[0] = INT32_MAX;
-    range[1] = -1;
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch(&p.map_qkv);
     tma_prefetch(&p.map_do);
     tma_prefetch(&p.map_aux);
+    tma_prefetch(&p.map_out);
   }
   if (warp == 1) {
     tmem_alloc(tmem_holder, 512);
@@ -257,47 +268,24 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  if (warp == 0 && lane == 0) {
-    // K and V, of which the preparation writes nothing: to stay (d > 80), or in
-    // the last stage until the compute warps have copied them to TMEM
-    uint8_t* kv = C::KV_TMEM ? sStage + (QS - 1) * STAGE : sKV;
+  auto load_kv = [&](int g, int bi, int j) {
+    if (lane != 0) return;
     mbar_expect_tx(kv_full, 2 * T::TILE);
 #pragma unroll
     for (int c = 0; c < T::NCH; ++c) {
-      tma_load_3d(kv + c * T::CHUNK, &p.map_qkv, kv_full, p.k_col + g * D + c * T::CW, j * 128, bi);
-      tma_load_3d(kv + T::TILE + c * T::CHUNK, &p.map_qkv, kv_full, p.v_col + g * D + c * T::CW, j * 128, bi);
+      tma_load_3d(sKV + c * T::CHUNK, &p.map_qkv, kv_full, p.k_col + g * D + c * T::CW, j * 128, bi);
+      tma_load_3d(sKV + T::TILE + c * T::CHUNK, &p.map_qkv, kv_full, p.v_col + g * D + c * T::CW, j * 128, bi);
     }
+  };
+  if (warp == 11) {
+    // the first K and V, of which the preparation writes nothing
+    const Item item = item_of(p.order_kv, blockIdx.x / split);
+    load_kv(item.kv % p.Hkv, item.kv / p.Hkv, item.tile);
   }
   // what the preparation wrote; the dQ kernel, which needs nothing of this
   // one, fills the SMs that this one's last round leaves idle
   wait_for_previous();
   let_next_start();
-  {
-    // query tiles with a row that may see this key tile; tiles between the
-    // first and the last that see nothing of it are masked like any other
-    int first = INT32_MAX, last = -1;
-    for (int i = threadIdx.x; i < nq_total; i += blockDim.x) {
-      const int2 w = p.span[(long long)bi * nq_total + i];
-      if (w.x < (j + 1) * 128 && w.y > j * 128) {
-        first = min(first, i);
-        last = max(last, i);
-      }
-    }
-    first = __reduce_min_sync(0xffffffffu, first);
-    last = __reduce_max_sync(0xffffffffu, last);
-    if (lane == 0 && last >= 0) {
-      atomicMin(&range[0], first);
-      atomicMax(&range[1], last);
-    }
-    __syncthreads();
-  }
-  const int i0 = range[0];
-  const int n_i = range[1] < 0 ? 0 : range[1] - i0 + 1;
-  const int T_all = p.G * n_i;   // (query head, query tile) pairs of the item
-  auto part = [&](int r) { return (int)((long long)T_all * r / split); };
-  const int t0 = part(rank);
-  const int T_iter = part(rank + 1) - t0;  // stages: this CTA's pairs, from t0
-  const int U = 2 * T_iter;                // sub-tiles
   const uint32_t tS = tmem;          // + 64 b
   const uint32_t tdP = tmem + 128;   // + 64 b
   const uint32_t tdV = tmem + C::COL_DV;
@@ -305,319 +293,372 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
   const uint32_t tKA = tmem + C::COL_K;
   const uint32_t tVA = tmem + C::COL_V;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------ TMA producer
-      int issued = 0;
-      for (int t = 0; t < T_iter; ++t) {
-        const int st = t % QS;
-        if (t >= QS && !bounded_wait(&qdo_empty[st], ((t / QS) & 1) ^ 1, abort_flag, 701, p.err)) break;
-        if (C::KV_TMEM && t == QS - 1 && !bounded_wait(kv_ready, 0, abort_flag, 702, p.err)) break;
-        const int hn = g * p.G + (t0 + t) / n_i;
-        const int i = i0 + (t0 + t) % n_i;
-        uint8_t* sQ = sStage + st * STAGE;
-        uint8_t* sdO = sQ + T::TILE;
-        mbar_expect_tx(&qdo_full[st], C::REC + (int)sizeof(WinRecord) + (CAP ? 512 : 0));
-#pragma unroll
-        for (int c = 0; c < T::NCH; ++c) {
-          tma_load_3d(sQ + c * T::CHUNK, &p.map_qkv, &qdo_full[st], hn * D + c * T::CW, i * 128, bi);
-          tma_load_3d(sdO + c * T::CHUNK, &p.map_do, &qdo_full[st], hn * D + c * T::CW, i * 128, bi);
+  // a published item: key/value head n, sequence bi, key tile q0, and the query
+  // tiles [j0, j0 + nkv) with a row that may see it
+  if (warp == 11) {
+    // ------------------------------------------------ items, K and V (the whole warp)
+    int loads = 1;
+    publish_items(queue, blockIdx.x / split, -1, split == 1, abort_flag, p.err, [&](int block) {
+      const Item item = item_of(p.order_kv, block);
+      const int bi = item.kv / p.Hkv, j = item.tile;
+      // tiles between the first and the last that see nothing of it are masked
+      // like any other
+      int first = INT32_MAX, last = -1;
+#pragma unroll 4
+      for (int i = lane; i < nq_total; i += 32) {
+        const int2 w = p.span[(long long)bi * nq_total + i];
+        if (w.x < (j + 1) * 128 && w.y > j * 128) {
+          first = min(first, i);
+          last = max(last, i);
         }
-        const int row = (bi * p.H + hn) * p.s_pad + i * 128;
-        tma_load_2d(sQ + 2 * T::TILE, &p.map_aux, &qdo_full[st], 0, row);
-        bulk_load(sQ + C::REC, p.rec + (long long)bi * nq_total + i, sizeof(WinRecord), &qdo_full[st]);
-        if constexpr (CAP) bulk_load(sQ + C::NL2, p.nl2 + row, 512, &qdo_full[st]);
-        issued = t + 1;
       }
-      // every copy lands before the shared memory goes, also when a wait
-      // elsewhere in the block gives up later
-      drain_wait(kv_full, 0);
-      for (int t = (issued > QS ? issued - QS : 0); t < issued; ++t)
-        drain_wait(&qdo_full[t % QS], (t / QS) & 1);
+      first = __reduce_min_sync(0xffffffffu, first);
+      last = __reduce_max_sync(0xffffffffu, last);
+      return WorkItem{item.kv % p.Hkv, bi, j, first, last < 0 ? 0 : last - first + 1};
+    }, [&](int it, const WorkItem& w) {
+      if (it == 0) return true;
+      if (!bounded_wait_w(kv_free, (it - 1) & 1, abort_flag, 702, p.err)) return false;
+      load_kv(w.n, w.bi, w.q0);
+      loads = it + 1;
+      return true;
+    });
+    // every copy lands before the shared memory goes
+    drain_wait(kv_full, (loads - 1) & 1);
+  } else if (warp == 0) {
+    // ------------------------------------------------ Q/dO stages (the whole
+    // warp runs the loop, one lane issues)
+    int c = 0;  // stages loaded
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      WorkItem w;
+      if (!next_item<true>(queue, it, &w, abort_flag, p.err) || w.n < 0) break;
+      const int pairs = p.G * w.nkv, t1 = part(pairs, rank + 1);
+      for (int t = part(pairs, rank); t < t1; ++t, ++c) {
+        const int st = c % QS;
+        ok = c < QS || bounded_wait_w(&qdo_empty[st], ((c / QS) & 1) ^ 1, abort_flag, 701, p.err);
+        if (!ok) break;
+        if (lane == 0) {
+          const int hn = w.n * p.G + t / w.nkv, i = w.j0 + t % w.nkv, bi = w.bi;
+          uint8_t* sQ = sStage + st * STAGE;
+          uint8_t* sdO = sQ + T::TILE;
+          mbar_expect_tx(&qdo_full[st], C::REC + (int)sizeof(WinRecord) + (CAP ? 512 : 0));
+#pragma unroll
+          for (int k = 0; k < T::NCH; ++k) {
+            tma_load_3d(sQ + k * T::CHUNK, &p.map_qkv, &qdo_full[st], hn * D + k * T::CW, i * 128, bi);
+            tma_load_3d(sdO + k * T::CHUNK, &p.map_do, &qdo_full[st], hn * D + k * T::CW, i * 128, bi);
+          }
+          const int row = (bi * p.H + hn) * p.s_pad + i * 128;
+          tma_load_2d(sQ + 2 * T::TILE, &p.map_aux, &qdo_full[st], 0, row);
+          bulk_load(sQ + C::REC, p.rec + (long long)bi * nq_total + i, sizeof(WinRecord), &qdo_full[st]);
+          if constexpr (CAP) bulk_load(sQ + C::NL2, p.nl2 + row, 512, &qdo_full[st]);
+        }
+        __syncwarp();
+      }
+      if (ok) release_item(queue, it);
     }
+    // every copy lands before the shared memory goes, also when a wait
+    // elsewhere in the block gives up later
+    for (int k = (c > QS ? c - QS : 0); k < c; ++k) drain_wait(&qdo_full[k % QS], (k / QS) & 1);
   } else if (warp == 1 || warp == 10) {
     // the whole warp runs the issue loop, one elected lane issues.  One
     // issuer (fixed-order mode): warp 1 issues every sub-tile's products
-    // in sub-tile order, so dV and dK take their products in a fixed order
-    if (U > 0 && !(p.one_issuer && warp == 10)) {
-      // ------------------------------------------------ MMA issuers
-      const int b0 = warp == 1 ? 0 : 1;  // this issuer's first sub-tile
-      const int ustep = p.one_issuer ? 1 : 2;
-      const uint32_t uZero = smem_u32(sZero);
-      // the 64 query rows of sub-tile half b start 64 b rows into every
-      // chunk of the stage's tiles (whole swizzle atoms), and 64 b rows into
-      // its extra rows; sub-tile u uses buffer b = u % 2
-      auto stage_u = [&](int u) { return smem_u32(sStage + ((u >> 1) % QS) * STAGE); };
-      // K, V and their extra chunks in shared memory (head dims above 80):
-      // the extra chunk is 128 rows of 16 bytes, K-major core matrices
-      // without swizzle, its upper 8 columns the zeros
-      const uint32_t uK = smem_u32(sKV), uV = uK + T::TILE;
-      const uint32_t uKx = uK + 2 * T::TILE, uVx = uKx + C::AUX;
-      const uint64_t dK = T::kmajor(uK, 0), dV = T::kmajor(uV, 0);
-      const uint64_t dKx = sdesc(uKx, uZero - uKx, 128, 0u), dVx = sdesc(uVx, uZero - uVx, 128, 0u);
-      auto issue_s = [&](int u) {
-        const int b = u & 1;
-        const uint32_t tSb = tS + 64 * b;
-        const uint64_t q = T::kmajor(stage_u(u) + 64 * T::SWB * b, 0);
-        const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
-        if constexpr (C::KV_TMEM) {
+    // in sub-tile order, so dV and dK take their products in a fixed order,
+    // and warp 10 only reads the items
+    // ------------------------------------------------ MMA issuers
+    const bool issues = !(p.one_issuer && warp == 10);
+    const int b0 = warp == 1 ? 0 : 1;  // this issuer's first sub-tile
+    const int ustep = p.one_issuer ? 1 : 2;
+    const uint32_t uZero = smem_u32(sZero);
+    int tg = 0, ki = 0;  // stages, items with pairs before this one
+    bool ok = true;
+    // the 64 query rows of sub-tile half b start 64 b rows into every
+    // chunk of the stage's tiles (whole swizzle atoms), and 64 b rows into
+    // its extra rows; sub-tile u uses buffer b = u % 2
+    auto stage_u = [&](int u) { return smem_u32(sStage + ((tg + (u >> 1)) % QS) * STAGE); };
+    // K, V and their extra chunks in shared memory (head dims above 80):
+    // the extra chunk is 128 rows of 16 bytes, K-major core matrices
+    // without swizzle, its upper 8 columns the zeros
+    const uint32_t uK = smem_u32(sKV), uV = uK + T::TILE;
+    const uint32_t uKx = uK + 2 * T::TILE, uVx = uKx + C::AUX;
+    const uint64_t dK = T::kmajor(uK, 0), dV = T::kmajor(uV, 0);
+    const uint64_t dKx = sdesc(uKx, uZero - uKx, 128, 0u), dVx = sdesc(uVx, uZero - uVx, 128, 0u);
+    auto issue_s = [&](int u) {
+      const int b = u & 1;
+      const uint32_t tSb = tS + 64 * b;
+      const uint64_t q = T::kmajor(stage_u(u) + 64 * T::SWB * b, 0);
+      const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
+      if constexpr (C::KV_TMEM) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_tmem_a_w(tSb, tKA + kk * 8, q + T::kmajor_step(kk), ID_S, kk > 0);
-          umma_bf16_tmem_a_w(tSb, tKA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
-        } else {
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_tmem_a_w(tSb, tKA + kk * 8, q + T::kmajor_step(kk), ID_S, kk > 0);
+        umma_bf16_tmem_a_w(tSb, tKA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+      } else {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_w(tSb, dK + T::kmajor_step(kk), q + T::kmajor_step(kk), ID_S, kk > 0);
-          umma_bf16_w(tSb, dKx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
-        }
-        umma_commit_w(&s_full[b]);
-      };
-      auto issue_dp = [&](int u) {
-        const int b = u & 1;
-        const uint32_t tdPb = tdP + 64 * b;
-        const uint64_t o = T::kmajor(stage_u(u) + T::TILE + 64 * T::SWB * b, 0);
-        const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
-        if constexpr (C::KV_TMEM) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_tmem_a_w(tdPb, tVA + kk * 8, o + T::kmajor_step(kk), ID_S, kk > 0);
-          umma_bf16_tmem_a_w(tdPb, tVA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16_w(tdPb, dV + T::kmajor_step(kk), o + T::kmajor_step(kk), ID_S, kk > 0);
-          umma_bf16_w(tdPb, dVx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
-        }
-        umma_commit_w(&dp_full[b]);
-      };
-      auto wait_stage = [&](int u) {
-        const int t = u >> 1;
-        return bounded_wait_w(&qdo_full[t % QS], (t / QS) & 1, abort_flag, 711, p.err);
-      };
-      bool ok = bounded_wait_w(kv_ready, 0, abort_flag, 712, p.err) &&
-                (C::KV_TMEM || bounded_wait_w(kv_full, 0, abort_flag, 716, p.err)) && wait_stage(b0);
-      if (ok) {
-        tc_fence_after();
-        // sub-tiles 0 and 1 share stage 0 (U is even)
-        for (int u = b0; u < 2; u += ustep) {
-          issue_s(u);
-          issue_dp(u);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_w(tSb, dK + T::kmajor_step(kk), q + T::kmajor_step(kk), ID_S, kk > 0);
+        umma_bf16_w(tSb, dKx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
       }
-      for (int u = b0; ok && u < U; u += ustep) {
+      umma_commit_w(&s_full[b]);
+    };
+    auto issue_dp = [&](int u) {
+      const int b = u & 1;
+      const uint32_t tdPb = tdP + 64 * b;
+      const uint64_t o = T::kmajor(stage_u(u) + T::TILE + 64 * T::SWB * b, 0);
+      const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
+      if constexpr (C::KV_TMEM) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_tmem_a_w(tdPb, tVA + kk * 8, o + T::kmajor_step(kk), ID_S, kk > 0);
+        umma_bf16_tmem_a_w(tdPb, tVA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_bf16_w(tdPb, dV + T::kmajor_step(kk), o + T::kmajor_step(kk), ID_S, kk > 0);
+        umma_bf16_w(tdPb, dVx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+      }
+      umma_commit_w(&dp_full[b]);
+    };
+    auto wait_stage = [&](int u) {
+      const int t = tg + (u >> 1);
+      return bounded_wait_w(&qdo_full[t % QS], (t / QS) & 1, abort_flag, 711, p.err);
+    };
+    for (int it = 0; ok; ++it) {
+      WorkItem w;
+      if (!next_item(queue, it, &w, abort_flag, p.err)) { ok = false; break; }
+      if (w.n < 0) break;
+      const int pairs = p.G * w.nkv, T_iter = part(pairs, rank + 1) - part(pairs, rank), U = 2 * T_iter;
+      if (U == 0 || !issues) continue;
+      ok = bounded_wait_w(kv_ready, ki & 1, abort_flag, 712, p.err) &&
+           (C::KV_TMEM || bounded_wait_w(kv_full, it & 1, abort_flag, 716, p.err)) && wait_stage(b0);
+      if (!ok) break;
+      tc_fence_after();
+      // sub-tiles 0 and 1 share the first stage (U is even)
+      for (int u = b0; u < 2; u += ustep) {
+        issue_s(u);
+        issue_dp(u);
+      }
+      for (int u = b0; u < U; u += ustep) {
         const int b = u & 1;
+        const uint32_t phase = (tg + (u >> 1)) & 1;
         const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
-        const int st = (u >> 1) % QS;
         const uint64_t dQm = T::mnmajor(stage_u(u), 4 * b), dOm = T::mnmajor(stage_u(u) + T::TILE, 4 * b);
         const bool more = u + 2 < U;
         // dV += P^T(u) dO(u): the P^T pairs sit over the first 32 columns of
         // buffer b; dO rows 64b.. are K blocks 4b..4b+3 of the stage's tile
-        if (!bounded_wait_w(&p_full[b], (u >> 1) & 1, abort_flag, 713, p.err)) { ok = false; break; }
+        ok = bounded_wait_w(&p_full[b], phase, abort_flag, 713, p.err);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16_tmem_a_w(tdV, tSb + kk * 8, dOm + T::mnmajor_step(kk), ID_KV, 1);
         if (more) {
           // S(u+2) overwrites P^T(u), after dV(u) in issue order
-          if (!wait_stage(u + 2)) { ok = false; break; }
+          ok = wait_stage(u + 2);
+          if (!ok) break;
           tc_fence_after();
           issue_s(u + 2);
         }
         // dK += dS^T(u) Q(u)
-        if (!bounded_wait_w(&ds_full[b], (u >> 1) & 1, abort_flag, 714, p.err)) { ok = false; break; }
+        ok = bounded_wait_w(&ds_full[b], phase, abort_flag, 714, p.err);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16_tmem_a_w(tdK, tdPb + kk * 8, dQm + T::mnmajor_step(kk), ID_KV, 1);
-        umma_commit_w(&qdo_empty[st]);
+        umma_commit_w(&qdo_empty[(tg + (u >> 1)) % QS]);
         // dP(u+2) overwrites dS^T(u), after dK(u) in issue order
         if (more) issue_dp(u + 2);
       }
-      if (ok) {
-        // all_done counts two commits: one per issuer, or both from one
-        umma_commit_w(all_done);
-        if (p.one_issuer) umma_commit_w(all_done);
-      }
-      if (!ok) {
-        umma_commit_w(&drain[b0]);
-        drain_wait(&drain[b0], 0);
-      }
+      if (!ok) break;
+      // all_done counts two commits: one per issuer, or both from one
+      umma_commit_w(all_done);
+      if (p.one_issuer) umma_commit_w(all_done);
+      tg += T_iter;
+      ++ki;
+    }
+    if (!ok) {
+      umma_commit_w(&drain[b0]);
+      drain_wait(&drain[b0], 0);
     }
   } else {
-    // ------------------------------------------------ compute (warps 2..9;
-    // warp 10 in the one-issuer mode falls through to the final barrier)
+    // ------------------------------------------------ compute (warps 2..9)
     const int quarter = warp & 3;
     const int b = (warp - 2) >> 2;  // group = buffer = sub-tile parity
     const int r = quarter * 32 + lane;
-    const int kvp = j * 128 + r;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
+    const uint32_t tOut = (b == 0 ? tdV : tdK) + lane_off;  // this group's accumulator
+    uint32_t zero[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) zero[c] = 0u;
+#pragma unroll
+    for (int cc = 0; cc < D / 16; ++cc) tmem_st16_nw(tOut + cc * 16, zero);
     if constexpr (!C::KV_TMEM) {
       // the extra chunk of this thread's K row (group 0: 1 in columns 0..2)
       // or V row (group 1: in columns 3..5), which pick the three terms of
-      // -LSE sqrt(d) and of -D from the query's extra row; and the group's
-      // accumulator (dV, dK) zeroed: both issuers add into it
+      // -LSE sqrt(d) and of -D from the query's extra row
       reinterpret_cast<uint4*>(sKV + 2 * T::TILE + b * C::AUX)[r] =
           b ? make_uint4(0u, 0x3F800000u, 0x3F803F80u, 0u) : make_uint4(0x3F803F80u, 0x00003F80u, 0u, 0u);
       fence_proxy_async_smem();
-      uint32_t z[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) z[c] = 0u;
-#pragma unroll
-      for (int cc = 0; cc < D / 16; ++cc) tmem_st16_nw((b ? tdK : tdV) + lane_off + cc * 16, z);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(kv_ready);
-    } else {
-      // K (group 0) or V (group 1) row of this thread from the last stage,
-      // where TMA put them (zeros past the sequence), into TMEM with the
-      // extra chunk, and the group's accumulator (dV, dK) zeroed: both
-      // issuers add into it
-      uint32_t w[D / 2 + 8];
-      const bool got = U == 0 || __all_sync(0xffffffffu, bounded_wait(kv_full, 0, abort_flag, 725, p.err));
-      if (got && U > 0) load_tile_row<D>(sStage + (QS - 1) * STAGE + b * T::TILE, r, w);
-      // the extra chunk: K picks the three terms of -LSE sqrt(d) (columns
-      // 0..2 of the query's extra row), V those of -D (columns 3..5)
-      w[D / 2] = b ? 0u : 0x3F803F80u;
-      w[D / 2 + 1] = b ? 0x3F800000u : 0x00003F80u;
-      w[D / 2 + 2] = b ? 0x3F803F80u : 0u;
-#pragma unroll
-      for (int c = 3; c < 8; ++c) w[D / 2 + c] = 0u;
-      tmem_store_row<D / 2 + 8>((b ? tVA : tKA) + lane_off, w);
-      uint32_t z[16];
-#pragma unroll
-      for (int c = 0; c < 16; ++c) z[c] = 0u;
-#pragma unroll
-      for (int cc = 0; cc < D / 16; ++cc) tmem_st16_nw((b ? tdK : tdV) + lane_off + cc * 16, z);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(kv_ready);
     }
-    const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
+    int tg = 0, ki = 0;  // stages, items with pairs before this one
     bool ok = true;
-    for (int u = b; u < U; u += 2) {
-      const int t = u >> 1;
-      const int q0 = (i0 + (t0 + t) % n_i) * 128 + 64 * b;
-      const uint8_t* stage = sStage + (t % QS) * STAGE;
-      // the stage's windows and (with a cap) -LSE's, read while the scores are
-      // still being made: the products take most of the shared memory's
-      // bandwidth, and loads among the exponentials waited for it (dK/dV of
-      // 8192 x (32 + 8 + 8) heads of 128, capped: 963 us, 930 so).  With K and V
-      // in TMEM there is room for them there and the registers are worth more
-      // (32 heads of 80: 768 us, 869 so).
-      constexpr bool EARLY = CAP && !C::KV_TMEM;
-      ok = bounded_wait(&qdo_full[t % QS], (t / QS) & 1, abort_flag, 724, p.err);
-      const WinRecord* rec = reinterpret_cast<const WinRecord*>(stage + C::REC);
-      const int2 cut = rec->cut[b];
-      const uint64_t* late = reinterpret_cast<const uint64_t*>(stage + C::NL2) + 32 * b;
-      uint64_t nl2[EARLY ? 32 : 1];
-      if constexpr (EARLY) {
-        const ulonglong2* from = reinterpret_cast<const ulonglong2*>(stage + C::NL2) + 16 * b;
+    for (int it = 0; ok; ++it) {
+      WorkItem item;
+      if (!next_item(queue, it, &item, abort_flag, p.err) || item.n < 0) break;
+      const int g = item.n, bi = item.bi, j = item.q0, i0 = item.j0, n_i = item.nkv;
+      const int kvp = j * 128 + r;
+      const int t0 = part(p.G * n_i, rank), T_iter = part(p.G * n_i, rank + 1) - t0;
+      if (T_iter == 0) {
+        ok = __all_sync(0xffffffffu, bounded_wait(kv_full, it & 1, abort_flag, 725, p.err));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(kv_free);
+        if (n_i == 0 && rank == 0 && kvp < p.s) {
+          // nothing sees this key tile
+          uint4* row = reinterpret_cast<uint4*>(p.dqkv + ((long long)bi * p.s + kvp) * p.width +
+                                                (b == 0 ? p.v_col : p.k_col) + (long long)g * D);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const ulonglong2 v = from[k];
-          nl2[2 * k] = v.x;
-          nl2[2 * k + 1] = v.y;
+          for (int cc = 0; cc < D / 8; ++cc) row[cc] = make_uint4(0u, 0u, 0u, 0u);
         }
+        continue;
       }
-      ok = ok && bounded_wait(&s_full[b], (u >> 1) & 1, abort_flag, 721, p.err);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      tc_fence_after();
-      // ---- phase 1: P^T = exp2 of the modified scores - LSE log2(e)
-      const bool all = cut.x <= j * 128 && cut.y >= j * 128 + 128;
-      const int2* win = rec->row + 64 * b;
-      auto on = [&](int x) {
-        const int2 w = win[x];
-        return (unsigned)(kvp - w.x) < (unsigned)w.y;
-      };
-      float pe[64];
-      uint32_t pk[32];
-      {
-        uint32_t sv[64];
-        const float am = load_scores<true>(tSb + lane_off, sv);
-        auto lse2 = [&](int x) -> uint64_t {
-          if constexpr (EARLY) return nl2[x / 2];
-          else if constexpr (CAP) return late[x / 2];
-          else return 0ull;
-        };
-        if constexpr (!BIAS) {
-          probabilities<CAP, true>(p, sv, am, pe, pk, all, lse2, on);
-        } else {
-          const float slope2 = p.slopes[g * p.G + (t0 + t) / n_i] * 1.4426950408889634f;
-          // along the queries; with a causal mask those before the key are masked
-          const BiasLine bl = bias_line(slope2, kvp, q0, 64, false, p.causal != 0);
-          if (!__any_sync(0xffffffffu, bl.mixed)) {
-            const uint64_t step2 = both(bl.step), base2 = both(bl.base);
-            auto add = [&](int x) {
-              return CAP ? add2(lse2(x), on_line(x, step2, base2)) : on_line(x, step2, base2);
-            };
-            probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
-          } else {
-            const float dist = (float)(kvp - q0);
-            auto add = [&](int x) {
-              return add2(lse2(x), f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
-            };
-            probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
+      if constexpr (C::KV_TMEM) {
+        // K (group 0) or V (group 1) row of this thread (zeros past the
+        // sequence) into TMEM with the extra chunk: K picks the three terms of
+        // -LSE sqrt(d) (columns 0..2 of the query's extra row), V those of -D
+        // (columns 3..5)
+        uint32_t w[D / 2 + 8];
+        ok = __all_sync(0xffffffffu, bounded_wait(kv_full, it & 1, abort_flag, 725, p.err));
+        if (!ok) break;
+        load_tile_row<D>(sKV + b * T::TILE, r, w);
+        w[D / 2] = b ? 0u : 0x3F803F80u;
+        w[D / 2 + 1] = b ? 0x3F800000u : 0x00003F80u;
+        w[D / 2 + 2] = b ? 0x3F803F80u : 0u;
+#pragma unroll
+        for (int c = 3; c < 8; ++c) w[D / 2 + c] = 0u;
+        tmem_store_row<D / 2 + 8>((b ? tVA : tKA) + lane_off, w);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv_free);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kv_ready);
+      for (int u = b; u < 2 * T_iter; u += 2) {
+        const int t = u >> 1;
+        const int q0 = (i0 + (t0 + t) % n_i) * 128 + 64 * b;
+        const int tt = tg + t;
+        const uint8_t* stage = sStage + (tt % QS) * STAGE;
+        // the stage's windows and (with a cap) -LSE's, read while the scores are
+        // still being made: the products take most of the shared memory's
+        // bandwidth, and loads among the exponentials waited for it (dK/dV of
+        // 8192 x (32 + 8 + 8) heads of 128, capped: 963 us, 930 so).  With K and V
+        // in TMEM there is room for them there and the registers are worth more
+        // (32 heads of 80: 768 us, 869 so).
+        constexpr bool EARLY = CAP && !C::KV_TMEM;
+        ok = bounded_wait(&qdo_full[tt % QS], (tt / QS) & 1, abort_flag, 724, p.err);
+        const WinRecord* rec = reinterpret_cast<const WinRecord*>(stage + C::REC);
+        const int2 cut = rec->cut[b];
+        const uint64_t* late = reinterpret_cast<const uint64_t*>(stage + C::NL2) + 32 * b;
+        uint64_t nl2[EARLY ? 32 : 1];
+        if constexpr (EARLY) {
+          const ulonglong2* from = reinterpret_cast<const ulonglong2*>(stage + C::NL2) + 16 * b;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const ulonglong2 v = from[k];
+            nl2[2 * k] = v.x;
+            nl2[2 * k + 1] = v.y;
           }
         }
-      }
-      tmem_st32(tSb + lane_off, pk);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[b]);
-      // ---- phase 2: dx^T = P^T (1 - u^2) dP'^T (dP' offset by -D)
-      ok = bounded_wait(&dp_full[b], (u >> 1) & 1, abort_flag, 722, p.err);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-      tc_fence_after();
-      uint32_t dr[64];
-      tmem_ld32_nw(tdPb + lane_off, dr);
-      tmem_ld32_nw(tdPb + lane_off + 32, dr + 32);
-      tmem_wait_ld(dr);
-      if (!all) mask_gradient(dr, pe);
-      uint32_t o[32];
+        ok = ok && bounded_wait(&s_full[b], tt & 1, abort_flag, 721, p.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        // ---- phase 1: P^T = exp2 of the modified scores - LSE log2(e)
+        const bool all = cut.x <= j * 128 && cut.y >= j * 128 + 128;
+        const int2* win = rec->row + 64 * b;
+        auto on = [&](int x) {
+          const int2 w = win[x];
+          return (unsigned)(kvp - w.x) < (unsigned)w.y;
+        };
+        float pe[64];
+        uint32_t pk[32];
+        {
+          uint32_t sv[64];
+          const float am = load_scores<true>(tSb + lane_off, sv);
+          auto lse2 = [&](int x) -> uint64_t {
+            if constexpr (EARLY) return nl2[x / 2];
+            else if constexpr (CAP) return late[x / 2];
+            else return 0ull;
+          };
+          if constexpr (!BIAS) {
+            probabilities<CAP, true>(p, sv, am, pe, pk, all, lse2, on);
+          } else {
+            const float slope2 = p.slopes[g * p.G + (t0 + t) / n_i] * 1.4426950408889634f;
+            // along the queries; with a causal mask those before the key are masked
+            const BiasLine bl = bias_line(slope2, kvp, q0, 64, false, p.causal != 0);
+            if (!__any_sync(0xffffffffu, bl.mixed)) {
+              const uint64_t step2 = both(bl.step), base2 = both(bl.base);
+              auto add = [&](int x) {
+                return CAP ? add2(lse2(x), on_line(x, step2, base2)) : on_line(x, step2, base2);
+              };
+              probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
+            } else {
+              const float dist = (float)(kvp - q0);
+              auto add = [&](int x) {
+                return add2(lse2(x), f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
+              };
+              probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
+            }
+          }
+        }
+        tmem_st32(tSb + lane_off, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[b]);
+        // ---- phase 2: dx^T = P^T (1 - u^2) dP'^T (dP' offset by -D)
+        ok = bounded_wait(&dp_full[b], tt & 1, abort_flag, 722, p.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t dr[64];
+        tmem_ld32_nw(tdPb + lane_off, dr);
+        tmem_ld32_nw(tdPb + lane_off + 32, dr + 32);
+        tmem_wait_ld(dr);
+        if (!all) mask_gradient(dr, pe);
+        uint32_t o[32];
 #pragma unroll
-      for (int k = 0; k < 64; k += 2) {
-        const float2 v = f2split(mul2(f2(pe[k], pe[k + 1]), f2(__uint_as_float(dr[k]), __uint_as_float(dr[k + 1]))));
-        o[k / 2] = pack_bf16(v.x, v.y);
+        for (int k = 0; k < 64; k += 2) {
+          const float2 v = f2split(mul2(f2(pe[k], pe[k + 1]), f2(__uint_as_float(dr[k]), __uint_as_float(dr[k + 1]))));
+          o[k / 2] = pack_bf16(v.x, v.y);
+        }
+        tmem_st32(tdPb + lane_off, o);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ds_full[b]);
       }
-      tmem_st32(tdPb + lane_off, o);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[b]);
-    }
-    // epilogue: group 0 writes dV, group 1 dK, once both issuers' products
-    // are done (TMEM loads by every lane, stores only for rows inside the
-    // sequence)
-    if (T_all == 0 && rank == 0) {
-      // nothing sees this key tile
-      if (kvp < p.s) {
-        uint4* row = reinterpret_cast<uint4*>(p.dqkv + ((long long)bi * p.s + kvp) * p.width +
-                                              (b == 0 ? p.v_col : p.k_col) + (long long)g * D);
-#pragma unroll
-        for (int cc = 0; cc < D / 8; ++cc) row[cc] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    ok = ok && U > 0;
-    if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, 0, abort_flag, 723, p.err));
-    if (ok) {
+      tg += T_iter;
+      // epilogue: group 0 writes dV, group 1 dK, once both issuers' products
+      // are done (TMEM loads by every lane, stores only for rows inside the
+      // sequence), and zeroes its accumulator for the next item
+      if (ok) ok = __all_sync(0xffffffffu, bounded_wait(all_done, ki & 1, abort_flag, 723, p.err));
+      if (!ok) break;
+      ++ki;
       tc_fence_after();
-      // staged in the first stage's Q (dV) and dO (dK) tiles, which every
-      // product has read, and stored by TMA: whole lines, rows past the
-      // sequence left out
-      // (for the cluster's sum: units of four fp32 columns by 128 rows)
-      const uint32_t tsrc = (b == 0 ? tdV : tdK) + lane_off;
-      uint8_t* tile = sStage + b * T::TILE;
+      // stored by TMA: whole lines, rows past the sequence left out (for the
+      // cluster's sum: units of four fp32 columns by 128 rows, in the stages,
+      // which every product has read)
+      uint8_t* tile = sOut + b * T::TILE;
       uint4* sums = reinterpret_cast<uint4*>(sStage) + b * (D / 4) * 128;
       const float sc = b == 0 ? 1.f : p.scale;
+      if (C::KV_TMEM && lane == 0) bulk_wait_read0();  // this warp's part of the tile is free
+      __syncwarp();
 #pragma unroll
       for (int cc = 0; cc < D / 16; ++cc) {
         uint32_t v[16];
-        tmem_ld16_nw(tsrc + cc * 16, v);
+        tmem_ld16_nw(tOut + cc * 16, v);
         tmem_wait_ld(v);
+        tmem_st16_nw(tOut + cc * 16, zero);
         if (split == 1) {
           store_tile16<D>(tile, r, cc, v, sc);
         } else {
@@ -628,14 +669,21 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (split == 1 && lane == 0 && kvp < p.s) {
-        for (int c = 0; c < T::NCH; ++c)
-          tma_store_3d(&p.map_out, tile + c * T::CHUNK + quarter * 32 * T::SWB,
-                       (b == 0 ? p.v_col : p.k_col) + g * D + c * T::CW, kvp, bi);
-        bulk_commit();
-        bulk_wait0();  // before the shared memory goes
+      if (lane == 0) {
+        if (split == 1 && kvp < p.s) {
+          for (int c = 0; c < T::NCH; ++c)
+            tma_store_3d(&p.map_out, tile + c * T::CHUNK + quarter * 32 * T::SWB,
+                         (b == 0 ? p.v_col : p.k_col) + g * D + c * T::CW, kvp, bi);
+          bulk_commit();
+        }
+        if (!C::KV_TMEM) {
+          bulk_wait_read0();
+          mbar_arrive(kv_free);
+        }
       }
+      __syncwarp();
     }
+    if (lane == 0) bulk_wait0();  // before the shared memory goes
   }
 
   if (split > 1) {
@@ -643,6 +691,8 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
     static_assert(QS * STAGE >= 128 * 2 * D * 4, "the sums' columns");
     __syncwarp();
     cluster_sync_all();
+    const volatile WorkItem* item = queue.item(0);
+    const int T_all = p.G * item->nkv, j = item->q0, bi = item->bi, g = item->n;
     if (warp >= 2 && warp < 10 && T_all > 0) {
       const int rows = 128 / split, r0 = rank * rows;
       const uint32_t mine = smem_u32(sStage);
@@ -652,7 +702,7 @@ __global__ void __launch_bounds__(352, 1) attn_mod_dkdv_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < 16; ++k) acc[k] = 0.f;
         for (int c = 0; c < split; ++c) {
-          if (part(c + 1) == part(c)) continue;  // it had no pairs
+          if (part(T_all, c + 1) == part(T_all, c)) continue;  // it had no pairs
           const uint32_t from = cluster_addr(mine, c) + (4 * cc * 128 + row) * 16;
           float4 v[4];
 #pragma unroll
@@ -791,7 +841,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
 
   if (warp == 11) {
     // ------------------------------------------------ items (the whole warp)
-    took_last = publish_items(queue, blockIdx.x, gridDim.x - 1, abort_flag, p.err, [&](int block) {
+    took_last = publish_items(queue, blockIdx.x, gridDim.x - 1, true, abort_flag, p.err, [&](int block) {
       // the last (with a causal mask heaviest) query tiles first; the query
       // heads of one key/value head are adjacent
       const Item w = item_of(p.order_q, block);
@@ -800,7 +850,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
       const int2 span = p.span[(long long)bi * p.n_t + i];
       const int j0 = span.x < span.y ? span.x / 128 : 0;
       return WorkItem{w.kv % p.Hkv * p.G + w.sub, bi, i * 128, j0, span.x < span.y ? (span.y + 127) / 128 - j0 : 0};
-    });
+    }, [](int, const WorkItem&) { return true; });
   } else if (warp == 0) {
     // ------------------------------------------------ loads (the whole warp
     // runs the loop, one lane issues)
@@ -1196,7 +1246,7 @@ int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
     ProfScope prof(PROF_ATTN_BWD, 8.0 * D * pairs * p.H * b, 0.0, st);
     // CTAs per item: see split_for
     const int items = p.n_t * p.Hkv * b, split = split_for(items, p.G * p.n_t);
-    if (launch_dependent(attn_mod_dkdv_kernel<D, CAP, BIAS>, items * split, split, dim3(352), SMEM_KV, st, p) != cudaSuccess)
+    if (launch_dependent(attn_mod_dkdv_kernel<D, CAP, BIAS>, items * split, split, dim3(384), SMEM_KV, st, p) != cudaSuccess)
       return BPT_ECUDA;
   }
   ProfScope prof(PROF_ATTN_BWD, 2.0 * D * pairs * p.H * b, 0.0, st);

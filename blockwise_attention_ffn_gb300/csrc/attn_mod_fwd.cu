@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
 
   if (warp == 11) {
     // ------------------------------------------------ items (the whole warp)
-    publish_items(queue, blockIdx.x, -1, abort_flag, p.err, [&](int block) {
+    publish_items(queue, blockIdx.x, -1, true, abort_flag, p.err, [&](int block) {
       const Item w = item_of(p.order, block);
       const int bi = w.kv / (p.H / p.G), n = w.kv % (p.H / p.G) * p.G + w.sub;
       const int q0 = (p.order.tiles - 1 - w.tile) * 128;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       hi = __reduce_max_sync(0xffffffffu, hi);
       const int j0 = lo < hi ? lo / 128 : 0;
       return WorkItem{n, bi, q0, j0, lo < hi ? (hi + 127) / 128 - j0 : 0};
-    });
+    }, [](int, const WorkItem&) { return true; });
   } else if (warp == 0) {
     // ------------------------------------------------ loads (the whole warp
     // runs the loop, one lane issues).  The next item is asked for three key
