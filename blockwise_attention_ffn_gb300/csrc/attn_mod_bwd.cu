@@ -26,13 +26,13 @@
 // signs that do not build up; dqkv is off by 2.5e-3 to 3.3e-3 (relative norm, its
 // own bf16 rounding of 1.7e-3 included).
 //
-// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: dK/dV 804 us, dQ 518,
-// capped 900 and 597; documents of 1500: 221 and 154.  dK/dV is bound by its four
+// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: dK/dV 792 us, dQ 516,
+// capped 889 and 585; documents of 1500: 202 and 154.  dK/dV is bound by its four
 // products (tensor core 57 to 70% busy: at head dims above 80 S^T and dP^T take
 // both operands from shared memory, and 64 columns of them cost 48 cycles a step of
 // 16 where 32 are arithmetic) and by the chain between them; one product of 128
 // columns for both groups saves a fifth of the tensor core's time but makes the
-// groups run in step: 774 us plain, 1,064 capped.
+// groups run in step: 774 us plain (against 807 then), 1,064 capped (against 901).
 #include <math.h>
 #include <string.h>
 
@@ -1221,16 +1221,17 @@ __global__ void __launch_bounds__(256) attn_mod_prep_kernel(int b, int s, int n_
   }
 }
 
-// CTAs that share one dK/dV item.  Sharing costs the sum over the cluster (some
-// 4,000 cycles a CTA), so only where items leave SMs idle, up to two CTAs per
-// SM, while a CTA's stream keeps a dozen query tiles.  Measured, dK/dV alone:
-// 108 items of up to 27 tiles (d = 96) 82 us unshared, 65 by 2, 85 by 4; 32
-// items of up to 256 tiles (d = 128) 417 us, 112 by 8; 1024 items of up to 16
-// tiles (d = 80) 121 us, 218 by 2.
+// CTAs that share one dK/dV item.  Sharing costs the sum over the cluster and
+// the persistence, so only where items leave SMs idle that dQ cannot fill: up to
+// three CTAs for two SMs, while a CTA's stream keeps a dozen query tiles.  Measured,
+// the whole backward: 32 items of up to 256 tiles (d = 128) 421 us unshared, 227 by
+// 2, 124 by 4, 133 by 8; 108 items of up to 27 tiles (d = 96) 86 us unshared, 95 by
+// 2, 120 by 4, and with a quarter of the rows padding 82 unshared, 76 by 2; 1024
+// items of up to 16 tiles (d = 80) 191 us, 304 by 2.
 int split_for(int items, int stream) {
   const int nsm = sm_count();
   int s = 1;
-  while (s < 8 && items * 2 * s <= 2 * nsm && stream >= 2 * s * 12) s *= 2;
+  while (s < 8 && items * 4 * s <= nsm * 3 && stream >= 2 * s * 12) s *= 2;
   return s;
 }
 
