@@ -287,6 +287,44 @@ def test_streams_and_graphs():
     assert bpt.bpt_last_device_error() == (bpt.BPT_OK, 0)
 
 
+@pytest.mark.parametrize("d,cap,biased", [(64, 0.0, False), (64, 30.0, True), (80, 0.0, True), (80, 20.0, False), (96, 0.0, False),
+                                          (96, 50.0, True), (112, 30.0, False), (128, 0.0, True), (128, 50.0, False),
+                                          (128, 0.0, False)])
+def test_many_items_per_block(d, cap, biased):
+    """Far more query and key tiles than blocks, some of them seen by nothing:
+    every sequence of a batch gets bitwise what it gets alone (fixed-order mode),
+    again and again, and within the roundings' size in the default mode."""
+    b, s, H, K = 40, 391, 8, 4
+    cfg = LayerConfig(b=b, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64, causal=0)
+    gen = torch.Generator().manual_seed(d)
+    begin, end = torch.zeros(b, s, dtype=torch.int32), torch.zeros(b, s, dtype=torch.int32)
+    q = torch.arange(s, dtype=torch.int32)
+    for i in range(b):
+        n = [s, 0, 130, 257, 1][i % 5]  # the sequence's length
+        size = int(torch.randint(1, s, (1,), generator=gen))
+        if i % 3:  # documents
+            begin[i] = q // size * size
+        end[i] = torch.where(q < n, torch.clamp(q + 1, min=min(n, 40)) if i % 2 else torch.clamp(begin[i] + size, max=n), 0)
+    slopes = torch.linspace(0.0, 0.3, H, device="cuda") if biased else None
+    qkv, dout = make(b, s, H, K, d, seed=3)
+    flag = bpt.BPT_FLAG_DETERMINISTIC
+    mod = bpt.ScoreMod(begin.view(-1).cuda(), end.view(-1).cuda(), slopes, cap)
+    got = [t.clone() for t in run(cfg, mod, qkv, dout, flag)]
+    for i in range(b):
+        rows = slice(i * s, (i + 1) * s)
+        part = bpt.ScoreMod(begin[i].cuda(), end[i].cuda(), slopes, cap)
+        o, lse, dx = run(cfg.with_(b=1), part, qkv[rows], dout[rows], flag)
+        assert torch.equal(o, got[0][rows]) and torch.equal(lse[0], got[1][i]) and torch.equal(dx, got[2][rows]), i
+    for _ in range(5):
+        for a, c in zip(run(cfg, mod, qkv, dout, flag), got):
+            assert torch.equal(a, c)
+    # the forward has one order of sums in every mode; the backward's fp32 sums
+    # differ in their last bits, so a rounding to bf16 may go the other way
+    o, lse, dx = run(cfg, mod, qkv, dout)
+    assert torch.equal(o, got[0]) and torch.equal(lse, got[1])
+    assert float((dx.double() - got[2].double()).norm()) <= 2.0 ** -8 * float(got[2].double().norm())
+
+
 def test_far_offsets():
     """A packed buffer of more than 2^31 elements: documents at its end equal
     the same documents alone, within both sides' roundings (their tiles differ)."""
