@@ -740,15 +740,17 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
 // ===========================================================================
 // dQ
 // ===========================================================================
-// Shared memory of the dQ kernel: dQ on its way out, a ring of tiles (Q, dO,
-// K_0, V_0, K_1, ... of one item after the other), barriers.
+// Shared memory of the dQ kernel: dQ on its way out, a ring of pairs of tiles
+// ((Q, dO), (K_0, V_0), (K_1, V_1), ... of one item after the other), barriers.
+// (Each wait of an issuing warp costs a hundred cycles, and its loop bounds the
+// kernel as much as the products do: one barrier for two tiles.)
 template <int D>
 struct ModDqCfg {
   using T = TileGeom<D>;
   static constexpr int CTL = 640;
-  static constexpr int FIT = (232448 - T::TILE - CTL) / T::TILE;
-  static constexpr int NT = FIT > 10 ? 10 : FIT;
-  static constexpr int SMEM = (1 + NT) * T::TILE + CTL;
+  static constexpr int FIT = (232448 - T::TILE - CTL) / (2 * T::TILE);
+  static constexpr int NP = FIT > 5 ? 5 : FIT;
+  static constexpr int SMEM = (1 + 2 * NP) * T::TILE + CTL;
 };
 
 // One work item per 128-row query tile of one head, over the key tiles that
@@ -769,10 +771,10 @@ template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_constant__ ModBwdParams p) {
   using T = TileGeom<D>;
   using C = ModDqCfg<D>;
-  constexpr int NT = C::NT;
-  static_assert(NT >= 6, "Q, dO, K and V of two tiles");
+  constexpr int NP = C::NP;
+  static_assert(NP >= 3, "Q, dO, K and V of two tiles");
   static_assert(256 + 2 * D <= 512, "TMEM columns");
-  static_assert((2 * NT + 17) * 8 + WORK_BYTES + 8 <= C::CTL, "control block");
+  static_assert((2 * NP + 17) * 8 + WORK_BYTES + 8 <= C::CTL, "control block");
   constexpr uint32_t ID_S = idesc_bf16(128, 64, false, false);
   constexpr uint32_t ID_DQ = idesc_bf16(128, D, false, true);
   constexpr uint32_t COL_DQ = 256, COL_Q = 256 + D, COL_DO = 256 + D + D / 2;
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sOut = smem;                 // dQ
   uint8_t* sRing = smem + T::TILE;
-  uint8_t* control = sRing + NT * T::TILE;
+  uint8_t* control = sRing + 2 * NP * T::TILE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(control + WORK_BYTES);
   // (read by 8 compute warps, 2 issuers, the loads)
   const WorkQueue queue{control, bars, bars + 2, bars + 4};
@@ -792,9 +794,9 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
   uint64_t* ds_full = bars + 12;   // [2] dS(u) written (4 warps)
   uint64_t* all_done = bars + 14;  // both issuers' last products of an item done
   uint64_t* drain = bars + 15;     // [2], one per issuer
-  uint64_t* t_full = bars + 17;    // [NT]
-  uint64_t* t_empty = t_full + NT; // [NT], once per issuer (both sub-tiles' products of a K or V tile)
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(t_empty + NT);
+  uint64_t* t_full = bars + 17;    // [NP]
+  uint64_t* t_empty = t_full + NP; // [NP], once per issuer (both sub-tiles' products of K and V)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(t_empty + NP);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = warp_id();
@@ -812,7 +814,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
     mbar_init(queue.answered, 1);
     mbar_init(qo_ready, 8);
     mbar_init(all_done, 2);
-    for (int k = 0; k < NT; ++k) {
+    for (int k = 0; k < NP; ++k) {
       mbar_init(&t_full[k], 1);
       mbar_init(&t_empty[k], 2);
     }
@@ -854,15 +856,19 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
   } else if (warp == 0) {
     // ------------------------------------------------ loads (the whole warp
     // runs the loop, one lane issues)
-    int c = 0;  // tiles loaded
-    auto load_tile = [&](const CUtensorMap* map, int col, int row, int bi) -> bool {
-      const int st = c % NT;
-      if (c >= NT && !bounded_wait_w(&t_empty[st], ((c / NT) & 1) ^ 1, abort_flag, 731, p.err)) return false;
+    int c = 0;  // pairs loaded
+    // columns x of `first` and y of `second`, from the same row
+    auto load_pair = [&](const CUtensorMap* first, int x, const CUtensorMap* second, int y, int row, int bi) -> bool {
+      const int st = c % NP;
+      if (c >= NP && !bounded_wait_w(&t_empty[st], ((c / NP) & 1) ^ 1, abort_flag, 731, p.err)) return false;
       if (lane == 0) {
-        mbar_expect_tx(&t_full[st], T::TILE);
+        uint8_t* to = sRing + 2 * st * T::TILE;
+        mbar_expect_tx(&t_full[st], 2 * T::TILE);
+#pragma unroll
+        for (int k = 0; k < T::NCH; ++k) tma_load_3d(to + k * T::CHUNK, first, &t_full[st], x + k * T::CW, row, bi);
 #pragma unroll
         for (int k = 0; k < T::NCH; ++k)
-          tma_load_3d(sRing + st * T::TILE + k * T::CHUNK, map, &t_full[st], col + k * T::CW, row, bi);
+          tma_load_3d(to + T::TILE + k * T::CHUNK, second, &t_full[st], y + k * T::CW, row, bi);
       }
       ++c;
       return true;
@@ -875,15 +881,15 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
         release_item(queue, it);
         continue;
       }
-      ok = load_tile(&p.map_qkv, w.n * D, w.q0, w.bi) && load_tile(&p.map_do, w.n * D, w.q0, w.bi);
+      ok = load_pair(&p.map_qkv, w.n * D, &p.map_do, w.n * D, w.q0, w.bi);
       const int k_col = p.k_col + w.n / p.G * D, v_col = p.v_col + w.n / p.G * D;
       for (int j = w.j0; ok && j < w.j0 + w.nkv; ++j)
-        ok = load_tile(&p.map_qkv, k_col, j * 128, w.bi) && load_tile(&p.map_qkv, v_col, j * 128, w.bi);
+        ok = load_pair(&p.map_qkv, k_col, &p.map_qkv, v_col, j * 128, w.bi);
       release_item(queue, it);
     }
     // every copy lands before the shared memory goes, also when a wait elsewhere
     // in the block gives up later
-    for (int k = (c > NT ? c - NT : 0); k < c; ++k) drain_wait(&t_full[k % NT], (k / NT) & 1);
+    for (int k = (c > NP ? c - NP : 0); k < c; ++k) drain_wait(&t_full[k % NP], (k / NP) & 1);
   } else if (warp == 1 || warp == 10) {
     // ------------------------------------------------ MMA issuers (the whole
     // warp runs the loop, one elected lane issues).  One issuer (fixed-order
@@ -897,15 +903,16 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
     // V's tiles (whole swizzle atoms); sub-tile u uses buffer b = u % 2.  tg,
     // qi: key tiles, items with keys before this one
     int tg = 0, qi = 0;
-    auto tile = [&](int u, int v) { return 2 * (tg + qi) + 2 + 2 * (u >> 1) + v; };
-    auto slot = [&](int u, int v) { return tile(u, v) % NT; };
-    auto landed = [&](int u, int v) {
-      return bounded_wait_w(&t_full[slot(u, v)], (tile(u, v) / NT) & 1, abort_flag, 741, p.err);
+    // sub-tile u's K and V
+    auto pair = [&](int u) { return tg + qi + 1 + (u >> 1); };
+    auto k_tile = [&](int u) { return ring + 2 * (pair(u) % NP) * T::TILE; };
+    auto landed = [&](int u) {
+      return bounded_wait_w(&t_full[pair(u) % NP], (pair(u) / NP) & 1, abort_flag, 741, p.err);
     };
     auto issue_s = [&](int u) {
       const int b = u & 1;
       const uint32_t tSb = tS + 64 * b;
-      const uint64_t k = T::kmajor(ring + slot(u, 0) * T::TILE + 64 * T::SWB * b, 0);
+      const uint64_t k = T::kmajor(k_tile(u) + 64 * T::SWB * b, 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tQA + kk * 8, k + T::kmajor_step(kk), ID_S, kk > 0);
       umma_commit_w(&s_full[b]);
@@ -913,11 +920,10 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
     auto issue_dp = [&](int u) {
       const int b = u & 1;
       const uint32_t tdPb = tdP + 64 * b;
-      const uint64_t v = T::kmajor(ring + slot(u, 1) * T::TILE + 64 * T::SWB * b, 0);
+      const uint64_t v = T::kmajor(k_tile(u) + T::TILE + 64 * T::SWB * b, 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tdPb, tOA + kk * 8, v + T::kmajor_step(kk), ID_S, kk > 0);
       umma_commit_w(&dp_full[b]);
-      umma_commit_w(&t_empty[slot(u, 1)]);
     };
     bool ok = true;
     for (int it = 0; ok; ++it) {
@@ -930,28 +936,25 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
       if (!ok) break;
       if (lane == 0) {
         // the tiles of Q and dO are free
-        for (int k = 0; k < 2; ++k) {
-          uint64_t* bar = &t_empty[(2 * (tg + qi) + k) % NT];
-          mbar_arrive(bar);
-          if (p.one_issuer) mbar_arrive(bar);
-        }
+        uint64_t* bar = &t_empty[(tg + qi) % NP];
+        mbar_arrive(bar);
+        if (p.one_issuer) mbar_arrive(bar);
       }
-      ok = landed(b0, 0);
+      ok = landed(b0);
       if (!ok) break;
       tc_fence_after();
       // sub-tiles 0 and 1 share the first tiles (U is even)
-      for (int u = b0; u < 2; u += ustep) issue_s(u);
-      ok = landed(b0, 1);
-      if (!ok) break;
-      tc_fence_after();
-      for (int u = b0; u < 2; u += ustep) issue_dp(u);
+      for (int u = b0; u < 2; u += ustep) {
+        issue_s(u);
+        issue_dp(u);
+      }
       for (int u = b0; u < U; u += ustep) {
         const int b = u & 1;
         const uint32_t phase = (tg + (u >> 1)) & 1;
         const bool more = u + 2 < U;
         if (more) {
           // S(u+2) once the group has read S(u)
-          ok = bounded_wait_w(&s_free[b], phase, abort_flag, 743, p.err) && landed(u + 2, 0);
+          ok = bounded_wait_w(&s_free[b], phase, abort_flag, 743, p.err) && landed(u + 2);
           if (!ok) break;
           tc_fence_after();
           issue_s(u + 2);
@@ -960,18 +963,12 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
         ok = bounded_wait_w(&ds_full[b], phase, abort_flag, 744, p.err);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t k = T::mnmajor(ring + slot(u, 0) * T::TILE, 4 * b);
+        const uint64_t k = T::mnmajor(k_tile(u), 4 * b);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16_tmem_a_w(tdQ, tdP + 64 * b + kk * 8, k + T::mnmajor_step(kk), ID_DQ, 1);
-        umma_commit_w(&t_empty[slot(u, 0)]);
-        if (more) {
-          // dP(u+2) overwrites dS(u), after dQ(u) in issue order
-          ok = landed(u + 2, 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_dp(u + 2);
-        }
+        umma_commit_w(&t_empty[pair(u) % NP]);
+        if (more) issue_dp(u + 2);  // over dS(u), after dQ(u) in issue order
       }
       if (!ok) break;
       // all_done counts two commits: one per issuer, or both from one
@@ -1021,10 +1018,10 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
         // Q (group 0) or dO (group 1) row of this thread into TMEM (zeros past
         // the sequence)
         uint32_t row[D / 2];
-        const int c = 2 * (tg + qi) + b;
-        ok = __all_sync(0xffffffffu, bounded_wait(&t_full[c % NT], (c / NT) & 1, abort_flag, 754, p.err));
+        const int c = tg + qi;
+        ok = __all_sync(0xffffffffu, bounded_wait(&t_full[c % NP], (c / NP) & 1, abort_flag, 754, p.err));
         if (!ok) break;
-        load_tile_row<D>(sRing + c % NT * T::TILE, r, row);
+        load_tile_row<D>(sRing + (2 * (c % NP) + b) * T::TILE, r, row);
         tmem_store_row<D / 2>((b == 0 ? tQA : tOA) + lane_off, row);
         tmem_st_wait();
         tc_fence_before();

@@ -66,17 +66,17 @@ struct ModFwdParams {
 };
 
 // TMEM: S of half b as two 64-column buffers at 128 b, O_b at 256 + b D.
-// Shared memory: two Q tiles, a ring of K and V tiles in the order they are
-// used (K_0, K_1, V_0, K_2, V_1, ..., V_last, then the next item's), the
-// merge's maxima and sums, barriers.
+// Shared memory: two Q tiles, a ring of pairs of K and V tiles as a step takes
+// them ((K_0, -), (K_1, V_0), (K_2, V_1), ..., (-, V_last), then the next item's),
+// the merge's maxima and sums, barriers.
 template <int D>
 struct ModFwdCfg {
   using T = TileGeom<D>;
   static constexpr int RED = 4 * 128 * 4;
   static constexpr int CTL = 640;  // barriers, work items, answers
-  static constexpr int FIT = (232448 - 2 * T::TILE - RED - CTL) / T::TILE;
-  static constexpr int NT = FIT > 10 ? 10 : FIT;
-  static constexpr int SMEM = (2 + NT) * T::TILE + RED + CTL;
+  static constexpr int FIT = (232448 - 2 * T::TILE - RED - CTL) / (2 * T::TILE);
+  static constexpr int NP = FIT > 5 ? 5 : FIT;
+  static constexpr int SMEM = (2 + 2 * NP) * T::TILE + RED + CTL;
   static constexpr uint32_t COL_O = 256;
 };
 
@@ -84,10 +84,10 @@ template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_constant__ ModFwdParams p) {
   using T = TileGeom<D>;
   using C = ModFwdCfg<D>;
-  constexpr int NT = C::NT;
-  static_assert(NT >= 4, "K and V of two steps");
+  constexpr int NP = C::NP;
+  static_assert(NP >= 2, "K and V of two steps");
   static_assert(C::COL_O + 2 * D <= 512, "TMEM columns");
-  static_assert((2 * NT + 30) * 8 + WORK_BYTES + 8 <= C::CTL, "control block");
+  static_assert((2 * NP + 30) * 8 + WORK_BYTES + 8 <= C::CTL, "control block");
   constexpr uint32_t IDESC_S = idesc_bf16(128, 64, false, false);
   constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
   constexpr float NEG_INF = -INFINITY;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + 2 * T::TILE;
-  float* red_m = reinterpret_cast<float*>(sKV + NT * T::TILE);  // [half][row]
+  float* red_m = reinterpret_cast<float*>(sKV + 2 * NP * T::TILE);  // [half][row]
   float* red_l = red_m + 256;
   uint8_t* control = reinterpret_cast<uint8_t*>(red_l + 256);
   uint64_t* bars = reinterpret_cast<uint64_t*>(control + WORK_BYTES);
@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
   uint64_t* o_free = bars + 18;         // both O's read (8 warps)
   uint64_t* drain = bars + 20;          // [half]
   uint64_t* merged = bars + 22;         // [half][quarter] its maxima and sums are written
-  uint64_t* t_full = bars + 30;         // [NT]
-  uint64_t* t_empty = t_full + NT;      // [NT] both issuers
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(t_empty + NT);
+  uint64_t* t_full = bars + 30;         // [NP]
+  uint64_t* t_empty = t_full + NP;      // [NP] both issuers
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(t_empty + NP);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   // Step j's key tile.  With a bias the last comes first: the keys nearest to a
   // row set its maximum, and the rest never move it (32 heads of 80, causal:
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     for (int i = 0; i < 8; ++i) mbar_init(&merged[i], 1);
     mbar_init(o_free, 8);
     mbar_init(queue.answered, 1);
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < NP; ++i) {
       mbar_init(&t_full[i], 1);
       mbar_init(&t_empty[i], 2);
     }
@@ -187,16 +187,25 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     // the item's start too early to balance the CTAs (324 items of prefix rows,
     // heads of 96: 38 us against 32)
     constexpr int LEAD = 3;
-    int qi = 0, c = 0;  // items with keys, tiles loaded
+    int qi = 0, c = 0;  // items with keys, pairs loaded
     bool ok = true;
-    auto load_tile = [&](int col, int row, int bi) -> bool {
-      const int st = c % NT;
-      if (c >= NT && !bounded_wait_w(&t_empty[st], ((c / NT) & 1) ^ 1, abort_flag, 251, p.err)) return false;
+    // K's row k_row and V's row v_row (negative: none)
+    auto load_pair = [&](int k_col, int k_row, int v_col, int v_row, int bi) -> bool {
+      const int st = c % NP;
+      if (c >= NP && !bounded_wait_w(&t_empty[st], ((c / NP) & 1) ^ 1, abort_flag, 251, p.err)) return false;
       if (lane == 0) {
-        mbar_expect_tx(&t_full[st], T::TILE);
+        uint8_t* to = sKV + 2 * st * T::TILE;
+        mbar_expect_tx(&t_full[st], (k_row >= 0 && v_row >= 0 ? 2 : 1) * T::TILE);
+        if (k_row >= 0) {
 #pragma unroll
-        for (int k = 0; k < T::NCH; ++k)
-          tma_load_3d(sKV + st * T::TILE + k * T::CHUNK, &p.map_qkv, &t_full[st], col + k * T::CW, row, bi);
+          for (int k = 0; k < T::NCH; ++k)
+            tma_load_3d(to + k * T::CHUNK, &p.map_qkv, &t_full[st], k_col + k * T::CW, k_row, bi);
+        }
+        if (v_row >= 0) {
+#pragma unroll
+          for (int k = 0; k < T::NCH; ++k)
+            tma_load_3d(to + T::TILE + k * T::CHUNK, &p.map_qkv, &t_full[st], v_col + k * T::CW, v_row, bi);
+        }
       }
       ++c;
       return true;
@@ -219,15 +228,15 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       ++qi;
       const int k_col = p.k_col + n / p.G * D, v_col = p.v_col + n / p.G * D;
       for (int j = 0; ok && j <= nkv; ++j) {
-        if (j < nkv) ok = load_tile(k_col, key_tile(j, j0, nkv) * 128, bi);
-        if (ok && j > 0) ok = load_tile(v_col, key_tile(j - 1, j0, nkv) * 128, bi);
+        ok = load_pair(k_col, j < nkv ? key_tile(j, j0, nkv) * 128 : -1, v_col,
+                       j > 0 ? key_tile(j - 1, j0, nkv) * 128 : -1, bi);
         if (j == nkv - LEAD) release_item(queue, it);
       }
     }
     // every copy lands before the shared memory goes, also when a wait elsewhere
     // in the block gives up later
     for (int k = (qi > 2 ? qi - 2 : 0); k < qi; ++k) drain_wait(&q_full[k & 1], (k >> 1) & 1);
-    for (int k = (c > NT ? c - NT : 0); k < c; ++k) drain_wait(&t_full[k % NT], (k / NT) & 1);
+    for (int k = (c > NP ? c - NP : 0); k < c; ++k) drain_wait(&t_full[k % NP], (k / NP) & 1);
   } else if (warp == 1 || warp == 10) {
     // ------------------------------------------------ MMA issuers (the
     // whole warp runs the loop, one elected lane issues).  Steps are counted
@@ -240,20 +249,18 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     const uint32_t uKV = smem_u32(sKV), uQ = smem_u32(sQ);
     const uint32_t tSb = tmem + 128 * b;
     const uint32_t tOb = tmem + C::COL_O + b * D;
-    int t = 0, c = 0, qi = 0;  // steps and tiles through all items, items with keys
+    int t = 0, c = 0, qi = 0;  // steps and pairs through all items, items with keys
+    auto landed = [&]() { return bounded_wait_w(&t_full[c % NP], (c / NP) & 1, abort_flag, 253, p.err); };
     auto pv = [&](int tp, bool first) -> bool {  // PV of step tp, its item's first
       const int sb = tp & 1;
+      const uint64_t v = T::mnmajor(uKV + (2 * (c % NP) + 1) * T::TILE, 4 * b);
       if (!bounded_wait_w(&p_full[2 * b + sb], (tp >> 1) & 1, abort_flag, 255, p.err)) return false;
       if (first && qi > 0 && !bounded_wait_w(o_free, (qi - 1) & 1, abort_flag, 258, p.err)) return false;
-      if (!bounded_wait_w(&t_full[c % NT], (c / NT) & 1, abort_flag, 253, p.err)) return false;
       tc_fence_after();
-      const uint64_t v = T::mnmajor(uKV + (c % NT) * T::TILE, 4 * b);
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
         umma_bf16_tmem_a_w(tOb, tSb + sb * 64 + kk * 8, v + T::mnmajor_step(kk), IDESC_PV, !first || kk > 0);
-      umma_commit_w(&t_empty[c % NT]);
       umma_commit_w(&pv_done[b]);
-      ++c;
       return true;
     };
     bool ok = true;
@@ -266,19 +273,22 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       if (!bounded_wait_w(&q_full[qi & 1], (qi >> 1) & 1, abort_flag, 259, p.err)) { ok = false; break; }
       const uint64_t q = T::kmajor(uQ + (qi & 1) * T::TILE, 0);
       for (int j = 0; j < nkv; ++j, ++t) {
-        if (!bounded_wait_w(&t_full[c % NT], (c / NT) & 1, abort_flag, 253, p.err)) { ok = false; break; }
+        if (!landed()) { ok = false; break; }
         tc_fence_after();
-        const uint64_t k = T::kmajor(uKV + (c % NT) * T::TILE + 64 * T::SWB * b, 0);
+        const uint64_t k = T::kmajor(uKV + 2 * (c % NP) * T::TILE + 64 * T::SWB * b, 0);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma_bf16_w(tSb + (t & 1) * 64, q + T::kmajor_step(kk), k + T::kmajor_step(kk), IDESC_S, kk > 0);
         umma_commit_w(&s_full[2 * b + (t & 1)]);
-        umma_commit_w(&t_empty[c % NT]);
         if (j == nkv - 1) umma_commit_w(&q_empty[qi & 1]);
-        ++c;
         if (j > 0 && !pv(t - 1, j == 1)) { ok = false; break; }
+        umma_commit_w(&t_empty[c % NP]);
+        ++c;
       }
-      if (ok) ok = pv(t - 1, nkv == 1);
+      ok = ok && landed() && pv(t - 1, nkv == 1);
+      if (!ok) break;
+      umma_commit_w(&t_empty[c % NP]);
+      ++c;
       ++qi;
     }
     if (!ok) {
