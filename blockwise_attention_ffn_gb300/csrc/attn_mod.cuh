@@ -108,6 +108,21 @@ __device__ __forceinline__ Item item_of(const ItemOrder& o, int block) {
   return Item{rem / heads, g * o.group + head / o.per_head, head % o.per_head};
 }
 
+// A place in a ring of N and the parity of the round, counted up instead of
+// divided: the issuing warps' loops feel every instruction (a remainder by 3 or 5
+// in them cost the forward up to a third).
+template <int N>
+struct RingPos {
+  int at = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ RingPos next() const {
+    RingPos r;
+    r.at = at + 1 == N ? 0 : at + 1;
+    r.round = at + 1 == N ? round ^ 1 : round;
+    return r;
+  }
+};
+
 // One work item as the scheduling warp of a persistent CTA publishes it; n < 0:
 // no more.
 struct WorkItem {

@@ -370,11 +370,12 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
     const int ustep = p.one_issuer ? 1 : 2;
     const uint32_t uZero = smem_u32(sZero);
     int tg = 0, ki = 0;  // stages, items with pairs before this one
+    RingPos<QS> c;       // the sub-tile's stage
     bool ok = true;
     // the 64 query rows of sub-tile half b start 64 b rows into every
     // chunk of the stage's tiles (whole swizzle atoms), and 64 b rows into
     // its extra rows; sub-tile u uses buffer b = u % 2
-    auto stage_u = [&](int u) { return smem_u32(sStage + ((tg + (u >> 1)) % QS) * STAGE); };
+    auto stage_at = [&](RingPos<QS> c) { return smem_u32(sStage) + c.at * STAGE; };
     // K, V and their extra chunks in shared memory (head dims above 80):
     // the extra chunk is 128 rows of 16 bytes, K-major core matrices
     // without swizzle, its upper 8 columns the zeros
@@ -382,11 +383,10 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
     const uint32_t uKx = uK + 2 * T::TILE, uVx = uKx + C::AUX;
     const uint64_t dK = T::kmajor(uK, 0), dV = T::kmajor(uV, 0);
     const uint64_t dKx = sdesc(uKx, uZero - uKx, 128, 0u), dVx = sdesc(uVx, uZero - uVx, 128, 0u);
-    auto issue_s = [&](int u) {
-      const int b = u & 1;
+    auto issue_s = [&](int b, RingPos<QS> c) {
       const uint32_t tSb = tS + 64 * b;
-      const uint64_t q = T::kmajor(stage_u(u) + 64 * T::SWB * b, 0);
-      const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
+      const uint64_t q = T::kmajor(stage_at(c) + 64 * T::SWB * b, 0);
+      const uint32_t uA = stage_at(c) + 2 * T::TILE + 64 * 16 * b;
       if constexpr (C::KV_TMEM) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
@@ -400,11 +400,10 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
       }
       umma_commit_w(&s_full[b]);
     };
-    auto issue_dp = [&](int u) {
-      const int b = u & 1;
+    auto issue_dp = [&](int b, RingPos<QS> c) {
       const uint32_t tdPb = tdP + 64 * b;
-      const uint64_t o = T::kmajor(stage_u(u) + T::TILE + 64 * T::SWB * b, 0);
-      const uint32_t uA = stage_u(u) + 2 * T::TILE + 64 * 16 * b;
+      const uint64_t o = T::kmajor(stage_at(c) + T::TILE + 64 * T::SWB * b, 0);
+      const uint32_t uA = stage_at(c) + 2 * T::TILE + 64 * 16 * b;
       if constexpr (C::KV_TMEM) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
@@ -418,9 +417,8 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
       }
       umma_commit_w(&dp_full[b]);
     };
-    auto wait_stage = [&](int u) {
-      const int t = tg + (u >> 1);
-      return bounded_wait_w(&qdo_full[t % QS], (t / QS) & 1, abort_flag, 711, p.err);
+    auto wait_stage = [&](RingPos<QS> c) {
+      return bounded_wait_w(&qdo_full[c.at], c.round, abort_flag, 711, p.err);
     };
     for (int it = 0; ok; ++it) {
       WorkItem w;
@@ -429,20 +427,21 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
       const int pairs = p.G * w.nkv, T_iter = part(pairs, rank + 1) - part(pairs, rank), U = 2 * T_iter;
       if (U == 0 || !issues) continue;
       ok = bounded_wait_w(kv_ready, ki & 1, abort_flag, 712, p.err) &&
-           (C::KV_TMEM || bounded_wait_w(kv_full, it & 1, abort_flag, 716, p.err)) && wait_stage(b0);
+           (C::KV_TMEM || bounded_wait_w(kv_full, it & 1, abort_flag, 716, p.err)) && wait_stage(c);
       if (!ok) break;
       tc_fence_after();
       // sub-tiles 0 and 1 share the first stage (U is even)
       for (int u = b0; u < 2; u += ustep) {
-        issue_s(u);
-        issue_dp(u);
+        issue_s(u, c);
+        issue_dp(u, c);
       }
       for (int u = b0; u < U; u += ustep) {
         const int b = u & 1;
         const uint32_t phase = (tg + (u >> 1)) & 1;
         const uint32_t tSb = tS + 64 * b, tdPb = tdP + 64 * b;
-        const uint64_t dQm = T::mnmajor(stage_u(u), 4 * b), dOm = T::mnmajor(stage_u(u) + T::TILE, 4 * b);
+        const uint64_t dQm = T::mnmajor(stage_at(c), 4 * b), dOm = T::mnmajor(stage_at(c) + T::TILE, 4 * b);
         const bool more = u + 2 < U;
+        const RingPos<QS> ahead = c.next();
         // dV += P^T(u) dO(u): the P^T pairs sit over the first 32 columns of
         // buffer b; dO rows 64b.. are K blocks 4b..4b+3 of the stage's tile
         ok = bounded_wait_w(&p_full[b], phase, abort_flag, 713, p.err);
@@ -453,10 +452,10 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
           umma_bf16_tmem_a_w(tdV, tSb + kk * 8, dOm + T::mnmajor_step(kk), ID_KV, 1);
         if (more) {
           // S(u+2) overwrites P^T(u), after dV(u) in issue order
-          ok = wait_stage(u + 2);
+          ok = wait_stage(ahead);
           if (!ok) break;
           tc_fence_after();
-          issue_s(u + 2);
+          issue_s(b, ahead);
         }
         // dK += dS^T(u) Q(u)
         ok = bounded_wait_w(&ds_full[b], phase, abort_flag, 714, p.err);
@@ -465,9 +464,10 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16_tmem_a_w(tdK, tdPb + kk * 8, dQm + T::mnmajor_step(kk), ID_KV, 1);
-        umma_commit_w(&qdo_empty[(tg + (u >> 1)) % QS]);
+        umma_commit_w(&qdo_empty[c.at]);
         // dP(u+2) overwrites dS^T(u), after dK(u) in issue order
-        if (more) issue_dp(u + 2);
+        if (more) issue_dp(b, ahead);
+        if (ustep == 2 || b == 1) c = ahead;
       }
       if (!ok) break;
       // all_done counts two commits: one per issuer, or both from one
@@ -903,24 +903,19 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
     // V's tiles (whole swizzle atoms); sub-tile u uses buffer b = u % 2.  tg,
     // qi: key tiles, items with keys before this one
     int tg = 0, qi = 0;
-    // sub-tile u's K and V
-    auto pair = [&](int u) { return tg + qi + 1 + (u >> 1); };
-    auto k_tile = [&](int u) { return ring + 2 * (pair(u) % NP) * T::TILE; };
-    auto landed = [&](int u) {
-      return bounded_wait_w(&t_full[pair(u) % NP], (pair(u) / NP) & 1, abort_flag, 741, p.err);
-    };
-    auto issue_s = [&](int u) {
-      const int b = u & 1;
+    RingPos<NP> c;  // the pair of K and V (before an item's first, of Q and dO)
+    auto k_tile = [&](RingPos<NP> c) { return ring + 2 * c.at * T::TILE; };
+    auto landed = [&](RingPos<NP> c) { return bounded_wait_w(&t_full[c.at], c.round, abort_flag, 741, p.err); };
+    auto issue_s = [&](int b, RingPos<NP> c) {
       const uint32_t tSb = tS + 64 * b;
-      const uint64_t k = T::kmajor(k_tile(u) + 64 * T::SWB * b, 0);
+      const uint64_t k = T::kmajor(k_tile(c) + 64 * T::SWB * b, 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tQA + kk * 8, k + T::kmajor_step(kk), ID_S, kk > 0);
       umma_commit_w(&s_full[b]);
     };
-    auto issue_dp = [&](int u) {
-      const int b = u & 1;
+    auto issue_dp = [&](int b, RingPos<NP> c) {
       const uint32_t tdPb = tdP + 64 * b;
-      const uint64_t v = T::kmajor(k_tile(u) + T::TILE + 64 * T::SWB * b, 0);
+      const uint64_t v = T::kmajor(k_tile(c) + T::TILE + 64 * T::SWB * b, 0);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tdPb, tOA + kk * 8, v + T::kmajor_step(kk), ID_S, kk > 0);
       umma_commit_w(&dp_full[b]);
@@ -936,39 +931,42 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
       if (!ok) break;
       if (lane == 0) {
         // the tiles of Q and dO are free
-        uint64_t* bar = &t_empty[(tg + qi) % NP];
+        uint64_t* bar = &t_empty[c.at];
         mbar_arrive(bar);
         if (p.one_issuer) mbar_arrive(bar);
       }
-      ok = landed(b0);
+      c = c.next();
+      ok = landed(c);
       if (!ok) break;
       tc_fence_after();
       // sub-tiles 0 and 1 share the first tiles (U is even)
       for (int u = b0; u < 2; u += ustep) {
-        issue_s(u);
-        issue_dp(u);
+        issue_s(u, c);
+        issue_dp(u, c);
       }
       for (int u = b0; u < U; u += ustep) {
         const int b = u & 1;
         const uint32_t phase = (tg + (u >> 1)) & 1;
         const bool more = u + 2 < U;
+        const RingPos<NP> ahead = c.next();
         if (more) {
           // S(u+2) once the group has read S(u)
-          ok = bounded_wait_w(&s_free[b], phase, abort_flag, 743, p.err) && landed(u + 2);
+          ok = bounded_wait_w(&s_free[b], phase, abort_flag, 743, p.err) && landed(ahead);
           if (!ok) break;
           tc_fence_after();
-          issue_s(u + 2);
+          issue_s(b, ahead);
         }
         // dQ += dS(u) K_u: key rows 64b.. are K blocks 4b..4b+3 of the tile
         ok = bounded_wait_w(&ds_full[b], phase, abort_flag, 744, p.err);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t k = T::mnmajor(k_tile(u), 4 * b);
+        const uint64_t k = T::mnmajor(k_tile(c), 4 * b);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           umma_bf16_tmem_a_w(tdQ, tdP + 64 * b + kk * 8, k + T::mnmajor_step(kk), ID_DQ, 1);
-        umma_commit_w(&t_empty[pair(u) % NP]);
-        if (more) issue_dp(u + 2);  // over dS(u), after dQ(u) in issue order
+        umma_commit_w(&t_empty[c.at]);
+        if (more) issue_dp(b, ahead);  // over dS(u), after dQ(u) in issue order
+        if (ustep == 2 || b == 1) c = ahead;
       }
       if (!ok) break;
       // all_done counts two commits: one per issuer, or both from one

@@ -249,11 +249,12 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     const uint32_t uKV = smem_u32(sKV), uQ = smem_u32(sQ);
     const uint32_t tSb = tmem + 128 * b;
     const uint32_t tOb = tmem + C::COL_O + b * D;
-    int t = 0, c = 0, qi = 0;  // steps and pairs through all items, items with keys
-    auto landed = [&]() { return bounded_wait_w(&t_full[c % NP], (c / NP) & 1, abort_flag, 253, p.err); };
+    int t = 0, qi = 0;  // steps through all items, items with keys
+    RingPos<NP> c;      // pair
+    auto landed = [&]() { return bounded_wait_w(&t_full[c.at], c.round, abort_flag, 253, p.err); };
     auto pv = [&](int tp, bool first) -> bool {  // PV of step tp, its item's first
       const int sb = tp & 1;
-      const uint64_t v = T::mnmajor(uKV + (2 * (c % NP) + 1) * T::TILE, 4 * b);
+      const uint64_t v = T::mnmajor(uKV + (2 * c.at + 1) * T::TILE, 4 * b);
       if (!bounded_wait_w(&p_full[2 * b + sb], (tp >> 1) & 1, abort_flag, 255, p.err)) return false;
       if (first && qi > 0 && !bounded_wait_w(o_free, (qi - 1) & 1, abort_flag, 258, p.err)) return false;
       tc_fence_after();
@@ -275,20 +276,20 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       for (int j = 0; j < nkv; ++j, ++t) {
         if (!landed()) { ok = false; break; }
         tc_fence_after();
-        const uint64_t k = T::kmajor(uKV + 2 * (c % NP) * T::TILE + 64 * T::SWB * b, 0);
+        const uint64_t k = T::kmajor(uKV + 2 * c.at * T::TILE + 64 * T::SWB * b, 0);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma_bf16_w(tSb + (t & 1) * 64, q + T::kmajor_step(kk), k + T::kmajor_step(kk), IDESC_S, kk > 0);
         umma_commit_w(&s_full[2 * b + (t & 1)]);
         if (j == nkv - 1) umma_commit_w(&q_empty[qi & 1]);
         if (j > 0 && !pv(t - 1, j == 1)) { ok = false; break; }
-        umma_commit_w(&t_empty[c % NP]);
-        ++c;
+        umma_commit_w(&t_empty[c.at]);
+        c = c.next();
       }
       ok = ok && landed() && pv(t - 1, nkv == 1);
       if (!ok) break;
-      umma_commit_w(&t_empty[c % NP]);
-      ++c;
+      umma_commit_w(&t_empty[c.at]);
+      c = c.next();
       ++qi;
     }
     if (!ok) {
