@@ -24,15 +24,19 @@ namespace bpt {
 
 // Window of query row q (index in its sequence) of sequence bi: the given
 // begin and end, clamped to the sequence, and the causal limit; empty (0, 0)
-// where nothing is visible and for rows past the sequence.
+// where nothing is visible and for rows past the sequence.  In two steps, so
+// that a kernel can read a window long before it needs it.
+__device__ __forceinline__ int2 raw_window(const int32_t* row_begin, const int32_t* row_end, int s, int bi, int q) {
+  const long long at = (long long)bi * s + q;
+  return make_int2(row_begin && q < s ? row_begin[at] : 0, row_end && q < s ? row_end[at] : s);
+}
+__device__ __forceinline__ int2 clamped_window(int2 raw, int causal, int s, int q) {
+  const int lo = max(raw.x, 0), hi = causal ? min(min(raw.y, s), q + 1) : min(raw.y, s);
+  return q < s && lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+}
 __device__ __forceinline__ int2 key_window(const int32_t* row_begin, const int32_t* row_end, int causal, int s, int bi,
                                            int q) {
-  if (q >= s) return make_int2(0, 0);
-  const long long at = (long long)bi * s + q;
-  int lo = row_begin ? max(row_begin[at], 0) : 0;
-  int hi = row_end ? min(row_end[at], s) : s;
-  if (causal) hi = min(hi, q + 1);
-  return lo < hi ? make_int2(lo, hi) : make_int2(0, 0);
+  return clamped_window(raw_window(row_begin, row_end, s, bi, q), causal, s, q);
 }
 
 // The cap as the kernels take it: with z a raw score (q.k), x = z / sqrt(d)

@@ -32,11 +32,13 @@
 // still in the current one, and its first S is made during the current item's
 // merge.
 //
-// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: 433 us plain scores
-// (1,270 TFLOP/s of unmasked pairs), 480 capped (1,145), 469 biased; documents of
-// 1500: 126 us, 145 capped.  What bounds it is the chain S, modified softmax, P,
-// PV of each half (at 4096 rows, capped: tensor core 43% busy, issue slots 41%):
-// the two halves' warps overlap each other's waits but not all of them.
+// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: 370 us plain scores
+// (1,485 TFLOP/s of unmasked pairs), 434 capped (1,267), 424 biased; documents of
+// 1500: 121 us, 137 capped.  What bounds it: at d = 128 a step's products take
+// 1,280 of 1,620 cycles (S reads both operands from shared memory, 48 cycles for
+// 16 of depth and 64 columns), with a cap the chain S, modified softmax, P, PV of
+// each half.  The issuing warps' loops are part of that chain: with a barrier per
+// tile instead of per pair of K and V the plain scores took 434 us.
 #include <math.h>
 #include <string.h>
 
@@ -316,15 +318,21 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
         mbar_arrive(&q_empty[(items - 1) & 1]);
       }
     };
-    bool ok = true;
+    // an item and its row's window; the next one's are read during the merge
+    WorkItem w{-1, 0, 0, 0, 0};
+    int2 raw;
+    auto take = [&](int it) -> bool {
+      if (!next_item(queue, it, &w, abort_flag, p.err)) return false;
+      raw = w.n < 0 ? make_int2(0, 0) : raw_window(p.row_begin, p.row_end, p.s, w.bi, w.q0 + r);
+      return true;
+    };
+    bool ok = take(0);
     for (int it = 0; ok; ++it) {
-      WorkItem w;
-      if (!next_item(queue, it, &w, abort_flag, p.err)) break;
       const int n = w.n, bi = w.bi, qpos = w.q0 + r, j0 = w.j0, nkv = w.nkv;
       if (n < 0) break;
       // (an item without keys leaves it to the next one with some)
       if (nkv > 0) stored();
-      const int2 win = key_window(p.row_begin, p.row_end, p.causal, p.s, bi, qpos);
+      const int2 win = clamped_window(raw, p.causal, p.s, qpos);
       const bool valid = qpos < p.s;
       __nv_bfloat16* orow = p.o + (((long long)bi * p.s + qpos) * p.H + n) * D;
       float* lse = p.lse ? p.lse + ((long long)bi * p.H + n) * p.s_pad + qpos : nullptr;
@@ -337,6 +345,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
           }
           if (lse) *lse = valid ? NEG_INF : 0.f;
         }
+        ok = take(it + 1);
         continue;
       }
       const float slope2 = BIAS ? p.slopes[n] * 1.4426950408889634f : 0.f;
@@ -518,6 +527,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[2 * b + sb]);
       }
+      if (ok) ok = take(it + 1);
       if (ok) ok = __all_sync(0xffffffffu, bounded_wait(&pv_done[b], (t - 1) & 1, abort_flag, 263, p.err));
       if (!ok) break;
       // merge: each half leaves its maxima and row sums for the other
