@@ -371,6 +371,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
     const uint32_t uZero = smem_u32(sZero);
     int tg = 0, ki = 0;  // stages, items with pairs before this one
     RingPos<QS> c;       // the sub-tile's stage
+    const bool leader = elected();
     bool ok = true;
     // the 64 query rows of sub-tile half b start 64 b rows into every
     // chunk of the stage's tiles (whole swizzle atoms), and 64 b rows into
@@ -387,35 +388,41 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
       const uint32_t tSb = tS + 64 * b;
       const uint64_t q = T::kmajor(stage_at(c) + 64 * T::SWB * b, 0);
       const uint32_t uA = stage_at(c) + 2 * T::TILE + 64 * 16 * b;
-      if constexpr (C::KV_TMEM) {
+      if (leader) {
+        if constexpr (C::KV_TMEM) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_tmem_a_w(tSb, tKA + kk * 8, q + T::kmajor_step(kk), ID_S, kk > 0);
-        umma_bf16_tmem_a_w(tSb, tKA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
-      } else {
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_tmem_a_1(tSb, tKA + kk * 8, q + T::kmajor_step(kk), ID_S, kk > 0);
+          umma_bf16_tmem_a_1(tSb, tKA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_w(tSb, dK + T::kmajor_step(kk), q + T::kmajor_step(kk), ID_S, kk > 0);
-        umma_bf16_w(tSb, dKx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_1(tSb, dK + T::kmajor_step(kk), q + T::kmajor_step(kk), ID_S, kk > 0);
+          umma_bf16_1(tSb, dKx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+        }
+        umma_commit_1(&s_full[b]);
       }
-      umma_commit_w(&s_full[b]);
+      __syncwarp();
     };
     auto issue_dp = [&](int b, RingPos<QS> c) {
       const uint32_t tdPb = tdP + 64 * b;
       const uint64_t o = T::kmajor(stage_at(c) + T::TILE + 64 * T::SWB * b, 0);
       const uint32_t uA = stage_at(c) + 2 * T::TILE + 64 * 16 * b;
-      if constexpr (C::KV_TMEM) {
+      if (leader) {
+        if constexpr (C::KV_TMEM) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_tmem_a_w(tdPb, tVA + kk * 8, o + T::kmajor_step(kk), ID_S, kk > 0);
-        umma_bf16_tmem_a_w(tdPb, tVA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
-      } else {
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_tmem_a_1(tdPb, tVA + kk * 8, o + T::kmajor_step(kk), ID_S, kk > 0);
+          umma_bf16_tmem_a_1(tdPb, tVA + D / 2, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_w(tdPb, dV + T::kmajor_step(kk), o + T::kmajor_step(kk), ID_S, kk > 0);
-        umma_bf16_w(tdPb, dVx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_1(tdPb, dV + T::kmajor_step(kk), o + T::kmajor_step(kk), ID_S, kk > 0);
+          umma_bf16_1(tdPb, dVx, sdesc(uA, uZero - uA, 128, 0u), ID_S, 1);
+        }
+        umma_commit_1(&dp_full[b]);
       }
-      umma_commit_w(&dp_full[b]);
+      __syncwarp();
     };
     auto wait_stage = [&](RingPos<QS> c) {
       return bounded_wait_w(&qdo_full[c.at], c.round, abort_flag, 711, p.err);
@@ -447,9 +454,12 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
         ok = bounded_wait_w(&p_full[b], phase, abort_flag, 713, p.err);
         if (!ok) break;
         tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16_tmem_a_w(tdV, tSb + kk * 8, dOm + T::mnmajor_step(kk), ID_KV, 1);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_tmem_a_1(tdV, tSb + kk * 8, dOm + T::mnmajor_step(kk), ID_KV, 1);
+        }
+        __syncwarp();
         if (more) {
           // S(u+2) overwrites P^T(u), after dV(u) in issue order
           ok = wait_stage(ahead);
@@ -461,23 +471,29 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
         ok = bounded_wait_w(&ds_full[b], phase, abort_flag, 714, p.err);
         if (!ok) break;
         tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16_tmem_a_w(tdK, tdPb + kk * 8, dQm + T::mnmajor_step(kk), ID_KV, 1);
-        umma_commit_w(&qdo_empty[c.at]);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_tmem_a_1(tdK, tdPb + kk * 8, dQm + T::mnmajor_step(kk), ID_KV, 1);
+          umma_commit_1(&qdo_empty[c.at]);
+        }
+        __syncwarp();
         // dP(u+2) overwrites dS^T(u), after dK(u) in issue order
         if (more) issue_dp(b, ahead);
         if (ustep == 2 || b == 1) c = ahead;
       }
       if (!ok) break;
       // all_done counts two commits: one per issuer, or both from one
-      umma_commit_w(all_done);
-      if (p.one_issuer) umma_commit_w(all_done);
+      if (leader) {
+        umma_commit_1(all_done);
+        if (p.one_issuer) umma_commit_1(all_done);
+      }
+      __syncwarp();
       tg += T_iter;
       ++ki;
     }
     if (!ok) {
-      umma_commit_w(&drain[b0]);
+      if (leader) umma_commit_1(&drain[b0]);
       drain_wait(&drain[b0], 0);
     }
   } else {
@@ -904,21 +920,28 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
     // qi: key tiles, items with keys before this one
     int tg = 0, qi = 0;
     RingPos<NP> c;  // the pair of K and V (before an item's first, of Q and dO)
+    const bool leader = elected();
     auto k_tile = [&](RingPos<NP> c) { return ring + 2 * c.at * T::TILE; };
     auto landed = [&](RingPos<NP> c) { return bounded_wait_w(&t_full[c.at], c.round, abort_flag, 741, p.err); };
     auto issue_s = [&](int b, RingPos<NP> c) {
       const uint32_t tSb = tS + 64 * b;
       const uint64_t k = T::kmajor(k_tile(c) + 64 * T::SWB * b, 0);
+      if (leader) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tSb, tQA + kk * 8, k + T::kmajor_step(kk), ID_S, kk > 0);
-      umma_commit_w(&s_full[b]);
+        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_1(tSb, tQA + kk * 8, k + T::kmajor_step(kk), ID_S, kk > 0);
+        umma_commit_1(&s_full[b]);
+      }
+      __syncwarp();
     };
     auto issue_dp = [&](int b, RingPos<NP> c) {
       const uint32_t tdPb = tdP + 64 * b;
       const uint64_t v = T::kmajor(k_tile(c) + T::TILE + 64 * T::SWB * b, 0);
+      if (leader) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_w(tdPb, tOA + kk * 8, v + T::kmajor_step(kk), ID_S, kk > 0);
-      umma_commit_w(&dp_full[b]);
+        for (int kk = 0; kk < D / 16; ++kk) umma_bf16_tmem_a_1(tdPb, tOA + kk * 8, v + T::kmajor_step(kk), ID_S, kk > 0);
+        umma_commit_1(&dp_full[b]);
+      }
+      __syncwarp();
     };
     bool ok = true;
     for (int it = 0; ok; ++it) {
@@ -961,22 +984,28 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
         if (!ok) break;
         tc_fence_after();
         const uint64_t k = T::mnmajor(k_tile(c), 4 * b);
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_bf16_tmem_a_w(tdQ, tdP + 64 * b + kk * 8, k + T::mnmajor_step(kk), ID_DQ, 1);
-        umma_commit_w(&t_empty[c.at]);
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_tmem_a_1(tdQ, tdP + 64 * b + kk * 8, k + T::mnmajor_step(kk), ID_DQ, 1);
+          umma_commit_1(&t_empty[c.at]);
+        }
+        __syncwarp();
         if (more) issue_dp(b, ahead);  // over dS(u), after dQ(u) in issue order
         if (ustep == 2 || b == 1) c = ahead;
       }
       if (!ok) break;
       // all_done counts two commits: one per issuer, or both from one
-      umma_commit_w(all_done);
-      if (p.one_issuer) umma_commit_w(all_done);
+      if (leader) {
+        umma_commit_1(all_done);
+        if (p.one_issuer) umma_commit_1(all_done);
+      }
+      __syncwarp();
       tg += w.nkv;
       ++qi;
     }
     if (!ok) {
-      umma_commit_w(&drain[b0]);
+      if (leader) umma_commit_1(&drain[b0]);
       drain_wait(&drain[b0], 0);
     }
   } else {

@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     const uint32_t tOb = tmem + C::COL_O + b * D;
     int t = 0, qi = 0;  // steps through all items, items with keys
     RingPos<NP> c;      // pair
+    const bool leader = elected();
     auto landed = [&]() { return bounded_wait_w(&t_full[c.at], c.round, abort_flag, 253, p.err); };
     auto pv = [&](int tp, bool first) -> bool {  // PV of step tp, its item's first
       const int sb = tp & 1;
@@ -260,10 +261,14 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
       if (!bounded_wait_w(&p_full[2 * b + sb], (tp >> 1) & 1, abort_flag, 255, p.err)) return false;
       if (first && qi > 0 && !bounded_wait_w(o_free, (qi - 1) & 1, abort_flag, 258, p.err)) return false;
       tc_fence_after();
+      if (leader) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        umma_bf16_tmem_a_w(tOb, tSb + sb * 64 + kk * 8, v + T::mnmajor_step(kk), IDESC_PV, !first || kk > 0);
-      umma_commit_w(&pv_done[b]);
+        for (int kk = 0; kk < 4; ++kk)
+          umma_bf16_tmem_a_1(tOb, tSb + sb * 64 + kk * 8, v + T::mnmajor_step(kk), IDESC_PV, !first || kk > 0);
+        umma_commit_1(&pv_done[b]);
+        umma_commit_1(&t_empty[c.at]);
+      }
+      __syncwarp();
       return true;
     };
     bool ok = true;
@@ -279,23 +284,25 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
         if (!landed()) { ok = false; break; }
         tc_fence_after();
         const uint64_t k = T::kmajor(uKV + 2 * c.at * T::TILE + 64 * T::SWB * b, 0);
+        if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_bf16_w(tSb + (t & 1) * 64, q + T::kmajor_step(kk), k + T::kmajor_step(kk), IDESC_S, kk > 0);
-        umma_commit_w(&s_full[2 * b + (t & 1)]);
-        if (j == nkv - 1) umma_commit_w(&q_empty[qi & 1]);
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_bf16_1(tSb + (t & 1) * 64, q + T::kmajor_step(kk), k + T::kmajor_step(kk), IDESC_S, kk > 0);
+          umma_commit_1(&s_full[2 * b + (t & 1)]);
+          if (j == nkv - 1) umma_commit_1(&q_empty[qi & 1]);
+          if (j == 0) umma_commit_1(&t_empty[c.at]);
+        }
+        __syncwarp();
         if (j > 0 && !pv(t - 1, j == 1)) { ok = false; break; }
-        umma_commit_w(&t_empty[c.at]);
         c = c.next();
       }
       ok = ok && landed() && pv(t - 1, nkv == 1);
       if (!ok) break;
-      umma_commit_w(&t_empty[c.at]);
       c = c.next();
       ++qi;
     }
     if (!ok) {
-      umma_commit_w(&drain[b]);
+      if (leader) umma_commit_1(&drain[b]);
       drain_wait(&drain[b], 0);
     }
   } else {
