@@ -26,8 +26,8 @@
 // signs that do not build up; dqkv is off by 2.5e-3 to 3.3e-3 (relative norm, its
 // own bf16 rounding of 1.7e-3 included).
 //
-// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: dK/dV 795 us, dQ 475,
-// capped 905 and 590; documents of 1500: 205 and 145.  dK/dV is bound by its four
+// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: dK/dV 802 us, dQ 457,
+// capped 900 and 580; documents of 1500: 200 and 139.  dK/dV is bound by its four
 // products (tensor core 57 to 70% busy: at head dims above 80 S^T and dP^T take
 // both operands from shared memory, and 64 columns of them cost 48 cycles a step of
 // 16 where 32 are arithmetic) and by the chain between them; one product of 128

@@ -33,8 +33,8 @@
 // merge.
 //
 // Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: 370 us plain scores
-// (1,485 TFLOP/s of unmasked pairs), 434 capped (1,267), 424 biased; documents of
-// 1500: 121 us, 137 capped.  What bounds it: at d = 128 a step's products take
+// (1,485 TFLOP/s of unmasked pairs), 434 capped (1,267), 413 biased; documents of
+// 1500: 119 us, 136 capped.  What bounds it: at d = 128 a step's products take
 // 1,280 of 1,620 cycles (S reads both operands from shared memory, 48 cycles for
 // 16 of depth and 64 columns), with a cap the chain S, modified softmax, P, PV of
 // each half.  The issuing warps' loops are part of that chain: with a barrier per
