@@ -19,7 +19,7 @@ int check(const bpt_config* cfg, const bpt_score_mod* mod, PackedDims* D) {
   if ((reinterpret_cast<uintptr_t>(mod->row_begin) & 3) || (reinterpret_cast<uintptr_t>(mod->row_end) & 3) ||
       (reinterpret_cast<uintptr_t>(mod->slopes) & 3))
     return BPT_EINVAL;
-  // 0: no cap; outside these the powers in the cap's polynomials would leave
+  // 0: no cap; outside these the powers in the cap's first polynomial would leave
   // fp32, and no score is that small or large
   if (!(mod->softcap == 0.f || (mod->softcap >= 0x1p-10f && mod->softcap <= 0x1p20f))) return BPT_EINVAL;
   // grid sizes, 32-bit columns and the extra rows' 32-bit row coordinate

@@ -10,10 +10,15 @@
 // units already bound the softmax.  Trained scores sit well inside the cap, so
 // a warp whose 64 columns all have |x| <= C/4 takes an odd polynomial of
 // degree 5 in x (error 8e-8 C, below an fp32 step of the largest of them),
-// within 0.6 C one of degree 9 (3e-8 C), both in packed fp32 arithmetic, and
-// only beyond that the exact form.
+// within 0.6 C one of degree 9 (3e-8 C), both in packed fp32 arithmetic.  Only
+// beyond that the exponential is taken, whose error of 2^-23 C would swamp small
+// scores under a large cap: those keep the first polynomial, element by element.
+// So a capped score is right to 2^-21 of itself, whatever the cap and the warp's
+// other scores are.
 #pragma once
 
+#include <float.h>
+#include <math.h>
 #include <string.h>
 
 #include <algorithm>
@@ -44,7 +49,7 @@ __device__ __forceinline__ int2 key_window(const int32_t* row_begin, const int32
 // in powers of z: z (c[0] + w (c[1] + w c[2])) for |k z| <= 0.25 and
 // z (e[0] + w (e[1] + ... )) for |k z| <= 0.6, w = z^2, each times `out`.
 struct CapCoef {
-  float near1, near2;  // largest |z| of the two
+  float near1, near2;  // largest |z| of the two (near2 = near1: the second is not taken)
   uint64_t c[3], e[5];  // the coefficients, twice each: operands of packed arithmetic
   float k2, out;        // 2 log2(e) k, and what tanh is multiplied with
 };
@@ -59,13 +64,18 @@ inline CapCoef cap_coef(double k, double out) {
   CapCoef f;
   f.near1 = (float)(0.25 / k);
   f.near2 = (float)(0.6 / k);
-  double kk = k * out;
+  double kk = k * out, least = INFINITY;
   for (int i = 0; i < 5; ++i, kk *= k * k) {
     if (i < 3) f.c[i] = twice((float)(n5[i] * kk));
     f.e[i] = twice((float)(n9[i] * kk));
+    least = std::min(least, fabs(n9[i] * kk));
   }
   f.k2 = (float)(2.8853900817779268 * k);
   f.out = (float)out;
+  // Under a large cap the powers of k leave fp32 (from C = 917 at d = 128 where
+  // out = 1; caps of up to 2^20 leave the first polynomial's within it): lost terms
+  // would be wrong scores, so the exact form takes the second one's range.
+  if (least < FLT_MIN) f.near2 = f.near1;
   return f;
 }
 __device__ __forceinline__ uint64_t both(float v) { return f2(v, v); }
@@ -82,6 +92,20 @@ __device__ __forceinline__ uint64_t near2_factor(const CapCoef& f, uint64_t z) {
 }
 __device__ __forceinline__ uint64_t cap_near1(const CapCoef& f, uint64_t z) { return mul2(z, near1_factor(f, z)); }
 __device__ __forceinline__ uint64_t cap_near2(const CapCoef& f, uint64_t z) { return mul2(z, near2_factor(f, z)); }
+
+// tanh(y) = 1 - 2 / (1 + e^(2y)): absolute error about 2^-23, saturating
+// exactly; y2 = 2 log2(e) y
+__device__ __forceinline__ float tanh_any(float y2) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y2)));
+  return fmaf(-2.f, r, 1.f);
+}
+// the capped scores of a pair beyond the polynomials' ranges
+__device__ __forceinline__ uint64_t cap_far(const CapCoef& f, uint64_t z) {
+  const float2 v = f2split(z), near = f2split(cap_near1(f, z));
+  return f2(fabsf(v.x) <= f.near1 ? near.x : tanh_any(v.x * f.k2) * f.out,
+            fabsf(v.y) <= f.near1 ? near.y : tanh_any(v.y * f.k2) * f.out);
+}
 
 // The order of the grid: work items of tiles x heads, the tiles of all heads
 // of a group in turn, first tile index first, then the next group, so that a
@@ -207,14 +231,6 @@ __device__ __forceinline__ bool next_item(const WorkQueue& q, int it, WorkItem* 
   *w = WorkItem{from->n, from->bi, from->q0, from->j0, from->nkv};
   if (!keep) release_item(q, it);
   return true;
-}
-
-// tanh(y) = 1 - 2 / (1 + e^(2y)): absolute error about 2^-23, saturating
-// exactly; y2 = 2 log2(e) y
-__device__ __forceinline__ float tanh_any(float y2) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y2)));
-  return fmaf(-2.f, r, 1.f);
 }
 
 // 64 score columns of this thread's row, and the largest of them (of their

@@ -103,7 +103,7 @@ __device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&
       for (int k = 0; k < 64; k += 2) put(k, cap_near2(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
     } else {
 #pragma unroll
-      for (int k = 0; k < 64; ++k) sv[k] = __float_as_uint(tanh_any(__uint_as_float(sv[k]) * p.cap.k2));
+      for (int k = 0; k < 64; k += 2) put(k, cap_far(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
     }
   }
   if (!all) {

@@ -462,8 +462,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
                 for (int i = 0; i < 64; i += 2) put(i, cap_near2(p.cap, z2(i)));
               } else {
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                  sv[i] = __float_as_uint(tanh_any(__uint_as_float(sv[i]) * p.cap.k2) * p.cap.out);
+                for (int i = 0; i < 64; i += 2) put(i, cap_far(p.cap, z2(i)));
               }
             }
             if (BIAS) {
