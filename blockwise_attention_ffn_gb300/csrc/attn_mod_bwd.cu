@@ -101,9 +101,13 @@ __device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&
     } else if (__all_sync(0xffffffffu, am <= p.cap.near2)) {
 #pragma unroll
       for (int k = 0; k < 64; k += 2) put(k, cap_near2(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
-    } else {
+    } else if (!p.cap.large) {
 #pragma unroll
       for (int k = 0; k < 64; k += 2) put(k, cap_far(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 64; k += 2)
+        put(k, cap_far_large(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
     }
   }
   if (!all) {
@@ -1354,7 +1358,7 @@ int attention_mod_bwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   p.scale = 1.f / sqrtf((float)D.d);
   p.scale_log2 = p.scale * 1.4426950408889634f;
   if (cap) {
-    p.cap = cap_coef(1.0 / (mod.softcap * sqrt((double)D.d)), 1.0);
+    p.cap = cap_coef(mod.softcap, 1.0 / (mod.softcap * sqrt((double)D.d)), 1.0);
     p.cap_log2 = mod.softcap * 1.4426950408889634f;
   }
   p.one_issuer = D.det ? 1 : 0;

@@ -460,9 +460,12 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
               } else if (near2) {
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) put(i, cap_near2(p.cap, z2(i)));
-              } else {
+              } else if (!p.cap.large) {
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) put(i, cap_far(p.cap, z2(i)));
+              } else {
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) put(i, cap_far_large(p.cap, z2(i)));
               }
             }
             if (BIAS) {
@@ -655,7 +658,7 @@ int attention_mod_fwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   const bool cap = mod.softcap > 0.f;
   if (cap) {
     const double out = mod.softcap * 1.4426950408889634;
-    p.cap = cap_coef(1.0 / (mod.softcap * sqrt((double)D.d)), out);
+    p.cap = cap_coef(mod.softcap, 1.0 / (mod.softcap * sqrt((double)D.d)), out);
     p.bounded = out <= 88.0;
   }
   p.err = device_error_word();

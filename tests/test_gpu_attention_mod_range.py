@@ -93,7 +93,7 @@ def test_caps_of_every_size(cap, slope, d):
     one_head(s, d, 0, cap, slope, x, do)
 
 
-@pytest.mark.parametrize("cap", [50.0, 8192.0, 2.0 ** 20])
+@pytest.mark.parametrize("cap", [20.0, 50.0, 64.0, 65.0, 8192.0, 2.0 ** 20])
 def test_small_scores_beside_large_ones(cap):
     """Rows of a few units among rows beyond the cap: a row's scores keep their
     own accuracy whatever its neighbours in the tile are."""
