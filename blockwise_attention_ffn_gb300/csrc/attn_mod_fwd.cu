@@ -8,10 +8,13 @@
 //  * A tile's first and last key tile come from its rows' windows, so packed
 //    documents, prefixes and padding cost only the tiles that some row sees.
 //  * Scores are modified between the tensor core and the softmax.  With a cap
-//    of at most 61 the exponentials stay within 2^-88 and 2^88, which leaves
-//    fp32 sums 2^39 for keys and values: no maximum is looked for, m = 0 (or
-//    the largest bias seen).  Biased scores without a cap take the load's own
-//    maximum and the nearest key's bias for an upper bound of theirs.
+//    of at most 61, scores within 0.6 C (where a polynomial does for the tanh)
+//    have exponentials between 2^-47 and 2^47: no maximum is looked for in such
+//    a tile, m is at least 0 (with a bias the largest bias seen, less up to 8).
+//    That leaves fp32 sums 2^72 for values times keys.  Tiles with a score beyond
+//    0.6 C take their maximum: with m = 0 there too, P reached 2^88 and values of
+//    2^39 over the keys overflowed.  Biased scores without a cap take the load's
+//    own maximum and the nearest key's bias for an upper bound of theirs.
 //  * Row sums are fp32 sums of the fp32 exponentials, so the log-sum-exp is an
 //    fp32-exact output; the tensor core's row sums of bf16 P would be off by
 //    up to 2^-9.
@@ -63,7 +66,7 @@ struct ModFwdParams {
   const float* slopes;
   float scale_log2;  // log2(e)/sqrt(d)
   CapCoef cap;       // capped scores in log2 units
-  int bounded;  // the capped scores' exponentials and their sums stay in fp32's range
+  float bounded;  // largest |z| of capped scores that need no maximum (negative: none)
   unsigned int* err;
 };
 
@@ -316,8 +319,6 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
     // the units of m and of the scores when exponentiated: raw scores times
     // log2(e)/sqrt(d) without a modifier, else already log2
     const float ce = (CAP || BIAS) ? 1.f : p.scale_log2;
-    // bounded scores: the maximum is that of the bias alone (0 without one)
-    const bool bounded = CAP && p.bounded;
     int t = 0, items = 0;  // steps, through all items, and items with keys
     auto stored = [&]() {  // the last item's O has left its Q buffer
       if (lane == 0 && items > 0) {
@@ -356,20 +357,32 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
         continue;
       }
       const float slope2 = BIAS ? p.slopes[n] * 1.4426950408889634f : 0.f;
-      float m_run = bounded && !BIAS ? 0.f : NEG_INF, l_run = 0.f;
+      // capped without a bias: 0 until the warp meets a tile beyond 0.6 C, so that
+      // the ordinary ones need not look at it
+      bool zero = CAP && !BIAS && p.bounded > 0.f;
+      float m_run = zero ? 0.f : NEG_INF, l_run = 0.f;
       // a maximum taken from the raw scores and the nearest key's bias is too
       // large by what the bias falls within the 64 columns: 2^-40 at most of P
       const bool gentle = fabsf(slope2) <= 0.6f;
       for (int j = 0; j < nkv; ++j, ++t) {
         const int sb = t & 1;
         const uint32_t tb = tSb + sb * 64 + lane_off;
-        ok = bounded_wait(&s_full[2 * b + sb], (t >> 1) & 1, abort_flag, 261, p.err);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        tc_fence_after();
         // this half's key columns [klo, khi) of the 64 are visible
         const int kv0 = key_tile(j, j0, nkv) * 128 + 64 * b;
         const int klo = max(win.x - kv0, 0), khi = min(win.y - kv0, 64);
         const bool full = klo == 0 && khi == 64;
+        float top = NEG_INF;
+        if (BIAS) {
+          // the nearest visible key's bias is the tile's largest (with a
+          // negative slope the farthest one's)
+          const int first = kv0 + klo, last = kv0 + khi - 1;
+          const int dist = slope2 >= 0.f ? abs(qpos - min(max(qpos, first), last))
+                                         : max(abs(qpos - first), abs(qpos - last));
+          if (klo < khi) top = -slope2 * (float)dist;
+        }
+        ok = bounded_wait(&s_full[2 * b + sb], (t >> 1) & 1, abort_flag, 261, p.err);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
         uint32_t pk[32];
         bool rescale = false;
         float alpha = 1.f;
@@ -404,28 +417,27 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
             }
           };
           const bool all = __all_sync(0xffffffffu, full);
-          bool near1 = false, near2 = false, done = false;
+          bool near1 = false, bounded = false, done = false;
           if constexpr (CAP) {
             near1 = __all_sync(0xffffffffu, largest <= p.cap.near1);
-            near2 = near1 || __all_sync(0xffffffffu, largest <= p.cap.near2);
+            // scores so far within the cap that a reference of 0, or the largest
+            // bias, serves for their maximum
+            bounded = __all_sync(0xffffffffu, largest <= p.bounded);
           }
           BiasLine line{0.f, 0.f, false};
           if (BIAS) line = bias_line(slope2, qpos, kv0, 64, p.causal != 0, false);
-          if (BIAS && (bounded || (!CAP && gentle && all))) {
-            // the nearest visible key's bias bounds the tile's (with a
-            // negative slope the farthest one's)
-            const int first = kv0 + klo, last = kv0 + khi - 1;
-            const int dist = slope2 >= 0.f ? abs(qpos - min(max(qpos, first), last))
-                                           : max(abs(qpos - first), abs(qpos - last));
-            const float top = klo < khi ? -slope2 * (float)dist : NEG_INF;
-            refer(bounded ? top : fmaf(largest, p.scale_log2, top));
+          if (BIAS && bounded) refer(top);
+          if (BIAS && !CAP && gentle && all) refer(fmaf(largest, p.scale_log2, top));
+          if (CAP && !BIAS && bounded && !zero) {
+            refer(0.f);
+            zero = __all_sync(0xffffffffu, m_run == 0.f);
           }
           // nothing masked and no maximum to look for: straight to the
           // exponentials, of (score) + (bias - m) on the line
           if (all && (!BIAS || !__any_sync(0xffffffffu, line.mixed))) {
             const uint64_t step2 = both(line.step), base2 = both(line.base - m_run);
             if constexpr (CAP) {
-              if (bounded && near2) {
+              if (bounded && (BIAS || zero)) {
                 done = true;
                 if (!BIAS) {
                   if (near1) exps([&](int i) { return cap_near1(p.cap, z2(i)); });
@@ -457,7 +469,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
               if (near1) {
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) put(i, cap_near1(p.cap, z2(i)));
-              } else if (near2) {
+              } else if (__all_sync(0xffffffffu, largest <= p.cap.near2)) {
 #pragma unroll
                 for (int i = 0; i < 64; i += 2) put(i, cap_near2(p.cap, z2(i)));
               } else if (!p.cap.large) {
@@ -498,13 +510,14 @@ __global__ void __launch_bounds__(384, 1) attn_mod_fwd_kernel(const __grid_const
 #pragma unroll
               for (int i = 0; i < 64; i += 2)
                 m4[(i >> 1) & 3] = max3f(m4[(i >> 1) & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+              if (CAP && !BIAS && l_run == 0.f) m_run = NEG_INF;  // nothing seen yet
               refer(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+              zero = false;
             }
             // a row that has seen no key keeps m = -inf: offset 0, P = 2^-inf
             const float mc = (m_run == NEG_INF) ? 0.f : m_run * ce;
             const uint64_t c2 = both(ce), nmc2 = both(-mc);
-            if (bounded && !BIAS) exps(z2);
-            else exps([&](int i) { return fma2(z2(i), c2, nmc2); });
+            exps([&](int i) { return fma2(z2(i), c2, nmc2); });
           }
           const float2 rsum = f2split(add2(rs[0], rs[1]));
           l_run = fmaf(l_run, alpha, rsum.x + rsum.y);
@@ -659,7 +672,7 @@ int attention_mod_fwd(const PackedDims& D, int causal, const bpt_score_mod& mod,
   if (cap) {
     const double out = mod.softcap * 1.4426950408889634;
     p.cap = cap_coef(mod.softcap, 1.0 / (mod.softcap * sqrt((double)D.d)), out);
-    p.bounded = out <= 88.0;
+    p.bounded = out <= 88.0 ? p.cap.near2 : -1.f;
   }
   p.err = device_error_word();
   if (!p.err) return BPT_ECUDA;

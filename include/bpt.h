@@ -332,7 +332,9 @@ int bpt_attention_bwd_noalloc(const bpt_config* cfg, const void* qkv, const void
  * lse [b, H, s_pad] is an fp32-accurate sum (0 in the rows past s); the
  * backward takes it back with o.  Biases far beyond the scores' size cost the
  * rebuilt probabilities what lse's fp32 cannot hold (2^-24 of its size); the
- * windows above keep near keys in view, where lse is small.  Rows that no
+ * windows above keep near keys in view, where lse is small.  The forward's
+ * sums are finite while |v| times the number of visible keys stays below 2^72
+ * with a cap of at most 61, below 2^119 otherwise.  Rows that no
  * window reaches may hold any finite values: they leave no trace.  An infinity
  * or a NaN in V does (0 * inf) wherever its 128-key tile is loaded, as in
  * bpt_attention_fwd.

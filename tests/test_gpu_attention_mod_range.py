@@ -1,5 +1,5 @@
 """The modified attention over the whole range of caps and scores: caps up to
-the largest accepted, scores at and beyond the cap.
+the largest accepted, scores at and beyond the cap, values of any size.
 
 Every score here is one product: a query has a single nonzero column, so q.k is
 exact in fp32 and a score's error comes from its modification alone.  That is
@@ -100,6 +100,18 @@ def test_small_scores_beside_large_ones(cap):
     s, d = 384, 80
     x, do = inputs(s, d, [3.0, 1.5 * cap, 0.5], seed=3, block=1)
     one_head(s, d, 0, cap, 0.0, x, do)
+
+
+@pytest.mark.parametrize("v_scale", [2.0 ** 55, 1.0, 2.0 ** -60])
+@pytest.mark.parametrize("signs", ["plus", "minus", "both"])
+@pytest.mark.parametrize("slope", [0.0, 0.02, -0.02, 2.0])
+@pytest.mark.parametrize("cap", [60.0, 30.0])
+def test_saturated_scores(cap, slope, signs, v_scale):
+    """Whole rows at +cap and at -cap, beside rows in the cap's nearly linear
+    range, with values far from 1."""
+    s, d = 640, 64
+    x, do = inputs(s, d, [3 * cap, 0.55 * cap, 0.1 * cap, cap], seed=4, v_scale=v_scale, block=96, signs=signs)
+    one_head(s, d, 1, cap, slope, x, do)
 
 
 @pytest.mark.parametrize("slope", [0.0, 0.02, 1.5])
