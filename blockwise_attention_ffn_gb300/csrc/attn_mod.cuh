@@ -258,6 +258,22 @@ __device__ __forceinline__ float load_scores(uint32_t taddr, uint32_t (&sv)[64])
   return fmaxf(a, b);
 }
 
+// the largest magnitude of the columns that on(i) says, NaN left out
+template <class On>
+__device__ __forceinline__ float largest_of(const uint32_t (&sv)[64], On on) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    if (on(i)) m = fmaxf(m, fabsf(__uint_as_float(sv[i])));
+  return m;
+}
+// of the columns [lo, hi), lo < hi
+__device__ __forceinline__ float largest_within(const uint32_t (&sv)[64], int lo, int hi) {
+  const uint64_t bits = lo < hi ? ~0ull << lo & ~0ull >> (64 - hi) : 0ull;
+  const uint32_t b0 = (uint32_t)bits, b1 = (uint32_t)(bits >> 32);
+  return largest_of(sv, [&](int i) { return ((i < 32 ? b0 >> i : b1 >> (i - 32)) & 1u) != 0u; });
+}
+
 // The bias -a |i - j| along a run of n consecutive indices from `first`
 // against the fixed index `self`, as base + k * step for k < n, unless
 // the run passes `self` strictly inside (mixed).  below_only: indices above

@@ -82,12 +82,13 @@ struct ModBwdParams {
 // exp2 of 64 modified scores in log2 units and what dx multiplies (dP - D)
 // with: sv in, am their largest magnitude, pe = P (1 - u^2) out, pk = P as
 // bf16 pairs (WANT_P).  add(k): what is added to the scaled scores of the pair
-// (k, k + 1), the bias and -LSE; on(k): visible; all: every element is.
+// (k, k + 1), the bias and -LSE; on(k): visible; all: every element is; seen(sv):
+// the largest magnitude of the visible ones.
 // A masked u is replaced by one whose exponential is 0 and whose square is
 // finite, in a pass of its own, so that unmasked sub-tiles pay nothing for it.
-template <bool CAP, bool WANT_P, class Add, class On>
+template <bool CAP, bool WANT_P, class Add, class On, class Seen>
 __device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&sv)[64], float am, float (&pe)[64],
-                                              uint32_t (&pk)[32], bool all, Add add, On on) {
+                                              uint32_t (&pk)[32], bool all, Add add, On on, Seen seen) {
   if constexpr (CAP) {
     // u over sv
     auto put = [&](int k, uint64_t v) {
@@ -98,16 +99,25 @@ __device__ __forceinline__ void probabilities(const ModBwdParams& p, uint32_t (&
     if (__all_sync(0xffffffffu, am <= p.cap.near1)) {
 #pragma unroll
       for (int k = 0; k < 64; k += 2) put(k, cap_near1(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
-    } else if (__all_sync(0xffffffffu, am <= p.cap.near2)) {
-#pragma unroll
-      for (int k = 0; k < 64; k += 2) put(k, cap_near2(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
-    } else if (!p.cap.large) {
-#pragma unroll
-      for (int k = 0; k < 64; k += 2) put(k, cap_far(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
     } else {
+      // masked scores have no say in the form that the others take, as in the
+      // forward (tiles beyond C/4: 4% of the whole backward at documents of 4000,
+      // cap 30, 794 us without, 826 so; a form of its own for masked tiles 840)
+      if (!all) am = seen(sv);
+      if (__all_sync(0xffffffffu, am <= p.cap.near1)) {
 #pragma unroll
-      for (int k = 0; k < 64; k += 2)
-        put(k, cap_far_large(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
+        for (int k = 0; k < 64; k += 2) put(k, cap_near1(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
+      } else if (__all_sync(0xffffffffu, am <= p.cap.near2)) {
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) put(k, cap_near2(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
+      } else if (!p.cap.large) {
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) put(k, cap_far(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 64; k += 2)
+          put(k, cap_far_large(p.cap, f2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1]))));
+      }
     }
   }
   if (!all) {
@@ -600,6 +610,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
           const int2 w = win[x];
           return (unsigned)(kvp - w.x) < (unsigned)w.y;
         };
+        auto seen = [&](const uint32_t (&sv)[64]) { return largest_of(sv, on); };
         float pe[64];
         uint32_t pk[32];
         {
@@ -611,7 +622,7 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
             else return 0ull;
           };
           if constexpr (!BIAS) {
-            probabilities<CAP, true>(p, sv, am, pe, pk, all, lse2, on);
+            probabilities<CAP, true>(p, sv, am, pe, pk, all, lse2, on, seen);
           } else {
             const float slope2 = p.slopes[g * p.G + (t0 + t) / n_i] * 1.4426950408889634f;
             // along the queries; with a causal mask those before the key are masked
@@ -621,13 +632,13 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dkdv_kernel(const __grid_cons
               auto add = [&](int x) {
                 return CAP ? add2(lse2(x), on_line(x, step2, base2)) : on_line(x, step2, base2);
               };
-              probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
+              probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on, seen);
             } else {
               const float dist = (float)(kvp - q0);
               auto add = [&](int x) {
                 return add2(lse2(x), f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
               };
-              probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on);
+              probabilities<CAP, true>(p, sv, am, pe, pk, all, add, on, seen);
             }
           }
         }
@@ -1075,25 +1086,26 @@ __global__ void __launch_bounds__(384, 1) attn_mod_dq_kernel(const __grid_consta
         if (lane == 0) mbar_arrive(&s_free[b]);
         const bool all = klo == 0 && khi == 64;
         auto on = [&](int x) { return x >= klo && x < khi; };
+        auto seen = [&](const uint32_t (&sv)[64]) { return largest_within(sv, klo, khi); };
         float pe[64];
         {
           uint32_t pk[32];
           const uint64_t nl2 = f2(nl, nl);
           if constexpr (!BIAS) {
             auto add = [&](int) { return nl2; };
-            probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
+            probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on, seen);
           } else {
             const BiasLine bl = bias_line(slope2, qpos, kv0, 64, p.causal != 0, false);
             if (!__any_sync(0xffffffffu, bl.mixed)) {
               const uint64_t step2 = both(bl.step), base2 = both(bl.base + nl);
               auto add = [&](int x) { return on_line(x, step2, base2); };
-              probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
+              probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on, seen);
             } else {
               const float dist = (float)(qpos - kv0);
               auto add = [&](int x) {
                 return add2(nl2, f2(-slope2 * fabsf(dist - (float)x), -slope2 * fabsf(dist - (float)(x + 1))));
               };
-              probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on);
+              probabilities<CAP, false>(p, sv, am, pe, pk, all, add, on, seen);
             }
           }
         }

@@ -1,5 +1,6 @@
 """The modified attention over the whole range of caps and scores: caps up to
-the largest accepted, scores at and beyond the cap, values of any size.
+the largest accepted, scores at and beyond the cap, values of any size, and
+masked rows holding anything finite.
 
 Every score here is one product: a query has a single nonzero column, so q.k is
 exact in fp32 and a score's error comes from its modification alone.  That is
@@ -18,7 +19,7 @@ import blockwise_attention_ffn_gb300 as bpt
 from blockwise_attention_ffn_gb300.presets import LayerConfig
 from oracle import train_ops as T
 from tests.gpu_helpers import to64
-from tests.test_gpu_attention_mod import as_int32, check, run
+from tests.test_gpu_attention_mod import as_int32, check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +121,26 @@ def test_large_scores_without_a_cap(level, slope):
     s, d = 400, 112
     x, do = inputs(s, d, [level, -0.3 * level, 2.0], seed=5)
     one_head(s, d, 1, 0.0, slope, x, do, end=[max(q + 1, 150) for q in range(s)])
+
+
+@pytest.mark.parametrize("d", [64, 96, 128])
+@pytest.mark.parametrize("cap,biased", [(20.0, True), (50.0, False), (100.0, False), (100.0, True)])
+def test_masked_rows_leave_no_trace_with_a_cap(d, cap, biased):
+    """What (finite) lies in rows that no window reaches changes no bit of any
+    output: the largest bf16 values, and values near the scores' own size."""
+    b, s, H, K = 3, 300, 4, 2
+    cfg = LayerConfig(b=b, s=s, h=H * d, n_heads=H, n_kv_heads=K, head_dim=d, ffn_dim=64, causal=0)
+    n = [300, 131, 0]
+    end = as_int32([n[i] if q < n[i] else 0 for i in range(b) for q in range(s)])
+    qkv, dout = make(b, s, H, K, d, seed=2)
+    mod = bpt.ScoreMod(None, end, torch.tensor([0.5, 0.1, 0.01, 0.0], device="cuda") if biased else None, cap)
+    clean = [t.clone() for t in run(cfg, mod, qkv, dout, bpt.BPT_FLAG_DETERMINISTIC)]
+    for fill in (3.3e38, 6.0, -40.0):
+        dirty, ddirty = qkv.clone().view(b, s, -1), dout.clone().view(b, s, -1)
+        for i in range(b):
+            dirty[i, n[i]:] = fill
+            dirty[i, n[i]:, ::2] = -fill
+            ddirty[i, n[i]:] = fill
+        got = run(cfg, mod, dirty.view(b * s, -1), ddirty.view(b * s, -1), bpt.BPT_FLAG_DETERMINISTIC)
+        for what, a, c in zip(("o", "lse", "dqkv"), got, clean):
+            assert torch.equal(a, c), (what, fill)
