@@ -25,6 +25,7 @@ another implementation of the layer on the CPU).
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from dataclasses import dataclass, field
 
@@ -43,27 +44,43 @@ def held_inputs(L: int, k: int) -> int:
 
 
 class LibOps:
-    """The library's layer calls on the tensors' CUDA device and a stream."""
+    """The library's layer calls on the tensors' CUDA device and a stream
+    (None: the current one).  Every buffer is allocated on that stream, so one
+    that is dropped while its kernels are still queued goes to nothing but later
+    work of the same stream.  What the stack returns belongs to it as well:
+    another stream waits for it first, and marks what it still reads
+    (Tensor.record_stream) before dropping it."""
 
     def __init__(self, stream=None):
         self.stream = stream
 
+    def _on_stream(self, like):
+        if self.stream is None:
+            return contextlib.nullcontext()
+        import torch
+        s = self.stream
+        return torch.cuda.stream(torch.cuda.ExternalStream(s, device=like.device) if isinstance(s, int) else s)
+
     def workspace(self, cfg, like):
         from . import BPT_PASS_BWD, BPT_PASS_FWD, alloc_bytes, bpt_workspace_bytes
-        return alloc_bytes(max(bpt_workspace_bytes(cfg, BPT_PASS_FWD), bpt_workspace_bytes(cfg, BPT_PASS_BWD)),
-                           device=like.device)
+        n = max(bpt_workspace_bytes(cfg, BPT_PASS_FWD), bpt_workspace_bytes(cfg, BPT_PASS_BWD))
+        with self._on_stream(like):
+            return alloc_bytes(n, device=like.device)
 
     def saved(self, cfg, like):
         from . import alloc_bytes, bpt_saved_bytes
-        return alloc_bytes(bpt_saved_bytes(cfg), device=like.device)
+        with self._on_stream(like):
+            return alloc_bytes(bpt_saved_bytes(cfg), device=like.device)
 
     def empty_like(self, t):
         import torch
-        return torch.empty_like(t)
+        with self._on_stream(t):
+            return torch.empty_like(t)
 
     def grads(self, W, like):
         from . import alloc_grads
-        return alloc_grads(W, device=like.device)
+        with self._on_stream(like):
+            return alloc_grads(W, device=like.device)
 
     def layer_fwd(self, cfg, W, x, y, saved, ws):
         from . import bpt_layer_fwd
@@ -76,8 +93,9 @@ class LibOps:
     def clip(self, grads, max_norm, like):
         import torch
         from . import alloc_bytes, bpt_clip_grads, bpt_clip_workspace_bytes
-        norm = torch.empty(1, dtype=torch.float32, device=like.device)
-        ws = alloc_bytes(bpt_clip_workspace_bytes(), device=like.device)
+        with self._on_stream(like):
+            norm = torch.empty(1, dtype=torch.float32, device=like.device)
+            ws = alloc_bytes(bpt_clip_workspace_bytes(), device=like.device)
         bpt_clip_grads([g for d in grads for g in d.values() if g is not None], max_norm, norm, ws, stream=self.stream)
         return norm
 
