@@ -26,6 +26,7 @@ another implementation of the layer on the CPU).
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import math
 from dataclasses import dataclass, field
 
@@ -139,10 +140,17 @@ def stack_bwd(cfg, weights: list, state: StackState, dy, ws=None, ops=None, grad
     gradient dict per layer (fp32, overwritten, or those passed in).  With
     max_norm the weight gradients of all layers are then clipped in place by
     their global norm (bpt_clip_grads; inf: not clipped), and the norm, one
-    fp32 element on the device, is returned too: (dx, grads, norm)."""
+    fp32 element on the device, is returned too: (dx, grads, norm).  That is the
+    norm over the layers alone: a model with other weights (the one behind
+    bpt_lm_loss_bwd's dw, embeddings) leaves max_norm out and gives all its
+    gradients to one bpt_clip_grads.  A max_norm that the clip would refuse is
+    refused before the state is consumed."""
     L = len(weights)
     if L != state.n_layers:
         raise ValueError("weights do not match the forward pass")
+    if max_norm is not None and not ctypes.c_float(max_norm).value > 0:  # as the clip takes it
+        from . import BPT_EINVAL, BptError
+        raise BptError(BPT_EINVAL, f"stack_bwd: max_norm must be above 0, got {max_norm}")
     ops = ops or LibOps()
     ws = ops.workspace(cfg, dy) if ws is None else ws
     grads = [ops.grads(W, dy) for W in weights] if grads is None else grads
