@@ -1261,18 +1261,45 @@ __global__ void __launch_bounds__(256) attn_mod_prep_kernel(int b, int s, int n_
   }
 }
 
-// CTAs that share one dK/dV item.  Sharing costs the sum over the cluster and
-// the persistence, so only where items leave SMs idle that dQ cannot fill: up to
-// three CTAs for two SMs, while a CTA's stream keeps a dozen query tiles.  Measured,
-// the whole backward: 32 items of up to 256 tiles (d = 128) 421 us unshared, 227 by
-// 2, 124 by 4, 133 by 8; 108 items of up to 27 tiles (d = 96) 86 us unshared, 95 by
-// 2, 120 by 4, and with a quarter of the rows padding 82 unshared, 76 by 2; 1024
-// items of up to 16 tiles (d = 80) 191 us, 304 by 2.
-int split_for(int items, int stream) {
-  const int nsm = sm_count();
-  int s = 1;
-  while (s < 8 && items * 4 * s <= nsm * 3 && stream >= 2 * s * 12) s *= 2;
-  return s;
+// CTAs that share one dK/dV item (a key tile's stream of up to `stream` query
+// tiles): whichever of 1, 2, 4, 8 an estimate in query tiles makes shortest.  A CTA
+// takes its part of the longest stream, and sharing costs it the sum over the
+// cluster, a start and the persistence, some 3 + s tiles.  Clusters that do not fit
+// at once (of four and eight, not every SM finds partners in its GPC) take a second
+// round; with a causal mask it has the lighter items.  And no split beats the work
+// of all SMs, dQ's 0.8 of dK/dV's with it, which fills what one leaves idle: that
+// is why full rows share later than causal ones.  Windows, which live on the device,
+// are not known here.
+// Measured, the whole backward in us at d = 128 by 1 / 2 / 4 / 8 (chosen: *):
+//   108 items of up to 27 tiles   causal 61* / 73 / 88 / 161, all 91* / 102 / 107 / 182
+//   108 items of up to 54 tiles   causal 105 / 86* / 105 / 183, all 136* / 149 / 168 / 236
+//   108 items of up to 216 tiles  causal 377 / 259* / 283 / 372, all 477* / 497 / 528 / 625
+//   36 items of up to 72 tiles    causal 130 / 79 / 52* / 82, all 136 / 83 / 75* / 107
+//   9 items of up to 72 tiles     causal 130 / 78 / 50 / 38*, all 138 / 81 / 52 / 40*
+// Over 595 such shapes (d = 80 and 128, 4 to 152 items, a quarter padded too) the
+// choice is 2% behind the best on average, at worst 38% (64 items of up to 128 tiles,
+// d = 80, causal: 128 by four, 93 by two); up to three CTAs for two SMs and a dozen
+// tiles each, whatever the mask, was 9% behind on average, at worst 69%.
+int split_for(int items, int stream, int n_t, bool causal) {
+  const double nsm = sm_count();
+  const double mean = causal ? stream * (n_t + 1) / (2.0 * n_t) : stream;
+  double least = 0;
+  int best = 1;
+  for (int s = 1; s <= 8 && (s == 1 || stream >= 2 * s); s *= 2) {
+    const double ctas = (double)items * s, part = (double)stream / s, cost = s == 1 ? 0 : 3 + s;
+    const double room = nsm * (s <= 2 ? 1.0 : s == 4 ? 18.0 / 19 : 16.0 / 19);
+    double t = part + cost;
+    if (s > 1 && ctas > room) {
+      if (ctas > 2 * room) break;
+      t += (causal ? 1 - room / ctas : 1.0) * part + cost;
+    }
+    t = std::max(t, (1.8 * items * mean + ctas * cost) / nsm);
+    if (s == 1 || t < least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
 }
 
 template <int D, bool CAP, bool BIAS>
@@ -1286,7 +1313,7 @@ int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
   {
     ProfScope prof(PROF_ATTN_BWD, 8.0 * D * pairs * p.H * b, 0.0, st);
     // CTAs per item: see split_for
-    const int items = p.n_t * p.Hkv * b, split = split_for(items, p.G * p.n_t);
+    const int items = p.n_t * p.Hkv * b, split = split_for(items, p.G * p.n_t, p.n_t, p.causal != 0);
     if (launch_dependent(attn_mod_dkdv_kernel<D, CAP, BIAS>, items * split, split, dim3(384), SMEM_KV, st, p) != cudaSuccess)
       return BPT_ECUDA;
   }
