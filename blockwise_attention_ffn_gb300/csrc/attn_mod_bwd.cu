@@ -26,13 +26,16 @@
 // signs that do not build up; dqkv is off by 2.5e-3 to 3.3e-3 (relative norm, its
 // own bf16 rounding of 1.7e-3 included).
 //
-// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: dK/dV 802 us, dQ 457,
-// capped 900 and 580; documents of 1500: 200 and 139.  dK/dV is bound by its four
+// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: dK/dV 791 us, dQ 457,
+// capped 904 and 563, capped and biased 948 and 568, in fixed order 1,031 and 626;
+// documents of 1500: 204 and 141, capped 237 and 168.  dK/dV is bound by its four
 // products (tensor core 57 to 70% busy: at head dims above 80 S^T and dP^T take
 // both operands from shared memory, and 64 columns of them cost 48 cycles a step of
 // 16 where 32 are arithmetic) and by the chain between them; one product of 128
 // columns for both groups saves a fifth of the tensor core's time but makes the
 // groups run in step: 774 us plain (against 807 then), 1,064 capped (against 901).
+// The capped dK/dV kernels hold more than their 168 registers and spill 20 to 84
+// bytes a thread.
 #include <math.h>
 #include <string.h>
 

@@ -18,6 +18,10 @@
 //  * Row sums are fp32 sums of the fp32 exponentials, so the log-sum-exp is an
 //    fp32-exact output; the tensor core's row sums of bf16 P would be off by
 //    up to 2^-9.
+//  * P is rounded to bf16, V's type, to be an operand of the second product: by at
+//    most 2^-8 of its value, with signs that do not build up.  Two terms of it would
+//    double that product.  o is off by 1.7e-3 to 2.4e-3 (relative norm, its own bf16
+//    rounding of 1.6e-3 included).
 //
 // Work item = one 128-row query tile of one head, the last (with a causal mask
 // heaviest) tiles first.  The 128 keys of a tile are split in two halves, each with its own
@@ -35,9 +39,10 @@
 // still in the current one, and its first S is made during the current item's
 // merge.
 //
-// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: 370 us plain scores
-// (1,485 TFLOP/s of unmasked pairs), 434 capped (1,267), 413 biased; documents of
-// 1500: 119 us, 136 capped.  What bounds it: at d = 128 a step's products take
+// Measured at 8192 rows of 32 + 8 + 8 heads of 128, causal: 371 us plain scores
+// (1,482 TFLOP/s of unmasked pairs), 430 capped (1,279; 812 where most scores are
+// beyond the cap), 403 biased, 490 capped and biased; documents of 1500: 119 us, 139
+// capped.  What bounds it: at d = 128 a step's products take
 // 1,280 of 1,620 cycles (S reads both operands from shared memory, 48 cycles for
 // 16 of depth and 64 columns), with a cap the chain S, modified softmax, P, PV of
 // each half.  The issuing warps' loops are part of that chain: with a barrier per

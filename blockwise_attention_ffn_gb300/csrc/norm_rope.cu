@@ -21,8 +21,9 @@
 //
 // Two forms.  With rows for every SM several times over, blocks stream tiles
 // of whole rows through shared memory by bulk copies (32768 rows of 32 + 32 + 32
-// heads of 64: 135 us, 89% of a copy's bandwidth; of 80: 153 us, 96%, backward 233 us;
-// 65536 rows of 32 + 8 + 8 heads of 128: 258 us, 91%, backward 409 us).  Fewer rows are read straight into registers, their
+// heads of 64: 137 us, 87% of a copy's bandwidth; of 80: 155 us, 97%, backward 235 us,
+// 85%; 65536 rows of 32 + 8 + 8 heads of 128: 258 us, 93%, backward 411 us, 83%; the
+// rotation alone, in place, 215 us either way, 93%).  Fewer rows are read straight into registers, their
 // heads spread over all warps (40 heads of 8 rows: one step of 80 warps).
 //
 // Angles: p * theta in turns, as a 64-bit fraction of a turn.  The product of
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rope_staged_kernel(const _
       const int pairs = rows * n;
       // Between the sections the stage before this one has been stored, and
       // its next tile still has half of this one's time to arrive (loaded at
-      // this tile's end: backward of 32 + 32 + 32 heads of 80 285 us, 249 so; a
+      // this tile's end: backward of 32 + 32 + 32 heads of 80 285 us against 249; a
       // check inside the loop below costs more than a better moment gains).
       if (sec == 1 && k > 0 && threadIdx.x == 0) {
         bulk_wait_read0();
@@ -527,9 +528,9 @@ int launch_staged(const NormRopeParams& p, const Stages& g, int blocks, int smem
 
 // The stages for rows of these sizes, two blocks per SM: two of up to 56 KB.
 // Smaller ones leave warps without a head at every stage's end (forward, three
-// of 36 KB: 32768 rows of 32 + 32 + 32 heads of 80 189 us, 162 so; of 64 125 us,
-// 130 so); three blocks of two of 37 KB, 85 registers a thread, are no faster
-// where rows are long (heads of 128: 259 us, 244 so).
+// of 36 KB, when the choice was made: 32768 rows of 32 + 32 + 32 heads of 80 189 us
+// against 162, of 64 125 us against 130); three blocks of two of 37 KB, 85 registers a thread, are no faster
+// where rows are long (heads of 128, same time: 259 us against 244).
 Stages stages_for(const PackedDims& D, int y_bytes, int x_bytes, int* smem) {
   const int table = (int)(2 * D.d * 4);            // weights
   const int angles = (int)(D.d / 2 * 2 * 4);       // of one row

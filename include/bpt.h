@@ -334,10 +334,14 @@ int bpt_attention_bwd_noalloc(const bpt_config* cfg, const void* qkv, const void
  * rebuilt probabilities what lse's fp32 cannot hold (2^-24 of its size); the
  * windows above keep near keys in view, where lse is small.  The forward's
  * sums are finite while |v| times the number of visible keys stays below 2^72
- * with a cap of at most 61, below 2^119 otherwise.  Rows that no
- * window reaches may hold any finite values: they leave no trace.  An infinity
- * or a NaN in V does (0 * inf) wherever its 128-key tile is loaded, as in
- * bpt_attention_fwd.
+ * with a cap of at most 61, below 2^119 otherwise.  Rows that no window reaches
+ * may hold any finite values: they leave no trace in other rows' results (not a
+ * bit, where sums have a fixed order).  An infinity or a NaN does (0 * inf)
+ * wherever its 128-row tile is loaded: in V in the forward, as in
+ * bpt_attention_fwd; in Q, K or dout in the backward.  P is rounded to bf16 where
+ * it multiplies V, P and the scores' gradient where they multiply dout, K and Q
+ * (the tensor core's operands, as in the plain attention): each by at most 2^-8
+ * of its value.  Sums, row sums and lse are fp32.
  * dqkv as for bpt_attention_bwd, whose notes on the order of sums and on
  * BPT_FLAG_DETERMINISTIC hold here too; b*H*s_pad above 2^31 - 1 returns
  * BPT_EUNSUPPORTED from both calls.  Outputs and ws that share bytes with an
@@ -455,14 +459,16 @@ int bpt_qk_norm_rope_bwd(const bpt_config* cfg, const void* qkv, const void* wq,
  *            device pointers aligned to their element; out == grad clips in
  *            place (nothing is written where the norm is within max_norm).
  *            An output may not share memory with any other tensor of the call,
- *            with norm or with ws (BPT_EINVAL): each is scaled once.
+ *            with norm or with ws (BPT_EINVAL): each is scaled once.  Where out
+ *            and grad differ modulo 16 bytes the copy goes element by element,
+ *            2.5 (fp32) to 4 (bf16) times slower.
  *   max_norm > 0; +inf computes the norm and copies
  *   flags    0 or BPT_FLAG_DEBUG_CHECKS
  *   norm     one fp32 (device), the norm before clipping; not part of a tensor
  *   ws       bpt_clip_workspace_bytes() bytes, one per call in flight
- * A norm that is inf gives a factor of 0, a NaN norm a NaN factor, as the
- * formula says.  Squares are summed in fp32 by 32 (rescaled where they leave
- * its range) and then in fp64, in an order fixed by the tensors' sizes,
+ * Under a finite max_norm a norm that is inf gives a factor of 0, a NaN norm a
+ * NaN factor, as the formula says.  Squares are summed in fp32 by 32 (bf16: by
+ * 64; rescaled where they leave its range) and then in fp64, in an order fixed by the tensors' sizes,
  * addresses modulo 16 and the device's SM count. */
 enum { BPT_DTYPE_F32 = 0, BPT_DTYPE_BF16 = 1 };
 typedef struct {
@@ -478,7 +484,8 @@ int bpt_clip_grads(int32_t n, const bpt_clip_tensor* t, float max_norm, int32_t 
 /* Opt-in launch profiler.  bpt_profile_enable(1) makes every later launch
  * of this process record a pair of CUDA events on its stream, tagged with
  * the launch's kind and its algorithmic work (FLOPs for tensor-core kernels,
- * bytes for memory-bound ones); bpt_profile_enable(0) stops recording.
+ * bytes for memory-bound ones; the modified attention's as if no windows were
+ * given, which live on the device, so its rates can exceed the chip's); bpt_profile_enable(0) stops recording.
  * bpt_profile_collect synchronises on the recorded events, writes per kind
  * k < nkinds the summed device time (ms), FLOPs, bytes and launch count, and
  * clears the record.  Kinds: 0 GEMM, 1 attention forward, 2 attention
