@@ -48,9 +48,9 @@ class LibOps:
     """The library's layer calls on the tensors' CUDA device and a stream
     (None: the current one).  Every buffer is allocated on that stream, so one
     that is dropped while its kernels are still queued goes to nothing but later
-    work of the same stream.  What the stack returns belongs to it as well:
-    another stream waits for it first, and marks what it still reads
-    (Tensor.record_stream) before dropping it."""
+    work of the same stream.  What the stack returns is marked as read by the
+    caller's current stream too: once that stream has waited for this one it may
+    use the results and drop them."""
 
     def __init__(self, stream=None):
         self.stream = stream
@@ -61,6 +61,15 @@ class LibOps:
         import torch
         s = self.stream
         return torch.cuda.stream(torch.cuda.ExternalStream(s, device=like.device) if isinstance(s, int) else s)
+
+    def hand_back(self, *tensors):
+        """What the caller gets is not reused before its current stream is
+        through with it either."""
+        if self.stream is None:
+            return
+        import torch
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
 
     def workspace(self, cfg, like):
         from . import BPT_PASS_BWD, BPT_PASS_FWD, alloc_bytes, bpt_workspace_bytes
@@ -113,6 +122,11 @@ class StackState:
     peak_held: int = 0  # most layer inputs the backward pass held at once
 
 
+def _hand_back(ops, *tensors):
+    if hasattr(ops, "hand_back"):  # (what replaces the library's calls need not have it)
+        ops.hand_back(*(t for t in tensors if t is not None))
+
+
 def stack_fwd(cfg, weights: list, x, k: int, ws=None, ops=None):
     """y = layer_{L-1}(... layer_0(x)), keeping a checkpoint every k layers.
     weights: one weight dict per layer (the layer call's layout).  Returns
@@ -132,6 +146,7 @@ def stack_fwd(cfg, weights: list, x, k: int, ws=None, ops=None):
         ops.layer_fwd(cfg, W, h, y, sv, ws)
         st.saved.append(sv)
         h = y
+    _hand_back(ops, h)
     return h, st
 
 
@@ -173,6 +188,6 @@ def stack_bwd(cfg, weights: list, state: StackState, dy, ws=None, ops=None, grad
             g = dx
         del seg_in
         del state.ckpt[s0]
-    if max_norm is None:
-        return g, grads
-    return g, grads, ops.clip(grads, max_norm, dy)
+    norm = None if max_norm is None else ops.clip(grads, max_norm, dy)
+    _hand_back(ops, g, norm, *(t for d in grads for t in d.values()))
+    return (g, grads) if max_norm is None else (g, grads, norm)

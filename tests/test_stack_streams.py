@@ -17,11 +17,13 @@ from blockwise_attention_ffn_gb300.presets import LayerConfig
 
 
 class FakeCuda:
-    """torch.cuda's notion of the current stream, and the streams on which
-    buffers were allocated and given to the library."""
+    """torch.cuda's notion of the current stream, the streams on which buffers
+    were allocated and given to the library, and those they were marked for."""
 
     def __init__(self, monkeypatch):
-        self.current, self.where, self.used = "default", {}, []
+        self.current, self.where, self.used, self.marked = "default", {}, [], []
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.current)
+        monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: self.marked.append((t.data_ptr(), s)))
         monkeypatch.setattr(torch.cuda, "stream", self.stream)
         monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
         for name in ("empty", "empty_like"):
