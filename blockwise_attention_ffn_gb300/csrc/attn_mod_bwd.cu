@@ -1272,20 +1272,23 @@ __global__ void __launch_bounds__(256) attn_mod_prep_kernel(int b, int s, int n_
 // round; with a causal mask it has the lighter items.  And no split beats the work
 // of all SMs, dQ's 0.8 of dK/dV's with it, which fills what one leaves idle: that
 // is why full rows share later than causal ones.  Windows, which live on the device,
-// are not known here.
+// are taken to leave half of the pairs, unevenly, as a causal mask does.
 // Measured, the whole backward in us at d = 128 by 1 / 2 / 4 / 8 (chosen: *):
 //   108 items of up to 27 tiles   causal 61* / 73 / 88 / 161, all 91* / 102 / 107 / 182
 //   108 items of up to 54 tiles   causal 105 / 86* / 105 / 183, all 136* / 149 / 168 / 236
 //   108 items of up to 216 tiles  causal 377 / 259* / 283 / 372, all 477* / 497 / 528 / 625
 //   36 items of up to 72 tiles    causal 130 / 79 / 52* / 82, all 136 / 83 / 75* / 107
 //   9 items of up to 72 tiles     causal 130 / 78 / 50 / 38*, all 138 / 81 / 52 / 40*
-// Over 595 such shapes (d = 80 and 128, 4 to 152 items, a quarter padded too) the
-// choice is 2% behind the best on average, at worst 38% (64 items of up to 128 tiles,
-// d = 80, causal: 128 by four, 93 by two); up to three CTAs for two SMs and a dozen
-// tiles each, whatever the mask, was 9% behind on average, at worst 69%.
-int split_for(int items, int stream, int n_t, bool causal) {
+// Over 1,335 such calls (4 to 152 items, d = 80, 96 and 128; causal, full, prefixes,
+// documents seen both ways, a quarter padded; plain or capped and biased) the choice
+// is 2% behind the best on average, at worst 46%; windows taken for full rows 3%, at
+// worst 82%; up to three CTAs for two SMs and a dozen tiles each, whatever the mask,
+// 9%, at worst twice.  (3 x 1111 rows of 12 + 4 + 4 heads of 96 behind prefixes of a
+// quarter, 108 items of up to 27 tiles: 89 us, 78 by two; 3456 rows of 8 + 4 + 4 of
+// 128, all keys of the first three quarters: 105 by two, 88 unshared.)
+int split_for(int items, int stream, int n_t, bool uneven) {
   const double nsm = sm_count();
-  const double mean = causal ? stream * (n_t + 1) / (2.0 * n_t) : stream;
+  const double mean = uneven ? stream * (n_t + 1) / (2.0 * n_t) : stream;
   double least = 0;
   int best = 1;
   for (int s = 1; s <= 8 && (s == 1 || stream >= 2 * s); s *= 2) {
@@ -1294,7 +1297,7 @@ int split_for(int items, int stream, int n_t, bool causal) {
     double t = part + cost;
     if (s > 1 && ctas > room) {
       if (ctas > 2 * room) break;
-      t += (causal ? 1 - room / ctas : 1.0) * part + cost;
+      t += (uneven ? 1 - room / ctas : 1.0) * part + cost;
     }
     t = std::max(t, (1.8 * items * mean + ctas * cost) / nsm);
     if (s == 1 || t < least) {
@@ -1316,7 +1319,8 @@ int launch_both(const ModBwdParams& p, int b, double pairs, cudaStream_t st) {
   {
     ProfScope prof(PROF_ATTN_BWD, 8.0 * D * pairs * p.H * b, 0.0, st);
     // CTAs per item: see split_for
-    const int items = p.n_t * p.Hkv * b, split = split_for(items, p.G * p.n_t, p.n_t, p.causal != 0);
+    const int items = p.n_t * p.Hkv * b;
+    const int split = split_for(items, p.G * p.n_t, p.n_t, p.causal || p.row_begin || p.row_end);
     if (launch_dependent(attn_mod_dkdv_kernel<D, CAP, BIAS>, items * split, split, dim3(384), SMEM_KV, st, p) != cudaSuccess)
       return BPT_ECUDA;
   }
