@@ -11,6 +11,8 @@ bpt_lm_loss_fwd, bpt_lm_loss_bwd, bpt_lm_workspace_bytes,
 bpt_attention_mod_fwd, bpt_attention_mod_bwd, bpt_attention_mod_bwd_workspace_bytes,
 bpt_qk_norm_rope_fwd, bpt_qk_norm_rope_bwd, bpt_qk_norm_rope_workspace_bytes,
 bpt_clip_grads, bpt_clip_workspace_bytes,
+bpt_moe_route_fwd, bpt_moe_route_bwd, bpt_moe_route_workspace_bytes,
+bpt_moe_ffn_fwd, bpt_moe_ffn_bwd, bpt_moe_ffn_workspace_bytes, bpt_moe_saved_bytes, bpt_grouped_gemm,
 bpt_workspace_bytes, bpt_saved_bytes, bpt_attention_bwd_workspace_bytes,
 bpt_status_string, bpt_last_device_error, bpt_check_device_range, bpt_watchdog_selftest,
 bpt_profile_enable, bpt_profile_collect, bpt_profile_list.  The layer stack
@@ -38,6 +40,8 @@ BPT_FLAG_ONE_STREAM = 2
 BPT_FLAG_DETERMINISTIC = 4
 BPT_FLAG_DEBUG_CHECKS = 8
 BPT_DTYPE_F32, BPT_DTYPE_BF16 = 0, 1
+BPT_GROUPED_NT, BPT_GROUPED_NN, BPT_GROUPED_TN = 0, 1, 2
+BPT_MOE_BAD_LOGIT_SITE, BPT_GROUPED_BAD_OFFSET_SITE = 951, 953
 
 WEIGHT_FIELDS = ("ln1_w", "ln1_b", "wq", "bq", "wk", "bk", "wv", "bv", "wo", "bo",
                  "ln2_w", "ln2_b", "w1", "b1", "w2", "b2", "w3")
@@ -70,6 +74,20 @@ class BptScoreMod(ctypes.Structure):
 
 class BptClipTensor(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class BptMoeConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "h", "ffn_dim", "n_experts", "top_k", "act", "logits_dtype",
+                                              "weights_dtype", "grads_dtype", "norm_topk")] + \
+        [("balance_coef", ctypes.c_float), ("z_coef", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class BptMoeRoute(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("ids", "weights", "offsets", "order", "slot")]
+
+
+class BptGroupedConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n", "k", "groups", "form", "out_dtype", "flags")]
 
 
 class BptError(RuntimeError):
@@ -138,6 +156,23 @@ def lib() -> ctypes.CDLL:
         L.bpt_clip_workspace_bytes.restype = sz
         L.bpt_clip_grads.argtypes = [i32, vp, ctypes.c_float, i32, vp, vp, sz, vp]
         L.bpt_clip_grads.restype = i32
+        moep, routep = ctypes.POINTER(BptMoeConfig), ctypes.POINTER(BptMoeRoute)
+        L.bpt_moe_route_workspace_bytes.argtypes = [moep]
+        L.bpt_moe_route_workspace_bytes.restype = sz
+        L.bpt_moe_route_fwd.argtypes = [moep, vp, routep, vp, vp, sz, vp]
+        L.bpt_moe_route_fwd.restype = i32
+        L.bpt_moe_route_bwd.argtypes = [moep, vp, routep, vp, ctypes.c_float, vp, vp]
+        L.bpt_moe_route_bwd.restype = i32
+        L.bpt_moe_saved_bytes.argtypes = [moep]
+        L.bpt_moe_saved_bytes.restype = sz
+        L.bpt_moe_ffn_workspace_bytes.argtypes = [moep, i32]
+        L.bpt_moe_ffn_workspace_bytes.restype = sz
+        L.bpt_moe_ffn_fwd.argtypes = [moep, routep] + [vp] * 7 + [sz, vp]
+        L.bpt_moe_ffn_fwd.restype = i32
+        L.bpt_moe_ffn_bwd.argtypes = [moep, routep] + [vp] * 12 + [sz, vp]
+        L.bpt_moe_ffn_bwd.restype = i32
+        L.bpt_grouped_gemm.argtypes = [ctypes.POINTER(BptGroupedConfig), vp, vp, vp, vp, vp]
+        L.bpt_grouped_gemm.restype = i32
         L.bpt_check_device_range.argtypes = [vp, sz]
         L.bpt_check_device_range.restype = i32
         L.bpt_watchdog_selftest.argtypes = [vp]
@@ -408,6 +443,131 @@ def bpt_clip_grads(grads, max_norm, norm, ws, out=None, flags=0, stream=None) ->
                                 ws.numel(), _stream(stream)), where)
 
 
+def make_moe_config(c) -> BptMoeConfig:
+    """BptMoeConfig from a MoeConfig (or any object with the same fields)."""
+    return BptMoeConfig(c.n, c.h, c.ffn_dim, c.n_experts, c.top_k, c.act, c.logits_dtype, c.weights_dtype, c.grads_dtype,
+                        c.norm_topk, c.balance_coef, c.z_coef, c.flags)
+
+
+@dataclass(frozen=True)
+class MoeRoute:
+    """Where bpt_moe_route_fwd sends every position (device tensors): ids
+    [n, k] int32, weights [n, k], offsets [E + 2], order [n * k] and slot
+    [n * k] int32.  alloc_moe_route makes one."""
+    ids: object
+    weights: object
+    offsets: object
+    order: object
+    slot: object
+
+
+def _dtype(kind):
+    import torch
+    return torch.bfloat16 if kind == BPT_DTYPE_BF16 else torch.float32
+
+
+def _moe_route(where, cfg, r, dev, ids=True):
+    import torch
+    i32, pairs = torch.int32, cfg.n * cfg.top_k
+    return BptMoeRoute(_want(where, "ids", r.ids, i32, pairs, dev) if ids else None,
+                       _want(where, "weights", r.weights, _dtype(cfg.weights_dtype), pairs, dev),
+                       _want(where, "offsets", r.offsets, i32, cfg.n_experts + 2, dev),
+                       _want(where, "order", r.order, i32, pairs, dev), _want(where, "slot", r.slot, i32, pairs, dev))
+
+
+def bpt_moe_route_workspace_bytes(cfg) -> int:
+    return int(lib().bpt_moe_route_workspace_bytes(make_moe_config(cfg)))
+
+
+def bpt_moe_route_fwd(cfg, logits, route, loss, ws, stream=None) -> None:
+    """Routes of logits [n, E] (cfg.logits_dtype) into the tensors of route (a
+    MoeRoute), and the router's losses into loss (one fp32; None: not wanted,
+    where both coefficients are 0)."""
+    import torch
+    where, dev = "bpt_moe_route_fwd", torch.cuda.current_device()
+    c, r = make_moe_config(cfg), _moe_route(where, cfg, route, dev)
+    _check(lib().bpt_moe_route_fwd(
+        c, _want(where, "logits", logits, _dtype(cfg.logits_dtype), cfg.n * cfg.n_experts, dev), r,
+        _may(where, "loss", loss, torch.float32, 1, dev), _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(),
+        _stream(stream)), where)
+
+
+def bpt_moe_route_bwd(cfg, logits, route, dweights, dloss, dlogits, stream=None) -> None:
+    """dlogits [n, E] of the weights' gradients dweights [n, k] and of dloss
+    times the losses."""
+    import torch
+    where, dev = "bpt_moe_route_bwd", torch.cuda.current_device()
+    c, r, kind, n = make_moe_config(cfg), _moe_route(where, cfg, route, dev), _dtype(cfg.logits_dtype), cfg.n * cfg.n_experts
+    _check(lib().bpt_moe_route_bwd(
+        c, _want(where, "logits", logits, kind, n, dev), r,
+        _want(where, "dweights", dweights, _dtype(cfg.weights_dtype), cfg.n * cfg.top_k, dev), float(dloss),
+        _want(where, "dlogits", dlogits, kind, n, dev), _stream(stream)), where)
+
+
+def bpt_moe_saved_bytes(cfg) -> int:
+    return int(lib().bpt_moe_saved_bytes(make_moe_config(cfg)))
+
+
+def bpt_moe_ffn_workspace_bytes(cfg, pass_: int) -> int:
+    return int(lib().bpt_moe_ffn_workspace_bytes(make_moe_config(cfg), int(pass_)))
+
+
+def _experts(where, cfg, what, t, kind, dev):
+    """The address of a tensor of the experts' matrices (the third only with SwiGLU)."""
+    if what.endswith("3") and cfg.act != 2:
+        if t is not None:
+            raise BptError(BPT_EINVAL, f"{where}: {what} is given, but the activation takes two matrices")
+        return None
+    return _want(where, what, t, kind, cfg.n_experts * cfg.ffn_dim * cfg.h, dev)
+
+
+def bpt_moe_ffn_fwd(cfg, route, x, w1, w3, w2, y, saved, ws, stream=None) -> None:
+    """The experts' network on x [n, h] by route: y [n, h] bf16.  w1, w3 [E, f,
+    h], w2 [E, h, f]; w3 is None without SwiGLU.  saved:
+    bpt_moe_saved_bytes(cfg) for the backward, None: inference."""
+    import torch
+    where, dev, bf16 = "bpt_moe_ffn_fwd", torch.cuda.current_device(), torch.bfloat16
+    c, r = make_moe_config(cfg), _moe_route(where, cfg, route, dev, ids=False)
+    keep = 0 if saved is None else bpt_moe_saved_bytes(cfg)
+    _check(lib().bpt_moe_ffn_fwd(
+        c, r, _want(where, "x", x, bf16, cfg.n * cfg.h, dev), _experts(where, cfg, "w1", w1, bf16, dev),
+        _experts(where, cfg, "w3", w3, bf16, dev), _experts(where, cfg, "w2", w2, bf16, dev),
+        _want(where, "y", y, bf16, cfg.n * cfg.h, dev), _may(where, "saved", saved, torch.uint8, keep, dev),
+        _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(), _stream(stream)), where)
+
+
+def bpt_moe_ffn_bwd(cfg, route, x, w1, w3, w2, saved, dy, dx, dweights, dw1, dw3, dw2, ws, stream=None) -> None:
+    """Gradients of bpt_moe_ffn_fwd: dx [n, h] bf16, dweights [n, k]
+    (cfg.weights_dtype) and the matrices' (cfg.grads_dtype), from dy [n, h]
+    and what the forward saved."""
+    import torch
+    where, dev, bf16 = "bpt_moe_ffn_bwd", torch.cuda.current_device(), torch.bfloat16
+    c, r, kind, nh = make_moe_config(cfg), _moe_route(where, cfg, route, dev, ids=False), _dtype(cfg.grads_dtype), cfg.n * cfg.h
+    _check(lib().bpt_moe_ffn_bwd(
+        c, r, _want(where, "x", x, bf16, nh, dev), _experts(where, cfg, "w1", w1, bf16, dev),
+        _experts(where, cfg, "w3", w3, bf16, dev), _experts(where, cfg, "w2", w2, bf16, dev),
+        _want(where, "saved", saved, torch.uint8, bpt_moe_saved_bytes(cfg), dev), _want(where, "dy", dy, bf16, nh, dev),
+        _want(where, "dx", dx, bf16, nh, dev),
+        _want(where, "dweights", dweights, _dtype(cfg.weights_dtype), cfg.n * cfg.top_k, dev),
+        _experts(where, cfg, "dw1", dw1, kind, dev), _experts(where, cfg, "dw3", dw3, kind, dev),
+        _experts(where, cfg, "dw2", dw2, kind, dev), _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(),
+        _stream(stream)), where)
+
+
+def bpt_grouped_gemm(cfg, a, b, offsets, out, stream=None) -> None:
+    """Products over ragged groups of rows (a GroupedConfig says which form):
+    NT out = a b_e^T, NN out = a b_e, TN out_e = a_e^T b_e, group e the rows
+    [offsets[e], offsets[e + 1]); offsets [groups + 1] int32 on the device."""
+    import torch
+    where, dev, bf16 = "bpt_grouped_gemm", torch.cuda.current_device(), torch.bfloat16
+    tn, mats = cfg.form == BPT_GROUPED_TN, cfg.groups * cfg.n * cfg.k
+    c = BptGroupedConfig(cfg.rows, cfg.n, cfg.k, cfg.groups, cfg.form, cfg.out_dtype, cfg.flags)
+    _check(lib().bpt_grouped_gemm(
+        c, _want(where, "a", a, bf16, cfg.rows * cfg.k, dev), _want(where, "b", b, bf16, cfg.rows * cfg.n if tn else mats, dev),
+        _want(where, "offsets", offsets, torch.int32, cfg.groups + 1, dev),
+        _want(where, "out", out, _dtype(cfg.out_dtype), mats if tn else cfg.rows * cfg.n, dev), _stream(stream)), where)
+
+
 BPT_LM_BAD_TARGET_SITE = 950
 NOALLOC_SCRATCH_BYTES = 192 * 1024 * 1024
 
@@ -488,6 +648,15 @@ def alloc_bytes(n: int, device="cuda"):
     """A 256-byte aligned uint8 device buffer of at least n bytes."""
     import torch
     return torch.empty(max(int(n), 256), dtype=torch.uint8, device=device)
+
+
+def alloc_moe_route(cfg, device="cuda") -> MoeRoute:
+    """The tensors bpt_moe_route_fwd writes."""
+    import torch
+    n, k = cfg.n, cfg.top_k
+    ints = lambda *shape: torch.empty(*shape, dtype=torch.int32, device=device)  # noqa: E731
+    return MoeRoute(ints(n, k), torch.empty(n, k, dtype=_dtype(cfg.weights_dtype), device=device), ints(cfg.n_experts + 2),
+                    ints(n * k), ints(n * k))
 
 
 def alloc_grads(weights: dict, device="cuda") -> dict:

@@ -1,0 +1,100 @@
+// grouped.cu -- grouped_gemm(): tensor maps, parameters and the choice of the
+// tile for the grouped GEMM (grouped_kernel.cuh), and the public products over
+// ragged groups.
+#include "grouped_kernel.cuh"
+
+namespace bpt {
+
+using namespace gg;
+
+int64_t grouped_part_tiles(int64_t N) { return (N + 255) / 256; }
+
+int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
+  Params p;
+  memset(&p, 0, sizeof(p));
+  const bool tn = op.form == GROUPED_TN;
+  const bool dual = op.form == GROUPED_NT && op.w2 != nullptr;
+  const bool two = op.form == GROUPED_NN && op.a2 != nullptr;
+  if (op.groups < 1 || op.groups > GROUPED_MAX_GROUPS || op.rows < 1) return 1;
+  // Tiles.  Rows a group: a pair of SMs takes 256 at a time, one SM 128; the
+  // pair's product needs two thirds of the shared-memory reads but leaves 128
+  // rows idle in a group's last tile on average against 64.
+  // Few rows: the weights' bytes bound the product, and 64-column tiles give
+  // the SMs more units to share them.
+  const bool small = op.form == GROUPED_NT && op.mean_rows <= 64;
+  bool pair = tn ? op.M > BM : op.mean_rows >= 512;
+  if (pair && gk::pair_units() <= 0) pair = false;
+  const int BN = small ? 64 : dual ? 128 : 256;
+  const int TM = pair ? 2 * BM : BM;
+  const int BNS = pair ? BN / 2 : BN;
+  p.offsets = op.offsets;
+  p.groups = op.groups;
+  p.rows = (int)op.rows;
+  p.N = (int)op.N;
+  p.nt = (int)((op.N + BN - 1) / BN);
+  p.a_rows = (int)op.a_rows;
+  p.order = op.order;
+  p.top_k = op.top_k;
+  p.pairs = (int)op.rows;
+  p.out = op.out;
+  p.out2 = op.out2;
+  p.out3 = op.out3;
+  p.out_f32 = op.out_f32;
+  p.beta = op.beta;
+  p.act = op.act;
+  p.aux = reinterpret_cast<const __nv_bfloat16*>(op.aux);
+  p.aux2 = reinterpret_cast<const __nv_bfloat16*>(op.aux2);
+  p.row_weight = op.row_weight;
+  p.row_weight_f32 = op.row_weight_f32;
+  p.part = op.part;
+  p.err = device_error_word();
+  if (!p.err) return 3;
+  const int out_elem = op.epi == GROUPED_STORE && op.out_f32 ? 4 : 2;
+  auto ok32 = [&](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 31) == 0; };
+  p.vec32 = (op.N * out_elem) % 32 == 0 && (op.N * 2) % 32 == 0 && ok32(op.out) && ok32(op.out2) && ok32(op.out3) && ok32(op.aux) &&
+            ok32(op.aux2);
+  int64_t units, mt_all;
+  const int64_t some = std::min<int64_t>(op.groups, op.rows);  // groups that can hold a row
+  int rc = 0;
+  if (!tn) {
+    p.segs = two ? 2 : 1;
+    p.nkt = (int)((op.K + BK - 1) / BK);
+    for (int i = 0; i < p.segs; ++i) {
+      const void* a = i ? op.a2 : op.a;
+      rc |= make_map_2d(&p.map_a[i], a, op.a_rows, op.K, op.K, BK, BM, 128);
+      rc |= make_map_2d(&p.map_ag[i], a, op.a_rows, op.K, op.K, BK, 1, 128);
+    }
+    for (int i = 0; i < (dual || two ? 2 : 1); ++i) {
+      const void* w = i ? op.w2 : op.w;
+      rc |= op.form == GROUPED_NT ? make_map_stack(&p.map_b[i], w, op.groups, op.N, op.K, BK, BNS)
+                                  : make_map_stack(&p.map_b[i], w, op.groups, op.K, op.N, 64, BK);
+    }
+    mt_all = std::min<int64_t>(op.rows, op.rows / TM + some);
+    units = mt_all * p.nt;
+  } else {
+    p.segs = op.a2 ? 2 : 1;
+    p.M = (int)op.M;
+    p.mt = (int)((op.M + TM - 1) / TM);
+    p.b_rows = (int)op.b_rows;
+    for (int i = 0; i < p.segs; ++i) {
+      const void* a = i ? op.a2 : op.a;
+      rc |= make_map_2d(&p.map_a[i], a, op.a_rows, op.M, op.M, 64, BK, 128);
+      rc |= make_map_2d(&p.map_ag[i], a, op.a_rows, op.M, op.M, 64, 1, 128);
+    }
+    rc |= make_map_2d(&p.map_b[0], op.b, op.b_rows, op.N, op.N, 64, BK, 128);
+    rc |= make_map_2d(&p.map_bg, op.b, op.b_rows, op.N, op.N, 64, 1, 128);
+    mt_all = (int64_t)op.groups * p.segs * p.mt;
+    units = mt_all * p.nt;
+  }
+  if (rc) return 1;
+  if (units > INT32_MAX) return 5;
+  // bands of 4096 rows (TN: of 4096 of M): the wave in flight shares the
+  // band's rows in L2 while the other operand streams through once a band
+  p.band = 4096 / TM;
+  ProfScope prof(PROF_GEMM, 2.0 * (double)op.rows * (double)op.N * (double)(tn ? op.M * p.segs : op.K * p.segs) * (dual ? 2 : 1), 0.0, st);
+  if (op.form == GROUPED_NT) return launch_nt(p, op.epi, op.a_gather || small, dual, pair, small, units, st);
+  if (op.form == GROUPED_NN) return launch_nn(p, op.epi, pair, units, st);
+  return launch_tn(p, op.a_gather, op.b_gather, pair, units, st);
+}
+
+}  // namespace bpt

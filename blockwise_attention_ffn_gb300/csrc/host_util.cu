@@ -10,6 +10,7 @@
 
 #include "../../include/bpt.h"
 
+#include "grouped.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -147,6 +148,22 @@ int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, i
 
 int make_attn_map(CUtensorMap* map, const void* qkv, int b, int s, int64_t ld, int d) {
   return make_attn_map(map, qkv, b, s, ld, d, 128);
+}
+
+// 3-D map over [count, rows, cols] row-major bf16 matrices (grouped.h).
+int make_map_stack(CUtensorMap* map, const void* ptr, uint64_t count, uint64_t rows, uint64_t cols, uint32_t box_cols,
+                   uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn || !ptr || box_rows > 256 || box_cols > 64) return 1;
+  if ((reinterpret_cast<uintptr_t>(ptr) & 15) || ((cols * 2) & 15)) return 1;
+  cuuint64_t dims[3] = {cols, rows, count};
+  cuuint64_t strides[2] = {cols * 2, cols * 2 * rows};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? 0 : 1;
 }
 
 // Watchdog self-test.  One thread waits, through the same bounded_wait every

@@ -76,3 +76,42 @@ class LmConfig:
 # The loss after the GPT-3B-shaped layer at s = 32768, over the GPT-2 BPE
 # vocabulary of the OpenWebText models (50257 tokens).
 LM3 = LmConfig(name="gpt-3b lm head s=32768 h=2560 V=50257", n=32768, h=2560, vocab=50257, seed=5)
+
+
+@dataclass(frozen=True)
+class MoeConfig:
+    """A layer whose feed-forward network is a mixture of experts: n positions
+    of width h, top_k of n_experts networks of width ffn_dim each."""
+    n: int
+    h: int
+    ffn_dim: int
+    n_experts: int
+    top_k: int
+    act: int = 2            # 0 GeLU (erf), 1 GeLU (tanh), 2 SwiGLU
+    logits_dtype: int = 0   # 0 fp32, 1 bf16: logits and their gradient
+    weights_dtype: int = 0  # of the routes' weights and their gradient
+    grads_dtype: int = 0    # of the experts' weight gradients
+    norm_topk: int = 1      # weights: 1 softmax over the chosen, 0 over all
+    balance_coef: float = 0.0
+    z_coef: float = 0.0
+    flags: int = 0
+    name: str = ""
+
+    def with_(self, **kw) -> "MoeConfig":
+        return replace(self, **kw)
+
+
+@dataclass(frozen=True)
+class GroupedConfig:
+    """Products over ragged groups of rows (form 0 NT, 1 NN, 2 TN)."""
+    rows: int
+    n: int
+    k: int
+    groups: int
+    form: int = 0
+    out_dtype: int = 1      # 0 fp32, 1 bf16
+    flags: int = 0
+    name: str = ""
+
+    def with_(self, **kw) -> "GroupedConfig":
+        return replace(self, **kw)

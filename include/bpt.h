@@ -481,6 +481,120 @@ size_t bpt_clip_workspace_bytes(void);
 int bpt_clip_grads(int32_t n, const bpt_clip_tensor* t, float max_norm, int32_t flags, float* norm, void* ws,
                    size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A layer whose feed-forward network is a mixture of experts: the router, the
+ * experts' network on the rows the router sends them, and the products over
+ * ragged groups of rows that it is made of.
+ *
+ *   n, h, ffn_dim  positions, model width, width of each expert (multiples of
+ *                  8: h and ffn_dim)
+ *   n_experts      E in 1 .. 1024;  top_k  k in 1 .. min(E, 32)
+ *   act            BPT_ACT_*: y = W2 (silu(W1 x) * W3 x), or W2 gelu(W1 x)
+ *   logits_dtype   BPT_DTYPE_* of logits and dlogits
+ *   weights_dtype  BPT_DTYPE_* of the routes' weights and dweights
+ *   grads_dtype    BPT_DTYPE_* of dw1, dw2, dw3
+ *   norm_topk      1: a row's weights are the softmax over its chosen experts;
+ *                  0: the chosen values of the softmax over all
+ *   balance_coef, z_coef   of the router's losses
+ *   flags          BPT_FLAG_ACCUM_GRADS (dw += ; fp32 grads only),
+ *                  BPT_FLAG_DETERMINISTIC (accepted: every sum has a fixed
+ *                  order in any case), BPT_FLAG_DEBUG_CHECKS
+ * The router's calls read neither h, ffn_dim nor act, the network's calls none
+ * of the router's options; all must be valid.  n * k above 2^29 returns
+ * BPT_EUNSUPPORTED.  Outputs, saved and ws that share bytes with an input or
+ * one another are refused (BPT_EINVAL). */
+typedef struct {
+  int32_t n, h, ffn_dim, n_experts, top_k, act;
+  int32_t logits_dtype, weights_dtype, grads_dtype, norm_topk;
+  float balance_coef, z_coef;
+  int32_t flags;
+} bpt_moe_config;
+
+/* Where every position goes (device).  A pair p = t * k + j is position t's
+ * j-th choice.
+ *   ids      [n, k] expert of each pair, the largest logit first; -1: none
+ *   weights  [n, k]
+ *   offsets  [E + 2] rows [offsets[e], offsets[e + 1]) of the order are expert
+ *            e's; offsets[E + 1] is the number of routed positions
+ *   order    [n * k] pair at each row: by expert, then by pair; -1 behind the
+ *            last routed row
+ *   slot     [n * k] row of each pair; -1: none */
+typedef struct {
+  int32_t* ids;
+  void* weights;
+  int32_t *offsets, *order, *slot;
+} bpt_moe_route;
+
+/* The router, from logits [n, E] (z):
+ *   chosen: the k largest z of a row, the lowest index of equals.  An expert
+ *   whose logit is -inf is never chosen: a row with fewer than k others has
+ *   ids of -1 with weight 0 behind them, a row of -inf (padding) goes nowhere
+ *   and counts in none of the losses.  A NaN or +inf counts as -inf and is
+ *   recorded in the device error word (BPT_EINVAL, BPT_MOE_BAD_LOGIT_SITE).
+ *   p = softmax(z), lse = log sum exp z, nv = routed positions:
+ *   loss = balance_coef * E / (nv k) * sum_e count_e * (mean of p_e)
+ *          + z_coef * (mean of lse^2)            (means over the nv positions)
+ * with count_e the rows of expert e, a constant in the gradient.  loss (one
+ * fp32) may be NULL when both coefficients are 0, else it is written in any
+ * case.  Sums over rows are fp32 within a block of at most n / 256 + 64 rows,
+ * fp64 across.
+ * bpt_moe_route_bwd: dlogits [n, E] from dweights [n, k] and dloss; of r it
+ * reads ids and offsets. */
+#define BPT_MOE_BAD_LOGIT_SITE 951
+size_t bpt_moe_route_workspace_bytes(const bpt_moe_config* cfg);
+int bpt_moe_route_fwd(const bpt_moe_config* cfg, const void* logits, const bpt_moe_route* r, float* loss, void* ws,
+                      size_t ws_bytes, void* stream);
+int bpt_moe_route_bwd(const bpt_moe_config* cfg, const void* logits, const bpt_moe_route* r, const void* dweights,
+                      float dloss, void* dlogits, void* stream);
+
+/* The experts' network: y_t = sum_j weights[t, j] * W2_e act(W1_e x_t [, W3_e
+ * x_t]) with e the expert of pair (t, j); pairs without a row add nothing.
+ *   x, y      [n, h] bf16;  w1, w3 [E, f, h], w2 [E, h, f] bf16 (w3: SwiGLU)
+ *   r         weights, offsets, order and slot are read (ids is not); any
+ *             grouping of pairs in this form will do.  An order or slot entry
+ *             outside its range is taken as none.
+ *   saved     bpt_moe_saved_bytes(cfg) for the backward (two [n k, f] bf16
+ *             tensors), or NULL: inference
+ *   ws        bpt_moe_ffn_workspace_bytes(cfg, pass), one per call in flight
+ *   dy, dx    [n, h] bf16;  dweights [n, k];  dw1, dw3, dw2 like the weights
+ * An expert without rows has gradients of 0.  The activation, its gradient and
+ * each choice's row of y and dx are rounded to bf16 (2^-9 of their value) where
+ * they are a tensor core's operand or wait for the sum over the choices; sums
+ * are fp32. */
+size_t bpt_moe_saved_bytes(const bpt_moe_config* cfg);
+size_t bpt_moe_ffn_workspace_bytes(const bpt_moe_config* cfg, int pass);
+int bpt_moe_ffn_fwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const void* x, const void* w1, const void* w3,
+                    const void* w2, void* y, void* saved, void* ws, size_t ws_bytes, void* stream);
+int bpt_moe_ffn_bwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const void* x, const void* w1, const void* w3,
+                    const void* w2, const void* saved, const void* dy, void* dx, void* dweights, void* dw1, void* dw3,
+                    void* dw2, void* ws, size_t ws_bytes, void* stream);
+
+/* Products over ragged groups of rows, group e the rows [offsets[e],
+ * offsets[e + 1]) and its own matrix:
+ *   BPT_GROUPED_NT  out[r, :] = a[r, :] b_e^T   a [rows, k], b [groups, n, k], out [rows, n]
+ *   BPT_GROUPED_NN  out[r, :] = a[r, :] b_e     a [rows, k], b [groups, k, n], out [rows, n]
+ *   BPT_GROUPED_TN  out_e = a_e^T b_e           a [rows, k], b [rows, n], out [groups, k, n]
+ *   rows         of a;  n, k multiples of 8;  groups 1 .. 1024
+ *   offsets      [groups + 1] int32 (device), rising within [0, rows]; a group
+ *                may be empty (TN: its matrix is 0).  Rows in no group are not
+ *                written and not read into any result.  A group whose offsets
+ *                fall, leave [0, rows] or start before an earlier group's end
+ *                counts as empty and is recorded in the device error word
+ *                (BPT_EINVAL, BPT_GROUPED_BAD_OFFSET_SITE).
+ *   out_dtype    BPT_DTYPE_*;  a and b are bf16, sums fp32
+ *   flags        BPT_FLAG_ACCUM_GRADS (out +=; fp32 only),
+ *                BPT_FLAG_DETERMINISTIC (accepted: sums have a fixed order),
+ *                BPT_FLAG_DEBUG_CHECKS
+ * rows above 2^29 returns BPT_EUNSUPPORTED; out may not share bytes with an
+ * input. */
+enum { BPT_GROUPED_NT = 0, BPT_GROUPED_NN = 1, BPT_GROUPED_TN = 2 };
+#define BPT_GROUPED_BAD_OFFSET_SITE 953
+typedef struct {
+  int32_t rows, n, k, groups, form, out_dtype, flags;
+} bpt_grouped_config;
+int bpt_grouped_gemm(const bpt_grouped_config* cfg, const void* a, const void* b, const int32_t* offsets, void* out,
+                     void* stream);
+
 /* Opt-in launch profiler.  bpt_profile_enable(1) makes every later launch
  * of this process record a pair of CUDA events on its stream, tagged with
  * the launch's kind and its algorithmic work (FLOPs for tensor-core kernels,
