@@ -32,9 +32,9 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   p.rows = (int)op.rows;
   p.N = (int)op.N;
   p.nt = (int)((op.N + BN - 1) / BN);
-  p.a_rows = (int)op.a_rows;
   p.order = op.order;
-  p.top_k = op.top_k;
+  p.by_k = ((1ull << 37) + op.top_k - 1) / op.top_k;
+  p.a_cols = (int)(tn ? op.M : op.K);
   p.pairs = (int)op.rows;
   p.out = op.out;
   p.out2 = op.out2;
@@ -62,7 +62,7 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
     for (int i = 0; i < p.segs; ++i) {
       const void* a = i ? op.a2 : op.a;
       rc |= make_map_2d(&p.map_a[i], a, op.a_rows, op.K, op.K, BK, BM, 128);
-      rc |= make_map_2d(&p.map_ag[i], a, op.a_rows, op.K, op.K, BK, 1, 128);
+      p.a[i] = reinterpret_cast<const __nv_bfloat16*>(a);
     }
     for (int i = 0; i < (dual || two ? 2 : 1); ++i) {
       const void* w = i ? op.w2 : op.w;
@@ -75,14 +75,14 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
     p.segs = op.a2 ? 2 : 1;
     p.M = (int)op.M;
     p.mt = (int)((op.M + TM - 1) / TM);
-    p.b_rows = (int)op.b_rows;
     for (int i = 0; i < p.segs; ++i) {
       const void* a = i ? op.a2 : op.a;
       rc |= make_map_2d(&p.map_a[i], a, op.a_rows, op.M, op.M, 64, BK, 128);
-      rc |= make_map_2d(&p.map_ag[i], a, op.a_rows, op.M, op.M, 64, 1, 128);
+      p.a[i] = reinterpret_cast<const __nv_bfloat16*>(a);
     }
     rc |= make_map_2d(&p.map_b[0], op.b, op.b_rows, op.N, op.N, 64, BK, 128);
-    rc |= make_map_2d(&p.map_bg, op.b, op.b_rows, op.N, op.N, 64, 1, 128);
+    p.b = reinterpret_cast<const __nv_bfloat16*>(op.b);
+    p.b_cols = (int)op.N;
     mt_all = (int64_t)op.groups * p.segs * p.mt;
     units = mt_all * p.nt;
   }

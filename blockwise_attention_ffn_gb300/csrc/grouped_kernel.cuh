@@ -14,15 +14,18 @@
 // Warp roles, ring and accumulators are those of gemm_kernel.cuh (a producer
 // warp, an issuing warp, eight epilogue warps; two accumulators; one SM or a
 // pair of SMs per tile).  What is different:
-//   - Rows are gathered on the way in: the 32 lanes of the producer warp hold
-//     the four row indices of a quad each and issue one 4-row TMA gather a
-//     stage, so the 128 rows of a CTA's A tile come from where the router left
-//     them and no copy in the groups' order is ever made.  Quads behind the
-//     group's last row are not loaded: what their shared memory holds reaches
-//     only accumulator rows that are never stored.
+//   - Rows are gathered on the way in: two more warps copy them, 16 bytes a
+//     lane, from where the router left them into the ring (cp.async, eight
+//     lanes a 128-byte line, the swizzle applied by hand), so no copy in the
+//     groups' order is ever made.  Lines behind the group's last row are not
+//     copied: what their shared memory holds reaches only accumulator rows
+//     that are never stored.  (TMA's own four-row gathers were taken first:
+//     an instruction each, they fed a stage in about 1000 cycles where the
+//     products take 256: 458 TFLOP/s on the gate and up products of 8 experts
+//     of 4096 x 14336, 4096 positions.)
 //   - TN runs over a group's rows as K.  The last, partial block of 64 rows
-//     is loaded by gathers too, with an index outside the tensor (a row of
-//     zeros) behind the group's end: what lies there, a NaN even, stays out.
+//     is copied by those warps too, with zeros behind the group's end: what
+//     lies there, a NaN even, stays out.
 //   - Weights are 3-D maps [G, rows, cols]: a tile that runs over a matrix's
 //     edge reads zeros, not the next group's matrix.
 #pragma once
@@ -37,21 +40,24 @@ using gk::A_BYTES;
 using gk::BK;
 using gk::BM;
 using gk::NUM_EPI_WARPS;
-using gk::NUM_THREADS;
+constexpr int COPY_WARP = 2 + NUM_EPI_WARPS;  // the first of the two that copy rows
+constexpr int COPY_WARPS = 2;
 
 struct Params {
-  CUtensorMap map_a[2];   // A tiles (TN: {64, 64} boxes)
-  CUtensorMap map_ag[2];  // A gathers (one-row boxes)
-  CUtensorMap map_b[2];   // weights, or TN: B tiles
-  CUtensorMap map_bg;     // TN: B gathers
+  CUtensorMap map_a[2];  // A tiles (TN: {64, 64} boxes)
+  CUtensorMap map_b[2];  // weights, or TN: B tiles
+  // A and TN's B for the copying warps: row-major, a_rows and b_rows rows of
+  // a_cols and b_cols columns
+  const __nv_bfloat16 *a[2], *b;
+  int a_cols, b_cols;
   const int* offsets;
   int groups, rows;
   int M, N, nkt, segs;    // TN: M; NT, NN: k-tiles of one segment and the number of segments (TN: segments of M)
   int mt, nt;             // TN: tile rows per segment; tile columns
   int band;               // tile rows walked before the next tile column (m fastest)
-  int a_rows, b_rows;     // rows of the gathered tensors (the index of a row of zeros)
   const int* order;       // pair at each sorted row, or NULL: row r is row r
-  int top_k, pairs;
+  unsigned long long by_k;  // ceil(2^37 / top_k): pair / top_k = pair * by_k >> 37, exact below 2^29 pairs and 32 choices
+  int pairs;
   void *out, *out2, *out3;
   int out_f32;
   float beta;
@@ -132,20 +138,21 @@ __device__ __forceinline__ void place(const Params& p, int unit, const int* s_un
   at.n0 = nb * BN;
 }
 
-// four rows of 64 columns, by index
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int4 r) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
-      : "memory");
+// 16 bytes into shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(some ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int4 r) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w)
-      : "memory");
+// arrives once for this thread on `bar` (whose count has this thread in it)
+// when its copies so far have landed
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// arrive on another CTA's mbarrier (shared::cluster address), ordering this
+// CTA's memory alone: the products that wait for it read this CTA's copies
+// from this CTA's shared memory
+__device__ __forceinline__ void mbar_arrive_other(uint32_t cl_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
   asm volatile(
@@ -262,10 +269,20 @@ constexpr int smem_bytes() {
 // BN: tile width.  AG, BG: rows of A (TN: of A, of B) gathered.  DUAL: two
 // weight tiles against one A tile (gate and up).  PAIR: a 256-row tile per
 // cluster of two CTAs.
+template <int FORM, bool AG>
+constexpr bool copies() {  // whether the kernel has the copying warps
+  return AG || FORM == GROUPED_TN;
+}
+template <int FORM, bool AG>
+constexpr int threads() {
+  return 32 * (2 + NUM_EPI_WARPS + (copies<FORM, AG>() ? COPY_WARPS : 0));
+}
+
 template <int FORM, int EPI, int BN, bool AG, bool BG, bool DUAL, bool PAIR>
-__global__ void __launch_bounds__(NUM_THREADS, 1) grouped_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const __grid_constant__ Params p) {
   constexpr bool TN = FORM == GROUPED_TN;
   constexpr bool B_MN = FORM != GROUPED_NT;
+  constexpr bool COPY = copies<FORM, AG>();
   constexpr int BNS = PAIR ? BN / 2 : BN;  // rows (columns) of each B this CTA stages
   constexpr int STAGE_BYTES = stage_bytes<BN, DUAL, PAIR>();
   constexpr int STAGES = ring_stages<STAGE_BYTES>();
@@ -283,12 +300,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) grouped_kernel(const __grid_co
   uint64_t* acc_full = empty + STAGES;  // [2]
   uint64_t* acc_empty = acc_full + 2;   // [2]
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* copied = drain + 1;  // [STAGES], this CTA's copying warps
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(copied + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* s_unit = reinterpret_cast<int*>(smem + STAGES * STAGE_BYTES + 256);  // [groups + 1]
   int* s_lo = s_unit + GROUPED_MAX_GROUPS + 4;
   int* s_cnt = s_lo + GROUPED_MAX_GROUPS;
-  static_assert((2 * STAGES + 5) * 8 + 8 <= 256, "barriers");
+  static_assert((3 * STAGES + 5) * 8 + 8 <= 256, "barriers");
 
   const int warp = warp_id();
   const int lane = lane_id();
@@ -298,8 +316,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) grouped_kernel(const __grid_co
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      // the loads' bytes, and word of the other CTA's copies
+      mbar_init(&full[s], 1 + (COPY && PAIR ? 1 : 0));
       mbar_init(&empty[s], 1);
+      mbar_init(&copied[s], 32 * COPY_WARPS);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&acc_full[a], 1);
@@ -332,76 +352,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) grouped_kernel(const __grid_co
   auto k_tiles = [&](const Place& at) { return TN ? (at.cnt + BK - 1) / BK : p.segs * p.nkt; };
 
   if (warp == 0) {
-    // -------------------------------------------------- producer (the warp)
-    const uint32_t full0 = PAIR ? cluster_addr(smem_u32(full), 0) : smem_u32(full);
-    const uint32_t smem_base = smem_u32(smem);
-    uint32_t it = 0;
-    bool ok = true;
-    Place at;
-    at.e = 0;
-    auto gather = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int4 r) {
-      if constexpr (PAIR) tma_gather4_pair(dst, map, bar, x, r);
-      else tma_gather4(dst, map, bar, x, r);
-    };
-    auto load2 = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
-      if constexpr (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-            : "memory");
-      else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-            : "memory");
-    };
-    auto load3 = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
-      if constexpr (PAIR) tma_load_3d_pair(dst, map, bar, x, y, z);
-      else tma_load_3d(dst, map, bar, x, y, z);
-    };
-    // row of the rows operand at sorted row r (in range), by the router's order
-    auto row_of = [&](int r) {
-      const int q = p.order[r];
-      return q < 0 || q >= p.pairs ? p.a_rows + p.b_rows : q / p.top_k;
-    };
-    auto claim = [&](int s) {  // the stage is free, by one verdict of the warp
-      return it < (uint32_t)STAGES || bounded_wait_w(&empty[s], ((it / STAGES) & 1) ^ 1, abort_flag, 101, p.err);
-    };
-    for (int unit = unit0; ok && unit < nunits; unit += units_in_flight) {
-      place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
-      const int nbs = at.n0 + (int)rank * BNS;
-      if constexpr (!TN) {
-        const int mine = at.m0 + (int)rank * BM;  // this CTA's first row in the group
-        int4 q = make_int4(0, 0, 0, 0);           // this lane's quad
-        bool live = false;
-        uint32_t bytes = STAGE_BYTES * (PAIR ? 2 : 1);
-        if constexpr (AG) {
-          const int r0 = mine + 4 * lane;
-          live = r0 < at.cnt;
-          auto one = [&](int r) { return r >= at.cnt ? p.a_rows : p.order ? row_of(at.lo + r) : at.lo + r; };
-          if (live) q = make_int4(one(r0), one(r0 + 1), one(r0 + 2), one(r0 + 3));
-          // bytes of both CTAs' live quads and weights
-          bytes = (PAIR ? 2 : 1) * (STAGE_BYTES - A_BYTES);
-          const int left = at.cnt - at.m0;
-          bytes += (uint32_t)((min(left, TM) + 3) / 4) * 512u;
-        }
-        const int nk = p.segs * p.nkt;
+    if (lane == 0) {
+      // ------------------------------------------------ producer
+      const uint32_t full0 = PAIR ? cluster_addr(smem_u32(full), 0) : smem_u32(full);
+      const uint32_t smem_base = smem_u32(smem);
+      uint32_t it = 0;
+      bool ok = true;
+      Place at;
+      at.e = 0;
+      auto load2 = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+        if constexpr (PAIR)
+          asm volatile(
+              "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+              " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+              "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+              : "memory");
+        else
+          asm volatile(
+              "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+              " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+              "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+              : "memory");
+      };
+      auto load3 = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+        if constexpr (PAIR) tma_load_3d_pair(dst, map, bar, x, y, z);
+        else tma_load_3d(dst, map, bar, x, y, z);
+      };
+      for (int unit = unit0; ok && unit < nunits; unit += units_in_flight) {
+        place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
+        const int nbs = at.n0 + (int)rank * BNS;
+        const int ma = at.m0 + (int)rank * BM;
+        const int nk = k_tiles(at);
         for (int kt = 0; kt < nk; ++kt) {
           const int s = it % STAGES;
-          if (!claim(s)) {
+          if (it >= (uint32_t)STAGES && !bounded_wait(&empty[s], ((it / STAGES) & 1) ^ 1, abort_flag, 101, p.err)) {
             ok = false;
             break;
           }
           const uint32_t sa = smem_base + s * STAGE_BYTES;
           const uint32_t sb = sa + A_BYTES;
           const uint32_t fb = full0 + 8u * (uint32_t)s;
-          const int seg = FORM == GROUPED_NN && kt >= p.nkt ? 1 : 0;
-          const int kx = (kt - seg * p.nkt) * BK;
-          if (lane == 0) {
-            if (rank == 0) mbar_expect_tx(&full[s], bytes);
-            if constexpr (!AG) load2(sa, &p.map_a[seg], fb, kx, at.lo + mine);
+          if constexpr (!TN) {
+            const int seg = FORM == GROUPED_NN && kt >= p.nkt ? 1 : 0;
+            const int kx = (kt - seg * p.nkt) * BK;
+            if (rank == 0) mbar_expect_tx(&full[s], (PAIR ? 2 : 1) * (STAGE_BYTES - (AG ? A_BYTES : 0)));
+            if constexpr (!AG) load2(sa, &p.map_a[seg], fb, kx, at.lo + ma);
             if constexpr (FORM == GROUPED_NT) {
               load3(sb, &p.map_b[0], fb, kx, nbs, at.e);
               if constexpr (DUAL) load3(sb + BNS * BK * 2, &p.map_b[1], fb, kx, nbs, at.e);
@@ -409,92 +404,160 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) grouped_kernel(const __grid_co
 #pragma unroll
               for (int c = 0; c < BNS / 64; ++c) load3(sb + c * 8192, &p.map_b[seg], fb, nbs + c * 64, kx, at.e);
             }
-          }
-          __syncwarp();
-          if constexpr (AG) {
-            if (live) gather(sa + lane * 512, &p.map_ag[seg], fb, kx, q);
+          } else {
+            const bool whole = (kt + 1) * BK <= at.cnt;
+            const int y = at.lo + kt * BK;
+            const uint32_t bytes = whole ? (AG ? 0 : A_BYTES) + (BG ? 0 : STAGE_BYTES - A_BYTES) : 0;
+            if (rank == 0) mbar_expect_tx(&full[s], (PAIR ? 2 : 1) * bytes);
+            if (!AG && whole) {
+              load2(sa, &p.map_a[at.seg], fb, ma, y);
+              load2(sa + 8192, &p.map_a[at.seg], fb, ma + 64, y);
+            }
+            if (!BG && whole) {
+#pragma unroll
+              for (int c = 0; c < BNS / 64; ++c) load2(sb + c * 8192, &p.map_b[0], fb, nbs + c * 64, y);
+            }
           }
           ++it;
         }
+      }
+      if (*abort_flag) {
+        // let every load issued land before the CTA goes away; a pair's ranks
+        // cannot wait for one another's stragglers and give them a fixed time
+        if (rank == 0 && !COPY)
+          for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; ++j) drain_wait(&full[j % STAGES], (j / STAGES) & 1);
+        if (PAIR || COPY) {
+          const long long t0 = clock64();
+          while (clock64() - t0 < 1000000) {
+          }
+        }
+      }
+    }
+  } else if (COPY && warp >= COPY_WARP) {
+    // -------------------------------------------------- copying warps
+    // A stage's operand is 128 lines of 128 bytes for the CTA's 128 rows (TN:
+    // 64 rows of each 64-column chunk).  A lane holds 16 bytes of a line at
+    // their swizzled place: chunk (lane % 8) ^ (line % 8).
+    const int w = warp - COPY_WARP;
+    const uint32_t smem_base = smem_u32(smem);
+    const int col = (lane & 7) * 8;  // this lane's columns of a line
+    uint32_t it = 0;
+    bool ok = true;
+    Place at;
+    at.e = 0;
+    auto row_of = [&](int r) {  // row of the gathered tensor at row r of the order; -1: none
+      const int q = p.order[r];
+      return q < 0 || q >= p.pairs ? -1 : (int)(((unsigned long long)(unsigned)q * p.by_k) >> 37);
+    };
+    auto claim = [&]() {
+      const int s = it % STAGES;
+      return it < (uint32_t)STAGES || bounded_wait_w(&empty[s], ((it / STAGES) & 1) ^ 1, abort_flag, 102, p.err);
+    };
+    auto next = [&]() {
+      copy_arrive(&copied[it % STAGES]);
+      ++it;
+    };
+    for (int unit = unit0; ok && unit < nunits; unit += units_in_flight) {
+      place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
+      const int nk = k_tiles(at);
+      if constexpr (!TN) {
+        // lines w * 64 + 4 i + lane / 8 of the CTA's rows
+        const int r0 = at.m0 + (int)rank * BM + w * 64 + (lane >> 3);
+        int idx[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int r = r0 + 4 * i;
+          idx[i] = r >= at.cnt ? -2 : p.order ? row_of(at.lo + r) : at.lo + r;
+        }
+        const int live = (at.cnt - r0 + 3) / 4;  // lines of this lane with a row
+        const uint32_t line0 = (uint32_t)(w * 64 + (lane >> 3));
+        for (int kt = 0; kt < nk; ++kt) {
+          if (!claim()) {
+            ok = false;
+            break;
+          }
+          const int seg = FORM == GROUPED_NN && kt >= p.nkt ? 1 : 0;
+          const int x = (kt - seg * p.nkt) * BK + col;
+          const bool in = x < p.a_cols;
+          const __nv_bfloat16* src = p.a[seg] + (in ? x : 0);
+          const uint32_t sa = smem_base + (it % STAGES) * STAGE_BYTES;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (i < live) {
+              const uint32_t line = line0 + 4 * i;
+              copy16(sa + line * 128 + ((((lane & 7) ^ line) & 7) << 4), src + (long long)max(idx[i], 0) * p.a_cols, in && idx[i] >= 0);
+            }
+          }
+          next();
+        }
       } else {
-        const int ma = at.m0 + (int)rank * BM;
-        const int nk = (at.cnt + BK - 1) / BK;
-        const int quad = lane & 15, c0 = lane >> 4;
-        // rows of this lane's quad in block kt: by the router's order
-        // (gathered operands), or as they lie (the last, partial block)
-        auto rows_of = [&](int kt) {
-          const int r0 = kt * BK + 4 * quad;
-          auto one = [&](int r) { return r < at.cnt ? row_of(at.lo + r) : p.a_rows + p.b_rows; };
-          return make_int4(one(r0), one(r0 + 1), one(r0 + 2), one(r0 + 3));
+        // rows w * 32 + 4 i + lane / 8 of a block, in every chunk of 64 columns
+        const int ma = at.m0 + (int)rank * BM, nbs = at.n0 + (int)rank * BNS;
+        constexpr int AHEAD = 4;  // blocks whose rows of the order are on their way
+        int ring[AG || BG ? AHEAD : 1][8];
+        auto fetch = [&](int kt, int (&v)[8]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = kt * BK + w * 32 + 4 * i + (lane >> 3);
+            v[i] = r < at.cnt ? p.order[at.lo + r] : -1;
+          }
         };
-        constexpr int AHEAD = 4;  // blocks whose indices are on their way
-        int4 ring[AHEAD];
+        auto lines = [&](uint32_t dst, const __nv_bfloat16* src, int cols, int x0, int chunks, const int (&rows)[8]) {
+          for (int c = 0; c < chunks; ++c) {
+            const int x = x0 + c * 64 + col;
+            const bool in = x < cols;
+            const __nv_bfloat16* from = src + (in ? x : 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t line = (uint32_t)(w * 32 + 4 * i + (lane >> 3));
+              copy16(dst + c * 8192 + line * 128 + ((((lane & 7) ^ line) & 7) << 4), from + (long long)max(rows[i], 0) * cols,
+                     in && rows[i] >= 0);
+            }
+          }
+        };
         if constexpr (AG || BG) {
 #pragma unroll
-          for (int u = 0; u < AHEAD; ++u) ring[u] = rows_of(u);
+          for (int u = 0; u < AHEAD; ++u) fetch(u, ring[u]);
         }
         for (int k4 = 0; ok && k4 < nk; k4 += AHEAD) {
 #pragma unroll
           for (int u = 0; u < AHEAD; ++u) {
             const int kt = k4 + u;
             if (kt >= nk) break;
-            const int s = it % STAGES;
-            if (!claim(s)) {
+            if (!claim()) {
               ok = false;
               break;
             }
-            int4 by_order = make_int4(0, 0, 0, 0);
-            if constexpr (AG || BG) {
-              by_order = ring[u];
-              ring[u] = rows_of(kt + AHEAD);
-            }
-            const uint32_t sa = smem_base + s * STAGE_BYTES;
+            const uint32_t sa = smem_base + (it % STAGES) * STAGE_BYTES;
             const uint32_t sb = sa + A_BYTES;
-            const uint32_t fb = full0 + 8u * (uint32_t)s;
             const bool whole = (kt + 1) * BK <= at.cnt;
-            const int y = at.lo + kt * BK;
-            int4 as_is = make_int4(0, 0, 0, 0);
+            if constexpr (AG || BG) {
+              int rows[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int q = ring[u][i];
+                rows[i] = q < 0 || q >= p.pairs ? -1 : (int)(((unsigned long long)(unsigned)q * p.by_k) >> 37);
+              }
+              fetch(kt + AHEAD, ring[u]);
+              if constexpr (AG) lines(sa, p.a[0], p.a_cols, ma, 2, rows);
+              else lines(sb, p.b, p.b_cols, nbs, BNS / 64, rows);
+            }
             if (!whole) {
-              const int r0 = kt * BK + 4 * quad;
-              auto one = [&](int r) { return r < at.cnt ? at.lo + r : p.a_rows + p.b_rows; };
-              as_is = make_int4(one(r0), one(r0 + 1), one(r0 + 2), one(r0 + 3));
-            }
-            if (lane == 0) {
-              if (rank == 0) mbar_expect_tx(&full[s], (PAIR ? 2 : 1) * STAGE_BYTES);
-              if (!AG && whole) {
-                load2(sa, &p.map_a[at.seg], fb, ma, y);
-                load2(sa + 8192, &p.map_a[at.seg], fb, ma + 64, y);
-              }
-              if (!BG && whole) {
+              int rows[8];
 #pragma unroll
-                for (int c = 0; c < BNS / 64; ++c) load2(sb + c * 8192, &p.map_b[0], fb, nbs + c * 64, y);
+              for (int i = 0; i < 8; ++i) {
+                const int r = kt * BK + w * 32 + 4 * i + (lane >> 3);
+                rows[i] = r < at.cnt ? at.lo + r : -1;
               }
+              if constexpr (!AG) lines(sa, at.seg ? p.a[1] : p.a[0], p.a_cols, ma, 2, rows);
+              if constexpr (!BG) lines(sb, p.b, p.b_cols, nbs, BNS / 64, rows);
             }
-            __syncwarp();
-            if (AG || !whole) gather(sa + c0 * 8192 + quad * 512, &p.map_ag[at.seg], fb, ma + c0 * 64, AG ? by_order : as_is);
-            if (BG || !whole) {
-#pragma unroll
-              for (int c = 0; c < BNS / 64; c += 2)
-                if (c + c0 < BNS / 64)
-                  gather(sb + (c + c0) * 8192 + quad * 512, &p.map_bg, fb, nbs + (c + c0) * 64, BG ? by_order : as_is);
-            }
-            ++it;
+            next();
           }
         }
       }
     }
-    __syncwarp();
-    if (lane == 0 && *abort_flag) {
-      // let every load issued land before the CTA goes away; a pair's ranks
-      // cannot wait for one another's stragglers and give them a fixed time
-      if (rank == 0)
-        for (uint32_t j = (it > (uint32_t)STAGES ? it - STAGES : 0); j < it; ++j) drain_wait(&full[j % STAGES], (j / STAGES) & 1);
-      if (PAIR) {
-        const long long t0 = clock64();
-        while (clock64() - t0 < 1000000) {
-        }
-      }
-    }
+    copy_wait_all();
   } else if (warp == 1) {
     // -------------------------------------------------- MMA issuer
     if (rank == 0) {
@@ -522,10 +585,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) grouped_kernel(const __grid_co
         const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
         for (int kt = 0; kt < nk; ++kt) {
           const int s = it % STAGES;
-          if (!bounded_wait_w(&full[s], (it / STAGES) & 1, abort_flag, 103, p.err)) {
+          if (!bounded_wait_w(&full[s], (it / STAGES) & 1, abort_flag, 103, p.err) ||
+              (COPY && !bounded_wait_w(&copied[s], (it / STAGES) & 1, abort_flag, 104, p.err))) {
             ok = false;
             break;
           }
+          if constexpr (COPY) fence_proxy_async_smem();  // the copies are read by the tensor core
           tc_fence_after();
           const uint32_t sa = smem_base + s * STAGE_BYTES;
           const uint32_t sb = sa + A_BYTES;
@@ -556,8 +621,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) grouped_kernel(const __grid_co
         else umma_commit_w(drain);
         drain_wait(drain, 0);
       }
+    } else if (COPY) {
+      // the pair's other CTA: word of every stage's copies to the one that issues
+      const uint32_t full0 = cluster_addr(smem_u32(full), 0);
+      uint32_t it = 0;
+      bool ok = true;
+      Place at;
+      at.e = 0;
+      for (int unit = unit0; ok && unit < nunits; unit += units_in_flight) {
+        place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
+        const int nk = k_tiles(at);
+        for (int kt = 0; kt < nk; ++kt, ++it) {
+          const int s = it % STAGES;
+          if (!bounded_wait_w(&copied[s], (it / STAGES) & 1, abort_flag, 104, p.err)) {
+            ok = false;
+            break;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_other(full0 + 8u * (uint32_t)s);
+        }
+      }
     }
-  } else {
+  } else if (warp < COPY_WARP) {
     // -------------------------------------------------- epilogue (warps 2..9)
     constexpr int EPI_COLS = BN / 2;
     constexpr int CH = EPI_COLS < 32 ? EPI_COLS : 32;
@@ -675,7 +761,7 @@ int launch(Params& p, int64_t units, cudaStream_t st) {
   }
   if (slots <= 0) return 3;
   const int n = (int)std::min<int64_t>(units, slots);
-  return launch_dependent(kern, PAIR ? 2 * n : n, PAIR ? 2 : 1, dim3(NUM_THREADS), (size_t)SMEM, st, p) == cudaSuccess ? 0 : 3;
+  return launch_dependent(kern, PAIR ? 2 * n : n, PAIR ? 2 : 1, dim3(threads<FORM, AG>()), (size_t)SMEM, st, p) == cudaSuccess ? 0 : 3;
 }
 
 // One translation unit per form (they compile in parallel); `small`: 64

@@ -128,36 +128,28 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
 #pragma unroll
       for (int i = 0; i < V; ++i) v[i] = -INFINITY;
     }
-    uint32_t taken = 0;  // of this lane's values
+    uint32_t key[V];  // 0: taken, or not to be chosen
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = v[i] > -INFINITY ? sort_key(v[i]) : 0u;
     float m = 0.f, total = 0.f, top_sum = 0.f, mine = 0.f, first = 0.f;
     for (int j = 0; j < p.k; ++j) {
-      // the lane's largest value left, the lowest index of equals
-      uint32_t best = 0;
-      int at = 0;
+      // the largest key left; of equals the first lane's, and its first
+      uint32_t best = key[0];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t key = v[i] > -INFINITY && !((taken >> i) & 1u) ? sort_key(v[i]) : 0u;
-        if (key > best) {
-          best = key;
-          at = i;
-        }
-      }
-      int idx = c + at;
+      for (int i = 1; i < V; ++i) best = max(best, key[i]);
+      const uint32_t own = best;
       if constexpr (G == 32) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        idx = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)idx : 0x7fffffffu);
-        best = top;
+        best = __reduce_max_sync(0xffffffffu, best);
       } else {
 #pragma unroll
-        for (int d = 1; d < G; d <<= 1) {
-          const uint32_t ob = __shfl_xor_sync(0xffffffffu, best, d);
-          const int oi = __shfl_xor_sync(0xffffffffu, idx, d);
-          if (ob > best || (ob == best && oi < idx)) {
-            best = ob;
-            idx = oi;
-          }
-        }
+        for (int d = 1; d < G; d <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, d));
       }
+      int at = 0;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) at = key[i] == best ? i : at;
+      const uint32_t holds = __ballot_sync(0xffffffffu, own == best) >> (lane - sub);
+      const int from = __ffs(holds) - 1;  // below G: the group's own maximum is among its lanes
+      const int idx = from * V + __shfl_sync(0xffffffffu, at, lane - sub + from);
       const bool some = best != 0u;
       const float val = some ? __uint_as_float((best & 0x80000000u) ? (best & 0x7fffffffu) : ~best) : -INFINITY;
       if (j == 0) {
@@ -170,7 +162,11 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
       }
       const float ex = some ? expf(val - m) : 0.f;
       top_sum += ex;
-      if (some && idx >= c && idx < c + V) taken |= 1u << (idx - c);
+      if (sub == from) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i == at) key[i] = 0u;
+      }
       // lane j % G of the group keeps the j-th choice until all are known
       if (in && sub == j % G) {
         p.ids[row * p.k + j] = some ? idx : -1;
@@ -276,7 +272,7 @@ __device__ void place_rows(const RouteParams& p, int64_t r0, int64_t r1, int b, 
     const int e = e0 + (int)threadIdx.x % span, sl = (int)threadIdx.x / span;
     int before = 0, all = 0;
     if (sl < slices)
-#pragma unroll 8
+#pragma unroll 16
       for (int q = sl; q < p.nblk; q += slices) {
         const int v = p.hist[(int64_t)q * p.E + e];
         all += v;
@@ -357,38 +353,56 @@ __device__ void place_rows(const RouteParams& p, int64_t r0, int64_t r1, int b, 
   // behind the last routed row
   const int64_t pairs = p.n * p.k;
   for (int64_t i = s_all + (int64_t)b * THREADS + threadIdx.x; i < pairs; i += (int64_t)p.nblk * THREADS) p.order[i] = -1;
-  if (b == 0) {
-    // the losses, over the blocks in order
-    __shared__ double s_loss[WARPS];
-    __shared__ int s_live;
-    if (threadIdx.x == 0) {
-      int l = 0;
-      for (int q = 0; q < p.nblk; ++q) l += p.live[q];
-      s_live = l;
-      p.offsets[p.E + 1] = l;
-    }
-    __syncthreads();
-    if (p.loss) {
-      const double nv = s_live > 0 ? s_live : 1;
-      double t = 0.0;
-      if (p.balance != 0.f)
-        for (int e = threadIdx.x; e < p.E; e += THREADS) {
-          double ps = 0.0;
-          for (int q = 0; q < p.nblk; ++q) ps += (double)p.psum[(int64_t)q * p.E + e];
-          t += (double)p.balance * p.E / (nv * p.k) * s_tot[e] * (ps / nv);
-        }
-      if (p.zc != 0.f)
-        for (int q = threadIdx.x; q < p.nblk; q += THREADS) t += (double)p.zc * (double)p.zsum[q] / nv;
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) t += __shfl_down_sync(0xffffffffu, t, d);
-      if (lane == 0) s_loss[warp] = t;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        double s = 0.0;
-        for (int w = 0; w < WARPS; ++w) s += s_loss[w];
-        *p.loss = (float)s;
+}
+
+// The losses and the number of routed rows, by one block: sums over the
+// blocks of rows, in an order fixed by their number.
+__device__ void finish_losses(const RouteParams& p) {
+  __shared__ double s_loss[WARPS];
+  __shared__ int s_live[WARPS];
+  const int lane = lane_id(), warp = warp_id();
+  int l = 0;
+  for (int q = threadIdx.x; q < p.nblk; q += THREADS) l += p.live[q];
+  l = __reduce_add_sync(0xffffffffu, l);
+  if (lane == 0) s_live[warp] = l;
+  __syncthreads();
+  l = 0;
+  for (int w = 0; w < WARPS; ++w) l += s_live[w];
+  if (threadIdx.x == 0) p.offsets[p.E + 1] = l;
+  if (!p.loss) return;
+  const double nv = l > 0 ? l : 1;
+  double t = 0.0;
+  if (p.balance != 0.f) {
+    // sum_e count_e sum_t p_te: slices of the blocks per expert
+    for (int e0 = 0; e0 < p.E; e0 += THREADS) {
+      const int span = min(p.E - e0, THREADS), slices = THREADS / span;
+      const int e = e0 + (int)threadIdx.x % span, sl = (int)threadIdx.x / span;
+      // an expert's count is needed whole: every slice adds its own
+      int count = 0;
+      double ps = 0.0;
+      if (sl < slices) {
+#pragma unroll 16
+        for (int q = 0; q < p.nblk; ++q) count += p.hist[(int64_t)q * p.E + e];
+#pragma unroll 16
+        for (int q = sl; q < p.nblk; q += slices) ps += (double)p.psum[(int64_t)q * p.E + e];
       }
+      t += ps * (double)count;
     }
+    t *= (double)p.balance * p.E / (nv * nv * p.k);
+  }
+  if (p.zc != 0.f) {
+    double z = 0.0;
+    for (int q = threadIdx.x; q < p.nblk; q += THREADS) z += (double)p.zsum[q];
+    t += (double)p.zc / nv * z;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) t += __shfl_down_sync(0xffffffffu, t, d);
+  if (lane == 0) s_loss[warp] = t;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double sum = 0.0;
+    for (int w = 0; w < WARPS; ++w) sum += s_loss[w];
+    *p.loss = (float)sum;
   }
 }
 
@@ -408,6 +422,7 @@ __global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams 
   int* s_count = reinterpret_cast<int*>(s_dyn);
   wait_for_previous();
   let_next_start();
+  if ((int)blockIdx.x == p.nblk) return finish_losses(p);
   const int64_t r0 = min(p.n, blockIdx.x * p.per), r1 = min(p.n, r0 + p.per);
   place_rows(p, r0, r1, blockIdx.x, s_count, s_count + WARPS * p.E, s_count + (WARPS + 1) * p.E);
 }
@@ -421,6 +436,7 @@ __global__ void __launch_bounds__(THREADS) route_one_kernel(const RouteParams p)
   let_next_start();
   choose_rows<G, V>(p, 0, p.n, 0, s_int, s_dyn + p.E);
   place_rows(p, 0, p.n, 0, s_int, s_int + WARPS * p.E, s_int + (WARPS + 1) * p.E);
+  finish_losses(p);
 }
 
 struct RouteBwdParams {
@@ -449,11 +465,10 @@ __global__ void __launch_bounds__(THREADS) route_bwd_kernel(const RouteBwdParams
   const float nv = nv_i > 0 ? (float)nv_i : 1.f;
   const bool aux = p.balance != 0.f || p.zc != 0.f;
   float share[V];
+  const float each = p.balance * (float)p.E / nv / (nv * (float)p.k);
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    share[i] = p.balance != 0.f && c + i < p.E
-                   ? (float)((double)p.balance * p.E / ((double)nv * nv * p.k) * (p.offsets[c + i + 1] - p.offsets[c + i]))
-                   : 0.f;
+    share[i] = p.balance != 0.f && c + i < p.E ? each * (float)(p.offsets[c + i + 1] - p.offsets[c + i]) : 0.f;
   const int64_t step = (int64_t)gridDim.x * WARPS * ROWS;
   for (int64_t base = ((int64_t)blockIdx.x * WARPS + warp_id()) * ROWS; base < p.n; base += step) {
     const int64_t row = base + lane / G;
@@ -468,18 +483,28 @@ __global__ void __launch_bounds__(THREADS) route_bwd_kernel(const RouteBwdParams
     uint32_t chosen = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] = 0.f;
-    if (in)
-      for (int j = 0; j < p.k; ++j) {
-        const int id = p.ids[row * p.k + j];
-        const float d = p.weights_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.dweights)[row * p.k + j])
-                                       : reinterpret_cast<const float*>(p.dweights)[row * p.k + j];
+    for (int j0 = 0; j0 < p.k; j0 += G) {
+      // a choice a lane, then handed round the row's lanes
+      int id = -1;
+      float d = 0.f;
+      if (in && j0 + sub < p.k) {
+        const int64_t q = row * p.k + j0 + sub;
+        id = p.ids[q];
+        d = p.weights_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.dweights)[q])
+                           : reinterpret_cast<const float*>(p.dweights)[q];
+      }
+      const int left = min(G, p.k - j0);
+      for (int j = 0; j < left; ++j) {
+        const int at = __shfl_sync(0xffffffffu, id, lane - sub + j) - c;
+        const float dj = __shfl_sync(0xffffffffu, d, lane - sub + j);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (id == c + i) {
-            g[i] += d;
+          if (at == i) {
+            g[i] += dj;
             chosen |= 1u << i;
           }
       }
+    }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) m = fmaxf(m, v[i]);
@@ -546,7 +571,7 @@ __global__ void __launch_bounds__(THREADS) route_bwd_kernel(const RouteBwdParams
 }
 
 // blocks of rows of the two-launch form
-int route_blocks(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(256, (n + 63) / 64)); }
+int route_blocks(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(152, (n + 63) / 64)); }
 
 // Up to this many rows one block does it all in one launch.
 constexpr int64_t ONE_BLOCK_ROWS = 256;
@@ -568,7 +593,7 @@ int route_launch(const RouteParams& p, cudaStream_t st) {
       smem_limit_once(reinterpret_cast<const void*>(route_place_kernel), TOP, &a2))
     return BPT_ECUDA;
   if (launch_dependent(k, p.nblk, 1, dim3(THREADS), choose, st, p) != cudaSuccess) return BPT_ECUDA;
-  return launch_dependent(route_place_kernel, p.nblk, 1, dim3(THREADS), place, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
+  return launch_dependent(route_place_kernel, p.nblk + 1, 1, dim3(THREADS), place, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
 }
 
 // G lanes of V logits hold a row: 8 a lane (a 32- or 16-byte load) as long as
