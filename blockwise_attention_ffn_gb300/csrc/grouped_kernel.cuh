@@ -40,8 +40,13 @@ using gk::A_BYTES;
 using gk::BK;
 using gk::BM;
 using gk::NUM_EPI_WARPS;
-constexpr int COPY_WARP = 2 + NUM_EPI_WARPS;  // the first of the two that copy rows
-constexpr int COPY_WARPS = 2;
+constexpr int COPY_WARP = 2 + NUM_EPI_WARPS;  // the first of those that copy rows
+// TN reads the rows' places anew for every block, about 1190 cycles a stage
+// with two warps (8 experts of 4096 x 14336) where the products take 512
+template <int FORM>
+constexpr int copy_warps() {
+  return FORM == GROUPED_TN ? 4 : 2;
+}
 
 struct Params {
   CUtensorMap map_a[2];  // A tiles (TN: {64, 64} boxes)
@@ -181,8 +186,7 @@ __device__ __forceinline__ float fast_sigmoid(float z) {
 // W consecutive columns n .. of output row `row` (in the groups' order; TN:
 // of all the groups' matrices), the accumulators a (and b: the up product)
 template <int EPI, bool DUAL, int W>
-__device__ __forceinline__ void epi_cols(const Params& p, void* out, long long row, int n, const float (&a)[W], const float (&b)[W],
-                                         float w, float& dot) {
+__device__ __forceinline__ void epi_cols(const Params& p, void* out, long long row, int n, const float (&a)[W], const float (&b)[W]) {
   const long long i = row * p.N + n;
   if constexpr (EPI == GROUPED_STORE) {
     if (p.out_f32) {
@@ -218,36 +222,63 @@ __device__ __forceinline__ void epi_cols(const Params& p, void* out, long long r
       for (int j = 0; j < W; ++j) v[j] = gk::gelu_f(a[j], p.act);
     }
     gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(out) + i, v);
+  }  // GROUPED_ACT_BWD: act_bwd_cols
+}
+
+// The saved pair of W columns, as loaded
+template <int W>
+struct SavedPair {
+  uint32_t s0[W / 2], s1[W / 2];
+};
+template <int W>
+__device__ __forceinline__ void load_pair(const Params& p, long long i, SavedPair<W>& r) {
+  if constexpr (W == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p.aux + i), v = *reinterpret_cast<const uint4*>(p.aux2 + i);
+    r.s0[0] = u.x, r.s0[1] = u.y, r.s0[2] = u.z, r.s0[3] = u.w;
+    r.s1[0] = v.x, r.s1[1] = v.y, r.s1[2] = v.z, r.s1[3] = v.w;
   } else {
-    // The saved pair is bf16 (2^-9 of its size each): the activation and its
-    // slopes are taken again from it in fp32 and rounded once.
-    float s0[W], s1[W], v[W], aw[W];
-    gk::loadw_bf16<W>(p.aux + i, s0);
-    gk::loadw_bf16<W>(p.aux2 + i, s1);
-    if (p.act == BPT_ACT_SWIGLU) {
-      float dv[W];
 #pragma unroll
-      for (int j = 0; j < W; ++j) {
-        const float sg = fast_sigmoid(s0[j]);
-        const float si = s0[j] * sg;  // silu(g)
-        const float act = si * s1[j];
-        const float wa = w * a[j];
-        dot = fmaf(a[j], act, dot);
+    for (int h = 0; h < W / 16; ++h) {
+      gk::ld32B(p.aux + i + 16 * h, *reinterpret_cast<uint32_t(*)[8]>(&r.s0[8 * h]));
+      gk::ld32B(p.aux2 + i + 16 * h, *reinterpret_cast<uint32_t(*)[8]>(&r.s1[8 * h]));
+    }
+  }
+}
+// GROUPED_ACT_BWD of W columns at element i from their saved pair.  The pair is
+// bf16 (off by up to 2^-8 of its size): the activation and its slopes are taken
+// again from it in fp32 and rounded once.
+template <int W>
+__device__ __forceinline__ void act_bwd_cols(const Params& p, void* out, long long i, const uint32_t* acc, const SavedPair<W>& r, float w,
+                                             float& dot) {
+  constexpr int S = W < 16 ? W : 16;  // columns at a time
+#pragma unroll
+  for (int h = 0; h < W / S; ++h) {
+    float v[S], aw[S], dv[S];
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+      const int c = h * S + j;
+      const float a = __uint_as_float(acc[c]);
+      const float s0 = c & 1 ? bf16_hi(r.s0[c / 2]) : bf16_lo(r.s0[c / 2]);
+      const float s1 = c & 1 ? bf16_hi(r.s1[c / 2]) : bf16_lo(r.s1[c / 2]);
+      const float wa = w * a;
+      if (p.act == BPT_ACT_SWIGLU) {
+        const float sg = fast_sigmoid(s0);
+        const float si = s0 * sg;  // silu(g)
+        const float act = si * s1;
+        dot = fmaf(a, act, dot);
         aw[j] = w * act;
-        v[j] = wa * s1[j] * (sg + si * (1.f - sg));
+        v[j] = wa * s1 * (sg + si * (1.f - sg));
         dv[j] = wa * si;
-      }
-      gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(p.out2) + i, dv);
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        dot = fmaf(a[j], s0[j], dot);
-        aw[j] = w * s0[j];
-        v[j] = w * a[j] * s1[j];
+      } else {
+        dot = fmaf(a, s0, dot);
+        aw[j] = w * s0;
+        v[j] = wa * s1;
+        dv[j] = 0.f;
       }
     }
-    gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(out) + i, v);
-    gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(p.out3) + i, aw);
+    gk::storew_bf16<S>(reinterpret_cast<__nv_bfloat16*>(out) + i + h * S, v);
+    if (p.act == BPT_ACT_SWIGLU) gk::storew_bf16<S>(reinterpret_cast<__nv_bfloat16*>(p.out2) + i + h * S, dv);
+    gk::storew_bf16<S>(reinterpret_cast<__nv_bfloat16*>(p.out3) + i + h * S, aw);
   }
 }
 
@@ -275,7 +306,7 @@ constexpr bool copies() {  // whether the kernel has the copying warps
 }
 template <int FORM, bool AG>
 constexpr int threads() {
-  return 32 * (2 + NUM_EPI_WARPS + (copies<FORM, AG>() ? COPY_WARPS : 0));
+  return 32 * (2 + NUM_EPI_WARPS + (copies<FORM, AG>() ? copy_warps<FORM>() : 0));
 }
 
 template <int FORM, int EPI, int BN, bool AG, bool BG, bool DUAL, bool PAIR>
@@ -283,6 +314,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
   constexpr bool TN = FORM == GROUPED_TN;
   constexpr bool B_MN = FORM != GROUPED_NT;
   constexpr bool COPY = copies<FORM, AG>();
+  constexpr int COPY_WARPS = copy_warps<FORM>();
   constexpr int BNS = PAIR ? BN / 2 : BN;  // rows (columns) of each B this CTA stages
   constexpr int STAGE_BYTES = stage_bytes<BN, DUAL, PAIR>();
   constexpr int STAGES = ring_stages<STAGE_BYTES>();
@@ -461,16 +493,17 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
       const int nk = k_tiles(at);
       if constexpr (!TN) {
-        // lines w * 64 + 4 i + lane / 8 of the CTA's rows
-        const int r0 = at.m0 + (int)rank * BM + w * 64 + (lane >> 3);
-        int idx[16];
+        // lines w * PER + 4 i + lane / 8 of the CTA's rows
+        constexpr int PER = BM / COPY_WARPS;
+        const int r0 = at.m0 + (int)rank * BM + w * PER + (lane >> 3);
+        int idx[PER / 4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < PER / 4; ++i) {
           const int r = r0 + 4 * i;
           idx[i] = r >= at.cnt ? -2 : p.order ? row_of(at.lo + r) : at.lo + r;
         }
         const int live = (at.cnt - r0 + 3) / 4;  // lines of this lane with a row
-        const uint32_t line0 = (uint32_t)(w * 64 + (lane >> 3));
+        const uint32_t line0 = (uint32_t)(w * PER + (lane >> 3));
         for (int kt = 0; kt < nk; ++kt) {
           if (!claim()) {
             ok = false;
@@ -482,7 +515,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
           const __nv_bfloat16* src = p.a[seg] + (in ? x : 0);
           const uint32_t sa = smem_base + (it % STAGES) * STAGE_BYTES;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < PER / 4; ++i) {
             if (i < live) {
               const uint32_t line = line0 + 4 * i;
               copy16(sa + line * 128 + ((((lane & 7) ^ line) & 7) << 4), src + (long long)max(idx[i], 0) * p.a_cols, in && idx[i] >= 0);
@@ -491,30 +524,35 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
           next();
         }
       } else {
-        // rows w * 32 + 4 i + lane / 8 of a block, in every chunk of 64 columns
+        // rows w * PER + 4 i + lane / 8 of a block, in every chunk of 64 columns
+        constexpr int PER = BK / COPY_WARPS, LINES = PER / 4;
         const int ma = at.m0 + (int)rank * BM, nbs = at.n0 + (int)rank * BNS;
         constexpr int AHEAD = 4;  // blocks whose rows of the order are on their way
-        int ring[AG || BG ? AHEAD : 1][8];
-        auto fetch = [&](int kt, int (&v)[8]) {
+        int ring[AG || BG ? AHEAD : 1][LINES];
+        auto fetch = [&](int kt, int (&v)[LINES]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = kt * BK + w * 32 + 4 * i + (lane >> 3);
+          for (int i = 0; i < LINES; ++i) {
+            const int r = kt * BK + w * PER + 4 * i + (lane >> 3);
             v[i] = r < at.cnt ? p.order[at.lo + r] : -1;
           }
         };
-        auto lines = [&](uint32_t dst, const __nv_bfloat16* src, int cols, int x0, int chunks, const int (&rows)[8]) {
-          for (int c = 0; c < chunks; ++c) {
-            const int x = x0 + c * 64 + col;
-            const bool in = x < cols;
-            const __nv_bfloat16* from = src + (in ? x : 0);
+        const uint32_t line0 = (uint32_t)(w * PER + (lane >> 3));
+        auto lines = [&](uint32_t dst, const __nv_bfloat16* src, int cols, int x0, int chunks, const int (&rows)[LINES]) {
+          const __nv_bfloat16* from[LINES];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t line = (uint32_t)(w * 32 + 4 * i + (lane >> 3));
-              copy16(dst + c * 8192 + line * 128 + ((((lane & 7) ^ line) & 7) << 4), from + (long long)max(rows[i], 0) * cols,
-                     in && rows[i] >= 0);
+          for (int i = 0; i < LINES; ++i) from[i] = src + (long long)max(rows[i], 0) * cols + x0 + col;
+#pragma unroll
+          for (int c = 0; c < chunks; ++c) {
+            const bool in = x0 + c * 64 + col < cols;
+#pragma unroll
+            for (int i = 0; i < LINES; ++i) {
+              const uint32_t line = line0 + 4 * i;
+              const bool some = in && rows[i] >= 0;
+              copy16(dst + c * 8192 + line * 128 + ((((lane & 7) ^ line) & 7) << 4), some ? from[i] + c * 64 : src, some);
             }
           }
         };
+        constexpr int A_CHUNKS = 2, B_CHUNKS = BNS / 64;
         if constexpr (AG || BG) {
 #pragma unroll
           for (int u = 0; u < AHEAD; ++u) fetch(u, ring[u]);
@@ -532,25 +570,25 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
             const uint32_t sb = sa + A_BYTES;
             const bool whole = (kt + 1) * BK <= at.cnt;
             if constexpr (AG || BG) {
-              int rows[8];
+              int rows[LINES];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
+              for (int i = 0; i < LINES; ++i) {
                 const int q = ring[u][i];
                 rows[i] = q < 0 || q >= p.pairs ? -1 : (int)(((unsigned long long)(unsigned)q * p.by_k) >> 37);
               }
               fetch(kt + AHEAD, ring[u]);
-              if constexpr (AG) lines(sa, p.a[0], p.a_cols, ma, 2, rows);
-              else lines(sb, p.b, p.b_cols, nbs, BNS / 64, rows);
+              if constexpr (AG) lines(sa, p.a[0], p.a_cols, ma, A_CHUNKS, rows);
+              else lines(sb, p.b, p.b_cols, nbs, B_CHUNKS, rows);
             }
             if (!whole) {
-              int rows[8];
+              int rows[LINES];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = kt * BK + w * 32 + 4 * i + (lane >> 3);
+              for (int i = 0; i < LINES; ++i) {
+                const int r = kt * BK + w * PER + 4 * i + (lane >> 3);
                 rows[i] = r < at.cnt ? at.lo + r : -1;
               }
-              if constexpr (!AG) lines(sa, at.seg ? p.a[1] : p.a[0], p.a_cols, ma, 2, rows);
-              if constexpr (!BG) lines(sb, p.b, p.b_cols, nbs, BNS / 64, rows);
+              if constexpr (!AG) lines(sa, at.seg ? p.a[1] : p.a[0], p.a_cols, ma, A_CHUNKS, rows);
+              if constexpr (!BG) lines(sb, p.b, p.b_cols, nbs, B_CHUNKS, rows);
             }
             next();
           }
@@ -658,6 +696,27 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
       const bool none = k_tiles(at) == 0;
       const int acc = tc & 1;
+      const int m = at.m0 + (int)rank * BM + q * 32 + lane;
+      const bool mine = m < (TN ? p.M : at.cnt);
+      const long long row = TN ? (long long)at.e * p.M + m : (long long)at.lo + m;
+      void* out = TN && at.seg ? p.out2 : p.out;
+      float w = 0.f, dot = 0.f;
+      SavedPair<EPI == GROUPED_ACT_BWD ? 32 : 8> pair;
+      // the saved pair of a chunk of 32 columns is on its way while the chunk
+      // before is worked on, the first while the products are
+      auto fetch = [&](int c) {
+        const int nb = at.n0 + half * EPI_COLS + c * 32;
+        if (mine && p.vec32 && nb + 32 <= p.N) load_pair(p, row * p.N + nb, pair);
+      };
+      if constexpr (EPI == GROUPED_ACT_BWD) {
+        if (mine) {
+          const int q1 = p.order[row];
+          if (q1 >= 0 && q1 < p.pairs)
+            w = p.row_weight_f32 ? reinterpret_cast<const float*>(p.row_weight)[q1]
+                                 : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.row_weight)[q1]);
+        }
+        fetch(0);
+      }
       if (!none) {
         // the TMEM loads below are warp-collective, so the decision is too
         const bool ok = __all_sync(0xffffffffu, bounded_wait(&acc_full[acc], (tc >> 1) & 1, abort_flag, 105, p.err));
@@ -665,19 +724,6 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
         tc_fence_after();
       } else if (p.beta != 0.f) {
         continue;  // nothing to add
-      }
-      const int m = at.m0 + (int)rank * BM + q * 32 + lane;
-      const bool mine = m < (TN ? p.M : at.cnt);
-      const long long row = TN ? (long long)at.e * p.M + m : (long long)at.lo + m;
-      void* out = TN && at.seg ? p.out2 : p.out;
-      float w = 0.f, dot = 0.f;
-      if constexpr (EPI == GROUPED_ACT_BWD) {
-        if (mine) {
-          const int pair = p.order[row];
-          if (pair >= 0 && pair < p.pairs)
-            w = p.row_weight_f32 ? reinterpret_cast<const float*>(p.row_weight)[pair]
-                                 : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.row_weight)[pair]);
-        }
       }
       const uint32_t tbase = tmem + (uint32_t)(acc * ACC_COLS) + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
@@ -693,7 +739,21 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
 #pragma unroll
           for (int j = 0; j < 32; ++j) ra[j] = rb[j] = 0u;
         }
-        if (mine) {
+        if constexpr (EPI == GROUPED_ACT_BWD) {
+          if (nb + 32 <= p.N && p.vec32) {
+            const SavedPair<32> now = pair;
+            if (c + 1 < EPI_COLS / 32) fetch(c + 1);
+            if (mine) act_bwd_cols<32>(p, out, row * p.N + nb, ra, now, w, dot);
+          } else if (mine) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (nb + g * 8 < p.N) {  // N is a multiple of 8
+                SavedPair<8> now;
+                load_pair(p, row * p.N + nb + g * 8, now);
+                act_bwd_cols<8>(p, out, row * p.N + nb + g * 8, ra + g * 8, now, w, dot);
+              }
+          }
+        } else if (mine) {
           if (nb + 32 <= p.N && p.vec32) {
             float a32[32], b32[32];
 #pragma unroll
@@ -701,7 +761,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
               a32[j] = __uint_as_float(ra[j]);
               b32[j] = DUAL ? __uint_as_float(rb[j]) : 0.f;
             }
-            epi_cols<EPI, DUAL, 32>(p, out, row, nb, a32, b32, w, dot);
+            epi_cols<EPI, DUAL, 32>(p, out, row, nb, a32, b32);
           } else {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -712,7 +772,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
                   a8[j] = __uint_as_float(ra[g * 8 + j]);
                   b8[j] = DUAL ? __uint_as_float(rb[g * 8 + j]) : 0.f;
                 }
-                epi_cols<EPI, DUAL, 8>(p, out, row, nb + g * 8, a8, b8, w, dot);
+                epi_cols<EPI, DUAL, 8>(p, out, row, nb + g * 8, a8, b8);
               }
             }
           }
