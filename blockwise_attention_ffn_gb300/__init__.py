@@ -13,6 +13,7 @@ bpt_qk_norm_rope_fwd, bpt_qk_norm_rope_bwd, bpt_qk_norm_rope_workspace_bytes,
 bpt_clip_grads, bpt_clip_workspace_bytes,
 bpt_moe_route_fwd, bpt_moe_route_bwd, bpt_moe_route_workspace_bytes,
 bpt_moe_ffn_fwd, bpt_moe_ffn_bwd, bpt_moe_ffn_workspace_bytes, bpt_moe_saved_bytes, bpt_grouped_gemm,
+bpt_lm_distill_fwd, bpt_lm_distill_bwd, bpt_lm_distill_workspace_bytes, bpt_lm_distill_saved_bytes,
 bpt_workspace_bytes, bpt_saved_bytes, bpt_attention_bwd_workspace_bytes,
 bpt_status_string, bpt_last_device_error, bpt_check_device_range, bpt_watchdog_selftest,
 bpt_profile_enable, bpt_profile_collect, bpt_profile_list.  The layer stack
@@ -41,7 +42,8 @@ BPT_FLAG_DETERMINISTIC = 4
 BPT_FLAG_DEBUG_CHECKS = 8
 BPT_DTYPE_F32, BPT_DTYPE_BF16 = 0, 1
 BPT_GROUPED_NT, BPT_GROUPED_NN, BPT_GROUPED_TN = 0, 1, 2
-BPT_MOE_BAD_LOGIT_SITE, BPT_GROUPED_BAD_OFFSET_SITE = 951, 953
+BPT_TEACHER_LOGITS, BPT_TEACHER_LOGPROBS = 0, 1
+BPT_MOE_BAD_LOGIT_SITE, BPT_DISTILL_BAD_ENTRY_SITE, BPT_GROUPED_BAD_OFFSET_SITE = 951, 952, 953
 
 WEIGHT_FIELDS = ("ln1_w", "ln1_b", "wq", "bq", "wk", "bk", "wv", "bv", "wo", "bo",
                  "ln2_w", "ln2_b", "w1", "b1", "w2", "b2", "w3")
@@ -88,6 +90,11 @@ class BptMoeRoute(ctypes.Structure):
 
 class BptGroupedConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("rows", "n", "k", "groups", "form", "out_dtype", "flags")]
+
+
+class BptDistillConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n", "h", "vocab", "vocab_block", "top_k", "teacher", "grads_dtype")] + \
+        [("temperature", ctypes.c_float), ("flags", ctypes.c_int32)]
 
 
 class BptError(RuntimeError):
@@ -173,6 +180,15 @@ def lib() -> ctypes.CDLL:
         L.bpt_moe_ffn_bwd.restype = i32
         L.bpt_grouped_gemm.argtypes = [ctypes.POINTER(BptGroupedConfig), vp, vp, vp, vp, vp]
         L.bpt_grouped_gemm.restype = i32
+        kdp = ctypes.POINTER(BptDistillConfig)
+        L.bpt_lm_distill_saved_bytes.argtypes = [kdp]
+        L.bpt_lm_distill_saved_bytes.restype = sz
+        L.bpt_lm_distill_workspace_bytes.argtypes = [kdp, i32]
+        L.bpt_lm_distill_workspace_bytes.restype = sz
+        L.bpt_lm_distill_fwd.argtypes = [kdp] + [vp] * 8 + [sz, vp]
+        L.bpt_lm_distill_fwd.restype = i32
+        L.bpt_lm_distill_bwd.argtypes = [kdp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp, sz, vp]
+        L.bpt_lm_distill_bwd.restype = i32
         L.bpt_check_device_range.argtypes = [vp, sz]
         L.bpt_check_device_range.restype = i32
         L.bpt_watchdog_selftest.argtypes = [vp]
@@ -566,6 +582,48 @@ def bpt_grouped_gemm(cfg, a, b, offsets, out, stream=None) -> None:
         c, _want(where, "a", a, bf16, cfg.rows * cfg.k, dev), _want(where, "b", b, bf16, cfg.rows * cfg.n if tn else mats, dev),
         _want(where, "offsets", offsets, torch.int32, cfg.groups + 1, dev),
         _want(where, "out", out, _dtype(cfg.out_dtype), mats if tn else cfg.rows * cfg.n, dev), _stream(stream)), where)
+
+
+def make_distill_config(c) -> BptDistillConfig:
+    """BptDistillConfig from a DistillConfig (or any object with the same fields)."""
+    return BptDistillConfig(c.n, c.h, c.vocab, c.vocab_block, c.top_k, c.teacher, c.grads_dtype, c.temperature, c.flags)
+
+
+def bpt_lm_distill_saved_bytes(cfg) -> int:
+    return int(lib().bpt_lm_distill_saved_bytes(make_distill_config(cfg)))
+
+
+def bpt_lm_distill_workspace_bytes(cfg, pass_: int) -> int:
+    return int(lib().bpt_lm_distill_workspace_bytes(make_distill_config(cfg), int(pass_)))
+
+
+def bpt_lm_distill_fwd(cfg, x, w, ids, values, row_weight, loss, saved, ws, stream=None) -> None:
+    """Divergence of the student's softmax(x w^T / T) from a teacher's stored
+    entries ids, values [n, k], into loss (one fp32).  x [n, h], w [V, h];
+    row_weight [n] fp32 or None (1 / n each); saved: for the backward."""
+    import torch
+    where, dev, bf16, f32 = "bpt_lm_distill_fwd", torch.cuda.current_device(), torch.bfloat16, torch.float32
+    c = make_distill_config(cfg)
+    _check(lib().bpt_lm_distill_fwd(
+        c, _want(where, "x", x, bf16, cfg.n * cfg.h, dev), _want(where, "w", w, bf16, cfg.vocab * cfg.h, dev),
+        _want(where, "ids", ids, torch.int32, cfg.n * cfg.top_k, dev), _want(where, "values", values, f32, cfg.n * cfg.top_k, dev),
+        _may(where, "row_weight", row_weight, f32, cfg.n, dev), _want(where, "loss", loss, f32, 1, dev),
+        _want(where, "saved", saved, torch.uint8, bpt_lm_distill_saved_bytes(cfg), dev),
+        _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(), _stream(stream)), where)
+
+
+def bpt_lm_distill_bwd(cfg, x, w, row_weight, saved, dloss, dx, dw, ws, stream=None) -> None:
+    """Gradients of dloss * loss: dx [n, h] bf16 and dw [V, h]
+    (cfg.grads_dtype), from what the forward saved."""
+    import torch
+    where, dev, bf16 = "bpt_lm_distill_bwd", torch.cuda.current_device(), torch.bfloat16
+    c = make_distill_config(cfg)
+    _check(lib().bpt_lm_distill_bwd(
+        c, _want(where, "x", x, bf16, cfg.n * cfg.h, dev), _want(where, "w", w, bf16, cfg.vocab * cfg.h, dev),
+        _may(where, "row_weight", row_weight, torch.float32, cfg.n, dev),
+        _want(where, "saved", saved, torch.uint8, bpt_lm_distill_saved_bytes(cfg), dev), float(dloss),
+        _want(where, "dx", dx, bf16, cfg.n * cfg.h, dev), _want(where, "dw", dw, _dtype(cfg.grads_dtype), cfg.vocab * cfg.h, dev),
+        _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(), _stream(stream)), where)
 
 
 BPT_LM_BAD_TARGET_SITE = 950

@@ -85,6 +85,13 @@ struct GemmParams {
   const int* rowi;     // loss epilogues: per-row target id
   float scale;
   long long col0;      // vocabulary id of column 0
+  // the distillation loss's epilogues (internal.h): entries of each row in
+  // rising order of id, the first one of each 128 columns, and the rows' mass
+  const int* ent_id;
+  const unsigned char* ent_at;
+  int ent_k;
+  float inv_t;
+  const float *rowp, *roww;
   unsigned int* err;
 };
 
@@ -493,12 +500,110 @@ inline int pair_slots(const void* kernel, int smem, std::atomic<int>* fit) {
   return n;
 }
 
+// The distillation loss's epilogues (a set of kernels of their own, so that
+// they cost the others no registers), with logits z = acc / T:
+//   EPI_KD_LSE   the pair (max z, sum exp(z - max)) of EPI_LSE, and z at the
+//                row's entries among these columns -> out2[m, entry].  The
+//                entries are sorted, so each chunk of 32 columns takes the next
+//                ones; a lane's entry is picked out of its registers by 32
+//                selections, all lanes of the warp at once.
+//   EPI_KD_GRAD  out = exp(z - rowf[m]) * rowp[m] * roww[m] * scale -> bf16
+template <int EPI_COLS>
+__device__ __forceinline__ void distill_tile(const GemmParams& p, uint32_t tbase, int m, int n0, int half) {
+  const float c2 = p.inv_t * 1.4426950408889634f;
+  if (p.epi == EPI_KD_LSE) {
+    float mx = -INFINITY, sm = 0.f;  // mx of the accumulators
+    const long long part = (long long)(n0 / EPI_COLS) + half;
+    int j = 0, je = 0;
+    if (m < p.M) {
+      j = p.ent_at[part * p.ldo + m];
+      je = p.ent_at[(part + 1) * p.ldo + m];
+    }
+    const int* ids = p.ent_id + (long long)m * p.ent_k;
+    int id = j < je ? ids[j] : 0x7fffffff;
+#pragma unroll 1
+    for (int c = 0; c < EPI_COLS / 32; ++c) {
+      const int col = half * EPI_COLS + c * 32;
+      const int nb = n0 + col;
+      uint32_t ra[32];
+      tmem_ld32(tbase + col, ra);
+      float cm = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (nb + i < p.N) cm = fmaxf(cm, __uint_as_float(ra[i]));
+      if (cm > -INFINITY) {
+        const float nm = fmaxf(mx, cm);
+        const float nl2 = nm * c2;
+        float e, sum = 0.f;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(mx, c2, -nl2)));
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float x;
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(fmaf(__uint_as_float(ra[i]), c2, -nl2)));
+          sum += nb + i < p.N ? x : 0.f;
+        }
+        sm = fmaf(sm, e, sum);
+        mx = nm;
+      }
+      while (__any_sync(0xffffffffu, id < nb + 32)) {
+        if (id < nb + 32) {
+          float z = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (id - nb == i) z = __uint_as_float(ra[i]);
+          reinterpret_cast<float*>(p.out2)[(long long)m * p.ent_k + j] = z * p.inv_t;
+          ++j;
+          id = j < je ? ids[j] : 0x7fffffff;
+        }
+        __syncwarp();
+      }
+    }
+    if (m < p.M) reinterpret_cast<float2*>(p.out)[part * p.ldo + m] = make_float2(mx * p.inv_t, sm);
+    return;
+  }
+  float l2 = 0.f, w = 0.f;
+  if (m < p.M) {
+    l2 = p.rowf[m] * 1.4426950408889634f;
+    w = p.rowp[m] * p.scale;
+    if (p.roww) w *= p.roww[m];
+  }
+#pragma unroll 1
+  for (int c = 0; c < EPI_COLS / 32; ++c) {
+    const int col = half * EPI_COLS + c * 32;
+    const int nb = n0 + col;
+    uint32_t ra[32];
+    tmem_ld32(tbase + col, ra);
+    if (m < p.M && nb < p.N) {
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(__uint_as_float(ra[i]), c2, -l2)));
+        v[i] = w != 0.f ? e * w : 0.f;  // a row without weight gives nothing, whatever its logits are
+      }
+      __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + (long long)m * p.ldo + nb;
+      if (nb + 32 <= p.N && p.vec32) {
+        storew_bf16<32>(o, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (nb + i < p.N) o[i] = __float2bfloat16(v[i]);
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // The epilogue of one accumulator for one warp: this thread's row m of the
 // tile starting at column n0, the half `half` of its BN columns, read from
 // TMEM at tbase (the warp's lane quarter, the accumulator's first column).
-template <int BN, bool DUAL>
+template <int BN, bool DUAL, int SET>
 __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tbase, int m, int n0, int half) {
   constexpr int EPI_COLS = BN / 2;  // columns of one accumulator half per epilogue warp
+  if constexpr (SET == 1) {
+    distill_tile<EPI_COLS>(p, tbase, m, n0, half);
+    return;
+  }
   if (!DUAL && p.epi == EPI_LSE) {
     // this thread's row over its half of the tile: online max and sum of
     // exp over the valid columns, 32 at a time, and the target's logit
@@ -589,7 +694,8 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tbas
 // Persistent: each CTA (or pair) walks work units u0, u0 + units in flight,
 // ... with two TMEM accumulators, so the epilogue of one tile overlaps the
 // main loop of the next.
-template <int BN, bool A_MN, bool B_MN, bool DUAL, bool PAIR>
+// SET: 0 the layer's and the loss's epilogues, 1 the distillation loss's.
+template <int BN, bool A_MN, bool B_MN, bool DUAL, bool PAIR, int SET = 0>
 __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int STAGES = stages<PAIR>();
   constexpr int BNS = PAIR ? BN / 2 : BN;  // rows of each B this CTA stages
@@ -801,7 +907,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       int m0, n0;
       tile_origin(p, unit, TM, BN, m0, n0);
       const uint32_t tbase = tmem + (uint32_t)(acc * ACC_COLS) + ((uint32_t)(q * 32) << 16);
-      epilogue_tile<BN, DUAL>(p, tbase, m0 + row, n0, half);
+      epilogue_tile<BN, DUAL, SET>(p, tbase, m0 + row, n0, half);
       // this warp's part of the accumulator has been read: hand it back
       tc_fence_before();
       __syncwarp();
@@ -826,13 +932,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
 }
 
 // Units in flight (CTAs, or pairs) and the L2-aware walk, then the launch.
-template <int BN, bool A_MN, bool B_MN, bool DUAL, bool PAIR>
+template <int BN, bool A_MN, bool B_MN, bool DUAL, bool PAIR, int SET = 0>
 int launch(GemmParams& p, cudaStream_t st) {
   constexpr int BNS = PAIR ? BN / 2 : BN;
   constexpr int B_BYTES = (DUAL ? 2 : 1) * BNS * BK * 2;
   constexpr int SMEM = stages<PAIR>() * (A_BYTES + B_BYTES) + 1024 + 256;
   constexpr int TM = PAIR ? 2 * BM : BM;
-  auto kern = gemm_kernel<BN, A_MN, B_MN, DUAL, PAIR>;
+  auto kern = gemm_kernel<BN, A_MN, B_MN, DUAL, PAIR, SET>;
   static std::atomic<uint64_t> attr{0};  // per instantiation: devices whose limit is set
   if (smem_limit_once(reinterpret_cast<const void*>(kern), SMEM, &attr)) return 3;
   int slots;
@@ -899,6 +1005,8 @@ int launch(GemmParams& p, cudaStream_t st) {
 // threads; 0 when the device cannot hold one, and then gemm() takes the
 // one-SM form).
 int launch_pair(GemmParams& p, bool a_mn, bool b_mn, bool dual, cudaStream_t st);
+// the launches with the distillation loss's epilogues (gemm_distill.cu)
+int launch_distill(GemmParams& p, bool pair, cudaStream_t st);
 int pair_units();
 
 }  // namespace gk

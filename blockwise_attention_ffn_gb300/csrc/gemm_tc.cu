@@ -75,6 +75,12 @@ int gemm(int64_t M, int64_t N, int64_t K, const MatView& A, bool a_mn, const Mat
   p.rowi = e.rowi;
   p.scale = e.scale;
   p.col0 = e.col0;
+  p.ent_id = e.ent_id;
+  p.ent_at = e.ent_at;
+  p.ent_k = e.ent_k;
+  p.inv_t = e.inv_t;
+  p.rowp = e.rowp;
+  p.roww = e.roww;
   p.err = device_error_word();
   if (!p.err) return 3;
   {
@@ -109,6 +115,10 @@ int gemm(int64_t M, int64_t N, int64_t K, const MatView& A, bool a_mn, const Mat
     if (p.ksplit > 1 && e.beta == 0.f) {
       if (cudaMemset2DAsync(e.out, (size_t)e.ldo * 4, 0, (size_t)N * 4, (size_t)M, stream) != cudaSuccess) return 3;
     }
+  }
+  if (e.kind == EPI_KD_LSE || e.kind == EPI_KD_GRAD) {
+    if (a_mn || b_mn || dual || nseg != 1) return 1;
+    return launch_distill(p, pair, stream);
   }
   if (pair) return launch_pair(p, a_mn, b_mn, dual, stream);
   if (dual) return launch<128, false, false, true, false>(p, stream);

@@ -129,6 +129,11 @@ enum EpiKind {
                        // wide, so part = column / 128); z of the row's target
                        // rowi[m] (if in this tile) -> float out2[m]
   EPI_CE_GRAD = 7,     // out = (exp(z - rowf[m]) - [col0 + n == rowi[m]]) * scale -> bf16
+  // distillation loss, z = acc * inv_t:
+  EPI_KD_LSE = 8,      // EPI_LSE's pairs -> float2 out[part * ldo + m]; z at row m's
+                       // entry j (column ent_id[m, j], sorted; the first entry at or
+                       // past column 128 q is ent_at[q * ldo + m]) -> float out2[m, j]
+  EPI_KD_GRAD = 9,     // out = exp(z - rowf[m]) * rowp[m] (* roww[m]) * scale -> bf16
 };
 
 struct Epilogue {
@@ -158,6 +163,12 @@ struct Epilogue {
   const int* rowi = nullptr;
   float scale = 1.f;
   int64_t col0 = 0;
+  // the distillation loss's entries and row factors
+  const int* ent_id = nullptr;
+  const unsigned char* ent_at = nullptr;
+  int ent_k = 0;
+  float inv_t = 1.f;
+  const float *rowp = nullptr, *roww = nullptr;
 };
 
 // Returns 0 or a BPT_* status.

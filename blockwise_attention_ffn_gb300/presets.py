@@ -115,3 +115,22 @@ class GroupedConfig:
 
     def with_(self, **kw) -> "GroupedConfig":
         return replace(self, **kw)
+
+
+@dataclass(frozen=True)
+class DistillConfig:
+    """Distillation from a teacher's top_k stored logits (teacher 0) or
+    log-probabilities (1) of each of n positions."""
+    n: int
+    h: int
+    vocab: int
+    top_k: int
+    temperature: float = 1.0
+    teacher: int = 0
+    vocab_block: int = 0
+    grads_dtype: int = 0    # 0 fp32, 1 bf16
+    flags: int = 0
+    name: str = ""
+
+    def with_(self, **kw) -> "DistillConfig":
+        return replace(self, **kw)

@@ -595,6 +595,57 @@ typedef struct {
 int bpt_grouped_gemm(const bpt_grouped_config* cfg, const void* a, const void* b, const int32_t* offsets, void* out,
                      void* stream);
 
+/* ------------------------------------------------------------------------
+ * Distillation from a teacher's stored top logits, through the vocabulary
+ * projection of the language-model loss (whose blockwise schedule it shares).
+ *   z = x W^T / T,  q = softmax(z) over the vocabulary
+ *   loss = T^2 sum_i c_i sum_j p_ij (log p_ij - log q_i,ids[i,j])
+ * the divergence of the teacher's p over its stored entries from the student,
+ * with T^2 so that its gradient keeps its size as T grows, and c_i =
+ * row_weight[i], or 1 / n without row weights.
+ *
+ *   n, h, vocab, vocab_block   as for bpt_lm_config
+ *   top_k        k in 1 .. 128: entries stored of each row
+ *   teacher      BPT_TEACHER_LOGITS: values are the teacher's logits, p their
+ *                softmax at T over the row's entries;
+ *                BPT_TEACHER_LOGPROBS: values are log-probabilities, p = exp(value)
+ *                as stored (at the temperature they are stored for); the mass
+ *                outside the entries is left out
+ *   temperature  T in [2^-10, 2^10]
+ *   grads_dtype  BPT_DTYPE_* of dw
+ *   flags        BPT_FLAG_ACCUM_GRADS (dw += ; fp32 only),
+ *                BPT_FLAG_DETERMINISTIC, BPT_FLAG_DEBUG_CHECKS
+ *   ids          [n, k] int32, in any order; below 0: no entry (a row may have
+ *                none: it gives no loss and no gradient).  An id that appears
+ *                twice counts with both its values.  An id of vocab or more, a
+ *                NaN or +inf value is no entry and is recorded in the device
+ *                error word (BPT_EINVAL, BPT_DISTILL_BAD_ENTRY_SITE)
+ *   values       [n, k] fp32; -inf: probability 0
+ *   row_weight   [n] fp32 or NULL: 1 / n each.  A row of weight 0 (padding)
+ *                leaves no trace, whatever finite values its x holds
+ *   loss         one fp32 (device)
+ *   saved        bpt_lm_distill_saved_bytes(cfg): what the backward takes back
+ *   dx           [n, h] bf16;  dw [V, h]
+ *   ws           bpt_lm_distill_workspace_bytes(cfg, pass), one per call in flight
+ * The backward gives the gradients of dloss * loss; row_weight as in the
+ * forward.  Its gradient of the logits is rounded to bf16 (the products'
+ * operand), each value once; sums are fp32, the loss's fp64.  Outputs, saved
+ * and ws that share bytes with an input or one another are refused
+ * (BPT_EINVAL). */
+enum { BPT_TEACHER_LOGITS = 0, BPT_TEACHER_LOGPROBS = 1 };
+#define BPT_DISTILL_BAD_ENTRY_SITE 952
+typedef struct {
+  int32_t n, h, vocab, vocab_block, top_k, teacher, grads_dtype;
+  float temperature;
+  int32_t flags;
+} bpt_distill_config;
+size_t bpt_lm_distill_saved_bytes(const bpt_distill_config* cfg);
+size_t bpt_lm_distill_workspace_bytes(const bpt_distill_config* cfg, int pass);
+int bpt_lm_distill_fwd(const bpt_distill_config* cfg, const void* x, const void* w, const int32_t* ids, const float* values,
+                       const float* row_weight, float* loss, void* saved, void* ws, size_t ws_bytes, void* stream);
+int bpt_lm_distill_bwd(const bpt_distill_config* cfg, const void* x, const void* w, const float* row_weight,
+                       const void* saved, float dloss, void* dx, void* dw, void* ws, size_t ws_bytes, void* stream);
+
 /* Opt-in launch profiler.  bpt_profile_enable(1) makes every later launch
  * of this process record a pair of CUDA events on its stream, tagged with
  * the launch's kind and its algorithmic work (FLOPs for tensor-core kernels,
