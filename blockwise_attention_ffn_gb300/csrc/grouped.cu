@@ -49,10 +49,6 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   p.part = op.part;
   p.err = device_error_word();
   if (!p.err) return 3;
-  const int out_elem = op.epi == GROUPED_STORE && op.out_f32 ? 4 : 2;
-  auto ok32 = [&](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 31) == 0; };
-  p.vec32 = (op.N * out_elem) % 32 == 0 && (op.N * 2) % 32 == 0 && ok32(op.out) && ok32(op.out2) && ok32(op.out3) && ok32(op.aux) &&
-            ok32(op.aux2);
   int64_t units, mt_all;
   const int64_t some = std::min<int64_t>(op.groups, op.rows);  // groups that can hold a row
   int rc = 0;

@@ -13,10 +13,11 @@ namespace bpt {
 enum GroupedForm { GROUPED_NT = 0, GROUPED_NN = 1, GROUPED_TN = 2 };
 enum GroupedEpi {
   GROUPED_STORE = 0,    // out = acc (+ beta out), bf16 or fp32
-  GROUPED_ACT = 1,      // out = act(acc); out2, out3 (optional) = what the backward takes:
-                        // SwiGLU (w2 given): the gate and up products; GeLU: out2 = gelu'
-  GROUPED_ACT_BWD = 2,  // acc = dy W2 of a row (unweighted), w its routing weight, from the saved pair:
-                        // SwiGLU: out = w acc dact/dg, out2 = w acc dact/du; GeLU: out = w acc gelu';
+  GROUPED_ACT = 1,      // out = act(acc); out2, out3 (optional): what the backward takes, in
+                        // a layout of these kernels' own (grouped_kernel.cuh): SwiGLU (w2
+                        // given) the gate and the up product, GeLU the product (out2 alone)
+  GROUPED_ACT_BWD = 2,  // acc = dy W2 of a row (unweighted), w its routing weight, aux and aux2
+                        // as kept: out = w acc dact/dg, out2 = w acc dact/du (SwiGLU),
                         // out3 = w act; part[2 * tile column + half][row] = sum of acc * act
 };
 

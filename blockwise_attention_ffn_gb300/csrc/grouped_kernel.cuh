@@ -71,7 +71,6 @@ struct Params {
   const void* row_weight;
   int row_weight_f32;
   float* part;
-  int vec32;
   unsigned int* err;
 };
 
@@ -183,106 +182,90 @@ __device__ __forceinline__ float fast_sigmoid(float z) {
   return r;
 }
 
-// W consecutive columns n .. of output row `row` (in the groups' order; TN:
-// of all the groups' matrices), the accumulators a (and b: the up product)
-template <int EPI, bool DUAL, int W>
-__device__ __forceinline__ void epi_cols(const Params& p, void* out, long long row, int n, const float (&a)[W], const float (&b)[W]) {
-  const long long i = row * p.N + n;
-  if constexpr (EPI == GROUPED_STORE) {
-    if (p.out_f32) {
-      float* o = reinterpret_cast<float*>(out) + i;
-      float v[W];
-      if (p.beta != 0.f) {
-        gk::loadw_f32<W>(o, v);
-#pragma unroll
-        for (int j = 0; j < W; ++j) v[j] = fmaf(p.beta, v[j], a[j]);
-        gk::storew_f32<W>(o, v);
-      } else {
-        gk::storew_f32<W>(o, a);
-      }
-    } else {
-      gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(out) + i, a);
-    }
-  } else if constexpr (EPI == GROUPED_ACT) {
-    float v[W];
-    if constexpr (DUAL) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) v[j] = a[j] * fast_sigmoid(a[j]) * b[j];
-      if (p.out2) {
-        gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(p.out2) + i, a);
-        gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(p.out3) + i, b);
-      }
-    } else if (p.out2) {
-      float d[W];
-#pragma unroll
-      for (int j = 0; j < W; ++j) gk::gelu_and_grad_f(a[j], p.act, v[j], d[j]);
-      gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(p.out2) + i, d);
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; ++j) v[j] = gk::gelu_f(a[j], p.act);
-    }
-    gk::storew_bf16<W>(reinterpret_cast<__nv_bfloat16*>(out) + i, v);
-  }  // GROUPED_ACT_BWD: act_bwd_cols
-}
-
-// The saved pair of W columns, as loaded
-template <int W>
-struct SavedPair {
-  uint32_t s0[W / 2], s1[W / 2];
-};
-template <int W>
-__device__ __forceinline__ void load_pair(const Params& p, long long i, SavedPair<W>& r) {
-  if constexpr (W == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p.aux + i), v = *reinterpret_cast<const uint4*>(p.aux2 + i);
-    r.s0[0] = u.x, r.s0[1] = u.y, r.s0[2] = u.z, r.s0[3] = u.w;
-    r.s1[0] = v.x, r.s1[1] = v.y, r.s1[2] = v.z, r.s1[3] = v.w;
+// GeLU and its slope: z cdf(z), cdf + z pdf(z), or the tanh form as z s with
+// s = sigmoid(2 c (z + 0.044715 z^3)), c = sqrt(2 / pi).
+__device__ __forceinline__ void fast_gelu(float z, int act, float& g, float& d) {
+  if (act == BPT_ACT_GELU_ERF) {
+    gk::gelu_and_grad_f(z, 0, g, d);
   } else {
-#pragma unroll
-    for (int h = 0; h < W / 16; ++h) {
-      gk::ld32B(p.aux + i + 16 * h, *reinterpret_cast<uint32_t(*)[8]>(&r.s0[8 * h]));
-      gk::ld32B(p.aux2 + i + 16 * h, *reinterpret_cast<uint32_t(*)[8]>(&r.s1[8 * h]));
-    }
-  }
-}
-// GROUPED_ACT_BWD of W columns at element i from their saved pair.  The pair is
-// bf16 (off by up to 2^-8 of its size): the activation and its slopes are taken
-// again from it in fp32 and rounded once.
-template <int W>
-__device__ __forceinline__ void act_bwd_cols(const Params& p, void* out, long long i, const uint32_t* acc, const SavedPair<W>& r, float w,
-                                             float& dot) {
-  constexpr int S = W < 16 ? W : 16;  // columns at a time
-#pragma unroll
-  for (int h = 0; h < W / S; ++h) {
-    float v[S], aw[S], dv[S];
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-      const int c = h * S + j;
-      const float a = __uint_as_float(acc[c]);
-      const float s0 = c & 1 ? bf16_hi(r.s0[c / 2]) : bf16_lo(r.s0[c / 2]);
-      const float s1 = c & 1 ? bf16_hi(r.s1[c / 2]) : bf16_lo(r.s1[c / 2]);
-      const float wa = w * a;
-      if (p.act == BPT_ACT_SWIGLU) {
-        const float sg = fast_sigmoid(s0);
-        const float si = s0 * sg;  // silu(g)
-        const float act = si * s1;
-        dot = fmaf(a, act, dot);
-        aw[j] = w * act;
-        v[j] = wa * s1 * (sg + si * (1.f - sg));
-        dv[j] = wa * si;
-      } else {
-        dot = fmaf(a, s0, dot);
-        aw[j] = w * s0;
-        v[j] = wa * s1;
-        dv[j] = 0.f;
-      }
-    }
-    gk::storew_bf16<S>(reinterpret_cast<__nv_bfloat16*>(out) + i + h * S, v);
-    if (p.act == BPT_ACT_SWIGLU) gk::storew_bf16<S>(reinterpret_cast<__nv_bfloat16*>(p.out2) + i + h * S, dv);
-    gk::storew_bf16<S>(reinterpret_cast<__nv_bfloat16*>(p.out3) + i + h * S, aw);
+    const float c2 = 1.5957691216057308f, z2 = z * z;
+    const float s = fast_sigmoid(c2 * z * fmaf(0.044715f, z2, 1.f));
+    g = z * s;
+    d = fmaf(g * (1.f - s), c2 * fmaf(3.f * 0.044715f, z2, 1.f), s);
   }
 }
 
-// ring stages that fit beside the group lists
+// A warp's 32 output rows, one a lane in registers, to global memory by whole
+// 64- or 128-byte pieces of a row, through the warp's 2 KB of shared memory.
+// (Stored straight from the registers, 32 bytes of 32 rows at a time, the
+// stores took as long as the products of 1024 rows: without them the
+// weight gradients of 8 experts of 4096 x 14336 ran at 1680 TFLOP/s, with them
+// at 1330.)  P 16-byte words a row: 4, all rows at once, or 8, 16 rows at a
+// time.  The words' places are swapped so that neither the rows' writes nor
+// the lines' reads meet in a bank.  to: the first row's first byte; ld: bytes
+// from row to row; rows, words: how many of them there are.
+template <int P, bool ADD>
+__device__ __forceinline__ void put_rows(const uint32_t* v, uint4* stage, char* to, long long ld, int rows, int words, float beta) {
+  const int lane = lane_id();
+  constexpr int STEPS = P == 8 ? 2 : 1, AT_ONCE = 32 / P;  // rows a store covers
+#pragma unroll
+  for (int h = 0; h < STEPS; ++h) {
+    if (STEPS == 1 || (lane >> 4) == h) {
+      const int r = STEPS == 1 ? lane : lane & 15;
+      const int mix = P == 8 ? r & 7 : (r >> 1) & 3;
+#pragma unroll
+      for (int j = 0; j < P; ++j) stage[r * P + (j ^ mix)] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int r = t * AT_ONCE + lane / P, j = lane % P;
+      const int mix = P == 8 ? r & 7 : (r >> 1) & 3;
+      uint4 w = stage[r * P + (j ^ mix)];
+      const int row = h * 16 + r;
+      if (row < rows && j < words) {
+        uint4* o = reinterpret_cast<uint4*>(to + row * ld) + j;
+        if constexpr (ADD) {
+          const float4 old = *reinterpret_cast<const float4*>(o);
+          w.x = __float_as_uint(fmaf(beta, old.x, __uint_as_float(w.x)));
+          w.y = __float_as_uint(fmaf(beta, old.y, __uint_as_float(w.y)));
+          w.z = __float_as_uint(fmaf(beta, old.z, __uint_as_float(w.z)));
+          w.w = __float_as_uint(fmaf(beta, old.w, __uint_as_float(w.w)));
+        }
+        *o = w;
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// What the forward leaves for the backward (SwiGLU: the gate and the up
+// product; GeLU: the product) is read by these kernels alone, so it lies as a
+// warp holds it: blocks of 32 rows of a group (the last one of fewer), in them
+// chunks of 32 columns, in them the 16-byte words of 8 columns, each for all
+// rows of the block.  A warp's words are then whole lines.  Element of word 0
+// of chunk c for the row at `lane` of the block of `rows` rows that begins
+// `first` rows into the order; a word further is 8 * rows.
+__device__ __forceinline__ long long kept_at(const Params& p, long long first, int rows, int c, int lane) {
+  return first * p.N + ((long long)c * 4 * rows + lane) * 8;
+}
+__device__ __forceinline__ void keep(void* t, long long at, int rows, int words, const uint32_t* v) {
+  uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(t) + at);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < words) o[j * rows] = make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+}
+__device__ __forceinline__ void kept(const __nv_bfloat16* t, long long at, int rows, int words, uint32_t* v) {
+  const uint4* o = reinterpret_cast<const uint4*>(t + at);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 u = j < words ? __ldg(o + j * rows) : make_uint4(0, 0, 0, 0);
+    v[4 * j] = u.x, v[4 * j + 1] = u.y, v[4 * j + 2] = u.z, v[4 * j + 3] = u.w;
+  }
+}
+
+constexpr int PUT_BYTES = 2048;  // shared memory of put_rows, a warp
+// ring stages that fit beside that and the group lists
 template <int STAGE_BYTES>
 constexpr int ring_stages() {
   return 200 * 1024 / STAGE_BYTES > 8 ? 8 : 200 * 1024 / STAGE_BYTES;
@@ -293,7 +276,7 @@ constexpr int stage_bytes() {
 }
 template <int BN, bool DUAL, bool PAIR>
 constexpr int smem_bytes() {
-  return ring_stages<stage_bytes<BN, DUAL, PAIR>()>() * stage_bytes<BN, DUAL, PAIR>() + 1024 + 256 +
+  return ring_stages<stage_bytes<BN, DUAL, PAIR>()>() * stage_bytes<BN, DUAL, PAIR>() + NUM_EPI_WARPS * PUT_BYTES + 1024 + 256 +
          (3 * GROUPED_MAX_GROUPS + 4) * 4;
 }
 
@@ -327,7 +310,8 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES);
+  uint8_t* put = smem + STAGES * STAGE_BYTES;  // the epilogue warps'
+  uint64_t* full = reinterpret_cast<uint64_t*>(put + NUM_EPI_WARPS * PUT_BYTES);
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;  // [2]
   uint64_t* acc_empty = acc_full + 2;   // [2]
@@ -335,7 +319,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
   uint64_t* copied = drain + 1;  // [STAGES], this CTA's copying warps
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(copied + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  int* s_unit = reinterpret_cast<int*>(smem + STAGES * STAGE_BYTES + 256);  // [groups + 1]
+  int* s_unit = reinterpret_cast<int*>(put + NUM_EPI_WARPS * PUT_BYTES + 256);  // [groups + 1]
   int* s_lo = s_unit + GROUPED_MAX_GROUPS + 4;
   int* s_cnt = s_lo + GROUPED_MAX_GROUPS;
   static_assert((3 * STAGES + 5) * 8 + 8 <= 256, "barriers");
@@ -684,11 +668,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
   } else if (warp < COPY_WARP) {
     // -------------------------------------------------- epilogue (warps 2..9)
     constexpr int EPI_COLS = BN / 2;
-    constexpr int CH = EPI_COLS < 32 ? EPI_COLS : 32;
-    static_assert(CH == 32, "32 columns a chunk");
     const int q = warp & 3;
     const int half = (warp - 2) >> 2;
     const uint32_t acc_empty0 = PAIR ? cluster_addr(smem_u32(acc_empty), 0) : 0u;
+    uint4* stage = reinterpret_cast<uint4*>(put + (warp - 2) * PUT_BYTES);
     int tc = 0;
     Place at;
     at.e = 0;
@@ -696,21 +679,26 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
       const bool none = k_tiles(at) == 0;
       const int acc = tc & 1;
-      const int m = at.m0 + (int)rank * BM + q * 32 + lane;
-      const bool mine = m < (TN ? p.M : at.cnt);
-      const long long row = TN ? (long long)at.e * p.M + m : (long long)at.lo + m;
+      const int m0 = at.m0 + (int)rank * BM + q * 32;  // the warp's first row in the group (TN: of the matrix)
+      const int rows = max(0, min(32, (TN ? p.M : at.cnt) - m0));
+      const long long first = TN ? (long long)at.e * p.M + m0 : (long long)at.lo + m0;
       void* out = TN && at.seg ? p.out2 : p.out;
+      const bool mine = lane < rows;
+      const int n0 = at.n0 + half * EPI_COLS;  // the warp's first column
       float w = 0.f, dot = 0.f;
-      SavedPair<EPI == GROUPED_ACT_BWD ? 32 : 8> pair;
-      // the saved pair of a chunk of 32 columns is on its way while the chunk
-      // before is worked on, the first while the products are
+      uint32_t s0[EPI == GROUPED_ACT_BWD ? 16 : 1], s1[EPI == GROUPED_ACT_BWD ? 16 : 1];
       auto fetch = [&](int c) {
-        const int nb = at.n0 + half * EPI_COLS + c * 32;
-        if (mine && p.vec32 && nb + 32 <= p.N) load_pair(p, row * p.N + nb, pair);
+        const int words = (p.N - n0 - c * 32) / 8;
+        if (mine && words > 0) {
+          const long long k = kept_at(p, first, rows, n0 / 32 + c, lane);
+          kept(p.aux, k, rows, words, s0);
+          if (p.act == BPT_ACT_SWIGLU) kept(p.aux2, k, rows, words, s1);
+        }
       };
       if constexpr (EPI == GROUPED_ACT_BWD) {
+        // on their way while the products are; a chunk's while the one before is worked on
         if (mine) {
-          const int q1 = p.order[row];
+          const int q1 = p.order[first + lane];
           if (q1 >= 0 && q1 < p.pairs)
             w = p.row_weight_f32 ? reinterpret_cast<const float*>(p.row_weight)[q1]
                                  : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.row_weight)[q1]);
@@ -725,63 +713,129 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       } else if (p.beta != 0.f) {
         continue;  // nothing to add
       }
-      const uint32_t tbase = tmem + (uint32_t)(acc * ACC_COLS) + ((uint32_t)(q * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < EPI_COLS / 32; ++c) {
-        const int col = half * EPI_COLS + c * 32;
-        const int nb = at.n0 + col;
-        if (nb >= p.N) break;  // warp-uniform
-        uint32_t ra[32], rb[32];
+      const uint32_t tbase = tmem + (uint32_t)(acc * ACC_COLS) + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * EPI_COLS);
+      auto read = [&](int col, uint32_t (&r)[32]) {
         if (!none) {
-          tmem_ld32(tbase + col, ra);
-          if (DUAL) tmem_ld32(tbase + BN + col, rb);
+          tmem_ld32(tbase + col, r);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) ra[j] = rb[j] = 0u;
+          for (int j = 0; j < 32; ++j) r[j] = 0u;
         }
-        if constexpr (EPI == GROUPED_ACT_BWD) {
-          if (nb + 32 <= p.N && p.vec32) {
-            const SavedPair<32> now = pair;
-            if (c + 1 < EPI_COLS / 32) fetch(c + 1);
-            if (mine) act_bwd_cols<32>(p, out, row * p.N + nb, ra, now, w, dot);
-          } else if (mine) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (nb + g * 8 < p.N) {  // N is a multiple of 8
-                SavedPair<8> now;
-                load_pair(p, row * p.N + nb + g * 8, now);
-                act_bwd_cols<8>(p, out, row * p.N + nb + g * 8, ra + g * 8, now, w, dot);
-              }
+      };
+      char* to = reinterpret_cast<char*>(out) + (first * p.N + n0) * (EPI == GROUPED_STORE && p.out_f32 ? 4 : 2);
+      const int left = p.N - n0;  // columns
+      if constexpr (EPI == GROUPED_STORE) {
+        if (p.out_f32) {
+#pragma unroll 1
+          for (int c = 0; c < EPI_COLS && c < left; c += 32) {
+            uint32_t r[32];
+            read(c, r);
+            const int words = min(8, (left - c) / 4);
+            if (p.beta != 0.f) put_rows<8, true>(r, stage, to + c * 4, p.N * 4ll, rows, words, p.beta);
+            else put_rows<8, false>(r, stage, to + c * 4, p.N * 4ll, rows, words, 0.f);
           }
-        } else if (mine) {
-          if (nb + 32 <= p.N && p.vec32) {
-            float a32[32], b32[32];
+        } else {
+          constexpr int W = EPI_COLS < 64 ? EPI_COLS : 64;
+#pragma unroll 1
+          for (int c = 0; c < EPI_COLS && c < left; c += W) {
+            uint32_t v[W / 2];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              a32[j] = __uint_as_float(ra[j]);
-              b32[j] = DUAL ? __uint_as_float(rb[j]) : 0.f;
+            for (int h = 0; h < W / 32; ++h) {
+              uint32_t r[32];
+              read(c + 32 * h, r);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[16 * h + j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
             }
-            epi_cols<EPI, DUAL, 32>(p, out, row, nb, a32, b32);
-          } else {
+            put_rows<W / 8, false>(v, stage, to + c * 2, p.N * 2ll, rows, min(W / 8, (left - c) / 8), 0.f);
+          }
+        }
+      } else if constexpr (EPI == GROUPED_ACT) {
+        constexpr int W = EPI_COLS < 64 ? EPI_COLS : 64;
+#pragma unroll 1
+        for (int c = 0; c < EPI_COLS && c < left; c += W) {
+          uint32_t v[W / 2];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              if (nb + g * 8 < p.N) {  // N is a multiple of 8
-                float a8[8], b8[8];
+          for (int h = 0; h < W / 32; ++h) {
+            uint32_t r[32], u[DUAL ? 32 : 1];
+            read(c + 32 * h, r);
+            if constexpr (DUAL) read(BN + c + 32 * h, u);
+            const int words = (left - c) / 8 - 4 * h;
+            if (p.out2 && mine && words > 0) {
+              const long long k = kept_at(p, first, rows, (n0 + c) / 32 + h, lane);
+              uint32_t t[16];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  a8[j] = __uint_as_float(ra[g * 8 + j]);
-                  b8[j] = DUAL ? __uint_as_float(rb[g * 8 + j]) : 0.f;
+              for (int j = 0; j < 16; ++j) t[j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+              keep(p.out2, k, rows, words, t);
+              if constexpr (DUAL) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) t[j] = pack_bf16(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+                keep(p.out3, k, rows, words, t);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float y[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float z = __uint_as_float(r[2 * j + i]);
+                if constexpr (DUAL) {
+                  y[i] = z * fast_sigmoid(z) * __uint_as_float(u[2 * j + i]);
+                } else {
+                  float slope;
+                  fast_gelu(z, p.act, y[i], slope);
                 }
-                epi_cols<EPI, DUAL, 8>(p, out, row, nb + g * 8, a8, b8);
               }
+              v[16 * h + j] = pack_bf16(y[0], y[1]);
             }
           }
+          put_rows<W / 8, false>(v, stage, to + c * 2, p.N * 2ll, rows, min(W / 8, (left - c) / 8), 0.f);
         }
-        __syncwarp();
-      }
-      if constexpr (EPI == GROUPED_ACT_BWD) {
+      } else {
+        // what was kept is bf16 (off by up to 2^-8 of its size): the activation
+        // and its slopes are taken again from it in fp32 and rounded once
+#pragma unroll 1
+        for (int c = 0; c < EPI_COLS && c < left; c += 32) {
+          uint32_t r[32], v[16], dv[16], aw[16];
+          read(c, r);
+          const int words = min(4, (left - c) / 8);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float x[2], y[2], z[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float a = mine && j < 4 * words ? __uint_as_float(r[2 * j + i]) : 0.f;
+              const float g = i ? bf16_hi(s0[j]) : bf16_lo(s0[j]);
+              const float wa = w * a;
+              if (p.act == BPT_ACT_SWIGLU) {
+                const float u = i ? bf16_hi(s1[j]) : bf16_lo(s1[j]);
+                const float sg = fast_sigmoid(g), si = g * sg;  // silu(g)
+                const float act = si * u;
+                dot = j < 4 * words ? fmaf(a, act, dot) : dot;
+                x[i] = wa * u * (sg + si * (1.f - sg));
+                y[i] = wa * si;
+                z[i] = w * act;
+              } else {
+                float act, slope;
+                fast_gelu(g, p.act, act, slope);
+                dot = j < 4 * words ? fmaf(a, act, dot) : dot;
+                x[i] = wa * slope;
+                y[i] = 0.f;
+                z[i] = w * act;
+              }
+            }
+            v[j] = pack_bf16(x[0], x[1]);
+            dv[j] = pack_bf16(y[0], y[1]);
+            aw[j] = pack_bf16(z[0], z[1]);
+          }
+          if (c + 32 < EPI_COLS) fetch(c / 32 + 1);
+          const long long ld = p.N * 2ll;
+          put_rows<4, false>(v, stage, to + c * 2, ld, rows, words, 0.f);
+          if (p.act == BPT_ACT_SWIGLU)
+            put_rows<4, false>(dv, stage, reinterpret_cast<char*>(p.out2) + (first * p.N + n0 + c) * 2, ld, rows, words, 0.f);
+          put_rows<4, false>(aw, stage, reinterpret_cast<char*>(p.out3) + (first * p.N + n0 + c) * 2, ld, rows, words, 0.f);
+        }
         // one sum per row and half tile, added in this order later
-        if (mine) p.part[(long long)(2 * (at.n0 / BN) + half) * p.rows + row] = dot;
+        if (mine) p.part[(long long)(2 * (at.n0 / BN) + half) * p.rows + first + lane] = dot;
       }
       if (!none) {
         tc_fence_before();

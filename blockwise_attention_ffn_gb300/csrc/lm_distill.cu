@@ -131,8 +131,9 @@ struct PrepParams {
   Saved s;
   unsigned int* err;
 };
-constexpr int PREP_ROWS = 32, PREP_WARPS = 8;
+constexpr int PREP_ROWS = 32, PREP_WARPS = 32;  // a row a warp: 59 us for 4001 rows of 64 entries with 8 warps
 
+template <int C>  // entries a lane holds
 __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepParams q) {
   extern __shared__ int s_id[];  // [PREP_ROWS][k | 1]
   const int lane = lane_id(), warp = warp_id();
@@ -140,15 +141,15 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
   const int64_t r0 = (int64_t)blockIdx.x * PREP_ROWS;
   wait_for_previous();
   let_next_start();
-  for (int i = warp; i < PREP_ROWS; i += PREP_WARPS) {
-    const int64_t row = r0 + i;
-    if (row >= q.n) break;  // the rows of a warp rise
-    int id[MAX_K / 32], rank[MAX_K / 32];
-    float v[MAX_K / 32];
+  static_assert(PREP_ROWS == PREP_WARPS, "a row a warp");
+  if (const int64_t row = r0 + warp; row < q.n) {
+    const int i = warp;
+    int id[C], rank[C];
+    float v[C];
     float m = -INFINITY;
     bool bad = false;
 #pragma unroll
-    for (int c = 0; c < MAX_K / 32; ++c) {
+    for (int c = 0; c < C; ++c) {
       const int j = c * 32 + lane;
       id[c] = NO_ID;
       rank[c] = 0;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
       if (m == -INFINITY) m = 0.f;
       total = 0.f;
 #pragma unroll
-      for (int c = 0; c < MAX_K / 32; ++c) {
+      for (int c = 0; c < C; ++c) {
         v[c] -= m;
         total += expf(v[c]);
       }
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
     const float log_total = total > 0.f ? logf(total) : 0.f;
     float mass = 0.f, ent = 0.f;
 #pragma unroll
-    for (int c = 0; c < MAX_K / 32; ++c) {
+    for (int c = 0; c < C; ++c) {
       const float lp = v[c] - log_total;
       const float p = expf(lp);
       v[c] = p;
@@ -203,16 +204,16 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
     }
     // an entry's rank: how many come before it
 #pragma unroll
-    for (int o = 0; o < MAX_K / 32; ++o) {
+    for (int o = 0; o < C; ++o) {
       if (o * 32 >= q.k) break;
       for (int l = 0; l < min(32, q.k - o * 32); ++l) {
         const int other = __shfl_sync(0xffffffffu, id[o], l);
 #pragma unroll
-        for (int c = 0; c < MAX_K / 32; ++c) rank[c] += other < id[c] || (other == id[c] && o * 32 + l < c * 32 + lane);
+        for (int c = 0; c < C; ++c) rank[c] += other < id[c] || (other == id[c] && o * 32 + l < c * 32 + lane);
       }
     }
 #pragma unroll
-    for (int c = 0; c < MAX_K / 32; ++c)
+    for (int c = 0; c < C; ++c)
       if (c * 32 + lane < q.k) {
         s_id[i * ld + rank[c]] = id[c];
         q.s.id[row * q.k + rank[c]] = id[c];
@@ -379,7 +380,8 @@ int bpt_lm_distill_fwd(const bpt_distill_config* cfg, const void* x, const void*
     PrepParams q{ids, teacher, D.n, D.V, D.nparts, (int)D.k, D.teacher, 1.f / D.T, S, err};
     ProfScope prof(PROF_MISC, 0.0, (double)D.n * (20.0 * D.k + D.nparts), st);
     const size_t smem = (size_t)PREP_ROWS * (D.k | 1) * 4;
-    if (launch_dependent(prepare_kernel, (int)((D.n + PREP_ROWS - 1) / PREP_ROWS), 1, dim3(32 * PREP_WARPS), smem, st, q) != cudaSuccess)
+    auto k = D.k <= 32 ? prepare_kernel<1> : D.k <= 64 ? prepare_kernel<2> : prepare_kernel<4>;
+    if (launch_dependent(k, (int)((D.n + PREP_ROWS - 1) / PREP_ROWS), 1, dim3(32 * PREP_WARPS), smem, st, q) != cudaSuccess)
       return BPT_ECUDA;
   }
   {

@@ -165,14 +165,14 @@ struct Planner {
 };
 
 // What the backward takes back: SwiGLU the gate and up products, GeLU the
-// activation and its slope; [pairs, f] bf16 each, in the groups' order.
+// product; pairs * f bf16 values each, in the grouped GEMM's own layout.
 struct Saved {
   void *s0, *s1;
 };
 size_t plan_saved(const MoeDims& D, void* base, Saved* s) {
   Planner pl{reinterpret_cast<uint8_t*>(base)};
   s->s0 = pl.take(D.pairs * D.f * 2);
-  s->s1 = pl.take(D.pairs * D.f * 2);
+  s->s1 = D.act == BPT_ACT_SWIGLU ? pl.take(D.pairs * D.f * 2) : nullptr;
   return pl.off;
 }
 struct FwdWs {
@@ -258,7 +258,6 @@ int bpt_moe_ffn_fwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const voi
   if (D.debug && debug_spans(sp, 11)) return BPT_EINVAL;
   plan_fwd(D, ws, &W);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  void* act = W.act;
   {
     GroupedOp op = op_base(D, r);
     op.form = GROUPED_NT;
@@ -271,16 +270,11 @@ int bpt_moe_ffn_fwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const voi
     op.order = r->order;
     op.w = w1;
     op.w2 = w3;
-    op.out = act;
+    op.out = W.act;
     if (saved) {
       plan_saved(D, saved, &S);
-      if (swiglu) {
-        op.out2 = S.s0;
-        op.out3 = S.s1;
-      } else {
-        op.out = act = S.s0;
-        op.out2 = S.s1;
-      }
+      op.out2 = S.s0;
+      op.out3 = S.s1;
     }
     if ((rc = grouped_gemm(op, st))) return rc;
   }
@@ -289,7 +283,7 @@ int bpt_moe_ffn_fwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const voi
     op.form = GROUPED_NT;
     op.N = D.h;
     op.K = D.f;
-    op.a = act;
+    op.a = W.act;
     op.a_rows = D.pairs;
     op.w = w2;
     op.out = W.ys;

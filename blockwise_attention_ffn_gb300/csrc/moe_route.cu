@@ -25,9 +25,15 @@ namespace bpt {
 
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int WARPS = THREADS / 32;
-constexpr int MAX_EXPERTS = 1024;
+// Threads a block: 1024 where the registers suffice.  A row's choice is a chain
+// of k dependent steps, so the time is that of the rows a warp does in turn: at
+// n = 32768, E = 64, k = 6 choosing and placing took 41 and 20 us with 256
+// threads in 152 blocks.
+constexpr int BWD_THREADS = 256;
+template <int V>
+constexpr int choose_threads() {
+  return V == 8 ? 1024 : V == 16 ? 512 : 256;
+}
 
 struct RouteParams {
   const void* logits;
@@ -106,11 +112,12 @@ __device__ __forceinline__ float group_max(float v) {
 
 // Rows [r0, r1) of one block: their choice, weights and the block's sums.
 // G lanes hold a row, V = 8 or more consecutive logits each.
-template <int G, int V>
+template <int G, int V, int THREADS>
 __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b, int* s_hist, float* s_sum) {
   const int lane = lane_id(), warp = warp_id();
   const int sub = lane % G, c = sub * V;
   constexpr int ROWS = 32 / G;  // rows a warp holds at once
+  constexpr int WARPS = THREADS / 32;
   for (int e = threadIdx.x; e < p.E; e += THREADS) s_hist[e] = 0;
   __syncthreads();
   const bool sums = p.balance != 0.f, zsums = p.zc != 0.f;
@@ -219,17 +226,20 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
       }
     }
   }
-  // the block's sums, in a fixed order: by expert over the row groups, the
-  // scalars over the threads
+  // the block's sums, in a fixed order: over the rows a warp held at once, then
+  // over the warps
   if (sums) {
-    const int slots = WARPS * ROWS;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c + i < p.E) s_sum[(warp * ROWS + lane / G) * p.E + c + i] = acc[i];
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int d = G; d < 32; d <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
+      if (lane < G && c + i < p.E) s_sum[warp * p.E + c + i] = acc[i];
+    }
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += THREADS) {
       float t = 0.f;
-      for (int q = 0; q < slots; ++q) t += s_sum[q * p.E + e];
+#pragma unroll 8
+      for (int q = 0; q < WARPS; ++q) t += s_sum[q * p.E + e];
       p.psum[(int64_t)b * p.E + e] = t;
     }
   }
@@ -261,8 +271,10 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
 // Places of block b's pairs: an expert's rows are those of the blocks before,
 // then of this block's warps before, then in the order of the pairs.
 // s_count: [WARPS][E]; s_tot, s_base: [E].
+template <int THREADS>
 __device__ void place_rows(const RouteParams& p, int64_t r0, int64_t r1, int b, int* s_count, int* s_tot, int* s_base) {
   const int lane = lane_id(), warp = warp_id();
+  constexpr int WARPS = THREADS / 32;
   __shared__ int s_part[2][THREADS];
   for (int e0 = 0; e0 < p.E; e0 += THREADS) {
     // rows of each expert in all blocks and in those before b: slices of the
@@ -357,9 +369,11 @@ __device__ void place_rows(const RouteParams& p, int64_t r0, int64_t r1, int b, 
 
 // The losses and the number of routed rows, by one block: sums over the
 // blocks of rows, in an order fixed by their number.
+template <int THREADS>
 __device__ void finish_losses(const RouteParams& p) {
-  __shared__ double s_loss[WARPS];
-  __shared__ int s_live[WARPS];
+  constexpr int WARPS = THREADS / 32;
+  __shared__ double s_loss[WARPS], s_ps[THREADS];
+  __shared__ int s_live[WARPS], s_rows[THREADS];
   const int lane = lane_id(), warp = warp_id();
   int l = 0;
   for (int q = threadIdx.x; q < p.nblk; q += THREADS) l += p.live[q];
@@ -377,16 +391,25 @@ __device__ void finish_losses(const RouteParams& p) {
     for (int e0 = 0; e0 < p.E; e0 += THREADS) {
       const int span = min(p.E - e0, THREADS), slices = THREADS / span;
       const int e = e0 + (int)threadIdx.x % span, sl = (int)threadIdx.x / span;
-      // an expert's count is needed whole: every slice adds its own
-      int count = 0;
+      int rows = 0;
       double ps = 0.0;
-      if (sl < slices) {
-#pragma unroll 16
-        for (int q = 0; q < p.nblk; ++q) count += p.hist[(int64_t)q * p.E + e];
-#pragma unroll 16
-        for (int q = sl; q < p.nblk; q += slices) ps += (double)p.psum[(int64_t)q * p.E + e];
+      if (sl < slices)
+#pragma unroll 8
+        for (int q = sl; q < p.nblk; q += slices) {
+          rows += p.hist[(int64_t)q * p.E + e];
+          ps += (double)p.psum[(int64_t)q * p.E + e];
+        }
+      s_rows[threadIdx.x] = rows;
+      s_ps[threadIdx.x] = ps;
+      __syncthreads();
+      if ((int)threadIdx.x < span) {
+        for (int q = 1; q < slices; ++q) {
+          rows += s_rows[q * span + threadIdx.x];
+          ps += s_ps[q * span + threadIdx.x];
+        }
+        t += ps * (double)rows;
       }
-      t += ps * (double)count;
+      __syncthreads();
     }
     t *= (double)p.balance * p.E / (nv * nv * p.k);
   }
@@ -407,36 +430,40 @@ __device__ void finish_losses(const RouteParams& p) {
 }
 
 template <int G, int V>
-__global__ void __launch_bounds__(THREADS) route_choose_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(choose_threads<V>()) route_choose_kernel(const RouteParams p) {
   extern __shared__ float s_dyn[];
   int* s_hist = reinterpret_cast<int*>(s_dyn);
   float* s_sum = s_dyn + p.E;
   wait_for_previous();
   let_next_start();
   const int64_t r0 = min(p.n, blockIdx.x * p.per), r1 = min(p.n, r0 + p.per);
-  choose_rows<G, V>(p, r0, r1, blockIdx.x, s_hist, s_sum);
+  choose_rows<G, V, choose_threads<V>()>(p, r0, r1, blockIdx.x, s_hist, s_sum);
 }
 
+template <int THREADS>
 __global__ void __launch_bounds__(THREADS) route_place_kernel(const RouteParams p) {
   extern __shared__ float s_dyn[];
+  constexpr int WARPS = THREADS / 32;
   int* s_count = reinterpret_cast<int*>(s_dyn);
   wait_for_previous();
   let_next_start();
-  if ((int)blockIdx.x == p.nblk) return finish_losses(p);
+  if ((int)blockIdx.x == p.nblk) return finish_losses<THREADS>(p);
   const int64_t r0 = min(p.n, blockIdx.x * p.per), r1 = min(p.n, r0 + p.per);
-  place_rows(p, r0, r1, blockIdx.x, s_count, s_count + WARPS * p.E, s_count + (WARPS + 1) * p.E);
+  place_rows<THREADS>(p, r0, r1, blockIdx.x, s_count, s_count + WARPS * p.E, s_count + (WARPS + 1) * p.E);
 }
 
 // Few rows: one block does both
+constexpr int ONE_THREADS = 256;
 template <int G, int V>
-__global__ void __launch_bounds__(THREADS) route_one_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(ONE_THREADS) route_one_kernel(const RouteParams p) {
   extern __shared__ float s_dyn[];
+  constexpr int WARPS = ONE_THREADS / 32;
   int* s_int = reinterpret_cast<int*>(s_dyn);
   wait_for_previous();
   let_next_start();
-  choose_rows<G, V>(p, 0, p.n, 0, s_int, s_dyn + p.E);
-  place_rows(p, 0, p.n, 0, s_int, s_int + WARPS * p.E, s_int + (WARPS + 1) * p.E);
-  finish_losses(p);
+  choose_rows<G, V, ONE_THREADS>(p, 0, p.n, 0, s_int, s_dyn + p.E);
+  place_rows<ONE_THREADS>(p, 0, p.n, 0, s_int, s_int + WARPS * p.E, s_int + (WARPS + 1) * p.E);
+  finish_losses<ONE_THREADS>(p);
 }
 
 struct RouteBwdParams {
@@ -455,10 +482,10 @@ struct RouteBwdParams {
 // gradients at the chosen; the balance loss: the same with p and
 // g_e = balance E count_e / (nv^2 k); the z loss: 2 z_coef lse / nv p_e.
 template <int G, int V>
-__global__ void __launch_bounds__(THREADS) route_bwd_kernel(const RouteBwdParams p) {
+__global__ void __launch_bounds__(BWD_THREADS) route_bwd_kernel(const RouteBwdParams p) {
   const int lane = lane_id();
   const int sub = lane % G, c = sub * V;
-  constexpr int ROWS = 32 / G;
+  constexpr int ROWS = 32 / G, WARPS = BWD_THREADS / 32;
   wait_for_previous();
   let_next_start();
   const int nv_i = p.offsets[p.E + 1];
@@ -579,21 +606,19 @@ constexpr int64_t ONE_BLOCK_ROWS = 256;
 template <int G, int V>
 int route_launch(const RouteParams& p, cudaStream_t st) {
   // shared memory: the choice's counts and sums, then the placing's counts
-  const size_t choose = (size_t)(p.E + std::max(WARPS * (32 / G) * p.E, 2 * WARPS)) * 4;
-  const size_t place = (size_t)(WARPS + 2) * p.E * 4;
-  static std::atomic<uint64_t> a0{0}, a1{0}, a2{0};
-  constexpr int TOP = (MAX_EXPERTS * (WARPS + 2)) * 4 + 4096;
+  auto choose = [&](int warps) { return (size_t)(p.E + std::max(warps * p.E, 2 * warps)) * 4; };
+  auto place = [&](int warps) { return (size_t)(warps + 2) * p.E * 4; };
   if (p.nblk == 1) {
-    auto k = route_one_kernel<G, V>;
-    if (smem_limit_once(reinterpret_cast<const void*>(k), TOP, &a0)) return BPT_ECUDA;
-    return launch_dependent(k, 1, 1, dim3(THREADS), std::max(choose, place), st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
+    constexpr int W = ONE_THREADS / 32;
+    return launch_dependent(route_one_kernel<G, V>, 1, 1, dim3(ONE_THREADS), std::max(choose(W), place(W)), st, p) == cudaSuccess ? BPT_OK
+                                                                                                                                : BPT_ECUDA;
   }
-  auto k = route_choose_kernel<G, V>;
-  if (smem_limit_once(reinterpret_cast<const void*>(k), TOP, &a1) ||
-      smem_limit_once(reinterpret_cast<const void*>(route_place_kernel), TOP, &a2))
-    return BPT_ECUDA;
-  if (launch_dependent(k, p.nblk, 1, dim3(THREADS), choose, st, p) != cudaSuccess) return BPT_ECUDA;
-  return launch_dependent(route_place_kernel, p.nblk + 1, 1, dim3(THREADS), place, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
+  constexpr int T = choose_threads<V>(), PT = V == 8 ? 1024 : 256;
+  if (launch_dependent(route_choose_kernel<G, V>, p.nblk, 1, dim3(T), choose(T / 32), st, p) != cudaSuccess) return BPT_ECUDA;
+  auto k = route_place_kernel<PT>;
+  static std::atomic<uint64_t> attr{0};
+  if (smem_limit_once(reinterpret_cast<const void*>(k), 48 * 1024, &attr)) return BPT_ECUDA;
+  return launch_dependent(k, p.nblk + 1, 1, dim3(PT), place(PT / 32), st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
 }
 
 // G lanes of V logits hold a row: 8 a lane (a 32- or 16-byte load) as long as
@@ -736,9 +761,9 @@ int bpt_moe_route_bwd(const bpt_moe_config* cfg, const void* logits, const bpt_m
   {
     ProfScope prof(PROF_MISC, 0.0, 2.0 * (double)D.n * D.E * D.logit_bytes + 8.0 * (double)D.pairs, st);
     rc = by_width(p.E, [&](auto g, auto v) {
-      constexpr int per = WARPS * (32 / g.value);
+      constexpr int per = BWD_THREADS / 32 * (32 / g.value);
       const int grid = (int)std::min<int64_t>((D.n + per - 1) / per, 8 * (int64_t)sms);
-      return launch_dependent(route_bwd_kernel<g.value, v.value>, grid, 1, dim3(THREADS), 0, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
+      return launch_dependent(route_bwd_kernel<g.value, v.value>, grid, 1, dim3(BWD_THREADS), 0, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
     });
   }
   if (rc) return rc;

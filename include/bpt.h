@@ -553,8 +553,8 @@ int bpt_moe_route_bwd(const bpt_moe_config* cfg, const void* logits, const bpt_m
  *   r         weights, offsets, order and slot are read (ids is not); any
  *             grouping of pairs in this form will do.  An order or slot entry
  *             outside its range is taken as none.
- *   saved     bpt_moe_saved_bytes(cfg) for the backward (two [n k, f] bf16
- *             tensors), or NULL: inference
+ *   saved     bpt_moe_saved_bytes(cfg) for the backward (n k f bf16 values,
+ *             twice with SwiGLU), or NULL: inference
  *   ws        bpt_moe_ffn_workspace_bytes(cfg, pass), one per call in flight
  *   dy, dx    [n, h] bf16;  dweights [n, k];  dw1, dw3, dw2 like the weights
  * An expert without rows has gradients of 0.  The activation, its gradient and
