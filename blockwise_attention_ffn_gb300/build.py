@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbpt.so")
 SOURCES = ["bpt_api.cu", "gemm_tc.cu", "gemm_pair.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_noalloc.cu", "norm_misc.cu",
            "host_util.cu", "lm_loss.cu", "norm_rope.cu", "grad_clip.cu", "attn_mod.cu", "attn_mod_fwd.cu", "attn_mod_bwd.cu",
-           "grouped.cu", "grouped_nt.cu", "grouped_nn.cu", "grouped_tn.cu", "moe_route.cu", "moe_ffn.cu",
+           "grouped.cu", "grouped_nt.cu", "grouped_nn.cu", "grouped_tn.cu", "moe_route.cu", "moe_ffn.cu", "moe_few.cu",
            "gemm_distill.cu", "lm_distill.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

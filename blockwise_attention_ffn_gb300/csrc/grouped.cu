@@ -22,7 +22,7 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   // Few rows: the weights' bytes bound the product, and 64-column tiles give
   // the SMs more units to share them.
   const bool small = op.form == GROUPED_NT && op.mean_rows <= 64;
-  bool pair = tn ? op.M > BM : op.mean_rows >= 512;
+  bool pair = tn ? op.M > BM : op.mean_rows >= 384;
   if (pair && gk::pair_units() <= 0) pair = false;
   const int BN = small ? 64 : dual ? 128 : 256;
   const int TM = pair ? 2 * BM : BM;

@@ -182,7 +182,7 @@ size_t plan_fwd(const MoeDims& D, void* base, FwdWs* w) {
   Planner pl{reinterpret_cast<uint8_t*>(base)};
   w->act = pl.take(D.pairs * D.f * 2);
   w->ys = pl.take(D.pairs * D.h * 2);
-  return pl.off;
+  return moe_few_rows(D) ? std::max(pl.off, moe_few_ws_bytes(D)) : pl.off;
 }
 struct BwdWs {
   void *dg, *du, *aw, *dxs;
@@ -258,6 +258,10 @@ int bpt_moe_ffn_fwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const voi
   if (D.debug && debug_spans(sp, 11)) return BPT_EINVAL;
   plan_fwd(D, ws, &W);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!saved && moe_few_rows(D)) {
+    if ((rc = moe_few_fwd(D, r, x, w1, w3, w2, y, ws, st))) return rc;
+    return D.debug ? debug_finish(st) : BPT_OK;
+  }
   {
     GroupedOp op = op_base(D, r);
     op.form = GROUPED_NT;

@@ -211,6 +211,9 @@ FFN = [
     (1, 64, 64, 8, 2, 2, False),
     (1, 264, 136, 4, 4, 0, False),
     (5, 40, 72, 64, 3, 2, False),
+    (1, 264, 136, 16, 4, 0, False),     # rows one by one (inference)
+    (3, 1000, 520, 64, 6, 1, True),
+    (8, 2056, 1032, 128, 8, 2, False),
     (70, 256, 200, 12, 2, 1, True),
     (300, 136, 264, 4, 2, 2, True),     # one-SM tiles
     (333, 512, 328, 3, 3, 0, False),
@@ -271,20 +274,22 @@ def test_experts(case, wt, gt):
     ws = bpt.alloc_bytes(bpt.bpt_moe_ffn_workspace_bytes(cfg, bpt.BPT_PASS_BWD)).fill_(255)
     bpt.bpt_moe_ffn_bwd(cfg, r, x, w1, w3, w2, saved, dy, dx, dwt, *dm, ws)
     sync()
-    assert torch.equal(y, plain)
+    if 2 * n * k > E:  # fewer rows: inference takes them one by one
+        assert torch.equal(y, plain)
     leaves = [t.double().requires_grad_() for t in (x, r.weights, w1, w3, w2) if t is not None]
     if w3 is None:
         leaves.insert(3, None)
     want = network(r, act, *leaves)
     grads = iter(torch.autograd.grad(want, [t for t in leaves if t is not None], dy.double()))
     near(y, want.detach(), 3, "y")
+    near(plain, want.detach(), 3, "y without saved")
     near(dx, next(grads), 5, "dx")
     near(dwt, next(grads), 3, "dweights")
     for name, got in zip(("dw1", "dw3", "dw2"), dm):
         if got is not None:
             near(got, next(grads), 4, name)
     gone = r.ids[:, 0] < 0
-    assert bool((y[gone] == 0).all()) and bool((dx[gone] == 0).all()) and bool((dwt[r.ids < 0] == 0).all())
+    assert bool((y[gone] == 0).all()) and bool((plain[gone] == 0).all()) and bool((dx[gone] == 0).all()) and bool((dwt[r.ids < 0] == 0).all())
     empty = (r.offsets[1:E + 1] == r.offsets[:E]).nonzero()[:, 0]
     assert all(bool((m[empty] == 0).all()) for m in dm if m is not None)
 
