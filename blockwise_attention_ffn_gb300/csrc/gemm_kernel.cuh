@@ -92,6 +92,7 @@ struct GemmParams {
   int ent_k;
   float inv_t;
   const float *rowp, *roww;
+  long long slab;      // EPI_SLABS: elements from one K range's product to the next's
   unsigned int* err;
 };
 
@@ -594,6 +595,28 @@ __device__ __forceinline__ void distill_tile(const GemmParams& p, uint32_t tbase
   }
 }
 
+// EPI_SLABS: each K range's product to a place of its own, for a sum in a fixed
+// order afterwards
+template <int EPI_COLS>
+__device__ __forceinline__ void slab_tile(const GemmParams& p, uint32_t tbase, int m, int n0, int half, int ks) {
+#pragma unroll 1
+  for (int c = 0; c < EPI_COLS / 32; ++c) {
+    const int col = half * EPI_COLS + c * 32;
+    const int nb = n0 + col;
+    uint32_t ra[32];
+    tmem_ld32(tbase + col, ra);
+    if (m < p.M && nb < p.N) {
+      float* o = reinterpret_cast<float*>(p.out) + ks * p.slab + (long long)m * p.ldo + nb;
+#pragma unroll
+      for (int i = 0; i < 32; i += 4)  // N is a multiple of 8
+        if (nb + i < p.N)
+          *reinterpret_cast<float4*>(o + i) = make_float4(__uint_as_float(ra[i]), __uint_as_float(ra[i + 1]),
+                                                          __uint_as_float(ra[i + 2]), __uint_as_float(ra[i + 3]));
+    }
+    __syncwarp();
+  }
+}
+
 // The epilogue of one accumulator for one warp: this thread's row m of the
 // tile starting at column n0, the half `half` of its BN columns, read from
 // TMEM at tbase (the warp's lane quarter, the accumulator's first column).
@@ -694,7 +717,8 @@ __device__ __forceinline__ void epilogue_tile(const GemmParams& p, uint32_t tbas
 // Persistent: each CTA (or pair) walks work units u0, u0 + units in flight,
 // ... with two TMEM accumulators, so the epilogue of one tile overlaps the
 // main loop of the next.
-// SET: 0 the layer's and the loss's epilogues, 1 the distillation loss's.
+// SET: 0 the layer's and the loss's epilogues, 1 the distillation loss's, 2
+// the products of K ranges side by side (EPI_SLABS).
 template <int BN, bool A_MN, bool B_MN, bool DUAL, bool PAIR, int SET = 0>
 __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   constexpr int STAGES = stages<PAIR>();
@@ -907,7 +931,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       int m0, n0;
       tile_origin(p, unit, TM, BN, m0, n0);
       const uint32_t tbase = tmem + (uint32_t)(acc * ACC_COLS) + ((uint32_t)(q * 32) << 16);
-      epilogue_tile<BN, DUAL, SET>(p, tbase, m0 + row, n0, half);
+      if constexpr (SET == 2) slab_tile<BN / 2>(p, tbase, m0 + row, n0, half, unit / (p.mt * p.nt));
+      else epilogue_tile<BN, DUAL, SET>(p, tbase, m0 + row, n0, half);
       // this warp's part of the accumulator has been read: hand it back
       tc_fence_before();
       __syncwarp();
@@ -1007,6 +1032,7 @@ int launch(GemmParams& p, cudaStream_t st) {
 int launch_pair(GemmParams& p, bool a_mn, bool b_mn, bool dual, cudaStream_t st);
 // the launches with the distillation loss's epilogues (gemm_distill.cu)
 int launch_distill(GemmParams& p, bool pair, cudaStream_t st);
+int launch_slabs(GemmParams& p, bool pair, cudaStream_t st);
 int pair_units();
 
 }  // namespace gk

@@ -81,6 +81,7 @@ int gemm(int64_t M, int64_t N, int64_t K, const MatView& A, bool a_mn, const Mat
   p.inv_t = e.inv_t;
   p.rowp = e.rowp;
   p.roww = e.roww;
+  p.slab = e.slab;
   p.err = device_error_word();
   if (!p.err) return 3;
   {
@@ -112,9 +113,14 @@ int gemm(int64_t M, int64_t N, int64_t K, const MatView& A, bool a_mn, const Mat
           break;
         }
     }
-    if (p.ksplit > 1 && e.beta == 0.f) {
+    if (e.kind == EPI_SLABS) p.ksplit = e.slabs;
+    else if (p.ksplit > 1 && e.beta == 0.f) {
       if (cudaMemset2DAsync(e.out, (size_t)e.ldo * 4, 0, (size_t)N * 4, (size_t)M, stream) != cudaSuccess) return 3;
     }
+  }
+  if (e.kind == EPI_SLABS) {
+    if (a_mn || !b_mn || dual || nseg != 1 || e.slabs < 1 || e.slabs > p.nkt) return 1;
+    return launch_slabs(p, pair, stream);
   }
   if (e.kind == EPI_KD_LSE || e.kind == EPI_KD_GRAD) {
     if (a_mn || b_mn || dual || nseg != 1) return 1;

@@ -134,6 +134,7 @@ enum EpiKind {
                        // entry j (column ent_id[m, j], sorted; the first entry at or
                        // past column 128 q is ent_at[q * ldo + m]) -> float out2[m, j]
   EPI_KD_GRAD = 9,     // out = exp(z - rowf[m]) * rowp[m] (* roww[m]) * scale -> bf16
+  EPI_SLABS = 10,      // the product of K range q of `slabs` -> fp32 out[q * slab + m * ldo + n]
 };
 
 struct Epilogue {
@@ -169,6 +170,8 @@ struct Epilogue {
   int ent_k = 0;
   float inv_t = 1.f;
   const float *rowp = nullptr, *roww = nullptr;
+  int slabs = 1;
+  int64_t slab = 0;
 };
 
 // Returns 0 or a BPT_* status.

@@ -108,14 +108,26 @@ size_t plan_fwd(const KdDims& D, void* base, FwdWs* w) {
   w->term = pl.take<double>(D.n);
   return pl.off;
 }
+// K ranges of dx = dz W that run side by side: a product of few tiles over
+// thousands of words would leave most SMs idle (100 rows of 256 against 5000
+// words took 36 us in one tile).  Each range's product has a place of its own
+// and they are added in order, so the sum does not depend on the run.
+int dx_slabs(const KdDims& D, int64_t nv) {
+  const int64_t tiles = ((D.n + 255) / 256) * ((D.h + 255) / 256), kt = (nv + 63) / 64;
+  const int want = tiles <= 9 ? 8 : tiles <= 19 ? 4 : tiles <= 38 ? 2 : 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(want, kt / 4));
+}
+
 struct BwdWs {
   __nv_bfloat16* dz;
-  float* dx_acc;
+  float *dx_acc, *slabs;
 };
 size_t plan_bwd(const KdDims& D, void* base, BwdWs* w) {
   Planner pl{reinterpret_cast<uint8_t*>(base)};
   w->dz = pl.take<__nv_bfloat16>(D.n * D.cv);
   w->dx_acc = D.nblk > 1 ? pl.take<float>(D.n * D.h) : nullptr;
+  const int s = dx_slabs(D, std::min(D.cv, D.V));
+  w->slabs = s > 1 ? pl.take<float>(s * D.n * D.h) : nullptr;
   return pl.off;
 }
 
@@ -330,6 +342,21 @@ __global__ void __launch_bounds__(256) entries_kernel(int64_t n, int k, int64_t 
   dz[row * ld + (id - v0)] = __float2bfloat16(w != 0.f ? w * (s.mass[row] * q - p) : 0.f);
 }
 
+// sum over the slabs in order, onto acc (NULL: 0): fp32 out, or bf16
+__global__ void __launch_bounds__(256) slabs_kernel(int64_t n4, int slabs, const float4* s, const float4* acc, float4* out_f32,
+                                                    uint2* out_bf16) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  float4 t = acc ? acc[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int q = 0; q < slabs; ++q) {
+    const float4 v = s[q * n4 + i];
+    t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+  }
+  if (out_f32) out_f32[i] = t;
+  else out_bf16[i] = make_uint2(pack_bf16(t.x, t.y), pack_bf16(t.z, t.w));
+}
+
 bool al(const void* p, int a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
@@ -463,12 +490,28 @@ int bpt_lm_distill_bwd(const bpt_distill_config* cfg, const void* x, const void*
       e.deterministic = D.det;
       if ((rc = gemm(nv, D.h, D.n, Z, true, &X, &Kn, 1, true, nullptr, e, st))) return rc;
     }
-    {
+    const int slabs = dx_slabs(D, nv);
+    const bool last = b == D.nblk - 1;
+    if (slabs > 1) {
+      Epilogue e;
+      e.kind = EPI_SLABS;
+      e.out = W.slabs;
+      e.ldo = D.h;
+      e.slabs = slabs;
+      e.slab = D.n * D.h;
+      if ((rc = gemm(D.n, D.h, nv, Z, false, &Wb, &Kv, 1, true, nullptr, e, st))) return rc;
+      const int64_t n4 = D.n * D.h / 4;
+      ProfScope prof(PROF_MISC, 0.0, 16.0 * (double)n4 * (slabs + 1), st);
+      slabs_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, st>>>(
+          n4, slabs, reinterpret_cast<const float4*>(W.slabs), b > 0 ? reinterpret_cast<const float4*>(W.dx_acc) : nullptr,
+          last ? nullptr : reinterpret_cast<float4*>(W.dx_acc), reinterpret_cast<uint2*>(dx));
+      if (cudaGetLastError() != cudaSuccess) return BPT_ECUDA;
+    } else {
       // dx: fp32 over the blocks, the last one rounds to bf16
       Epilogue e;
       e.deterministic = D.det;
       e.ldo = D.h;
-      if (b == D.nblk - 1) {
+      if (last) {
         e.kind = EPI_BF16;
         e.out = dx;
         if (b > 0) {

@@ -59,6 +59,13 @@ __device__ __forceinline__ uint32_t sort_key(float v) {  // rises with v; 0: not
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// e^x with a relative error of 2^-22 and |x| 2^-24
+__device__ __forceinline__ float exp_of(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+
 // V consecutive logits from column c of a row (past E: -inf)
 template <int V>
 __device__ __forceinline__ void load_logits(const void* z, int bf16, int64_t row, int E, int c, float (&v)[V], unsigned int* err) {
@@ -138,7 +145,7 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
     uint32_t key[V];  // 0: taken, or not to be chosen
 #pragma unroll
     for (int i = 0; i < V; ++i) key[i] = v[i] > -INFINITY ? sort_key(v[i]) : 0u;
-    float m = 0.f, total = 0.f, top_sum = 0.f, mine = 0.f, first = 0.f;
+    float m = 0.f, total = 0.f, inv = 0.f, top_sum = 0.f, mine = 0.f, first = 0.f;
     for (int j = 0; j < p.k; ++j) {
       // the largest key left; of equals the first lane's, and its first
       uint32_t best = key[0];
@@ -164,10 +171,14 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
         m = some ? val : 0.f;
         float part = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) part += v[i] > -INFINITY ? expf(v[i] - m) : 0.f;
+        for (int i = 0; i < V; ++i) {
+          v[i] = exp_of(v[i] - m);  // from here on the exponentials; -inf: 0
+          part += v[i];
+        }
         total = group_sum<G>(part);
+        inv = total > 0.f ? 1.f / total : 0.f;
       }
-      const float ex = some ? expf(val - m) : 0.f;
+      const float ex = some ? exp_of(val - m) : 0.f;
       top_sum += ex;
       if (sub == from) {
 #pragma unroll
@@ -180,7 +191,7 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
         if (some) atomicAdd(&s_hist[idx], 1);
         mine = ex;
         if (!p.norm) {
-          const float w = some ? ex / total : 0.f;
+          const float w = ex * inv;
           if (p.weights_bf16) reinterpret_cast<__nv_bfloat16*>(p.weights)[row * p.k + j] = __float2bfloat16(w);
           else reinterpret_cast<float*>(p.weights)[row * p.k + j] = w;
         } else if (p.k > G) {
@@ -190,10 +201,10 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
       }
     }
     if (p.norm && in) {
-      const float inv = top_sum > 0.f ? top_sum : 1.f;
+      const float of = top_sum > 0.f ? top_sum : 1.f;  // divided by: a single choice has weight 1 exactly
       if (p.k <= G) {
         if (sub < p.k) {
-          const float w = mine / inv;
+          const float w = mine / of;
           if (p.weights_bf16) reinterpret_cast<__nv_bfloat16*>(p.weights)[row * p.k + sub] = __float2bfloat16(w);
           else reinterpret_cast<float*>(p.weights)[row * p.k + sub] = w;
         }
@@ -204,10 +215,10 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
             const float z = id < 0 ? -INFINITY
                             : p.logits_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.logits)[row * p.E + id])
                                             : reinterpret_cast<const float*>(p.logits)[row * p.E + id];
-            reinterpret_cast<__nv_bfloat16*>(p.weights)[row * p.k + j] = __float2bfloat16(id < 0 ? 0.f : expf(z - m) / inv);
+            reinterpret_cast<__nv_bfloat16*>(p.weights)[row * p.k + j] = __float2bfloat16(id < 0 ? 0.f : exp_of(z - m) / of);
           } else {
             float* w = reinterpret_cast<float*>(p.weights) + row * p.k + j;
-            *w = *w / inv;
+            *w = *w / of;
           }
         }
       }
@@ -216,9 +227,8 @@ __device__ void choose_rows(const RouteParams& p, int64_t r0, int64_t r1, int b,
     if (routed) {
       live += sub == 0;
       if (sums) {
-        const float inv = 1.f / total;
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += v[i] > -INFINITY ? expf(v[i] - m) * inv : 0.f;
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
       }
       if (zsums && sub == 0) {
         const float lse = m + logf(total);
@@ -372,7 +382,7 @@ __device__ void place_rows(const RouteParams& p, int64_t r0, int64_t r1, int b, 
 template <int THREADS>
 __device__ void finish_losses(const RouteParams& p) {
   constexpr int WARPS = THREADS / 32;
-  __shared__ double s_loss[WARPS], s_ps[THREADS];
+  __shared__ float s_ps[THREADS];
   __shared__ int s_live[WARPS], s_rows[THREADS];
   const int lane = lane_id(), warp = warp_id();
   int l = 0;
@@ -384,48 +394,49 @@ __device__ void finish_losses(const RouteParams& p) {
   for (int w = 0; w < WARPS; ++w) l += s_live[w];
   if (threadIdx.x == 0) p.offsets[p.E + 1] = l;
   if (!p.loss) return;
-  const double nv = l > 0 ? l : 1;
+  // sum_e count_e sum_t p_te: slices of the blocks per expert, in fp32 by at
+  // most 152 blocks and then in fp64 (which this card adds slowly) by one warp
   double t = 0.0;
   if (p.balance != 0.f) {
-    // sum_e count_e sum_t p_te: slices of the blocks per expert
     for (int e0 = 0; e0 < p.E; e0 += THREADS) {
       const int span = min(p.E - e0, THREADS), slices = THREADS / span;
       const int e = e0 + (int)threadIdx.x % span, sl = (int)threadIdx.x / span;
       int rows = 0;
-      double ps = 0.0;
+      float ps = 0.f;
       if (sl < slices)
 #pragma unroll 8
         for (int q = sl; q < p.nblk; q += slices) {
           rows += p.hist[(int64_t)q * p.E + e];
-          ps += (double)p.psum[(int64_t)q * p.E + e];
+          ps += p.psum[(int64_t)q * p.E + e];
         }
       s_rows[threadIdx.x] = rows;
       s_ps[threadIdx.x] = ps;
       __syncthreads();
-      if ((int)threadIdx.x < span) {
-        for (int q = 1; q < slices; ++q) {
-          rows += s_rows[q * span + threadIdx.x];
-          ps += s_ps[q * span + threadIdx.x];
+      if (warp == 0)
+        for (int i = lane; i < span; i += 32) {
+          int r = 0;
+          double sum = 0.0;
+          for (int q = 0; q < slices; ++q) {
+            r += s_rows[q * span + i];
+            sum += (double)s_ps[q * span + i];
+          }
+          t += sum * (double)r;
         }
-        t += ps * (double)rows;
-      }
       __syncthreads();
     }
-    t *= (double)p.balance * p.E / (nv * nv * p.k);
   }
-  if (p.zc != 0.f) {
-    double z = 0.0;
-    for (int q = threadIdx.x; q < p.nblk; q += THREADS) z += (double)p.zsum[q];
-    t += (double)p.zc / nv * z;
-  }
+  if (warp) return;
+  double z = 0.0;
+  if (p.zc != 0.f)
+    for (int q = lane; q < p.nblk; q += 32) z += (double)p.zsum[q];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) t += __shfl_down_sync(0xffffffffu, t, d);
-  if (lane == 0) s_loss[warp] = t;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double sum = 0.0;
-    for (int w = 0; w < WARPS; ++w) sum += s_loss[w];
-    *p.loss = (float)sum;
+  for (int d = 16; d > 0; d >>= 1) {
+    t += __shfl_down_sync(0xffffffffu, t, d);
+    z += __shfl_down_sync(0xffffffffu, z, d);
+  }
+  if (lane == 0) {
+    const double nv = l > 0 ? l : 1;
+    *p.loss = (float)((double)p.balance * p.E / (nv * nv * p.k) * t + (double)p.zc / nv * z);
   }
 }
 
@@ -541,7 +552,7 @@ __global__ void __launch_bounds__(BWD_THREADS) route_bwd_kernel(const RouteBwdPa
     float ex[V], all = 0.f, some = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      ex[i] = v[i] > -INFINITY ? expf(v[i] - m) : 0.f;
+      ex[i] = exp_of(v[i] - m);
       all += ex[i];
       some += (chosen >> i) & 1u ? ex[i] : 0.f;
     }

@@ -29,6 +29,7 @@ CASES = [
     DistillConfig(n=257, h=136, vocab=257, top_k=128, name="dense entries"),
     DistillConfig(n=1000, h=512, vocab=8191, top_k=64, teacher=LOGPROBS, vocab_block=2048, name="four blocks"),
     DistillConfig(n=129, h=128, vocab=300, top_k=16, teacher=LOGPROBS, temperature=4.0, grads_dtype=1, name="bf16 grads"),
+    DistillConfig(n=300, h=2560, vocab=5000, top_k=16, vocab_block=1024, name="K in slabs"),
     DistillConfig(n=640, h=384, vocab=3000, top_k=20, vocab_block=768, flags=bpt.BPT_FLAG_DETERMINISTIC, name="fixed order"),
 ]
 
@@ -164,7 +165,7 @@ def test_a_row_of_weight_zero_leaves_no_trace():
 
 
 def test_accumulated_and_repeated():
-    cfg = CASES[7]
+    cfg = CASES[8]
     x, w, ids, v, weight = inputs(cfg, True)
     one, two = run(cfg, x, w, ids, v, weight), run(cfg, x, w, ids, v, weight)
     assert all(torch.equal(a, b) for a, b in zip(one, two))
