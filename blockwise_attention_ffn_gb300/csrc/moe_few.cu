@@ -86,12 +86,12 @@ __global__ void __launch_bounds__(THREADS) few_act_kernel(const FewParams p) {
   if (threadIdx.x == 0) s_e = p.E;
   wait_for_previous();
   let_next_start();
+  const int pair = p.order[r];
   __syncthreads();
   find_expert(p, r, &s_e);
   __syncthreads();
   const int e = s_e;
   if (e == p.E || i0 >= p.f) return;  // f is a multiple of 8: a warp's units are all there or none
-  const int pair = p.order[r];
   const bool some = pair >= 0 && pair < p.pairs;
   const __nv_bfloat16* x = p.x + (int64_t)(some ? pair / p.k : 0) * p.h;
   const __nv_bfloat16* w[4];

@@ -30,6 +30,7 @@ namespace {
 // n = 32768, E = 64, k = 6 choosing and placing took 41 and 20 us with 256
 // threads in 152 blocks.
 constexpr int BWD_THREADS = 256;
+constexpr int MAX_BLOCKS = 152;  // of rows: one on each SM
 template <int V>
 constexpr int choose_threads() {
   return V == 8 ? 1024 : V == 16 ? 512 : 256;
@@ -294,11 +295,19 @@ __device__ void place_rows(const RouteParams& p, int64_t r0, int64_t r1, int b, 
     const int e = e0 + (int)threadIdx.x % span, sl = (int)threadIdx.x / span;
     int before = 0, all = 0;
     if (sl < slices)
-#pragma unroll 16
-      for (int q = sl; q < p.nblk; q += slices) {
-        const int v = p.hist[(int64_t)q * p.E + e];
-        all += v;
-        before += q < b ? v : 0;
+      for (int q0 = sl; q0 < p.nblk; q0 += 10 * slices) {
+        // ten loads at once, so that few blocks are not one latency each
+        int v[10];
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+          const int q = q0 + i * slices;
+          v[i] = q < p.nblk ? p.hist[q * p.E + e] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 10; ++i) {
+          all += v[i];
+          before += q0 + i * slices < b ? v[i] : 0;
+        }
       }
     s_part[0][threadIdx.x] = all;
     s_part[1][threadIdx.x] = before;
@@ -404,10 +413,20 @@ __device__ void finish_losses(const RouteParams& p) {
       int rows = 0;
       float ps = 0.f;
       if (sl < slices)
-#pragma unroll 8
-        for (int q = sl; q < p.nblk; q += slices) {
-          rows += p.hist[(int64_t)q * p.E + e];
-          ps += p.psum[(int64_t)q * p.E + e];
+        for (int q0 = sl; q0 < p.nblk; q0 += 10 * slices) {
+          int v[10];
+          float f[10];
+#pragma unroll
+          for (int i = 0; i < 10; ++i) {
+            const int q = q0 + i * slices;
+            v[i] = q < p.nblk ? p.hist[q * p.E + e] : 0;
+            f[i] = q < p.nblk ? p.psum[q * p.E + e] : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 10; ++i) {
+            rows += v[i];
+            ps += f[i];
+          }
         }
       s_rows[threadIdx.x] = rows;
       s_ps[threadIdx.x] = ps;
@@ -427,8 +446,14 @@ __device__ void finish_losses(const RouteParams& p) {
   }
   if (warp) return;
   double z = 0.0;
-  if (p.zc != 0.f)
-    for (int q = lane; q < p.nblk; q += 32) z += (double)p.zsum[q];
+  if (p.zc != 0.f) {
+    static_assert(MAX_BLOCKS <= 160, "five of them a lane");
+    float f[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) f[i] = lane + 32 * i < p.nblk ? p.zsum[lane + 32 * i] : 0.f;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) z += (double)f[i];
+  }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     t += __shfl_down_sync(0xffffffffu, t, d);
@@ -609,7 +634,7 @@ __global__ void __launch_bounds__(BWD_THREADS) route_bwd_kernel(const RouteBwdPa
 }
 
 // blocks of rows of the two-launch form
-int route_blocks(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(152, (n + 63) / 64)); }
+int route_blocks(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(MAX_BLOCKS, (n + 63) / 64)); }
 
 // Up to this many rows one block does it all in one launch.
 constexpr int64_t ONE_BLOCK_ROWS = 256;
