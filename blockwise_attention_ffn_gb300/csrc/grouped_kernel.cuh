@@ -41,11 +41,14 @@ using gk::BK;
 using gk::BM;
 using gk::NUM_EPI_WARPS;
 constexpr int COPY_WARP = 2 + NUM_EPI_WARPS;  // the first of those that copy rows
-// TN reads the rows' places anew for every block, about 1190 cycles a stage
-// with two warps (8 experts of 4096 x 14336) where the products take 512
+// TN reads the rows' places anew for every block: about 1190 cycles a stage with
+// two warps (8 experts of 4096 x 14336), 860 with four, where the products take
+// 512; eight cost the epilogue its registers and gain nothing.  Of the others NN
+// (the backward's first product: 772 us with two, 720 with four) takes four, NT
+// two (1227 and 1355 us: its epilogue keeps two accumulators' columns).
 template <int FORM>
 constexpr int copy_warps() {
-  return FORM == GROUPED_TN ? 4 : 2;
+  return FORM == GROUPED_NT ? 2 : 4;
 }
 
 struct Params {
