@@ -64,7 +64,7 @@ struct Params {
   int mt, nt;             // TN: tile rows per segment; tile columns
   int band;               // tile rows walked before the next tile column (m fastest)
   const int* order;       // pair at each sorted row, or NULL: row r is row r
-  unsigned long long by_k;  // ceil(2^37 / top_k): pair / top_k = pair * by_k >> 37, exact below 2^29 pairs and 32 choices
+  unsigned long long by_k;  // ceil(2^37 / top_k): pair / top_k = pair * by_k >> 37, exact up to 2^26 pairs and 32 choices
   int pairs;
   void *out, *out2, *out3;
   int out_f32;

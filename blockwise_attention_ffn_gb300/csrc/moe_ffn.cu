@@ -53,7 +53,7 @@ int moe_dims(const bpt_moe_config* c, MoeDims* D) {
   D->debug = (c->flags & BPT_FLAG_DEBUG_CHECKS) != 0;
   D->accum = (c->flags & BPT_FLAG_ACCUM_GRADS) != 0;
   if (D->accum && !D->grads_f32) return BPT_EINVAL;  // a running sum is not kept in 8 bits of mantissa
-  if (D->pairs > (int64_t(1) << 29)) return BPT_EUNSUPPORTED;
+  if (D->pairs > (int64_t(1) << 26)) return BPT_EUNSUPPORTED;
   return BPT_OK;
 }
 

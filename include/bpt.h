@@ -500,7 +500,7 @@ int bpt_clip_grads(int32_t n, const bpt_clip_tensor* t, float max_norm, int32_t 
  *                  BPT_FLAG_DETERMINISTIC (accepted: every sum has a fixed
  *                  order in any case), BPT_FLAG_DEBUG_CHECKS
  * The router's calls read neither h, ffn_dim nor act, the network's calls none
- * of the router's options; all must be valid.  n * k above 2^29 returns
+ * of the router's options; all must be valid.  n * k above 2^26 returns
  * BPT_EUNSUPPORTED.  Outputs, saved and ws that share bytes with an input or
  * one another are refused (BPT_EINVAL). */
 typedef struct {
