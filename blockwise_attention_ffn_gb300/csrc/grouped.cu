@@ -19,13 +19,13 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   // Tiles.  Rows a group: a pair of SMs takes 256 at a time, one SM 128; the
   // pair's product needs two thirds of the shared-memory reads but leaves 128
   // rows idle in a group's last tile on average against 64.
-  // Few rows: the weights' bytes bound the product, and 64-column tiles give
-  // the SMs more units to share them.
-  const bool small = op.form == GROUPED_NT && op.mean_rows <= 64;
+  // Few rows: the weights' bytes bound the product; 64-column tiles of 32 rows
+  // give the SMs more units to share them and a ring of little but weights.
+  const bool small = op.form == GROUPED_NT && op.mean_rows <= 24;
   bool pair = tn ? op.M > BM : op.mean_rows >= 384;
   if (pair && gk::pair_units() <= 0) pair = false;
   const int BN = small ? 64 : dual ? 128 : 256;
-  const int TM = pair ? 2 * BM : BM;
+  const int TM = small ? 32 : pair ? 2 * BM : BM;
   const int BNS = pair ? BN / 2 : BN;
   p.offsets = op.offsets;
   p.groups = op.groups;

@@ -36,7 +36,6 @@
 namespace bpt {
 namespace gg {
 
-using gk::A_BYTES;
 using gk::BK;
 using gk::BM;
 using gk::NUM_EPI_WARPS;
@@ -268,14 +267,26 @@ __device__ __forceinline__ void kept(const __nv_bfloat16* t, long long at, int r
 }
 
 constexpr int PUT_BYTES = 2048;  // shared memory of put_rows, a warp
-// ring stages that fit beside that and the group lists
-template <int STAGE_BYTES>
-constexpr int ring_stages() {
-  return 200 * 1024 / STAGE_BYTES > 8 ? 8 : 200 * 1024 / STAGE_BYTES;
+// Few rows a group (64-column tiles): the weights' bytes bound the product and a
+// stage's hand-overs, some 600 cycles, its rate.  So a stage holds two blocks of
+// 64 K, and 32 rows of A at most: the product's other 96 rows are whatever lies
+// behind them in the ring (in bounds; accumulator rows that are never stored).
+template <int BN>
+constexpr int k_blocks() {  // of a stage
+  return BN == 64 ? 2 : 1;
+}
+template <int BN>
+constexpr int a_rows() {  // staged by a CTA
+  return BN == 64 ? 32 : BM;
 }
 template <int BN, bool DUAL, bool PAIR>
 constexpr int stage_bytes() {
-  return A_BYTES + (DUAL ? 2 : 1) * (PAIR ? BN / 2 : BN) * BK * 2;
+  return k_blocks<BN>() * (a_rows<BN>() + (DUAL ? 2 : 1) * (PAIR ? BN / 2 : BN)) * BK * 2;
+}
+// ring stages that fit beside put_rows' memory and the group lists
+template <int STAGE_BYTES>
+constexpr int ring_stages() {
+  return 198 * 1024 / STAGE_BYTES > 8 ? 8 : 198 * 1024 / STAGE_BYTES;
 }
 template <int BN, bool DUAL, bool PAIR>
 constexpr int smem_bytes() {
@@ -308,8 +319,11 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
   constexpr uint32_t TMEM_COLS = 2 * ACC_COLS;
   static_assert(TMEM_COLS <= 512 && TMEM_COLS >= 32 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "two accumulators");
   static_assert(BN % 64 == 0 && (!DUAL || FORM == GROUPED_NT), "tile width");
-  constexpr int TM = PAIR ? 2 * BM : BM;
-  constexpr uint32_t IDESC = idesc_bf16(TM, BN, TN, B_MN);
+  constexpr int KB = k_blocks<BN>(), A_ROWS = a_rows<BN>();
+  constexpr int A_STAGE = KB * A_ROWS * BK * 2, B_BLOCK = (DUAL ? 2 : 1) * BNS * BK * 2;
+  static_assert(BN != 64 || (FORM == GROUPED_NT && AG && !PAIR), "few rows");
+  constexpr int TM = PAIR ? 2 * BM : A_ROWS;
+  constexpr uint32_t IDESC = idesc_bf16(PAIR ? 2 * BM : BM, BN, TN, B_MN);
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -368,7 +382,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
   const uint32_t tmem = *tmem_holder;
   const int nunits = s_unit[p.groups];
   // k-tiles of a unit
-  auto k_tiles = [&](const Place& at) { return TN ? (at.cnt + BK - 1) / BK : p.segs * p.nkt; };
+  auto k_tiles = [&](const Place& at) { return TN ? (at.cnt + BK - 1) / BK : p.segs * ((p.nkt + KB - 1) / KB); };
 
   if (warp == 0) {
     if (lane == 0) {
@@ -409,16 +423,19 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
             break;
           }
           const uint32_t sa = smem_base + s * STAGE_BYTES;
-          const uint32_t sb = sa + A_BYTES;
+          const uint32_t sb = sa + A_STAGE;
           const uint32_t fb = full0 + 8u * (uint32_t)s;
           if constexpr (!TN) {
             const int seg = FORM == GROUPED_NN && kt >= p.nkt ? 1 : 0;
-            const int kx = (kt - seg * p.nkt) * BK;
-            if (rank == 0) mbar_expect_tx(&full[s], (PAIR ? 2 : 1) * (STAGE_BYTES - (AG ? A_BYTES : 0)));
+            const int kx = (kt - seg * p.nkt) * (KB * BK);
+            if (rank == 0) mbar_expect_tx(&full[s], (PAIR ? 2 : 1) * (STAGE_BYTES - (AG ? A_STAGE : 0)));
             if constexpr (!AG) load2(sa, &p.map_a[seg], fb, kx, at.lo + ma);
             if constexpr (FORM == GROUPED_NT) {
-              load3(sb, &p.map_b[0], fb, kx, nbs, at.e);
-              if constexpr (DUAL) load3(sb + BNS * BK * 2, &p.map_b[1], fb, kx, nbs, at.e);
+#pragma unroll
+              for (int i = 0; i < KB; ++i) {
+                load3(sb + i * B_BLOCK, &p.map_b[0], fb, kx + i * BK, nbs, at.e);
+                if constexpr (DUAL) load3(sb + i * B_BLOCK + BNS * BK * 2, &p.map_b[1], fb, kx + i * BK, nbs, at.e);
+              }
             } else {
 #pragma unroll
               for (int c = 0; c < BNS / 64; ++c) load3(sb + c * 8192, &p.map_b[seg], fb, nbs + c * 64, kx, at.e);
@@ -426,7 +443,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
           } else {
             const bool whole = (kt + 1) * BK <= at.cnt;
             const int y = at.lo + kt * BK;
-            const uint32_t bytes = whole ? (AG ? 0 : A_BYTES) + (BG ? 0 : STAGE_BYTES - A_BYTES) : 0;
+            const uint32_t bytes = whole ? (AG ? 0 : A_STAGE) + (BG ? 0 : STAGE_BYTES - A_STAGE) : 0;
             if (rank == 0) mbar_expect_tx(&full[s], (PAIR ? 2 : 1) * bytes);
             if (!AG && whole) {
               load2(sa, &p.map_a[at.seg], fb, ma, y);
@@ -481,7 +498,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       const int nk = k_tiles(at);
       if constexpr (!TN) {
         // lines w * PER + 4 i + lane / 8 of the CTA's rows
-        constexpr int PER = BM / COPY_WARPS;
+        constexpr int PER = A_ROWS / COPY_WARPS;
         const int r0 = at.m0 + (int)rank * BM + w * PER + (lane >> 3);
         int idx[PER / 4];
 #pragma unroll
@@ -497,15 +514,18 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
             break;
           }
           const int seg = FORM == GROUPED_NN && kt >= p.nkt ? 1 : 0;
-          const int x = (kt - seg * p.nkt) * BK + col;
-          const bool in = x < p.a_cols;
-          const __nv_bfloat16* src = p.a[seg] + (in ? x : 0);
-          const uint32_t sa = smem_base + (it % STAGES) * STAGE_BYTES;
 #pragma unroll
-          for (int i = 0; i < PER / 4; ++i) {
-            if (i < live) {
-              const uint32_t line = line0 + 4 * i;
-              copy16(sa + line * 128 + ((((lane & 7) ^ line) & 7) << 4), src + (long long)max(idx[i], 0) * p.a_cols, in && idx[i] >= 0);
+          for (int kb = 0; kb < KB; ++kb) {
+            const int x = ((kt - seg * p.nkt) * KB + kb) * BK + col;
+            const bool in = x < p.a_cols;
+            const __nv_bfloat16* src = p.a[seg] + (in ? x : 0);
+            const uint32_t sa = smem_base + (it % STAGES) * STAGE_BYTES + kb * (A_ROWS * BK * 2);
+#pragma unroll
+            for (int i = 0; i < PER / 4; ++i) {
+              if (i < live) {
+                const uint32_t line = line0 + 4 * i;
+                copy16(sa + line * 128 + ((((lane & 7) ^ line) & 7) << 4), src + (long long)max(idx[i], 0) * p.a_cols, in && idx[i] >= 0);
+              }
             }
           }
           next();
@@ -554,7 +574,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
               break;
             }
             const uint32_t sa = smem_base + (it % STAGES) * STAGE_BYTES;
-            const uint32_t sb = sa + A_BYTES;
+            const uint32_t sb = sa + A_STAGE;
             const bool whole = (kt + 1) * BK <= at.cnt;
             if constexpr (AG || BG) {
               int rows[LINES];
@@ -618,16 +638,18 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
           if constexpr (COPY) fence_proxy_async_smem();  // the copies are read by the tensor core
           tc_fence_after();
           const uint32_t sa = smem_base + s * STAGE_BYTES;
-          const uint32_t sb = sa + A_BYTES;
+          const uint32_t sb = sa + A_STAGE;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = TN ? sdesc(sa + kk * 2048, 8192, 1024, 2) : sdesc(sa + kk * 32, 16, 1024, 2);
-            const uint64_t bd = B_MN ? sdesc(sb + kk * 2048, 8192, 1024, 2) : sdesc(sb + kk * 32, 16, 1024, 2);
+          for (int kk = 0; kk < KB * BK / 16; ++kk) {
+            const uint32_t ka = sa + (kk / 4) * (A_ROWS * BK * 2), kb = sb + (kk / 4) * B_BLOCK;  // the block of 64
+            const int in = kk % 4;
+            const uint64_t ad = TN ? sdesc(ka + in * 2048, 8192, 1024, 2) : sdesc(ka + in * 32, 16, 1024, 2);
+            const uint64_t bd = B_MN ? sdesc(kb + in * 2048, 8192, 1024, 2) : sdesc(kb + in * 32, 16, 1024, 2);
             const bool accum = kt != 0 || kk != 0;
             if constexpr (PAIR) umma_bf16_pair_w(d, ad, bd, IDESC, accum);
             else umma_bf16_w(d, ad, bd, IDESC, accum);
             if (DUAL) {
-              const uint64_t bd2 = sdesc(sb + BNS * BK * 2 + kk * 32, 16, 1024, 2);
+              const uint64_t bd2 = sdesc(kb + BNS * BK * 2 + in * 32, 16, 1024, 2);
               if constexpr (PAIR) umma_bf16_pair_w(d + BN, ad, bd2, IDESC, accum);
               else umma_bf16_w(d + BN, ad, bd2, IDESC, accum);
             }
@@ -683,7 +705,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       const bool none = k_tiles(at) == 0;
       const int acc = tc & 1;
       const int m0 = at.m0 + (int)rank * BM + q * 32;  // the warp's first row in the group (TN: of the matrix)
-      const int rows = max(0, min(32, (TN ? p.M : at.cnt) - m0));
+      const int rows = TM == 32 && q ? 0 : max(0, min(32, (TN ? p.M : at.cnt) - m0));
       const long long first = TN ? (long long)at.e * p.M + m0 : (long long)at.lo + m0;
       void* out = TN && at.seg ? p.out2 : p.out;
       const bool mine = lane < rows;
@@ -726,7 +748,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
         }
       };
       char* to = reinterpret_cast<char*>(out) + (first * p.N + n0) * (EPI == GROUPED_STORE && p.out_f32 ? 4 : 2);
-      const int left = p.N - n0;  // columns
+      const int left = rows ? p.N - n0 : 0;  // columns to store
       if constexpr (EPI == GROUPED_STORE) {
         if (p.out_f32) {
 #pragma unroll 1

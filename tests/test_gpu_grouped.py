@@ -28,7 +28,8 @@ CASES = [
     (1000, 256, 64, [128, 256, 1, 0, 300, 17], 0),
     (1500, 328, 1000, [700, 0, 513, 255], 3),
     (4000, 776, 264, [3000, 900], 11),   # 256-row tiles of a pair of SMs
-    (2600, 1288, 72, [40] * 64, 0),      # 64-column tiles
+    (2600, 1288, 72, [40] * 64, 0),
+    (400, 328, 456, [5] * 36 + [70, 0, 33, 97], 4),  # 32-row tiles of 64 columns
     (300, 24, 16, [1] * 300, 0),
 ]
 

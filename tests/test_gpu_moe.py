@@ -215,6 +215,8 @@ FFN = [
     (3, 1000, 520, 64, 6, 1, True),
     (8, 2056, 1032, 128, 8, 2, False),
     (70, 256, 200, 12, 2, 1, True),
+    (90, 392, 136, 16, 3, 2, True),     # 32-row tiles, several an expert
+    (90, 136, 392, 16, 3, 0, False),
     (300, 136, 264, 4, 2, 2, True),     # one-SM tiles
     (333, 512, 328, 3, 3, 0, False),
     (1300, 72, 520, 2, 1, 2, False),    # 256-row tiles
