@@ -19,7 +19,8 @@
 //     lanes a 128-byte line, the swizzle applied by hand), so no copy in the
 //     groups' order is ever made.  Lines behind the group's last row are not
 //     copied: what their shared memory holds reaches only accumulator rows
-//     that are never stored.  (TMA's own four-row gathers were taken first:
+//     that are never stored.  The copies complete a barrier of their CTA; a
+//     pair's second CTA passes word of it on.  (TMA's own four-row gathers were taken first:
 //     an instruction each, they fed a stage in about 1000 cycles where the
 //     products take 256: 458 TFLOP/s on the gate and up products of 8 experts
 //     of 4096 x 14336, 4096 positions.)
