@@ -14,16 +14,15 @@
 // Warp roles, ring and accumulators are those of gemm_kernel.cuh (a producer
 // warp, an issuing warp, eight epilogue warps; two accumulators; one SM or a
 // pair of SMs per tile).  What is different:
-//   - Rows are gathered on the way in: two more warps copy them, 16 bytes a
+//   - Rows are gathered on the way in: two or four more warps copy them, 16 bytes a
 //     lane, from where the router left them into the ring (cp.async, eight
 //     lanes a 128-byte line, the swizzle applied by hand), so no copy in the
 //     groups' order is ever made.  Lines behind the group's last row are not
 //     copied: what their shared memory holds reaches only accumulator rows
 //     that are never stored.  The copies complete a barrier of their CTA; a
-//     pair's second CTA passes word of it on.  (TMA's own four-row gathers were taken first:
-//     an instruction each, they fed a stage in about 1000 cycles where the
-//     products take 256: 458 TFLOP/s on the gate and up products of 8 experts
-//     of 4096 x 14336, 4096 positions.)
+//     pair's second CTA passes word of it on.  (TMA's own four-row gathers, an
+//     instruction for each quad of rows, reached 458 TFLOP/s on the gate and up
+//     products of 8 experts of 4096 x 14336, 4096 positions; the copies 1570.)
 //   - TN runs over a group's rows as K.  The last, partial block of 64 rows
 //     is copied by those warps too, with zeros behind the group's end: what
 //     lies there, a NaN even, stays out.
@@ -200,10 +199,9 @@ __device__ __forceinline__ void fast_gelu(float z, int act, float& g, float& d) 
 
 // A warp's 32 output rows, one a lane in registers, to global memory by whole
 // 64- or 128-byte pieces of a row, through the warp's 2 KB of shared memory.
-// (Stored straight from the registers, 32 bytes of 32 rows at a time, the
-// stores took as long as the products of 1024 rows: without them the
-// weight gradients of 8 experts of 4096 x 14336 ran at 1680 TFLOP/s, with them
-// at 1330.)  P 16-byte words a row: 4, all rows at once, or 8, 16 rows at a
+// (Stored straight from the registers, 32 bytes of 32 rows at a time, the fp32
+// gradient of 16 matrices of 2048 x 2560 over 14336 rows took 155 us, this way
+// 141, and the GeLU product of 12 experts of 1000 x 2744 116 and 84.)  P 16-byte words a row: 4, all rows at once, or 8, 16 rows at a
 // time.  The words' places are swapped so that neither the rows' writes nor
 // the lines' reads meet in a bank.  to: the first row's first byte; ld: bytes
 // from row to row; rows, words: how many of them there are.

@@ -31,6 +31,7 @@ CASES = [
     (2600, 1288, 72, [40] * 64, 0),
     (400, 328, 456, [5] * 36 + [70, 0, 33, 97], 4),  # 32-row tiles of 64 columns
     (300, 24, 16, [1] * 300, 0),
+    (1100, 16, 24, [1] * 1000 + [0] * 20 + [3, 0, 90, 0], 3),
 ]
 
 

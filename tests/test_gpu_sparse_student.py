@@ -154,6 +154,50 @@ def test_repeats_captures_and_streams():
     assert bpt.bpt_last_device_error() == (bpt.BPT_OK, 0)
 
 
+def test_debug_checks():
+    """BPT_FLAG_DEBUG_CHECKS: the same results, every pointer looked at first."""
+    t = Step(200, 64, 136, 8, 2, 500, 5)
+    t.run()
+    torch.cuda.synchronize()
+    want = t.results()
+    f = bpt.BPT_FLAG_DEBUG_CHECKS
+    t.moe, t.kd, t.gate = t.moe.with_(flags=f), t.kd.with_(flags=t.kd.flags | f), t.gate.with_(flags=f)
+    t.run()
+    assert same(t.results(), want)
+    short = t.saved[:1024]  # a device tensor, but the call keeps more than its allocation may hold
+    with pytest.raises(bpt.BptError):
+        bpt.bpt_moe_ffn_fwd(t.moe, t.route, t.x, t.w1, t.w3, t.w2, t.y, short, t.ws)
+
+
+@pytest.mark.parametrize("n,E", [(90, 16), (1300, 2), (3, 64)])
+def test_padded_positions_leave_no_trace(n, E):
+    """Positions without a route may hold anything, NaN too, in x and in dy."""
+    cfg = MoeConfig(n=n, h=136, ffn_dim=200, n_experts=E, top_k=2)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    rnd = lambda *s, sc=1.0: (sc * torch.randn(*s, generator=g, device="cuda")).bfloat16()  # noqa: E731
+    z = torch.randn(n, E, generator=g, device="cuda")
+    gone = torch.arange(n, device="cuda") % 3 == 1
+    z[gone] = -math.inf
+    x, dy, w1, w3, w2 = rnd(n, 136), rnd(n, 136), rnd(E, 200, 136, sc=0.1), rnd(E, 200, 136, sc=0.1), rnd(E, 136, 200, sc=0.1)
+    r = bpt.alloc_moe_route(cfg)
+    ws = bpt.alloc_bytes(max(bpt.bpt_moe_route_workspace_bytes(cfg), *(bpt.bpt_moe_ffn_workspace_bytes(cfg, p) for p in (0, 1))))
+    bpt.bpt_moe_route_fwd(cfg, z, r, None, ws)
+    saved = bpt.alloc_bytes(bpt.bpt_moe_saved_bytes(cfg))
+    runs = []
+    for fill in (0.0, float("nan")):
+        x[gone] = dy[gone] = fill
+        ws.fill_(255), saved.fill_(255)
+        y, plain, dx, dwt = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty(n, 2, device="cuda")
+        dm = [torch.empty(m.shape, device="cuda") for m in (w1, w3, w2)]
+        bpt.bpt_moe_ffn_fwd(cfg, r, x, w1, w3, w2, plain, None, ws)
+        bpt.bpt_moe_ffn_fwd(cfg, r, x, w1, w3, w2, y, saved, ws)
+        bpt.bpt_moe_ffn_bwd(cfg, r, x, w1, w3, w2, saved, dy, dx, dwt, *dm, ws)
+        torch.cuda.synchronize()
+        runs.append([y, plain, dx, dwt, *dm])
+    assert all(torch.equal(a, b) and a.isfinite().all() for a, b in zip(*runs))
+    assert bool((runs[0][0][gone] == 0).all()) and bool((runs[0][2][gone] == 0).all())
+
+
 def test_offsets_beyond_31_bits():
     """200000 rows of a network 16384 wide: 3.3e9 values in every tensor between
     the products."""
