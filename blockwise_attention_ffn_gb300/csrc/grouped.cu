@@ -41,7 +41,6 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   p.out3 = op.out3;
   p.out_f32 = op.out_f32;
   p.beta = op.beta;
-  p.act = op.act;
   p.aux = reinterpret_cast<const __nv_bfloat16*>(op.aux);
   p.aux2 = reinterpret_cast<const __nv_bfloat16*>(op.aux2);
   p.row_weight = op.row_weight;
@@ -88,8 +87,8 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   // band's rows in L2 while the other operand streams through once a band
   p.band = 4096 / TM;
   ProfScope prof(PROF_GEMM, 2.0 * (double)op.rows * (double)op.N * (double)(tn ? op.M * p.segs : op.K * p.segs) * (dual ? 2 : 1), 0.0, st);
-  if (op.form == GROUPED_NT) return launch_nt(p, op.epi, op.a_gather || small, dual, pair, small, units, st);
-  if (op.form == GROUPED_NN) return launch_nn(p, op.epi, pair, units, st);
+  if (op.form == GROUPED_NT) return launch_nt(p, op.epi, op.act, op.a_gather || small, pair, small, units, st);
+  if (op.form == GROUPED_NN) return launch_nn(p, op.epi, op.act, pair, units, st);
   return launch_tn(p, op.a_gather, op.b_gather, pair, units, st);
 }
 

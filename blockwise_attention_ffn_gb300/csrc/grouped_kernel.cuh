@@ -68,7 +68,6 @@ struct Params {
   void *out, *out2, *out3;
   int out_f32;
   float beta;
-  int act;
   const __nv_bfloat16 *aux, *aux2;
   const void* row_weight;
   int row_weight_f32;
@@ -186,8 +185,9 @@ __device__ __forceinline__ float fast_sigmoid(float z) {
 
 // GeLU and its slope: z cdf(z), cdf + z pdf(z), or the tanh form as z s with
 // s = sigmoid(2 c (z + 0.044715 z^3)), c = sqrt(2 / pi).
-__device__ __forceinline__ void fast_gelu(float z, int act, float& g, float& d) {
-  if (act == BPT_ACT_GELU_ERF) {
+template <int ACT>
+__device__ __forceinline__ void fast_gelu(float z, float& g, float& d) {
+  if constexpr (ACT == BPT_ACT_GELU_ERF) {
     gk::gelu_and_grad_f(z, 0, g, d);
   } else {
     const float c2 = 1.5957691216057308f, z2 = z * z;
@@ -305,8 +305,12 @@ constexpr int threads() {
   return 32 * (2 + NUM_EPI_WARPS + (copies<FORM, AG>() ? copy_warps<FORM>() : 0));
 }
 
-template <int FORM, int EPI, int BN, bool AG, bool BG, bool DUAL, bool PAIR>
+// ACT: the activation of GROUPED_ACT and GROUPED_ACT_BWD (a branch for each
+// value otherwise; 0 elsewhere).
+template <int FORM, int EPI, int ACT, int BN, bool AG, bool BG, bool DUAL, bool PAIR>
 __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const __grid_constant__ Params p) {
+  constexpr bool GATED = ACT == BPT_ACT_SWIGLU;
+  static_assert(EPI != GROUPED_ACT || GATED == DUAL, "gate and up");
   constexpr bool TN = FORM == GROUPED_TN;
   constexpr bool B_MN = FORM != GROUPED_NT;
   constexpr bool COPY = copies<FORM, AG>();
@@ -710,13 +714,13 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       const bool mine = lane < rows;
       const int n0 = at.n0 + half * EPI_COLS;  // the warp's first column
       float w = 0.f, dot = 0.f;
-      uint32_t s0[EPI == GROUPED_ACT_BWD ? 16 : 1], s1[EPI == GROUPED_ACT_BWD ? 16 : 1];
+      uint32_t s0[EPI == GROUPED_ACT_BWD ? 16 : 1], s1[EPI == GROUPED_ACT_BWD && GATED ? 16 : 1];
       auto fetch = [&](int c) {
         const int words = (p.N - n0 - c * 32) / 8;
         if (mine && words > 0) {
           const long long k = kept_at(p, first, rows, n0 / 32 + c, lane);
           kept(p.aux, k, rows, words, s0);
-          if (p.act == BPT_ACT_SWIGLU) kept(p.aux2, k, rows, words, s1);
+          if constexpr (GATED) kept(p.aux2, k, rows, words, s1);
         }
       };
       if constexpr (EPI == GROUPED_ACT_BWD) {
@@ -806,7 +810,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
                   y[i] = z * fast_sigmoid(z) * __uint_as_float(u[2 * j + i]);
                 } else {
                   float slope;
-                  fast_gelu(z, p.act, y[i], slope);
+                  fast_gelu<ACT>(z, y[i], slope);
                 }
               }
               v[16 * h + j] = pack_bf16(y[0], y[1]);
@@ -819,42 +823,42 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
         // and its slopes are taken again from it in fp32 and rounded once
 #pragma unroll 1
         for (int c = 0; c < EPI_COLS && c < left; c += 32) {
-          uint32_t r[32], v[16], dv[16], aw[16];
+          uint32_t r[32], v[16], dv[GATED ? 16 : 1], aw[16];
           read(c, r);
           const int words = min(4, (left - c) / 8);
+          // columns past N are zeros in r and in what was kept; rows past the
+          // group's end hold anything and are not stored
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             float x[2], y[2], z[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float a = mine && j < 4 * words ? __uint_as_float(r[2 * j + i]) : 0.f;
+              const float a = __uint_as_float(r[2 * j + i]);
               const float g = i ? bf16_hi(s0[j]) : bf16_lo(s0[j]);
               const float wa = w * a;
-              if (p.act == BPT_ACT_SWIGLU) {
+              float act;
+              if constexpr (GATED) {
                 const float u = i ? bf16_hi(s1[j]) : bf16_lo(s1[j]);
                 const float sg = fast_sigmoid(g), si = g * sg;  // silu(g)
-                const float act = si * u;
-                dot = j < 4 * words ? fmaf(a, act, dot) : dot;
-                x[i] = wa * u * (sg + si * (1.f - sg));
+                act = si * u;
+                x[i] = wa * u * fmaf(si, 1.f - sg, sg);
                 y[i] = wa * si;
-                z[i] = w * act;
               } else {
-                float act, slope;
-                fast_gelu(g, p.act, act, slope);
-                dot = j < 4 * words ? fmaf(a, act, dot) : dot;
+                float slope;
+                fast_gelu<ACT>(g, act, slope);
                 x[i] = wa * slope;
-                y[i] = 0.f;
-                z[i] = w * act;
               }
+              dot = fmaf(a, act, dot);
+              z[i] = w * act;
             }
             v[j] = pack_bf16(x[0], x[1]);
-            dv[j] = pack_bf16(y[0], y[1]);
+            if constexpr (GATED) dv[j] = pack_bf16(y[0], y[1]);
             aw[j] = pack_bf16(z[0], z[1]);
           }
           if (c + 32 < EPI_COLS) fetch(c / 32 + 1);
           const long long ld = p.N * 2ll;
           put_rows<4, false>(v, stage, to + c * 2, ld, rows, words, 0.f);
-          if (p.act == BPT_ACT_SWIGLU)
+          if constexpr (GATED)
             put_rows<4, false>(dv, stage, reinterpret_cast<char*>(p.out2) + (first * p.N + n0 + c) * 2, ld, rows, words, 0.f);
           put_rows<4, false>(aw, stage, reinterpret_cast<char*>(p.out3) + (first * p.N + n0 + c) * 2, ld, rows, words, 0.f);
         }
@@ -884,10 +888,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
   }
 }
 
-template <int FORM, int EPI, int BN, bool AG, bool BG, bool DUAL, bool PAIR>
+template <int FORM, int EPI, int ACT, int BN, bool AG, bool BG, bool DUAL, bool PAIR>
 int launch(Params& p, int64_t units, cudaStream_t st) {
   constexpr int SMEM = smem_bytes<BN, DUAL, PAIR>();
-  auto kern = grouped_kernel<FORM, EPI, BN, AG, BG, DUAL, PAIR>;
+  auto kern = grouped_kernel<FORM, EPI, ACT, BN, AG, BG, DUAL, PAIR>;
   static std::atomic<uint64_t> attr{0};
   if (smem_limit_once(reinterpret_cast<const void*>(kern), SMEM, &attr)) return 3;
   int slots;
@@ -904,8 +908,8 @@ int launch(Params& p, int64_t units, cudaStream_t st) {
 
 // One translation unit per form (they compile in parallel); `small`: 64
 // columns a tile, `pair`: a pair of SMs a tile.
-int launch_nt(Params& p, int epi, bool gather, bool dual, bool pair, bool small, int64_t units, cudaStream_t st);
-int launch_nn(Params& p, int epi, bool pair, int64_t units, cudaStream_t st);
+int launch_nt(Params& p, int epi, int act, bool gather, bool pair, bool small, int64_t units, cudaStream_t st);
+int launch_nn(Params& p, int epi, int act, bool pair, int64_t units, cudaStream_t st);
 int launch_tn(Params& p, bool a_gather, bool b_gather, bool pair, int64_t units, cudaStream_t st);
 
 }  // namespace gg

@@ -5,14 +5,27 @@
 namespace bpt {
 namespace gg {
 
-int launch_nn(Params& p, int epi, bool pair, int64_t units, cudaStream_t st) {
-  constexpr int NN = GROUPED_NN;
-  if (epi == GROUPED_ACT_BWD)
-    return pair ? launch<NN, GROUPED_ACT_BWD, 256, true, false, false, true>(p, units, st)
-                : launch<NN, GROUPED_ACT_BWD, 256, true, false, false, false>(p, units, st);
+namespace {
+
+template <int ACT>
+int launch_act_bwd(Params& p, bool pair, int64_t units, cudaStream_t st) {
+  constexpr int NN = GROUPED_NN, EPI = GROUPED_ACT_BWD;
+  return pair ? launch<NN, EPI, ACT, 256, true, false, false, true>(p, units, st)
+              : launch<NN, EPI, ACT, 256, true, false, false, false>(p, units, st);
+}
+
+}  // namespace
+
+int launch_nn(Params& p, int epi, int act, bool pair, int64_t units, cudaStream_t st) {
+  constexpr int NN = GROUPED_NN, STORE = GROUPED_STORE;
+  if (epi == GROUPED_ACT_BWD) {
+    if (act == BPT_ACT_SWIGLU) return launch_act_bwd<BPT_ACT_SWIGLU>(p, pair, units, st);
+    if (act == BPT_ACT_GELU_ERF) return launch_act_bwd<BPT_ACT_GELU_ERF>(p, pair, units, st);
+    return launch_act_bwd<BPT_ACT_GELU_TANH>(p, pair, units, st);
+  }
   if (epi != GROUPED_STORE) return 1;
-  return pair ? launch<NN, GROUPED_STORE, 256, false, false, false, true>(p, units, st)
-              : launch<NN, GROUPED_STORE, 256, false, false, false, false>(p, units, st);
+  return pair ? launch<NN, STORE, 0, 256, false, false, false, true>(p, units, st)
+              : launch<NN, STORE, 0, 256, false, false, false, false>(p, units, st);
 }
 
 }  // namespace gg

@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
   }
 }
 
-// Rows' log-sum-exp from their pairs, 32 rows a block with the parts in 8
+// Rows' log-sum-exp from their pairs, 32 rows a block with the parts in 32
 // slices, and their terms of the loss.
 struct RowParams {
   const float2* part;
@@ -261,7 +261,7 @@ struct RowParams {
   Saved s;
   double* term;
 };
-constexpr int ROW_SLICES = 8;
+constexpr int ROW_SLICES = 32;  // 15 us for 4001 rows of 394 pairs with 8
 __global__ void __launch_bounds__(32 * ROW_SLICES) rows_kernel(const RowParams q) {
   __shared__ float s_m[ROW_SLICES][32], s_l[ROW_SLICES][32], s_dot[ROW_SLICES][32];
   const int lane = lane_id(), sl = warp_id();

@@ -83,6 +83,7 @@ struct CombineParams {
 
 constexpr int CT = 128;
 
+template <int ROWS>
 __global__ void __launch_bounds__(CT) combine_kernel(const CombineParams p) {
   wait_for_previous();
   let_next_start();
@@ -95,23 +96,29 @@ __global__ void __launch_bounds__(CT) combine_kernel(const CombineParams p) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) s[q] = 0.f;
     const int* slot = p.slot + t * p.k;
-    for (int j0 = 0; j0 < p.k; j0 += 4) {
-      // four rows on their way at once
-      uint4 u[4];
-      float w[4];
+    for (int j0 = 0; j0 < p.k; j0 += ROWS) {
+      // ROWS rows on their way at once
+      int at[ROWS];
+      uint4 u[ROWS];
+      float w[ROWS];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = j0 + j < p.k ? slot[j0 + j] : -1;
-        const bool some = at >= 0 && at < p.pairs;
-        u[j] = some ? reinterpret_cast<const uint4*>(p.rows)[(int64_t)at * p.h8 + c] : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < ROWS; ++j) at[j] = j0 + j < p.k ? slot[j0 + j] : -1;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j) {
+        const bool some = at[j] >= 0 && at[j] < p.pairs;
+        // without a row: the first one, not used
+        asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(u[j].x), "=r"(u[j].y), "=r"(u[j].z), "=r"(u[j].w)
+                     : "l"(reinterpret_cast<const uint4*>(p.rows) + (some ? at[j] : 0) * (int64_t)p.h8 + c));
         w[j] = !some         ? 0.f
                : !p.weight   ? 1.f
                : p.weight_f32 ? reinterpret_cast<const float*>(p.weight)[t * p.k + j0 + j]
                               : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.weight)[t * p.k + j0 + j]);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t v[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+      for (int j = 0; j < ROWS; ++j) {
+        const bool some = at[j] >= 0 && at[j] < p.pairs;
+        const uint32_t v[4] = {some ? u[j].x : 0u, some ? u[j].y : 0u, some ? u[j].z : 0u, some ? u[j].w : 0u};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           s[2 * q] = fmaf(w[j], bf16_lo(v[q]), s[2 * q]);
@@ -156,7 +163,8 @@ int combine(const MoeDims& D, const void* rows, const int* slot, const void* wei
   const int64_t grid = p.blocks + (part ? (D.pairs + CT - 1) / CT : 0);
   if (grid > INT32_MAX) return BPT_EUNSUPPORTED;
   ProfScope prof(PROF_MISC, 0.0, 2.0 * (double)(D.pairs + D.n) * D.h, st);
-  return launch_dependent(combine_kernel, (int)grid, 1, dim3(CT), 0, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
+  auto kern = D.k <= 2 ? combine_kernel<2> : D.k <= 4 ? combine_kernel<4> : combine_kernel<8>;
+  return launch_dependent(kern, (int)grid, 1, dim3(CT), 0, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
 }
 
 struct Planner {
