@@ -118,20 +118,61 @@ __device__ __forceinline__ void lay_out(const Params& p, int* s_unit, int* s_lo,
   if (lane == 0) s_unit[0] = 0;
 }
 
+// TN: the groups by falling row count, equal ones in their order, by all
+// threads of the block after lay_out (whose lists they reorder; s_id: the
+// group at each place).  A unit's work is its group's rows, and the units go
+// round the CTAs in snakes (unit_of below), so heavy and light ones even out.
+constexpr int SORT_MOST = (GROUPED_MAX_GROUPS + 319) / 320;  // groups a thread, of at least 320
+__device__ __forceinline__ void sort_groups(const Params& p, int* s_lo, int* s_cnt, int* s_id) {
+  int lo[SORT_MOST], cnt[SORT_MOST], rank[SORT_MOST];
+#pragma unroll
+  for (int i = 0; i < SORT_MOST; ++i) {
+    const int e = (int)threadIdx.x + i * (int)blockDim.x;
+    rank[i] = 0;
+    if (e < p.groups) {
+      lo[i] = s_lo[e];
+      cnt[i] = s_cnt[e];
+      for (int o = 0; o < p.groups; ++o) rank[i] += s_cnt[o] > cnt[i] || (s_cnt[o] == cnt[i] && o < e);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < SORT_MOST; ++i) {
+    const int e = (int)threadIdx.x + i * (int)blockDim.x;
+    if (e < p.groups) {
+      s_lo[rank[i]] = lo[i];
+      s_cnt[rank[i]] = cnt[i];
+      s_id[rank[i]] = e;
+    }
+  }
+}
+
 // A work unit's place: group, first row of the tile in the group (TN: of the
 // matrix), first column, segment of M (TN).
 struct Place {
   int e, lo, cnt, m0, n0, seg;
 };
 template <bool TN, int TM, int BN>
-__device__ __forceinline__ void place(const Params& p, int unit, const int* s_unit, const int* s_lo, const int* s_cnt, Place& at) {
-  int e = at.e;  // units come in rising order
-  while (unit >= s_unit[e + 1]) ++e;
-  at.e = e;
-  at.lo = s_lo[e];
-  at.cnt = s_cnt[e];
-  const int local = unit - s_unit[e];
-  const int mt = TN ? p.segs * p.mt : (at.cnt + TM - 1) / TM;
+__device__ __forceinline__ void place(const Params& p, int unit, const int* s_unit, const int* s_lo, const int* s_cnt, const int* s_id,
+                                      Place& at) {
+  int local, mt;
+  if constexpr (TN) {
+    // every group has the same units; the groups with the most rows first
+    mt = p.segs * p.mt;
+    const int g = unit / (mt * p.nt);
+    at.e = s_id[g];
+    at.lo = s_lo[g];
+    at.cnt = s_cnt[g];
+    local = unit - g * (mt * p.nt);
+  } else {
+    int e = at.e;  // units come in rising order
+    while (unit >= s_unit[e + 1]) ++e;
+    at.e = e;
+    at.lo = s_lo[e];
+    at.cnt = s_cnt[e];
+    local = unit - s_unit[e];
+    mt = (at.cnt + TM - 1) / TM;
+  }
   const int per = p.band * p.nt;
   const int g = local / per, r = local - g * per;
   const int gs = min(p.band, mt - g * p.band);
@@ -290,7 +331,7 @@ constexpr int ring_stages() {
 template <int BN, bool DUAL, bool PAIR>
 constexpr int smem_bytes() {
   return ring_stages<stage_bytes<BN, DUAL, PAIR>()>() * stage_bytes<BN, DUAL, PAIR>() + NUM_EPI_WARPS * PUT_BYTES + 1024 + 256 +
-         (3 * GROUPED_MAX_GROUPS + 4) * 4;
+         (4 * GROUPED_MAX_GROUPS + 4) * 4;
 }
 
 // BN: tile width.  AG, BG: rows of A (TN: of A, of B) gathered.  DUAL: two
@@ -342,6 +383,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
   int* s_unit = reinterpret_cast<int*>(put + NUM_EPI_WARPS * PUT_BYTES + 256);  // [groups + 1]
   int* s_lo = s_unit + GROUPED_MAX_GROUPS + 4;
   int* s_cnt = s_lo + GROUPED_MAX_GROUPS;
+  int* s_id = s_cnt + GROUPED_MAX_GROUPS;
   static_assert((3 * STAGES + 5) * 8 + 8 <= 256, "barriers");
 
   const int warp = warp_id();
@@ -378,12 +420,19 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
   wait_for_previous();
   let_next_start();
   if (warp == 0) lay_out<TN, TM>(p, s_unit, s_lo, s_cnt);
+  if constexpr (TN) {
+    __syncthreads();
+    sort_groups(p, s_lo, s_cnt, s_id);
+  }
   tc_fence_before();
   if constexpr (PAIR) cluster_sync_all();
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int nunits = s_unit[p.groups];
+  // this CTA's (or pair's) unit in a round over all of them: TN's rounds run to
+  // and fro
+  auto unit_of = [&](int round) { return round * units_in_flight + (TN && (round & 1) ? units_in_flight - 1 - unit0 : unit0); };
   // k-tiles of a unit
   auto k_tiles = [&](const Place& at) { return TN ? (at.cnt + BK - 1) / BK : p.segs * ((p.nkt + KB - 1) / KB); };
 
@@ -414,8 +463,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
         if constexpr (PAIR) tma_load_3d_pair(dst, map, bar, x, y, z);
         else tma_load_3d(dst, map, bar, x, y, z);
       };
-      for (int unit = unit0; ok && unit < nunits; unit += units_in_flight) {
-        place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
+      for (int round = 0; ok; ++round) {
+        const int unit = unit_of(round);
+        if (unit >= nunits) break;  // the last round's
+        place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, s_id, at);
         const int nbs = at.n0 + (int)rank * BNS;
         const int ma = at.m0 + (int)rank * BM;
         const int nk = k_tiles(at);
@@ -496,8 +547,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       copy_arrive(&copied[it % STAGES]);
       ++it;
     };
-    for (int unit = unit0; ok && unit < nunits; unit += units_in_flight) {
-      place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
+    for (int round = 0; ok; ++round) {
+      const int unit = unit_of(round);
+      if (unit >= nunits) break;  // the last round's
+      place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, s_id, at);
       const int nk = k_tiles(at);
       if constexpr (!TN) {
         // lines w * PER + 4 i + lane / 8 of the CTA's rows
@@ -615,8 +668,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       bool ok = true;
       Place at;
       at.e = 0;
-      for (int unit = unit0; ok && unit < nunits; unit += units_in_flight) {
-        place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
+      for (int round = 0; ok; ++round) {
+        const int unit = unit_of(round);
+        if (unit >= nunits) break;  // the last round's
+        place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, s_id, at);
         const int nk = k_tiles(at);
         if (nk == 0) continue;  // an empty group's matrix: the epilogue writes zeros
         const int acc = tc & 1;
@@ -678,8 +733,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       bool ok = true;
       Place at;
       at.e = 0;
-      for (int unit = unit0; ok && unit < nunits; unit += units_in_flight) {
-        place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
+      for (int round = 0; ok; ++round) {
+        const int unit = unit_of(round);
+        if (unit >= nunits) break;  // the last round's
+        place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, s_id, at);
         const int nk = k_tiles(at);
         for (int kt = 0; kt < nk; ++kt, ++it) {
           const int s = it % STAGES;
@@ -703,8 +760,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
     int tc = 0;
     Place at;
     at.e = 0;
-    for (int unit = unit0; unit < nunits; unit += units_in_flight) {
-      place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, at);
+    for (int round = 0;; ++round) {
+      const int unit = unit_of(round);
+      if (unit >= nunits) break;  // the last round's
+      place<TN, TM, BN>(p, unit, s_unit, s_lo, s_cnt, s_id, at);
       const bool none = k_tiles(at) == 0;
       const int acc = tc & 1;
       const int m0 = at.m0 + (int)rank * BM + q * 32;  // the warp's first row in the group (TN: of the matrix)
