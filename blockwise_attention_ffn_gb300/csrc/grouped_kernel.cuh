@@ -30,6 +30,7 @@
 //     edge reads zeros, not the next group's matrix.
 #pragma once
 
+#include "attn_common.cuh"
 #include "gemm_kernel.cuh"
 #include "grouped.h"
 
@@ -215,26 +216,53 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// sigmoid with an error of a few units of fp32's last place: what it enters
-// is rounded to bf16
-__device__ __forceinline__ float fast_sigmoid(float z) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * z));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+// The activations' arithmetic on two columns at a time (attn_common.cuh's
+// packed forms): the epilogues are bound by issue slots, two warps a scheduler
+// with some 34 scalar instructions a column (the tanh GeLU's gradient of a
+// 32-column chunk took 2300 cycles).
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ uint64_t rcp2(uint64_t v) {
+  const float2 x = f2split(v);
+  return f2(rcp(x.x), rcp(x.y));
+}
+__device__ __forceinline__ uint64_t exp2_2(uint64_t v) {
+  const float2 x = f2split(v);
+  return f2(ex2(x.x), ex2(x.y));
+}
+// 1 / (1 + 2^x), with an error of a few units of fp32's last place: what it
+// enters is rounded to bf16.  sigmoid(z) at x = -z log2(e)
+__device__ __forceinline__ uint64_t sigmoid_of(uint64_t x) { return rcp2(add2(exp2_2(x), f2(1.f, 1.f))); }
 
-// GeLU and its slope: z cdf(z), cdf + z pdf(z), or the tanh form as z s with
+// GeLU and its slope: z cdf(z), cdf + z pdf(z) with the cdf as in
+// gemm_kernel.cuh (gelu_erf_parts), or the tanh form as z s with
 // s = sigmoid(2 c (z + 0.044715 z^3)), c = sqrt(2 / pi).
 template <int ACT>
-__device__ __forceinline__ void fast_gelu(float z, float& g, float& d) {
+__device__ __forceinline__ void gelu2(uint64_t z, uint64_t& g, uint64_t& d) {
+  auto c2 = [](float v) { return f2(v, v); };
+  const uint64_t zz = mul2(z, z);
   if constexpr (ACT == BPT_ACT_GELU_ERF) {
-    gk::gelu_and_grad_f(z, 0, g, d);
+    const float2 v = f2split(z);
+    const uint64_t t = rcp2(fma2(f2(fabsf(v.x), fabsf(v.y)), c2(0.3275911f * 0.70710678118654752f), c2(1.f)));
+    uint64_t poly = fma2(c2(1.061405429f), t, c2(-1.453152027f));
+    poly = fma2(poly, t, c2(1.421413741f));
+    poly = fma2(poly, t, c2(-0.284496736f));
+    poly = fma2(poly, t, c2(0.254829592f));
+    const uint64_t e = exp2_2(mul2(zz, c2(-0.72134752044448170f)));  // exp(-z^2 / 2)
+    const uint64_t tail = mul2(mul2(poly, t), mul2(e, c2(0.5f)));     // 0.5 (1 - erf(|z| / sqrt 2))
+    const float2 lo = f2split(tail), hi = f2split(sub2(c2(1.f), tail));
+    const uint64_t cdf = f2(v.x >= 0.f ? hi.x : lo.x, v.y >= 0.f ? hi.y : lo.y);
+    g = mul2(z, cdf);
+    d = fma2(mul2(z, e), c2(0.3989422804014327f), cdf);
   } else {
-    const float c2 = 1.5957691216057308f, z2 = z * z;
-    const float s = fast_sigmoid(c2 * z * fmaf(0.044715f, z2, 1.f));
-    g = z * s;
-    d = fmaf(g * (1.f - s), c2 * fmaf(3.f * 0.044715f, z2, 1.f), s);
+    const float c = 1.5957691216057308f;
+    const uint64_t s = sigmoid_of(mul2(mul2(z, fma2(zz, c2(0.044715f), c2(1.f))), c2(-1.4426950408889634f * c)));
+    g = mul2(z, s);
+    const uint64_t rest = mul2(g, sub2(c2(1.f), s));
+    d = fma2(rest, fma2(zz, c2(3.f * 0.044715f * c), c2(c)), s);
   }
 }
 
@@ -772,7 +800,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       void* out = TN && at.seg ? p.out2 : p.out;
       const bool mine = lane < rows;
       const int n0 = at.n0 + half * EPI_COLS;  // the warp's first column
-      float w = 0.f, dot = 0.f;
+      float w = 0.f;
       uint32_t s0[EPI == GROUPED_ACT_BWD ? 16 : 1], s1[EPI == GROUPED_ACT_BWD && GATED ? 16 : 1];
       auto fetch = [&](int c) {
         const int words = (p.N - n0 - c * 32) / 8;
@@ -861,18 +889,17 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              float y[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float z = __uint_as_float(r[2 * j + i]);
-                if constexpr (DUAL) {
-                  y[i] = z * fast_sigmoid(z) * __uint_as_float(u[2 * j + i]);
-                } else {
-                  float slope;
-                  fast_gelu<ACT>(z, y[i], slope);
-                }
+              const uint64_t z = f2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+              uint64_t y;
+              if constexpr (DUAL) {
+                const uint64_t up = f2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
+                y = mul2(mul2(z, up), sigmoid_of(mul2(z, f2(-1.4426950408889634f, -1.4426950408889634f))));
+              } else {
+                uint64_t slope;
+                gelu2<ACT>(z, y, slope);
               }
-              v[16 * h + j] = pack_bf16(y[0], y[1]);
+              const float2 o = f2split(y);
+              v[16 * h + j] = pack_bf16(o.x, o.y);
             }
           }
           put_rows<W / 8, false>(v, stage, to + c * 2, p.N * 2ll, rows, min(W / 8, (left - c) / 8), 0.f);
@@ -880,6 +907,8 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
       } else {
         // what was kept is bf16 (off by up to 2^-8 of its size): the activation
         // and its slopes are taken again from it in fp32 and rounded once
+        const uint64_t w2 = f2(w, w);
+        uint64_t dot2 = f2(0.f, 0.f);
 #pragma unroll 1
         for (int c = 0; c < EPI_COLS && c < left; c += 32) {
           uint32_t r[32], v[16], dv[GATED ? 16 : 1], aw[16];
@@ -889,30 +918,27 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
           // group's end hold anything and are not stored
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float x[2], y[2], z[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float a = __uint_as_float(r[2 * j + i]);
-              const float g = i ? bf16_hi(s0[j]) : bf16_lo(s0[j]);
-              const float wa = w * a;
-              float act;
-              if constexpr (GATED) {
-                const float u = i ? bf16_hi(s1[j]) : bf16_lo(s1[j]);
-                const float sg = fast_sigmoid(g), si = g * sg;  // silu(g)
-                act = si * u;
-                x[i] = wa * u * fmaf(si, 1.f - sg, sg);
-                y[i] = wa * si;
-              } else {
-                float slope;
-                fast_gelu<ACT>(g, act, slope);
-                x[i] = wa * slope;
-              }
-              dot = fmaf(a, act, dot);
-              z[i] = w * act;
+            const uint64_t a = f2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+            const uint64_t g = f2(bf16_lo(s0[j]), bf16_hi(s0[j]));
+            const uint64_t wa = mul2(w2, a);
+            uint64_t act, x;
+            if constexpr (GATED) {
+              const uint64_t u = f2(bf16_lo(s1[j]), bf16_hi(s1[j]));
+              const uint64_t sg = sigmoid_of(mul2(g, f2(-1.4426950408889634f, -1.4426950408889634f)));
+              const uint64_t si = mul2(g, sg);  // silu(g)
+              act = mul2(si, u);
+              x = mul2(mul2(wa, u), fma2(si, sub2(f2(1.f, 1.f), sg), sg));
+              const float2 y = f2split(mul2(wa, si));
+              dv[j] = pack_bf16(y.x, y.y);
+            } else {
+              uint64_t slope;
+              gelu2<ACT>(g, act, slope);
+              x = mul2(wa, slope);
             }
-            v[j] = pack_bf16(x[0], x[1]);
-            if constexpr (GATED) dv[j] = pack_bf16(y[0], y[1]);
-            aw[j] = pack_bf16(z[0], z[1]);
+            dot2 = fma2(a, act, dot2);
+            const float2 xs = f2split(x), zs = f2split(mul2(w2, act));
+            v[j] = pack_bf16(xs.x, xs.y);
+            aw[j] = pack_bf16(zs.x, zs.y);
           }
           if (c + 32 < EPI_COLS) fetch(c / 32 + 1);
           const long long ld = p.N * 2ll;
@@ -922,7 +948,8 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
           put_rows<4, false>(aw, stage, reinterpret_cast<char*>(p.out3) + (first * p.N + n0 + c) * 2, ld, rows, words, 0.f);
         }
         // one sum per row and half tile, added in this order later
-        if (mine) p.part[(long long)(2 * (at.n0 / BN) + half) * p.rows + first + lane] = dot;
+        const float2 dot = f2split(dot2);
+        if (mine) p.part[(long long)(2 * (at.n0 / BN) + half) * p.rows + first + lane] = dot.x + dot.y;
       }
       if (!none) {
         tc_fence_before();
