@@ -777,6 +777,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_kernel(const __grid_const
       tmem_relinquish();
     }
   }
+  if constexpr (SET > 0) {  // launched as the dependent of the kernel before
+    wait_for_previous();
+    let_next_start();
+  }
   tc_fence_before();
   // a pair: the other CTA's barriers are initialised before anything of this
   // one can arrive on them
@@ -1005,7 +1009,9 @@ int launch(GemmParams& p, cudaStream_t st) {
     }
   }
   const int units = p.ntiles < slots ? p.ntiles : slots;
-  if constexpr (!PAIR) {
+  if constexpr (SET > 0) {
+    return launch_dependent(kern, PAIR ? 2 * units : units, PAIR ? 2 : 1, dim3(NUM_THREADS), (size_t)SMEM, st, p) == cudaSuccess ? 0 : 3;
+  } else if constexpr (!PAIR) {
     kern<<<units, NUM_THREADS, SMEM, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : 3;
   } else {

@@ -263,6 +263,8 @@ struct RowParams {
 };
 constexpr int ROW_SLICES = 32;  // 15 us for 4001 rows of 394 pairs with 8
 __global__ void __launch_bounds__(32 * ROW_SLICES) rows_kernel(const RowParams q) {
+  wait_for_previous();
+  let_next_start();
   __shared__ float s_m[ROW_SLICES][32], s_l[ROW_SLICES][32], s_dot[ROW_SLICES][32];
   const int lane = lane_id(), sl = warp_id();
   const int64_t row = (int64_t)blockIdx.x * 32 + lane;
@@ -329,6 +331,8 @@ __global__ void __launch_bounds__(1024) total_kernel(int64_t n, const double* te
 // that appears more than once added up by the first of them.
 __global__ void __launch_bounds__(256) entries_kernel(int64_t n, int k, int64_t v0, int64_t v1, const Saved s, const float* weight,
                                                       float scale, __nv_bfloat16* dz, int64_t ld) {
+  wait_for_previous();
+  let_next_start();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n * k) return;
   const int id = s.id[i];
@@ -346,6 +350,8 @@ __global__ void __launch_bounds__(256) entries_kernel(int64_t n, int k, int64_t 
 // sum over the slabs in order, onto acc (NULL: 0): fp32 out, or bf16
 __global__ void __launch_bounds__(256) slabs_kernel(int64_t n4, int slabs, const float4* s, const float4* acc, float4* out_f32,
                                                     uint2* out_bf16) {
+  wait_for_previous();
+  let_next_start();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n4) return;
   float4 t = acc ? acc[i] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -431,8 +437,7 @@ int bpt_lm_distill_fwd(const bpt_distill_config* cfg, const void* x, const void*
     ProfScope prof(PROF_MISC, 0.0, (double)D.n * (D.nparts * 8.0 + 8.0 * D.k), st);
     const float scale = row_weight ? D.T * D.T : D.T * D.T / (float)D.n;
     RowParams q{W.part, D.n, D.nparts, (int)D.k, scale, row_weight, S, W.term};
-    rows_kernel<<<(unsigned)((D.n + 31) / 32), 32 * ROW_SLICES, 0, st>>>(q);
-    if (cudaGetLastError() != cudaSuccess) return BPT_ECUDA;
+    if (launch_dependent(rows_kernel, (int)((D.n + 31) / 32), 1, dim3(32 * ROW_SLICES), 0, st, q) != cudaSuccess) return BPT_ECUDA;
     if (launch_dependent(total_kernel, 1, 1, dim3(1024), 0, st, D.n, (const double*)W.term, loss) != cudaSuccess) return BPT_ECUDA;
   }
   return D.debug ? debug_finish(st) : BPT_OK;
@@ -479,8 +484,9 @@ int bpt_lm_distill_bwd(const bpt_distill_config* cfg, const void* x, const void*
     }
     {
       ProfScope prof(PROF_MISC, 0.0, 4.0 * (double)D.n * D.k, st);
-      entries_kernel<<<(unsigned)((D.n * D.k + 255) / 256), 256, 0, st>>>(D.n, (int)D.k, v0, v0 + nv, S, row_weight, scale, W.dz, D.cv);
-      if (cudaGetLastError() != cudaSuccess) return BPT_ECUDA;
+      if (launch_dependent(entries_kernel, (int)((D.n * D.k + 255) / 256), 1, dim3(256), 0, st, D.n, (int)D.k, v0, v0 + nv, S, row_weight,
+                           scale, W.dz, D.cv) != cudaSuccess)
+        return BPT_ECUDA;
     }
     {
       Epilogue e;
@@ -503,10 +509,11 @@ int bpt_lm_distill_bwd(const bpt_distill_config* cfg, const void* x, const void*
       if ((rc = gemm(D.n, D.h, nv, Z, false, &Wb, &Kv, 1, true, nullptr, e, st))) return rc;
       const int64_t n4 = D.n * D.h / 4;
       ProfScope prof(PROF_MISC, 0.0, 16.0 * (double)n4 * (slabs + 1), st);
-      slabs_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, st>>>(
-          n4, slabs, reinterpret_cast<const float4*>(W.slabs), b > 0 ? reinterpret_cast<const float4*>(W.dx_acc) : nullptr,
-          last ? nullptr : reinterpret_cast<float4*>(W.dx_acc), reinterpret_cast<uint2*>(dx));
-      if (cudaGetLastError() != cudaSuccess) return BPT_ECUDA;
+      if (launch_dependent(slabs_kernel, (int)((n4 + 255) / 256), 1, dim3(256), 0, st, n4, slabs,
+                           reinterpret_cast<const float4*>(W.slabs),
+                           b > 0 ? reinterpret_cast<const float4*>(W.dx_acc) : (const float4*)nullptr,
+                           last ? (float4*)nullptr : reinterpret_cast<float4*>(W.dx_acc), reinterpret_cast<uint2*>(dx)) != cudaSuccess)
+        return BPT_ECUDA;
     } else {
       // dx: fp32 over the blocks, the last one rounds to bf16
       Epilogue e;
