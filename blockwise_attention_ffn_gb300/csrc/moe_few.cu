@@ -138,14 +138,20 @@ __global__ void __launch_bounds__(THREADS) few_act_kernel(const FewParams p) {
   }
 }
 
-// y[t, i] = sum_j w_tj <act of pair (t, j), W2_e[i, :]>, two i a warp.
+// y[t, i] = sum_j w_tj <act of pair (t, j), W2_e[i, :]>: two i a group of JS
+// warps, which share the choices out and add their sums in order.  (One warp for
+// all of four choices is four round trips to memory in a row.)
 constexpr int MAX_TOP_K = 32;
+template <int JS>
 __global__ void __launch_bounds__(THREADS) few_out_kernel(const FewParams p) {
+  constexpr int PAIRS = WARPS / JS;  // row pairs of W2 a block
   __shared__ int s_e[MAX_TOP_K];
-  const int lane = lane_id();
-  const int chunks = (p.h + WARPS * 2 - 1) / (WARPS * 2);
+  __shared__ float s_sum[WARPS][2];
+  const int lane = lane_id(), js = warp_id() % JS;
+  const int chunks = (p.h + PAIRS * 2 - 1) / (PAIRS * 2);
   const int t = blockIdx.x / chunks;
-  const int i0 = ((int)(blockIdx.x % chunks) * WARPS + warp_id()) * 2;
+  const int i0 = ((int)(blockIdx.x % chunks) * PAIRS + warp_id() / JS) * 2;
+  const bool in = i0 < p.h;  // h is even
   if (threadIdx.x < MAX_TOP_K) s_e[threadIdx.x] = p.E;
   // the routes are older than the activations: the kernel before has waited
   // for them before it let this one start
@@ -155,8 +161,8 @@ __global__ void __launch_bounds__(THREADS) few_out_kernel(const FewParams p) {
     if (r >= 0 && r < p.pairs) find_expert(p, r, &s_e[j]);
   }
   __syncthreads();
-  if (i0 < p.h)
-    for (int j = 0; j < p.k; ++j)
+  if (in)
+    for (int j = js; j < p.k; j += JS)
       if (s_e[j] < p.E)  // on their way to L2 meanwhile
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -164,42 +170,52 @@ __global__ void __launch_bounds__(THREADS) few_out_kernel(const FewParams p) {
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.w2 + ((int64_t)s_e[j] * p.h + i0 + q) * p.f + c));
   wait_for_previous();
   let_next_start();
-  if (i0 >= p.h) return;
   float s[2] = {0.f, 0.f};
-  for (int j = 0; j < p.k; ++j) {
-    const int e = s_e[j];
-    if (e == p.E) continue;
-    const int64_t q = (int64_t)t * p.k + j;
-    const float weight = p.weight_f32 ? reinterpret_cast<const float*>(p.weight)[q]
-                                      : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.weight)[q]);
-    const float* a = p.act + (int64_t)p.slot[q] * p.f;
-    const __nv_bfloat16* w0 = p.w2 + ((int64_t)e * p.h + i0) * p.f;
-    float d[2] = {0.f, 0.f};
-    for (int c0 = lane * 8; c0 < p.f; c0 += 256 * STEP) {
-      uint4 wv[STEP][2];
-      float4 av[STEP][2];
+  if (in)
+    for (int j = js; j < p.k; j += JS) {
+      const int e = s_e[j];
+      if (e == p.E) continue;
+      const int64_t q = (int64_t)t * p.k + j;
+      const float weight = p.weight_f32 ? reinterpret_cast<const float*>(p.weight)[q]
+                                        : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.weight)[q]);
+      const float* a = p.act + (int64_t)p.slot[q] * p.f;
+      const __nv_bfloat16* w0 = p.w2 + ((int64_t)e * p.h + i0) * p.f;
+      float d[2] = {0.f, 0.f};
+      for (int c0 = lane * 8; c0 < p.f; c0 += 256 * STEP) {
+        uint4 wv[STEP][2];
+        float4 av[STEP][2];
 #pragma unroll
-      for (int u = 0; u < STEP; ++u) {
-        const int c = c0 + 256 * u;
-        const bool in = c < p.f;
-        wv[u][0] = load16(w0 + c, in);
-        wv[u][1] = load16(w0 + p.f + c, in);
+        for (int u = 0; u < STEP; ++u) {
+          const int c = c0 + 256 * u;
+          const bool some = c < p.f;
+          wv[u][0] = load16(w0 + c, some);
+          wv[u][1] = load16(w0 + p.f + c, some);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) av[u][i] = in ? reinterpret_cast<const float4*>(a + c)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < 2; ++i) av[u][i] = some ? reinterpret_cast<const float4*>(a + c)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < STEP; ++u) {
+          const float v[8] = {av[u][0].x, av[u][0].y, av[u][0].z, av[u][0].w, av[u][1].x, av[u][1].y, av[u][1].z, av[u][1].w};
+          d[0] = dot8(wv[u][0], v, d[0]);
+          d[1] = dot8(wv[u][1], v, d[1]);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < STEP; ++u) {
-        const float v[8] = {av[u][0].x, av[u][0].y, av[u][0].z, av[u][0].w, av[u][1].x, av[u][1].y, av[u][1].z, av[u][1].w};
-        d[0] = dot8(wv[u][0], v, d[0]);
-        d[1] = dot8(wv[u][1], v, d[1]);
-      }
+      s[0] = fmaf(weight, d[0], s[0]);
+      s[1] = fmaf(weight, d[1], s[1]);
     }
-    s[0] = fmaf(weight, d[0], s[0]);
-    s[1] = fmaf(weight, d[1], s[1]);
-  }
   s[0] = warp_sum(s[0]);
   s[1] = warp_sum(s[1]);
-  if (lane == 0) *reinterpret_cast<uint32_t*>(p.y + (int64_t)t * p.h + i0) = pack_bf16(s[0], s[1]);
+  if constexpr (JS > 1) {
+    if (lane < 2) s_sum[warp_id()][lane] = lane ? s[1] : s[0];
+    __syncthreads();
+    if (js) return;
+#pragma unroll
+    for (int q = 1; q < JS; ++q) {
+      s[0] += s_sum[warp_id() + q][0];
+      s[1] += s_sum[warp_id() + q][1];
+    }
+  }
+  if (in && lane == 0) *reinterpret_cast<uint32_t*>(p.y + (int64_t)t * p.h + i0) = pack_bf16(s[0], s[1]);
 }
 
 }  // namespace
@@ -233,11 +249,13 @@ int moe_few_fwd(const MoeDims& D, const bpt_moe_route* r, const void* x, const v
   const int64_t mats = gated ? 3 : 2;
   ProfScope prof(PROF_MISC, 0.0, 2.0 * (double)(D.pairs * mats * D.h * D.f), st);
   const int64_t per = WARPS * (gated ? 2 : 4);
-  const int64_t g1 = D.pairs * ((D.f + per - 1) / per), g2 = D.n * ((D.h + WARPS * 2 - 1) / (WARPS * 2));
+  const int js = D.k >= 4 ? 4 : D.k >= 2 ? 2 : 1;
+  const int64_t g1 = D.pairs * ((D.f + per - 1) / per), g2 = D.n * ((D.h + WARPS / js * 2 - 1) / (WARPS / js * 2));
   if (g1 > INT32_MAX || g2 > INT32_MAX) return BPT_EUNSUPPORTED;
   if (launch_dependent(gated ? few_act_kernel<true> : few_act_kernel<false>, (int)g1, 1, dim3(THREADS), 0, st, p) != cudaSuccess)
     return BPT_ECUDA;
-  return launch_dependent(few_out_kernel, (int)g2, 1, dim3(THREADS), 0, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
+  auto out = js == 4 ? few_out_kernel<4> : js == 2 ? few_out_kernel<2> : few_out_kernel<1>;
+  return launch_dependent(out, (int)g2, 1, dim3(THREADS), 0, st, p) == cudaSuccess ? BPT_OK : BPT_ECUDA;
 }
 
 }  // namespace bpt

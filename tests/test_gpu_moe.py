@@ -213,6 +213,8 @@ FFN = [
     (5, 40, 72, 64, 3, 2, False),
     (1, 264, 136, 16, 4, 0, False),     # rows one by one (inference)
     (3, 1000, 520, 64, 6, 1, True),
+    (4, 72, 2056, 16, 2, 2, True),
+    (7, 40, 104, 14, 1, 2, False),
     (8, 2056, 1032, 128, 8, 2, False),
     (70, 256, 200, 12, 2, 1, True),
     (90, 392, 136, 16, 3, 2, True),     # 32-row tiles, several an expert
