@@ -15,7 +15,7 @@
 // P q - p, formed in fp32 from the kept logits and rounded once, at the
 // entries.  No n x V logits: one n x c_v bf16 block.
 // Bound by the tensor cores: 2 n h V FLOPs forward, 6 backward.  8000 rows of
-// 2560 against 50257 words, 32 entries: 5.47 ms for both (1507 TFLOP/s).
+// 2560 against 50257 words, 32 entries: 5.5 ms for both (1500 TFLOP/s).
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
 }
 
 // Rows' log-sum-exp from their pairs, 32 rows a block with the parts in 32
-// slices, and their terms of the loss.
+// slices, and their terms of the loss, sum p z by a warp a row.
 struct RowParams {
   const float2* part;
   int64_t n, nparts;
@@ -261,52 +261,61 @@ struct RowParams {
   Saved s;
   double* term;
 };
-constexpr int ROW_SLICES = 32;  // 15 us for 4001 rows of 394 pairs with 8
+constexpr int ROW_SLICES = 32;
 __global__ void __launch_bounds__(32 * ROW_SLICES) rows_kernel(const RowParams q) {
   wait_for_previous();
   let_next_start();
-  __shared__ float s_m[ROW_SLICES][32], s_l[ROW_SLICES][32], s_dot[ROW_SLICES][32];
+  __shared__ float s_m[ROW_SLICES][32], s_l[ROW_SLICES][32], s_dot[32];
   const int lane = lane_id(), sl = warp_id();
-  const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t r0 = (int64_t)blockIdx.x * 32, row = r0 + lane;
   const bool in = row < q.n;
   float m = -INFINITY, l = 0.f;
-  if (in) {
-#pragma unroll 8
-    for (int64_t p = sl; p < q.nparts; p += ROW_SLICES) {
-      const float2 v = q.part[p * q.n + row];
-      const float nm = fmaxf(m, v.x);
-      // pairs of columns past the vocabulary are (-inf, 0)
-      if (nm > -INFINITY) l = l * expf(m - nm) + v.y * expf(v.x - nm);
-      m = nm;
+  for (int64_t p0 = sl; p0 < q.nparts; p0 += 8 * ROW_SLICES) {
+    // eight pairs on their way at once; those past the last are (-inf, 0) like
+    // the pairs of columns past the vocabulary
+    float2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t p = p0 + i * ROW_SLICES;
+      v[i] = in && p < q.nparts ? q.part[p * q.n + row] : make_float2(-INFINITY, 0.f);
     }
-    // sum p (z - lse) needs lse: p z here
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, v[i].x);
+    if (top > -INFINITY) {
+      l *= expf(m - top);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) l += v[i].y * expf(v[i].x - top);
+      m = top;
+    }
   }
   s_m[sl][lane] = m;
   s_l[sl][lane] = l;
+  static_assert(ROW_SLICES == 32, "a warp a row");
   float dot = 0.f;
-  if (in)
-    for (int j = sl; j < q.k; j += ROW_SLICES) {
-      const float p = q.s.p[row * q.k + j];
-      dot += p > 0.f ? p * q.s.z[row * q.k + j] : 0.f;
+  if (r0 + sl < q.n)
+    for (int j = lane; j < q.k; j += 32) {
+      const int64_t at = (r0 + sl) * q.k + j;
+      const float p = q.s.p[at], z = q.s.z[at];  // z holds nothing where there is no entry
+      dot += p > 0.f ? p * z : 0.f;
     }
-  s_dot[sl][lane] = dot;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+  if (lane == 0) s_dot[sl] = dot;
   __syncthreads();
   if (sl || !in) return;
   float top = s_m[0][lane];
 #pragma unroll
   for (int i = 1; i < ROW_SLICES; ++i) top = fmaxf(top, s_m[i][lane]);
   float sum = 0.f;
-  double pz = 0.0;
 #pragma unroll
-  for (int i = 0; i < ROW_SLICES; ++i) {
-    sum += s_l[i][lane] * expf(s_m[i][lane] - top);
-    pz += (double)s_dot[i][lane];
-  }
+  for (int i = 0; i < ROW_SLICES; ++i) sum += s_l[i][lane] * expf(s_m[i][lane] - top);
   const float lse = top + logf(sum);
   q.s.lse[row] = lse;
   const float w = q.weight ? q.weight[row] : 1.f;
   // the divergence is a small difference of these: in fp64
-  q.term[row] = w != 0.f ? (double)q.scale * w * ((double)q.s.ent[row] - pz + (double)q.s.mass[row] * lse) : 0.0;
+  q.term[row] =
+      w != 0.f ? (double)q.scale * w * ((double)q.s.ent[row] - (double)s_dot[lane] + (double)q.s.mass[row] * lse) : 0.0;
 }
 
 // loss = the rows' terms, added in a fixed order

@@ -19,9 +19,9 @@
 // Every sum is fp32 in a fixed order: no atomics.
 //
 // Bound by the tensor cores: 4096 rows, 2 of 8 experts of 4096 x 14336, 1.9 ms
-// forward and 4.0 backward (in one call after another 6.6 ms in all, under the
-// power cap: 1310 TFLOP/s); a few rows by the weights' bytes (48 rows over 32
-// experts of 2560 x 2048: 155 us, 6.5 TB/s).
+// forward and 3.9 backward (in one call after another 6.7 ms in all, under the
+// power cap: 1290 TFLOP/s); a few rows by the weights' bytes (48 rows over 32
+// experts of 2560 x 2048: 158 us, 6.4 TB/s).
 #include <math.h>
 
 #include <algorithm>
