@@ -16,11 +16,15 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   const bool dual = op.form == GROUPED_NT && op.w2 != nullptr;
   const bool two = op.form == GROUPED_NN && op.a2 != nullptr;
   if (op.groups < 1 || op.groups > GROUPED_MAX_GROUPS || op.rows < 1) return 1;
-  // Tiles.  Rows a group: a pair of SMs takes 256 at a time, one SM 128; the
-  // pair's product needs two thirds of the shared-memory reads but leaves 128
-  // rows idle in a group's last tile on average against 64.
-  // Few rows: the weights' bytes bound the product; 64-column tiles of 32 rows
-  // give the SMs more units to share them and a ring of little but weights.
+  // Tiles, by the rows a group has on average (what each has, only the device
+  // knows).  A pair of SMs takes 256 rows at a time: its product reads two thirds
+  // of the bytes from L2 and shared memory, but leaves 128 rows idle in a group's
+  // last tile on average against one SM's 64.  Few rows: the weights' bytes bound
+  // the product; 64-column tiles of 32 rows give the SMs more units to share them
+  // and a ring of little but weights.  us at 16, 32, 64, 256, 384, 512 rows, 64
+  // groups of 1024 x 2048: few-row tiles 61, 70, 104, 326, 467, 619; one SM 64,
+  // 64, 64, 90, 101, 124; a pair 68, 68, 70, 79, 96, 117; 16 of 2048 x 2048: 37,
+  // 39, 53, 166, 238, 313; 37, 37, 37, 47, 57, 68; 41, 41, 41, 49, 57, 59.
   const bool small = op.form == GROUPED_NT && op.mean_rows <= 24;
   bool pair = tn ? op.M > BM : op.mean_rows >= 384;
   if (pair && gk::pair_units() <= 0) pair = false;

@@ -10,8 +10,12 @@
 // pass to add them, and the activation stays fp32.
 //   one token, 4 of 64 experts of 2048 x 1024 (50 MB, 7.4 us of HBM time):
 //   18.5 us in two launches against 29.6 in the grouped GEMM's three.
-// Weights that two rows share are read twice, the second time from L2: taken up
-// to half as many rows as experts (moe_few_rows), where at most a quarter are.
+// Weights that two rows share are read twice, the second time from L2, and long
+// streams go faster by TMA: taken up to a quarter as many rows as experts and
+// 256 MB (moe_few_rows).  us here and through the grouped GEMM: 64 experts of
+// 2048 x 1024, 4 pairs 17 and 25, 16 pairs (201 MB) 42 and 46, 32 pairs 77 and
+// 68; 128 of 2560 x 2048, 4 pairs 28 and 43, 16 pairs (503 MB) 92 and 99; 64 of
+// 4096 x 2048, 8 pairs (403 MB) 81 and 80; 16 of 4096 x 8192, 2 pairs 85 and 74.
 #include <math.h>
 
 #include <algorithm>
@@ -220,7 +224,10 @@ __global__ void __launch_bounds__(THREADS) few_out_kernel(const FewParams p) {
 
 }  // namespace
 
-bool moe_few_rows(const MoeDims& D) { return 2 * D.pairs <= D.E; }
+bool moe_few_rows(const MoeDims& D) {
+  const int64_t mats = D.act == BPT_ACT_SWIGLU ? 3 : 2;
+  return 4 * D.pairs <= D.E && 2 * D.pairs * mats * D.h * D.f <= (int64_t(256) << 20);
+}
 size_t moe_few_ws_bytes(const MoeDims& D) { return (size_t)D.pairs * D.f * 4; }
 
 int moe_few_fwd(const MoeDims& D, const bpt_moe_route* r, const void* x, const void* w1, const void* w3, const void* w2, void* y, void* ws,
