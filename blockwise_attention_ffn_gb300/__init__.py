@@ -26,8 +26,9 @@ import ctypes
 import os
 from array import array
 from dataclasses import dataclass
+from functools import lru_cache
 
-from .presets import PRESETS, LayerConfig  # noqa: F401
+from .presets import PRESETS, DistillConfig, LayerConfig, MoeConfig  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libbpt.so")
@@ -465,6 +466,19 @@ def make_moe_config(c) -> BptMoeConfig:
                         c.norm_topk, c.balance_coef, c.z_coef, c.flags)
 
 
+# Config records and sizes, once for each value of the frozen config classes
+# (other objects may change between calls); the records are read only.
+@lru_cache(maxsize=256)
+def _kept_moe_record(cfg):
+    c = make_moe_config(cfg)
+    return c, int(lib().bpt_moe_saved_bytes(c))
+
+
+def _moe_record(cfg):
+    """(BptMoeConfig, bytes that the forward saves) of cfg."""
+    return _kept_moe_record(cfg) if type(cfg) is MoeConfig else _kept_moe_record.__wrapped__(cfg)
+
+
 @dataclass(frozen=True)
 class MoeRoute:
     """Where bpt_moe_route_fwd sends every position (device tensors): ids
@@ -501,7 +515,7 @@ def bpt_moe_route_fwd(cfg, logits, route, loss, ws, stream=None) -> None:
     where both coefficients are 0)."""
     import torch
     where, dev = "bpt_moe_route_fwd", torch.cuda.current_device()
-    c, r = make_moe_config(cfg), _moe_route(where, cfg, route, dev)
+    c, r = _moe_record(cfg)[0], _moe_route(where, cfg, route, dev)
     _check(lib().bpt_moe_route_fwd(
         c, _want(where, "logits", logits, _dtype(cfg.logits_dtype), cfg.n * cfg.n_experts, dev), r,
         _may(where, "loss", loss, torch.float32, 1, dev), _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(),
@@ -513,7 +527,7 @@ def bpt_moe_route_bwd(cfg, logits, route, dweights, dloss, dlogits, stream=None)
     times the losses."""
     import torch
     where, dev = "bpt_moe_route_bwd", torch.cuda.current_device()
-    c, r, kind, n = make_moe_config(cfg), _moe_route(where, cfg, route, dev), _dtype(cfg.logits_dtype), cfg.n * cfg.n_experts
+    c, r, kind, n = _moe_record(cfg)[0], _moe_route(where, cfg, route, dev), _dtype(cfg.logits_dtype), cfg.n * cfg.n_experts
     _check(lib().bpt_moe_route_bwd(
         c, _want(where, "logits", logits, kind, n, dev), r,
         _want(where, "dweights", dweights, _dtype(cfg.weights_dtype), cfg.n * cfg.top_k, dev), float(dloss),
@@ -543,8 +557,7 @@ def bpt_moe_ffn_fwd(cfg, route, x, w1, w3, w2, y, saved, ws, stream=None) -> Non
     bpt_moe_saved_bytes(cfg) for the backward, None: inference."""
     import torch
     where, dev, bf16 = "bpt_moe_ffn_fwd", torch.cuda.current_device(), torch.bfloat16
-    c, r = make_moe_config(cfg), _moe_route(where, cfg, route, dev, ids=False)
-    keep = 0 if saved is None else bpt_moe_saved_bytes(cfg)
+    (c, keep), r = _moe_record(cfg), _moe_route(where, cfg, route, dev, ids=False)
     _check(lib().bpt_moe_ffn_fwd(
         c, r, _want(where, "x", x, bf16, cfg.n * cfg.h, dev), _experts(where, cfg, "w1", w1, bf16, dev),
         _experts(where, cfg, "w3", w3, bf16, dev), _experts(where, cfg, "w2", w2, bf16, dev),
@@ -558,11 +571,12 @@ def bpt_moe_ffn_bwd(cfg, route, x, w1, w3, w2, saved, dy, dx, dweights, dw1, dw3
     and what the forward saved."""
     import torch
     where, dev, bf16 = "bpt_moe_ffn_bwd", torch.cuda.current_device(), torch.bfloat16
-    c, r, kind, nh = make_moe_config(cfg), _moe_route(where, cfg, route, dev, ids=False), _dtype(cfg.grads_dtype), cfg.n * cfg.h
+    (c, keep), r = _moe_record(cfg), _moe_route(where, cfg, route, dev, ids=False)
+    kind, nh = _dtype(cfg.grads_dtype), cfg.n * cfg.h
     _check(lib().bpt_moe_ffn_bwd(
         c, r, _want(where, "x", x, bf16, nh, dev), _experts(where, cfg, "w1", w1, bf16, dev),
         _experts(where, cfg, "w3", w3, bf16, dev), _experts(where, cfg, "w2", w2, bf16, dev),
-        _want(where, "saved", saved, torch.uint8, bpt_moe_saved_bytes(cfg), dev), _want(where, "dy", dy, bf16, nh, dev),
+        _want(where, "saved", saved, torch.uint8, keep, dev), _want(where, "dy", dy, bf16, nh, dev),
         _want(where, "dx", dx, bf16, nh, dev),
         _want(where, "dweights", dweights, _dtype(cfg.weights_dtype), cfg.n * cfg.top_k, dev),
         _experts(where, cfg, "dw1", dw1, kind, dev), _experts(where, cfg, "dw3", dw3, kind, dev),
@@ -597,18 +611,29 @@ def bpt_lm_distill_workspace_bytes(cfg, pass_: int) -> int:
     return int(lib().bpt_lm_distill_workspace_bytes(make_distill_config(cfg), int(pass_)))
 
 
+@lru_cache(maxsize=256)
+def _kept_distill_record(cfg):
+    c = make_distill_config(cfg)
+    return c, int(lib().bpt_lm_distill_saved_bytes(c))
+
+
+def _distill_record(cfg):
+    """(BptDistillConfig, bytes that the forward saves) of cfg."""
+    return _kept_distill_record(cfg) if type(cfg) is DistillConfig else _kept_distill_record.__wrapped__(cfg)
+
+
 def bpt_lm_distill_fwd(cfg, x, w, ids, values, row_weight, loss, saved, ws, stream=None) -> None:
     """Divergence of the student's softmax(x w^T / T) from a teacher's stored
     entries ids, values [n, k], into loss (one fp32).  x [n, h], w [V, h];
     row_weight [n] fp32 or None (1 / n each); saved: for the backward."""
     import torch
     where, dev, bf16, f32 = "bpt_lm_distill_fwd", torch.cuda.current_device(), torch.bfloat16, torch.float32
-    c = make_distill_config(cfg)
+    c, keep = _distill_record(cfg)
     _check(lib().bpt_lm_distill_fwd(
         c, _want(where, "x", x, bf16, cfg.n * cfg.h, dev), _want(where, "w", w, bf16, cfg.vocab * cfg.h, dev),
         _want(where, "ids", ids, torch.int32, cfg.n * cfg.top_k, dev), _want(where, "values", values, f32, cfg.n * cfg.top_k, dev),
         _may(where, "row_weight", row_weight, f32, cfg.n, dev), _want(where, "loss", loss, f32, 1, dev),
-        _want(where, "saved", saved, torch.uint8, bpt_lm_distill_saved_bytes(cfg), dev),
+        _want(where, "saved", saved, torch.uint8, keep, dev),
         _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(), _stream(stream)), where)
 
 
@@ -617,11 +642,11 @@ def bpt_lm_distill_bwd(cfg, x, w, row_weight, saved, dloss, dx, dw, ws, stream=N
     (cfg.grads_dtype), from what the forward saved."""
     import torch
     where, dev, bf16 = "bpt_lm_distill_bwd", torch.cuda.current_device(), torch.bfloat16
-    c = make_distill_config(cfg)
+    c, keep = _distill_record(cfg)
     _check(lib().bpt_lm_distill_bwd(
         c, _want(where, "x", x, bf16, cfg.n * cfg.h, dev), _want(where, "w", w, bf16, cfg.vocab * cfg.h, dev),
         _may(where, "row_weight", row_weight, torch.float32, cfg.n, dev),
-        _want(where, "saved", saved, torch.uint8, bpt_lm_distill_saved_bytes(cfg), dev), float(dloss),
+        _want(where, "saved", saved, torch.uint8, keep, dev), float(dloss),
         _want(where, "dx", dx, bf16, cfg.n * cfg.h, dev), _want(where, "dw", dw, _dtype(cfg.grads_dtype), cfg.vocab * cfg.h, dev),
         _want(where, "ws", ws, torch.uint8, 0, dev), ws.numel(), _stream(stream)), where)
 
