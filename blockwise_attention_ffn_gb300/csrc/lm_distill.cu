@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
         if (t >= 0) {
           if ((int64_t)t < q.V && x < INFINITY) {
             id[c] = t;
-            v[c] = q.teacher == BPT_TEACHER_LOGITS ? x * q.inv_t : x;
+            v[c] = q.teacher == BPT_TEACHER_LOGITS ? fminf(x * q.inv_t, 3.402823466e38f) : x;  // finite over T stays so
           } else {
             bad = true;
           }
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(32 * ROW_SLICES) rows_kernel(const RowParams q
   const float w = q.weight ? q.weight[row] : 1.f;
   // the divergence is a small difference of these: in fp64
   q.term[row] =
-      w != 0.f ? (double)q.scale * w * ((double)q.s.ent[row] - (double)s_dot[lane] + (double)q.s.mass[row] * lse) : 0.0;
+      w != 0.f && q.s.mass[row] != 0.f ? (double)q.scale * w * ((double)q.s.ent[row] - (double)s_dot[lane] + (double)q.s.mass[row] * lse) : 0.0;
 }
 
 // loss = the rows' terms, added in a fixed order

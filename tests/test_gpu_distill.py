@@ -164,6 +164,28 @@ def test_a_row_of_weight_zero_leaves_no_trace():
         assert torch.equal(a, b)
 
 
+def test_extreme_rows():
+    """A row without entries gives nothing whatever its logits are (infinite
+    here); a teacher value beyond fp32 over T is as good as certain."""
+    cfg = DistillConfig(n=70, h=64, vocab=500, top_k=6, temperature=2.0 ** -8, flags=bpt.BPT_FLAG_DETERMINISTIC)
+    x, w, ids, v, _ = inputs(cfg)
+    ids[::2] = -1
+    v[1] = torch.tensor([1.0, -3e38, 3e38, 5.0, -math.inf, 0.0], device="cuda")
+    once = run(cfg, x, w, ids, v, None)
+    assert all(t.isfinite().all() for t in once)
+    x64, w64 = x.double(), w.double()
+    sure = ids[1].clone()
+    sure[[0, 1, 3, 4, 5]] = -1
+    same = ids.clone()
+    same[1] = sure
+    want, off = loss_of(cfg, x64, w64, same, v.clamp(max=1e30), None)
+    assert abs(float(once[0]) - float(want)) <= off + 2.0 ** -23 * abs(float(want))
+    big = x.clone()
+    big[::2] = 3e38
+    loss, dx, dw = run(cfg, big, w, ids, v, None)
+    assert torch.equal(loss, once[0]) and torch.equal(dx, once[1])
+
+
 def test_accumulated_and_repeated():
     cfg = CASES[8]
     x, w, ids, v, weight = inputs(cfg, True)
