@@ -28,7 +28,23 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   const bool small = op.form == GROUPED_NT && op.mean_rows <= 24;
   bool pair = tn ? op.M > BM : op.mean_rows >= 384;
   if (pair && gk::pair_units() <= 0) pair = false;
-  const int BN = small ? 64 : dual ? 128 : 256;
+  // One SM a tile and few rounds of tiles: half as wide ones, of three quarters of
+  // the time, where that takes less time in whole rounds, on average over tile
+  // counts around the one of even groups.  NT, us at 64 rows: 12 groups of 1000 x
+  // 2744 27.2 and 19.7, 3 of 2000 x 640 6.9 and 5.6 (one round either way); 40 of
+  // 776 x 1304 at 256 rows 46.6 and 49.1 (three rounds, four), at 66 very uneven
+  // ones 20.7 and 23.7 (one, two).
+  bool half = false;
+  if (!tn && !dual && op.epi == GROUPED_STORE && !small && !pair) {
+    const int64_t mt = std::min<int64_t>(op.groups, op.rows) * ((op.mean_rows + BM - 1) / BM), sms = std::max(1, sm_count());
+    auto rounds = [&](int64_t bn) {
+      double r = 0;
+      for (double by : {0.85, 1.0, 1.15}) r += ceil(by * (double)(mt * ((op.N + bn - 1) / bn)) / (double)sms);
+      return r;
+    };
+    half = 0.75 * rounds(128) < rounds(256);
+  }
+  const int BN = small ? 64 : dual || half ? 128 : 256;
   const int TM = small ? 32 : pair ? 2 * BM : BM;
   const int BNS = pair ? BN / 2 : BN;
   p.offsets = op.offsets;
@@ -91,8 +107,8 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   // band's rows in L2 while the other operand streams through once a band
   p.band = 4096 / TM;
   ProfScope prof(PROF_GEMM, 2.0 * (double)op.rows * (double)op.N * (double)(tn ? op.M * p.segs : op.K * p.segs) * (dual ? 2 : 1), 0.0, st);
-  if (op.form == GROUPED_NT) return launch_nt(p, op.epi, op.act, op.a_gather || small, pair, small, units, st);
-  if (op.form == GROUPED_NN) return launch_nn(p, op.epi, op.act, pair, units, st);
+  if (op.form == GROUPED_NT) return launch_nt(p, op.epi, op.act, op.a_gather || small, pair, BN, units, st);
+  if (op.form == GROUPED_NN) return launch_nn(p, op.epi, op.act, pair, BN, units, st);
   return launch_tn(p, op.a_gather, op.b_gather, pair, units, st);
 }
 

@@ -992,10 +992,10 @@ int launch(Params& p, int64_t units, cudaStream_t st) {
   return launch_dependent(kern, PAIR ? 2 * n : n, PAIR ? 2 : 1, dim3(threads<FORM, AG>()), (size_t)SMEM, st, p) == cudaSuccess ? 0 : 3;
 }
 
-// One translation unit per form (they compile in parallel); `small`: 64
-// columns a tile, `pair`: a pair of SMs a tile.
-int launch_nt(Params& p, int epi, int act, bool gather, bool pair, bool small, int64_t units, cudaStream_t st);
-int launch_nn(Params& p, int epi, int act, bool pair, int64_t units, cudaStream_t st);
+// One translation unit per form (they compile in parallel); bn: columns a tile,
+// pair: a pair of SMs a tile.
+int launch_nt(Params& p, int epi, int act, bool gather, bool pair, int bn, int64_t units, cudaStream_t st);
+int launch_nn(Params& p, int epi, int act, bool pair, int bn, int64_t units, cudaStream_t st);
 int launch_tn(Params& p, bool a_gather, bool b_gather, bool pair, int64_t units, cudaStream_t st);
 
 }  // namespace gg

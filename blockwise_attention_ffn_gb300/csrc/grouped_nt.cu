@@ -19,11 +19,13 @@ int launch_act(Params& p, bool pair, bool small, int64_t units, cudaStream_t st)
 
 }  // namespace
 
-int launch_nt(Params& p, int epi, int act, bool gather, bool pair, bool small, int64_t units, cudaStream_t st) {
+int launch_nt(Params& p, int epi, int act, bool gather, bool pair, int bn, int64_t units, cudaStream_t st) {
+  const bool small = bn == 64;
   constexpr int NT = GROUPED_NT, STORE = GROUPED_STORE;
   if (epi == GROUPED_STORE) {
     if (small) return launch<NT, STORE, 0, 64, true, false, false, false>(p, units, st);
     if (gather) return 1;
+    if (bn == 128) return launch<NT, STORE, 0, 128, false, false, false, false>(p, units, st);
     return pair ? launch<NT, STORE, 0, 256, false, false, false, true>(p, units, st)
                 : launch<NT, STORE, 0, 256, false, false, false, false>(p, units, st);
   }
