@@ -195,12 +195,6 @@ __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// arrive on another CTA's mbarrier (shared::cluster address), ordering this
-// CTA's memory alone: the products that wait for it read this CTA's copies
-// from this CTA's shared memory
-__device__ __forceinline__ void mbar_arrive_other(uint32_t cl_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cl_addr) : "memory");
-}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -716,8 +710,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
         const uint32_t d = tmem + (uint32_t)(acc * ACC_COLS);
         for (int kt = 0; kt < nk; ++kt) {
           const int s = it % STAGES;
-          if (!bounded_wait_w(&full[s], (it / STAGES) & 1, abort_flag, 103, p.err) ||
-              (COPY && !bounded_wait_w(&copied[s], (it / STAGES) & 1, abort_flag, 104, p.err))) {
+          // with copies in the pair's other CTA, its word of them is on `full` too
+          const bool landed = COPY && PAIR ? bounded_wait_cluster_w(&full[s], (it / STAGES) & 1, abort_flag, 103, p.err)
+                                           : bounded_wait_w(&full[s], (it / STAGES) & 1, abort_flag, 103, p.err);
+          if (!landed || (COPY && !bounded_wait_w(&copied[s], (it / STAGES) & 1, abort_flag, 104, p.err))) {
             ok = false;
             break;
           }
@@ -755,7 +751,10 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
         drain_wait(drain, 0);
       }
     } else if (COPY) {
-      // the pair's other CTA: word of every stage's copies to the one that issues
+      // The pair's other CTA: word of every stage's copies to the one that issues.
+      // The products there read this CTA's shared memory, so the arrival releases
+      // at the cluster's scope and the issuing warp's wait acquires at it; one lane
+      // does it (from each copying thread, a release takes 1000 cycles a stage).
       const uint32_t full0 = cluster_addr(smem_u32(full), 0);
       uint32_t it = 0;
       bool ok = true;
@@ -774,7 +773,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_other(full0 + 8u * (uint32_t)s);
+          if (lane == 0) mbar_arrive_cluster(full0 + 8u * (uint32_t)s);
         }
       }
     }
