@@ -753,8 +753,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
     } else if (COPY) {
       // The pair's other CTA: word of every stage's copies to the one that issues.
       // The products there read this CTA's shared memory, so the arrival releases
-      // at the cluster's scope and the issuing warp's wait acquires at it; one lane
-      // does it (from each copying thread, a release takes 1000 cycles a stage).
+      // that at the cluster's scope and the issuing warp's wait acquires at it.
       const uint32_t full0 = cluster_addr(smem_u32(full), 0);
       uint32_t it = 0;
       bool ok = true;
@@ -773,7 +772,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(full0 + 8u * (uint32_t)s);
+          if (lane == 0) mbar_arrive_cluster_smem(full0 + 8u * (uint32_t)s);
         }
       }
     }

@@ -1,7 +1,8 @@
 """How the kernels hand shared memory from one CTA of a cluster to another:
-an arrival on another CTA's barrier must release at the cluster's scope (the
-default scope is the CTA, which orders nothing for the other one), and a kernel
-that sends such arrivals must wait for them with an acquire at that scope.
+an arrival on another CTA's barrier must release at the cluster's scope, itself
+or by a fence before it (the default scope is the CTA, which orders nothing for
+the other one), and a kernel that sends such arrivals must wait for them with an
+acquire at that scope.
 Read from the sources: a missing order shows in no result that can be relied
 on."""
 import glob
@@ -20,11 +21,13 @@ def sources():
 def test_arrivals_on_other_ctas_release_at_cluster_scope():
     found = 0
     for name, text in sources().items():
-        for line in text.splitlines():
-            for op in re.findall(r"\bmbarrier\.arrive[\w.:]*", line.split("//")[0]):
+        code = re.sub(r"//[^\n]*", "", text)
+        for asm in re.findall(r"\basm volatile\((.*?)\);", code, re.S):
+            for op in re.findall(r"\bmbarrier\.arrive[\w.:]*", asm):
                 if "shared::cluster" in op and not op.startswith("mbarrier.arrive.expect_tx"):
                     found += 1
-                    assert ".release.cluster" in op, f"{name}: {op}"
+                    fenced = re.search(r"fence\.release\.[\w.:]*\.cluster;.*mbarrier\.arrive\.relaxed\.cluster", asm, re.S)
+                    assert ".release.cluster" in op or fenced, f"{name}: {op}"
     assert found
 
 
@@ -37,7 +40,7 @@ def test_kernels_that_arrive_across_wait_at_cluster_scope():
             continue
         code = re.sub(r"//[^\n]*", "", text)
         bars = dict(re.findall(r"(\w+) = (?:PAIR \? )?cluster_addr\(smem_u32\((\w+)\), 0\)", code))
-        for var in set(re.findall(r"mbar_arrive_cluster\((\w+)", code)):
+        for var in set(re.findall(r"mbar_arrive_cluster(?:_smem)?\((\w+)", code)):
             if var in bars:
                 found += 1
                 assert re.search(r"bounded_wait_cluster_w\(&%s\[" % bars[var], code), f"{name}: {bars[var]}"
