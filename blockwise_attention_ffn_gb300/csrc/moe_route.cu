@@ -56,8 +56,9 @@ struct RouteParams {
   unsigned int* err;
 };
 
-__device__ __forceinline__ uint32_t sort_key(float v) {  // rises with v; 0: not to be chosen
-  const uint32_t u = __float_as_uint(v);
+// rises with v, equal for equal values; 0: not to be chosen
+__device__ __forceinline__ uint32_t sort_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);  // -0 becomes +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
