@@ -565,8 +565,9 @@ __device__ __forceinline__ void distill_tile(const GemmParams& p, uint32_t tbase
   float l2 = 0.f, w = 0.f;
   if (m < p.M) {
     l2 = p.rowf[m] * 1.4426950408889634f;
-    w = p.rowp[m] * p.scale;
-    if (p.roww) w *= p.roww[m];
+    // the row's weight first: where it is 0 (padding) the mass may be infinite
+    const float r = p.roww ? p.roww[m] : 1.f;
+    w = r != 0.f ? p.rowp[m] * (p.scale * r) : 0.f;
   }
 #pragma unroll 1
   for (int c = 0; c < EPI_COLS / 32; ++c) {
