@@ -891,7 +891,8 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
               uint64_t y;
               if constexpr (DUAL) {
                 const uint64_t up = f2(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]));
-                y = mul2(mul2(z, up), sigmoid_of(mul2(z, f2(-1.4426950408889634f, -1.4426950408889634f))));
+                // the gate first: a closed one is 0 whatever z up would be
+                y = mul2(mul2(z, sigmoid_of(mul2(z, f2(-1.4426950408889634f, -1.4426950408889634f)))), up);
               } else {
                 uint64_t slope;
                 gelu2<ACT>(z, y, slope);
@@ -925,7 +926,7 @@ __global__ void __launch_bounds__(threads<FORM, AG>(), 1) grouped_kernel(const _
               const uint64_t sg = sigmoid_of(mul2(g, f2(-1.4426950408889634f, -1.4426950408889634f)));
               const uint64_t si = mul2(g, sg);  // silu(g)
               act = mul2(si, u);
-              x = mul2(mul2(wa, u), fma2(si, sub2(f2(1.f, 1.f), sg), sg));
+              x = mul2(wa, mul2(u, fma2(si, sub2(f2(1.f, 1.f), sg), sg)));  // the slope first, as above
               const float2 y = f2split(mul2(wa, si));
               dv[j] = pack_bf16(y.x, y.y);
             } else {

@@ -37,3 +37,51 @@ def test_zeros_of_both_signs_are_equal(n, E, k, lt):
     for got, want in ((r.ids, ids), (r.offsets, offsets), (r.order, order), (r.slot, slot)):
         assert torch.equal(got.long(), want)
     assert torch.allclose(r.weights.double(), w, rtol=(64 + E / 4) * U, atol=0)
+
+
+# few rows (rows one by one in inference), 32-row tiles, one SM a tile, a pair
+SIZES = [(5, 64), (40, 8), (300, 4), (1000, 2)]
+
+
+def outlying(n, h, f, E, k, act):
+    """Inputs of which every third position alone has a first column, 2^60."""
+    r, x, w1, w3, w2, dy = ffn_inputs(n, h, f, E, k, act, False, F32)
+    big = torch.arange(n, device="cuda") % 3 == 1
+    x[:, 0] = 0
+    x[big, 0] = 2.0 ** 60
+    return r, x, w1, w3, w2, dy, big
+
+
+def both_passes(cfg, r, x, w1, w3, w2, dy):
+    ws, saved = spaces(cfg)
+    y, plain, dx = (torch.full_like(x, float("nan")) for _ in range(3))
+    dwt = torch.full_like(r.weights, float("nan"))
+    dm = [None if m is None else torch.full(m.shape, float("nan"), device="cuda") for m in (w1, w3, w2)]
+    bpt.bpt_moe_ffn_fwd(cfg, r, x, w1, w3, w2, plain, None, ws)
+    ws.fill_(255)
+    bpt.bpt_moe_ffn_fwd(cfg, r, x, w1, w3, w2, y, saved, ws)
+    ws.fill_(255)
+    bpt.bpt_moe_ffn_bwd(cfg, r, x, w1, w3, w2, saved, dy, dx, dwt, *dm, ws)
+    sync()
+    return y, plain, dx, dwt, dm
+
+
+@pytest.mark.parametrize("n,E", SIZES)
+def test_a_closed_gate_closes_any_up_product(n, E):
+    """silu(g) u is 0 for g far below zero, also where g u is beyond fp32
+    (2^130 here), and so are the gradients, also where dy u is beyond it."""
+    h, f, k = 72, 136, 2
+    cfg = MoeConfig(n=n, h=h, ffn_dim=f, n_experts=E, top_k=k)
+    r, x, w1, w3, w2, dy, big = outlying(n, h, f, E, k, 2)
+    w1[:, :, 0], w3[:, :, 0] = -2.0 ** 10, 1.0  # g = -2^70, u = 2^60
+    dy[big] *= 2.0 ** 70
+    y, plain, dx, dwt, dm = both_passes(cfg, r, x, w1, w3, w2, dy)
+    for t in (y, plain, dx, dwt):
+        assert bool((t[big] == 0).all())
+    leaves = [t.double().requires_grad_() for t in (x, r.weights, w1, w3, w2)]
+    want = network(r, 2, *leaves)
+    grads = torch.autograd.grad(want, leaves, dy.double())
+    near(y, want.detach(), 3, "y")
+    near(plain, want.detach(), 3, "y without saved")
+    for name, got, g, c in zip(("dx", "dweights", "dw1", "dw3", "dw2"), (dx, dwt, *dm), grads, (5, 3, 4, 4, 4)):
+        near(got, g, c, name)
