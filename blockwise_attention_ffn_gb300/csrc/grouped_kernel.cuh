@@ -237,8 +237,8 @@ __device__ __forceinline__ uint64_t sigmoid_of(uint64_t x) { return rcp2(add2(ex
 template <int ACT>
 __device__ __forceinline__ void gelu2(uint64_t z, uint64_t& g, uint64_t& d) {
   auto c2 = [](float v) { return f2(v, v); };
-  const uint64_t zz = mul2(z, z);
   if constexpr (ACT == BPT_ACT_GELU_ERF) {
+    const uint64_t zz = mul2(z, z);
     const float2 v = f2split(z);
     const uint64_t t = rcp2(fma2(f2(fabsf(v.x), fabsf(v.y)), c2(0.3275911f * 0.70710678118654752f), c2(1.f)));
     uint64_t poly = fma2(c2(1.061405429f), t, c2(-1.453152027f));
@@ -252,11 +252,13 @@ __device__ __forceinline__ void gelu2(uint64_t z, uint64_t& g, uint64_t& d) {
     g = mul2(z, cdf);
     d = fma2(mul2(z, e), c2(0.3989422804014327f), cdf);
   } else {
-    const float c = 1.5957691216057308f;
-    const uint64_t s = sigmoid_of(mul2(mul2(z, fma2(zz, c2(0.044715f), c2(1.f))), c2(-1.4426950408889634f * c)));
+    const float c = 1.5957691216057308f, l2e = 1.4426950408889634f;
+    const uint64_t kz = mul2(z, c2(-l2e * c * 0.044715f));
+    const uint64_t s = sigmoid_of(mul2(z, fma2(kz, z, c2(-l2e * c))));
     g = mul2(z, s);
     const uint64_t rest = mul2(g, sub2(c2(1.f), s));
-    d = fma2(rest, fma2(zz, c2(3.f * 0.044715f * c), c2(c)), s);
+    // s + rest c (1 + 3 * 0.044715 z^2), z by z: far out rest is 0 where z^2 is infinite
+    d = fma2(mul2(rest, z), mul2(kz, c2(-3.f / l2e)), fma2(rest, c2(c), s));
   }
 }
 

@@ -85,3 +85,28 @@ def test_a_closed_gate_closes_any_up_product(n, E):
     near(plain, want.detach(), 3, "y without saved")
     for name, got, g, c in zip(("dx", "dweights", "dw1", "dw3", "dw2"), (dx, dwt, *dm), grads, (5, 3, 4, 4, 4)):
         near(got, g, c, name)
+
+
+@pytest.mark.parametrize("n,E", SIZES)
+@pytest.mark.parametrize("act", [0, 1])
+def test_far_out_gelu(n, E, act):
+    """Far out the GeLU is z or 0 and its slope 1 or 0, also where z^2 is
+    beyond fp32 (z = 2^70 and -2^70 here).  The other positions' results are
+    looked at by themselves: beside 2^70 they would not count."""
+    h, f, k = 72, 136, 2
+    cfg = MoeConfig(n=n, h=h, ffn_dim=f, n_experts=E, top_k=k, act=act)
+    r, x, w1, _, w2, dy, big = outlying(n, h, f, E, k, act)
+    w1[:, :, 0] = 2.0 ** 10
+    w1[:, 1::2, 0] = -2.0 ** 10
+    y, plain, dx, dwt, (dw1, _, dw2) = both_passes(cfg, r, x, w1, None, w2, dy)
+    leaves = [t.double().requires_grad_() for t in (x, r.weights, w1, w2)]
+    want = network(r, act, *leaves[:3], None, leaves[3])
+    gx, gwt, gw1, gw2 = torch.autograd.grad(want, leaves, dy.double())
+    for rows in (big, ~big):
+        near(y[rows], want.detach()[rows], 3, "y")
+        near(plain[rows], want.detach()[rows], 3, "y without saved")
+        near(dx[rows], gx[rows], 5, "dx")
+        near(dwt[rows], gwt[rows], 3, "dweights")
+    near(dw1[:, :, 0], gw1[:, :, 0], 4, "dw1's first column")
+    near(dw1[:, :, 1:], gw1[:, :, 1:], 4, "dw1's others")
+    near(dw2, gw2, 4, "dw2")
