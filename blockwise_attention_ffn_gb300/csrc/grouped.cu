@@ -66,6 +66,7 @@ int grouped_gemm(const GroupedOp& op, cudaStream_t st) {
   p.row_weight = op.row_weight;
   p.row_weight_f32 = op.row_weight_f32;
   p.part = op.part;
+  p.span = op.span;
   p.err = device_error_word();
   if (!p.err) return 3;
   int64_t units, mt_all;

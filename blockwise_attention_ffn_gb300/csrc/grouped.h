@@ -53,6 +53,7 @@ struct GroupedOp {
   const void* row_weight = nullptr;  // [rows] by pair (order[r]), fp32 or bf16
   bool row_weight_f32 = true;
   float* part = nullptr;
+  int2* span = nullptr;  // if given: the rows [x, y) that the groups hold; x = -1: some offsets are bad
 };
 
 // Returns 0 or a BPT_* status.

@@ -73,6 +73,7 @@ struct Params {
   const void* row_weight;
   int row_weight_f32;
   float* part;
+  int2* span;  // for the rows that the groups hold (grouped.h), or NULL
   unsigned int* err;
 };
 
@@ -84,6 +85,7 @@ template <bool TN, int TM>
 __device__ __forceinline__ void lay_out(const Params& p, int* s_unit, int* s_lo, int* s_cnt) {
   const int lane = lane_id();
   int base = 0, end = 0;  // units and the largest end of the groups before
+  bool odd = false;
   for (int e0 = 0; e0 < p.groups; e0 += 32) {
     const int e = e0 + lane;
     const bool in = e < p.groups;
@@ -101,6 +103,7 @@ __device__ __forceinline__ void lay_out(const Params& p, int* s_unit, int* s_lo,
     end = max(end, __shfl_sync(0xffffffffu, top, 31));
     const bool ok = inside && lo >= before;
     if (in && !ok && blockIdx.x == 0) report_bad_data(p.err, BPT_GROUPED_BAD_OFFSET_SITE);
+    odd |= in && !ok;
     const int cnt = ok ? hi - lo : 0;
     lo = ok ? lo : 0;
     if (in) {
@@ -116,7 +119,11 @@ __device__ __forceinline__ void lay_out(const Params& p, int* s_unit, int* s_lo,
     if (in) s_unit[e + 1] = base + u;
     base += __shfl_sync(0xffffffffu, u, 31);
   }
-  if (lane == 0) s_unit[0] = 0;
+  odd = __any_sync(0xffffffffu, odd);
+  if (lane == 0) {
+    s_unit[0] = 0;
+    if (p.span && blockIdx.x == 0) *p.span = make_int2(odd ? -1 : p.offsets[0], p.offsets[p.groups]);
+  }
 }
 
 // TN: the groups by falling row count, equal ones in their order, by all

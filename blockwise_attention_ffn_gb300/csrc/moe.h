@@ -16,6 +16,23 @@ struct MoeDims {
 // 0 or a BPT_* status
 int moe_dims(const bpt_moe_config* cfg, MoeDims* out);
 
+// Whether the offsets lo, hi of a group of `rows` rows in all fall or leave
+// them.  Where none do, the groups hold [offsets[0], offsets[E]) between them.
+__device__ __forceinline__ bool bad_offsets(int lo, int hi, int64_t rows) { return lo < 0 || hi < lo || hi > rows; }
+// The group that row r is of (E: none), as the grouped GEMM lays them out where
+// some offsets are bad: those groups hold nothing, nor do those that start
+// before an earlier one's end.
+static __device__ __noinline__ int group_of(const int32_t* offsets, int E, int64_t rows, int r) {
+  int end = 0;
+  for (int e = 0; e < E; ++e) {
+    const int lo = offsets[e], hi = offsets[e + 1];
+    if (bad_offsets(lo, hi, rows)) continue;
+    if (lo >= end && r >= lo && r < hi) return e;
+    end = max(end, hi);
+  }
+  return E;
+}
+
 // The forward for so few rows that an expert's matrices meet about one
 // (moe_few.cu): whether they are, its workspace, its launches.
 bool moe_few_rows(const MoeDims& D);

@@ -66,15 +66,17 @@ namespace {
 
 // One sum over each position's choices: out[t, :] = sum_j w_tj rows[slot_tj, :]
 // (w NULL: 1), j in order.  8 columns a thread; behind those blocks, with
-// `part`, the weights' gradients: dw[pair] = sum over the parts in order.
+// `part`, the weights' gradients: dw[pair] = sum over the parts in order.  Rows
+// that no expert's offsets hold were not written: their pairs add nothing.
 struct CombineParams {
   const __nv_bfloat16* rows;
-  const int* slot;
+  const int *slot, *offsets;
   const void* weight;
   int weight_f32;
   __nv_bfloat16* out;
   int64_t n, pairs;
-  int h8, k;
+  int h8, k, E;
+  const int2* span;  // rows that the offsets hold; x < 0: some of them are bad
   int64_t blocks;  // of the sum
   const float* part;
   int nparts;
@@ -83,10 +85,45 @@ struct CombineParams {
 
 constexpr int CT = 128;
 
+// The same where some offsets are bad, one value at a time: rows of the groups
+// that are left.
+static __device__ __noinline__ void combine_odd(const CombineParams& p) {
+  auto row = [&](int64_t q) {  // of pair q; -1: none
+    const int at = p.slot[q];
+    return group_of(p.offsets, p.E, p.pairs, at) < p.E ? at : -1;
+  };
+  if (blockIdx.x < p.blocks) {
+    const int64_t i = (int64_t)blockIdx.x * CT + threadIdx.x;
+    if (i >= p.n * p.h8) return;
+    const int64_t t = i / p.h8, c = (i - t * p.h8) * 8;
+    for (int q = 0; q < 8; ++q) {
+      float s = 0.f;
+      for (int64_t j = t * p.k; j < (t + 1) * p.k; ++j) {
+        const int at = row(j);
+        const float w = !p.weight     ? 1.f
+                        : p.weight_f32 ? reinterpret_cast<const float*>(p.weight)[j]
+                                       : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.weight)[j]);
+        if (at >= 0) s = fmaf(w, __bfloat162float(p.rows[at * (int64_t)p.h8 * 8 + c + q]), s);
+      }
+      p.out[i * 8 + q] = __float2bfloat16(s);
+    }
+    return;
+  }
+  const int64_t q = ((int64_t)blockIdx.x - p.blocks) * CT + threadIdx.x;
+  if (q >= p.pairs) return;
+  const int at = row(q);
+  float s = 0.f;
+  for (int i = 0; i < p.nparts && at >= 0; ++i) s += p.part[(int64_t)i * p.pairs + at];
+  if (p.weight_f32) reinterpret_cast<float*>(p.dweight)[q] = s;
+  else reinterpret_cast<__nv_bfloat16*>(p.dweight)[q] = __float2bfloat16(s);
+}
+
 template <int ROWS>
-__global__ void __launch_bounds__(CT) combine_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(CT) combine_kernel(const __grid_constant__ CombineParams p) {
   wait_for_previous();
   let_next_start();
+  const int2 span = *p.span;
+  if (span.x < 0) return combine_odd(p);
   if (blockIdx.x < p.blocks) {
     const int64_t i = (int64_t)blockIdx.x * CT + threadIdx.x;
     if (i >= p.n * p.h8) return;
@@ -105,7 +142,7 @@ __global__ void __launch_bounds__(CT) combine_kernel(const CombineParams p) {
       for (int j = 0; j < ROWS; ++j) at[j] = j0 + j < p.k ? slot[j0 + j] : -1;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
-        const bool some = at[j] >= 0 && at[j] < p.pairs;
+        const bool some = at[j] >= span.x && at[j] < span.y;
         // without a row: the first one, not used
         asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
                      : "=r"(u[j].x), "=r"(u[j].y), "=r"(u[j].z), "=r"(u[j].w)
@@ -117,7 +154,7 @@ __global__ void __launch_bounds__(CT) combine_kernel(const CombineParams p) {
       }
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
-        const bool some = at[j] >= 0 && at[j] < p.pairs;
+        const bool some = at[j] >= span.x && at[j] < span.y;
         const uint32_t v[4] = {some ? u[j].x : 0u, some ? u[j].y : 0u, some ? u[j].z : 0u, some ? u[j].w : 0u};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -138,17 +175,19 @@ __global__ void __launch_bounds__(CT) combine_kernel(const CombineParams p) {
   if (q >= p.pairs) return;
   const int at = p.slot[q];
   float s = 0.f;
-  if (at >= 0 && at < p.pairs)
+  if (at >= span.x && at < span.y)
     for (int i = 0; i < p.nparts; ++i) s += p.part[(int64_t)i * p.pairs + at];
   if (p.weight_f32) reinterpret_cast<float*>(p.dweight)[q] = s;
   else reinterpret_cast<__nv_bfloat16*>(p.dweight)[q] = __float2bfloat16(s);
 }
 
-int combine(const MoeDims& D, const void* rows, const int* slot, const void* weight, void* out, const float* part, int nparts,
-            void* dweight, cudaStream_t st) {
+int combine(const MoeDims& D, const void* rows, const bpt_moe_route* r, const int2* span, const void* weight, void* out, const float* part,
+            int nparts, void* dweight, cudaStream_t st) {
   CombineParams p;
   p.rows = reinterpret_cast<const __nv_bfloat16*>(rows);
-  p.slot = slot;
+  p.slot = r->slot;
+  p.offsets = r->offsets;
+  p.span = span;
   p.weight = weight;
   p.weight_f32 = D.weight_bytes == 4;
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
@@ -156,6 +195,7 @@ int combine(const MoeDims& D, const void* rows, const int* slot, const void* wei
   p.pairs = D.pairs;
   p.h8 = (int)(D.h / 8);
   p.k = (int)D.k;
+  p.E = (int)D.E;
   p.blocks = (D.n * p.h8 + CT - 1) / CT;
   p.part = part;
   p.nparts = nparts;
@@ -190,16 +230,19 @@ size_t plan_saved(const MoeDims& D, void* base, Saved* s) {
 }
 struct FwdWs {
   void *act, *ys;
+  int2* span;
 };
 size_t plan_fwd(const MoeDims& D, void* base, FwdWs* w) {
   Planner pl{reinterpret_cast<uint8_t*>(base)};
   w->act = pl.take(D.pairs * D.f * 2);
   w->ys = pl.take(D.pairs * D.h * 2);
+  w->span = reinterpret_cast<int2*>(pl.take(8));
   return moe_few_rows(D) ? std::max(pl.off, moe_few_ws_bytes(D)) : pl.off;
 }
 struct BwdWs {
   void *dg, *du, *aw, *dxs;
   float* part;
+  int2* span;
 };
 size_t plan_bwd(const MoeDims& D, void* base, BwdWs* w) {
   Planner pl{reinterpret_cast<uint8_t*>(base)};
@@ -208,6 +251,7 @@ size_t plan_bwd(const MoeDims& D, void* base, BwdWs* w) {
   w->aw = pl.take(D.pairs * D.f * 2);
   w->dxs = pl.take(D.pairs * D.h * 2);
   w->part = reinterpret_cast<float*>(pl.take(2 * grouped_part_tiles(D.f) * D.pairs * 4));
+  w->span = reinterpret_cast<int2*>(pl.take(8));
   return pl.off;
 }
 
@@ -304,9 +348,10 @@ int bpt_moe_ffn_fwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const voi
     op.a_rows = D.pairs;
     op.w = w2;
     op.out = W.ys;
+    op.span = W.span;
     if ((rc = grouped_gemm(op, st))) return rc;
   }
-  if ((rc = combine(D, W.ys, r->slot, r->weights, y, nullptr, 0, nullptr, st))) return rc;
+  if ((rc = combine(D, W.ys, r, W.span, r->weights, y, nullptr, 0, nullptr, st))) return rc;
   return D.debug ? debug_finish(st) : BPT_OK;
 }
 
@@ -370,6 +415,7 @@ int bpt_moe_ffn_bwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const voi
     op.w = w1;
     op.w2 = w3;
     op.out = W.dxs;
+    op.span = W.span;
     if ((rc = grouped_gemm(op, st))) return rc;
   }
   {
@@ -406,7 +452,7 @@ int bpt_moe_ffn_bwd(const bpt_moe_config* cfg, const bpt_moe_route* r, const voi
     op.beta = D.accum ? 1.f : 0.f;
     if ((rc = grouped_gemm(op, st))) return rc;
   }
-  if ((rc = combine(D, W.dxs, r->slot, nullptr, dx, W.part, (int)(2 * grouped_part_tiles(D.f)), dweights, st))) return rc;
+  if ((rc = combine(D, W.dxs, r, W.span, nullptr, dx, W.part, (int)(2 * grouped_part_tiles(D.f)), dweights, st))) return rc;
   return D.debug ? debug_finish(st) : BPT_OK;
 }
 

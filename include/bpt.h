@@ -552,7 +552,8 @@ int bpt_moe_route_bwd(const bpt_moe_config* cfg, const void* logits, const bpt_m
  *   x, y      [n, h] bf16;  w1, w3 [E, f, h], w2 [E, h, f] bf16 (w3: SwiGLU)
  *   r         weights, offsets, order and slot are read (ids is not); any
  *             grouping of pairs in this form will do.  An order or slot entry
- *             outside its range is taken as none.
+ *             outside its range is taken as none, and so is a slot among the
+ *             rows of no expert; bad offsets as for bpt_grouped_gemm.
  *   saved     bpt_moe_saved_bytes(cfg) for the backward (n k f bf16 values,
  *             twice with SwiGLU), or NULL: inference
  *   ws        bpt_moe_ffn_workspace_bytes(cfg, pass), one per call in flight

@@ -110,3 +110,83 @@ def test_far_out_gelu(n, E, act):
     near(dw1[:, :, 0], gw1[:, :, 0], 4, "dw1's first column")
     near(dw1[:, :, 1:], gw1[:, :, 1:], 4, "dw1's others")
     near(dw2, gw2, 4, "dw2")
+
+
+def rows_of(offsets, pairs):
+    """The rows of each group as the products take them: none for a group whose
+    offsets fall, leave [0, pairs] or start before an earlier one's end."""
+    rows, end = [], 0
+    for lo, hi in zip(offsets, offsets[1:]):
+        inside = 0 <= lo <= hi <= pairs
+        rows.append(range(lo, hi) if inside and lo >= end else range(0))
+        end = max(end, hi if inside else 0)
+    return rows
+
+
+def malformed(how, offsets, pairs):
+    """Offsets of which some rows are in no group, and whether that is an error."""
+    E = len(offsets) - 2
+    o, used = list(offsets), [e for e in range(E) if offsets[e + 1] > offsets[e]]
+    if how == "cut":        # the last rows are in no group
+        last = used[-1]
+        o[last + 1:E + 1] = [o[last]] * (E - last)
+        return o, False
+    if how == "late":       # nor are the first
+        first = used[0]
+        o[:first + 1] = [o[first + 1]] * (first + 1)
+        return o, False
+    mid = len(used) // 2
+    e, after = used[mid], used[mid + 1]
+    if how == "far":        # a group ends behind the last row
+        o[e + 1] = pairs + 1000
+    if how == "negative":   # the first one begins before the first row
+        o[used[0]] = -5
+    if how == "falling":    # a later one begins before the end of an earlier one
+        o[e] = offsets[e + 1]
+        o[e + 1:after + 1] = [offsets[e]] * (after - e)
+    return o, True
+
+
+@pytest.mark.parametrize("n,E", [(40, 8), (300, 4), (1600, 4)])
+@pytest.mark.parametrize("how", ["cut", "late", "far", "negative", "falling"])
+@pytest.mark.parametrize("act", [2, 0])
+def test_pairs_in_no_group_add_nothing(n, E, how, act):
+    """Rows that no expert's offsets hold: their pairs add nothing to y, dx and
+    dweights, whatever the workspace holds."""
+    h, f, k = 72, 136, 2
+    cfg = MoeConfig(n=n, h=h, ffn_dim=f, n_experts=E, top_k=k, act=act)
+    r, x, w1, w3, w2, dy = ffn_inputs(n, h, f, E, k, act, False, F32)
+    offsets, error = malformed(how, r.offsets.tolist(), n * k)
+    bad = bpt.MoeRoute(r.ids, r.weights, torch.tensor(offsets, dtype=torch.int32, device="cuda"), r.order, r.slot)
+    # the same network with the pairs of the rows that are left
+    ids = torch.full((n * k,), -1, device="cuda")
+    for e, rows in enumerate(rows_of(offsets[:E + 1], n * k)):
+        ids[r.order[list(rows)].long()] = e
+    ids = ids.view(n, k)
+    assert bool((ids < 0).any()) and bool((ids >= 0).any())
+    left = bpt.MoeRoute(ids, r.weights, None, None, None)
+    ws, saved = spaces(cfg)
+    y, plain, dx, dwt = *(torch.full_like(x, float("nan")) for _ in range(3)), torch.full_like(r.weights, float("nan"))
+    dm = [None if m is None else torch.full(m.shape, float("nan"), device="cuda") for m in (w1, w3, w2)]
+    for call in (lambda: bpt.bpt_moe_ffn_fwd(cfg, bad, x, w1, w3, w2, plain, None, ws),
+                 lambda: bpt.bpt_moe_ffn_fwd(cfg, bad, x, w1, w3, w2, y, saved, ws),
+                 lambda: bpt.bpt_moe_ffn_bwd(cfg, bad, x, w1, w3, w2, saved, dy, dx, dwt, *dm, ws)):
+        ws.fill_(255)
+        call()
+        torch.cuda.synchronize()
+        assert bpt.bpt_last_device_error() == ((bpt.BPT_EINVAL, bpt.BPT_GROUPED_BAD_OFFSET_SITE) if error else (bpt.BPT_OK, 0))
+    leaves = [t.double().requires_grad_() for t in (x, r.weights, w1, w3, w2) if t is not None]
+    if w3 is None:
+        leaves.insert(3, None)
+    want = network(left, act, leaves[0], *leaves[1:])
+    grads = iter(torch.autograd.grad(want, [t for t in leaves if t is not None], dy.double()))
+    near(y, want.detach(), 3, "y")
+    near(plain, want.detach(), 3, "y without saved")
+    near(dx, next(grads), 5, "dx")
+    near(dwt, next(grads), 3, "dweights")
+    for name, got in zip(("dw1", "dw3", "dw2"), dm):
+        if got is not None:
+            near(got, next(grads), 4, name)
+    assert bool((dwt[ids < 0] == 0).all())
+    gone = (ids < 0).all(-1)
+    assert bool((y[gone] == 0).all()) and bool((plain[gone] == 0).all()) and bool((dx[gone] == 0).all())
