@@ -44,16 +44,19 @@ struct FewParams {
 };
 
 // The expert of row r of the order (E: none) into *s, by all threads of the
-// block; offsets as the grouped GEMM takes them.
-__device__ __forceinline__ void find_expert(const FewParams& p, int r, int* s) {
+// block, where no offsets are bad; whether this thread saw bad ones.
+__device__ __forceinline__ bool find_expert(const FewParams& p, int r, int* s) {
+  bool bad = false;
   for (int e = threadIdx.x; e < p.E; e += THREADS) {
     const int lo = p.offsets[e], hi = p.offsets[e + 1];
-    if (lo < 0 || hi < lo || hi > p.pairs) {
+    if (bad_offsets(lo, hi, p.pairs)) {
       if (blockIdx.x == 0) report_bad_data(p.err, BPT_GROUPED_BAD_OFFSET_SITE);
+      bad = true;
     } else if (r >= lo && r < hi) {
       atomicMin(s, e);
     }
   }
+  return bad;
 }
 
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p, bool in) {
@@ -92,9 +95,8 @@ __global__ void __launch_bounds__(THREADS) few_act_kernel(const FewParams p) {
   let_next_start();
   const int pair = p.order[r];
   __syncthreads();
-  find_expert(p, r, &s_e);
-  __syncthreads();
-  const int e = s_e;
+  const bool odd = __syncthreads_or(find_expert(p, r, &s_e));
+  const int e = odd ? group_of(p.offsets, p.E, p.pairs, r) : s_e;
   if (e == p.E || i0 >= p.f) return;  // f is a multiple of 8: a warp's units are all there or none
   const bool some = pair >= 0 && pair < p.pairs;
   const __nv_bfloat16* x = p.x + (int64_t)(some ? pair / p.k : 0) * p.h;
@@ -160,11 +162,15 @@ __global__ void __launch_bounds__(THREADS) few_out_kernel(const FewParams p) {
   // the routes are older than the activations: the kernel before has waited
   // for them before it let this one start
   __syncthreads();
+  bool bad = false;
   for (int j = 0; j < p.k; ++j) {
     const int r = p.slot[t * p.k + j];
-    if (r >= 0 && r < p.pairs) find_expert(p, r, &s_e[j]);
+    if (r >= 0 && r < p.pairs) bad |= find_expert(p, r, &s_e[j]);
   }
-  __syncthreads();
+  if (__syncthreads_or(bad)) {
+    if ((int)threadIdx.x < p.k) s_e[threadIdx.x] = group_of(p.offsets, p.E, p.pairs, p.slot[t * p.k + threadIdx.x]);
+    __syncthreads();
+  }
   if (in)
     for (int j = js; j < p.k; j += JS)
       if (s_e[j] < p.E)  // on their way to L2 meanwhile

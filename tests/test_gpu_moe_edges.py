@@ -147,12 +147,12 @@ def malformed(how, offsets, pairs):
     return o, True
 
 
-@pytest.mark.parametrize("n,E", [(40, 8), (300, 4), (1600, 4)])
+@pytest.mark.parametrize("n,E", [(3, 64), (9, 96), (40, 8), (300, 4), (1600, 4)])
 @pytest.mark.parametrize("how", ["cut", "late", "far", "negative", "falling"])
 @pytest.mark.parametrize("act", [2, 0])
 def test_pairs_in_no_group_add_nothing(n, E, how, act):
     """Rows that no expert's offsets hold: their pairs add nothing to y, dx and
-    dweights, whatever the workspace holds."""
+    dweights, whatever the workspace holds and by which path the rows go."""
     h, f, k = 72, 136, 2
     cfg = MoeConfig(n=n, h=h, ffn_dim=f, n_experts=E, top_k=k, act=act)
     r, x, w1, w3, w2, dy = ffn_inputs(n, h, f, E, k, act, False, F32)
