@@ -524,10 +524,13 @@ def bpt_moe_route_fwd(cfg, logits, route, loss, ws, stream=None) -> None:
 
 def bpt_moe_route_bwd(cfg, logits, route, dweights, dloss, dlogits, stream=None) -> None:
     """dlogits [n, E] of the weights' gradients dweights [n, k] and of dloss
-    times the losses."""
+    times the losses.  Of route it reads ids and offsets; the others may be
+    None."""
     import torch
     where, dev = "bpt_moe_route_bwd", torch.cuda.current_device()
-    c, r, kind, n = _moe_record(cfg)[0], _moe_route(where, cfg, route, dev), _dtype(cfg.logits_dtype), cfg.n * cfg.n_experts
+    c, kind, n, i32 = _moe_record(cfg)[0], _dtype(cfg.logits_dtype), cfg.n * cfg.n_experts, torch.int32
+    r = BptMoeRoute(ids=_want(where, "ids", route.ids, i32, cfg.n * cfg.top_k, dev),
+                    offsets=_want(where, "offsets", route.offsets, i32, cfg.n_experts + 2, dev))
     _check(lib().bpt_moe_route_bwd(
         c, _want(where, "logits", logits, kind, n, dev), r,
         _want(where, "dweights", dweights, _dtype(cfg.weights_dtype), cfg.n * cfg.top_k, dev), float(dloss),

@@ -190,3 +190,21 @@ def test_pairs_in_no_group_add_nothing(n, E, how, act):
     assert bool((dwt[ids < 0] == 0).all())
     gone = (ids < 0).all(-1)
     assert bool((y[gone] == 0).all()) and bool((plain[gone] == 0).all()) and bool((dx[gone] == 0).all())
+
+
+def test_route_backward_takes_what_it_reads():
+    """ids and offsets: the other tensors of a route may be gone by then."""
+    cfg = MoeConfig(n=70, h=8, ffn_dim=8, n_experts=12, top_k=3, balance_coef=0.1, z_coef=0.01)
+    g = gen(5)
+    z, dw = torch.randn(70, 12, generator=g, device="cuda"), torch.randn(70, 3, generator=g, device="cuda")
+    r, loss = bpt.alloc_moe_route(cfg), torch.empty(1, device="cuda")
+    bpt.bpt_moe_route_fwd(cfg, z, r, loss, bpt.alloc_bytes(bpt.bpt_moe_route_workspace_bytes(cfg)))
+    want, got = torch.empty_like(z), torch.empty_like(z)
+    bpt.bpt_moe_route_bwd(cfg, z, r, dw, 1.0, want)
+    bpt.bpt_moe_route_bwd(cfg, z, bpt.MoeRoute(r.ids, None, r.offsets, None, None), dw, 1.0, got)
+    sync()
+    assert torch.equal(got, want)
+    for bad in (bpt.MoeRoute(None, r.weights, r.offsets, r.order, r.slot), bpt.MoeRoute(r.ids, r.weights, None, r.order, r.slot),
+                bpt.MoeRoute(r.ids.long(), None, r.offsets, None, None), bpt.MoeRoute(r.ids, None, r.offsets[:13], None, None)):
+        with pytest.raises(bpt.BptError):
+            bpt.bpt_moe_route_bwd(cfg, z, bad, dw, 1.0, got)
