@@ -95,8 +95,11 @@ __global__ void __launch_bounds__(THREADS) few_act_kernel(const FewParams p) {
   let_next_start();
   const int pair = p.order[r];
   __syncthreads();
-  const bool odd = __syncthreads_or(find_expert(p, r, &s_e));
-  const int e = odd ? group_of(p.offsets, p.E, p.pairs, r) : s_e;
+  if (__syncthreads_or(find_expert(p, r, &s_e))) {
+    if (threadIdx.x == 0) s_e = group_of(p.offsets, p.E, p.pairs, r);
+    __syncthreads();
+  }
+  const int e = s_e;
   if (e == p.E || i0 >= p.f) return;  // f is a multiple of 8: a warp's units are all there or none
   const bool some = pair >= 0 && pair < p.pairs;
   const __nv_bfloat16* x = p.x + (int64_t)(some ? pair / p.k : 0) * p.h;
