@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
         if (t >= 0) {
           if ((int64_t)t < q.V && x < INFINITY) {
             id[c] = t;
-            v[c] = q.teacher == BPT_TEACHER_LOGITS ? fminf(x * q.inv_t, 3.402823466e38f) : x;  // finite over T stays so
+            v[c] = x;
           } else {
             bad = true;
           }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(32 * PREP_WARPS) prepare_kernel(const PrepPara
       total = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        v[c] -= m;
+        v[c] = (v[c] - m) * q.inv_t;  // the difference first: values / T may be beyond fp32, or have no digits left for it
         total += expf(v[c]);
       }
 #pragma unroll

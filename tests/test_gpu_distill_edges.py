@@ -27,3 +27,28 @@ def test_padding_may_hold_any_finite_value(teacher, value, grads):
     v[weight == 0] = value
     for a, b in zip(once, run(cfg, x, w, ids, v, weight)):
         assert torch.equal(a, b)
+
+
+def test_teacher_logits_are_taken_from_their_maximum():
+    """p = softmax(values / T) goes by the values' differences: at an offset of
+    2^20 (whose fp32 neighbours are 2^-3 away) as without it, and where values / T
+    are beyond fp32.  Differences of multiples of 2^-3 are exact in fp32."""
+    cfg = DistillConfig(n=120, h=64, vocab=500, top_k=6, temperature=3.0, flags=DET)
+    x, w, ids, v, _ = inputs(cfg)
+    v = (v * 8).round() / 8
+    want, off = loss_of(cfg, x.double(), w.double(), ids, v, None)
+    loss, dx, dw = run(cfg, x, w, ids, v, None)
+    far, fx, fw = run(cfg, x, w, ids, v + 2.0 ** 20, None)
+    assert abs(float(loss) - float(want)) <= off + 2.0 ** -23 * float(want)
+    assert torch.equal(far, loss) and torch.equal(fx, dx) and torch.equal(fw, dw)
+    # values / T beyond fp32: the largest alone
+    cold = cfg.with_(temperature=2.0 ** -8)
+    v[::2] = torch.tensor([1e38, 3e38, 2e38, -3e38, 2.9e38, 0.0], device="cuda")
+    sure = ids.clone()
+    sure[::2, [0, 2, 3, 4, 5]] = -1
+    got, want = run(cold, x, w, ids, v, None), run(cold, x, w, sure, v, None)
+    exact, off = loss_of(cold, x.double(), w.double(), sure, v, None)
+    assert abs(float(got[0]) - float(exact)) <= off + 2.0 ** -23 * float(exact)
+    assert torch.equal(got[0], want[0])
+    near(got[1], want[1].double(), 2, "dx")
+    near(got[2], want[2].double(), 2, "dw")
