@@ -353,7 +353,9 @@ __global__ void __launch_bounds__(256) entries_kernel(int64_t n, int k, int64_t 
   for (int o = 1; j + o < k && s.id[i + o] == id; ++o) p += s.p[i + o];
   const float w = scale * (weight ? weight[row] : 1.f);
   const float q = expf(s.z[i] - s.lse[row]);
-  dz[row * ld + (id - v0)] = __float2bfloat16(w != 0.f ? w * (s.mass[row] * q - p) : 0.f);
+  // a row without mass gives nothing, whatever its logits (and q) are
+  const float mass = s.mass[row];
+  dz[row * ld + (id - v0)] = __float2bfloat16(w != 0.f && mass != 0.f ? w * (mass * q - p) : 0.f);
 }
 
 // sum over the slabs in order, onto acc (NULL: 0): fp32 out, or bf16

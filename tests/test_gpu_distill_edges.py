@@ -52,3 +52,18 @@ def test_teacher_logits_are_taken_from_their_maximum():
     assert torch.equal(got[0], want[0])
     near(got[1], want[1].double(), 2, "dx")
     near(got[2], want[2].double(), 2, "dw")
+
+
+def test_rows_of_probability_zero_give_nothing():
+    """Entries that are there but all of probability 0 (-inf): no loss and no
+    gradient, whatever the row's logits are (infinite here)."""
+    cfg = DistillConfig(n=70, h=64, vocab=500, top_k=6, vocab_block=256, flags=DET)
+    for teacher in (0, LOGPROBS):
+        c = cfg.with_(teacher=teacher)
+        x, w, ids, v, _ = inputs(c)
+        v[::2] = -math.inf
+        once = run(c, x, w, ids, v, None)
+        assert all(t.isfinite().all() for t in once) and bool((once[1][::2] == 0).all())
+        x[::2] = 3e38
+        for a, b in zip(once, run(c, x, w, ids, v, None)):
+            assert torch.equal(a, b)
