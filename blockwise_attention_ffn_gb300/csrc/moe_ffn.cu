@@ -5,9 +5,9 @@
 //   y_t = sum_j w_tj W2_e act(x_t W1_e^T [, x_t W3_e^T]),  e = ids[t, j]
 //
 // Forward, in the groups' order of the pairs (moe_route.cu): the first product
-// gathers the rows of x by TMA and applies the activation in its epilogue, the
-// second multiplies by W2, and a last pass adds each position's k rows with
-// their weights.  Backward, with da = dy W2 (dy gathered):
+// gathers the rows of x by copying warps and applies the activation in its
+// epilogue, the second multiplies by W2, and a last pass adds each position's k
+// rows with their weights.  Backward, with da = dy W2 (dy gathered):
 //   dg, du = w da dact/dg, dact/du    aw = w act    dw = <act, da>   (epilogue)
 //   dx rows = dg W1 + du W3 (one accumulator), added over the k choices
 //   dW1 = dg^T x, dW3 = du^T x (x gathered), dW2 = dy^T aw (dy gathered)

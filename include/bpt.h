@@ -536,8 +536,8 @@ typedef struct {
  *          + z_coef * (mean of lse^2)            (means over the nv positions)
  * with count_e the rows of expert e, a constant in the gradient.  loss (one
  * fp32) may be NULL when both coefficients are 0, else it is written in any
- * case.  Sums over rows are fp32 within blocks of at most n / 152 + 64 rows and
- * over at most 152 of them, fp64 across.
+ * case.  Sums over rows are fp32 within blocks of at most max(128, n / 152 + 1)
+ * rows and over at most 152 of them, fp64 across.
  * bpt_moe_route_bwd: dlogits [n, E] from dweights [n, k] and dloss; of r it
  * reads ids and offsets. */
 #define BPT_MOE_BAD_LOGIT_SITE 951
